@@ -55,7 +55,9 @@ EXPORTED = (
     "scan_log_fwd", "scan_log_bwd", "affine_scan_fwd", "affine_scan_bwd", "affine_prefix_fwd",
     "affine_prefix_bwd", "gdn_checkpoint_bytes", "gdn_fwd", "gdn_workspace_bytes", "gdn_bwd",
     "scan_fwd_noalloc", "scan_noalloc_device_status", "scan_step_host", "scan_copy",
-    "rglru_fwd", "rglru_bwd",
+    "rglru_fwd", "rglru_bwd", "qk_norm_rope_workspace_bytes", "qk_norm_rope_fwd",
+    "qk_norm_rope_bwd", "linattn_workspace_bytes", "linattn_fwd", "linattn_bwd", "linattn_step",
+    "window_attn_workspace_bytes", "window_attn_fwd", "window_attn_bwd", "window_attn_step",
 )
 
 
@@ -88,11 +90,19 @@ class DeviceIO(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in ("a", "x", "h0", "dh", "h", "da", "dx", "dh0")]
 
 
+class View4(ctypes.Structure):
+    """scan_view4: a [B, T, H, D] operand and its strides in elements."""
+    _fields_ = [("ptr", ctypes.c_void_p), ("stride_b", ctypes.c_int64),
+                ("stride_t", ctypes.c_int64), ("stride_h", ctypes.c_int64)]
+
+
 _vp = ctypes.c_void_p
 _i64 = ctypes.c_int64
 _i32 = ctypes.c_int32
 _sz = ctypes.c_size_t
+_f32 = ctypes.c_float
 _opt = ctypes.POINTER(ScanOpts)
+_v4 = ctypes.POINTER(View4)
 
 _SIGS = {
     "scan_status_string": ([ctypes.c_int], ctypes.c_char_p),
@@ -136,6 +146,25 @@ _SIGS = {
     "rglru_bwd": ([_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64,
                    _i64, ctypes.c_int, _vp], ctypes.c_int),
     "scan_copy": ([_vp, _vp, _sz, _i32, _vp, _vp], ctypes.c_int),
+    "qk_norm_rope_workspace_bytes": ([_i64], _sz),
+    "qk_norm_rope_fwd": ([_v4] * 2 + [_vp] * 5 + [_v4] * 2 + [_i64] * 7
+                         + [_i32, _f32, ctypes.c_int, _vp], ctypes.c_int),
+    "qk_norm_rope_bwd": ([_v4] * 2 + [_vp] * 5 + [_v4] * 4 + [_vp] * 2 + [_i64] * 7
+                         + [_i32, _f32, ctypes.c_int, _vp, _sz, _vp], ctypes.c_int),
+    "linattn_workspace_bytes": ([_i64] * 6, _sz),
+    "linattn_fwd": ([_v4] * 3 + [_vp] * 3 + [_i32, _v4, _vp] + [_i64] * 5
+                    + [_f32, ctypes.c_int, _vp, _sz, _vp], ctypes.c_int),
+    "linattn_bwd": ([_v4] * 3 + [_vp] * 3 + [_i32, _v4, _vp] + [_v4] * 3 + [_vp] + [_i64] * 5
+                    + [_f32, ctypes.c_int, _vp, _sz, _vp], ctypes.c_int),
+    "linattn_step": ([_v4] * 3 + [_vp] * 3 + [_i64, _v4] + [_i64] * 4 + [_f32, ctypes.c_int, _vp],
+                     ctypes.c_int),
+    "window_attn_workspace_bytes": ([_i64] * 9 + [_i32], _sz),
+    "window_attn_fwd": ([_v4] * 3 + [_vp, _i32, _v4, _vp] + [_i64] * 8
+                        + [_f32, ctypes.c_int, _vp, _sz, _vp], ctypes.c_int),
+    "window_attn_bwd": ([_v4] * 4 + [_vp, _v4, _vp, _i32] + [_v4] * 3 + [_i64] * 8
+                        + [_f32, ctypes.c_int, _vp, _sz, _vp], ctypes.c_int),
+    "window_attn_step": ([_v4] * 3 + [_vp] * 4 + [_i64, _v4] + [_i64] * 6
+                         + [_f32, ctypes.c_int, _vp], ctypes.c_int),
 }
 
 _lock = threading.Lock()
@@ -282,6 +311,9 @@ class _Workspaces:
 
 
 _ws = _Workspaces()
+# The attention operators keep partial sums in theirs, which the scans' look-back
+# records must never be mistaken for: a pool of its own.
+_mixer_ws = _Workspaces()
 
 
 def workspace_for(op: int, B: int, C: int, T: int, k: int, v: int, opts, device, stream):
@@ -318,13 +350,15 @@ def scan_workspace_init(workspace: torch.Tensor, stream=None) -> None:
 
 
 def scan_get_device_status(device=None, stream=None) -> int:
-    """Sticky device status of the workspace used on (device, stream); resets it."""
+    """Sticky device status of the workspaces used on (device, stream); resets it."""
     device = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
     s = _stream(stream, device)
-    buf = _ws.current(device, s)
-    if buf is None:
-        return SCAN_OK
-    return int(_call(device, "scan_get_device_status", _ptr(buf), s))
+    found = SCAN_OK
+    for pool in (_ws, _mixer_ws):
+        buf = pool.current(device, s)
+        if buf is not None:
+            found = int(_call(device, "scan_get_device_status", _ptr(buf), s)) or found
+    return found
 
 
 def scan_fwd(a, x, h0=None, cu_seqlens=None, reverse=False, *, out=None, opts=None, stream=None):
@@ -820,3 +854,333 @@ def scan_copy(src, dst, mode=SCAN_COPY_VEC, *, status=None, stream=None):
                _stream(stream, dev))
     _check(st, "scan_copy")
     return dst
+
+
+# ---------------------------------------------------------------------------
+# token mixers: strided [B, T, H, D] operands
+# ---------------------------------------------------------------------------
+
+def _heads(t, name, dtype=None, shape=None, device=None):
+    """Checks a [B, T, H, D] (or, for single tokens, [B, H, D]) operand."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.stride(-1) != 1 and t.shape[-1] > 1:
+        raise ValueError(f"{name} must have a unit stride along its last axis")
+    return t
+
+
+def _written(t, name, **want):
+    """An output: as _heads, and no two of its elements in one place."""
+    _heads(t, name, **want)
+    reach = 1
+    for stride, n in sorted((s, n) for s, n in zip(t.stride(), t.shape) if n > 1):
+        if stride < reach:
+            raise ValueError(f"{name} must not overlap itself")
+        reach += stride * (n - 1)
+    return t
+
+
+def _view4(t):
+    s = t.stride()
+    if t.dim() == 3:  # [B, H, D]: one token a request
+        return View4(t.data_ptr(), s[0], 0, s[1])
+    return View4(t.data_ptr(), s[0], s[1], s[2])
+
+
+def _rank(t, name, n):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dim() != n:
+        raise ValueError(f"{name}: expected {'[B, T, H, D]' if n == 4 else '[B, H, D]'}")
+    return t
+
+
+def _mixer_workspace(nbytes, dev, s):
+    ws = _mixer_ws.get(max(int(nbytes), 256), dev, s)
+    return ws.data_ptr(), ws.numel()
+
+
+def qk_norm_rope_workspace_bytes(D) -> int:
+    return int(lib().qk_norm_rope_workspace_bytes(D))
+
+
+def _qk_args(q, k, q_weight, k_weight, cos, sin, positions):
+    _heads(_rank(q, "q", 4), "q")
+    dev, dt = q.device, q.dtype
+    B, T, Hq, D = q.shape
+    _heads(_rank(k, "k", 4), "k", dtype=dt, shape=(B, T, k.shape[2], D), device=dev)
+    for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+        _need(w, name, dtype=torch.float32, shape=(D,), device=dev)
+    P = R = 0
+    if (cos is None) != (sin is None):
+        raise ValueError("cos and sin are given together or not at all")
+    if cos is not None:
+        _need(cos, "cos", dtype=torch.float32, device=dev)
+        if cos.dim() != 2:
+            raise ValueError("cos: expected [P, R / 2]")
+        _need(sin, "sin", dtype=torch.float32, shape=cos.shape, device=dev)
+        P, R = cos.shape[0], 2 * cos.shape[1]
+    _need(positions, "positions", dtype=torch.int32, shape=(B, T), device=dev)
+    return dev, dt, B, T, Hq, k.shape[2], D, R, P
+
+
+def qk_norm_rope_fwd(q, k, q_weight, k_weight, cos, sin, positions=None, *, eps=1e-6,
+                     interleaved=False, out=None, stream=None):
+    """RMS norm of every query and key head and the rotation of its position.
+    q [B, T, Hq, D], k [B, T, Hk, D] fp32 or bf16, unit stride along D;
+    q_weight, k_weight fp32 [D] or None; cos, sin fp32 [P, R / 2] (R <= D
+    elements are rotated; None: none); positions int32 [B, T] or None (t). out:
+    (q_out, k_out), which may be (q, k). Returns (q_out, k_out)."""
+    dev, dt, B, T, Hq, Hk, D, R, P = _qk_args(q, k, q_weight, k_weight, cos, sin, positions)
+    if out is not None:
+        yq, yk = out
+        _written(yq, "q_out", dtype=dt, shape=q.shape, device=dev)
+        _written(yk, "k_out", dtype=dt, shape=k.shape, device=dev)
+    else:
+        yq = torch.empty(q.shape, dtype=dt, device=dev)
+        yk = torch.empty(k.shape, dtype=dt, device=dev)
+    st = _call(dev, "qk_norm_rope_fwd", _view4(q), _view4(k), _ptr(q_weight), _ptr(k_weight),
+               _ptr(cos), _ptr(sin), _ptr(positions), _view4(yq), _view4(yk), B, T, Hq, Hk, D, R, P,
+               int(bool(interleaved)), eps, _dtype_code(q), _stream(stream, dev))
+    _check(st, "qk_norm_rope_fwd")
+    return yq, yk
+
+
+def qk_norm_rope_bwd(q, k, q_weight, k_weight, cos, sin, dq_out, dk_out, positions=None, *,
+                     eps=1e-6, interleaved=False, out=None, stream=None):
+    """Gradients of L = sum dq_out q_out + dk_out k_out for the forward's inputs:
+    (dq, dk, dq_weight, dk_weight), the weights' in fp32 (None without weights)."""
+    dev, dt, B, T, Hq, Hk, D, R, P = _qk_args(q, k, q_weight, k_weight, cos, sin, positions)
+    _heads(dq_out, "dq_out", dtype=dt, shape=q.shape, device=dev)
+    _heads(dk_out, "dk_out", dtype=dt, shape=k.shape, device=dev)
+    if out is not None:
+        dq, dk, dwq, dwk = out
+        _written(dq, "dq", dtype=dt, shape=q.shape, device=dev)
+        _written(dk, "dk", dtype=dt, shape=k.shape, device=dev)
+        for w, name in ((dwq, "dq_weight"), (dwk, "dk_weight")):
+            _need(w, name, dtype=torch.float32, shape=(D,), device=dev)
+    else:
+        dq = torch.empty(q.shape, dtype=dt, device=dev)
+        dk = torch.empty(k.shape, dtype=dt, device=dev)
+        dwq, dwk = (None if w is None else torch.empty(D, dtype=torch.float32, device=dev)
+                    for w in (q_weight, k_weight))
+    s = _stream(stream, dev)
+    ws, nws = _mixer_workspace(256 + qk_norm_rope_workspace_bytes(D), dev, s)
+    st = _call(dev, "qk_norm_rope_bwd", _view4(q), _view4(k), _ptr(q_weight), _ptr(k_weight),
+               _ptr(cos), _ptr(sin), _ptr(positions), _view4(dq_out), _view4(dk_out), _view4(dq),
+               _view4(dk), _ptr(dwq), _ptr(dwk), B, T, Hq, Hk, D, R, P, int(bool(interleaved)), eps,
+               _dtype_code(q), ws + 256, nws - 256, s)  # past the status word
+    _check(st, "qk_norm_rope_bwd")
+    return dq, dk, dwq, dwk
+
+
+def linattn_workspace_bytes(B, T, H, Dk, Dv, n_seqs=0) -> int:
+    return int(lib().linattn_workspace_bytes(B, T, H, Dk, Dv, n_seqs))
+
+
+def _lin_args(q, k, v, log_decay, cu_seqlens):
+    _heads(_rank(q, "q", 4), "q")
+    dev, dt = q.device, q.dtype
+    B, T, H, Dk = q.shape
+    _heads(k, "k", dtype=dt, shape=q.shape, device=dev)
+    _heads(_rank(v, "v", 4), "v", dtype=dt, shape=(B, T, H, v.shape[3]), device=dev)
+    _need(log_decay, "log_decay", dtype=torch.float32, shape=(H,), device=dev)
+    n = _packed(cu_seqlens, B, dev)
+    return dev, dt, B, T, H, Dk, v.shape[3], n
+
+
+def _packed(cu_seqlens, B, dev):
+    """Sequences of a packed row; 0 when dense."""
+    if cu_seqlens is None:
+        return 0
+    _need(cu_seqlens, "cu_seqlens", dtype=torch.int32, device=dev)
+    if B != 1 or cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1:
+        raise ValueError("packed operands are [1, T, H, D] with cu_seqlens [n_seqs + 1]")
+    return cu_seqlens.numel() - 1
+
+
+def linattn_fwd(q, k, v, log_decay, h0=None, cu_seqlens=None, *, scale=None, need_state=True,
+                out=None, stream=None):
+    """Linear attention with a decay for each head: S_t = exp(log_decay[h])
+    S_{t-1} + k_t v_t^T, o_t = scale q_t S_t. q, k [B, T, H, Dk], v [B, T, H,
+    Dv] fp32 or bf16, unit stride along the last axis; log_decay fp32 [H]; h0
+    fp32 [B or n_seqs, H, Dk, Dv] or None; scale: Dk^-0.5 when None. Returns
+    (o, hT): o in q's dtype, the last state hT in fp32 (None when need_state is
+    False). out: (o, hT)."""
+    dev, dt, B, T, H, Dk, Dv, n = _lin_args(q, k, v, log_decay, cu_seqlens)
+    states = (n if cu_seqlens is not None else B, H, Dk, Dv)
+    _need(h0, "h0", dtype=torch.float32, shape=states, device=dev)
+    if out is not None:
+        o, hT = out
+        _written(o, "o", dtype=dt, shape=v.shape, device=dev)
+        _need(hT, "hT", dtype=torch.float32, shape=states, device=dev)
+    else:
+        o = torch.empty(v.shape, dtype=dt, device=dev)
+        hT = torch.empty(states, dtype=torch.float32, device=dev) if need_state else None
+    s = _stream(stream, dev)
+    ws, nws = _mixer_workspace(linattn_workspace_bytes(B, T, H, Dk, Dv, n), dev, s)
+    st = _call(dev, "linattn_fwd", _view4(q), _view4(k), _view4(v), _ptr(log_decay), _ptr(h0),
+               _ptr(cu_seqlens), n, _view4(o), _ptr(hT), B, T, H, Dk, Dv,
+               Dk ** -0.5 if scale is None else scale, _dtype_code(q), ws, nws, s)
+    _check(st, "linattn_fwd")
+    return o, hT
+
+
+def linattn_bwd(q, k, v, log_decay, dout, h0=None, cu_seqlens=None, dhT=None, *, scale=None,
+                need_dh0=True, out=None, stream=None):
+    """Gradients of L = sum dout o + sum dhT hT for linattn_fwd's inputs: (dq,
+    dk, dv, dh0), the first three in q's dtype, dh0 in fp32 (None when need_dh0
+    is False). Nothing of the forward is needed."""
+    dev, dt, B, T, H, Dk, Dv, n = _lin_args(q, k, v, log_decay, cu_seqlens)
+    states = (n if cu_seqlens is not None else B, H, Dk, Dv)
+    _need(h0, "h0", dtype=torch.float32, shape=states, device=dev)
+    _need(dhT, "dhT", dtype=torch.float32, shape=states, device=dev)
+    _heads(dout, "dout", dtype=dt, shape=v.shape, device=dev)
+    if out is not None:
+        dq, dk, dv, dh0 = out
+        for t, name, like in ((dq, "dq", q), (dk, "dk", k), (dv, "dv", v)):
+            _written(t, name, dtype=dt, shape=like.shape, device=dev)
+        _need(dh0, "dh0", dtype=torch.float32, shape=states, device=dev)
+    else:
+        dq, dk, dv = (torch.empty(t.shape, dtype=dt, device=dev) for t in (q, k, v))
+        dh0 = torch.empty(states, dtype=torch.float32, device=dev) if need_dh0 else None
+    s = _stream(stream, dev)
+    ws, nws = _mixer_workspace(linattn_workspace_bytes(B, T, H, Dk, Dv, n), dev, s)
+    st = _call(dev, "linattn_bwd", _view4(q), _view4(k), _view4(v), _ptr(log_decay), _ptr(h0),
+               _ptr(cu_seqlens), n, _view4(dout), _ptr(dhT), _view4(dq), _view4(dk), _view4(dv),
+               _ptr(dh0), B, T, H, Dk, Dv, Dk ** -0.5 if scale is None else scale, _dtype_code(q),
+               ws, nws, s)
+    _check(st, "linattn_bwd")
+    return dq, dk, dv, dh0
+
+
+def linattn_step(q, k, v, log_decay, state, slots=None, *, scale=None, out=None, stream=None):
+    """One token of each request: state[slot] = exp(log_decay) state[slot] +
+    k v^T in place, o = scale q state[slot]. q, k [B, H, Dk], v [B, H, Dv];
+    state fp32 [n_slots, H, Dk, Dv]; slots int32 [B] or None (request b has
+    state b), a slot outside the pool marking an idle request (o = 0). Returns
+    o [B, H, Dv]."""
+    _heads(_rank(q, "q", 3), "q")
+    dev, dt = q.device, q.dtype
+    B, H, Dk = q.shape
+    _heads(k, "k", dtype=dt, shape=q.shape, device=dev)
+    _heads(_rank(v, "v", 3), "v", dtype=dt, shape=(B, H, v.shape[2]), device=dev)
+    Dv = v.shape[2]
+    _need(log_decay, "log_decay", dtype=torch.float32, shape=(H,), device=dev)
+    _need(state, "state", dtype=torch.float32, device=dev)
+    if state.dim() != 4 or state.shape[1:] != (H, Dk, Dv):
+        raise ValueError(f"state has shape {tuple(state.shape)}, expected (n_slots, {H}, {Dk}, {Dv})")
+    _need(slots, "slots", dtype=torch.int32, shape=(B,), device=dev)
+    o = out if out is not None else torch.empty(v.shape, dtype=dt, device=dev)
+    if out is not None:
+        _written(o, "out", dtype=dt, shape=v.shape, device=dev)
+    st = _call(dev, "linattn_step", _view4(q), _view4(k), _view4(v), _ptr(log_decay), _ptr(state),
+               _ptr(slots), state.shape[0], _view4(o), B, H, Dk, Dv,
+               Dk ** -0.5 if scale is None else scale, _dtype_code(q), _stream(stream, dev))
+    _check(st, "linattn_step")
+    return o
+
+
+def window_attn_workspace_bytes(B, Tq, Tk, Hq, Hk, D, window, sinks=0, n_seqs=0,
+                                backward=False) -> int:
+    return int(lib().window_attn_workspace_bytes(B, Tq, Tk, Hq, Hk, D, window, sinks, n_seqs,
+                                                 int(bool(backward))))
+
+
+def _win_args(q, k, v, cu_seqlens):
+    _heads(_rank(q, "q", 4), "q")
+    dev, dt = q.device, q.dtype
+    B, Tq, Hq, D = q.shape
+    _rank(k, "k", 4)
+    Tk, Hk = k.shape[1:3]
+    _heads(k, "k", dtype=dt, shape=(B, Tk, Hk, D), device=dev)
+    _heads(v, "v", dtype=dt, shape=k.shape, device=dev)
+    n = _packed(cu_seqlens, B, dev)
+    return dev, dt, B, Tq, Tk, Hq, Hk, D, n
+
+
+def window_attn_fwd(q, k, v, window, sinks=0, cu_seqlens=None, *, scale=None, out=None, stream=None):
+    """Causal attention of each query over the last `window` positions and the
+    first `sinks`. q [B, Tq, Hq, D], k, v [B, Tk, Hk, D] fp32 or bf16, unit
+    stride along D, the queries being the last Tq of Tk positions; Hq a multiple
+    of Hk; cu_seqlens: packed sequences (B = 1, Tq = Tk); scale: D^-0.5 when
+    None. Returns (o, lse): o in q's dtype, lse fp32 [B, Hq, Tq]."""
+    dev, dt, B, Tq, Tk, Hq, Hk, D, n = _win_args(q, k, v, cu_seqlens)
+    if out is not None:
+        o, lse = out
+        _written(o, "o", dtype=dt, shape=q.shape, device=dev)
+        _need(lse, "lse", dtype=torch.float32, shape=(B, Hq, Tq), device=dev)
+    else:
+        o = torch.empty(q.shape, dtype=dt, device=dev)
+        lse = torch.empty((B, Hq, Tq), dtype=torch.float32, device=dev)
+    s = _stream(stream, dev)
+    ws, nws = _mixer_workspace(
+        window_attn_workspace_bytes(B, Tq, Tk, Hq, Hk, D, window, sinks, n), dev, s)
+    st = _call(dev, "window_attn_fwd", _view4(q), _view4(k), _view4(v), _ptr(cu_seqlens), n,
+               _view4(o), _ptr(lse), B, Tq, Tk, Hq, Hk, D, window, sinks,
+               D ** -0.5 if scale is None else scale, _dtype_code(q), ws, nws, s)
+    _check(st, "window_attn_fwd")
+    return o, lse
+
+
+def window_attn_bwd(q, k, v, o, lse, dout, window, sinks=0, cu_seqlens=None, *, scale=None, out=None,
+                    stream=None):
+    """Gradients of L = sum dout o for window_attn_fwd's inputs, from its
+    outputs: (dq, dk, dv) in q's dtype."""
+    dev, dt, B, Tq, Tk, Hq, Hk, D, n = _win_args(q, k, v, cu_seqlens)
+    _heads(o, "o", dtype=dt, shape=q.shape, device=dev)
+    _heads(dout, "dout", dtype=dt, shape=q.shape, device=dev)
+    _need(lse, "lse", dtype=torch.float32, shape=(B, Hq, Tq), device=dev)
+    if out is not None:
+        dq, dk, dv = out
+        for t, name, like in ((dq, "dq", q), (dk, "dk", k), (dv, "dv", v)):
+            _written(t, name, dtype=dt, shape=like.shape, device=dev)
+    else:
+        dq, dk, dv = (torch.empty(t.shape, dtype=dt, device=dev) for t in (q, k, v))
+    s = _stream(stream, dev)
+    ws, nws = _mixer_workspace(
+        window_attn_workspace_bytes(B, Tq, Tk, Hq, Hk, D, window, sinks, n, True), dev, s)
+    st = _call(dev, "window_attn_bwd", _view4(q), _view4(k), _view4(v), _view4(o), _ptr(lse),
+               _view4(dout), _ptr(cu_seqlens), n, _view4(dq), _view4(dk), _view4(dv), B, Tq, Tk, Hq,
+               Hk, D, window, sinks, D ** -0.5 if scale is None else scale, _dtype_code(q), ws, nws, s)
+    _check(st, "window_attn_bwd")
+    return dq, dk, dv
+
+
+def window_attn_step(q, k, v, k_cache, v_cache, positions, window, sinks=0, slots=None, *, scale=None,
+                     out=None, stream=None):
+    """One token of each request over its ring of cached keys and values, which
+    it joins. q [B, Hq, D], k, v [B, Hk, D]; k_cache, v_cache [n_slots, sinks +
+    window, Hk, D], updated in place: position p is row p while p < sinks, then
+    row sinks + (p - sinks) % window; positions int32 [B], the new tokens' own
+    (negative: an idle request); slots int32 [B] or None (request b has cache
+    b). Returns o [B, Hq, D]."""
+    _heads(_rank(q, "q", 3), "q")
+    dev, dt = q.device, q.dtype
+    B, Hq, D = q.shape
+    Hk = _rank(k, "k", 3).shape[1]
+    _heads(k, "k", dtype=dt, shape=(B, Hk, D), device=dev)
+    _heads(v, "v", dtype=dt, shape=(B, Hk, D), device=dev)
+    _need(k_cache, "k_cache", dtype=dt, device=dev)
+    if k_cache.dim() != 4 or k_cache.shape[1:] != (sinks + window, Hk, D):
+        raise ValueError(f"k_cache has shape {tuple(k_cache.shape)}, expected "
+                         f"(n_slots, {sinks + window}, {Hk}, {D})")
+    _need(v_cache, "v_cache", dtype=dt, shape=k_cache.shape, device=dev)
+    _need(positions, "positions", dtype=torch.int32, shape=(B,), device=dev)
+    _need(slots, "slots", dtype=torch.int32, shape=(B,), device=dev)
+    o = out if out is not None else torch.empty(q.shape, dtype=dt, device=dev)
+    if out is not None:
+        _written(o, "out", dtype=dt, shape=q.shape, device=dev)
+    st = _call(dev, "window_attn_step", _view4(q), _view4(k), _view4(v), _ptr(k_cache), _ptr(v_cache),
+               _ptr(positions), _ptr(slots), k_cache.shape[0], _view4(o), B, Hq, Hk, D, window, sinks,
+               D ** -0.5 if scale is None else scale, _dtype_code(q), _stream(stream, dev))
+    _check(st, "window_attn_step")
+    return o

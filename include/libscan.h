@@ -496,6 +496,172 @@ scan_status scan_fwd_noalloc(const void* a, const void* x, const float* h0,
  * allocates nothing; the copies are synchronous. */
 scan_status scan_noalloc_device_status(cudaStream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * Token mixers that language models run next to the scans: the norm and
+ * rotation of queries and keys, linear attention with a decay for each head
+ * (the outer-product state above at the head sizes and types of such models)
+ * and attention with a sliding window and first tokens that stay visible. They
+ * have no counterpart in the source pages. The scans' conventions hold
+ * (asynchronous, no allocation, no fallback); the operands are
+ * [B, T, H, D] with a unit stride along D and any strides along the others, so
+ * that they may be slices of a fused projection. */
+
+/* A [B, T, H, D] device operand: element (b, t, h, d) is at
+ * ptr + b stride_b + t stride_t + h stride_h + d (strides in elements). */
+typedef struct scan_view4 {
+  void* ptr;
+  int64_t stride_b, stride_t, stride_h;
+} scan_view4;
+
+/* RMS norm of every query and key head, then the rotation of its position:
+ *   z = w x (mean(x^2) + eps)^(-1/2),  y = z with each pair (a, b) of its first
+ *   R elements replaced by (a cos - b sin, a sin + b cos).
+ * Pair i is elements (i, R/2 + i), or (2i, 2i + 1) when interleaved != 0; its
+ * cosine and sine are entry [position][i] of the fp32 tables [P, R/2].
+ *   q, q_out: [B, T, Hq, D], k, k_out: [B, T, Hk, D] of dtype dt; an output may
+ *   be its own input. Hq or Hk may be 0 (its pointers are not used).
+ *   q_weight, k_weight: fp32 [D] or NULL (ones). positions: int32 [B, T]
+ *   contiguous, or NULL (position t). A position outside [0, P) gives NaN in
+ *   the rotated elements. R = 0: no rotation (tables may be NULL).
+ * The norm and products are fp32; the result is rounded once.
+ * SCAN_ERR_UNSUPPORTED unless D % 8 == 0, D <= 256 and R % 8 == 0;
+ * SCAN_ERR_ALIGNMENT unless every pointer is 16-byte aligned and every stride
+ * a multiple of 16 bytes; SCAN_ERR_INVALID_ARG for negative sizes, R > D,
+ * a negative or NaN eps or a missing pointer. */
+scan_status qk_norm_rope_fwd(const scan_view4* q, const scan_view4* k, const float* q_weight,
+                             const float* k_weight, const float* cos_table, const float* sin_table,
+                             const int32_t* positions, const scan_view4* q_out,
+                             const scan_view4* k_out, int64_t B, int64_t T, int64_t Hq, int64_t Hk,
+                             int64_t D, int64_t R, int64_t P, int32_t interleaved, float eps,
+                             scan_dtype dt, cudaStream_t stream);
+
+/* Its backward: with n = x (mean(x^2) + eps)^(-1/2), dz the gradient turned
+ * back by the same angle and g = w dz,
+ *   dx = (mean(x^2) + eps)^(-1/2) (g - n mean(g n)),  dw = sum over b, t, h of dz n.
+ * q, k: the forward's inputs; dq_out, dk_out: the gradients of its outputs;
+ * dq, dk: written, of dtype dt; dq_weight, dk_weight: fp32 [D], written, or
+ * NULL. The sums over rows are fp32 in a fixed order. workspace:
+ * qk_norm_rope_workspace_bytes(D) bytes, 16-byte aligned, nothing kept between
+ * calls (else SCAN_ERR_WORKSPACE). Other errors as the forward's. */
+size_t qk_norm_rope_workspace_bytes(int64_t D);
+scan_status qk_norm_rope_bwd(const scan_view4* q, const scan_view4* k, const float* q_weight,
+                             const float* k_weight, const float* cos_table, const float* sin_table,
+                             const int32_t* positions, const scan_view4* dq_out,
+                             const scan_view4* dk_out, const scan_view4* dq, const scan_view4* dk,
+                             float* dq_weight, float* dk_weight, int64_t B, int64_t T, int64_t Hq,
+                             int64_t Hk, int64_t D, int64_t R, int64_t P, int32_t interleaved,
+                             float eps, scan_dtype dt, void* workspace, size_t workspace_bytes,
+                             cudaStream_t stream);
+
+/* Linear attention with a decay for each head, per (sequence, head):
+ *   S_t = lambda_h S_{t-1} + k_t v_t^T  (Dk x Dv, fp32),  S_{-1} = h0,
+ *   o_t = scale q_t S_t,   lambda_h = exp(log_decay[h]).
+ *   q, k: [B, T, H, Dk], v, o: [B, T, H, Dv] of dtype dt; log_decay: fp32 [H]
+ *   (a constant of the model: no gradient; -inf: no memory); h0 (nullable) and
+ *   hT (nullable, written): fp32 [B, H, Dk, Dv] contiguous.
+ * Packed (cu_seqlens != NULL): B = 1, int32 [n_seqs + 1] offsets from 0 to T
+ * on the device as for scan_fwd, h0 and hT [n_seqs, H, Dk, Dv]; empty sequences
+ * are allowed (their hT is h0, or 0). Malformed offsets set the workspace's
+ * device status to SCAN_ERR_SEQLENS.
+ * bf16 operands on 16-byte boundaries run chunk by chunk on the tensor cores:
+ * products of bf16 operands summed in fp32, the within-chunk weights and the
+ * state as read by a query rounded to bf16, the state itself carried and
+ * updated to fp32 accuracy. Other operands and short rows run the recurrence in
+ * fp32. Values outside the sequences are never used.
+ * workspace: linattn_workspace_bytes() bytes, zeroed once with
+ * scan_workspace_init (it starts with the device status word), for forward and
+ * backward; n_seqs = 0 when dense. SCAN_ERR_UNSUPPORTED unless Dk and Dv are
+ * multiples of 8 up to 128; SCAN_ERR_INVALID_ARG unless scale > 0 and finite. */
+size_t linattn_workspace_bytes(int64_t B, int64_t T, int64_t H, int64_t Dk, int64_t Dv,
+                               int64_t n_seqs);
+scan_status linattn_fwd(const scan_view4* q, const scan_view4* k, const scan_view4* v,
+                        const float* log_decay, const float* h0, const int32_t* cu_seqlens,
+                        int32_t n_seqs, const scan_view4* o, float* hT, int64_t B, int64_t T,
+                        int64_t H, int64_t Dk, int64_t Dv, float scale, scan_dtype dt,
+                        void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/* Its backward for L = sum <dout, o> + <dhT, hT>: three passes of the same
+ * recurrence, since each gradient is linear attention over the other operands:
+ *   dq: forward over (dout, v, k) from h0^T,
+ *   dk: reversed over (v, dout, q), dv: reversed over (k, q, dout), from dhT,
+ * dh0 = lambda (the state that the reversed pass ends in). dhT (nullable: 0),
+ * dh0 (nullable): fp32 in h0's layout; dq, dk, dv: dtype dt, written. Nothing
+ * of the forward is stored. Errors and workspace as the forward's. */
+scan_status linattn_bwd(const scan_view4* q, const scan_view4* k, const scan_view4* v,
+                        const float* log_decay, const float* h0, const int32_t* cu_seqlens,
+                        int32_t n_seqs, const scan_view4* dout, const float* dhT,
+                        const scan_view4* dq, const scan_view4* dk, const scan_view4* dv, float* dh0,
+                        int64_t B, int64_t T, int64_t H, int64_t Dk, int64_t Dv, float scale,
+                        scan_dtype dt, void* workspace, size_t workspace_bytes,
+                        cudaStream_t stream);
+
+/* One token of each of B requests: S = lambda_h S + k v^T in place, o = scale q S.
+ *   q, k: [B, H, Dk], v, o: [B, H, Dv] of dtype dt (views with stride_t unused);
+ *   state: fp32 [n_slots, H, Dk, Dv] contiguous, 16-byte aligned; slots: int32
+ *   [B], the state of each request, or NULL (request b has state b). Two requests
+ *   must not share a state. A slot outside [0, n_slots) marks an idle request:
+ *   o = 0 and no state is touched. */
+scan_status linattn_step(const scan_view4* q, const scan_view4* k, const scan_view4* v,
+                         const float* log_decay, float* state, const int32_t* slots, int64_t n_slots,
+                         const scan_view4* o, int64_t B, int64_t H, int64_t Dk, int64_t Dv,
+                         float scale, scan_dtype dt, cudaStream_t stream);
+
+/* Causal attention with a sliding window and first tokens that stay visible:
+ * the query at position i sees key j where j <= i and (i - j < window or
+ * j < sinks);  o_i = sum_j softmax_j(scale q_i k_j) v_j.
+ *   q, o: [B, Tq, Hq, D]; k, v: [B, Tk, Hk, D] of dtype dt, Hq a multiple of Hk
+ *   (query heads h Hq/Hk .. share key head h). The queries are the last Tq of
+ *   the Tk positions. A query that sees no key (Tq > Tk) has o = 0, lse = -inf.
+ *   lse: fp32 [B, Hq, Tq], the log of each row's sum of exponentials, written.
+ * Packed (cu_seqlens): B = 1, Tq = Tk, positions count from each sequence's
+ * start; device status as for linattn_fwd.
+ * bf16 operands on 16-byte boundaries run on the tensor cores, weights rounded
+ * to bf16 for the second product; statistics and sums are fp32.
+ * Values within a sequence must be finite; what lies outside is never used.
+ * workspace: window_attn_workspace_bytes() (backward != 0 for the backward's),
+ * zeroed once with scan_workspace_init. SCAN_ERR_UNSUPPORTED unless D is a
+ * multiple of 8 up to 128 and B Hq <= 65535; SCAN_ERR_INVALID_ARG unless
+ * window >= 1, sinks >= 0, Hq % Hk == 0 and scale > 0 and finite. */
+size_t window_attn_workspace_bytes(int64_t B, int64_t Tq, int64_t Tk, int64_t Hq, int64_t Hk,
+                                   int64_t D, int64_t window, int64_t sinks, int64_t n_seqs,
+                                   int32_t backward);
+scan_status window_attn_fwd(const scan_view4* q, const scan_view4* k, const scan_view4* v,
+                            const int32_t* cu_seqlens, int32_t n_seqs, const scan_view4* o,
+                            float* lse, int64_t B, int64_t Tq, int64_t Tk, int64_t Hq, int64_t Hk,
+                            int64_t D, int64_t window, int64_t sinks, float scale, scan_dtype dt,
+                            void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/* Its backward from the forward's o and lse:
+ *   p_ij = exp(scale q_i k_j - lse_i), ds_ij = scale p_ij (dout_i v_j - dout_i o_i),
+ *   dq_i = sum_j ds_ij k_j, dk_j = sum_i ds_ij q_i, dv_j = sum_i p_ij dout_i,
+ * the last two over the query heads that share the key head as well. dq, dk,
+ * dv: dtype dt, written. No sum depends on the order in which blocks run.
+ * Errors and workspace as the forward's. */
+scan_status window_attn_bwd(const scan_view4* q, const scan_view4* k, const scan_view4* v,
+                            const scan_view4* o, const float* lse, const scan_view4* dout,
+                            const int32_t* cu_seqlens, int32_t n_seqs, const scan_view4* dq,
+                            const scan_view4* dk, const scan_view4* dv, int64_t B, int64_t Tq,
+                            int64_t Tk, int64_t Hq, int64_t Hk, int64_t D, int64_t window,
+                            int64_t sinks, float scale, scan_dtype dt, void* workspace,
+                            size_t workspace_bytes, cudaStream_t stream);
+
+/* One token of each of B requests over cached keys and values, which it joins.
+ *   q, o: [B, Hq, D], k, v: [B, Hk, D] of dtype dt (views with stride_t unused);
+ *   k_cache, v_cache: [n_slots, sinks + window, Hk, D] of dtype dt, contiguous,
+ *   16-byte aligned: position p of a request is row p while p < sinks, then row
+ *   sinks + (p - sinks) % window, so a token takes the place of the one that
+ *   leaves the window. positions: int32 [B], the new token's position; the rows
+ *   of the min(positions, sinks + window) positions before it are filled.
+ *   slots: int32 [B], the cache of each request, or NULL (request b has cache
+ *   b); two requests must not share a cache. A slot outside [0, n_slots) or a
+ *   negative position marks an idle request: o = 0 and no cache is touched.
+ *   Rows that are not filled are never used. */
+scan_status window_attn_step(const scan_view4* q, const scan_view4* k, const scan_view4* v,
+                             void* k_cache, void* v_cache, const int32_t* positions,
+                             const int32_t* slots, int64_t n_slots, const scan_view4* o, int64_t B,
+                             int64_t Hq, int64_t Hk, int64_t D, int64_t window, int64_t sinks,
+                             float scale, scan_dtype dt, cudaStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
