@@ -15,6 +15,7 @@
 // thread x owns four columns, thread y every 8th or 16th row, so all loads and
 // stores are whole 512-byte rows, and the read-out's sum over rows ends in shared
 // memory.
+#include "scan_linattn_tc.h"
 #include "scan_mixer.h"
 
 namespace scan {
@@ -213,6 +214,7 @@ scan_status lin_common(const LinArgs& a, scan_dtype dt, int64_t H, int64_t Dk, i
 bool given(const scan_view4* v) { return v && v->ptr; }
 
 cudaError_t lin_launch(const LinArgs& a, scan_dtype dt, cudaStream_t s) {
+  if (linattn_tc_fits(a, dt)) return launch_linattn_tc(a, s);
   return launch_linattn_general(a, dt, s);
 }
 
@@ -239,7 +241,7 @@ size_t linattn_workspace_bytes(int64_t B, int64_t T, int64_t H, int64_t Dk, int6
                                int64_t n_seqs) {
   if (B < 0 || T < 0 || H < 0 || n_seqs < 0 || Dk < 1 || Dv < 1 || Dk > kMixMaxDim || Dv > kMixMaxDim)
     return 0;
-  return kWsHeaderBytes;
+  return kWsHeaderBytes + linattn_tc_workspace_bytes(B, T, H, Dk, Dv, n_seqs);
 }
 
 scan_status linattn_fwd(const scan_view4* q, const scan_view4* k, const scan_view4* v,

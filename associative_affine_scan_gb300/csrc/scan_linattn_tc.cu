@@ -1,0 +1,662 @@
+// scan_linattn_tc.cu -- linear attention with a decay for each head, chunk by
+// chunk on the tensor cores (bf16 operands).
+//
+// One pass over (x1, x2, x3) (see LinPass; forward: q, k, v), a chunk of 128
+// steps at a time in the order of the recurrence. r counts a chunk's n steps in
+// that order, e = 1 forward and 0 reversed, S (K x V) is the state before it:
+//   out_r = scale ( lambda^(r + e) x1_r S + sum_{r' <= r} lambda^(r - r') (x1_r x2_r') x3_r' )
+//   S    <- lambda^n S + sum_r' lambda^(n - e - r') x2_r' x3_r'^T
+// Four products of 128^3 a chunk at K = V = 128 (the state's update twice, see
+// below): 5 x 512 tensor cycles against the 5600 that one SM's share of DRAM
+// needs for the chunk's 128 KB, so the kernel is bound by DRAM as long as copies,
+// products and the conversions between them overlap. Roles of a block (one per
+// SM), each working on its own part of the chain at any time:
+//   copy warp     two to four chunks of x1, x2, x3 in flight
+//   product warp  S1 = x1 x2^T, O = x1 S, S^T += x3'^T x2, O += P x3
+//   weights       P = S1 * lambda^(r - r'), masked, to bf16 (over S1 in tensor memory)
+//   state         S^T to bf16 for the next chunk's x1 S, and S^T *= lambda^n
+//   update        x3'^T = lambda^(n - e - r') x3^T as hi + lo bf16 parts: the
+//                 state's update is then exact to 2^-17, so that the state (fp32
+//                 in tensor memory) keeps fp32 accuracy over any number of chunks
+//   output        O *= lambda^(r + e) between the two products into it; O to bf16
+// The state lies transposed (lanes are v): its bf16 copy is then written by rows
+// into the operand layout, and the weighted operand of the update is one that the
+// tensor cores read from tensor memory, which shared memory has no room for.
+//
+// Few (sequence, head) rows: each is cut into segments; the segments' own states
+// are found first (x2 and x3 only), chained, and each segment then starts from
+// the state before it. This reads x2 and x3 twice.
+#include "scan_linattn_tc.h"
+#include "scan_tc.cuh"
+
+namespace scan {
+
+namespace {
+
+using namespace tc;
+
+constexpr int kChunk = 128;
+constexpr int kThreads = 18 * 32;  // four roles of four warps, a copy and a product warp
+constexpr uint32_t kHalf = kChunk * kPitch;  // bytes of one panel of a chunk
+
+struct TcPass {
+  CUtensorMap x1, x2, x3, out;
+  __nv_bfloat16* o;  // the output, for rows that a tensor copy must not write
+  int64_t o_sb, o_st, o_sh;
+  const float* s_in;
+  float* s_out;
+  float* seg;  // states after segments: [sequences][H][nseg - 1][K][V]
+  float s_in_mul, s_out_mul;
+  int s_in_t, K, V, reverse;
+};
+
+struct TcArgs {
+  TcPass pass[3];
+  const float* log_decay;
+  const int32_t* cu;
+  WsHeader* hdr;
+  int64_t T;
+  int n_seqs, H, nseg, cps;  // segments of a row, chunks of a segment
+  float scale;
+};
+
+template <int KP, int VP>
+struct Plan {
+  static constexpr int kX1 = kChunk * 2 * (KP > VP ? KP : VP);  // also stages the output
+  static constexpr int kX2 = kChunk * 2 * KP;
+  static constexpr int kX3 = kChunk * 2 * VP;
+  static constexpr int kStage = kX1 + kX2 + kX3;
+  static constexpr int kState = VP * KP * 2;
+  static constexpr int kStages = (KP == 128 && VP == 128) ? 2 : (KP == 64 && VP == 64) ? 4 : 2;
+  static constexpr int kTables = 2048;  // barriers, decay tables
+  static constexpr int kSmem = kStages * kStage + kState + kTables + 1024;
+};
+
+// The part of the sequence that a block works on, in processing order.
+struct Span {
+  int64_t beg, len;  // the sequence
+  int64_t first;     // first chunk of the segment, in processing order
+  int nch;           // chunks of the segment
+};
+
+// Where the c-th chunk of the segment lies, and how many steps it holds.
+__device__ __forceinline__ void chunk_at(const Span& s, bool reverse, int c, int64_t* t0, int* n) {
+  const int64_t all = (s.len + kChunk - 1) / kChunk;
+  const int64_t i = reverse ? all - 1 - (s.first + c) : s.first + c;
+  *t0 = i * kChunk;
+  const int64_t left = s.len - *t0;
+  *n = (int)(left < kChunk ? left : kChunk);
+}
+
+template <int KP, int VP, bool STATE_ONLY>
+__global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_constant__ TcArgs a) {
+  using P = Plan<KP, VP>;
+  extern __shared__ uint8_t raw[];
+  const uint32_t base = (smem_addr(raw) + 1023) & ~1023u;
+  uint8_t* const gen = raw + (base - smem_addr(raw));
+  const TcPass& p = a.pass[blockIdx.z];
+  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+
+  // shared memory: stages, the state's bf16 copy, tables, barriers
+  const uint32_t sState = base + P::kStages * P::kStage;
+  float* const tab = reinterpret_cast<float*>(gen + P::kStages * P::kStage + P::kState);
+  float* const wtab = tab;           // [128] weights of the update
+  float* const dtab = tab + 128;     // [32] lambda^d
+  const uint32_t bars = smem_addr(tab + 160);
+  const uint32_t bFull = bars, bEmpty = bars + 32, bS1 = bars + 64, bP = bars + 72, bSb = bars + 80,
+                 bSt = bars + 88, bVp = bars + 96, bOi = bars + 104, bOs = bars + 112, bOf = bars + 120,
+                 bOx = bars + 128, bClean = bars + 136, bOut = bars + 144;
+  uint32_t* const tmem_ptr = reinterpret_cast<uint32_t*>(tab + 160) + 40;
+  uint32_t* const stop_flag = tmem_ptr + 1;
+
+  // which (sequence, head, segment)
+  const int segs = STATE_ONLY ? a.nseg - 1 : a.nseg;
+  const int seg = blockIdx.x % segs;
+  const int64_t row = blockIdx.x / segs;
+  const int h = (int)(row % a.H);
+  const int64_t sq = row / a.H;
+  Span s{0, a.T, 0, 0};
+  if (a.cu) {
+    int64_t e;
+    seq_bounds(a.cu, (int)sq, a.T, &s.beg, &e);
+    s.len = e - s.beg;
+    if (blockIdx.x == 0 && blockIdx.z == 0 && warp == 0) check_seqlens(a.cu, a.n_seqs, a.T, a.hdr);
+  }
+  const int b = a.cu ? 0 : (int)sq;
+  const int64_t all = (s.len + kChunk - 1) / kChunk;
+  if (a.nseg == 1) {
+    s.nch = (int)all;
+  } else {
+    s.first = (int64_t)seg * a.cps;
+    s.nch = (int)(all - s.first < a.cps ? all - s.first : a.cps);
+  }
+  const bool rev = p.reverse != 0;
+  const int e = rev ? 0 : 1;
+  const float l2 = a.log_decay[h] * 1.44269504088896341f;
+
+  // initial state: the caller's for the first segment, else the one before
+  const float* s0 = nullptr;
+  int64_t s0k = 0, s0v = 0;  // its strides
+  float s0m = 1.f;
+  if (seg == 0) {
+    if (p.s_in) {
+      s0 = p.s_in + row * p.K * p.V;
+      s0k = p.s_in_t ? 1 : p.V;
+      s0v = p.s_in_t ? p.K : 1;
+      s0m = p.s_in_mul;
+    }
+  } else if (!STATE_ONLY) {
+    s0 = p.seg + (row * (a.nseg - 1) + seg - 1) * p.K * p.V;
+    s0k = p.V;
+    s0v = 1;
+  }
+  // final state: after a segment, or the caller's after the last
+  float* s1 = nullptr;
+  float s1m = 1.f;
+  if (STATE_ONLY) {
+    s1 = p.seg + (row * (a.nseg - 1) + seg) * p.K * p.V;
+  } else if (seg == a.nseg - 1 && p.s_out) {
+    s1 = p.s_out + row * p.K * p.V;
+    s1m = p.s_out_mul;
+  }
+  const bool packed = a.cu != nullptr;
+  const int late = s0 ? 0 : 1;  // the first chunk whose queries read a state
+
+  if (tid < 128) wtab[tid] = decay_pow(l2, rev ? tid + 1 : 127 - tid);
+  if (tid < 32) dtab[tid] = decay_pow(l2, tid);
+  if (tid == 0) {
+    *stop_flag = 0;
+    for (int i = 0; i < P::kStages; ++i) {
+      bar_init(bFull + 8 * i, 1);
+      bar_init(bEmpty + 8 * i, STATE_ONLY ? 1 : 2);
+    }
+    bar_init(bS1, 1);
+    bar_init(bP, 4);
+    bar_init(bSb, 4);
+    bar_init(bSt, 1);
+    bar_init(bVp, 4);
+    bar_init(bOi, 1);
+    bar_init(bOs, 4);
+    bar_init(bOf, 1);
+    bar_init(bOx, 4);
+    bar_init(bClean, 4);
+    bar_init(bOut, 4);
+    bar_init_fence();
+  }
+  if (warp == 17) tmem_alloc(smem_addr(tmem_ptr), 512);
+  fence_before();
+  __syncthreads();
+  fence_after();
+  const uint32_t tm = *tmem_ptr;
+  const uint32_t tS1 = tm, tO = tm + 128, tSt = tm + 256, tX = tm + 384;
+  const uint32_t lanes = (uint32_t)(warp % 4) << 21;  // this warp's first tensor-memory lane
+  const Stop stop{stop_flag, a.hdr};
+  const int role = warp / 4;
+
+  if (warp == 16) {
+    // ---- copies
+    if (lane == 0) {
+      for (int c = 0; c < s.nch; ++c) {
+        const int st = c % P::kStages;
+        if (c >= P::kStages && !bar_wait(bEmpty + 8 * st, (c / P::kStages - 1) & 1, stop)) break;
+        int64_t t0;
+        int n;
+        chunk_at(s, rev, c, &t0, &n);
+        const int t = (int)(s.beg + t0);
+        const uint32_t d = base + st * P::kStage, bar = bFull + 8 * st;
+        bar_expect(bar, (STATE_ONLY ? 0 : P::kX2) + P::kX2 + P::kX3);
+#pragma unroll
+        for (int i = 0; i < KP / 64; ++i) {
+          if (!STATE_ONLY) copy_in_4d(d + i * kHalf, &p.x1, bar, 64 * i, h, t, b);
+          copy_in_4d(d + P::kX1 + i * kHalf, &p.x2, bar, 64 * i, h, t, b);
+        }
+#pragma unroll
+        for (int i = 0; i < VP / 64; ++i)
+          copy_in_4d(d + P::kX1 + P::kX2 + i * kHalf, &p.x3, bar, 64 * i, h, t, b);
+      }
+    }
+  } else if (warp == 17) {
+    // ---- products
+    if (lane == 0) {
+      constexpr uint32_t dS1 = product_desc(128, 128, false, false);
+      constexpr uint32_t dOi = product_desc(128, VP, false, false);
+      constexpr uint32_t dSt = product_desc(128, KP, false, true);
+      constexpr uint32_t dO = product_desc(128, VP, false, true);
+      for (int c = 0; c < s.nch; ++c) {
+        const int st = c % P::kStages;
+        const uint32_t x1 = base + st * P::kStage, x2 = x1 + P::kX1, x3 = x2 + P::kX2;
+        int64_t t0;
+        int n;
+        chunk_at(s, rev, c, &t0, &n);
+        const bool have = c > 0 || s0;
+        const bool more = c + 1 < s.nch || s1;
+        if (!bar_wait(bFull + 8 * st, (c / P::kStages) & 1, stop)) break;
+        if (packed && n < kChunk && !bar_wait(bClean, 0, stop)) break;
+        if (!STATE_ONLY) {
+          mma_kk<KP>(tS1, x1, kHalf, x2, kHalf, dS1, false);
+          mma_commit(bS1);
+          if (c > 0 && !bar_wait(bOx, (c - 1) & 1, stop)) break;
+        }
+        if (!bar_wait(bSb, c & 1, stop)) break;
+        fence_after();
+        if (!STATE_ONLY && have) {
+          mma_kk<KP>(tO, x1, kHalf, sState, VP * kPitch, dOi, false);
+          mma_commit(bOi);
+        }
+        if (more) {
+          if (!bar_wait(bVp, c & 1, stop)) break;
+          fence_after();
+          mma_tn<kChunk>(tSt, tX, x2, kHalf, dSt, have);
+          mma_tn<kChunk>(tSt, tX + 64, x2, kHalf, dSt, true);
+        }
+        mma_commit(bSt);
+        mma_commit(bEmpty + 8 * st);
+        if (!STATE_ONLY) {
+          if (!bar_wait(bP, c & 1, stop)) break;
+          if (have && !bar_wait(bOs, (c - late) & 1, stop)) break;
+          fence_after();
+          mma_tn<kChunk>(tO, tS1, x3, kHalf, dO, have);
+          mma_commit(bOf);
+        }
+      }
+    }
+  } else if (role == 0 && !STATE_ONLY) {
+    // ---- weights: row i of the chunk in lane i. Blocks of 32 columns before
+    // (reversed: after) the warp's own rows factor into a row and a column power
+    // of lambda that are both at most 1; the diagonal block takes the power of
+    // the difference.
+    const int w = warp % 4;
+    float rf[4];
+#pragma unroll
+    for (int jb = 0; jb < 4; ++jb) {
+      const int d = rev ? 32 * jb - (32 * w + lane) : 32 * w + lane - (32 * jb + 31);
+      rf[jb] = d > 0 ? decay_pow(l2, d) : 1.f;
+    }
+    for (int c = 0; c < s.nch; ++c) {
+      if (!warp_wait(bS1, c & 1, stop)) break;
+      fence_after();
+#pragma unroll
+      for (int jb = 0; jb < 4; ++jb) {
+        uint32_t o[16];
+        if (rev ? jb < w : jb > w) {
+#pragma unroll
+          for (int x = 0; x < 16; ++x) o[x] = 0;
+        } else {
+          uint32_t r[32];
+          tmem_ld32(tS1 + lanes + 32 * jb, r);
+          ld_wait();
+          if (jb == w) {
+#pragma unroll
+            for (int x = 0; x < 32; ++x) {
+              const int d = rev ? x - lane : lane - x;
+              r[x] = d >= 0 ? __float_as_uint(__uint_as_float(r[x]) * dtab[d & 31]) : 0u;
+            }
+          } else {
+#pragma unroll
+            for (int x = 0; x < 32; ++x)
+              r[x] = __float_as_uint(__uint_as_float(r[x]) * (rf[jb] * dtab[rev ? x : 31 - x]));
+          }
+#pragma unroll
+          for (int x = 0; x < 16; ++x)
+            o[x] = pack_bf16(__uint_as_float(r[2 * x]), __uint_as_float(r[2 * x + 1]));
+        }
+        tmem_st16(tS1 + lanes + 16 * jb, o);
+      }
+      st_wait();
+      fence_before();
+      __syncwarp();
+      if (lane == 0) bar_arrive(bP);
+    }
+  } else if (role == 1) {
+    // ---- state: column v of S (a row of S^T) in lane v
+    const int v = tid - 128;
+    for (int c = 0; c < s.nch; ++c) {
+      int64_t t0;
+      int n;
+      chunk_at(s, rev, c, &t0, &n);
+      if (c > 0) {
+        if (!warp_wait(bSt, (c - 1) & 1, stop)) break;
+        fence_after();
+      }
+      if (c > 0 || s0) {
+        const float keep = decay_pow(l2, n);
+#pragma unroll
+        for (int kb = 0; kb < KP / 32; ++kb) {
+          uint32_t r[32];
+          if (c > 0) {
+            tmem_ld32(tSt + lanes + 32 * kb, r);
+            ld_wait();
+          } else {
+#pragma unroll
+            for (int x = 0; x < 32; ++x) {
+              const int k = 32 * kb + x;
+              r[x] = v < p.V && k < p.K ? __float_as_uint(s0m * s0[k * s0k + v * s0v]) : 0u;
+            }
+          }
+          if (!STATE_ONLY && v < VP) {
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+              uint32_t o[4];
+#pragma unroll
+              for (int x = 0; x < 4; ++x)
+                o[x] = pack_bf16(__uint_as_float(r[8 * y + 2 * x]), __uint_as_float(r[8 * y + 2 * x + 1]));
+              st_shared16(swizzled(sState + (kb / 2) * VP * kPitch, v, (kb % 2) * 4 + y), o[0], o[1], o[2],
+                          o[3]);
+            }
+          }
+#pragma unroll
+          for (int x = 0; x < 32; ++x) r[x] = __float_as_uint(__uint_as_float(r[x]) * keep);
+          tmem_st32(tSt + lanes + 32 * kb, r);
+        }
+        st_wait();
+        fence_async();
+        fence_before();
+      }
+      __syncwarp();
+      if (lane == 0) bar_arrive(bSb);
+    }
+    if (s1) {
+      bool ok = true;
+      if (s.nch > 0) {
+        ok = warp_wait(bSt, (s.nch - 1) & 1, stop);
+        fence_after();
+      }
+      if (ok) {
+#pragma unroll
+        for (int kb = 0; kb < KP / 32; ++kb) {
+          uint32_t r[32];
+          if (s.nch > 0) {
+            tmem_ld32(tSt + lanes + 32 * kb, r);
+            ld_wait();
+          }
+#pragma unroll
+          for (int x = 0; x < 32; ++x) {
+            const int k = 32 * kb + x;
+            if (v < p.V && k < p.K) {
+              const float f = s.nch > 0 ? __uint_as_float(r[x]) : s0 ? s0m * s0[k * s0k + v * s0v] : 0.f;
+              s1[(int64_t)k * p.V + v] = s1m * f;
+            }
+          }
+        }
+      }
+    }
+  } else if (role == 2) {
+    // ---- update: column v of x3 in lane v, weighted and split in two
+    const int v = tid - 256;
+    if (v >= VP) {  // lanes past V: zeros, once
+      uint32_t z[32];
+#pragma unroll
+      for (int x = 0; x < 32; ++x) z[x] = 0;
+#pragma unroll
+      for (int x = 0; x < 4; ++x) tmem_st32(tX + lanes + 32 * x, z);
+      st_wait();
+    }
+    for (int c = 0; c < s.nch; ++c) {
+      const int st = c % P::kStages;
+      const uint32_t x2 = base + st * P::kStage + P::kX1, x3 = x2 + P::kX2;
+      int64_t t0;
+      int n;
+      chunk_at(s, rev, c, &t0, &n);
+      if (!warp_wait(bFull + 8 * st, (c / P::kStages) & 1, stop)) break;
+      if (packed && n < kChunk) {
+        // the rows from n on belong to the next sequence (one such chunk a row)
+        const int left = kChunk - n;
+        for (int i = tid - 256; i < left * 8 * (KP + VP) / 64; i += 128) {
+          const int piece = i % 8, r = n + (i / 8) % left, pn = i / 8 / left;
+          st_shared16(x2 + pn * kHalf + r * kPitch + piece * 16, 0, 0, 0, 0);
+        }
+        fence_async();
+        __syncwarp();
+        if (lane == 0) bar_arrive(bClean);
+        __syncwarp();
+      }
+      if (c > 0 && !warp_wait(bSt, (c - 1) & 1, stop)) break;
+      fence_after();
+      if (v < VP && (c + 1 < s.nch || s1)) {
+        const uint32_t col = x3 + (v / 64) * kHalf + (v % 8) * 2;
+        const int piece = (v % 64) / 8;
+        const float* wt = rev ? wtab : wtab + (kChunk - n);
+#pragma unroll 1
+        for (int jb = 0; jb < 4; ++jb) {
+          uint32_t hi[16], lo[16];
+#pragma unroll
+          for (int x = 0; x < 16; ++x) {
+            float f[2], g[2];
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+              const int j = 32 * jb + 2 * x + y;
+              const uint32_t u = ld_shared_u16(col + j * kPitch + ((piece ^ (j & 7)) << 4));
+              f[y] = j < n ? __uint_as_float(u << 16) * wt[j] : 0.f;
+            }
+            hi[x] = pack_bf16(f[0], f[1]);
+            g[0] = f[0] - __uint_as_float(hi[x] << 16);
+            g[1] = f[1] - __uint_as_float(hi[x] & 0xffff0000u);
+            lo[x] = pack_bf16(g[0], g[1]);
+          }
+          tmem_st16(tX + lanes + 16 * jb, hi);
+          tmem_st16(tX + lanes + 64 + 16 * jb, lo);
+        }
+        st_wait();
+      }
+      fence_before();
+      __syncwarp();
+      if (lane == 0) bar_arrive(bVp);
+    }
+  } else if (role == 3 && !STATE_ONLY) {
+    // ---- output: row i of the chunk in lane i
+    const int i = tid - 384;
+    for (int c = 0; c < s.nch; ++c) {
+      const int st = c % P::kStages;
+      const uint32_t so = base + st * P::kStage;  // x1's place: both its products are done by then
+      int64_t t0;
+      int n;
+      chunk_at(s, rev, c, &t0, &n);
+      if (c > 0 || s0) {
+        if (!warp_wait(bOi, (c - late) & 1, stop)) break;
+        fence_after();
+        const int r = rev ? n - 1 - i : i;
+        const float f = r >= 0 ? decay_pow(l2, r + e) : 0.f;
+#pragma unroll
+        for (int vb = 0; vb < VP / 32; ++vb) {
+          uint32_t x[32];
+          tmem_ld32(tO + lanes + 32 * vb, x);
+          ld_wait();
+#pragma unroll
+          for (int y = 0; y < 32; ++y) x[y] = __float_as_uint(__uint_as_float(x[y]) * f);
+          tmem_st32(tO + lanes + 32 * vb, x);
+        }
+        st_wait();
+        fence_before();
+        __syncwarp();
+        if (lane == 0) bar_arrive(bOs);
+      }
+      if (!warp_wait(bOf, c & 1, stop)) break;
+      fence_after();
+      const bool direct = packed && n < kChunk;
+      __nv_bfloat16* const orow = p.o + b * p.o_sb + (s.beg + t0 + i) * p.o_st + h * p.o_sh;
+#pragma unroll
+      for (int vb = 0; vb < VP / 32; ++vb) {
+        uint32_t x[32];
+        tmem_ld32(tO + lanes + 32 * vb, x);
+        ld_wait();
+        if (vb == VP / 32 - 1) {
+          fence_before();
+          __syncwarp();
+          if (lane == 0) bar_arrive(bOx);
+        }
+#pragma unroll
+        for (int y = 0; y < 4; ++y) {
+          uint32_t o[4];
+#pragma unroll
+          for (int z = 0; z < 4; ++z)
+            o[z] = pack_bf16(a.scale * __uint_as_float(x[8 * y + 2 * z]),
+                             a.scale * __uint_as_float(x[8 * y + 2 * z + 1]));
+          const int col = 32 * vb + 8 * y;
+          if (direct) {
+            if (i < n && col < p.V)
+              *reinterpret_cast<uint4*>(orow + col) = make_uint4(o[0], o[1], o[2], o[3]);
+          } else {
+            st_shared16(swizzled(so + (vb / 2) * kHalf, i, (vb % 2) * 4 + y), o[0], o[1], o[2], o[3]);
+          }
+        }
+      }
+      if (!direct) fence_async();
+      __syncwarp();
+      if (lane == 0) bar_arrive(bOut);
+      if (i == 0 && bar_wait(bOut, c & 1, stop)) {
+        if (!direct) {
+#pragma unroll
+          for (int vb = 0; vb < VP / 64; ++vb)
+            copy_out_4d(&p.out, so + vb * kHalf, 64 * vb, h, (int)(s.beg + t0), b);
+          copy_out_commit();
+          copy_out_read();
+        }
+        bar_arrive(bEmpty + 8 * st);
+      }
+    }
+    if (i == 0) copy_out_done();
+  }
+  __syncwarp();
+  linger(stop);
+  fence_before();
+  __syncthreads();
+  if (warp == 17) {
+    fence_after();
+    tmem_free(tm, 512);
+  }
+}
+
+// The states after segments, from each segment's own: S_s = lambda^len S_(s-1) + own_s.
+__global__ void __launch_bounds__(256) linattn_chain_kernel(const __grid_constant__ TcArgs a) {
+  const TcPass& p = a.pass[blockIdx.z];
+  const int64_t n = (int64_t)p.K * p.V, row = blockIdx.y;
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i >= n) return;
+  const float l2 = a.log_decay[row % a.H] * 1.44269504088896341f;
+  const float keep = decay_pow(l2, a.cps * kChunk);  // segments after the first are whole
+  float* s = p.seg + row * (a.nseg - 1) * n + i;
+  float h = s[0];
+  for (int g = 1; g < a.nseg - 1; ++g) {
+    h = fmaf(keep, h, s[g * n]);
+    s[g * n] = h;
+  }
+}
+
+struct Split {
+  int nseg, cps;
+};
+
+// Segments of a row: enough that the blocks fill the SMs once (152, one block
+// each), whole chunks. A row's segments cost a second read of x2 and x3, so rows
+// that fill more than half of the SMs by themselves are left whole.
+Split split_rows(int64_t rows, int64_t T, bool packed) {
+  const int64_t nch = (T + kChunk - 1) / kChunk;
+  if (packed || rows <= 0 || rows * 2 > 152 || nch < 4) return Split{1, (int)nch};
+  int64_t n = 152 / rows;
+  if (n > nch / 2) n = nch / 2;
+  const int64_t cps = (nch + n - 1) / n;
+  n = (nch + cps - 1) / cps;
+  return Split{(int)n, (int)cps};
+}
+
+int padded(int d) { return d <= 64 ? 64 : 128; }
+
+template <int KP, int VP>
+cudaError_t launch_kv(const TcArgs& t, int npass, int64_t rows, cudaStream_t s) {
+  using P = Plan<KP, VP>;
+  static_assert(P::kSmem <= 232448, "fits a block's shared memory");
+  cudaError_t e = cudaFuncSetAttribute(linattn_tc_kernel<KP, VP, false>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, P::kSmem);
+  if (e != cudaSuccess) return e;
+  if (t.nseg > 1) {
+    e = cudaFuncSetAttribute(linattn_tc_kernel<KP, VP, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             P::kSmem);
+    if (e != cudaSuccess) return e;
+    linattn_tc_kernel<KP, VP, true>
+        <<<dim3((unsigned)(rows * (t.nseg - 1)), 1, npass), kThreads, P::kSmem, s>>>(t);
+    linattn_chain_kernel<<<dim3(KP * VP / 256, (unsigned)rows, npass), 256, 0, s>>>(t);
+  }
+  linattn_tc_kernel<KP, VP, false>
+      <<<dim3((unsigned)(rows * t.nseg), 1, npass), kThreads, P::kSmem, s>>>(t);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_passes(const TcArgs& t, int npass, int64_t rows, cudaStream_t s) {
+  const int K = padded(t.pass[0].K), V = padded(t.pass[0].V);
+  if (K == 64 && V == 64) return launch_kv<64, 64>(t, npass, rows, s);
+  if (K == 64) return launch_kv<64, 128>(t, npass, rows, s);
+  if (V == 64) return launch_kv<128, 64>(t, npass, rows, s);
+  return launch_kv<128, 128>(t, npass, rows, s);
+}
+
+}  // namespace
+
+// bf16 operands that tensor copies can address, and rows long enough that a
+// chunk's fixed chain of products is shorter than the recurrence.
+bool linattn_tc_fits(const LinArgs& a, scan_dtype dt) {
+  if (dt != SCAN_BF16 || a.T < 1 || a.T > 0x7fffffffLL) return false;
+  const int64_t n = a.cu ? a.n_seqs : a.B;
+  if (a.T < 32 * (a.cu ? n : 1)) return false;
+  for (int i = 0; i < a.npass; ++i) {
+    const LinPass& p = a.pass[i];
+    if (!heads_map_fits(p.x1, a.B, a.T, a.H) || !heads_map_fits(p.x2, a.B, a.T, a.H) ||
+        !heads_map_fits(p.x3, a.B, a.T, a.H) || !heads_map_fits(p.out, a.B, a.T, a.H))
+      return false;
+  }
+  return true;
+}
+
+size_t linattn_tc_workspace_bytes(int64_t B, int64_t T, int64_t H, int64_t Dk, int64_t Dv,
+                                  int64_t n_seqs) {
+  if (n_seqs > 0) return 0;
+  const Split sp = split_rows(B * H, T, false);
+  return (size_t)(3 * B * H * (sp.nseg - 1) * Dk * Dv) * 4;
+}
+
+cudaError_t launch_linattn_tc(const LinArgs& a, cudaStream_t s) {
+  const int64_t n = a.cu ? a.n_seqs : a.B, rows = n * a.H;
+  const Split sp = split_rows(rows, a.T, a.cu != nullptr);
+  TcArgs t[2];
+  int count[2] = {0, 0};
+  for (int i = 0; i < a.npass; ++i) {
+    const LinPass& p = a.pass[i];
+    // passes of one padded shape go in one launch
+    const int g = i > 0 && (padded(p.K) != padded(a.pass[0].K) || padded(p.V) != padded(a.pass[0].V));
+    TcPass& d = t[g].pass[count[g]++];
+    if (!encode_heads_map(&d.x1, p.x1, a.B, a.T, a.H, p.K, kChunk) ||
+        !encode_heads_map(&d.x2, p.x2, a.B, a.T, a.H, p.K, kChunk) ||
+        !encode_heads_map(&d.x3, p.x3, a.B, a.T, a.H, p.V, kChunk) ||
+        !encode_heads_map(&d.out, p.out, a.B, a.T, a.H, p.V, kChunk))
+      return cudaErrorInvalidValue;
+    d.o = static_cast<__nv_bfloat16*>(p.out.ptr);
+    d.o_sb = p.out.stride_b;
+    d.o_st = p.out.stride_t;
+    d.o_sh = p.out.stride_h;
+    d.s_in = p.s_in;
+    d.s_out = p.s_out;
+    d.s_in_mul = p.s_in_mul;
+    d.s_out_mul = p.s_out_mul;
+    d.s_in_t = p.s_in_t;
+    d.K = p.K;
+    d.V = p.V;
+    d.reverse = p.reverse;
+    d.seg = a.ws + (int64_t)i * rows * (sp.nseg - 1) * p.K * p.V;
+  }
+  for (int g = 0; g < 2; ++g) {
+    if (!count[g]) continue;
+    t[g].log_decay = a.log_decay;
+    t[g].cu = a.cu;
+    t[g].hdr = a.hdr;
+    t[g].T = a.T;
+    t[g].n_seqs = a.n_seqs;
+    t[g].H = a.H;
+    t[g].nseg = sp.nseg;
+    t[g].cps = sp.cps;
+    t[g].scale = a.scale;
+    const cudaError_t e = launch_passes(t[g], count[g], rows, s);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
+}
+
+}  // namespace scan

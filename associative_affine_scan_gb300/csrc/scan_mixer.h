@@ -98,6 +98,10 @@ __device__ __forceinline__ bool locate_tile(const int32_t* cu, int n, int64_t T,
   return false;
 }
 
+bool heads_map_fits(const scan_view4& v, int64_t B, int64_t T, int64_t H);
+bool encode_heads_map(CUtensorMap* m, const scan_view4& v, int64_t B, int64_t T, int64_t H, int64_t D,
+                      int rows);
+
 // ---------------------------------------------------------------------------
 // linear attention: one direction of the recurrence
 //   S_t = lambda S_{t-1} + x2_t x3_t^T,  out_t = scale x1_t S_t       (forward)
@@ -150,6 +154,48 @@ struct WinArgs {
   float* ws;
   size_t ws_floats;
 };
+
+// Tiles of `rows` keys that the queries at positions [p0, p1] see: those that hold
+// first tokens, [0, sink), and those of the window, [near, last].
+struct KeyTiles {
+  int64_t sink, near, last;  // sink <= near; last < near: none
+  __device__ int64_t count() const { return sink + (last >= near ? last - near + 1 : 0); }
+  __device__ int64_t at(int64_t i) const { return i < sink ? i : near + (i - sink); }
+};
+__device__ __forceinline__ KeyTiles key_tiles(int64_t p0, int64_t p1, int64_t Tk, int64_t W, int64_t S,
+                                              int rows) {
+  KeyTiles t{0, 0, -1};
+  if (p1 < 0 || Tk <= 0) return t;
+  const int64_t hi = p1 < Tk ? p1 : Tk - 1;
+  int64_t lo = p0 - W + 1;
+  lo = lo < 0 ? 0 : lo;
+  t.near = lo / rows;
+  t.last = hi / rows;
+  const int64_t s = S < hi + 1 ? S : hi + 1;
+  const int64_t ns = (s + rows - 1) / rows;
+  t.sink = ns < t.near ? ns : t.near;
+  return t;
+}
+
+// Where a tile of rows lies: the sequence it belongs to and its first row there.
+struct TileRows {
+  int64_t qbeg, kbeg;   // first query and key row of the sequence
+  int64_t nq, nk, off;  // rows of each, and the position of the first query
+  int64_t t0;           // first row of the tile within the sequence
+};
+// Tile `tile` of `rows` rows; a whole warp (packed sequences are searched). False
+// past the last tile.
+__device__ __forceinline__ bool tile_rows(const int32_t* cu, int n_seqs, int64_t Tq, int64_t Tk,
+                                          int64_t tile, int rows, TileRows* r) {
+  if (!cu) {
+    *r = TileRows{0, 0, Tq, Tk, Tk - Tq, tile * rows};
+    return true;
+  }
+  int64_t beg, end, local;
+  if (!locate_tile(cu, n_seqs, Tq, tile, rows, &beg, &end, &local)) return false;
+  *r = TileRows{beg, beg, end - beg, end - beg, 0, local * rows};
+  return true;
+}
 
 cudaError_t launch_window_general_fwd(const WinArgs& a, scan_dtype dt, cudaStream_t s);
 cudaError_t launch_window_general_bwd(const WinArgs& a, scan_dtype dt, cudaStream_t s);

@@ -86,4 +86,32 @@ bool encode_blocks_map(CUtensorMap* m, const void* ptr, int64_t B, int64_t T, in
   return r == CUDA_SUCCESS;
 }
 
+// Whether a [B, T, H, D] bf16 operand has a map: 16-byte aligned, and no axis
+// that repeats or reverses elements.
+bool heads_map_fits(const scan_view4& v, int64_t B, int64_t T, int64_t H) {
+  if (reinterpret_cast<uintptr_t>(v.ptr) % 16) return false;
+  const int64_t n[3] = {B, T, H}, s[3] = {v.stride_b, v.stride_t, v.stride_h};
+  for (int i = 0; i < 3; ++i)
+    if (n[i] > 1 && (s[i] <= 0 || s[i] % 8 || s[i] >= (1LL << 38))) return false;
+  return true;
+}
+
+// A [B, T, H, D] bf16 operand as {D, H, T, B}: a box is 64 columns of one head by
+// `rows` steps, written to shared memory with the 128-byte swizzle. Columns from D
+// and steps from T on read as zeros and are not written.
+bool encode_heads_map(CUtensorMap* m, const scan_view4& v, int64_t B, int64_t T, int64_t H, int64_t D,
+                      int rows) {
+  std::call_once(g_encode_once, load_encoder);
+  if (!g_encode || !heads_map_fits(v, B, T, H)) return false;
+  // an axis of one element has no stride of its own
+  const auto stride = [](int64_t n, int64_t s) { return (cuuint64_t)(n > 1 ? s * 2 : 16); };
+  const cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)H, (cuuint64_t)T, (cuuint64_t)B};
+  const cuuint64_t strides[3] = {stride(H, v.stride_h), stride(T, v.stride_t), stride(B, v.stride_b)};
+  const cuuint32_t box[4] = {64, 1, (cuuint32_t)rows, 1};
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  return g_encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, v.ptr, dims, strides, box, estr,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 }  // namespace scan

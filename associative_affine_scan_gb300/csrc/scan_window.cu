@@ -15,33 +15,12 @@
 // multiply-adds, four threads a row: bound by the shared-memory reads of the
 // products. Only tiles with a seen pair are visited.
 #include "scan_mixer.h"
+#include "scan_window_tc.h"
 
 namespace scan {
 namespace {
 
 constexpr int kTile = 32;
-
-// Key tiles (of `rows` keys) that the queries at positions [p0, p1] see: the
-// tiles [0, sink) that hold first tokens before the window, then [near, last].
-struct KeyTiles {
-  int64_t sink, near, last;  // last < near: none
-  __device__ int64_t count() const { return sink + (last >= near ? last - near + 1 : 0); }
-  __device__ int64_t at(int64_t i) const { return i < sink ? i : near + (i - sink); }
-};
-__device__ __forceinline__ KeyTiles key_tiles(int64_t p0, int64_t p1, int64_t Tk, int64_t W,
-                                              int64_t S, int rows) {
-  KeyTiles t{0, 0, -1};
-  if (p1 < 0 || Tk <= 0) return t;
-  const int64_t hi = p1 < Tk ? p1 : Tk - 1;
-  int64_t lo = p0 - W + 1;
-  lo = lo < 0 ? 0 : lo;
-  t.near = lo / rows;
-  t.last = hi / rows;
-  const int64_t s = S < hi + 1 ? S : hi + 1;
-  const int64_t ns = (s + rows - 1) / rows;
-  t.sink = ns < t.near ? ns : t.near;
-  return t;
-}
 
 template <typename T>
 __device__ __forceinline__ View<T> vw(const scan_view4& v) {
@@ -62,30 +41,6 @@ __device__ __forceinline__ bool seen(int64_t i, int64_t j, const WinArgs& a) {
   return j <= i && (i - j < a.W || j < a.S);
 }
 
-// Where a tile of query rows (or key rows) lies.
-struct Rows {
-  int64_t qbeg, kbeg;  // first query and key row of the sequence
-  int64_t nq, nk, off; // rows of each, and the position of the first query
-  int64_t t0;          // first row of the tile within the sequence
-};
-__device__ __forceinline__ bool rows_of(const WinArgs& a, int64_t tile, Rows* r) {
-  if (!a.cu) {
-    r->qbeg = r->kbeg = 0;
-    r->nq = a.Tq;
-    r->nk = a.Tk;
-    r->off = a.Tk - a.Tq;
-    r->t0 = tile * kTile;
-    return true;
-  }
-  int64_t beg, end, local;
-  if (!locate_tile(a.cu, a.n_seqs, a.Tq, tile, kTile, &beg, &end, &local)) return false;
-  r->qbeg = r->kbeg = beg;
-  r->nq = r->nk = end - beg;
-  r->off = 0;
-  r->t0 = local * kTile;
-  return true;
-}
-
 constexpr int kLd = kMixMaxDim + 1;  // row pitch: rows of a column lie in different banks
 constexpr int kColsT = kMixMaxDim / 4;
 
@@ -95,8 +50,8 @@ __global__ void __launch_bounds__(4 * kTile) window_fwd_general(const WinArgs a)
   float *sq = sm, *sk = sq + kTile * kLd, *sv = sk + kTile * kLd, *sp = sv + kTile * kLd;
   if (a.cu && blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x < 32)
     check_seqlens(a.cu, a.n_seqs, a.Tq, a.hdr);
-  Rows g;
-  if (!rows_of(a, blockIdx.x, &g)) return;
+  TileRows g;
+  if (!tile_rows(a.cu, a.n_seqs, a.Tq, a.Tk, blockIdx.x, kTile, &g)) return;
   const int h = blockIdx.y % a.Hq, hk = h / (a.Hq / a.Hk);
   const int64_t b = blockIdx.y / a.Hq;
   const int r = threadIdx.x >> 2, c = threadIdx.x & 3;
@@ -178,8 +133,8 @@ __global__ void __launch_bounds__(4 * kTile) window_dq_general(const WinArgs a) 
   extern __shared__ float sm[];
   float *sq = sm, *sd = sq + kTile * kLd, *sk = sd + kTile * kLd, *sv = sk + kTile * kLd,
         *sp = sv + kTile * kLd;
-  Rows g;
-  if (!rows_of(a, blockIdx.x, &g)) return;
+  TileRows g;
+  if (!tile_rows(a.cu, a.n_seqs, a.Tq, a.Tk, blockIdx.x, kTile, &g)) return;
   const int h = blockIdx.y % a.Hq, hk = h / (a.Hq / a.Hk);
   const int64_t b = blockIdx.y / a.Hq;
   const int r = threadIdx.x >> 2, c = threadIdx.x & 3;
@@ -234,12 +189,8 @@ __global__ void __launch_bounds__(4 * kTile) window_dkv_general(const WinArgs a)
   extern __shared__ float sm[];
   float *sk = sm, *sv = sk + kTile * kLd, *sq = sv + kTile * kLd, *sd = sq + kTile * kLd,
         *sp = sd + kTile * kLd, *ss = sp + kTile * (kTile + 1), *st = ss + kTile * (kTile + 1);
-  Rows g;
-  if (a.cu) {
-    if (!rows_of(a, blockIdx.x, &g)) return;
-  } else {
-    g = Rows{0, 0, a.Tq, a.Tk, a.Tk - a.Tq, (int64_t)blockIdx.x * kTile};
-  }
+  TileRows g;
+  if (!tile_rows(a.cu, a.n_seqs, a.Tq, a.Tk, blockIdx.x, kTile, &g)) return;
   const int hk = blockIdx.y % a.Hk, G = a.Hq / a.Hk;
   const int64_t b = blockIdx.y / a.Hk;
   const int r = threadIdx.x >> 2, c = threadIdx.x & 3;
@@ -470,7 +421,8 @@ size_t window_attn_workspace_bytes(int64_t B, int64_t Tq, int64_t Tk, int64_t Hq
       sinks < 0 || n_seqs < 0)
     return 0;
   if (!backward) return kWsHeaderBytes;
-  return kWsHeaderBytes + round_up((size_t)(B * Hq * Tq) * 4, 256);
+  return kWsHeaderBytes + round_up((size_t)(B * Hq * Tq) * 4, 256) +
+         window_tc_bwd_floats(B, Tq, Tk, Hk, D, window, sinks, n_seqs > 0) * 4;
 }
 
 scan_status window_attn_fwd(const scan_view4* q, const scan_view4* k, const scan_view4* v,
@@ -498,7 +450,9 @@ scan_status window_attn_fwd(const scan_view4* q, const scan_view4* k, const scan
   if (Tk > 0) a.k = *k, a.v = *v;
   a.o = *o;
   a.lse = lse;
-  return launch_window_general_fwd(a, dt, stream) == cudaSuccess ? SCAN_OK : SCAN_ERR_CUDA;
+  const cudaError_t e = window_tc_fits(a, dt, false) ? launch_window_tc_fwd(a, stream)
+                                                     : launch_window_general_fwd(a, dt, stream);
+  return e == cudaSuccess ? SCAN_OK : SCAN_ERR_CUDA;
 }
 
 scan_status window_attn_bwd(const scan_view4* q, const scan_view4* k, const scan_view4* v,
@@ -529,7 +483,15 @@ scan_status window_attn_bwd(const scan_view4* q, const scan_view4* k, const scan
   if (Tk > 0) a.k = *k, a.v = *v, a.dk = *dk, a.dv = *dv;
   a.lse = const_cast<float*>(lse);
   a.delta = a.ws;
-  return launch_window_general_bwd(a, dt, stream) == cudaSuccess ? SCAN_OK : SCAN_ERR_CUDA;
+  cudaError_t e;
+  if (window_tc_fits(a, dt, true)) {
+    e = delta_launch<__nv_bfloat16>(a, stream);
+    if (e == cudaSuccess)
+      e = launch_window_tc_bwd(a, a.ws + round_up((size_t)(B * Hq * Tq) * 4, 256) / 4, stream);
+  } else {
+    e = launch_window_general_bwd(a, dt, stream);
+  }
+  return e == cudaSuccess ? SCAN_OK : SCAN_ERR_CUDA;
 }
 
 scan_status window_attn_step(const scan_view4* q, const scan_view4* k, const scan_view4* v,

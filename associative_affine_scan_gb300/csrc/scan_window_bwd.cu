@@ -1,0 +1,696 @@
+// scan_window_bwd.cu -- backward of sliding-window attention with first tokens
+// that stay visible, on the tensor cores (bf16 operands).
+//
+//   p = 2^(scale log2(e) q k - lse log2(e)), ds = p (do v - delta), delta = do o
+//   dv = sum p do, dk = scale sum ds q (over queries and the heads that share the
+//   key head), dq = scale sum ds k (over keys)
+//
+// Two kernels, each with its sums in tensor memory and no sum across blocks: the
+// five products become seven, but no result depends on the order in which blocks
+// run and nothing is added in global memory.
+//   keys:    a block owns 128 keys and walks the tiles of 128 queries that see
+//            them: S = k q^T, dP = v do^T, dv += P do, dk += dS q. Keys are the
+//            rows of S, so P and dS (bf16, over S and dP in tensor memory) are
+//            read as they lie by the two second products.
+//   queries: a block owns 128 queries of a head and walks the key tiles they see:
+//            S = q k^T, dP = do v^T, dq += dS k.
+// The order of issue keeps the tensor cores busy while two warpgroups turn S and
+// dP into P and dS, half of the columns each: the first product of the next tile
+// is issued between the two that wait for them. Both are bound by the tensor
+// cores (512 cycles a product at D = 128).
+//
+// The tile of keys that holds the first tokens is seen by every later query: its
+// walk is cut into pieces of about the length of any other tile's, whose partial
+// sums (fp32, workspace) are added in order by a last kernel.
+#include "scan_tc.cuh"
+#include "scan_window_tc.h"
+
+namespace scan {
+namespace {
+
+using namespace tc;
+
+constexpr int kRows = 128;
+constexpr int kThreads = 10 * 32;  // two warpgroups of softmax, copies, products
+constexpr uint32_t kHalf = kRows * kPitch;
+
+struct BwdArgs {
+  CUtensorMap q, k, v, dout, dq, dk, dv;
+  __nv_bfloat16 *dqp, *dkp, *dvp;
+  int64_t dq_sb, dq_st, dq_sh, dk_sb, dk_st, dk_sh, dv_sb, dv_st, dv_sh;
+  const float* lse;
+  const float* delta;
+  float* part;  // [B, Hk, pieces, sink tiles, 2, 128, D]
+  const int32_t* cu;
+  WsHeader* hdr;
+  int64_t Tq, Tk, W, S;
+  int n_seqs, Hq, Hk, G, D;
+  int sink_tiles, pieces;  // key tiles whose walk is cut (dense only), and into how many
+  float sl2, scale;
+};
+
+template <int DP>
+struct Plan {
+  static constexpr int kTileBytes = kRows * DP * 2;
+  static constexpr int kSlots = DP == 128 ? 5 : 8;
+  static constexpr int kMisc = 4096;  // barriers, row statistics
+  static constexpr int kSmem = (2 + kSlots) * kTileBytes + 1024 + (DP == 128 ? 2048 : kMisc);
+};
+
+// Rows [from, 128) of a tile to zeros, by 256 threads.
+template <int DP>
+__device__ __forceinline__ void clear_rows(uint32_t tile, int from, int t) {
+  const int left = kRows - from;
+  for (int i = t; i < left * 8 * (DP / 64); i += 256)
+    st_shared16(tile + (i / 8 / left) * kHalf + (from + i / 8 % left) * kPitch + (i % 8) * 16, 0, 0, 0, 0);
+  fence_async();
+  __syncwarp();
+}
+
+// A row of D fp32 sums in tensor memory times f, as bf16: to a tile in shared
+// memory, or straight to `out`.
+template <int DP>
+__device__ __forceinline__ void write_row(uint32_t tsum, float f, uint32_t tile, int r, bool direct, bool live,
+                                          __nv_bfloat16* out, int D) {
+#pragma unroll
+  for (int i = 0; i < DP / 32; ++i) {
+    uint32_t o[32];
+    tmem_ld32(tsum + 32 * i, o);
+    ld_wait();
+#pragma unroll
+    for (int c = 0; c < 32; c += 8) {
+      uint32_t w[4];
+#pragma unroll
+      for (int y = 0; y < 4; ++y)
+        w[y] = pack_bf16(__uint_as_float(o[c + 2 * y]) * f, __uint_as_float(o[c + 2 * y + 1]) * f);
+      const int col = 32 * i + c;
+      if (direct) {
+        if (live && col < D) *reinterpret_cast<uint4*>(out + col) = make_uint4(w[0], w[1], w[2], w[3]);
+      } else {
+        st_shared16(swizzled(tile + (col / 64) * kHalf, r, col % 64 / 8), w[0], w[1], w[2], w[3]);
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+
+template <int DP>
+__global__ void __launch_bounds__(kThreads, 1) window_dkv_kernel(const __grid_constant__ BwdArgs a) {
+  using P = Plan<DP>;
+  constexpr int NS = P::kSlots;
+  extern __shared__ uint8_t raw[];
+  const uint32_t base = (smem_addr(raw) + 1023) & ~1023u;
+  uint8_t* const gen = raw + (base - smem_addr(raw));
+  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+  const uint32_t sK = base, sV = base + P::kTileBytes, sR = base + 2 * P::kTileBytes;
+  uint32_t* const misc = reinterpret_cast<uint32_t*>(gen + (2 + NS) * P::kTileBytes);
+  const uint32_t bars = smem_addr(misc);
+  const uint32_t bKV = bars, bFull = bars + 8, bEmpty = bFull + 8 * NS, bS = bEmpty + 8 * NS, bDp = bS + 8,
+                 bP = bDp + 8, bDs = bP + 8, bEnd = bDs + 8, bOut = bEnd + 8, bStat = bOut + 16;
+  uint32_t* const tmem_ptr = misc + 64;
+  uint32_t* const stop_flag = misc + 65;
+  float* const stat = reinterpret_cast<float*>(misc + 72);  // 128 of (lse log2(e), delta)
+
+  // which keys: the cut tiles' pieces first, then the others
+  const int hk = blockIdx.y % a.Hk, b = blockIdx.y / a.Hk;
+  int piece = -1;
+  int64_t tile = blockIdx.x;
+  if (a.pieces > 1) {
+    const int cut = a.sink_tiles * a.pieces;
+    if (blockIdx.x < cut) {
+      piece = blockIdx.x % a.pieces;
+      tile = blockIdx.x / a.pieces;
+    } else {
+      tile = blockIdx.x - cut + a.sink_tiles;
+    }
+  }
+  TileRows g;
+  if (!tile_rows(a.cu, a.n_seqs, a.Tq, a.Tk, tile, kRows, &g)) return;
+  // query tiles [lo, hi] that see a key of the tile, over the heads that share it
+  const int64_t kend = g.t0 + kRows < g.nk ? g.t0 + kRows : g.nk;
+  int64_t qa = g.t0 - g.off, qz = kend - 1 + a.W - 1 - g.off;
+  qa = qa < 0 ? 0 : qa;
+  if (g.t0 < a.S || qz > g.nq - 1) qz = g.nq - 1;
+  const int64_t lo = qa / kRows;
+  const int per = qz < qa ? 0 : (int)(qz / kRows - lo + 1);
+  int u0 = 0, u1 = per * a.G;
+  if (piece >= 0) {
+    const int64_t total = u1;
+    u0 = (int)(total * piece / a.pieces);
+    u1 = (int)(total * (piece + 1) / a.pieces);
+  }
+  const int n = u1 - u0;
+  const auto head = [&](int u) { return hk * a.G + (u0 + u) / per; };
+  const auto qrow = [&](int u) { return (lo + (u0 + u) % per) * kRows; };
+
+  if (tid == 0) {
+    *stop_flag = 0;
+    bar_init(bKV, 1);
+    for (int i = 0; i < NS; ++i) {
+      bar_init(bFull + 8 * i, 1);
+      bar_init(bEmpty + 8 * i, 1);
+    }
+    bar_init(bS, 1);
+    bar_init(bDp, 1);
+    bar_init(bP, 8);
+    bar_init(bDs, 8);
+    bar_init(bEnd, 1);
+    bar_init(bOut, 4);
+    bar_init(bOut + 8, 4);
+    bar_init(bStat, 8);
+    bar_init_fence();
+  }
+  if (warp == 9) tmem_alloc(smem_addr(tmem_ptr), 512);
+  fence_before();
+  __syncthreads();
+  fence_after();
+  const uint32_t tm = *tmem_ptr, tS = tm, tDp = tm + 128, tDv = tm + 256, tDk = tm + 384;
+  const Stop stop{stop_flag, a.hdr};
+
+  if (warp == 8) {
+    // ---- copies: keys and values once, then queries and output gradients
+    if (lane == 0 && n > 0) {
+      bar_expect(bKV, 2 * P::kTileBytes);
+#pragma unroll
+      for (int i = 0; i < DP / 64; ++i) {
+        copy_in_4d(sK + i * kHalf, &a.k, bKV, 64 * i, hk, (int)(g.kbeg + g.t0), b);
+        copy_in_4d(sV + i * kHalf, &a.v, bKV, 64 * i, hk, (int)(g.kbeg + g.t0), b);
+      }
+      for (int u = 0; u < 2 * n; ++u) {
+        const int sl = u % NS;
+        if (u >= NS && !bar_wait(bEmpty + 8 * sl, (u / NS - 1) & 1, stop)) break;
+        const CUtensorMap* m = u & 1 ? &a.dout : &a.q;
+        bar_expect(bFull + 8 * sl, P::kTileBytes);
+#pragma unroll
+        for (int i = 0; i < DP / 64; ++i)
+          copy_in_4d(sR + sl * P::kTileBytes + i * kHalf, m, bFull + 8 * sl, 64 * i, head(u / 2),
+                     (int)(g.qbeg + qrow(u / 2)), b);
+      }
+    }
+  } else if (warp == 9) {
+    // ---- products
+    if (lane == 0 && n > 0) {
+      constexpr uint32_t dS = product_desc(128, 128, false, false);
+      constexpr uint32_t dO = product_desc(128, DP, false, true);
+      const auto slot = [&](int u) { return sR + (u % NS) * P::kTileBytes; };
+      const auto full = [&](int u) { return bar_wait(bFull + 8 * (u % NS), (u / NS) & 1, stop); };
+      // two halves of 64 query columns, each packed where its scores were
+      const auto second = [&](uint32_t d, uint32_t w, uint32_t t, bool add) {
+        mma_tn<64>(d, w, t, kHalf, dO, add);
+        mma_tn<64>(d, w + 64, t + 64 * kPitch, kHalf, dO, true);
+      };
+      bool ok = bar_wait(bKV, 0, stop) && full(0) && full(1);
+      if (ok) {
+        mma_kk<DP>(tS, sK, kHalf, slot(0), kHalf, dS, false);
+        mma_commit(bS);
+        mma_kk<DP>(tDp, sV, kHalf, slot(1), kHalf, dS, false);
+        mma_commit(bDp);
+      }
+      for (int u = 0; ok && u < n; ++u) {
+        if (!(ok = bar_wait(bP, u & 1, stop))) break;
+        fence_after();
+        second(tDv, tS, slot(2 * u + 1), u > 0);
+        if (u + 1 < n) {
+          if (!(ok = full(2 * u + 2))) break;
+          mma_kk<DP>(tS, sK, kHalf, slot(2 * u + 2), kHalf, dS, false);
+          mma_commit(bS);
+        }
+        if (!(ok = bar_wait(bDs, u & 1, stop))) break;
+        fence_after();
+        second(tDk, tDp, slot(2 * u), u > 0);
+        mma_commit(bEmpty + 8 * (2 * u % NS));
+        mma_commit(bEmpty + 8 * ((2 * u + 1) % NS));
+        if (u + 1 < n) {
+          if (!(ok = full(2 * u + 3))) break;
+          mma_kk<DP>(tDp, sV, kHalf, slot(2 * u + 3), kHalf, dS, false);
+          mma_commit(bDp);
+        }
+      }
+      mma_commit(bEnd);
+    }
+  } else {
+    // ---- P and dS: key r of the tile in lane r, 64 query columns a warpgroup
+    const int w = warp / 4, r = tid - 128 * w;
+    const uint32_t lanes = (uint32_t)(warp % 4) << 21;
+    const int64_t j = g.t0 + r;
+    const int64_t jlo = g.t0 + (warp % 4) * 32, jhi = jlo + 31;  // the warp's keys
+    const bool first = j < a.S;
+    bool ok = true;
+    // this thread's share of the row statistics: thread t < 128 has query t
+    const auto fetch = [&](int u, float* x, float* y) {
+      const int64_t row = qrow(u) + tid;
+      *x = INFINITY;  // rows past the sequence: p = 0
+      *y = 0.f;
+      if (u < n && tid < kRows && row < g.nq) {
+        const int64_t at = ((int64_t)b * a.Hq + head(u)) * a.Tq + g.qbeg + row;
+        *x = a.lse[at] * 1.44269504088896341f;
+        *y = a.delta[at];
+      }
+    };
+    float nx = 0.f, ny = 0.f;
+    if (n > 0) fetch(0, &nx, &ny);
+    for (int u = 0; u < n; ++u) {
+      // the statistics of the last tile have been read by all (they arrived on bDs after)
+      if (u > 0 && !(ok = warp_wait(bDs, (u - 1) & 1, stop))) break;
+      if (tid < kRows) *reinterpret_cast<float2*>(stat + 2 * tid) = make_float2(nx, ny);
+      __syncwarp();
+      if (lane == 0) bar_arrive(bStat);
+      if (u + 1 < n) fetch(u + 1, &nx, &ny);
+      const int64_t t0 = qrow(u), p0 = g.off + t0 + 64 * w;  // first position of the columns
+      if (!(ok = warp_wait(bStat, u & 1, stop))) break;
+      if (!(ok = warp_wait(bS, u & 1, stop))) break;
+      fence_after();
+      uint32_t s[2][32];
+      tmem_ld32(tS + lanes + 64 * w, s[0]);
+      tmem_ld32(tS + lanes + 64 * w + 32, s[1]);
+      ld_wait();
+      // columns [lo, hi] see key j
+      const bool whole = jhi <= p0 && (p0 + 63 - jlo < a.W || jhi < a.S) && t0 + 64 * w + 63 < g.nq;
+      if (whole) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int c = 0; c < 32; ++c)
+            s[i][c] = __float_as_uint(
+                fast_exp2(fmaf(__uint_as_float(s[i][c]), a.sl2, -stat[2 * (64 * w + 32 * i + c)])));
+      } else {
+        const int64_t left = g.nq - t0 - 64 * w - 1;
+        int64_t z = first ? 63 : j + a.W - 1 - p0;
+        z = z < left ? z : left;
+        const int lo_c = (int)(j - p0 < -1 ? -1 : j - p0 > 64 ? 64 : j - p0), hi_c = (int)(z < -1 ? -1 : z > 63 ? 63 : z);
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int c = 0; c < 32; ++c) {
+            const int x = 32 * i + c;
+            const float e = fast_exp2(fmaf(__uint_as_float(s[i][c]), a.sl2, -stat[2 * (64 * w + x)]));
+            s[i][c] = x >= lo_c && x <= hi_c ? __float_as_uint(e) : 0u;
+          }
+      }
+      {
+        uint32_t o[32];
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int c = 0; c < 16; ++c)
+            o[16 * i + c] = pack_bf16(__uint_as_float(s[i][2 * c]), __uint_as_float(s[i][2 * c + 1]));
+        tmem_st32(tS + lanes + 64 * w, o);
+      }
+      const int past = a.cu && t0 + kRows > g.nq ? (int)(g.nq - t0) : kRows;
+      if (past < kRows) {  // rows of the next sequence
+        const int sl = (2 * u + 1) % NS;
+        if (!(ok = warp_wait(bFull + 8 * sl, ((2 * u + 1) / NS) & 1, stop))) break;
+        clear_rows<DP>(sR + sl * P::kTileBytes, past, tid);
+      }
+      st_wait();
+      fence_before();
+      __syncwarp();
+      if (lane == 0) bar_arrive(bP);
+      if (!(ok = warp_wait(bDp, u & 1, stop))) break;
+      fence_after();
+      uint32_t o[32];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        uint32_t d[32];
+        tmem_ld32(tDp + lanes + 64 * w + 32 * i, d);
+        ld_wait();
+#pragma unroll
+        for (int c = 0; c < 32; c += 2) {
+          float e[2];
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {
+            const float p = __uint_as_float(s[i][c + y]);
+            const float v = p * (__uint_as_float(d[c + y]) - stat[2 * (64 * w + 32 * i + c + y) + 1]);
+            e[y] = whole || p != 0.f ? v : 0.f;  // what lies outside may be anything
+          }
+          o[16 * i + c / 2] = pack_bf16(e[0], e[1]);
+        }
+      }
+      tmem_st32(tDp + lanes + 64 * w, o);
+      if (past < kRows) clear_rows<DP>(sR + (2 * u % NS) * P::kTileBytes, past, tid);
+      st_wait();
+      fence_before();
+      __syncwarp();
+      if (lane == 0) bar_arrive(bDs);
+    }
+    if (ok && n > 0) ok = warp_wait(bEnd, 0, stop);
+    if (__all_sync(0xffffffffu, ok)) {
+      // ---- warpgroup 0 writes dv, warpgroup 1 dk
+      fence_after();
+      const uint32_t sum = (w == 0 ? tDv : tDk) + lanes;
+      const float f = w == 0 ? 1.f : a.scale;
+      const bool live = j < g.nk;
+      if (piece >= 0) {
+        float* out = a.part + ((((int64_t)(b * a.Hk + hk) * a.pieces + piece) * a.sink_tiles + tile) * 2 + w) * kRows * a.D +
+                     (int64_t)r * a.D;
+#pragma unroll
+        for (int i = 0; i < DP / 32; ++i) {
+          uint32_t o[32];
+          if (n > 0) {
+            tmem_ld32(sum + 32 * i, o);
+            ld_wait();
+          }
+#pragma unroll
+          for (int c = 0; c < 32; c += 4)
+            if (32 * i + c < a.D)
+              *reinterpret_cast<float4*>(out + 32 * i + c) =
+                  n > 0 ? make_float4(f * __uint_as_float(o[c]), f * __uint_as_float(o[c + 1]),
+                                      f * __uint_as_float(o[c + 2]), f * __uint_as_float(o[c + 3]))
+                        : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+      } else {
+        __nv_bfloat16* const out = w == 0 ? a.dvp + b * a.dv_sb + (g.kbeg + j) * a.dv_st + hk * a.dv_sh
+                                          : a.dkp + b * a.dk_sb + (g.kbeg + j) * a.dk_st + hk * a.dk_sh;
+        if (n == 0) {  // no query sees these keys
+          if (live)
+            for (int c = 0; c < a.D; c += 8) *reinterpret_cast<uint4*>(out + c) = make_uint4(0, 0, 0, 0);
+        } else {
+          const bool direct = a.cu && g.t0 + kRows > g.nk;
+          const uint32_t so = w == 0 ? sV : sK;
+          write_row<DP>(sum, f, so, r, direct, live, out, a.D);
+          if (!direct) {
+            fence_async();
+            __syncwarp();
+            if (lane == 0) bar_arrive(bOut + 8 * w);
+            if (r == 0 && bar_wait(bOut + 8 * w, 0, stop)) {
+#pragma unroll
+              for (int i = 0; i < DP / 64; ++i)
+                copy_out_4d(w == 0 ? &a.dv : &a.dk, so + i * kHalf, 64 * i, hk, (int)(g.kbeg + g.t0), b);
+              copy_out_commit();
+              copy_out_done();
+            }
+          }
+        }
+      }
+    }
+  }
+  __syncwarp();
+  linger(stop);
+  fence_before();
+  __syncthreads();
+  if (warp == 9) {
+    fence_after();
+    tmem_free(tm, 512);
+  }
+}
+
+// Adds the pieces of the cut key tiles in order: one block a (batch row and head,
+// sink tile, key), dk and dv.
+__global__ void __launch_bounds__(256) window_pieces_kernel(const __grid_constant__ BwdArgs a) {
+  const int64_t bh = blockIdx.y;
+  const int b = (int)(bh / a.Hk), hk = (int)(bh % a.Hk);
+  const int64_t j = blockIdx.x, tile = j / kRows;
+  if (j >= a.Tk) return;
+  for (int i = threadIdx.x; i < 2 * a.D; i += 256) {
+    const int w = i / a.D, c = i % a.D;
+    const int64_t step = (int64_t)a.sink_tiles * 2 * kRows * a.D;
+    const float* p = a.part + (bh * a.pieces * a.sink_tiles + tile) * 2 * kRows * a.D +
+                     ((int64_t)w * kRows + j % kRows) * a.D + c;
+    float s = 0.f;
+    for (int x = 0; x < a.pieces; ++x) s += p[x * step];
+    __nv_bfloat16* out = w == 0 ? a.dvp + b * a.dv_sb + j * a.dv_st + hk * a.dv_sh
+                                : a.dkp + b * a.dk_sb + j * a.dk_st + hk * a.dk_sh;
+    out[c] = __float2bfloat16_rn(s);
+  }
+}
+
+// ---------------------------------------------------------------------------
+
+template <int DP>
+__global__ void __launch_bounds__(kThreads, 1) window_dq_kernel(const __grid_constant__ BwdArgs a) {
+  using P = Plan<DP>;
+  constexpr int NS = P::kSlots;
+  extern __shared__ uint8_t raw[];
+  const uint32_t base = (smem_addr(raw) + 1023) & ~1023u;
+  uint8_t* const gen = raw + (base - smem_addr(raw));
+  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+  const uint32_t sQ = base, sD = base + P::kTileBytes, sR = base + 2 * P::kTileBytes;
+  uint32_t* const misc = reinterpret_cast<uint32_t*>(gen + (2 + NS) * P::kTileBytes);
+  const uint32_t bars = smem_addr(misc);
+  const uint32_t bQ = bars, bFull = bars + 8, bEmpty = bFull + 8 * NS, bS = bEmpty + 8 * NS, bDp = bS + 16,
+                 bDs = bDp + 8, bEnd = bDs + 8, bOut = bEnd + 8;
+  uint32_t* const tmem_ptr = misc + 64;
+  uint32_t* const stop_flag = misc + 65;
+
+  TileRows g;
+  if (!tile_rows(a.cu, a.n_seqs, a.Tq, a.Tk, blockIdx.x, kRows, &g)) return;
+  const int h = blockIdx.y % a.Hq, hk = h / a.G, b = blockIdx.y / a.Hq;
+  const int64_t rows = g.nq - g.t0 < kRows ? g.nq - g.t0 : kRows;
+  const KeyTiles kt = key_tiles(g.off + g.t0, g.off + g.t0 + rows - 1, g.nk, a.W, a.S, kRows);
+  const int n = (int)kt.count();
+
+  if (tid == 0) {
+    *stop_flag = 0;
+    bar_init(bQ, 1);
+    for (int i = 0; i < NS; ++i) {
+      bar_init(bFull + 8 * i, 1);
+      bar_init(bEmpty + 8 * i, 1);
+    }
+    bar_init(bS, 1);
+    bar_init(bS + 8, 1);
+    bar_init(bDp, 1);
+    bar_init(bDs, 8);
+    bar_init(bEnd, 1);
+    bar_init(bOut, 4);
+    bar_init_fence();
+  }
+  if (warp == 9) tmem_alloc(smem_addr(tmem_ptr), 512);
+  fence_before();
+  __syncthreads();
+  fence_after();
+  const uint32_t tm = *tmem_ptr, tS = tm, tDp = tm + 256, tDq = tm + 384;  // two S tiles
+  const Stop stop{stop_flag, a.hdr};
+
+  if (warp == 8) {
+    if (lane == 0 && n > 0) {
+      bar_expect(bQ, 2 * P::kTileBytes);
+#pragma unroll
+      for (int i = 0; i < DP / 64; ++i) {
+        copy_in_4d(sQ + i * kHalf, &a.q, bQ, 64 * i, h, (int)(g.qbeg + g.t0), b);
+        copy_in_4d(sD + i * kHalf, &a.dout, bQ, 64 * i, h, (int)(g.qbeg + g.t0), b);
+      }
+      for (int u = 0; u < 2 * n; ++u) {
+        const int sl = u % NS;
+        if (u >= NS && !bar_wait(bEmpty + 8 * sl, (u / NS - 1) & 1, stop)) break;
+        bar_expect(bFull + 8 * sl, P::kTileBytes);
+#pragma unroll
+        for (int i = 0; i < DP / 64; ++i)
+          copy_in_4d(sR + sl * P::kTileBytes + i * kHalf, u & 1 ? &a.v : &a.k, bFull + 8 * sl, 64 * i, hk,
+                     (int)(g.kbeg + kt.at(u / 2) * kRows), b);
+      }
+    }
+  } else if (warp == 9) {
+    if (lane == 0 && n > 0) {
+      constexpr uint32_t dS = product_desc(128, 128, false, false);
+      constexpr uint32_t dO = product_desc(128, DP, false, true);
+      const auto slot = [&](int u) { return sR + (u % NS) * P::kTileBytes; };
+      const auto full = [&](int u) { return bar_wait(bFull + 8 * (u % NS), (u / NS) & 1, stop); };
+      const auto scores = [&](int u) {
+        mma_kk<DP>(tS + 128 * (u & 1), sQ, kHalf, slot(2 * u), kHalf, dS, false);
+        mma_commit(bS + 8 * (u & 1));
+      };
+      const auto dprod = [&](int u) {
+        mma_kk<DP>(tDp, sD, kHalf, slot(2 * u + 1), kHalf, dS, false);
+        mma_commit(bDp);
+        mma_commit(bEmpty + 8 * ((2 * u + 1) % NS));
+      };
+      bool ok = bar_wait(bQ, 0, stop) && full(0) && full(1);
+      if (ok) {
+        scores(0);
+        dprod(0);
+        if (n > 1 && (ok = full(2))) scores(1);
+      }
+      for (int u = 0; ok && u < n; ++u) {
+        if (u + 1 < n && !(ok = full(2 * u + 3))) break;
+        if (!(ok = bar_wait(bDs, u & 1, stop))) break;
+        fence_after();
+        if (u + 1 < n) dprod(u + 1);
+        const uint32_t w = tS + 128 * (u & 1);
+        mma_tn<64>(tDq, w, slot(2 * u), kHalf, dO, u > 0);
+        mma_tn<64>(tDq, w + 64, slot(2 * u) + 64 * kPitch, kHalf, dO, true);
+        mma_commit(bEmpty + 8 * (2 * u % NS));
+        if (u + 2 < n) {
+          if (!(ok = full(2 * u + 4))) break;
+          scores(u + 2);
+        }
+      }
+      mma_commit(bEnd);
+    }
+  } else {
+    const int w = warp / 4, r = tid - 128 * w;
+    const uint32_t lanes = (uint32_t)(warp % 4) << 21;
+    const int64_t row = g.t0 + r, pos = g.off + row;
+    const int64_t wlo = g.off + g.t0 + (warp % 4) * 32, whi = wlo + 31;
+    const bool live = row < g.nq;
+    const int64_t at = ((int64_t)b * a.Hq + h) * a.Tq + g.qbeg + row;
+    const float lse = live ? a.lse[at] * 1.44269504088896341f : INFINITY, delta = live ? a.delta[at] : 0.f;
+    bool ok = true;
+    for (int u = 0; u < n; ++u) {
+      const int64_t j0 = kt.at(u) * kRows, c0 = j0 + 64 * w;  // first key of the columns
+      if (!(ok = warp_wait(bS + 8 * (u & 1), (u >> 1) & 1, stop))) break;
+      fence_after();
+      uint32_t s[2][32];
+      tmem_ld32(tS + 128 * (u & 1) + lanes + 64 * w, s[0]);
+      tmem_ld32(tS + 128 * (u & 1) + lanes + 64 * w + 32, s[1]);
+      ld_wait();
+      const bool whole = c0 + 63 <= wlo && (whi - c0 < a.W || c0 + 64 <= a.S) && g.t0 + (warp % 4) * 32 + 31 < g.nq;
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int c = 0; c < 32; ++c)
+          s[i][c] = __float_as_uint(fast_exp2(fmaf(__uint_as_float(s[i][c]), a.sl2, -lse)));
+      if (!whole) {
+        const auto cl = [](int64_t v) { return (int)(v < -1 ? -1 : v > 64 ? 64 : v); };
+        const int lo = cl(pos - a.W + 1 - c0), hi = live ? cl(pos - c0) : -1, sk = cl(a.S - c0);
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int c = 0; c < 32; ++c) {
+            const int x = 32 * i + c;
+            if (!(x <= hi && (x >= lo || x < sk))) s[i][c] = 0u;
+          }
+      }
+      if (!(ok = warp_wait(bDp, u & 1, stop))) break;
+      fence_after();
+      uint32_t o[32];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        uint32_t d[32];
+        tmem_ld32(tDp + lanes + 64 * w + 32 * i, d);
+        ld_wait();
+#pragma unroll
+        for (int c = 0; c < 32; c += 2) {
+          float e[2];
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {
+            const float p = __uint_as_float(s[i][c + y]);
+            const float v = p * (__uint_as_float(d[c + y]) - delta);
+            e[y] = whole || p != 0.f ? v : 0.f;
+          }
+          o[16 * i + c / 2] = pack_bf16(e[0], e[1]);
+        }
+      }
+      tmem_st32(tS + 128 * (u & 1) + lanes + 64 * w, o);
+      if (a.cu && j0 + kRows > g.nk)  // key rows of the next sequence (its scores are done)
+        clear_rows<DP>(sR + (2 * u % NS) * P::kTileBytes, (int)(g.nk - j0), tid);
+      st_wait();
+      fence_before();
+      __syncwarp();
+      if (lane == 0) bar_arrive(bDs);
+    }
+    if (ok && n > 0) ok = warp_wait(bEnd, 0, stop);
+    if (w == 0 && __all_sync(0xffffffffu, ok)) {
+      fence_after();
+      __nv_bfloat16* const out = a.dqp + b * a.dq_sb + (g.qbeg + row) * a.dq_st + h * a.dq_sh;
+      if (n == 0) {  // these queries see nothing
+        if (live)
+          for (int c = 0; c < a.D; c += 8) *reinterpret_cast<uint4*>(out + c) = make_uint4(0, 0, 0, 0);
+      } else {
+        const bool direct = a.cu && g.t0 + kRows > g.nq;
+        write_row<DP>(tDq + lanes, a.scale, sQ, r, direct, live, out, a.D);
+        if (!direct) {
+          fence_async();
+          __syncwarp();
+          if (lane == 0) bar_arrive(bOut);
+          if (r == 0 && bar_wait(bOut, 0, stop)) {
+#pragma unroll
+            for (int i = 0; i < DP / 64; ++i)
+              copy_out_4d(&a.dq, sQ + i * kHalf, 64 * i, h, (int)(g.qbeg + g.t0), b);
+            copy_out_commit();
+            copy_out_done();
+          }
+        }
+      }
+    }
+  }
+  __syncwarp();
+  linger(stop);
+  fence_before();
+  __syncthreads();
+  if (warp == 9) {
+    fence_after();
+    tmem_free(tm, 512);
+  }
+}
+
+template <int DP>
+cudaError_t launch_bwd(const BwdArgs& t, int64_t B, cudaStream_t s) {
+  using P = Plan<DP>;
+  static_assert(P::kSmem <= 232448, "fits a block's shared memory");
+  cudaError_t e = cudaFuncSetAttribute(window_dkv_kernel<DP>, cudaFuncAttributeMaxDynamicSharedMemorySize, P::kSmem);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(window_dq_kernel<DP>, cudaFuncAttributeMaxDynamicSharedMemorySize, P::kSmem);
+  if (e != cudaSuccess) return e;
+  const int64_t extra = t.cu ? t.n_seqs : 0;
+  const int64_t tk = (t.Tk + kRows - 1) / kRows + extra, tq = (t.Tq + kRows - 1) / kRows + extra;
+  const int64_t cut = t.pieces > 1 ? (int64_t)t.sink_tiles * (t.pieces - 1) : 0;
+  window_dkv_kernel<DP><<<dim3((unsigned)(tk + cut), (unsigned)(B * t.Hk)), kThreads, P::kSmem, s>>>(t);
+  window_dq_kernel<DP><<<dim3((unsigned)tq, (unsigned)(B * t.Hq)), kThreads, P::kSmem, s>>>(t);
+  if (t.pieces > 1)
+    window_pieces_kernel<<<dim3((unsigned)(t.sink_tiles * kRows), (unsigned)(B * t.Hk)), 256, 0, s>>>(t);
+  return cudaGetLastError();
+}
+
+// The walk of a key tile that holds first tokens, in pieces no longer than any
+// other tile's walk (dense rows; at most 64 pieces, and 16 cut tiles).
+struct Cut {
+  int tiles, pieces;
+};
+Cut cut_sinks(int64_t Tq, int64_t Tk, int64_t W, int64_t S, bool packed) {
+  if (packed || S < 1 || Tk < 1) return Cut{0, 1};
+  const int64_t all = (Tq + kRows - 1) / kRows, one = (W + 2 * kRows - 2) / kRows + 1;
+  const int64_t tiles = ((S < Tk ? S : Tk) + kRows - 1) / kRows;
+  int64_t p = (all + one - 1) / one;
+  if (p > 64) p = 64;
+  if (p < 2 || tiles > 16) return Cut{0, 1};
+  return Cut{(int)tiles, (int)p};
+}
+
+}  // namespace
+
+size_t window_tc_bwd_floats(int64_t B, int64_t Tq, int64_t Tk, int64_t Hk, int64_t D, int64_t W, int64_t S,
+                            bool packed) {
+  const Cut c = cut_sinks(Tq, Tk, W, S, packed);
+  return c.pieces < 2 ? 0 : (size_t)(B * Hk * c.pieces * c.tiles) * 2 * kRows * (size_t)D;
+}
+
+cudaError_t launch_window_tc_bwd(const WinArgs& a, float* part, cudaStream_t s) {
+  BwdArgs t;
+  if (!encode_heads_map(&t.q, a.q, a.B, a.Tq, a.Hq, a.D, kRows) ||
+      !encode_heads_map(&t.k, a.k, a.B, a.Tk, a.Hk, a.D, kRows) ||
+      !encode_heads_map(&t.v, a.v, a.B, a.Tk, a.Hk, a.D, kRows) ||
+      !encode_heads_map(&t.dout, a.dout, a.B, a.Tq, a.Hq, a.D, kRows) ||
+      !encode_heads_map(&t.dq, a.dq, a.B, a.Tq, a.Hq, a.D, kRows) ||
+      !encode_heads_map(&t.dk, a.dk, a.B, a.Tk, a.Hk, a.D, kRows) ||
+      !encode_heads_map(&t.dv, a.dv, a.B, a.Tk, a.Hk, a.D, kRows))
+    return cudaErrorInvalidValue;
+  t.dqp = static_cast<__nv_bfloat16*>(a.dq.ptr);
+  t.dq_sb = a.dq.stride_b, t.dq_st = a.dq.stride_t, t.dq_sh = a.dq.stride_h;
+  t.dkp = static_cast<__nv_bfloat16*>(a.dk.ptr);
+  t.dk_sb = a.dk.stride_b, t.dk_st = a.dk.stride_t, t.dk_sh = a.dk.stride_h;
+  t.dvp = static_cast<__nv_bfloat16*>(a.dv.ptr);
+  t.dv_sb = a.dv.stride_b, t.dv_st = a.dv.stride_t, t.dv_sh = a.dv.stride_h;
+  t.lse = a.lse;
+  t.delta = a.delta;
+  t.part = part;
+  t.cu = a.cu;
+  t.hdr = a.hdr;
+  t.Tq = a.Tq;
+  t.Tk = a.Tk;
+  t.W = a.W;
+  t.S = a.S;
+  t.n_seqs = a.n_seqs;
+  t.Hq = a.Hq;
+  t.Hk = a.Hk;
+  t.G = a.Hq / a.Hk;
+  t.D = a.D;
+  const Cut c = cut_sinks(a.Tq, a.Tk, a.W, a.S, a.cu != nullptr);
+  t.sink_tiles = c.tiles;
+  t.pieces = c.pieces;
+  t.sl2 = a.scale * 1.44269504088896341f;
+  t.scale = a.scale;
+  return a.D <= 64 ? launch_bwd<64>(t, a.B, s) : launch_bwd<128>(t, a.B, s);
+}
+
+}  // namespace scan
