@@ -13,11 +13,12 @@
 // SM), each working on its own part of the chain at any time:
 //   copy warp     two to four chunks of x1, x2, x3 in flight
 //   product warp  S1 = x1 x2^T, O = x1 S, S^T += x3'^T x2, O += P x3
-//   weights       P = S1 * lambda^(r - r'), masked, to bf16 (over S1 in tensor memory)
+//   weights       P = S1 * lambda^(r - r'), masked, to bf16
 //   state         S^T to bf16 for the next chunk's x1 S, and S^T *= lambda^n
-//   update        x3'^T = lambda^(n - e - r') x3^T as hi + lo bf16 parts: the
-//                 state's update is then exact to 2^-17, so that the state (fp32
-//                 in tensor memory) keeps fp32 accuracy over any number of chunks
+//   update        x3'^T = lambda^(n - e - r') x3^T as hi + lo bf16 parts, 32 steps
+//                 at a time: the state's update is then exact to 2^-17, so that the
+//                 state (fp32 in tensor memory) keeps fp32 accuracy over any number
+//                 of chunks
 //   output        O *= lambda^(r + e) between the two products into it; O to bf16
 // The state lies transposed (lanes are v): its bf16 copy is then written by rows
 // into the operand layout, and the weighted operand of the update is one that the
@@ -100,13 +101,14 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_co
   // shared memory: stages, the state's bf16 copy, tables, barriers
   const uint32_t sState = base + P::kStages * P::kStage;
   float* const tab = reinterpret_cast<float*>(gen + P::kStages * P::kStage + P::kState);
-  float* const wtab = tab;           // [128] weights of the update
-  float* const dtab = tab + 128;     // [32] lambda^d
-  const uint32_t bars = smem_addr(tab + 160);
-  const uint32_t bFull = bars, bEmpty = bars + 32, bS1 = bars + 64, bP = bars + 72, bSb = bars + 80,
-                 bSt = bars + 88, bVp = bars + 96, bOi = bars + 104, bOs = bars + 112, bOf = bars + 120,
-                 bOx = bars + 128, bClean = bars + 136, bOut = bars + 144;
-  uint32_t* const tmem_ptr = reinterpret_cast<uint32_t*>(tab + 160) + 40;
+  float* const wtab = tab;           // [128] weights of the update in a whole chunk
+  float* const wlast = tab + 128;    // [128] in the chunk that ends the sequence, 0 past it
+  float* const ctab = tab + 256;     // [32] column powers of the weights within a chunk
+  const uint32_t bars = smem_addr(tab + 288);
+  const uint32_t bFull = bars, bFree1 = bars + 32, bFree23 = bars + 64, bS1 = bars + 96, bP = bars + 104,
+                 bSb = bars + 112, bSt = bars + 120, bX = bars + 128, bXf = bars + 144, bOi = bars + 160,
+                 bOs = bars + 168, bOf = bars + 176, bOx = bars + 184, bClean = bars + 192, bOut = bars + 200;
+  uint32_t* const tmem_ptr = reinterpret_cast<uint32_t*>(tab + 288) + 56;
   uint32_t* const stop_flag = tmem_ptr + 1;
 
   // which (sequence, head, segment)
@@ -132,11 +134,12 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_co
   }
   const bool rev = p.reverse != 0;
   const int e = rev ? 0 : 1;
-  const float l2 = a.log_decay[h] * 1.44269504088896341f;
+  // log2(lambda); no memory at all (-inf) as a number, so that its 0th power is 1
+  const float l2 = fmaxf(a.log_decay[h] * 1.44269504088896341f, -1e30f);
 
   // initial state: the caller's for the first segment, else the one before
   const float* s0 = nullptr;
-  int64_t s0k = 0, s0v = 0;  // its strides
+  int s0k = 0, s0v = 0;  // its strides
   float s0m = 1.f;
   if (seg == 0) {
     if (p.s_in) {
@@ -162,19 +165,27 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_co
   const bool packed = a.cu != nullptr;
   const int late = s0 ? 0 : 1;  // the first chunk whose queries read a state
 
-  if (tid < 128) wtab[tid] = decay_pow(l2, rev ? tid + 1 : 127 - tid);
-  if (tid < 32) dtab[tid] = decay_pow(l2, tid);
+  if (tid < 128) {
+    const int n = s.len % kChunk ? (int)(s.len % kChunk) : kChunk;
+    wtab[tid] = exp2f(l2 * (float)(rev ? tid + 1 : 127 - tid));
+    wlast[tid] = tid < n ? exp2f(l2 * (float)(rev ? tid + 1 : n - 1 - tid)) : 0.f;
+  }
+  if (tid < 32) ctab[tid] = exp2f(l2 * (float)(rev ? tid : 31 - tid));
   if (tid == 0) {
     *stop_flag = 0;
     for (int i = 0; i < P::kStages; ++i) {
       bar_init(bFull + 8 * i, 1);
-      bar_init(bEmpty + 8 * i, STATE_ONLY ? 1 : 2);
+      bar_init(bFree1 + 8 * i, 1);
+      bar_init(bFree23 + 8 * i, 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      bar_init(bX + 8 * i, 4);
+      bar_init(bXf + 8 * i, 1);
     }
     bar_init(bS1, 1);
     bar_init(bP, 4);
     bar_init(bSb, 4);
     bar_init(bSt, 1);
-    bar_init(bVp, 4);
     bar_init(bOi, 1);
     bar_init(bOs, 4);
     bar_init(bOf, 1);
@@ -188,7 +199,8 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_co
   __syncthreads();
   fence_after();
   const uint32_t tm = *tmem_ptr;
-  const uint32_t tS1 = tm, tO = tm + 128, tSt = tm + 256, tX = tm + 384;
+  // tensor memory: S1, P, two 32-step pieces of the update's operand (hi, lo), O, S^T
+  const uint32_t tS1 = tm, tP = tm + 128, tX = tm + 192, tO = tm + 256, tSt = tm + 384;
   const uint32_t lanes = (uint32_t)(warp % 4) << 21;  // this warp's first tensor-memory lane
   const Stop stop{stop_flag, a.hdr};
   const int role = warp / 4;
@@ -198,7 +210,8 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_co
     if (lane == 0) {
       for (int c = 0; c < s.nch; ++c) {
         const int st = c % P::kStages;
-        if (c >= P::kStages && !bar_wait(bEmpty + 8 * st, (c / P::kStages - 1) & 1, stop)) break;
+        const uint32_t again = (c / P::kStages - 1) & 1;
+        if (c >= P::kStages && !bar_wait(bFree23 + 8 * st, again, stop)) break;
         int64_t t0;
         int n;
         chunk_at(s, rev, c, &t0, &n);
@@ -206,13 +219,15 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_co
         const uint32_t d = base + st * P::kStage, bar = bFull + 8 * st;
         bar_expect(bar, (STATE_ONLY ? 0 : P::kX2) + P::kX2 + P::kX3);
 #pragma unroll
-        for (int i = 0; i < KP / 64; ++i) {
-          if (!STATE_ONLY) copy_in_4d(d + i * kHalf, &p.x1, bar, 64 * i, h, t, b);
-          copy_in_4d(d + P::kX1 + i * kHalf, &p.x2, bar, 64 * i, h, t, b);
-        }
+        for (int i = 0; i < KP / 64; ++i) copy_in_4d(d + P::kX1 + i * kHalf, &p.x2, bar, 64 * i, h, t, b);
 #pragma unroll
         for (int i = 0; i < VP / 64; ++i)
           copy_in_4d(d + P::kX1 + P::kX2 + i * kHalf, &p.x3, bar, 64 * i, h, t, b);
+        if (!STATE_ONLY) {
+          if (c >= P::kStages && !bar_wait(bFree1 + 8 * st, again, stop)) break;
+#pragma unroll
+          for (int i = 0; i < KP / 64; ++i) copy_in_4d(d + i * kHalf, &p.x1, bar, 64 * i, h, t, b);
+        }
       }
     }
   } else if (warp == 17) {
@@ -222,42 +237,63 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_co
       constexpr uint32_t dOi = product_desc(128, VP, false, false);
       constexpr uint32_t dSt = product_desc(128, KP, false, true);
       constexpr uint32_t dO = product_desc(128, VP, false, true);
-      for (int c = 0; c < s.nch; ++c) {
-        const int st = c % P::kStages;
-        const uint32_t x1 = base + st * P::kStage, x2 = x1 + P::kX1, x3 = x2 + P::kX2;
+      const auto ready = [&](int c) {  // chunk c has arrived, and nothing in it is another sequence's
         int64_t t0;
         int n;
         chunk_at(s, rev, c, &t0, &n);
+        return bar_wait(bFull + 8 * (c % P::kStages), (c / P::kStages) & 1, stop) &&
+               (!packed || n == kChunk || bar_wait(bClean, 0, stop));
+      };
+      const auto scores = [&](int c) {
+        const uint32_t x1 = base + (c % P::kStages) * P::kStage;
+        mma_kk<KP>(tS1, x1, kHalf, x1 + P::kX1, kHalf, dS1, false);
+        mma_commit(bS1);
+      };
+      bool ok = s.nch > 0;
+      if (!STATE_ONLY && ok && (ok = ready(0))) scores(0);
+#pragma unroll 1
+      for (int c = 0; ok && c < s.nch; ++c) {
+        const int st = c % P::kStages;
+        const uint32_t x1 = base + st * P::kStage, x2 = x1 + P::kX1, x3 = x2 + P::kX2;
         const bool have = c > 0 || s0;
-        const bool more = c + 1 < s.nch || s1;
-        if (!bar_wait(bFull + 8 * st, (c / P::kStages) & 1, stop)) break;
-        if (packed && n < kChunk && !bar_wait(bClean, 0, stop)) break;
-        if (!STATE_ONLY) {
-          mma_kk<KP>(tS1, x1, kHalf, x2, kHalf, dS1, false);
-          mma_commit(bS1);
-          if (c > 0 && !bar_wait(bOx, (c - 1) & 1, stop)) break;
-        }
-        if (!bar_wait(bSb, c & 1, stop)) break;
+        if (STATE_ONLY && !(ok = ready(c))) break;
+        if (!(ok = bar_wait(bSb, c & 1, stop))) break;
         fence_after();
-        if (!STATE_ONLY && have) {
+        if (c + 1 < s.nch || s1) {
+#pragma unroll 1
+          for (int jb = 0; jb < 4; ++jb) {
+            const int buf = jb & 1;
+            if (!(ok = bar_wait(bX + 8 * buf, jb >> 1, stop))) break;
+            fence_after();
+            mma_tn<32>(tSt, tX + 32 * buf, x2 + 32 * jb * kPitch, kHalf, dSt, have || jb > 0);
+            mma_tn<32>(tSt, tX + 32 * buf + 16, x2 + 32 * jb * kPitch, kHalf, dSt, true);
+            mma_commit(bXf + 8 * buf);
+          }
+          if (!ok) break;
+        }
+        if (STATE_ONLY) {
+          mma_commit(bSt);
+          mma_commit(bFree23 + 8 * st);
+          continue;
+        }
+        if (c > 0 && !(ok = bar_wait(bOx, (c - 1) & 1, stop))) break;
+        fence_after();
+        if (have) {
           mma_kk<KP>(tO, x1, kHalf, sState, VP * kPitch, dOi, false);
           mma_commit(bOi);
         }
-        if (more) {
-          if (!bar_wait(bVp, c & 1, stop)) break;
-          fence_after();
-          mma_tn<kChunk>(tSt, tX, x2, kHalf, dSt, have);
-          mma_tn<kChunk>(tSt, tX + 64, x2, kHalf, dSt, true);
-        }
         mma_commit(bSt);
-        mma_commit(bEmpty + 8 * st);
-        if (!STATE_ONLY) {
-          if (!bar_wait(bP, c & 1, stop)) break;
-          if (have && !bar_wait(bOs, (c - late) & 1, stop)) break;
+        if (!(ok = bar_wait(bP, c & 1, stop))) break;
+        if (c + 1 < s.nch) {
+          if (!(ok = ready(c + 1))) break;
           fence_after();
-          mma_tn<kChunk>(tO, tS1, x3, kHalf, dO, have);
-          mma_commit(bOf);
+          scores(c + 1);
         }
+        if (have && !(ok = bar_wait(bOs, (c - late) & 1, stop))) break;
+        fence_after();
+        mma_tn<kChunk>(tO, tP, x3, kHalf, dO, have);
+        mma_commit(bOf);
+        mma_commit(bFree23 + 8 * st);
       }
     }
   } else if (role == 0 && !STATE_ONLY) {
@@ -266,17 +302,14 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_co
     // of lambda that are both at most 1; the diagonal block takes the power of
     // the difference.
     const int w = warp % 4;
-    float rf[4];
-#pragma unroll
-    for (int jb = 0; jb < 4; ++jb) {
-      const int d = rev ? 32 * jb - (32 * w + lane) : 32 * w + lane - (32 * jb + 31);
-      rf[jb] = d > 0 ? decay_pow(l2, d) : 1.f;
-    }
+    const float lanef = (float)lane;
+    bool ok = true;
+#pragma unroll 1
     for (int c = 0; c < s.nch; ++c) {
       if (!warp_wait(bS1, c & 1, stop)) break;
       fence_after();
-#pragma unroll
-      for (int jb = 0; jb < 4; ++jb) {
+#pragma unroll 1
+      for (int jb = 0; jb < 4; ++jb) {  // (rolled: the four roles' code has to fit the instruction cache)
         uint32_t o[16];
         if (rev ? jb < w : jb > w) {
 #pragma unroll
@@ -287,21 +320,31 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_co
           ld_wait();
           if (jb == w) {
 #pragma unroll
-            for (int x = 0; x < 32; ++x) {
-              const int d = rev ? x - lane : lane - x;
-              r[x] = d >= 0 ? __float_as_uint(__uint_as_float(r[x]) * dtab[d & 31]) : 0u;
+            for (int x = 0; x < 32; x += 2) {
+              float f[2];
+#pragma unroll
+              for (int y = 0; y < 2; ++y) {
+                const float d = rev ? (float)(x + y) - lanef : lanef - (float)(x + y);
+                f[y] = d >= 0.f ? __uint_as_float(r[x + y]) * fast_exp2(l2 * d) : 0.f;
+              }
+              o[x / 2] = pack_bf16(f[0], f[1]);
             }
           } else {
+            const float rf = exp2f(l2 * (float)(rev ? 32 * (jb - w) - lane : 32 * (w - jb) + lane - 31));
 #pragma unroll
-            for (int x = 0; x < 32; ++x)
-              r[x] = __float_as_uint(__uint_as_float(r[x]) * (rf[jb] * dtab[rev ? x : 31 - x]));
+            for (int x = 0; x < 32; x += 4) {
+              const float4 k = *reinterpret_cast<const float4*>(ctab + x);
+              o[x / 2] = pack_bf16(__uint_as_float(r[x]) * (rf * k.x), __uint_as_float(r[x + 1]) * (rf * k.y));
+              o[x / 2 + 1] =
+                  pack_bf16(__uint_as_float(r[x + 2]) * (rf * k.z), __uint_as_float(r[x + 3]) * (rf * k.w));
+            }
           }
-#pragma unroll
-          for (int x = 0; x < 16; ++x)
-            o[x] = pack_bf16(__uint_as_float(r[2 * x]), __uint_as_float(r[2 * x + 1]));
         }
-        tmem_st16(tS1 + lanes + 16 * jb, o);
+        // P of the chunk before has been used
+        if (jb == 0 && c > 0 && !(ok = warp_wait(bOf, (c - 1) & 1, stop))) break;
+        tmem_st16(tP + lanes + 16 * jb, o);
       }
+      if (!ok) break;
       st_wait();
       fence_before();
       __syncwarp();
@@ -310,50 +353,67 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_co
   } else if (role == 1) {
     // ---- state: column v of S (a row of S^T) in lane v
     const int v = tid - 128;
-    for (int c = 0; c < s.nch; ++c) {
+    // 32 rows of S to its bf16 copy, and decayed to tensor memory
+    const auto give = [&](uint32_t(&r)[32], int kb, float keep) {
+      if (!STATE_ONLY && v < VP) {
+#pragma unroll
+        for (int y = 0; y < 4; ++y) {
+          uint32_t o[4];
+#pragma unroll
+          for (int x = 0; x < 4; ++x)
+            o[x] = pack_bf16(__uint_as_float(r[8 * y + 2 * x]), __uint_as_float(r[8 * y + 2 * x + 1]));
+          st_shared16(swizzled(sState + (kb / 2) * VP * kPitch, v, (kb % 2) * 4 + y), o[0], o[1], o[2], o[3]);
+        }
+      }
+#pragma unroll
+      for (int x = 0; x < 32; ++x) r[x] = __float_as_uint(__uint_as_float(r[x]) * keep);
+      tmem_st32(tSt + lanes + 32 * kb, r);
+    };
+    const auto given = [&]() {
+      st_wait();
+      fence_async();
+      fence_before();
+      __syncwarp();
+      if (lane == 0) bar_arrive(bSb);
+    };
+    if (s.nch > 0) {  // the state that comes in
+      if (s0) {
+        int64_t t0;
+        int n;
+        chunk_at(s, rev, 0, &t0, &n);
+        const float keep = exp2f(l2 * (float)n);
+#pragma unroll 1
+        for (int kb = 0; kb < KP / 32; ++kb) {
+          uint32_t r[32];
+#pragma unroll
+          for (int x = 0; x < 32; ++x) {
+            const int k = 32 * kb + x;
+            r[x] = __float_as_uint(s0[(k < p.K ? k : 0) * s0k + (v < p.V ? v : 0) * s0v]);
+          }
+#pragma unroll
+          for (int x = 0; x < 32; ++x)
+            r[x] = v < p.V && 32 * kb + x < p.K ? __float_as_uint(s0m * __uint_as_float(r[x])) : 0u;
+          give(r, kb, keep);
+        }
+      }
+      given();
+    }
+#pragma unroll 1
+    for (int c = 1; c < s.nch; ++c) {
       int64_t t0;
       int n;
       chunk_at(s, rev, c, &t0, &n);
-      if (c > 0) {
-        if (!warp_wait(bSt, (c - 1) & 1, stop)) break;
-        fence_after();
+      const float keep = exp2f(l2 * (float)n);
+      if (!warp_wait(bSt, (c - 1) & 1, stop)) break;
+      fence_after();
+#pragma unroll 1
+      for (int kb = 0; kb < KP / 32; ++kb) {
+        uint32_t r[32];
+        tmem_ld32(tSt + lanes + 32 * kb, r);
+        ld_wait();
+        give(r, kb, keep);
       }
-      if (c > 0 || s0) {
-        const float keep = decay_pow(l2, n);
-#pragma unroll
-        for (int kb = 0; kb < KP / 32; ++kb) {
-          uint32_t r[32];
-          if (c > 0) {
-            tmem_ld32(tSt + lanes + 32 * kb, r);
-            ld_wait();
-          } else {
-#pragma unroll
-            for (int x = 0; x < 32; ++x) {
-              const int k = 32 * kb + x;
-              r[x] = v < p.V && k < p.K ? __float_as_uint(s0m * s0[k * s0k + v * s0v]) : 0u;
-            }
-          }
-          if (!STATE_ONLY && v < VP) {
-#pragma unroll
-            for (int y = 0; y < 4; ++y) {
-              uint32_t o[4];
-#pragma unroll
-              for (int x = 0; x < 4; ++x)
-                o[x] = pack_bf16(__uint_as_float(r[8 * y + 2 * x]), __uint_as_float(r[8 * y + 2 * x + 1]));
-              st_shared16(swizzled(sState + (kb / 2) * VP * kPitch, v, (kb % 2) * 4 + y), o[0], o[1], o[2],
-                          o[3]);
-            }
-          }
-#pragma unroll
-          for (int x = 0; x < 32; ++x) r[x] = __float_as_uint(__uint_as_float(r[x]) * keep);
-          tmem_st32(tSt + lanes + 32 * kb, r);
-        }
-        st_wait();
-        fence_async();
-        fence_before();
-      }
-      __syncwarp();
-      if (lane == 0) bar_arrive(bSb);
+      given();
     }
     if (s1) {
       bool ok = true;
@@ -362,7 +422,7 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_co
         fence_after();
       }
       if (ok) {
-#pragma unroll
+#pragma unroll 1
         for (int kb = 0; kb < KP / 32; ++kb) {
           uint32_t r[32];
           if (s.nch > 0) {
@@ -380,28 +440,31 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_co
         }
       }
     }
-  } else if (role == 2) {
-    // ---- update: column v of x3 in lane v, weighted and split in two
-    const int v = tid - 256;
+  } else if (role == 2 || (role == 0 && STATE_ONLY)) {
+    // ---- update: column v of x3 in lane v, weighted and split in two, 32 steps at a
+    // time (by two roles where only the state is wanted)
+    const int v = tid % 128;
     if (v >= VP) {  // lanes past V: zeros, once
       uint32_t z[32];
 #pragma unroll
       for (int x = 0; x < 32; ++x) z[x] = 0;
 #pragma unroll
-      for (int x = 0; x < 4; ++x) tmem_st32(tX + lanes + 32 * x, z);
+      for (int x = 0; x < 2; ++x) tmem_st32(tX + lanes + 32 * x, z);
       st_wait();
     }
-    for (int c = 0; c < s.nch; ++c) {
+    bool ok = true;
+#pragma unroll 1
+    for (int c = 0; ok && c < s.nch; ++c) {
       const int st = c % P::kStages;
-      const uint32_t x2 = base + st * P::kStage + P::kX1, x3 = x2 + P::kX2;
       int64_t t0;
       int n;
       chunk_at(s, rev, c, &t0, &n);
       if (!warp_wait(bFull + 8 * st, (c / P::kStages) & 1, stop)) break;
       if (packed && n < kChunk) {
         // the rows from n on belong to the next sequence (one such chunk a row)
+        const uint32_t x2 = base + st * P::kStage + P::kX1;
         const int left = kChunk - n;
-        for (int i = tid - 256; i < left * 8 * (KP + VP) / 64; i += 128) {
+        for (int i = v; i < left * 8 * (KP + VP) / 64; i += 128) {
           const int piece = i % 8, r = n + (i / 8) % left, pn = i / 8 / left;
           st_shared16(x2 + pn * kHalf + r * kPitch + piece * 16, 0, 0, 0, 0);
         }
@@ -409,42 +472,54 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_co
         __syncwarp();
         if (lane == 0) bar_arrive(bClean);
         __syncwarp();
+        if (!warp_wait(bClean, 0, stop)) break;
       }
-      if (c > 0 && !warp_wait(bSt, (c - 1) & 1, stop)) break;
-      fence_after();
-      if (v < VP && (c + 1 < s.nch || s1)) {
-        const uint32_t col = x3 + (v / 64) * kHalf + (v % 8) * 2;
-        const int piece = (v % 64) / 8;
-        const float* wt = rev ? wtab : wtab + (kChunk - n);
+      if (!(c + 1 < s.nch || s1)) break;  // no one reads the state after this chunk
+      const uint8_t* col = gen + st * P::kStage + P::kX1 + P::kX2 + (v < VP ? v / 64 : 0) * kHalf + (v % 8) * 2;
+      const int piece = (v % 64) / 8;
+      const float* wt = n < kChunk ? wlast : wtab;
 #pragma unroll 1
-        for (int jb = 0; jb < 4; ++jb) {
-          uint32_t hi[16], lo[16];
+      for (int jb = STATE_ONLY && role == 0; jb < 4; jb += STATE_ONLY ? 2 : 1) {
+        uint32_t hi[16], lo[16];
+        if (v < VP) {
 #pragma unroll
-          for (int x = 0; x < 16; ++x) {
-            float f[2], g[2];
+          for (int x = 0; x < 16; x += 2) {
+            const float4 w4 = *reinterpret_cast<const float4*>(wt + 32 * jb + 2 * x);
+            const float w[4] = {w4.x, w4.y, w4.z, w4.w};
+            float f[4];
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+              const int j = 2 * x + y;
+              const uint32_t u =
+                  *reinterpret_cast<const uint16_t*>(col + 32 * jb * kPitch + j * kPitch + ((piece ^ (j & 7)) << 4));
+              f[y] = __uint_as_float(u << 16) * w[y];
+            }
 #pragma unroll
             for (int y = 0; y < 2; ++y) {
-              const int j = 32 * jb + 2 * x + y;
-              const uint32_t u = ld_shared_u16(col + j * kPitch + ((piece ^ (j & 7)) << 4));
-              f[y] = j < n ? __uint_as_float(u << 16) * wt[j] : 0.f;
+              const uint32_t h = pack_bf16(f[2 * y], f[2 * y + 1]);
+              hi[x + y] = h;
+              lo[x + y] = pack_bf16(f[2 * y] - __uint_as_float(h << 16),
+                                    f[2 * y + 1] - __uint_as_float(h & 0xffff0000u));
             }
-            hi[x] = pack_bf16(f[0], f[1]);
-            g[0] = f[0] - __uint_as_float(hi[x] << 16);
-            g[1] = f[1] - __uint_as_float(hi[x] & 0xffff0000u);
-            lo[x] = pack_bf16(g[0], g[1]);
           }
-          tmem_st16(tX + lanes + 16 * jb, hi);
-          tmem_st16(tX + lanes + 64 + 16 * jb, lo);
         }
-        st_wait();
+        const int buf = jb & 1, use = 2 * c + (jb >> 1);  // the buffer's use-th time
+        if (use > 0 && !(ok = warp_wait(bXf + 8 * buf, (use - 1) & 1, stop))) break;
+        fence_after();
+        if (v < VP) {
+          tmem_st16(tX + 32 * buf + lanes, hi);
+          tmem_st16(tX + 32 * buf + 16 + lanes, lo);
+          st_wait();
+        }
+        fence_before();
+        __syncwarp();
+        if (lane == 0) bar_arrive(bX + 8 * buf);
       }
-      fence_before();
-      __syncwarp();
-      if (lane == 0) bar_arrive(bVp);
     }
   } else if (role == 3 && !STATE_ONLY) {
     // ---- output: row i of the chunk in lane i
     const int i = tid - 384;
+#pragma unroll 1
     for (int c = 0; c < s.nch; ++c) {
       const int st = c % P::kStages;
       const uint32_t so = base + st * P::kStage;  // x1's place: both its products are done by then
@@ -455,8 +530,8 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_co
         if (!warp_wait(bOi, (c - late) & 1, stop)) break;
         fence_after();
         const int r = rev ? n - 1 - i : i;
-        const float f = r >= 0 ? decay_pow(l2, r + e) : 0.f;
-#pragma unroll
+        const float f = r >= 0 ? exp2f(l2 * (float)(r + e)) : 0.f;
+#pragma unroll 1
         for (int vb = 0; vb < VP / 32; ++vb) {
           uint32_t x[32];
           tmem_ld32(tO + lanes + 32 * vb, x);
@@ -474,7 +549,7 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_co
       fence_after();
       const bool direct = packed && n < kChunk;
       __nv_bfloat16* const orow = p.o + b * p.o_sb + (s.beg + t0 + i) * p.o_st + h * p.o_sh;
-#pragma unroll
+#pragma unroll 1
       for (int vb = 0; vb < VP / 32; ++vb) {
         uint32_t x[32];
         tmem_ld32(tO + lanes + 32 * vb, x);
@@ -511,7 +586,7 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_co
           copy_out_commit();
           copy_out_read();
         }
-        bar_arrive(bEmpty + 8 * st);
+        bar_arrive(bFree1 + 8 * st);
       }
     }
     if (i == 0) copy_out_done();
@@ -532,8 +607,8 @@ __global__ void __launch_bounds__(256) linattn_chain_kernel(const __grid_constan
   const int64_t n = (int64_t)p.K * p.V, row = blockIdx.y;
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
   if (i >= n) return;
-  const float l2 = a.log_decay[row % a.H] * 1.44269504088896341f;
-  const float keep = decay_pow(l2, a.cps * kChunk);  // segments after the first are whole
+  const float l2 = fmaxf(a.log_decay[row % a.H] * 1.44269504088896341f, -1e30f);
+  const float keep = exp2f(l2 * (float)(a.cps * kChunk));  // segments after the first are whole
   float* s = p.seg + row * (a.nseg - 1) * n + i;
   float h = s[0];
   for (int g = 1; g < a.nseg - 1; ++g) {
