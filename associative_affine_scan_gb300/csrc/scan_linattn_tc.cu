@@ -57,19 +57,20 @@ struct TcArgs {
   const int32_t* cu;
   WsHeader* hdr;
   int64_t T;
-  int n_seqs, H, nseg, cps;  // segments of a row, chunks of a segment
+  int npass, n_seqs, H, nseg, cps;  // segments of a row, chunks of a segment
   float scale;
 };
 
-template <int KP, int VP>
+template <int KP, int VP, bool STATE_ONLY>
 struct Plan {
-  static constexpr int kX1 = kChunk * 2 * (KP > VP ? KP : VP);  // also stages the output
+  static constexpr int kX1 = STATE_ONLY ? 0 : kChunk * 2 * KP;
   static constexpr int kX2 = kChunk * 2 * KP;
-  static constexpr int kX3 = kChunk * 2 * VP;
+  static constexpr int kX3 = kChunk * 2 * VP;  // also stages the output
   static constexpr int kStage = kX1 + kX2 + kX3;
-  static constexpr int kState = VP * KP * 2;
-  static constexpr int kStages = (KP == 128 && VP == 128) ? 2 : (KP == 64 && VP == 64) ? 4 : 2;
+  static constexpr int kState = STATE_ONLY ? 0 : VP * KP * 2;
   static constexpr int kTables = 2048;  // barriers, decay tables
+  static constexpr int kFit = (232448 - 1024 - kTables - kState) / kStage;
+  static constexpr int kStages = kFit < 4 ? kFit : 4;
   static constexpr int kSmem = kStages * kStage + kState + kTables + 1024;
 };
 
@@ -91,11 +92,13 @@ __device__ __forceinline__ void chunk_at(const Span& s, bool reverse, int c, int
 
 template <int KP, int VP, bool STATE_ONLY>
 __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_constant__ TcArgs a) {
-  using P = Plan<KP, VP>;
+  using P = Plan<KP, VP, STATE_ONLY>;
   extern __shared__ uint8_t raw[];
   const uint32_t base = (smem_addr(raw) + 1023) & ~1023u;
   uint8_t* const gen = raw + (base - smem_addr(raw));
-  const TcPass& p = a.pass[blockIdx.z];
+  // the passes of one part of a row run side by side: they read the same operands
+  const unsigned item = blockIdx.x / a.npass;
+  const TcPass& p = a.pass[blockIdx.x % a.npass];
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
 
   // shared memory: stages, the state's bf16 copy, tables, barriers
@@ -105,16 +108,17 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_co
   float* const wlast = tab + 128;    // [128] in the chunk that ends the sequence, 0 past it
   float* const ctab = tab + 256;     // [32] column powers of the weights within a chunk
   const uint32_t bars = smem_addr(tab + 288);
-  const uint32_t bFull = bars, bFree1 = bars + 32, bFree23 = bars + 64, bS1 = bars + 96, bP = bars + 104,
-                 bSb = bars + 112, bSt = bars + 120, bX = bars + 128, bXf = bars + 144, bOi = bars + 160,
-                 bOs = bars + 168, bOf = bars + 176, bOx = bars + 184, bClean = bars + 192, bOut = bars + 200;
-  uint32_t* const tmem_ptr = reinterpret_cast<uint32_t*>(tab + 288) + 56;
+  const uint32_t bFull12 = bars, bFull3 = bars + 32, bFree12 = bars + 64, bFree3 = bars + 96, bS1 = bars + 128,
+                 bP = bars + 136, bSb = bars + 144, bSt = bars + 152, bX = bars + 160, bXf = bars + 176,
+                 bOi = bars + 192, bOs = bars + 200, bOf = bars + 208, bOx = bars + 216, bClean = bars + 224,
+                 bOut = bars + 232, bInit = bars + 240;
+  uint32_t* const tmem_ptr = reinterpret_cast<uint32_t*>(tab + 288) + 64;
   uint32_t* const stop_flag = tmem_ptr + 1;
 
   // which (sequence, head, segment)
   const int segs = STATE_ONLY ? a.nseg - 1 : a.nseg;
-  const int seg = blockIdx.x % segs;
-  const int64_t row = blockIdx.x / segs;
+  const int seg = item % segs;
+  const int64_t row = item / segs;
   const int h = (int)(row % a.H);
   const int64_t sq = row / a.H;
   Span s{0, a.T, 0, 0};
@@ -122,7 +126,7 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_co
     int64_t e;
     seq_bounds(a.cu, (int)sq, a.T, &s.beg, &e);
     s.len = e - s.beg;
-    if (blockIdx.x == 0 && blockIdx.z == 0 && warp == 0) check_seqlens(a.cu, a.n_seqs, a.T, a.hdr);
+    if (blockIdx.x == 0 && warp == 0) check_seqlens(a.cu, a.n_seqs, a.T, a.hdr);
   }
   const int b = a.cu ? 0 : (int)sq;
   const int64_t all = (s.len + kChunk - 1) / kChunk;
@@ -133,6 +137,9 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_co
     s.nch = (int)(all - s.first < a.cps ? all - s.first : a.cps);
   }
   const bool rev = p.reverse != 0;
+  // steps of the segment: chunks are whole but the one that ends the sequence
+  const int64_t steps = s.nch * (int64_t)kChunk -
+                        ((rev ? s.first == 0 : s.first + s.nch == all) ? all * kChunk - s.len : 0);
   const int e = rev ? 0 : 1;
   // log2(lambda); no memory at all (-inf) as a number, so that its 0th power is 1
   const float l2 = fmaxf(a.log_decay[h] * 1.44269504088896341f, -1e30f);
@@ -174,9 +181,10 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_co
   if (tid == 0) {
     *stop_flag = 0;
     for (int i = 0; i < P::kStages; ++i) {
-      bar_init(bFull + 8 * i, 1);
-      bar_init(bFree1 + 8 * i, 1);
-      bar_init(bFree23 + 8 * i, 1);
+      bar_init(bFull12 + 8 * i, 1);
+      bar_init(bFull3 + 8 * i, 1);
+      bar_init(bFree12 + 8 * i, 1);
+      bar_init(bFree3 + 8 * i, 1);
     }
     for (int i = 0; i < 2; ++i) {
       bar_init(bX + 8 * i, 4);
@@ -192,6 +200,7 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_co
     bar_init(bOx, 4);
     bar_init(bClean, 4);
     bar_init(bOut, 4);
+    bar_init(bInit, 4 * (KP / 32));
     bar_init_fence();
   }
   if (warp == 17) tmem_alloc(smem_addr(tmem_ptr), 512);
@@ -205,29 +214,70 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_co
   const Stop stop{stop_flag, a.hdr};
   const int role = warp / 4;
 
+  // 32 rows of S to its bf16 copy, and decayed to tensor memory
+  const auto give = [&](uint32_t(&r)[32], int kb, float keep) {
+    const int v = tid % 128;
+    if (!STATE_ONLY && v < VP) {
+#pragma unroll
+      for (int y = 0; y < 4; ++y) {
+        uint32_t o[4];
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+          o[x] = pack_bf16(__uint_as_float(r[8 * y + 2 * x]), __uint_as_float(r[8 * y + 2 * x + 1]));
+        st_shared16(swizzled(sState + (kb / 2) * VP * kPitch, v, (kb % 2) * 4 + y), o[0], o[1], o[2], o[3]);
+      }
+    }
+#pragma unroll
+    for (int x = 0; x < 32; ++x) r[x] = __float_as_uint(__uint_as_float(r[x]) * keep);
+    tmem_st32(tSt + lanes + 32 * kb, r);
+  };
+  if (!STATE_ONLY && s0 && s.nch > 0 && role < KP / 32) {
+    // the state that comes in: 32 of its rows a role, all loads in flight at once
+    const int v = tid % 128;
+    int64_t t0;
+    int n;
+    chunk_at(s, rev, 0, &t0, &n);
+    uint32_t r[32];
+#pragma unroll
+    for (int x = 0; x < 32; ++x) {
+      const int k = 32 * role + x;
+      r[x] = __float_as_uint(s0[(k < p.K ? k : 0) * s0k + (v < p.V ? v : 0) * s0v]);
+    }
+#pragma unroll
+    for (int x = 0; x < 32; ++x)
+      r[x] = v < p.V && 32 * role + x < p.K ? __float_as_uint(s0m * __uint_as_float(r[x])) : 0u;
+    give(r, role, exp2f(l2 * (float)n));
+    st_wait();
+    fence_async();
+    fence_before();
+    __syncwarp();
+    if (lane == 0) bar_arrive(bInit);
+    __syncwarp();
+  }
+
   if (warp == 16) {
     // ---- copies
     if (lane == 0) {
       for (int c = 0; c < s.nch; ++c) {
         const int st = c % P::kStages;
         const uint32_t again = (c / P::kStages - 1) & 1;
-        if (c >= P::kStages && !bar_wait(bFree23 + 8 * st, again, stop)) break;
+        if (c >= P::kStages && !bar_wait(bFree12 + 8 * st, again, stop)) break;
         int64_t t0;
         int n;
         chunk_at(s, rev, c, &t0, &n);
         const int t = (int)(s.beg + t0);
-        const uint32_t d = base + st * P::kStage, bar = bFull + 8 * st;
-        bar_expect(bar, (STATE_ONLY ? 0 : P::kX2) + P::kX2 + P::kX3);
+        const uint32_t d = base + st * P::kStage;
+        bar_expect(bFull12 + 8 * st, P::kX1 + P::kX2);
 #pragma unroll
-        for (int i = 0; i < KP / 64; ++i) copy_in_4d(d + P::kX1 + i * kHalf, &p.x2, bar, 64 * i, h, t, b);
+        for (int i = 0; i < KP / 64; ++i) {
+          if (!STATE_ONLY) copy_in_4d(d + i * kHalf, &p.x1, bFull12 + 8 * st, 64 * i, h, t, b);
+          copy_in_4d(d + P::kX1 + i * kHalf, &p.x2, bFull12 + 8 * st, 64 * i, h, t, b);
+        }
+        if (c >= P::kStages && !bar_wait(bFree3 + 8 * st, again, stop)) break;
+        bar_expect(bFull3 + 8 * st, P::kX3);
 #pragma unroll
         for (int i = 0; i < VP / 64; ++i)
-          copy_in_4d(d + P::kX1 + P::kX2 + i * kHalf, &p.x3, bar, 64 * i, h, t, b);
-        if (!STATE_ONLY) {
-          if (c >= P::kStages && !bar_wait(bFree1 + 8 * st, again, stop)) break;
-#pragma unroll
-          for (int i = 0; i < KP / 64; ++i) copy_in_4d(d + i * kHalf, &p.x1, bar, 64 * i, h, t, b);
-        }
+          copy_in_4d(d + P::kX1 + P::kX2 + i * kHalf, &p.x3, bFull3 + 8 * st, 64 * i, h, t, b);
       }
     }
   } else if (warp == 17) {
@@ -241,7 +291,7 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_co
         int64_t t0;
         int n;
         chunk_at(s, rev, c, &t0, &n);
-        return bar_wait(bFull + 8 * (c % P::kStages), (c / P::kStages) & 1, stop) &&
+        return bar_wait(bFull12 + 8 * (c % P::kStages), (c / P::kStages) & 1, stop) &&
                (!packed || n == kChunk || bar_wait(bClean, 0, stop));
       };
       const auto scores = [&](int c) {
@@ -255,9 +305,11 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_co
       for (int c = 0; ok && c < s.nch; ++c) {
         const int st = c % P::kStages;
         const uint32_t x1 = base + st * P::kStage, x2 = x1 + P::kX1, x3 = x2 + P::kX2;
-        const bool have = c > 0 || s0;
-        if (STATE_ONLY && !(ok = ready(c))) break;
-        if (!(ok = bar_wait(bSb, c & 1, stop))) break;
+        const bool have = c > 0 || (s0 && !STATE_ONLY);
+        if (STATE_ONLY) ok = ready(c);
+        else if (c > 0) ok = bar_wait(bSb, (c - 1) & 1, stop);
+        else if (s0) ok = bar_wait(bInit, 0, stop);
+        if (!ok) break;
         fence_after();
         if (c + 1 < s.nch || s1) {
 #pragma unroll 1
@@ -272,8 +324,9 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_co
           if (!ok) break;
         }
         if (STATE_ONLY) {
-          mma_commit(bSt);
-          mma_commit(bFree23 + 8 * st);
+          mma_commit(bFree12 + 8 * st);
+          mma_commit(bFree3 + 8 * st);
+          if (c + 1 == s.nch) mma_commit(bSt);
           continue;
         }
         if (c > 0 && !(ok = bar_wait(bOx, (c - 1) & 1, stop))) break;
@@ -283,6 +336,7 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_co
           mma_commit(bOi);
         }
         mma_commit(bSt);
+        mma_commit(bFree12 + 8 * st);
         if (!(ok = bar_wait(bP, c & 1, stop))) break;
         if (c + 1 < s.nch) {
           if (!(ok = ready(c + 1))) break;
@@ -290,10 +344,10 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_co
           scores(c + 1);
         }
         if (have && !(ok = bar_wait(bOs, (c - late) & 1, stop))) break;
+        if (!(ok = bar_wait(bFull3 + 8 * st, (c / P::kStages) & 1, stop))) break;
         fence_after();
         mma_tn<kChunk>(tO, tP, x3, kHalf, dO, have);
         mma_commit(bOf);
-        mma_commit(bFree23 + 8 * st);
       }
     }
   } else if (role == 0 && !STATE_ONLY) {
@@ -353,53 +407,8 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_co
   } else if (role == 1) {
     // ---- state: column v of S (a row of S^T) in lane v
     const int v = tid - 128;
-    // 32 rows of S to its bf16 copy, and decayed to tensor memory
-    const auto give = [&](uint32_t(&r)[32], int kb, float keep) {
-      if (!STATE_ONLY && v < VP) {
-#pragma unroll
-        for (int y = 0; y < 4; ++y) {
-          uint32_t o[4];
-#pragma unroll
-          for (int x = 0; x < 4; ++x)
-            o[x] = pack_bf16(__uint_as_float(r[8 * y + 2 * x]), __uint_as_float(r[8 * y + 2 * x + 1]));
-          st_shared16(swizzled(sState + (kb / 2) * VP * kPitch, v, (kb % 2) * 4 + y), o[0], o[1], o[2], o[3]);
-        }
-      }
-#pragma unroll
-      for (int x = 0; x < 32; ++x) r[x] = __float_as_uint(__uint_as_float(r[x]) * keep);
-      tmem_st32(tSt + lanes + 32 * kb, r);
-    };
-    const auto given = [&]() {
-      st_wait();
-      fence_async();
-      fence_before();
-      __syncwarp();
-      if (lane == 0) bar_arrive(bSb);
-    };
-    if (s.nch > 0) {  // the state that comes in
-      if (s0) {
-        int64_t t0;
-        int n;
-        chunk_at(s, rev, 0, &t0, &n);
-        const float keep = exp2f(l2 * (float)n);
 #pragma unroll 1
-        for (int kb = 0; kb < KP / 32; ++kb) {
-          uint32_t r[32];
-#pragma unroll
-          for (int x = 0; x < 32; ++x) {
-            const int k = 32 * kb + x;
-            r[x] = __float_as_uint(s0[(k < p.K ? k : 0) * s0k + (v < p.V ? v : 0) * s0v]);
-          }
-#pragma unroll
-          for (int x = 0; x < 32; ++x)
-            r[x] = v < p.V && 32 * kb + x < p.K ? __float_as_uint(s0m * __uint_as_float(r[x])) : 0u;
-          give(r, kb, keep);
-        }
-      }
-      given();
-    }
-#pragma unroll 1
-    for (int c = 1; c < s.nch; ++c) {
+    for (int c = 1; !STATE_ONLY && c < s.nch; ++c) {
       int64_t t0;
       int n;
       chunk_at(s, rev, c, &t0, &n);
@@ -413,15 +422,22 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_co
         ld_wait();
         give(r, kb, keep);
       }
-      given();
+      st_wait();
+      fence_async();
+      fence_before();
+      __syncwarp();
+      if (lane == 0) bar_arrive(bSb);
     }
     if (s1) {
       bool ok = true;
       if (s.nch > 0) {
-        ok = warp_wait(bSt, (s.nch - 1) & 1, stop);
+        ok = warp_wait(bSt, STATE_ONLY ? 0 : (s.nch - 1) & 1, stop);
         fence_after();
       }
       if (ok) {
+        // a segment on its own starts from nothing: what came in is added here
+        const float in = STATE_ONLY ? s0m * exp2f(l2 * (float)steps) : s0m;
+        const bool add = s0 && (STATE_ONLY || s.nch == 0);
 #pragma unroll 1
         for (int kb = 0; kb < KP / 32; ++kb) {
           uint32_t r[32];
@@ -433,7 +449,8 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_co
           for (int x = 0; x < 32; ++x) {
             const int k = 32 * kb + x;
             if (v < p.V && k < p.K) {
-              const float f = s.nch > 0 ? __uint_as_float(r[x]) : s0 ? s0m * s0[k * s0k + v * s0v] : 0.f;
+              float f = s.nch > 0 ? __uint_as_float(r[x]) : 0.f;
+              if (add) f = fmaf(in, s0[k * s0k + v * s0v], f);
               s1[(int64_t)k * p.V + v] = s1m * f;
             }
           }
@@ -459,8 +476,9 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_co
       int64_t t0;
       int n;
       chunk_at(s, rev, c, &t0, &n);
-      if (!warp_wait(bFull + 8 * st, (c / P::kStages) & 1, stop)) break;
+      if (!warp_wait(bFull3 + 8 * st, (c / P::kStages) & 1, stop)) break;
       if (packed && n < kChunk) {
+        if (!warp_wait(bFull12 + 8 * st, (c / P::kStages) & 1, stop)) break;
         // the rows from n on belong to the next sequence (one such chunk a row)
         const uint32_t x2 = base + st * P::kStage + P::kX1;
         const int left = kChunk - n;
@@ -478,6 +496,8 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_co
       const uint8_t* col = gen + st * P::kStage + P::kX1 + P::kX2 + (v < VP ? v / 64 : 0) * kHalf + (v % 8) * 2;
       const int piece = (v % 64) / 8;
       const float* wt = n < kChunk ? wlast : wtab;
+      // a segment on its own: weights to its end, the sums never rescaled
+      const float far = STATE_ONLY ? exp2f(l2 * (float)((s.nch - 1 - c) * kChunk)) : 1.f;
 #pragma unroll 1
       for (int jb = STATE_ONLY && role == 0; jb < 4; jb += STATE_ONLY ? 2 : 1) {
         uint32_t hi[16], lo[16];
@@ -485,7 +505,7 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_co
 #pragma unroll
           for (int x = 0; x < 16; x += 2) {
             const float4 w4 = *reinterpret_cast<const float4*>(wt + 32 * jb + 2 * x);
-            const float w[4] = {w4.x, w4.y, w4.z, w4.w};
+            const float w[4] = {w4.x * far, w4.y * far, w4.z * far, w4.w * far};
             float f[4];
 #pragma unroll
             for (int y = 0; y < 4; ++y) {
@@ -522,7 +542,7 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_co
 #pragma unroll 1
     for (int c = 0; c < s.nch; ++c) {
       const int st = c % P::kStages;
-      const uint32_t so = base + st * P::kStage;  // x1's place: both its products are done by then
+      const uint32_t so = base + st * P::kStage + P::kX1 + P::kX2;  // x3's place: its products are done by then
       int64_t t0;
       int n;
       chunk_at(s, rev, c, &t0, &n);
@@ -558,6 +578,7 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_co
           fence_before();
           __syncwarp();
           if (lane == 0) bar_arrive(bOx);
+          __syncwarp();
         }
 #pragma unroll
         for (int y = 0; y < 4; ++y) {
@@ -586,7 +607,7 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_co
           copy_out_commit();
           copy_out_read();
         }
-        bar_arrive(bFree1 + 8 * st);
+        bar_arrive(bFree3 + 8 * st);
       }
     }
     if (i == 0) copy_out_done();
@@ -638,21 +659,20 @@ int padded(int d) { return d <= 64 ? 64 : 128; }
 
 template <int KP, int VP>
 cudaError_t launch_kv(const TcArgs& t, int npass, int64_t rows, cudaStream_t s) {
-  using P = Plan<KP, VP>;
-  static_assert(P::kSmem <= 232448, "fits a block's shared memory");
+  using P = Plan<KP, VP, false>;
+  using Q = Plan<KP, VP, true>;
+  static_assert(P::kSmem <= 232448 && P::kStages >= 2 && Q::kSmem <= 232448, "fits a block's shared memory");
   cudaError_t e = cudaFuncSetAttribute(linattn_tc_kernel<KP, VP, false>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, P::kSmem);
   if (e != cudaSuccess) return e;
   if (t.nseg > 1) {
     e = cudaFuncSetAttribute(linattn_tc_kernel<KP, VP, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             P::kSmem);
+                             Q::kSmem);
     if (e != cudaSuccess) return e;
-    linattn_tc_kernel<KP, VP, true>
-        <<<dim3((unsigned)(rows * (t.nseg - 1)), 1, npass), kThreads, P::kSmem, s>>>(t);
+    linattn_tc_kernel<KP, VP, true><<<(unsigned)(rows * (t.nseg - 1) * npass), kThreads, Q::kSmem, s>>>(t);
     linattn_chain_kernel<<<dim3(KP * VP / 256, (unsigned)rows, npass), 256, 0, s>>>(t);
   }
-  linattn_tc_kernel<KP, VP, false>
-      <<<dim3((unsigned)(rows * t.nseg), 1, npass), kThreads, P::kSmem, s>>>(t);
+  linattn_tc_kernel<KP, VP, false><<<(unsigned)(rows * t.nseg * npass), kThreads, P::kSmem, s>>>(t);
   return cudaGetLastError();
 }
 
@@ -719,6 +739,7 @@ cudaError_t launch_linattn_tc(const LinArgs& a, cudaStream_t s) {
   }
   for (int g = 0; g < 2; ++g) {
     if (!count[g]) continue;
+    t[g].npass = count[g];
     t[g].log_decay = a.log_decay;
     t[g].cu = a.cu;
     t[g].hdr = a.hdr;
