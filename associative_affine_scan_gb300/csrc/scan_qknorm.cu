@@ -14,15 +14,19 @@
 // norm's sum is three to five shuffles and no row is read twice. A lane's eight
 // elements are four pairs (elements 4u.. and R/2 + 4u.., or 8u.. where
 // neighbours are paired), so the rotation needs no exchange. A group of lanes
-// takes up to four heads of one token: the token's cosines and sines are read
-// once for them, and four rows are in flight a lane.
+// takes up to four heads of one token (two in the backward): the token's cosines
+// and sines are read once for them. Blocks walk the tokens of either the queries
+// or the keys, so that a lane keeps its weights (and sums of weight gradients) in
+// registers, and read the next heads, their table entries and the position after
+// that while they work on the current ones.
 #include "scan_mixer.h"
 
 namespace scan {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kHeads = 4;  // heads of one token that a group of lanes takes
+constexpr int kFwdHeads = 4;  // heads of one token that a group of lanes takes
+constexpr int kBwdHeads = 2;
 
 struct QkArgs {
   scan_view4 x[2], y[2], dy[2], dx[2];  // queries, keys
@@ -30,38 +34,51 @@ struct QkArgs {
   const float* cs;
   const float* sn;
   const int32_t* pos;
-  float* part;   // backward: [blocks][2][D] partial weight gradients
+  float* part;   // backward: [blocks][D] partial weight gradients, the queries' first
   float* dw[2];
   int64_t BT, T, P;
   int H[2];
-  int chunks[2];  // ceil(H / kHeads)
+  int chunks[2];  // groups of heads
+  int blocks[2];  // blocks that walk the queries, and the keys
   int D, R;
   int pairs;
   float eps;
 };
 
-// Eight elements of a row: two runs of four (rotated halves apart) or one of eight.
+// Eight elements of a row as they are in memory: two runs of four (the halves of
+// rotated pairs) or one of eight.
 template <typename T>
-__device__ __forceinline__ void load8(const T* row, int lo, int hi, float (&v)[8]);
+struct Raw;
 template <>
-__device__ __forceinline__ void load8<float>(const float* row, int lo, int hi, float (&v)[8]) {
-  const float4 a = *reinterpret_cast<const float4*>(row + lo);
-  const float4 b = *reinterpret_cast<const float4*>(row + hi);
-  v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-  v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-}
-template <>
-__device__ __forceinline__ void load8<__nv_bfloat16>(const __nv_bfloat16* row, int lo, int hi,
-                                                     float (&v)[8]) {
-  const uint2 a = *reinterpret_cast<const uint2*>(row + lo);
-  const uint2 b = *reinterpret_cast<const uint2*>(row + hi);
-  const uint32_t u[4] = {a.x, a.y, b.x, b.y};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    v[2 * i] = __uint_as_float(u[i] << 16);
-    v[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+struct Raw<float> {
+  float4 a, b;
+  __device__ __forceinline__ void load(const float* row, int lo, int hi) {
+    a = *reinterpret_cast<const float4*>(row + lo);
+    b = *reinterpret_cast<const float4*>(row + hi);
   }
-}
+  __device__ __forceinline__ void clear() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
+  __device__ __forceinline__ void get(float (&v)[8]) const {
+    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+  }
+};
+template <>
+struct Raw<__nv_bfloat16> {
+  uint2 a, b;
+  __device__ __forceinline__ void load(const __nv_bfloat16* row, int lo, int hi) {
+    a = *reinterpret_cast<const uint2*>(row + lo);
+    b = *reinterpret_cast<const uint2*>(row + hi);
+  }
+  __device__ __forceinline__ void clear() { a = b = make_uint2(0u, 0u); }
+  __device__ __forceinline__ void get(float (&v)[8]) const {
+    const uint32_t u[4] = {a.x, a.y, b.x, b.y};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = __uint_as_float(u[i] << 16);
+      v[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+    }
+  }
+};
 template <typename T>
 __device__ __forceinline__ void store8(T* row, int lo, int hi, const float (&v)[8]);
 template <>
@@ -124,194 +141,263 @@ __device__ __forceinline__ float group_sum(float v) {
   return v;
 }
 
-// The token's cosines and sines; a position outside the tables gives NaN, so
-// that the mistake shows in the result instead of reading past them.
-__device__ __forceinline__ void load_turn(const QkArgs& a, int64_t tok, const Unit& u, float (&c)[4],
+// Cosines and sines of position p; one outside the tables gives NaN, so that the
+// mistake shows in the result instead of reading past them.
+__device__ __forceinline__ void load_turn(const QkArgs& a, int64_t p, const Unit& u, float (&c)[4],
                                           float (&s)[4]) {
-  const int64_t p = a.pos ? (int64_t)a.pos[tok] : tok % a.T;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) c[i] = 1.f, s[i] = 0.f;
   if (!u.rot) return;
-  if (p < 0 || p >= a.P) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) c[i] = s[i] = __int_as_float(0x7fc00000);
-    return;
-  }
-  const float4 cv = *reinterpret_cast<const float4*>(a.cs + p * (a.R / 2) + u.cs);
-  const float4 sv = *reinterpret_cast<const float4*>(a.sn + p * (a.R / 2) + u.cs);
-  c[0] = cv.x; c[1] = cv.y; c[2] = cv.z; c[3] = cv.w;
-  s[0] = sv.x; s[1] = sv.y; s[2] = sv.z; s[3] = sv.w;
+  const bool ok = p >= 0 && p < a.P;
+  const int64_t at = (ok ? p : 0) * (a.R / 2) + u.cs;
+  const float4 cv = *reinterpret_cast<const float4*>(a.cs + at);
+  const float4 sv = *reinterpret_cast<const float4*>(a.sn + at);
+  const float bad = __int_as_float(0x7fc00000);
+  c[0] = ok ? cv.x : bad; c[1] = ok ? cv.y : bad; c[2] = ok ? cv.z : bad; c[3] = ok ? cv.w : bad;
+  s[0] = ok ? sv.x : bad; s[1] = ok ? sv.y : bad; s[2] = ok ? sv.z : bad; s[3] = ok ? sv.w : bad;
 }
 
 __device__ __forceinline__ void load_weight(const float* w, const Unit& u, float (&v)[8]) {
-  if (w && u.on) load8<float>(w, u.lo, u.hi, v);
-  else {
+  Raw<float> r;
+  if (w && u.on) {
+    r.load(w, u.lo, u.hi);
+    r.get(v);
+  } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = 1.f;
   }
 }
 
-template <typename T, int G, bool PAIRS>
-__global__ void __launch_bounds__(kThreads) qknorm_fwd_kernel(const QkArgs a) {
-  const int per = a.chunks[0] + a.chunks[1];
-  const int64_t item = (int64_t)blockIdx.x * (kThreads / G) + threadIdx.x / G;
-  const bool live = item < a.BT * per;  // lanes of a dead group stay for the shuffles
-  const int64_t tok = live ? item / per : 0;
-  int c = live ? (int)(item % per) : 0;
-  const int m = c >= a.chunks[0];
-  if (m) c -= a.chunks[0];
-  const Unit u = unit_of(threadIdx.x % G, a);
-  const int64_t b = tok / a.T, t = tok % a.T;
-  const int h0 = c * kHeads;
-  const View<const T> x = {static_cast<const T*>(a.x[m].ptr), a.x[m].stride_b, a.x[m].stride_t,
-                           a.x[m].stride_h};
-  const View<T> y = {static_cast<T*>(a.y[m].ptr), a.y[m].stride_b, a.y[m].stride_t, a.y[m].stride_h};
-  float v[kHeads][8];
-#pragma unroll
-  for (int i = 0; i < kHeads; ++i) {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[i][j] = 0.f;
-    if (live && u.on && h0 + i < a.H[m]) load8<T>(x.row(b, t, h0 + i), u.lo, u.hi, v[i]);
+// A group's place in its walk over (token, heads): items `step` apart.
+struct Walk {
+  int64_t item, b, t;
+  int c;
+  int64_t step, db, dt;
+  int dc;
+  __device__ __forceinline__ Walk(const QkArgs& a, int m, int64_t first, int64_t by) {
+    const int per = a.chunks[m];
+    item = first;
+    step = by;
+    c = (int)(first % per);
+    const int64_t tok = first / per;
+    b = tok / a.T;
+    t = tok % a.T;
+    dc = (int)(by % per);
+    const int64_t dtok = by / per;
+    db = dtok / a.T;
+    dt = dtok % a.T;
   }
-  float cs[4], sn[4], w[8];
-  load_turn(a, tok, u, cs, sn);
-  load_weight(a.w[m], u, w);
+  __device__ __forceinline__ void next(const QkArgs& a, int m) {
+    item += step;
+    b += db;
+    t += dt;
+    c += dc;
+    if (c >= a.chunks[m]) c -= a.chunks[m], ++t;
+    if (t >= a.T) t -= a.T, ++b;
+  }
+  __device__ __forceinline__ int64_t position(const QkArgs& a) const {
+    return a.pos ? (int64_t)a.pos[b * a.T + t] : t;
+  }
+};
+
+template <typename T, int N>
+__device__ __forceinline__ void load_heads(const View<const T>& x, const Walk& w, const Unit& u, int H, bool live,
+                                           Raw<T> (&r)[N]) {
 #pragma unroll
-  for (int i = 0; i < kHeads; ++i) {
-    float sq = 0.f;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) sq = fmaf(v[i][j], v[i][j], sq);
-    const float r = rsqrtf(group_sum<G>(sq) / (float)a.D + a.eps);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[i][j] *= r * w[j];
-    if (u.rot) rotate(v[i], cs, sn, PAIRS);
-    if (live && u.on && h0 + i < a.H[m]) store8<T>(y.row(b, t, h0 + i), u.lo, u.hi, v[i]);
+  for (int i = 0; i < N; ++i) {
+    if (live && u.on && w.c * N + i < H) r[i].load(x.row(w.b, w.t, w.c * N + i), u.lo, u.hi);
+    else r[i].clear();
   }
 }
 
-// Each block walks tokens with the weight gradients in registers and leaves one
-// partial sum; the partial sums are added in block order by the kernel below,
-// so the result does not depend on the order in which blocks finish.
+template <typename T>
+__device__ __forceinline__ View<T> qk_view(const scan_view4& v) {
+  return View<T>{static_cast<T*>(v.ptr), v.stride_b, v.stride_t, v.stride_h};
+}
+
+template <typename T, int G, bool PAIRS>
+__global__ void __launch_bounds__(kThreads) qknorm_fwd_kernel(const QkArgs a) {
+  constexpr int N = kFwdHeads;
+  const int m = blockIdx.x >= a.blocks[0];
+  const int64_t block = m ? blockIdx.x - a.blocks[0] : blockIdx.x;
+  const int64_t items = a.BT * a.chunks[m];
+  const Unit u = unit_of(threadIdx.x % G, a);
+  const View<const T> x = m ? qk_view<const T>(a.x[1]) : qk_view<const T>(a.x[0]);
+  const View<T> y = m ? qk_view<T>(a.y[1]) : qk_view<T>(a.y[0]);
+  const int H = a.H[m];
+  Walk w(a, m, block * (kThreads / G) + threadIdx.x / G, (int64_t)a.blocks[m] * (kThreads / G));
+  Walk ahead = w;
+  float wt[8], cs[4] = {1.f, 1.f, 1.f, 1.f}, sn[4] = {0.f, 0.f, 0.f, 0.f};
+  Raw<T> r[N];
+  load_heads<T, N>(x, w, u, H, w.item < items, r);
+  if (w.item < items) load_turn(a, w.position(a), u, cs, sn);
+  load_weight(a.w[m], u, wt);
+  ahead.next(a, m);
+  int64_t p1 = ahead.item < items ? ahead.position(a) : 0;
+  // whole warps leave together: the bound is on the warp's first group
+  int64_t lead = w.item - (threadIdx.x % 32) / G;
+  while (lead < items) {
+    const bool more = ahead.item < items;
+    Raw<T> r1[N];
+    float cs1[4] = {1.f, 1.f, 1.f, 1.f}, sn1[4] = {0.f, 0.f, 0.f, 0.f};
+    load_heads<T, N>(x, ahead, u, H, more, r1);
+    if (more) load_turn(a, p1, u, cs1, sn1);
+    const Walk now = w;
+    w = ahead;
+    ahead.next(a, m);
+    if (ahead.item < items) p1 = ahead.position(a);
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      float v[8], sq = 0.f;
+      r[i].get(v);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) sq = fmaf(v[j], v[j], sq);
+      const float rs = rsqrtf(group_sum<G>(sq) / (float)a.D + a.eps);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] *= rs * wt[j];
+      if (u.rot) rotate(v, cs, sn, PAIRS);
+      if (now.item < items && u.on && now.c * N + i < H)
+        store8<T>(y.row(now.b, now.t, now.c * N + i), u.lo, u.hi, v);
+      r[i] = r1[i];
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) cs[i] = cs1[i], sn[i] = sn1[i];
+    lead += w.step;
+  }
+}
+
+// Each block leaves one partial sum of its weight's gradient; the partial sums are
+// added in block order by the kernel below, so the result does not depend on the
+// order in which blocks finish.
 template <typename T, int G, bool PAIRS>
 __global__ void __launch_bounds__(kThreads) qknorm_bwd_kernel(const QkArgs a) {
-  const int per = a.chunks[0] + a.chunks[1];
-  const int ng = kThreads / G;
+  constexpr int N = kBwdHeads, NG = kThreads / G;
+  const int m = blockIdx.x >= a.blocks[0];
+  const int64_t block = m ? blockIdx.x - a.blocks[0] : blockIdx.x;
+  const int64_t items = a.BT * a.chunks[m];
   const Unit u = unit_of(threadIdx.x % G, a);
-  float dw[2][8];
+  const View<const T> x = m ? qk_view<const T>(a.x[1]) : qk_view<const T>(a.x[0]);
+  const View<const T> dy = m ? qk_view<const T>(a.dy[1]) : qk_view<const T>(a.dy[0]);
+  const View<T> dx = m ? qk_view<T>(a.dx[1]) : qk_view<T>(a.dx[0]);
+  const int H = a.H[m];
+  Walk w(a, m, block * NG + threadIdx.x / G, (int64_t)a.blocks[m] * NG);
+  Walk ahead = w;
+  float wt[8], dw[8], cs[4] = {1.f, 1.f, 1.f, 1.f}, sn[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-  for (int j = 0; j < 8; ++j) dw[0][j] = dw[1][j] = 0.f;
-  const int64_t total = a.BT * per;
-  const int64_t step = (int64_t)gridDim.x * ng;
-  // whole warps leave together: the bound is on the warp's first group
-  for (int64_t base = (int64_t)blockIdx.x * ng + (threadIdx.x / 32) * (32 / G); base < total;
-       base += step) {
-    const int64_t item = base + (threadIdx.x % 32) / G;
-    const bool live = item < total;
-    const int64_t tok = live ? item / per : 0;
-    int c = live ? (int)(item % per) : 0;
-    const int m = c >= a.chunks[0];
-    if (m) c -= a.chunks[0];
-    const int64_t b = tok / a.T, t = tok % a.T;
-    const int h0 = c * kHeads;
-    const View<const T> x = {static_cast<const T*>(a.x[m].ptr), a.x[m].stride_b, a.x[m].stride_t,
-                             a.x[m].stride_h};
-    const View<const T> dy = {static_cast<const T*>(a.dy[m].ptr), a.dy[m].stride_b,
-                              a.dy[m].stride_t, a.dy[m].stride_h};
-    const View<T> dx = {static_cast<T*>(a.dx[m].ptr), a.dx[m].stride_b, a.dx[m].stride_t,
-                        a.dx[m].stride_h};
-    float v[kHeads][8], g[kHeads][8];
-#pragma unroll
-    for (int i = 0; i < kHeads; ++i) {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[i][j] = g[i][j] = 0.f;
-      if (live && u.on && h0 + i < a.H[m]) {
-        load8<T>(x.row(b, t, h0 + i), u.lo, u.hi, v[i]);
-        load8<T>(dy.row(b, t, h0 + i), u.lo, u.hi, g[i]);
-      }
-    }
-    float cs[4], sn[4], w[8];
-    load_turn(a, tok, u, cs, sn);
-    load_weight(a.w[m], u, w);
+  for (int j = 0; j < 8; ++j) dw[j] = 0.f;
+  Raw<T> r[N], g[N];
+  load_heads<T, N>(x, w, u, H, w.item < items, r);
+  load_heads<T, N>(dy, w, u, H, w.item < items, g);
+  if (w.item < items) load_turn(a, w.position(a), u, cs, sn);
+  load_weight(a.w[m], u, wt);
+  ahead.next(a, m);
+  int64_t p1 = ahead.item < items ? ahead.position(a) : 0;
+  int64_t lead = w.item - (threadIdx.x % 32) / G;
+  while (lead < items) {
+    const bool more = ahead.item < items;
+    Raw<T> r1[N], g1[N];
+    float cs1[4] = {1.f, 1.f, 1.f, 1.f}, sn1[4] = {0.f, 0.f, 0.f, 0.f};
+    load_heads<T, N>(x, ahead, u, H, more, r1);
+    load_heads<T, N>(dy, ahead, u, H, more, g1);
+    if (more) load_turn(a, p1, u, cs1, sn1);
+    const Walk now = w;
+    w = ahead;
+    ahead.next(a, m);
+    if (ahead.item < items) p1 = ahead.position(a);
 #pragma unroll
     for (int i = 0; i < 4; ++i) sn[i] = -sn[i];
 #pragma unroll
-    for (int i = 0; i < kHeads; ++i) {
-      const bool here = live && u.on && h0 + i < a.H[m];
-      if (u.rot) rotate(g[i], cs, sn, PAIRS);
-      float sq = 0.f, gn = 0.f;
+    for (int i = 0; i < N; ++i) {
+      const bool here = now.item < items && u.on && now.c * N + i < H;
+      float v[8], d[8], sq = 0.f, gn = 0.f;
+      r[i].get(v);
+      g[i].get(d);
+      if (u.rot) rotate(d, cs, sn, PAIRS);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        sq = fmaf(v[i][j], v[i][j], sq);
-        gn = fmaf(g[i][j] * w[j], v[i][j], gn);
+        sq = fmaf(v[j], v[j], sq);
+        gn = fmaf(d[j] * wt[j], v[j], gn);
       }
-      const float r = rsqrtf(group_sum<G>(sq) / (float)a.D + a.eps);
-      const float mean = group_sum<G>(gn) * r / (float)a.D;  // mean(g n)
-      float o[8];
+      const float rs = rsqrtf(group_sum<G>(sq) / (float)a.D + a.eps);
+      const float mean = group_sum<G>(gn) * rs / (float)a.D;  // mean(g n)
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const float n = v[i][j] * r;
-        const float d = here ? g[i][j] * n : 0.f;
-        if (m) dw[1][j] += d;
-        else dw[0][j] += d;
-        o[j] = r * (g[i][j] * w[j] - n * mean);
+        const float n = v[j] * rs;
+        dw[j] += here ? d[j] * n : 0.f;
+        v[j] = rs * (d[j] * wt[j] - n * mean);
       }
-      if (here) store8<T>(dx.row(b, t, h0 + i), u.lo, u.hi, o);
+      if (here) store8<T>(dx.row(now.b, now.t, now.c * N + i), u.lo, u.hi, v);
+      r[i] = r1[i];
+      g[i] = g1[i];
     }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) cs[i] = cs1[i], sn[i] = sn1[i];
+    lead += w.step;
   }
   // groups of the block, in order
   __shared__ float red[kThreads * 8];
 #pragma unroll
-  for (int m = 0; m < 2; ++m) {
-    __syncthreads();
-#pragma unroll
-    for (int j = 0; j < 8; ++j) red[threadIdx.x * 8 + j] = dw[m][j];
-    __syncthreads();
-    if (threadIdx.x < G && u.on) {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        float s = 0.f;
-        for (int k = 0; k < ng; ++k) s += red[(k * G + threadIdx.x) * 8 + j];
-        a.part[((int64_t)blockIdx.x * 2 + m) * a.D + (j < 4 ? u.lo + j : u.hi + j - 4)] = s;
-      }
-    }
+  for (int j = 0; j < 8; ++j) red[j * kThreads + threadIdx.x] = dw[j];
+  __syncthreads();
+  for (int i = threadIdx.x; i < 8 * G; i += kThreads) {
+    const int lane = i % G, j = i / G;
+    const Unit v = unit_of(lane, a);
+    if (!v.on) continue;
+    float s = 0.f;
+    for (int k = 0; k < NG; ++k) s += red[j * kThreads + k * G + lane];
+    a.part[(int64_t)blockIdx.x * a.D + (j < 4 ? v.lo + j : v.hi + j - 4)] = s;
   }
 }
 
-// Columns of the partial sums, one block per (matrix, 32 columns): 32 lanes of
-// columns by eight slices of blocks, the slices then added in order.
-__global__ void __launch_bounds__(256) qknorm_dw_kernel(const QkArgs a, int blocks) {
-  const int m = blockIdx.y, col = blockIdx.x * 32 + threadIdx.x % 32, sl = threadIdx.x / 32;
-  __shared__ float red[8][32];
+// Columns of the partial sums, one block per (queries or keys, 32 columns): 32
+// lanes of columns by 32 slices of blocks, the slices then added in order.
+__global__ void __launch_bounds__(1024) qknorm_dw_kernel(const QkArgs a) {
+  const int m = blockIdx.y, lane = threadIdx.x % 32, col = blockIdx.x * 32 + lane, sl = threadIdx.x / 32;
+  if (!a.dw[m]) return;
+  __shared__ float red[32][33];
+  const float* p = a.part + (int64_t)(m ? a.blocks[0] : 0) * a.D + col;
   float s = 0.f;
-  if (col < a.D)
-    for (int k = sl; k < blocks; k += 8) s += a.part[((int64_t)k * 2 + m) * a.D + col];
-  red[sl][threadIdx.x % 32] = s;
+  if (col < a.D) {
+#pragma unroll 4
+    for (int k = sl; k < a.blocks[m]; k += 32) s += p[(int64_t)k * a.D];
+  }
+  red[sl][lane] = s;
   __syncthreads();
-  if (sl == 0 && col < a.D && a.dw[m]) {
-    for (int k = 1; k < 8; ++k) s += red[k][threadIdx.x % 32];
+  if (sl == 0 && col < a.D) {
+    for (int k = 1; k < 32; ++k) s += red[k][lane];
     a.dw[m][col] = s;
   }
 }
 
-constexpr int kBwdBlocks = 152 * 4;
+// Blocks of a walk: as many as stay resident (four or five an SM), shared between
+// queries and keys by their numbers of items; a block more where one side has few.
+constexpr int kFwdBlocks = 152 * 5, kBwdBlocks = 152 * 4;
+
+void share_blocks(QkArgs* a, int groups, int most) {
+  const int64_t items[2] = {a->BT * a->chunks[0], a->BT * a->chunks[1]};
+  for (int m = 0; m < 2; ++m) {
+    const int64_t need = (items[m] + groups - 1) / groups;
+    const int64_t part = most * items[m] / (items[0] + items[1]);
+    a->blocks[m] = (int)(need < part ? need : part > 0 ? part : need > 0 ? 1 : 0);
+  }
+}
 
 int group_lanes(int D) { return D <= 64 ? 8 : D <= 128 ? 16 : 32; }
 
 template <typename T, int G>
-cudaError_t qk_launch_g(const QkArgs& a, bool fwd, cudaStream_t s) {
-  const int64_t items = a.BT * (a.chunks[0] + a.chunks[1]);
-  const int64_t need = (items + kThreads / G - 1) / (kThreads / G);
+cudaError_t qk_launch_g(QkArgs a, bool fwd, cudaStream_t s) {
+  const int heads = fwd ? kFwdHeads : kBwdHeads;
+  for (int m = 0; m < 2; ++m) a.chunks[m] = (a.H[m] + heads - 1) / heads;
+  share_blocks(&a, kThreads / G, fwd ? kFwdBlocks : kBwdBlocks);
+  const int blocks = a.blocks[0] + a.blocks[1];
   if (fwd) {
-    if (a.pairs) qknorm_fwd_kernel<T, G, true><<<(unsigned)need, kThreads, 0, s>>>(a);
-    else qknorm_fwd_kernel<T, G, false><<<(unsigned)need, kThreads, 0, s>>>(a);
+    if (a.pairs) qknorm_fwd_kernel<T, G, true><<<blocks, kThreads, 0, s>>>(a);
+    else qknorm_fwd_kernel<T, G, false><<<blocks, kThreads, 0, s>>>(a);
     return cudaGetLastError();
   }
-  const int blocks = (int)(need < kBwdBlocks ? need : kBwdBlocks);
   if (a.pairs) qknorm_bwd_kernel<T, G, true><<<blocks, kThreads, 0, s>>>(a);
   else qknorm_bwd_kernel<T, G, false><<<blocks, kThreads, 0, s>>>(a);
   cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
-  qknorm_dw_kernel<<<dim3((a.D + 31) / 32, 2), 256, 0, s>>>(a, blocks);
+  if (e != cudaSuccess || (!a.dw[0] && !a.dw[1])) return e;
+  qknorm_dw_kernel<<<dim3((a.D + 31) / 32, 2), 1024, 0, s>>>(a);
   return cudaGetLastError();
 }
 
@@ -340,9 +426,7 @@ scan_status qk_args(QkArgs* a, const scan_view4* q, const scan_view4* k, const f
   if (!(eps >= 0.f)) return SCAN_ERR_INVALID_ARG;
   if (D % 8 || D > 256 || R % 8) return SCAN_ERR_UNSUPPORTED;
   if (Hq > (1 << 20) || Hk > (1 << 20)) return SCAN_ERR_UNSUPPORTED;
-  // grid.x counts blocks of at least 8 items; the product is bounded step by step
   if (B > (1LL << 31) || T > (1LL << 31) || B * T > (1LL << 40)) return SCAN_ERR_UNSUPPORTED;
-  if (B * T * ((Hq + 3) / 4 + (Hk + 3) / 4) / 8 >= 0x7fffffffLL) return SCAN_ERR_UNSUPPORTED;
   if (R > 0 && B * T > 0 && (!cs || !sn)) return SCAN_ERR_INVALID_ARG;
   if ((uintptr_t)cs % 16 || (uintptr_t)sn % 16 || (uintptr_t)qw % 16 || (uintptr_t)kw % 16)
     return SCAN_ERR_ALIGNMENT;
@@ -361,8 +445,6 @@ scan_status qk_args(QkArgs* a, const scan_view4* q, const scan_view4* k, const f
   a->P = P;
   a->H[0] = (int)Hq;
   a->H[1] = (int)Hk;
-  a->chunks[0] = (int)((Hq + kHeads - 1) / kHeads);
-  a->chunks[1] = (int)((Hk + kHeads - 1) / kHeads);
   a->D = (int)D;
   a->R = (int)R;
   a->pairs = interleaved != 0;
@@ -381,7 +463,7 @@ extern "C" {
 
 size_t qk_norm_rope_workspace_bytes(int64_t D) {
   if (D < 1 || D % 8 || D > 256) return 0;
-  return (size_t)kBwdBlocks * 2 * (size_t)D * 4;
+  return (size_t)(kBwdBlocks + 2) * (size_t)D * 4;
 }
 
 scan_status qk_norm_rope_fwd(const scan_view4* q, const scan_view4* k, const float* q_weight,

@@ -15,6 +15,7 @@
 // multiply-adds, four threads a row: bound by the shared-memory reads of the
 // products. Only tiles with a seen pair are visited.
 #include "scan_mixer.h"
+#include "scan_window_step.h"
 #include "scan_window_tc.h"
 
 namespace scan {
@@ -321,18 +322,7 @@ scan_status win_workspace(WinArgs* a, void* ws, size_t bytes, size_t need) {
 }
 
 // ---------------------------------------------------------------------------
-// one token a request over a ring of S + W cached keys
-
-struct WinStepArgs {
-  scan_view4 q, k, v, o;
-  void *kc, *vc;  // [n_slots, S + W, Hk, D]
-  const int32_t* slots;
-  const int32_t* pos;
-  int64_t n_slots, cap;  // cap = S + W
-  int64_t W, S;
-  int Hq, Hk, D;
-  float scale;
-};
+// one token a request over a ring of S + W cached keys, any operands
 
 // One block a (request, query head), eight warps that take every eighth key.
 template <typename T>
@@ -484,13 +474,10 @@ scan_status window_attn_bwd(const scan_view4* q, const scan_view4* k, const scan
   a.lse = const_cast<float*>(lse);
   a.delta = a.ws;
   cudaError_t e;
-  if (window_tc_fits(a, dt, true)) {
-    e = delta_launch<__nv_bfloat16>(a, stream);
-    if (e == cudaSuccess)
-      e = launch_window_tc_bwd(a, a.ws + round_up((size_t)(B * Hq * Tq) * 4, 256) / 4, stream);
-  } else {
+  if (window_tc_fits(a, dt, true))
+    e = launch_window_tc_bwd(a, a.ws + round_up((size_t)(B * Hq * Tq) * 4, 256) / 4, stream);
+  else
     e = launch_window_general_bwd(a, dt, stream);
-  }
   return e == cudaSuccess ? SCAN_OK : SCAN_ERR_CUDA;
 }
 
@@ -515,6 +502,7 @@ scan_status window_attn_step(const scan_view4* q, const scan_view4* k, const sca
   if (window + sinks > 0x7fffffffLL) return SCAN_ERR_UNSUPPORTED;
   WinStepArgs a{*q, *k, *v, *o, k_cache, v_cache, slots, positions, n_slots, window + sinks,
                 window, sinks, (int)Hq, (int)Hk, (int)D, scale};
+  if (window_step_fits(a, dt)) return launch_window_step(a, B, stream) == cudaSuccess ? SCAN_OK : SCAN_ERR_CUDA;
   if (dt == SCAN_BF16) window_step_general<__nv_bfloat16><<<(unsigned)(B * Hq), 256, 0, stream>>>(a);
   else window_step_general<float><<<(unsigned)(B * Hq), 256, 0, stream>>>(a);
   return cudaGetLastError() == cudaSuccess ? SCAN_OK : SCAN_ERR_CUDA;

@@ -1,0 +1,276 @@
+// scan_window_step.cu -- sliding-window attention of one token a request over its
+// ring of cached keys and values (bf16 caches).
+//
+// Bound by DRAM: each cached row is read once for the query heads that share it
+// (4 G multiply-adds a byte pair at most). A warp takes 16 keys at a time: all of
+// its 16-byte loads of their K and V rows go out together, 8 KB a warp, then two
+// sets of m16n8k16 products: scores of up to 16 query heads (the rows) by 16 keys,
+// and weights by V. The sums' index order is free, so each fragment is what a
+// thread loaded 16 bytes of: the scores' index runs over the D elements in the
+// order that a row's quarter-warp chunks have, and the columns of the output are
+// the elements in the order 8 n + j. Fragments of V pair two keys' elements.
+//
+// A request's keys are split over the blocks of a cluster (up to 16) when the
+// requests alone do not fill the SMs; the partial maxima, sums and outputs meet
+// through distributed shared memory and are added in rank order.
+#include <cooperative_groups.h>
+
+#include "scan_window_step.h"
+
+namespace scan {
+namespace {
+
+namespace cg = cooperative_groups;
+
+constexpr int kWarps = 4;
+
+__device__ __forceinline__ uint4 ld16(const __nv_bfloat16* p, bool on) {
+  uint4 v = make_uint4(0u, 0u, 0u, 0u);
+  if (on) asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                       : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                       : "l"(p));
+  return v;
+}
+__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                         uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t word(const uint4& v, int i) {
+  return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
+}
+
+// ROWS: 8 or 16 query heads a block (the fragments' second eight rows are empty at 8).
+template <int DP, int ROWS>
+__global__ void __launch_bounds__(32 * kWarps) window_step_kernel(const WinStepArgs a) {
+  using bf16 = __nv_bfloat16;
+  constexpr int KK = DP / 32, HALF = DP / 64;
+  __shared__ float s_m[kWarps][ROWS], s_l[kWarps][ROWS];
+  __shared__ float s_o[kWarps][ROWS][DP];
+  __shared__ float b_m[ROWS], b_l[ROWS];
+  cg::cluster_group cluster = cg::this_cluster();
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+  const int g = lane / 4, c = lane % 4;
+  const int split = blockIdx.x, splits = gridDim.x;
+  const int G = a.Hq / a.Hk, tiles = (G + ROWS - 1) / ROWS;
+  const int hk = blockIdx.y / tiles, r0 = (blockIdx.y % tiles) * ROWS;  // heads r0.. of the group
+  const int rows = G - r0 < ROWS ? G - r0 : ROWS;
+  const int64_t b = blockIdx.z;
+  const int64_t slot = a.slots ? (int64_t)a.slots[b] : b, pos = a.pos[b];
+  bf16* const o = static_cast<bf16*>(a.o.ptr) + b * a.o.stride_b + ((int64_t)hk * G + r0) * a.o.stride_h;
+  if (slot < 0 || slot >= a.n_slots || pos < 0) {  // an idle request (the whole cluster)
+    if (split == 0)
+      for (int i = threadIdx.x; i < rows * a.D; i += 32 * kWarps)
+        o[(i / a.D) * a.o.stride_h + i % a.D] = __float2bfloat16_rn(0.f);
+    return;
+  }
+  const int64_t at = pos < a.S ? pos : a.S + (pos - a.S) % a.W;
+  const int64_t n = pos + 1 < a.cap ? pos + 1 : a.cap;
+  const int64_t row = (int64_t)a.Hk * a.D;
+  bf16* const kc = static_cast<bf16*>(a.kc) + slot * a.cap * row + (int64_t)hk * a.D;
+  bf16* const vc = static_cast<bf16*>(a.vc) + slot * a.cap * row + (int64_t)hk * a.D;
+  const bf16* const kn = static_cast<const bf16*>(a.k.ptr) + b * a.k.stride_b + hk * a.k.stride_h;
+  const bf16* const vn = static_cast<const bf16*>(a.v.ptr) + b * a.v.stride_b + hk * a.v.stride_h;
+  // the new token joins the cache; its row is read from k and v, never from there
+  if (split == 0 && r0 == 0)
+    for (int i = threadIdx.x; i < a.D; i += 32 * kWarps) kc[at * row + i] = kn[i], vc[at * row + i] = vn[i];
+
+  // queries as the left operand: rows g and g + 8
+  uint4 q[KK], q8[KK];
+  {
+    const bf16* qp = static_cast<const bf16*>(a.q.ptr) + b * a.q.stride_b + ((int64_t)hk * G + r0) * a.q.stride_h;
+#pragma unroll
+    for (int k = 0; k < KK; ++k) {
+      const int d = 32 * k + 8 * c;
+      q[k] = ld16(qp + g * a.q.stride_h + d, g < rows && d < a.D);
+      q8[k] = ROWS == 16 ? ld16(qp + (g + 8) * a.q.stride_h + d, g + 8 < rows && d < a.D) : make_uint4(0, 0, 0, 0);
+    }
+  }
+  const float sl2 = a.scale * 1.44269504088896341f;
+  float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+  float acc[HALF][8][4];
+#pragma unroll
+  for (int h = 0; h < HALF; ++h)
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+#pragma unroll
+      for (int x = 0; x < 4; ++x) acc[h][j][x] = 0.f;
+
+  const int64_t groups = (n + 15) / 16, per = (groups + splits - 1) / splits;
+  const int64_t first = split * per, last = first + per < groups ? first + per : groups;
+  for (int64_t t = first + warp; t < last; t += kWarps) {
+    const int64_t j0 = t * 16;
+    uint4 kv[2][KK], vv[4][HALF];
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      const int64_t j = j0 + 8 * x + g;
+      const bf16* p = j == at ? kn : kc + j * row;
+#pragma unroll
+      for (int k = 0; k < KK; ++k) kv[x][k] = ld16(p + 32 * k + 8 * c, j < n && 32 * k + 8 * c < a.D);
+    }
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      const int64_t j = j0 + 2 * c + (x & 1) + 8 * (x >> 1);
+      const bf16* p = j == at ? vn : vc + j * row;
+#pragma unroll
+      for (int h = 0; h < HALF; ++h) vv[x][h] = ld16(p + 64 * h + 8 * g, j < n && 64 * h + 8 * g < a.D);
+    }
+    float s[2][4];
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+#pragma unroll
+      for (int y = 0; y < 4; ++y) s[x][y] = 0.f;
+#pragma unroll
+      for (int k = 0; k < KK; ++k) {
+        mma16816(s[x], q[k].x, q8[k].x, q[k].y, q8[k].y, kv[x][k].x, kv[x][k].y);
+        mma16816(s[x], q[k].z, q8[k].z, q[k].w, q8[k].w, kv[x][k].z, kv[x][k].w);
+      }
+    }
+    // s[x][y], s[x][2 + y]: heads g and g + 8, key j0 + 8 x + 2 c + y
+#pragma unroll
+    for (int x = 0; x < 2; ++x)
+#pragma unroll
+      for (int y = 0; y < 2; ++y)
+        if (j0 + 8 * x + 2 * c + y >= n) s[x][y] = s[x][2 + y] = -INFINITY;
+    float p[2][4];
+#pragma unroll
+    for (int h = 0; h < ROWS / 8; ++h) {
+      float top = fmaxf(fmaxf(s[0][2 * h], s[0][2 * h + 1]), fmaxf(s[1][2 * h], s[1][2 * h + 1]));
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      const float mn = fmaxf(m[h], top * sl2);
+      const float from = mn == -INFINITY ? 0.f : mn, keep = ex2(m[h] - from);
+      m[h] = mn;
+      float sum = 0.f;
+#pragma unroll
+      for (int x = 0; x < 2; ++x)
+#pragma unroll
+        for (int y = 0; y < 2; ++y) sum += p[x][2 * h + y] = ex2(fmaf(s[x][2 * h + y], sl2, -from));
+      l[h] = l[h] * keep + sum;
+#pragma unroll
+      for (int i = 0; i < HALF; ++i)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          acc[i][j][2 * h] *= keep;
+          acc[i][j][2 * h + 1] *= keep;
+        }
+    }
+    const uint32_t a0 = pack2(p[0][0], p[0][1]), a2 = pack2(p[1][0], p[1][1]);
+    const uint32_t a1 = ROWS == 16 ? pack2(p[0][2], p[0][3]) : 0u, a3 = ROWS == 16 ? pack2(p[1][2], p[1][3]) : 0u;
+#pragma unroll
+    for (int i = 0; i < HALF; ++i)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const uint32_t sel = j & 1 ? 0x7632u : 0x5410u;
+        mma16816(acc[i][j], a0, a1, a2, a3, __byte_perm(word(vv[0][i], j / 2), word(vv[1][i], j / 2), sel),
+                 __byte_perm(word(vv[2][i], j / 2), word(vv[3][i], j / 2), sel));
+      }
+  }
+  // the warps' parts, then the block's
+#pragma unroll
+  for (int h = 0; h < ROWS / 8; ++h) {
+    l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
+    l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
+    if (c == 0) s_m[warp][8 * h + g] = m[h], s_l[warp][8 * h + g] = l[h];
+#pragma unroll
+    for (int i = 0; i < HALF; ++i)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        s_o[warp][8 * h + g][64 * i + 16 * c + j] = acc[i][j][2 * h];
+        s_o[warp][8 * h + g][64 * i + 16 * c + 8 + j] = acc[i][j][2 * h + 1];
+      }
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < ROWS * DP; i += 32 * kWarps) {
+    const int r = i / DP, d = i % DP;
+    float top = s_m[0][r];
+#pragma unroll
+    for (int w = 1; w < kWarps; ++w) top = fmaxf(top, s_m[w][r]);
+    const float from = top == -INFINITY ? 0.f : top;
+    float sum = 0.f, e = 0.f;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      const float f = ex2(s_m[w][r] - from);
+      sum = fmaf(s_l[w][r], f, sum);
+      e = fmaf(s_o[w][r][d], f, e);
+    }
+    if (splits == 1) {
+      if (r < rows && d < a.D) o[r * a.o.stride_h + d] = __float2bfloat16_rn(e / sum);
+    } else {
+      s_o[0][r][d] = e;  // read by no other thread
+      if (d == 0) b_m[r] = top, b_l[r] = sum;
+    }
+  }
+  if (splits == 1) return;
+  // the cluster's parts: rank by rank, each block a share of the outputs
+  cluster.sync();
+  for (int i = split * 32 * kWarps + threadIdx.x; i < rows * DP; i += splits * 32 * kWarps) {
+    const int r = i / DP, d = i % DP;
+    float top = -INFINITY;
+    for (int k = 0; k < splits; ++k) top = fmaxf(top, *cluster.map_shared_rank(&b_m[r], k));
+    float sum = 0.f, e = 0.f;
+    for (int k = 0; k < splits; ++k) {
+      const float f = ex2(*cluster.map_shared_rank(&b_m[r], k) - top);
+      sum = fmaf(*cluster.map_shared_rank(&b_l[r], k), f, sum);
+      e = fmaf(*cluster.map_shared_rank(&s_o[0][r][d], k), f, e);
+    }
+    if (d < a.D) o[r * a.o.stride_h + d] = __float2bfloat16_rn(e / sum);
+  }
+  cluster.sync();  // no block leaves while its part may be read
+}
+
+template <int DP, int ROWS>
+cudaError_t launch_step(const WinStepArgs& a, int64_t B, int splits, cudaStream_t s) {
+  const int G = a.Hq / a.Hk, tiles = (G + ROWS - 1) / ROWS;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(splits, (unsigned)(a.Hk * tiles), (unsigned)B);
+  cfg.blockDim = dim3(32 * kWarps);
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = splits;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  if (splits > 8) {
+    const cudaError_t e = cudaFuncSetAttribute(window_step_kernel<DP, ROWS>,
+                                               cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaLaunchKernelEx(&cfg, window_step_kernel<DP, ROWS>, a);
+}
+
+// Rows of 16-byte pieces that this kernel's loads can address.
+bool aligned16(const scan_view4& v) {
+  return (uintptr_t)v.ptr % 16 == 0 && v.stride_b % 8 == 0 && v.stride_h % 8 == 0;
+}
+
+}  // namespace
+
+bool window_step_fits(const WinStepArgs& a, scan_dtype dt) {
+  return dt == SCAN_BF16 && aligned16(a.q) && aligned16(a.k) && aligned16(a.v);
+}
+
+// Splits: two blocks an SM or more, as long as a warp still has 16 keys.
+cudaError_t launch_window_step(const WinStepArgs& a, int64_t B, cudaStream_t s) {
+  const int G = a.Hq / a.Hk, rows = G <= 8 ? 8 : 16;
+  const int64_t blocks = B * a.Hk * ((G + rows - 1) / rows);
+  int splits = 1;
+  while (splits < 16 && blocks * splits < 2 * 152 && a.cap >= (int64_t)splits * 2 * 16 * kWarps) splits *= 2;
+  if (a.D <= 64) return rows == 8 ? launch_step<64, 8>(a, B, splits, s) : launch_step<64, 16>(a, B, splits, s);
+  return rows == 8 ? launch_step<128, 8>(a, B, splits, s) : launch_step<128, 16>(a, B, splits, s);
+}
+
+}  // namespace scan
