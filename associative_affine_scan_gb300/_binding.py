@@ -12,6 +12,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 import threading
 from typing import Optional
 
@@ -90,19 +91,13 @@ class DeviceIO(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in ("a", "x", "h0", "dh", "h", "da", "dx", "dh0")]
 
 
-class View4(ctypes.Structure):
-    """scan_view4: a [B, T, H, D] operand and its strides in elements."""
-    _fields_ = [("ptr", ctypes.c_void_p), ("stride_b", ctypes.c_int64),
-                ("stride_t", ctypes.c_int64), ("stride_h", ctypes.c_int64)]
-
-
 _vp = ctypes.c_void_p
 _i64 = ctypes.c_int64
 _i32 = ctypes.c_int32
 _sz = ctypes.c_size_t
 _f32 = ctypes.c_float
 _opt = ctypes.POINTER(ScanOpts)
-_v4 = ctypes.POINTER(View4)
+_v4 = ctypes.c_void_p  # scan_view4*: the bytes of one (see _view4)
 
 _SIGS = {
     "scan_status_string": ([ctypes.c_int], ctypes.c_char_p),
@@ -860,6 +855,13 @@ def scan_copy(src, dst, mode=SCAN_COPY_VEC, *, status=None, stream=None):
 # token mixers: strided [B, T, H, D] operands
 # ---------------------------------------------------------------------------
 
+# A call for one token is as long as its host side, so these helpers do each check
+# once and make no object that the call does not need: pointers and streams go to
+# ctypes as plain integers, a scan_view4 as its bytes.
+
+_pack_view = struct.Struct("Pqqq").pack
+
+
 def _heads(t, name, dtype=None, shape=None, device=None):
     """Checks a [B, T, H, D] (or, for single tokens, [B, H, D]) operand."""
     if not isinstance(t, torch.Tensor):
@@ -890,9 +892,31 @@ def _written(t, name, **want):
 
 def _view4(t):
     s = t.stride()
-    if t.dim() == 3:  # [B, H, D]: one token a request
-        return View4(t.data_ptr(), s[0], 0, s[1])
-    return View4(t.data_ptr(), s[0], s[1], s[2])
+    if len(s) == 3:  # [B, H, D]: one token a request
+        return _pack_view(t.data_ptr(), s[0], 0, s[1])
+    return _pack_view(t.data_ptr(), s[0], s[1], s[2])
+
+
+def _at(t):
+    return None if t is None else t.data_ptr()
+
+
+def _raw_stream(stream, device):
+    if stream is None:
+        return torch.cuda.current_stream(device).cuda_stream
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def _enter(device, name, *args):
+    """_call, without a device switch where `device` is current, and _check."""
+    fn = getattr(_lib_handle or lib(), name)
+    if device.index == torch.cuda.current_device():
+        st = fn(*args)
+    else:
+        with torch.cuda.device(device):
+            st = fn(*args)
+    if st != SCAN_OK:
+        raise ScanError(st, name)
 
 
 def _rank(t, name, n):
@@ -904,7 +928,7 @@ def _rank(t, name, n):
 
 
 def _mixer_workspace(nbytes, dev, s):
-    ws = _mixer_ws.get(max(int(nbytes), 256), dev, s)
+    ws = _mixer_ws.get(max(int(nbytes), 256), dev, ctypes.c_void_p(s))
     return ws.data_ptr(), ws.numel()
 
 
@@ -947,10 +971,9 @@ def qk_norm_rope_fwd(q, k, q_weight, k_weight, cos, sin, positions=None, *, eps=
     else:
         yq = torch.empty(q.shape, dtype=dt, device=dev)
         yk = torch.empty(k.shape, dtype=dt, device=dev)
-    st = _call(dev, "qk_norm_rope_fwd", _view4(q), _view4(k), _ptr(q_weight), _ptr(k_weight),
-               _ptr(cos), _ptr(sin), _ptr(positions), _view4(yq), _view4(yk), B, T, Hq, Hk, D, R, P,
-               int(bool(interleaved)), eps, _dtype_code(q), _stream(stream, dev))
-    _check(st, "qk_norm_rope_fwd")
+    _enter(dev, "qk_norm_rope_fwd", _view4(q), _view4(k), _at(q_weight), _at(k_weight),
+               _at(cos), _at(sin), _at(positions), _view4(yq), _view4(yk), B, T, Hq, Hk, D, R, P,
+               int(bool(interleaved)), eps, _dtype_code(q), _raw_stream(stream, dev))
     return yq, yk
 
 
@@ -972,13 +995,12 @@ def qk_norm_rope_bwd(q, k, q_weight, k_weight, cos, sin, dq_out, dk_out, positio
         dk = torch.empty(k.shape, dtype=dt, device=dev)
         dwq, dwk = (None if w is None else torch.empty(D, dtype=torch.float32, device=dev)
                     for w in (q_weight, k_weight))
-    s = _stream(stream, dev)
+    s = _raw_stream(stream, dev)
     ws, nws = _mixer_workspace(256 + qk_norm_rope_workspace_bytes(D), dev, s)
-    st = _call(dev, "qk_norm_rope_bwd", _view4(q), _view4(k), _ptr(q_weight), _ptr(k_weight),
-               _ptr(cos), _ptr(sin), _ptr(positions), _view4(dq_out), _view4(dk_out), _view4(dq),
-               _view4(dk), _ptr(dwq), _ptr(dwk), B, T, Hq, Hk, D, R, P, int(bool(interleaved)), eps,
+    _enter(dev, "qk_norm_rope_bwd", _view4(q), _view4(k), _at(q_weight), _at(k_weight),
+               _at(cos), _at(sin), _at(positions), _view4(dq_out), _view4(dk_out), _view4(dq),
+               _view4(dk), _at(dwq), _at(dwk), B, T, Hq, Hk, D, R, P, int(bool(interleaved)), eps,
                _dtype_code(q), ws + 256, nws - 256, s)  # past the status word
-    _check(st, "qk_norm_rope_bwd")
     return dq, dk, dwq, dwk
 
 
@@ -1025,12 +1047,11 @@ def linattn_fwd(q, k, v, log_decay, h0=None, cu_seqlens=None, *, scale=None, nee
     else:
         o = torch.empty(v.shape, dtype=dt, device=dev)
         hT = torch.empty(states, dtype=torch.float32, device=dev) if need_state else None
-    s = _stream(stream, dev)
+    s = _raw_stream(stream, dev)
     ws, nws = _mixer_workspace(linattn_workspace_bytes(B, T, H, Dk, Dv, n), dev, s)
-    st = _call(dev, "linattn_fwd", _view4(q), _view4(k), _view4(v), _ptr(log_decay), _ptr(h0),
-               _ptr(cu_seqlens), n, _view4(o), _ptr(hT), B, T, H, Dk, Dv,
+    _enter(dev, "linattn_fwd", _view4(q), _view4(k), _view4(v), _at(log_decay), _at(h0),
+               _at(cu_seqlens), n, _view4(o), _at(hT), B, T, H, Dk, Dv,
                Dk ** -0.5 if scale is None else scale, _dtype_code(q), ws, nws, s)
-    _check(st, "linattn_fwd")
     return o, hT
 
 
@@ -1052,13 +1073,12 @@ def linattn_bwd(q, k, v, log_decay, dout, h0=None, cu_seqlens=None, dhT=None, *,
     else:
         dq, dk, dv = (torch.empty(t.shape, dtype=dt, device=dev) for t in (q, k, v))
         dh0 = torch.empty(states, dtype=torch.float32, device=dev) if need_dh0 else None
-    s = _stream(stream, dev)
+    s = _raw_stream(stream, dev)
     ws, nws = _mixer_workspace(linattn_workspace_bytes(B, T, H, Dk, Dv, n), dev, s)
-    st = _call(dev, "linattn_bwd", _view4(q), _view4(k), _view4(v), _ptr(log_decay), _ptr(h0),
-               _ptr(cu_seqlens), n, _view4(dout), _ptr(dhT), _view4(dq), _view4(dk), _view4(dv),
-               _ptr(dh0), B, T, H, Dk, Dv, Dk ** -0.5 if scale is None else scale, _dtype_code(q),
+    _enter(dev, "linattn_bwd", _view4(q), _view4(k), _view4(v), _at(log_decay), _at(h0),
+               _at(cu_seqlens), n, _view4(dout), _at(dhT), _view4(dq), _view4(dk), _view4(dv),
+               _at(dh0), B, T, H, Dk, Dv, Dk ** -0.5 if scale is None else scale, _dtype_code(q),
                ws, nws, s)
-    _check(st, "linattn_bwd")
     return dq, dk, dv, dh0
 
 
@@ -1082,10 +1102,9 @@ def linattn_step(q, k, v, log_decay, state, slots=None, *, scale=None, out=None,
     o = out if out is not None else torch.empty(v.shape, dtype=dt, device=dev)
     if out is not None:
         _written(o, "out", dtype=dt, shape=v.shape, device=dev)
-    st = _call(dev, "linattn_step", _view4(q), _view4(k), _view4(v), _ptr(log_decay), _ptr(state),
-               _ptr(slots), state.shape[0], _view4(o), B, H, Dk, Dv,
-               Dk ** -0.5 if scale is None else scale, _dtype_code(q), _stream(stream, dev))
-    _check(st, "linattn_step")
+    _enter(dev, "linattn_step", _view4(q), _view4(k), _view4(v), _at(log_decay), _at(state),
+               _at(slots), state.shape[0], _view4(o), B, H, Dk, Dv,
+               Dk ** -0.5 if scale is None else scale, _dtype_code(q), _raw_stream(stream, dev))
     return o
 
 
@@ -1121,13 +1140,12 @@ def window_attn_fwd(q, k, v, window, sinks=0, cu_seqlens=None, *, scale=None, ou
     else:
         o = torch.empty(q.shape, dtype=dt, device=dev)
         lse = torch.empty((B, Hq, Tq), dtype=torch.float32, device=dev)
-    s = _stream(stream, dev)
+    s = _raw_stream(stream, dev)
     ws, nws = _mixer_workspace(
         window_attn_workspace_bytes(B, Tq, Tk, Hq, Hk, D, window, sinks, n), dev, s)
-    st = _call(dev, "window_attn_fwd", _view4(q), _view4(k), _view4(v), _ptr(cu_seqlens), n,
-               _view4(o), _ptr(lse), B, Tq, Tk, Hq, Hk, D, window, sinks,
+    _enter(dev, "window_attn_fwd", _view4(q), _view4(k), _view4(v), _at(cu_seqlens), n,
+               _view4(o), _at(lse), B, Tq, Tk, Hq, Hk, D, window, sinks,
                D ** -0.5 if scale is None else scale, _dtype_code(q), ws, nws, s)
-    _check(st, "window_attn_fwd")
     return o, lse
 
 
@@ -1145,13 +1163,12 @@ def window_attn_bwd(q, k, v, o, lse, dout, window, sinks=0, cu_seqlens=None, *, 
             _written(t, name, dtype=dt, shape=like.shape, device=dev)
     else:
         dq, dk, dv = (torch.empty(t.shape, dtype=dt, device=dev) for t in (q, k, v))
-    s = _stream(stream, dev)
+    s = _raw_stream(stream, dev)
     ws, nws = _mixer_workspace(
         window_attn_workspace_bytes(B, Tq, Tk, Hq, Hk, D, window, sinks, n, True), dev, s)
-    st = _call(dev, "window_attn_bwd", _view4(q), _view4(k), _view4(v), _view4(o), _ptr(lse),
-               _view4(dout), _ptr(cu_seqlens), n, _view4(dq), _view4(dk), _view4(dv), B, Tq, Tk, Hq,
+    _enter(dev, "window_attn_bwd", _view4(q), _view4(k), _view4(v), _view4(o), _at(lse),
+               _view4(dout), _at(cu_seqlens), n, _view4(dq), _view4(dk), _view4(dv), B, Tq, Tk, Hq,
                Hk, D, window, sinks, D ** -0.5 if scale is None else scale, _dtype_code(q), ws, nws, s)
-    _check(st, "window_attn_bwd")
     return dq, dk, dv
 
 
@@ -1179,8 +1196,7 @@ def window_attn_step(q, k, v, k_cache, v_cache, positions, window, sinks=0, slot
     o = out if out is not None else torch.empty(q.shape, dtype=dt, device=dev)
     if out is not None:
         _written(o, "out", dtype=dt, shape=q.shape, device=dev)
-    st = _call(dev, "window_attn_step", _view4(q), _view4(k), _view4(v), _ptr(k_cache), _ptr(v_cache),
-               _ptr(positions), _ptr(slots), k_cache.shape[0], _view4(o), B, Hq, Hk, D, window, sinks,
-               D ** -0.5 if scale is None else scale, _dtype_code(q), _stream(stream, dev))
-    _check(st, "window_attn_step")
+    _enter(dev, "window_attn_step", _view4(q), _view4(k), _view4(v), _at(k_cache), _at(v_cache),
+               _at(positions), _at(slots), k_cache.shape[0], _view4(o), B, Hq, Hk, D, window, sinks,
+               D ** -0.5 if scale is None else scale, _dtype_code(q), _raw_stream(stream, dev))
     return o

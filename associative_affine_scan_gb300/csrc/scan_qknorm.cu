@@ -15,18 +15,37 @@
 // elements are four pairs (elements 4u.. and R/2 + 4u.., or 8u.. where
 // neighbours are paired), so the rotation needs no exchange. A group of lanes
 // takes up to four heads of one token (two in the backward): the token's cosines
-// and sines are read once for them. Blocks walk the tokens of either the queries
-// or the keys, so that a lane keeps its weights (and sums of weight gradients) in
-// registers, and read the next heads, their table entries and the position after
-// that while they work on the current ones.
+// and sines are read once for them. A block has either queries or keys; the
+// backward's walk over the tokens, with their weight's gradient in registers. What
+// hides the latency of DRAM is the number of warps: rows stay in their own type
+// until they are used, to keep registers for four (backward three) blocks an SM.
 #include "scan_mixer.h"
 
 namespace scan {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kFwdHeads = 4;  // heads of one token that a group of lanes takes
-constexpr int kBwdHeads = 2;
+// Heads of one token that a group of lanes takes: 64 bytes of each operand a lane
+// forward, 32 backward.
+template <typename T>
+constexpr int kFwdHeads = sizeof(T) == 2 ? 4 : 2;
+template <typename T>
+constexpr int kBwdHeads = sizeof(T) == 2 ? 2 : 1;
+
+// Division of numbers below 2^31 by a fixed divisor: one high product, one add and
+// one shift (Granlund and Montgomery, "Division by invariant integers using
+// multiplication").
+struct Divisor {
+  uint32_t d, mul;
+  int shift;
+  void set(int64_t by) {
+    d = (uint32_t)by;
+    shift = 0;
+    while ((1LL << shift) < by) ++shift;
+    mul = (uint32_t)((((1ULL << shift) - (uint64_t)by) << 32) / (uint64_t)by + 1);
+  }
+  __device__ __forceinline__ uint32_t operator()(uint32_t n) const { return (__umulhi(mul, n) + n) >> shift; }
+};
 
 struct QkArgs {
   scan_view4 x[2], y[2], dy[2], dx[2];  // queries, keys
@@ -39,7 +58,10 @@ struct QkArgs {
   int64_t BT, T, P;
   int H[2];
   int chunks[2];  // groups of heads
-  int blocks[2];  // blocks that walk the queries, and the keys
+  int blocks[2];  // blocks of the queries, and of the keys
+  int narrow;     // items fit 31 bits
+  Divisor by_chunks[2], by_T;
+  float inv_D;
   int D, R;
   int pairs;
   float eps;
@@ -150,9 +172,12 @@ __device__ __forceinline__ void load_turn(const QkArgs& a, int64_t p, const Unit
   const int64_t at = (ok ? p : 0) * (a.R / 2) + u.cs;
   const float4 cv = *reinterpret_cast<const float4*>(a.cs + at);
   const float4 sv = *reinterpret_cast<const float4*>(a.sn + at);
-  const float bad = __int_as_float(0x7fc00000);
-  c[0] = ok ? cv.x : bad; c[1] = ok ? cv.y : bad; c[2] = ok ? cv.z : bad; c[3] = ok ? cv.w : bad;
-  s[0] = ok ? sv.x : bad; s[1] = ok ? sv.y : bad; s[2] = ok ? sv.z : bad; s[3] = ok ? sv.w : bad;
+  c[0] = cv.x; c[1] = cv.y; c[2] = cv.z; c[3] = cv.w;
+  s[0] = sv.x; s[1] = sv.y; s[2] = sv.z; s[3] = sv.w;
+  if (!ok) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) c[i] = s[i] = __int_as_float(0x7fc00000);
+  }
 }
 
 __device__ __forceinline__ void load_weight(const float* w, const Unit& u, float (&v)[8]) {
@@ -166,45 +191,38 @@ __device__ __forceinline__ void load_weight(const float* w, const Unit& u, float
   }
 }
 
-// A group's place in its walk over (token, heads): items `step` apart.
-struct Walk {
-  int64_t item, b, t;
-  int c;
-  int64_t step, db, dt;
-  int dc;
-  __device__ __forceinline__ Walk(const QkArgs& a, int m, int64_t first, int64_t by) {
-    const int per = a.chunks[m];
-    item = first;
-    step = by;
-    c = (int)(first % per);
-    const int64_t tok = first / per;
-    b = tok / a.T;
-    t = tok % a.T;
-    dc = (int)(by % per);
-    const int64_t dtok = by / per;
-    db = dtok / a.T;
-    dt = dtok % a.T;
-  }
-  __device__ __forceinline__ void next(const QkArgs& a, int m) {
-    item += step;
-    b += db;
-    t += dt;
-    c += dc;
-    if (c >= a.chunks[m]) c -= a.chunks[m], ++t;
-    if (t >= a.T) t -= a.T, ++b;
-  }
-  __device__ __forceinline__ int64_t position(const QkArgs& a) const {
-    return a.pos ? (int64_t)a.pos[b * a.T + t] : t;
-  }
+// What an item (one token, N heads of the queries or the keys) is.
+struct Item {
+  int64_t tok, b, t;
+  int h;
 };
+template <int N>
+__device__ __forceinline__ Item item_at(const QkArgs& a, int m, int64_t i) {
+  Item r;
+  const int per = a.chunks[m];
+  if (a.narrow) {
+    const uint32_t tok = (m ? a.by_chunks[1] : a.by_chunks[0])((uint32_t)i), b = a.by_T(tok);
+    r.tok = tok;
+    r.h = (int)((uint32_t)i - tok * per) * N;
+    r.b = b;
+    r.t = tok - b * (uint32_t)a.T;
+  } else {
+    r.tok = i / per;
+    r.h = (int)(i - r.tok * per) * N;
+    r.b = r.tok / a.T;
+    r.t = r.tok - r.b * a.T;
+  }
+  return r;
+}
 
 template <typename T, int N>
-__device__ __forceinline__ void load_heads(const View<const T>& x, const Walk& w, const Unit& u, int H, bool live,
+__device__ __forceinline__ void load_heads(const View<const T>& x, const Item& w, const Unit& u, int H, bool live,
                                            Raw<T> (&r)[N]) {
+  const T* p = x.row(w.b, w.t, w.h);
 #pragma unroll
   for (int i = 0; i < N; ++i) {
-    if (live && u.on && w.c * N + i < H) r[i].load(x.row(w.b, w.t, w.c * N + i), u.lo, u.hi);
-    else r[i].clear();
+    r[i].clear();
+    if (live && u.on && w.h + i < H) r[i].load(p + i * x.sh, u.lo, u.hi);
   }
 }
 
@@ -214,123 +232,105 @@ __device__ __forceinline__ View<T> qk_view(const scan_view4& v) {
 }
 
 template <typename T, int G, bool PAIRS>
-__global__ void __launch_bounds__(kThreads) qknorm_fwd_kernel(const QkArgs a) {
-  constexpr int N = kFwdHeads;
+__global__ void __launch_bounds__(kThreads, 4) qknorm_fwd_kernel(const QkArgs a) {
+  constexpr int N = kFwdHeads<T>;
   const int m = blockIdx.x >= a.blocks[0];
   const int64_t block = m ? blockIdx.x - a.blocks[0] : blockIdx.x;
-  const int64_t items = a.BT * a.chunks[m];
+  const int64_t i0 = block * (kThreads / G) + threadIdx.x / G;
+  const bool live = i0 < a.BT * a.chunks[m];  // lanes of a dead group stay for the shuffles
+  const Item w = item_at<N>(a, m, live ? i0 : 0);
   const Unit u = unit_of(threadIdx.x % G, a);
-  const View<const T> x = m ? qk_view<const T>(a.x[1]) : qk_view<const T>(a.x[0]);
-  const View<T> y = m ? qk_view<T>(a.y[1]) : qk_view<T>(a.y[0]);
   const int H = a.H[m];
-  Walk w(a, m, block * (kThreads / G) + threadIdx.x / G, (int64_t)a.blocks[m] * (kThreads / G));
-  Walk ahead = w;
-  float wt[8], cs[4] = {1.f, 1.f, 1.f, 1.f}, sn[4] = {0.f, 0.f, 0.f, 0.f};
+  const int64_t p = a.pos ? (int64_t)a.pos[w.tok] : w.t;
   Raw<T> r[N];
-  load_heads<T, N>(x, w, u, H, w.item < items, r);
-  if (w.item < items) load_turn(a, w.position(a), u, cs, sn);
+  load_heads<T, N>(m ? qk_view<const T>(a.x[1]) : qk_view<const T>(a.x[0]), w, u, H, live, r);
+  float wt[8], cs[4] = {1.f, 1.f, 1.f, 1.f}, sn[4] = {0.f, 0.f, 0.f, 0.f};
   load_weight(a.w[m], u, wt);
-  ahead.next(a, m);
-  int64_t p1 = ahead.item < items ? ahead.position(a) : 0;
-  // whole warps leave together: the bound is on the warp's first group
-  int64_t lead = w.item - (threadIdx.x % 32) / G;
-  while (lead < items) {
-    const bool more = ahead.item < items;
-    Raw<T> r1[N];
-    float cs1[4] = {1.f, 1.f, 1.f, 1.f}, sn1[4] = {0.f, 0.f, 0.f, 0.f};
-    load_heads<T, N>(x, ahead, u, H, more, r1);
-    if (more) load_turn(a, p1, u, cs1, sn1);
-    const Walk now = w;
-    w = ahead;
-    ahead.next(a, m);
-    if (ahead.item < items) p1 = ahead.position(a);
+  load_turn(a, p, u, cs, sn);
+  const View<T> y = m ? qk_view<T>(a.y[1]) : qk_view<T>(a.y[0]);
+  T* out = y.row(w.b, w.t, w.h);
+  float rs[N];
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      float v[8], sq = 0.f;
-      r[i].get(v);
+  for (int i = 0; i < N; ++i) {
+    float v[8];
+    r[i].get(v);
+    rs[i] = 0.f;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) sq = fmaf(v[j], v[j], sq);
-      const float rs = rsqrtf(group_sum<G>(sq) / (float)a.D + a.eps);
+    for (int j = 0; j < 8; ++j) rs[i] = fmaf(v[j], v[j], rs[i]);
+  }
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] *= rs * wt[j];
-      if (u.rot) rotate(v, cs, sn, PAIRS);
-      if (now.item < items && u.on && now.c * N + i < H)
-        store8<T>(y.row(now.b, now.t, now.c * N + i), u.lo, u.hi, v);
-      r[i] = r1[i];
-    }
+  for (int i = 0; i < N; ++i) rs[i] = rsqrtf(fmaf(group_sum<G>(rs[i]), a.inv_D, a.eps));
 #pragma unroll
-    for (int i = 0; i < 4; ++i) cs[i] = cs1[i], sn[i] = sn1[i];
-    lead += w.step;
+  for (int i = 0; i < N; ++i) {
+    float v[8];
+    r[i].get(v);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] *= rs[i] * wt[j];
+    if (u.rot) rotate(v, cs, sn, PAIRS);
+    if (live && u.on && w.h + i < H) store8<T>(out + i * y.sh, u.lo, u.hi, v);
   }
 }
 
-// Each block leaves one partial sum of its weight's gradient; the partial sums are
-// added in block order by the kernel below, so the result does not depend on the
-// order in which blocks finish.
+// Each block walks tokens with its weight's gradient in registers and leaves one
+// partial sum; the partial sums are added in block order by the kernel below, so
+// the result does not depend on the order in which blocks finish.
 template <typename T, int G, bool PAIRS>
-__global__ void __launch_bounds__(kThreads) qknorm_bwd_kernel(const QkArgs a) {
-  constexpr int N = kBwdHeads, NG = kThreads / G;
+__global__ void __launch_bounds__(kThreads, 3) qknorm_bwd_kernel(const QkArgs a) {
+  constexpr int N = kBwdHeads<T>, NG = kThreads / G;
   const int m = blockIdx.x >= a.blocks[0];
   const int64_t block = m ? blockIdx.x - a.blocks[0] : blockIdx.x;
-  const int64_t items = a.BT * a.chunks[m];
+  const int64_t items = a.BT * a.chunks[m], step = (int64_t)a.blocks[m] * NG;
   const Unit u = unit_of(threadIdx.x % G, a);
   const View<const T> x = m ? qk_view<const T>(a.x[1]) : qk_view<const T>(a.x[0]);
   const View<const T> dy = m ? qk_view<const T>(a.dy[1]) : qk_view<const T>(a.dy[0]);
   const View<T> dx = m ? qk_view<T>(a.dx[1]) : qk_view<T>(a.dx[0]);
   const int H = a.H[m];
-  Walk w(a, m, block * NG + threadIdx.x / G, (int64_t)a.blocks[m] * NG);
-  Walk ahead = w;
-  float wt[8], dw[8], cs[4] = {1.f, 1.f, 1.f, 1.f}, sn[4] = {0.f, 0.f, 0.f, 0.f};
+  float wt[8], dw[8];
 #pragma unroll
   for (int j = 0; j < 8; ++j) dw[j] = 0.f;
-  Raw<T> r[N], g[N];
-  load_heads<T, N>(x, w, u, H, w.item < items, r);
-  load_heads<T, N>(dy, w, u, H, w.item < items, g);
-  if (w.item < items) load_turn(a, w.position(a), u, cs, sn);
   load_weight(a.w[m], u, wt);
-  ahead.next(a, m);
-  int64_t p1 = ahead.item < items ? ahead.position(a) : 0;
-  int64_t lead = w.item - (threadIdx.x % 32) / G;
-  while (lead < items) {
-    const bool more = ahead.item < items;
-    Raw<T> r1[N], g1[N];
-    float cs1[4] = {1.f, 1.f, 1.f, 1.f}, sn1[4] = {0.f, 0.f, 0.f, 0.f};
-    load_heads<T, N>(x, ahead, u, H, more, r1);
-    load_heads<T, N>(dy, ahead, u, H, more, g1);
-    if (more) load_turn(a, p1, u, cs1, sn1);
-    const Walk now = w;
-    w = ahead;
-    ahead.next(a, m);
-    if (ahead.item < items) p1 = ahead.position(a);
+  // whole warps leave together: the bound is on the warp's first group
+  int64_t lead = block * NG + (threadIdx.x / 32) * (32 / G), i0 = lead + (threadIdx.x % 32) / G;
+  Item w = item_at<N>(a, m, i0 < items ? i0 : 0);
+  int64_t p = a.pos ? (int64_t)a.pos[w.tok] : w.t;
+  for (; lead < items; lead += step) {
+    const bool live = i0 < items;
+    Raw<T> r[N], g[N];
+    load_heads<T, N>(x, w, u, H, live, r);
+    load_heads<T, N>(dy, w, u, H, live, g);
+    float cs[4] = {1.f, 1.f, 1.f, 1.f}, sn[4] = {0.f, 0.f, 0.f, 0.f};
+    load_turn(a, p, u, cs, sn);
 #pragma unroll
     for (int i = 0; i < 4; ++i) sn[i] = -sn[i];
+    T* out = dx.row(w.b, w.t, w.h);
+    const int h = w.h;
+    i0 += step;  // the next position now: its table entries depend on it
+    w = item_at<N>(a, m, i0 < items ? i0 : 0);
+    p = a.pos ? (int64_t)a.pos[w.tok] : w.t;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      const bool here = now.item < items && u.on && now.c * N + i < H;
+      const bool here = live && u.on && h + i < H;
       float v[8], d[8], sq = 0.f, gn = 0.f;
       r[i].get(v);
       g[i].get(d);
       if (u.rot) rotate(d, cs, sn, PAIRS);
+      // (rows that are not there are zeros, and add nothing)
+      float e[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
+        e[j] = d[j] * wt[j];
         sq = fmaf(v[j], v[j], sq);
-        gn = fmaf(d[j] * wt[j], v[j], gn);
+        gn = fmaf(e[j], v[j], gn);
       }
-      const float rs = rsqrtf(group_sum<G>(sq) / (float)a.D + a.eps);
-      const float mean = group_sum<G>(gn) * rs / (float)a.D;  // mean(g n)
+      const float rs = rsqrtf(fmaf(group_sum<G>(sq), a.inv_D, a.eps));
+      const float back = -(group_sum<G>(gn) * a.inv_D) * rs * rs * rs;  // -r^2 mean(g n) of each x
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const float n = v[j] * rs;
-        dw[j] += here ? d[j] * n : 0.f;
-        v[j] = rs * (d[j] * wt[j] - n * mean);
+        dw[j] = fmaf(d[j] * rs, v[j], dw[j]);
+        v[j] = fmaf(v[j], back, e[j] * rs);
       }
-      if (here) store8<T>(dx.row(now.b, now.t, now.c * N + i), u.lo, u.hi, v);
-      r[i] = r1[i];
-      g[i] = g1[i];
+      if (here) store8<T>(out + i * dx.sh, u.lo, u.hi, v);
     }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) cs[i] = cs1[i], sn[i] = sn1[i];
-    lead += w.step;
   }
   // groups of the block, in order
   __shared__ float red[kThreads * 8];
@@ -367,16 +367,21 @@ __global__ void __launch_bounds__(1024) qknorm_dw_kernel(const QkArgs a) {
   }
 }
 
-// Blocks of a walk: as many as stay resident (four or five an SM), shared between
-// queries and keys by their numbers of items; a block more where one side has few.
-constexpr int kFwdBlocks = 152 * 5, kBwdBlocks = 152 * 4;
+// Blocks of the backward's walk: what stays resident, shared between queries and
+// keys by their numbers of items.
+constexpr int kBwdBlocks = 152 * 3;
 
-void share_blocks(QkArgs* a, int groups, int most) {
+void share_blocks(QkArgs* a, int groups, bool fwd) {
   const int64_t items[2] = {a->BT * a->chunks[0], a->BT * a->chunks[1]};
   for (int m = 0; m < 2; ++m) {
     const int64_t need = (items[m] + groups - 1) / groups;
-    const int64_t part = most * items[m] / (items[0] + items[1]);
-    a->blocks[m] = (int)(need < part ? need : part > 0 ? part : need > 0 ? 1 : 0);
+    const int64_t part = kBwdBlocks * items[m] / (items[0] + items[1]);
+    a->blocks[m] = (int)(fwd || need < part ? need : part > 0 ? part : need > 0 ? 1 : 0);
+  }
+  a->narrow = items[0] < (1LL << 31) && items[1] < (1LL << 31) && a->T < (1LL << 31);
+  if (a->narrow) {
+    for (int m = 0; m < 2; ++m) a->by_chunks[m].set(a->chunks[m] > 0 ? a->chunks[m] : 1);
+    a->by_T.set(a->T);
   }
 }
 
@@ -384,9 +389,9 @@ int group_lanes(int D) { return D <= 64 ? 8 : D <= 128 ? 16 : 32; }
 
 template <typename T, int G>
 cudaError_t qk_launch_g(QkArgs a, bool fwd, cudaStream_t s) {
-  const int heads = fwd ? kFwdHeads : kBwdHeads;
+  const int heads = fwd ? kFwdHeads<T> : kBwdHeads<T>;
   for (int m = 0; m < 2; ++m) a.chunks[m] = (a.H[m] + heads - 1) / heads;
-  share_blocks(&a, kThreads / G, fwd ? kFwdBlocks : kBwdBlocks);
+  share_blocks(&a, kThreads / G, fwd);
   const int blocks = a.blocks[0] + a.blocks[1];
   if (fwd) {
     if (a.pairs) qknorm_fwd_kernel<T, G, true><<<blocks, kThreads, 0, s>>>(a);
@@ -427,7 +432,8 @@ scan_status qk_args(QkArgs* a, const scan_view4* q, const scan_view4* k, const f
   if (D % 8 || D > 256 || R % 8) return SCAN_ERR_UNSUPPORTED;
   if (Hq > (1 << 20) || Hk > (1 << 20)) return SCAN_ERR_UNSUPPORTED;
   if (B > (1LL << 31) || T > (1LL << 31) || B * T > (1LL << 40)) return SCAN_ERR_UNSUPPORTED;
-  if (R > 0 && B * T > 0 && (!cs || !sn)) return SCAN_ERR_INVALID_ARG;
+  if (B * T * ((Hq + 1) / 2 + (Hk + 1) / 2) / 8 >= 0x7fffffffLL) return SCAN_ERR_UNSUPPORTED;  // grid.x
+  if (R > 0 && B * T > 0 && (!cs || !sn || P < 1)) return SCAN_ERR_INVALID_ARG;
   if ((uintptr_t)cs % 16 || (uintptr_t)sn % 16 || (uintptr_t)qw % 16 || (uintptr_t)kw % 16)
     return SCAN_ERR_ALIGNMENT;
   const bool some = B * T > 0;  // an empty tensor may have no address
@@ -449,6 +455,7 @@ scan_status qk_args(QkArgs* a, const scan_view4* q, const scan_view4* k, const f
   a->R = (int)R;
   a->pairs = interleaved != 0;
   a->eps = eps;
+  a->inv_D = 1.f / (float)D;
   for (int m = 0; m < 2; ++m)
     if (a->H[m] && !view_aligned(&a->x[m], dt)) return SCAN_ERR_ALIGNMENT;
   return SCAN_OK;

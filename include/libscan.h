@@ -527,7 +527,7 @@ typedef struct scan_view4 {
  * SCAN_ERR_UNSUPPORTED unless D % 8 == 0, D <= 256 and R % 8 == 0;
  * SCAN_ERR_ALIGNMENT unless every pointer is 16-byte aligned and every stride
  * a multiple of 16 bytes; SCAN_ERR_INVALID_ARG for negative sizes, R > D,
- * a negative or NaN eps or a missing pointer. */
+ * a negative or NaN eps, an empty table with R > 0 or a missing pointer. */
 scan_status qk_norm_rope_fwd(const scan_view4* q, const scan_view4* k, const float* q_weight,
                              const float* k_weight, const float* cos_table, const float* sin_table,
                              const int32_t* positions, const scan_view4* q_out,
