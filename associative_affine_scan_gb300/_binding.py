@@ -901,8 +901,14 @@ def _at(t):
     return None if t is None else t.data_ptr()
 
 
+# the current stream's handle without a Stream object around it, where torch has it
+_current_raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _raw_stream(stream, device):
     if stream is None:
+        if _current_raw is not None:
+            return _current_raw(device.index)
         return torch.cuda.current_stream(device).cuda_stream
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 

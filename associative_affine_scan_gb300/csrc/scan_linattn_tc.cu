@@ -41,12 +41,12 @@ constexpr int kThreads = 18 * 32;  // four roles of four warps, a copy and a pro
 constexpr uint32_t kHalf = kChunk * kPitch;  // bytes of one panel of a chunk
 
 struct TcPass {
-  CUtensorMap x1, x2, x3, out;
-  __nv_bfloat16* o;  // the output, for rows that a tensor copy must not write
+  CUtensorMap x1, x2, x3;
+  __nv_bfloat16* o;
   int64_t o_sb, o_st, o_sh;
   const float* s_in;
   float* s_out;
-  float* seg;  // states after segments: [sequences][H][nseg - 1][K][V]
+  float* seg;  // states after pieces of segments: [sequences][H][nseg - 1][pieces][K][V]
   float s_in_mul, s_out_mul;
   int s_in_t, K, V, reverse;
 };
@@ -57,7 +57,8 @@ struct TcArgs {
   const int32_t* cu;
   WsHeader* hdr;
   int64_t T;
-  int npass, n_seqs, H, nseg, cps;  // segments of a row, chunks of a segment
+  int npass, n_seqs, H;
+  int nseg, cps, pieces;  // segments of a row, chunks of one, pieces in which its own state is found
   float scale;
 };
 
@@ -65,7 +66,7 @@ template <int KP, int VP, bool STATE_ONLY>
 struct Plan {
   static constexpr int kX1 = STATE_ONLY ? 0 : kChunk * 2 * KP;
   static constexpr int kX2 = kChunk * 2 * KP;
-  static constexpr int kX3 = kChunk * 2 * VP;  // also stages the output
+  static constexpr int kX3 = kChunk * 2 * VP;
   static constexpr int kStage = kX1 + kX2 + kX3;
   static constexpr int kState = STATE_ONLY ? 0 : VP * KP * 2;
   static constexpr int kTables = 2048;  // barriers, decay tables
@@ -109,16 +110,18 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_co
   float* const ctab = tab + 256;     // [32] column powers of the weights within a chunk
   const uint32_t bars = smem_addr(tab + 288);
   const uint32_t bFull12 = bars, bFull3 = bars + 32, bFree12 = bars + 64, bFree3 = bars + 96, bS1 = bars + 128,
-                 bP = bars + 136, bSb = bars + 144, bSt = bars + 152, bX = bars + 160, bXf = bars + 176,
-                 bOi = bars + 192, bOs = bars + 200, bOf = bars + 208, bOx = bars + 216, bClean = bars + 224,
-                 bOut = bars + 232, bInit = bars + 240;
-  uint32_t* const tmem_ptr = reinterpret_cast<uint32_t*>(tab + 288) + 64;
+                 bP = bars + 136, bSb = bars + 144, bSt = bars + 152, bX = bars + 160, bXf = bars + 192,
+                 bOi = bars + 224, bOs = bars + 232, bOf = bars + 240, bOx = bars + 248, bClean = bars + 256,
+                 bInit = bars + 264;
+  constexpr int kBufs = STATE_ONLY ? 4 : 2;  // of 32 steps of the update's operand
+  uint32_t* const tmem_ptr = reinterpret_cast<uint32_t*>(tab + 288) + 72;
   uint32_t* const stop_flag = tmem_ptr + 1;
 
   // which (sequence, head, segment)
-  const int segs = STATE_ONLY ? a.nseg - 1 : a.nseg;
-  const int seg = item % segs;
-  const int64_t row = item / segs;
+  const int parts = STATE_ONLY ? (a.nseg - 1) * a.pieces : a.nseg;
+  const int part = item % parts;
+  const int64_t row = item / parts;
+  const int seg = STATE_ONLY ? part / a.pieces : part;
   const int h = (int)(row % a.H);
   const int64_t sq = row / a.H;
   Span s{0, a.T, 0, 0};
@@ -130,14 +133,18 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_co
   }
   const int b = a.cu ? 0 : (int)sq;
   const int64_t all = (s.len + kChunk - 1) / kChunk;
-  if (a.nseg == 1) {
+  if (STATE_ONLY) {
+    const int i = part % a.pieces, c0 = a.cps * i / a.pieces;
+    s.first = (int64_t)seg * a.cps + c0;
+    s.nch = a.cps * (i + 1) / a.pieces - c0;
+  } else if (a.nseg == 1) {
     s.nch = (int)all;
   } else {
     s.first = (int64_t)seg * a.cps;
     s.nch = (int)(all - s.first < a.cps ? all - s.first : a.cps);
   }
   const bool rev = p.reverse != 0;
-  // steps of the segment: chunks are whole but the one that ends the sequence
+  // steps of this part: chunks are whole but the one that ends the sequence
   const int64_t steps = s.nch * (int64_t)kChunk -
                         ((rev ? s.first == 0 : s.first + s.nch == all) ? all * kChunk - s.len : 0);
   const int e = rev ? 0 : 1;
@@ -148,7 +155,7 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_co
   const float* s0 = nullptr;
   int s0k = 0, s0v = 0;  // its strides
   float s0m = 1.f;
-  if (seg == 0) {
+  if (s.first == 0) {
     if (p.s_in) {
       s0 = p.s_in + row * p.K * p.V;
       s0k = p.s_in_t ? 1 : p.V;
@@ -156,7 +163,7 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_co
       s0m = p.s_in_mul;
     }
   } else if (!STATE_ONLY) {
-    s0 = p.seg + (row * (a.nseg - 1) + seg - 1) * p.K * p.V;
+    s0 = p.seg + (row * (a.nseg - 1) + seg) * a.pieces * p.K * p.V - p.K * p.V;
     s0k = p.V;
     s0v = 1;
   }
@@ -164,7 +171,7 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_co
   float* s1 = nullptr;
   float s1m = 1.f;
   if (STATE_ONLY) {
-    s1 = p.seg + (row * (a.nseg - 1) + seg) * p.K * p.V;
+    s1 = p.seg + (row * (a.nseg - 1) * a.pieces + part) * p.K * p.V;
   } else if (seg == a.nseg - 1 && p.s_out) {
     s1 = p.s_out + row * p.K * p.V;
     s1m = p.s_out_mul;
@@ -186,7 +193,7 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_co
       bar_init(bFree12 + 8 * i, 1);
       bar_init(bFree3 + 8 * i, 1);
     }
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < kBufs; ++i) {
       bar_init(bX + 8 * i, 4);
       bar_init(bXf + 8 * i, 1);
     }
@@ -199,7 +206,6 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_co
     bar_init(bOf, 1);
     bar_init(bOx, 4);
     bar_init(bClean, 4);
-    bar_init(bOut, 4);
     bar_init(bInit, 4 * (KP / 32));
     bar_init_fence();
   }
@@ -209,7 +215,7 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_co
   fence_after();
   const uint32_t tm = *tmem_ptr;
   // tensor memory: S1, P, two 32-step pieces of the update's operand (hi, lo), O, S^T
-  const uint32_t tS1 = tm, tP = tm + 128, tX = tm + 192, tO = tm + 256, tSt = tm + 384;
+  const uint32_t tS1 = tm, tP = tm + 128, tX = STATE_ONLY ? tm : tm + 192, tO = tm + 256, tSt = tm + 384;
   const uint32_t lanes = (uint32_t)(warp % 4) << 21;  // this warp's first tensor-memory lane
   const Stop stop{stop_flag, a.hdr};
   const int role = warp / 4;
@@ -295,8 +301,8 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_co
                (!packed || n == kChunk || bar_wait(bClean, 0, stop));
       };
       const auto scores = [&](int c) {
-        const uint32_t x1 = base + (c % P::kStages) * P::kStage;
-        mma_kk<KP>(tS1, x1, kHalf, x1 + P::kX1, kHalf, dS1, false);
+        const uint32_t x1 = kmajor(base) + (c % P::kStages) * (P::kStage >> 4);
+        mma_kk<KP, kHalf, kHalf>(tS1, x1, x1 + (P::kX1 >> 4), dS1, false);
         mma_commit(bS1);
       };
       bool ok = s.nch > 0;
@@ -304,7 +310,8 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_co
 #pragma unroll 1
       for (int c = 0; ok && c < s.nch; ++c) {
         const int st = c % P::kStages;
-        const uint32_t x1 = base + st * P::kStage, x2 = x1 + P::kX1, x3 = x2 + P::kX2;
+        const uint32_t x1 = kmajor(base) + st * (P::kStage >> 4);
+        const uint32_t x2 = mnmajor(base + P::kX1, kHalf) + st * (P::kStage >> 4), x3 = x2 + (P::kX2 >> 4);
         const bool have = c > 0 || (s0 && !STATE_ONLY);
         if (STATE_ONLY) ok = ready(c);
         else if (c > 0) ok = bar_wait(bSb, (c - 1) & 1, stop);
@@ -312,13 +319,13 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_co
         if (!ok) break;
         fence_after();
         if (c + 1 < s.nch || s1) {
-#pragma unroll 1
+#pragma unroll
           for (int jb = 0; jb < 4; ++jb) {
-            const int buf = jb & 1;
-            if (!(ok = bar_wait(bX + 8 * buf, jb >> 1, stop))) break;
+            const int buf = jb % kBufs;
+            if (!(ok = bar_wait(bX + 8 * buf, (STATE_ONLY ? c : jb >> 1) & 1, stop))) break;
             fence_after();
-            mma_tn<32>(tSt, tX + 32 * buf, x2 + 32 * jb * kPitch, kHalf, dSt, have || jb > 0);
-            mma_tn<32>(tSt, tX + 32 * buf + 16, x2 + 32 * jb * kPitch, kHalf, dSt, true);
+            mma_tn<32>(tSt, tX + 32 * buf, x2 + jb * (32 * kPitch >> 4), dSt, have || jb > 0);
+            mma_tn<32>(tSt, tX + 32 * buf + 16, x2 + jb * (32 * kPitch >> 4), dSt, true);
             mma_commit(bXf + 8 * buf);
           }
           if (!ok) break;
@@ -332,7 +339,7 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_co
         if (c > 0 && !(ok = bar_wait(bOx, (c - 1) & 1, stop))) break;
         fence_after();
         if (have) {
-          mma_kk<KP>(tO, x1, kHalf, sState, VP * kPitch, dOi, false);
+          mma_kk<KP, kHalf, VP * kPitch>(tO, x1, kmajor(sState), dOi, false);
           mma_commit(bOi);
         }
         mma_commit(bSt);
@@ -346,8 +353,9 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_co
         if (have && !(ok = bar_wait(bOs, (c - late) & 1, stop))) break;
         if (!(ok = bar_wait(bFull3 + 8 * st, (c / P::kStages) & 1, stop))) break;
         fence_after();
-        mma_tn<kChunk>(tO, tP, x3, kHalf, dO, have);
+        mma_tn<kChunk>(tO, tP, x3, dO, have);
         mma_commit(bOf);
+        mma_commit(bFree3 + 8 * st);
       }
     }
   } else if (role == 0 && !STATE_ONLY) {
@@ -404,11 +412,10 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_co
       __syncwarp();
       if (lane == 0) bar_arrive(bP);
     }
-  } else if (role == 1) {
+  } else if (role == 1 && !STATE_ONLY) {
     // ---- state: column v of S (a row of S^T) in lane v
-    const int v = tid - 128;
 #pragma unroll 1
-    for (int c = 1; !STATE_ONLY && c < s.nch; ++c) {
+    for (int c = 1; c < s.nch; ++c) {
       int64_t t0;
       int n;
       chunk_at(s, rev, c, &t0, &n);
@@ -428,45 +435,16 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_co
       __syncwarp();
       if (lane == 0) bar_arrive(bSb);
     }
-    if (s1) {
-      bool ok = true;
-      if (s.nch > 0) {
-        ok = warp_wait(bSt, STATE_ONLY ? 0 : (s.nch - 1) & 1, stop);
-        fence_after();
-      }
-      if (ok) {
-        // a segment on its own starts from nothing: what came in is added here
-        const float in = STATE_ONLY ? s0m * exp2f(l2 * (float)steps) : s0m;
-        const bool add = s0 && (STATE_ONLY || s.nch == 0);
-#pragma unroll 1
-        for (int kb = 0; kb < KP / 32; ++kb) {
-          uint32_t r[32];
-          if (s.nch > 0) {
-            tmem_ld32(tSt + lanes + 32 * kb, r);
-            ld_wait();
-          }
-#pragma unroll
-          for (int x = 0; x < 32; ++x) {
-            const int k = 32 * kb + x;
-            if (v < p.V && k < p.K) {
-              float f = s.nch > 0 ? __uint_as_float(r[x]) : 0.f;
-              if (add) f = fmaf(in, s0[k * s0k + v * s0v], f);
-              s1[(int64_t)k * p.V + v] = s1m * f;
-            }
-          }
-        }
-      }
-    }
-  } else if (role == 2 || (role == 0 && STATE_ONLY)) {
+  } else if (role == 2 || (STATE_ONLY && role < 4)) {
     // ---- update: column v of x3 in lane v, weighted and split in two, 32 steps at a
-    // time (by two roles where only the state is wanted)
+    // time (by all four roles, each a quarter, where only the state is wanted)
     const int v = tid % 128;
     if (v >= VP) {  // lanes past V: zeros, once
       uint32_t z[32];
 #pragma unroll
       for (int x = 0; x < 32; ++x) z[x] = 0;
 #pragma unroll
-      for (int x = 0; x < 2; ++x) tmem_st32(tX + lanes + 32 * x, z);
+      for (int x = 0; x < kBufs; ++x) tmem_st32(tX + lanes + 32 * x, z);
       st_wait();
     }
     bool ok = true;
@@ -499,7 +477,7 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_co
       // a segment on its own: weights to its end, the sums never rescaled
       const float far = STATE_ONLY ? exp2f(l2 * (float)((s.nch - 1 - c) * kChunk)) : 1.f;
 #pragma unroll 1
-      for (int jb = STATE_ONLY && role == 0; jb < 4; jb += STATE_ONLY ? 2 : 1) {
+      for (int jb = STATE_ONLY ? role : 0; jb < 4; jb += STATE_ONLY ? 4 : 1) {
         uint32_t hi[16], lo[16];
         if (v < VP) {
 #pragma unroll
@@ -523,7 +501,7 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_co
             }
           }
         }
-        const int buf = jb & 1, use = 2 * c + (jb >> 1);  // the buffer's use-th time
+        const int buf = jb % kBufs, use = STATE_ONLY ? c : 2 * c + (jb >> 1);  // the buffer's use-th time
         if (use > 0 && !(ok = warp_wait(bXf + 8 * buf, (use - 1) & 1, stop))) break;
         fence_after();
         if (v < VP) {
@@ -541,8 +519,6 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_co
     const int i = tid - 384;
 #pragma unroll 1
     for (int c = 0; c < s.nch; ++c) {
-      const int st = c % P::kStages;
-      const uint32_t so = base + st * P::kStage + P::kX1 + P::kX2;  // x3's place: its products are done by then
       int64_t t0;
       int n;
       chunk_at(s, rev, c, &t0, &n);
@@ -567,8 +543,6 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_co
       }
       if (!warp_wait(bOf, c & 1, stop)) break;
       fence_after();
-      const bool direct = packed && n < kChunk;
-      __nv_bfloat16* const orow = p.o + b * p.o_sb + (s.beg + t0 + i) * p.o_st + h * p.o_sh;
 #pragma unroll 1
       for (int vb = 0; vb < VP / 32; ++vb) {
         uint32_t x[32];
@@ -580,38 +554,69 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_co
           if (lane == 0) bar_arrive(bOx);
           __syncwarp();
         }
+        uint32_t o[4][4];  // 16-byte pieces of the row
+#pragma unroll
+        for (int y = 0; y < 16; ++y)
+          o[y / 4][y % 4] = pack_bf16(a.scale * __uint_as_float(x[2 * y]), a.scale * __uint_as_float(x[2 * y + 1]));
+        // four lanes swap pieces, so that together they write 64 bytes of a row
+#pragma unroll
+        for (int d = 1; d < 4; d <<= 1) {
+          const bool up = lane & d;
+#pragma unroll
+          for (int y = 0; y < 4; ++y) {
+            if (y & d) continue;
+#pragma unroll
+            for (int z = 0; z < 4; ++z) {
+              const uint32_t got = __shfl_xor_sync(0xffffffffu, up ? o[y][z] : o[y | d][z], d);
+              if (up) o[y][z] = got;
+              else o[y | d][z] = got;
+            }
+          }
+        }
+        const int col = 32 * vb + 8 * (lane & 3);
 #pragma unroll
         for (int y = 0; y < 4; ++y) {
-          uint32_t o[4];
+          const int row_i = (i & ~3) + y;
+          if (row_i < n && col < p.V)
+            *reinterpret_cast<uint4*>(p.o + b * p.o_sb + (s.beg + t0 + row_i) * p.o_st + h * p.o_sh + col) =
+                make_uint4(o[y][0], o[y][1], o[y][2], o[y][3]);
+        }
+        __syncwarp();
+      }
+    }
+  }
+  __syncwarp();
+  if (role == 1 && s1) {
+    // ---- the final state, by the state's role: column v in lane v
+    const int v = tid % 128;
+    bool ok = true;
+    if (s.nch > 0) {
+      ok = warp_wait(bSt, STATE_ONLY ? 0 : (s.nch - 1) & 1, stop);
+      fence_after();
+    }
+    if (ok) {
+      // a segment on its own starts from nothing: what came in is added here
+      const float in = STATE_ONLY ? s0m * exp2f(l2 * (float)steps) : s0m;
+      const bool add = s0 && (STATE_ONLY || s.nch == 0);
+#pragma unroll 1
+      for (int kb = 0; kb < KP / 32; ++kb) {
+        uint32_t r[32];
+        if (s.nch > 0) {
+          tmem_ld32(tSt + lanes + 32 * kb, r);
+          ld_wait();
+        }
 #pragma unroll
-          for (int z = 0; z < 4; ++z)
-            o[z] = pack_bf16(a.scale * __uint_as_float(x[8 * y + 2 * z]),
-                             a.scale * __uint_as_float(x[8 * y + 2 * z + 1]));
-          const int col = 32 * vb + 8 * y;
-          if (direct) {
-            if (i < n && col < p.V)
-              *reinterpret_cast<uint4*>(orow + col) = make_uint4(o[0], o[1], o[2], o[3]);
-          } else {
-            st_shared16(swizzled(so + (vb / 2) * kHalf, i, (vb % 2) * 4 + y), o[0], o[1], o[2], o[3]);
+        for (int x = 0; x < 32; ++x) {
+          const int k = 32 * kb + x;
+          if (v < p.V && k < p.K) {
+            float f = s.nch > 0 ? __uint_as_float(r[x]) : 0.f;
+            if (add) f = fmaf(in, s0[k * s0k + v * s0v], f);
+            s1[(int64_t)k * p.V + v] = s1m * f;
           }
         }
       }
-      if (!direct) fence_async();
-      __syncwarp();
-      if (lane == 0) bar_arrive(bOut);
-      if (i == 0 && bar_wait(bOut, c & 1, stop)) {
-        if (!direct) {
-#pragma unroll
-          for (int vb = 0; vb < VP / 64; ++vb)
-            copy_out_4d(&p.out, so + vb * kHalf, 64 * vb, h, (int)(s.beg + t0), b);
-          copy_out_commit();
-          copy_out_read();
-        }
-        bar_arrive(bFree3 + 8 * st);
-      }
     }
-    if (i == 0) copy_out_done();
-  }
+    }
   __syncwarp();
   linger(stop);
   fence_before();
@@ -622,37 +627,51 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_co
   }
 }
 
-// The states after segments, from each segment's own: S_s = lambda^len S_(s-1) + own_s.
+// The states after pieces, from each piece's own: S_i = lambda^steps S_(i-1) + own_i.
 __global__ void __launch_bounds__(256) linattn_chain_kernel(const __grid_constant__ TcArgs a) {
   const TcPass& p = a.pass[blockIdx.z];
   const int64_t n = (int64_t)p.K * p.V, row = blockIdx.y;
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  __shared__ float keep[64];  // lambda^steps of a segment's pieces (whole chunks but the row's first,
+                              // which adds to nothing)
+  if (threadIdx.x < a.pieces) {
+    const float l2 = fmaxf(a.log_decay[row % a.H] * 1.44269504088896341f, -1e30f);
+    const int y = threadIdx.x, chunks = a.cps * (y + 1) / a.pieces - a.cps * y / a.pieces;
+    keep[y] = exp2f(l2 * (float)(chunks * kChunk));
+  }
+  __syncthreads();
   if (i >= n) return;
-  const float l2 = fmaxf(a.log_decay[row % a.H] * 1.44269504088896341f, -1e30f);
-  const float keep = exp2f(l2 * (float)(a.cps * kChunk));  // segments after the first are whole
-  float* s = p.seg + row * (a.nseg - 1) * n + i;
+  const int count = (a.nseg - 1) * a.pieces;
+  float* s = p.seg + row * count * n + i;
   float h = s[0];
-  for (int g = 1; g < a.nseg - 1; ++g) {
-    h = fmaf(keep, h, s[g * n]);
+  int y = 0;
+#pragma unroll 4
+  for (int g = 1; g < count; ++g) {
+    y = y + 1 == a.pieces ? 0 : y + 1;
+    h = fmaf(keep[y], h, s[g * n]);
     s[g * n] = h;
   }
 }
 
 struct Split {
-  int nseg, cps;
+  int nseg, cps, pieces;
 };
 
 // Segments of a row: enough that the blocks fill the SMs once (152, one block
 // each), whole chunks. A row's segments cost a second read of x2 and x3, so rows
-// that fill more than half of the SMs by themselves are left whole.
+// that fill more than half of the SMs by themselves are left whole. The segments'
+// own states are found in pieces, as many as fill the SMs.
 Split split_rows(int64_t rows, int64_t T, bool packed) {
   const int64_t nch = (T + kChunk - 1) / kChunk;
-  if (packed || rows <= 0 || rows * 2 > 152 || nch < 4) return Split{1, (int)nch};
+  if (packed || rows <= 0 || rows * 2 > 152 || nch < 4) return Split{1, (int)nch, 1};
   int64_t n = 152 / rows;
   if (n > nch / 2) n = nch / 2;
   const int64_t cps = (nch + n - 1) / n;
   n = (nch + cps - 1) / cps;
-  return Split{(int)n, (int)cps};
+  int64_t m = n > 1 ? 152 / (rows * (n - 1)) : 1;
+  m = m < 1 ? 1 : m > 64 ? 64 : m;
+  m = m > cps / 2 ? (cps / 2 > 0 ? cps / 2 : 1) : m;
+  return Split{(int)n, (int)cps, (int)m};
 }
 
 int padded(int d) { return d <= 64 ? 64 : 128; }
@@ -669,7 +688,7 @@ cudaError_t launch_kv(const TcArgs& t, int npass, int64_t rows, cudaStream_t s) 
     e = cudaFuncSetAttribute(linattn_tc_kernel<KP, VP, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              Q::kSmem);
     if (e != cudaSuccess) return e;
-    linattn_tc_kernel<KP, VP, true><<<(unsigned)(rows * (t.nseg - 1) * npass), kThreads, Q::kSmem, s>>>(t);
+    linattn_tc_kernel<KP, VP, true><<<(unsigned)(rows * (t.nseg - 1) * t.pieces * npass), kThreads, Q::kSmem, s>>>(t);
     linattn_chain_kernel<<<dim3(KP * VP / 256, (unsigned)rows, npass), 256, 0, s>>>(t);
   }
   linattn_tc_kernel<KP, VP, false><<<(unsigned)(rows * t.nseg * npass), kThreads, P::kSmem, s>>>(t);
@@ -705,7 +724,7 @@ size_t linattn_tc_workspace_bytes(int64_t B, int64_t T, int64_t H, int64_t Dk, i
                                   int64_t n_seqs) {
   if (n_seqs > 0) return 0;
   const Split sp = split_rows(B * H, T, false);
-  return (size_t)(3 * B * H * (sp.nseg - 1) * Dk * Dv) * 4;
+  return (size_t)(3 * B * H * (sp.nseg - 1) * sp.pieces * Dk * Dv) * 4;
 }
 
 cudaError_t launch_linattn_tc(const LinArgs& a, cudaStream_t s) {
@@ -720,8 +739,7 @@ cudaError_t launch_linattn_tc(const LinArgs& a, cudaStream_t s) {
     TcPass& d = t[g].pass[count[g]++];
     if (!encode_heads_map(&d.x1, p.x1, a.B, a.T, a.H, p.K, kChunk) ||
         !encode_heads_map(&d.x2, p.x2, a.B, a.T, a.H, p.K, kChunk) ||
-        !encode_heads_map(&d.x3, p.x3, a.B, a.T, a.H, p.V, kChunk) ||
-        !encode_heads_map(&d.out, p.out, a.B, a.T, a.H, p.V, kChunk))
+        !encode_heads_map(&d.x3, p.x3, a.B, a.T, a.H, p.V, kChunk))
       return cudaErrorInvalidValue;
     d.o = static_cast<__nv_bfloat16*>(p.out.ptr);
     d.o_sb = p.out.stride_b;
@@ -735,7 +753,7 @@ cudaError_t launch_linattn_tc(const LinArgs& a, cudaStream_t s) {
     d.K = p.K;
     d.V = p.V;
     d.reverse = p.reverse;
-    d.seg = a.ws + (int64_t)i * rows * (sp.nseg - 1) * p.K * p.V;
+    d.seg = a.ws + (int64_t)i * rows * (sp.nseg - 1) * sp.pieces * p.K * p.V;
   }
   for (int g = 0; g < 2; ++g) {
     if (!count[g]) continue;
@@ -748,6 +766,7 @@ cudaError_t launch_linattn_tc(const LinArgs& a, cudaStream_t s) {
     t[g].H = a.H;
     t[g].nseg = sp.nseg;
     t[g].cps = sp.cps;
+    t[g].pieces = sp.pieces;
     t[g].scale = a.scale;
     const cudaError_t e = launch_passes(t[g], count[g], rows, s);
     if (e != cudaSuccess) return e;

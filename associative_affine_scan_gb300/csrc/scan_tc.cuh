@@ -191,28 +191,31 @@ __device__ __forceinline__ constexpr uint32_t product_desc(int M, int N, bool a_
   return (1u << 4) | (1u << 7) | (1u << 10) | ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16) |
          ((uint32_t)(N / 8) << 17) | ((uint32_t)(M / 16) << 24);
 }
-__device__ __forceinline__ uint64_t operand_base(uint32_t lead) {
-  return ((uint64_t)(lead >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) | (1ull << 46) | (2ull << 61);
-}
-__device__ __forceinline__ uint64_t kmajor(uint32_t addr) {
-  return operand_base(16) | ((addr & 0x3ffff) >> 4);
-}
-__device__ __forceinline__ uint64_t mnmajor(uint32_t addr, uint32_t panel) {
-  return operand_base(panel) | ((addr & 0x3ffff) >> 4);
+// An operand's descriptor: the upper word is the same for all (rows of eight 1024
+// bytes apart, 128-byte swizzle); the lower word holds the tile's address and, for
+// MN-major tiles, the distance of its panels. One thread issues every product, and
+// its instructions are what bounds the issue, so a tile's lower word is made once
+// and steps along the summed index add constants to it.
+constexpr uint32_t kDescHigh = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t kmajor(uint32_t addr) { return (addr >> 4) | (1u << 16); }
+__device__ __forceinline__ uint32_t mnmajor(uint32_t addr, uint32_t panel) {
+  return (addr >> 4) | ((panel >> 4) << 16);
 }
 
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t desc, bool add) {
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t desc, bool add) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d),
-      "l"(a), "l"(b), "r"(desc), "r"((uint32_t)add)
+      "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "mov.b64 a, {%1, %5};\n\tmov.b64 b, {%2, %5};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n}" ::"r"(d),
+      "r"(a), "r"(b), "r"(desc), "r"((uint32_t)add), "r"(kDescHigh)
       : "memory");
 }
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t desc, bool add) {
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t desc, bool add) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d),
-      "r"(a), "l"(b), "r"(desc), "r"((uint32_t)add)
+      "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "mov.b64 b, {%2, %5};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n}" ::"r"(d),
+      "r"(a), "r"(b), "r"(desc), "r"((uint32_t)add), "r"(kDescHigh)
       : "memory");
 }
 // Arrives on `bar` when every product issued by this thread has finished.
@@ -221,24 +224,20 @@ __device__ __forceinline__ void mma_commit(uint32_t bar) {
                : "memory");
 }
 
-// d (+)= A B^T over K = 64 * panels columns; A and B K-major tiles whose panels
-// are a_panel and b_panel bytes apart.
-template <int K>
-__device__ __forceinline__ void mma_kk(uint32_t d, uint32_t a, uint32_t a_panel, uint32_t b,
-                                       uint32_t b_panel, uint32_t desc, bool add) {
-#pragma unroll
-  for (int k = 0; k < K / 16; ++k) {
-    const uint32_t in = (k % 4) * 32;
-    mma_ss(d, kmajor(a + (k / 4) * a_panel + in), kmajor(b + (k / 4) * b_panel + in), desc, add || k > 0);
-  }
-}
-// d (+)= A B over K rows; A in tensor memory (two bf16 a column), B MN-major.
-template <int K>
-__device__ __forceinline__ void mma_tn(uint32_t d, uint32_t a, uint32_t b, uint32_t b_panel,
-                                       uint32_t desc, bool add) {
+// d (+)= A B^T over K = 64 * panels columns; A and B K-major tiles (kmajor() of
+// their addresses) whose panels are AP and BP bytes apart.
+template <int K, uint32_t AP, uint32_t BP>
+__device__ __forceinline__ void mma_kk(uint32_t d, uint32_t a, uint32_t b, uint32_t desc, bool add) {
 #pragma unroll
   for (int k = 0; k < K / 16; ++k)
-    mma_ts(d, a + k * 8, mnmajor(b + k * 2048, b_panel), desc, add || k > 0);
+    mma_ss(d, a + (k / 4) * (AP >> 4) + (k % 4) * 2, b + (k / 4) * (BP >> 4) + (k % 4) * 2, desc, add || k > 0);
+}
+// d (+)= A B over K rows; A in tensor memory (two bf16 a column), B MN-major
+// (mnmajor() of its address).
+template <int K>
+__device__ __forceinline__ void mma_tn(uint32_t d, uint32_t a, uint32_t b, uint32_t desc, bool add) {
+#pragma unroll
+  for (int k = 0; k < K / 16; ++k) mma_ts(d, a + k * 8, b + k * (2048 >> 4), desc, add || k > 0);
 }
 
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {

@@ -150,8 +150,8 @@ __global__ void __launch_bounds__(kThreads, 1) window_fwd_kernel(const __grid_co
       int seen[2] = {0, 0};  // second products issued
       bool ok = bar_wait(bQ, 0, stop);
       const auto scores = [&](int x, int u) {
-        mma_kk<DP>(tm + 128 * x, sQ + x * P::kTileBytes, kHalf, sKV + (2 * u % NS) * P::kTileBytes, kHalf, dS,
-                   false);
+        mma_kk<DP, kHalf, kHalf>(tm + 128 * x, kmajor(sQ) + x * (P::kTileBytes >> 4),
+                                 kmajor(sKV) + (2 * u % NS) * (P::kTileBytes >> 4), dS, false);
         mma_commit(bS + 8 * x);
       };
       ok = ok && bar_wait(bFull, 0, stop);
@@ -169,7 +169,8 @@ __global__ void __launch_bounds__(kThreads, 1) window_fwd_kernel(const __grid_co
             ok = bar_wait(bP + 8 * x, seen[x] & 1, stop);
             if (!ok) break;
             fence_after();
-            mma_tn<kRows>(tm + 256 + 128 * x, tm + 128 * x, sKV + vs * P::kTileBytes, kHalf, dO, seen[x] > 0);
+            mma_tn<kRows>(tm + 256 + 128 * x, tm + 128 * x, mnmajor(sKV, kHalf) + vs * (P::kTileBytes >> 4), dO,
+                          seen[x] > 0);
             mma_commit(bO + 8 * x);
             ++seen[x];
           }
