@@ -288,7 +288,8 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_co
     }
   } else if (warp == 17) {
     // ---- products
-    if (lane == 0) {
+    {
+      const bool lead = lane == 0;
       constexpr uint32_t dS1 = product_desc(128, 128, false, false);
       constexpr uint32_t dOi = product_desc(128, VP, false, false);
       constexpr uint32_t dSt = product_desc(128, KP, false, true);
@@ -297,13 +298,13 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_co
         int64_t t0;
         int n;
         chunk_at(s, rev, c, &t0, &n);
-        return bar_wait(bFull12 + 8 * (c % P::kStages), (c / P::kStages) & 1, stop) &&
-               (!packed || n == kChunk || bar_wait(bClean, 0, stop));
+        return warp_wait(bFull12 + 8 * (c % P::kStages), (c / P::kStages) & 1, stop) &&
+               (!packed || n == kChunk || warp_wait(bClean, 0, stop));
       };
       const auto scores = [&](int c) {
         const uint32_t x1 = kmajor(base) + (c % P::kStages) * (P::kStage >> 4);
-        mma_kk<KP, kHalf, kHalf>(tS1, x1, x1 + (P::kX1 >> 4), dS1, false);
-        mma_commit(bS1);
+        mma_kk<KP, kHalf, kHalf>(lead, tS1, x1, x1 + (P::kX1 >> 4), dS1, false);
+        mma_commit(lead, bS1);
       };
       bool ok = s.nch > 0;
       if (!STATE_ONLY && ok && (ok = ready(0))) scores(0);
@@ -314,48 +315,48 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_co
         const uint32_t x2 = mnmajor(base + P::kX1, kHalf) + st * (P::kStage >> 4), x3 = x2 + (P::kX2 >> 4);
         const bool have = c > 0 || (s0 && !STATE_ONLY);
         if (STATE_ONLY) ok = ready(c);
-        else if (c > 0) ok = bar_wait(bSb, (c - 1) & 1, stop);
-        else if (s0) ok = bar_wait(bInit, 0, stop);
+        else if (c > 0) ok = warp_wait(bSb, (c - 1) & 1, stop);
+        else if (s0) ok = warp_wait(bInit, 0, stop);
         if (!ok) break;
         fence_after();
         if (c + 1 < s.nch || s1) {
 #pragma unroll
           for (int jb = 0; jb < 4; ++jb) {
             const int buf = jb % kBufs;
-            if (!(ok = bar_wait(bX + 8 * buf, (STATE_ONLY ? c : jb >> 1) & 1, stop))) break;
+            if (!(ok = warp_wait(bX + 8 * buf, (STATE_ONLY ? c : jb >> 1) & 1, stop))) break;
             fence_after();
-            mma_tn<32>(tSt, tX + 32 * buf, x2 + jb * (32 * kPitch >> 4), dSt, have || jb > 0);
-            mma_tn<32>(tSt, tX + 32 * buf + 16, x2 + jb * (32 * kPitch >> 4), dSt, true);
-            mma_commit(bXf + 8 * buf);
+            mma_tn<32>(lead, tSt, tX + 32 * buf, x2 + jb * (32 * kPitch >> 4), dSt, have || jb > 0);
+            mma_tn<32>(lead, tSt, tX + 32 * buf + 16, x2 + jb * (32 * kPitch >> 4), dSt, true);
+            mma_commit(lead, bXf + 8 * buf);
           }
           if (!ok) break;
         }
         if (STATE_ONLY) {
-          mma_commit(bFree12 + 8 * st);
-          mma_commit(bFree3 + 8 * st);
-          if (c + 1 == s.nch) mma_commit(bSt);
+          mma_commit(lead, bFree12 + 8 * st);
+          mma_commit(lead, bFree3 + 8 * st);
+          if (c + 1 == s.nch) mma_commit(lead, bSt);
           continue;
         }
-        if (c > 0 && !(ok = bar_wait(bOx, (c - 1) & 1, stop))) break;
+        if (c > 0 && !(ok = warp_wait(bOx, (c - 1) & 1, stop))) break;
         fence_after();
         if (have) {
-          mma_kk<KP, kHalf, VP * kPitch>(tO, x1, kmajor(sState), dOi, false);
-          mma_commit(bOi);
+          mma_kk<KP, kHalf, VP * kPitch>(lead, tO, x1, kmajor(sState), dOi, false);
+          mma_commit(lead, bOi);
         }
-        mma_commit(bSt);
-        mma_commit(bFree12 + 8 * st);
-        if (!(ok = bar_wait(bP, c & 1, stop))) break;
+        mma_commit(lead, bSt);
+        mma_commit(lead, bFree12 + 8 * st);
+        if (!(ok = warp_wait(bP, c & 1, stop))) break;
         if (c + 1 < s.nch) {
           if (!(ok = ready(c + 1))) break;
           fence_after();
           scores(c + 1);
         }
-        if (have && !(ok = bar_wait(bOs, (c - late) & 1, stop))) break;
-        if (!(ok = bar_wait(bFull3 + 8 * st, (c / P::kStages) & 1, stop))) break;
+        if (have && !(ok = warp_wait(bOs, (c - late) & 1, stop))) break;
+        if (!(ok = warp_wait(bFull3 + 8 * st, (c / P::kStages) & 1, stop))) break;
         fence_after();
-        mma_tn<kChunk>(tO, tP, x3, dO, have);
-        mma_commit(bOf);
-        mma_commit(bFree3 + 8 * st);
+        mma_tn<kChunk>(lead, tO, tP, x3, dO, have);
+        mma_commit(lead, bOf);
+        mma_commit(lead, bFree3 + 8 * st);
       }
     }
   } else if (role == 0 && !STATE_ONLY) {

@@ -202,42 +202,47 @@ __device__ __forceinline__ uint32_t mnmajor(uint32_t addr, uint32_t panel) {
   return (addr >> 4) | ((panel >> 4) << 16);
 }
 
-__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t desc, bool add) {
+// The product warp runs as a whole, so that descriptors and addresses stay in
+// uniform registers, which these instructions read; `lead` (one lane) issues.
+__device__ __forceinline__ void mma_ss(bool lead, uint32_t d, uint32_t a, uint32_t b, uint32_t desc, bool add) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "{\n\t.reg .pred p, q;\n\t.reg .b64 a, b;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %6, 0;\n\t"
       "mov.b64 a, {%1, %5};\n\tmov.b64 b, {%2, %5};\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n}" ::"r"(d),
-      "r"(a), "r"(b), "r"(desc), "r"((uint32_t)add), "r"(kDescHigh)
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n}" ::"r"(d),
+      "r"(a), "r"(b), "r"(desc), "r"((uint32_t)add), "r"(kDescHigh), "r"((uint32_t)lead)
       : "memory");
 }
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t desc, bool add) {
+__device__ __forceinline__ void mma_ts(bool lead, uint32_t d, uint32_t a, uint32_t b, uint32_t desc, bool add) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "{\n\t.reg .pred p, q;\n\t.reg .b64 b;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %6, 0;\n\t"
       "mov.b64 b, {%2, %5};\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n}" ::"r"(d),
-      "r"(a), "r"(b), "r"(desc), "r"((uint32_t)add), "r"(kDescHigh)
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n}" ::"r"(d),
+      "r"(a), "r"(b), "r"(desc), "r"((uint32_t)add), "r"(kDescHigh), "r"((uint32_t)lead)
       : "memory");
 }
 // Arrives on `bar` when every product issued by this thread has finished.
-__device__ __forceinline__ void mma_commit(uint32_t bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
-               : "memory");
+__device__ __forceinline__ void mma_commit(bool lead, uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}" ::"r"(bar),
+      "r"((uint32_t)lead)
+      : "memory");
 }
 
 // d (+)= A B^T over K = 64 * panels columns; A and B K-major tiles (kmajor() of
 // their addresses) whose panels are AP and BP bytes apart.
 template <int K, uint32_t AP, uint32_t BP>
-__device__ __forceinline__ void mma_kk(uint32_t d, uint32_t a, uint32_t b, uint32_t desc, bool add) {
+__device__ __forceinline__ void mma_kk(bool lead, uint32_t d, uint32_t a, uint32_t b, uint32_t desc, bool add) {
 #pragma unroll
   for (int k = 0; k < K / 16; ++k)
-    mma_ss(d, a + (k / 4) * (AP >> 4) + (k % 4) * 2, b + (k / 4) * (BP >> 4) + (k % 4) * 2, desc, add || k > 0);
+    mma_ss(lead, d, a + (k / 4) * (AP >> 4) + (k % 4) * 2, b + (k / 4) * (BP >> 4) + (k % 4) * 2, desc, add || k > 0);
 }
 // d (+)= A B over K rows; A in tensor memory (two bf16 a column), B MN-major
 // (mnmajor() of its address).
 template <int K>
-__device__ __forceinline__ void mma_tn(uint32_t d, uint32_t a, uint32_t b, uint32_t desc, bool add) {
+__device__ __forceinline__ void mma_tn(bool lead, uint32_t d, uint32_t a, uint32_t b, uint32_t desc, bool add) {
 #pragma unroll
-  for (int k = 0; k < K / 16; ++k) mma_ts(d, a + k * 8, b + k * (2048 >> 4), desc, add || k > 0);
+  for (int k = 0; k < K / 16; ++k) mma_ts(lead, d, a + k * 8, b + k * (2048 >> 4), desc, add || k > 0);
 }
 
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
@@ -249,6 +254,34 @@ __device__ __forceinline__ float fast_exp2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+// Pairs of fp32 in one operation.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n\t.reg .b64 x, y, z, w;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
+      "fma.rn.f32x2 w, x, y, z;\n\tmov.b64 {%0, %1}, w;\n}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 x, y, w;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+      "add.rn.f32x2 w, x, y;\n\tmov.b64 {%0, %1}, w;\n}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 x, y, w;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+      "mul.rn.f32x2 w, x, y;\n\tmov.b64 {%0, %1}, w;\n}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float2 pair_of(const uint32_t* r) {
+  return make_float2(__uint_as_float(r[0]), __uint_as_float(r[1]));
 }
 // Where piece `piece` (16 bytes) of row `row` of a panel lies.
 __device__ __forceinline__ uint32_t swizzled(uint32_t panel, int row, int piece) {

@@ -233,45 +233,46 @@ __global__ void __launch_bounds__(kThreads, 1) window_dkv_kernel(const __grid_co
     }
   } else if (warp == 9) {
     // ---- products
-    if (lane == 0 && n > 0) {
+    if (n > 0) {
+      const bool lead = lane == 0;
       constexpr uint32_t dS = product_desc(128, 128, false, false);
       constexpr uint32_t dO = product_desc(128, DP, false, true);
       const auto slot = [&](int u) { return kmajor(sR) + (u % NS) * (P::kTileBytes >> 4); };
       const auto slot_mn = [&](int u) { return mnmajor(sR, kHalf) + (u % NS) * (P::kTileBytes >> 4); };
-      const auto full = [&](int u) { return bar_wait(bFull + 8 * (u % NS), (u / NS) & 1, stop); };
+      const auto full = [&](int u) { return warp_wait(bFull + 8 * (u % NS), (u / NS) & 1, stop); };
       // two halves of 64 query columns, each packed where its scores were
       const auto second = [&](uint32_t d, uint32_t w, uint32_t t, bool add) {
-        mma_tn<64>(d, w, t, dO, add);
-        mma_tn<64>(d, w + 64, t + (64 * kPitch >> 4), dO, true);
+        mma_tn<64>(lead, d, w, t, dO, add);
+        mma_tn<64>(lead, d, w + 64, t + (64 * kPitch >> 4), dO, true);
       };
-      bool ok = bar_wait(bKV, 0, stop) && full(0) && full(1);
+      bool ok = warp_wait(bKV, 0, stop) && full(0) && full(1);
       if (ok) {
-        mma_kk<DP, kHalf, kHalf>(tS, kmajor(sK), slot(0), dS, false);
-        mma_commit(bS);
-        mma_kk<DP, kHalf, kHalf>(tDp, kmajor(sV), slot(1), dS, false);
-        mma_commit(bDp);
+        mma_kk<DP, kHalf, kHalf>(lead, tS, kmajor(sK), slot(0), dS, false);
+        mma_commit(lead, bS);
+        mma_kk<DP, kHalf, kHalf>(lead, tDp, kmajor(sV), slot(1), dS, false);
+        mma_commit(lead, bDp);
       }
       for (int u = 0; ok && u < n; ++u) {
-        if (!(ok = bar_wait(bP, u & 1, stop))) break;
+        if (!(ok = warp_wait(bP, u & 1, stop))) break;
         fence_after();
         second(tDv, tS, slot_mn(2 * u + 1), u > 0);
         if (u + 1 < n) {
           if (!(ok = full(2 * u + 2))) break;
-          mma_kk<DP, kHalf, kHalf>(tS, kmajor(sK), slot(2 * u + 2), dS, false);
-          mma_commit(bS);
+          mma_kk<DP, kHalf, kHalf>(lead, tS, kmajor(sK), slot(2 * u + 2), dS, false);
+          mma_commit(lead, bS);
         }
-        if (!(ok = bar_wait(bDs, u & 1, stop))) break;
+        if (!(ok = warp_wait(bDs, u & 1, stop))) break;
         fence_after();
         second(tDk, tDp, slot_mn(2 * u), u > 0);
-        mma_commit(bEmpty + 8 * (2 * u % NS));
-        mma_commit(bEmpty + 8 * ((2 * u + 1) % NS));
+        mma_commit(lead, bEmpty + 8 * (2 * u % NS));
+        mma_commit(lead, bEmpty + 8 * ((2 * u + 1) % NS));
         if (u + 1 < n) {
           if (!(ok = full(2 * u + 3))) break;
-          mma_kk<DP, kHalf, kHalf>(tDp, kmajor(sV), slot(2 * u + 3), dS, false);
-          mma_commit(bDp);
+          mma_kk<DP, kHalf, kHalf>(lead, tDp, kmajor(sV), slot(2 * u + 3), dS, false);
+          mma_commit(lead, bDp);
         }
       }
-      mma_commit(bEnd);
+      mma_commit(lead, bEnd);
     }
   } else {
     // ---- P and dS: key r of the tile in lane r, 64 query columns a warpgroup
@@ -525,22 +526,23 @@ __global__ void __launch_bounds__(kThreads, 1) window_dq_kernel(const __grid_con
       }
     }
   } else if (warp == 9) {
-    if (lane == 0 && n > 0) {
+    if (n > 0) {
+      const bool lead = lane == 0;
       constexpr uint32_t dS = product_desc(128, 128, false, false);
       constexpr uint32_t dO = product_desc(128, DP, false, true);
       const auto slot = [&](int u) { return kmajor(sR) + (u % NS) * (P::kTileBytes >> 4); };
       const auto slot_mn = [&](int u) { return mnmajor(sR, kHalf) + (u % NS) * (P::kTileBytes >> 4); };
-      const auto full = [&](int u) { return bar_wait(bFull + 8 * (u % NS), (u / NS) & 1, stop); };
+      const auto full = [&](int u) { return warp_wait(bFull + 8 * (u % NS), (u / NS) & 1, stop); };
       const auto scores = [&](int u) {
-        mma_kk<DP, kHalf, kHalf>(tS + 128 * (u & 1), kmajor(sQ), slot(2 * u), dS, false);
-        mma_commit(bS + 8 * (u & 1));
+        mma_kk<DP, kHalf, kHalf>(lead, tS + 128 * (u & 1), kmajor(sQ), slot(2 * u), dS, false);
+        mma_commit(lead, bS + 8 * (u & 1));
       };
       const auto dprod = [&](int u) {
-        mma_kk<DP, kHalf, kHalf>(tDp, kmajor(sD), slot(2 * u + 1), dS, false);
-        mma_commit(bDp);
-        mma_commit(bEmpty + 8 * ((2 * u + 1) % NS));
+        mma_kk<DP, kHalf, kHalf>(lead, tDp, kmajor(sD), slot(2 * u + 1), dS, false);
+        mma_commit(lead, bDp);
+        mma_commit(lead, bEmpty + 8 * ((2 * u + 1) % NS));
       };
-      bool ok = bar_wait(bQ, 0, stop) && full(0) && full(1);
+      bool ok = warp_wait(bQ, 0, stop) && full(0) && full(1);
       if (ok) {
         scores(0);
         dprod(0);
@@ -548,19 +550,19 @@ __global__ void __launch_bounds__(kThreads, 1) window_dq_kernel(const __grid_con
       }
       for (int u = 0; ok && u < n; ++u) {
         if (u + 1 < n && !(ok = full(2 * u + 3))) break;
-        if (!(ok = bar_wait(bDs, u & 1, stop))) break;
+        if (!(ok = warp_wait(bDs, u & 1, stop))) break;
         fence_after();
         if (u + 1 < n) dprod(u + 1);
         const uint32_t w = tS + 128 * (u & 1);
-        mma_tn<64>(tDq, w, slot_mn(2 * u), dO, u > 0);
-        mma_tn<64>(tDq, w + 64, slot_mn(2 * u) + (64 * kPitch >> 4), dO, true);
-        mma_commit(bEmpty + 8 * (2 * u % NS));
+        mma_tn<64>(lead, tDq, w, slot_mn(2 * u), dO, u > 0);
+        mma_tn<64>(lead, tDq, w + 64, slot_mn(2 * u) + (64 * kPitch >> 4), dO, true);
+        mma_commit(lead, bEmpty + 8 * (2 * u % NS));
         if (u + 2 < n) {
           if (!(ok = full(2 * u + 4))) break;
           scores(u + 2);
         }
       }
-      mma_commit(bEnd);
+      mma_commit(lead, bEnd);
     }
   } else {
     const int w = warp / 4, r = tid - 128 * w;

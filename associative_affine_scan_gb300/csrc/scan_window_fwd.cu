@@ -12,7 +12,10 @@
 // the tensor cores work on the other's products. Roles: a copy warp (a ring of
 // key and value tiles), a product warp, four softmax warps a query tile, a row a
 // thread. Tensor memory holds both tiles' scores and outputs (4 x 128 columns); p
-// replaces its scores there as bf16 and is read from there by the second product.
+// replaces its scores there as bf16 and is read from there by the second product,
+// which starts on the first 64 keys while the others' exponentials are still being
+// taken. Scores are read twice, for the maximum and for the exponentials, which is
+// cheaper than registers for 128 of them.
 // The maximum that p is taken from follows the true one only when that has grown
 // by more than 2^8: until then p stays below 2^8, which changes no rounding (bf16
 // and fp32 have the same exponents), and the outputs need no rescaling.
@@ -49,11 +52,7 @@ struct Plan {
   static constexpr int kSmem = (2 + kSlots) * kTileBytes + 1024 + 512;
 };
 
-// The keys that row position i sees among columns [0, 128) of a tile at j0:
-// [lo, hi], and those below sk.
-struct Seen {
-  int lo, hi, sk;
-};
+// A column number of a tile, or one before or past all of them.
 __device__ __forceinline__ int clamp_col(int64_t v) { return (int)(v < -1 ? -1 : v > 200 ? 200 : v); }
 
 template <int DP>
@@ -68,8 +67,8 @@ __global__ void __launch_bounds__(kThreads, 1) window_fwd_kernel(const __grid_co
   uint32_t* const misc = reinterpret_cast<uint32_t*>(gen + (2 + NS) * P::kTileBytes);
   const uint32_t bars = smem_addr(misc);
   const uint32_t bQ = bars, bFull = bars + 8, bEmpty = bFull + 8 * NS, bS = bEmpty + 8 * NS, bP = bS + 16,
-                 bO = bP + 16, bOut = bO + 16;
-  uint32_t* const tmem_ptr = misc + (8 + 16 * NS + 64) / 4;
+                 bO = bP + 32, bOut = bO + 16;
+  uint32_t* const tmem_ptr = misc + (8 + 16 * NS + 80) / 4;
   uint32_t* const stop_flag = tmem_ptr + 1;
 
   if (a.cu && blockIdx.x == 0 && blockIdx.y == 0 && warp == 0)
@@ -109,7 +108,8 @@ __global__ void __launch_bounds__(kThreads, 1) window_fwd_kernel(const __grid_co
     }
     for (int x = 0; x < 2; ++x) {
       bar_init(bS + 8 * x, 1);
-      bar_init(bP + 8 * x, 4);
+      bar_init(bP + 16 * x, 4);
+      bar_init(bP + 16 * x + 8, 4);
       bar_init(bO + 8 * x, 1);
       bar_init(bOut + 8 * x, 4);
     }
@@ -144,41 +144,45 @@ __global__ void __launch_bounds__(kThreads, 1) window_fwd_kernel(const __grid_co
     }
   } else if (warp == 9) {
     // ---- products
-    if (lane == 0 && n > 0) {
+    if (n > 0) {
+      const bool lead = lane == 0;
       constexpr uint32_t dS = product_desc(128, 128, false, false);
       constexpr uint32_t dO = product_desc(128, DP, false, true);
       int seen[2] = {0, 0};  // second products issued
-      bool ok = bar_wait(bQ, 0, stop);
+      bool ok = warp_wait(bQ, 0, stop);
       const auto scores = [&](int x, int u) {
-        mma_kk<DP, kHalf, kHalf>(tm + 128 * x, kmajor(sQ) + x * (P::kTileBytes >> 4),
+        mma_kk<DP, kHalf, kHalf>(lead, tm + 128 * x, kmajor(sQ) + x * (P::kTileBytes >> 4),
                                  kmajor(sKV) + (2 * u % NS) * (P::kTileBytes >> 4), dS, false);
-        mma_commit(bS + 8 * x);
+        mma_commit(lead, bS + 8 * x);
       };
-      ok = ok && bar_wait(bFull, 0, stop);
+      ok = ok && warp_wait(bFull, 0, stop);
       if (ok) {
         for (int x = 0; x < 2; ++x)
           if (visits(x, all.at(0))) scores(x, 0);
-        mma_commit(bEmpty);
+        mma_commit(lead, bEmpty);
       }
       for (int u = 0; ok && u < n; ++u) {
         const int kn = (2 * u + 2) % NS, vs = (2 * u + 1) % NS;
-        ok = bar_wait(bFull + 8 * vs, ((2 * u + 1) / NS) & 1, stop);
-        if (ok && u + 1 < n) ok = bar_wait(bFull + 8 * kn, ((2 * u + 2) / NS) & 1, stop);
+        ok = warp_wait(bFull + 8 * vs, ((2 * u + 1) / NS) & 1, stop);
+        if (ok && u + 1 < n) ok = warp_wait(bFull + 8 * kn, ((2 * u + 2) / NS) & 1, stop);
         for (int x = 0; ok && x < 2; ++x) {
           if (visits(x, all.at(u))) {
-            ok = bar_wait(bP + 8 * x, seen[x] & 1, stop);
-            if (!ok) break;
+            const uint32_t o = tm + 256 + 128 * x, p = tm + 128 * x;
+            const uint32_t v = mnmajor(sKV, kHalf) + vs * (P::kTileBytes >> 4);
+            if (!(ok = warp_wait(bP + 16 * x, seen[x] & 1, stop))) break;
             fence_after();
-            mma_tn<kRows>(tm + 256 + 128 * x, tm + 128 * x, mnmajor(sKV, kHalf) + vs * (P::kTileBytes >> 4), dO,
-                          seen[x] > 0);
-            mma_commit(bO + 8 * x);
+            mma_tn<64>(lead, o, p, v, dO, seen[x] > 0);
+            if (!(ok = warp_wait(bP + 16 * x + 8, seen[x] & 1, stop))) break;
+            fence_after();
+            mma_tn<64>(lead, o, p + 32, v + (64 * kPitch >> 4), dO, true);
+            mma_commit(lead, bO + 8 * x);
             ++seen[x];
           }
           if (u + 1 < n && visits(x, all.at(u + 1))) scores(x, u + 1);
         }
         if (!ok) break;
-        mma_commit(bEmpty + 8 * vs);
-        if (u + 1 < n) mma_commit(bEmpty + 8 * kn);
+        mma_commit(lead, bEmpty + 8 * vs);
+        if (u + 1 < n) mma_commit(lead, bEmpty + 8 * kn);
       }
     }
   } else {
@@ -195,31 +199,47 @@ __global__ void __launch_bounds__(kThreads, 1) window_fwd_kernel(const __grid_co
     for (int u = 0; u < n; ++u) {
       const int64_t t = all.at(u), j0 = t * kRows;
       if (!visits(x, t)) continue;
+      const bool tail = a.cu && j0 + kRows > g.nk;  // the tile holds rows of the next sequence
       if (!(ok = warp_wait(bS + 8 * x, k & 1, stop))) break;
       fence_after();
-      uint32_t s[4][32];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) tmem_ld32(tS + 32 * i, s[i]);
-      ld_wait();
       const bool whole = j0 + kRows - 1 <= wlo && (whi - j0 < a.W || j0 + kRows <= a.S);
-      if (!whole) {
-        const Seen e{clamp_col(pos - a.W + 1 - j0), clamp_col(pos - j0), clamp_col(a.S - j0)};
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
+      if (!whole) {  // what this row does not see becomes -inf where it lies
+        const int lo = clamp_col(pos - a.W + 1 - j0), hi = clamp_col(pos - j0), sk = clamp_col(a.S - j0);
+#pragma unroll 1
+        for (int i = 0; i < 4; ++i) {
+          uint32_t s[32];
+          tmem_ld32(tS + 32 * i, s);
+          ld_wait();
 #pragma unroll
           for (int c = 0; c < 32; ++c) {
             const int j = 32 * i + c;
-            if (!(j <= e.hi && (j >= e.lo || j < e.sk))) s[i][c] = 0xff800000u;
+            if (!(j <= hi && (j >= lo || j < sk))) s[c] = 0xff800000u;
           }
+          tmem_st32(tS + 32 * i, s);
+        }
+        st_wait();
       }
-      float mx[4];
+      float top;
+      {
+        uint32_t s[2][32];
+        float y[4];
+        tmem_ld32(tS, s[0]);
+        ld_wait();
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        mx[i] = __uint_as_float(s[i][0]);
+        for (int i = 0; i < 4; ++i) {  // the next columns are on their way while these are compared
+          const uint32_t(&now)[32] = s[i & 1];
+          if (i < 3) tmem_ld32(tS + 32 * (i + 1), s[(i + 1) & 1]);
 #pragma unroll
-        for (int c = 1; c < 32; ++c) mx[i] = fmaxf(mx[i], __uint_as_float(s[i][c]));
+          for (int c = 0; c < 32; c += 8)
+#pragma unroll
+            for (int z = 0; z < 4; ++z) {
+              const float v = fmaxf(__uint_as_float(now[c + z]), __uint_as_float(now[c + z + 4]));
+              y[z] = i == 0 && c == 0 ? v : fmaxf(y[z], v);
+            }
+          if (i < 3) ld_wait();
+        }
+        top = fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3])) * a.sl2;
       }
-      const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.sl2;
       const bool grow = top > m + 8.f;  // from -inf: always, once a key is seen
       if (__any_sync(0xffffffffu, grow)) {
         const float mn = grow ? top : m;
@@ -227,7 +247,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_fwd_kernel(const __grid_co
         if (k > 0) {
           if (!(ok = warp_wait(bO + 8 * x, (k - 1) & 1, stop))) break;
           fence_after();
-#pragma unroll
+#pragma unroll 1
           for (int i = 0; i < DP / 32; ++i) {
             uint32_t o[32];
             tmem_ld32(tO + 32 * i, o);
@@ -241,23 +261,40 @@ __global__ void __launch_bounds__(kThreads, 1) window_fwd_kernel(const __grid_co
         m = mn;
       }
       const float from = m == -INFINITY ? 0.f : m;
-      float sum[4] = {0.f, 0.f, 0.f, 0.f};
+      float2 sum[4] = {};
+      const float2 f2 = make_float2(-from, -from), sl2 = make_float2(a.sl2, a.sl2);
+      {
+        uint32_t s[2][32];
+        tmem_ld32(tS, s[0]);
+        ld_wait();
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        uint32_t o[32];
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t(&now)[32] = s[i & 1];
+          if (i < 3) tmem_ld32(tS + 32 * (i + 1), s[(i + 1) & 1]);
+          uint32_t o[16];
 #pragma unroll
           for (int c = 0; c < 32; c += 2) {
-            const float p0 = fast_exp2(fmaf(__uint_as_float(s[2 * h + i][c]), a.sl2, -from));
-            const float p1 = fast_exp2(fmaf(__uint_as_float(s[2 * h + i][c + 1]), a.sl2, -from));
-            sum[c / 2 % 4] += p0 + p1;
-            o[16 * i + c / 2] = pack_bf16(p0, p1);
+            const float2 z = fma2(pair_of(now + c), sl2, f2);
+            const float2 p = make_float2(fast_exp2(z.x), fast_exp2(z.y));
+            sum[c / 2 % 4] = add2(sum[c / 2 % 4], p);
+            o[c / 2] = pack_bf16(p.x, p.y);
           }
-        tmem_st32(tS + 32 * h, o);
+          if (i < 3) ld_wait();
+          tmem_st16(tS + 16 * i, o);  // over columns that have been read
+          if (i == 1) {
+            st_wait();
+            fence_before();
+            __syncwarp();
+            if (lane == 0 && !tail) bar_arrive(bP + 16 * x);
+            __syncwarp();
+          }
+        }
       }
-      l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-      if (a.cu && j0 + kRows > g.nk) {
+      {
+        const float2 z = add2(add2(sum[0], sum[1]), add2(sum[2], sum[3]));
+        l += z.x + z.y;
+      }
+      if (tail) {
         // value rows past the sequence belong to the next one: both roles clear
         // them before their product may start
         const int vs = (2 * u + 1) % NS;
@@ -272,7 +309,10 @@ __global__ void __launch_bounds__(kThreads, 1) window_fwd_kernel(const __grid_co
       st_wait();
       fence_before();
       __syncwarp();
-      if (lane == 0) bar_arrive(bP + 8 * x);
+      if (lane == 0) {
+        if (tail) bar_arrive(bP + 16 * x);
+        bar_arrive(bP + 16 * x + 8);
+      }
       ++k;
     }
     // ---- o / l to shared memory (the queries' place: their products are done), then out
