@@ -17,7 +17,9 @@
 // The order of issue keeps the tensor cores busy while two warpgroups turn S and
 // dP into P and dS, half of the columns each: the first product of the next tile
 // is issued between the two that wait for them. Both are bound by the tensor
-// cores (512 cycles a product at D = 128).
+// cores (512 cycles a product at D = 128). The queries' kernel issues dP from a
+// warp of its own (141 -> 132 us on 2 x 4096 x 16 heads, window 1024); the same
+// in the keys' kernel, whose two chains then alternate, took 170 us for 160.
 //
 // The tile of keys that holds the first tokens is seen by every later query: its
 // walk is cut into pieces of about the length of any other tile's, whose partial
@@ -31,7 +33,8 @@ namespace {
 using namespace tc;
 
 constexpr int kRows = 128;
-constexpr int kThreads = 10 * 32;  // two warpgroups of softmax, copies, products
+constexpr int kThreads = 10 * 32;    // two warpgroups of softmax, copies, products
+constexpr int kThreadsDq = 11 * 32;  // and a second product warp
 constexpr uint32_t kHalf = kRows * kPitch;
 
 struct BwdArgs {
@@ -463,7 +466,7 @@ __global__ void __launch_bounds__(256) window_pieces_kernel(const __grid_constan
 // ---------------------------------------------------------------------------
 
 template <int DP>
-__global__ void __launch_bounds__(kThreads, 1) window_dq_kernel(const __grid_constant__ BwdArgs a) {
+__global__ void __launch_bounds__(kThreadsDq, 1) window_dq_kernel(const __grid_constant__ BwdArgs a) {
   using P = Plan<DP>;
   constexpr int NS = P::kSlots;
   extern __shared__ uint8_t raw[];
@@ -526,36 +529,27 @@ __global__ void __launch_bounds__(kThreads, 1) window_dq_kernel(const __grid_con
       }
     }
   } else if (warp == 9) {
+    // ---- products: S and dq += dS k
     if (n > 0) {
       const bool lead = lane == 0;
       constexpr uint32_t dS = product_desc(128, 128, false, false);
       constexpr uint32_t dO = product_desc(128, DP, false, true);
-      const auto slot = [&](int u) { return kmajor(sR) + (u % NS) * (P::kTileBytes >> 4); };
-      const auto slot_mn = [&](int u) { return mnmajor(sR, kHalf) + (u % NS) * (P::kTileBytes >> 4); };
+      const auto slot = [&](int u) { return (u % NS) * (P::kTileBytes >> 4); };
       const auto full = [&](int u) { return warp_wait(bFull + 8 * (u % NS), (u / NS) & 1, stop); };
       const auto scores = [&](int u) {
-        mma_kk<DP, kHalf, kHalf>(lead, tS + 128 * (u & 1), kmajor(sQ), slot(2 * u), dS, false);
+        mma_kk<DP, kHalf, kHalf>(lead, tS + 128 * (u & 1), kmajor(sQ), kmajor(sR) + slot(2 * u), dS, false);
         mma_commit(lead, bS + 8 * (u & 1));
       };
-      const auto dprod = [&](int u) {
-        mma_kk<DP, kHalf, kHalf>(lead, tDp, kmajor(sD), slot(2 * u + 1), dS, false);
-        mma_commit(lead, bDp);
-        mma_commit(lead, bEmpty + 8 * ((2 * u + 1) % NS));
-      };
-      bool ok = warp_wait(bQ, 0, stop) && full(0) && full(1);
-      if (ok) {
-        scores(0);
-        dprod(0);
-        if (n > 1 && (ok = full(2))) scores(1);
-      }
+      bool ok = warp_wait(bQ, 0, stop) && full(0);
+      if (ok) scores(0);
+      if (ok && n > 1 && (ok = full(2))) scores(1);
+#pragma unroll 1
       for (int u = 0; ok && u < n; ++u) {
-        if (u + 1 < n && !(ok = full(2 * u + 3))) break;
         if (!(ok = warp_wait(bDs, u & 1, stop))) break;
         fence_after();
-        if (u + 1 < n) dprod(u + 1);
-        const uint32_t w = tS + 128 * (u & 1);
-        mma_tn<64>(lead, tDq, w, slot_mn(2 * u), dO, u > 0);
-        mma_tn<64>(lead, tDq, w + 64, slot_mn(2 * u) + (64 * kPitch >> 4), dO, true);
+        const uint32_t w = tS + 128 * (u & 1), t = mnmajor(sR, kHalf) + slot(2 * u);
+        mma_tn<64>(lead, tDq, w, t, dO, u > 0);
+        mma_tn<64>(lead, tDq, w + 64, t + (64 * kPitch >> 4), dO, true);
         mma_commit(lead, bEmpty + 8 * (2 * u % NS));
         if (u + 2 < n) {
           if (!(ok = full(2 * u + 4))) break;
@@ -563,6 +557,23 @@ __global__ void __launch_bounds__(kThreads, 1) window_dq_kernel(const __grid_con
         }
       }
       mma_commit(lead, bEnd);
+    }
+  } else if (warp == 10) {
+    // ---- products: dP
+    if (n > 0) {
+      const bool lead = lane == 0;
+      constexpr uint32_t dS = product_desc(128, 128, false, false);
+      bool ok = warp_wait(bQ, 0, stop);
+#pragma unroll 1
+      for (int u = 0; ok && u < n; ++u) {
+        const int v = (2 * u + 1) % NS;
+        if (!(ok = warp_wait(bFull + 8 * v, ((2 * u + 1) / NS) & 1, stop))) break;
+        if (u > 0 && !(ok = warp_wait(bDs, (u - 1) & 1, stop))) break;  // the last dP has been read
+        fence_after();
+        mma_kk<DP, kHalf, kHalf>(lead, tDp, kmajor(sD), kmajor(sR) + v * (P::kTileBytes >> 4), dS, false);
+        mma_commit(lead, bDp);
+        mma_commit(lead, bEmpty + 8 * v);
+      }
     }
   } else {
     const int w = warp / 4, r = tid - 128 * w;
@@ -673,7 +684,7 @@ cudaError_t launch_bwd(const BwdArgs& t, int64_t B, cudaStream_t s) {
   const int64_t tk = (t.Tk + kRows - 1) / kRows + extra, tq = (t.Tq + kRows - 1) / kRows + extra;
   const int64_t cut = t.pieces > 1 ? (int64_t)t.sink_tiles * (t.pieces - 1) : 0;
   window_dkv_kernel<DP><<<dim3((unsigned)(tk + cut), (unsigned)(B * t.Hk)), kThreads, P::kSmem, s>>>(t);
-  window_dq_kernel<DP><<<dim3((unsigned)tq, (unsigned)(B * t.Hq)), kThreads, P::kSmem, s>>>(t);
+  window_dq_kernel<DP><<<dim3((unsigned)tq, (unsigned)(B * t.Hq)), kThreadsDq, P::kSmem, s>>>(t);
   if (t.pieces > 1)
     window_pieces_kernel<<<dim3((unsigned)(t.sink_tiles * kRows), (unsigned)(B * t.Hk)), 256, 0, s>>>(t);
   return cudaGetLastError();
