@@ -44,9 +44,10 @@ struct TcPass {
   CUtensorMap x1, x2, x3;
   __nv_bfloat16* o;
   int64_t o_sb, o_st, o_sh;
+  int o_wide;  // its rows start on 32 bytes and hold whole 32-byte pieces
   const float* s_in;
   float* s_out;
-  float* seg;  // states after pieces of segments: [sequences][H][nseg - 1][pieces][K][V]
+  float* seg;  // states after parts: dense [B][H][nseg - 1][pieces][K][V], packed [segments][H][K][V]
   float s_in_mul, s_out_mul;
   int s_in_t, K, V, reverse;
 };
@@ -107,38 +108,55 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_co
   float* const tab = reinterpret_cast<float*>(gen + P::kStages * P::kStage + P::kState);
   float* const wtab = tab;           // [128] weights of the update in a whole chunk
   float* const wlast = tab + 128;    // [128] in the chunk that ends the sequence, 0 past it
-  float* const ctab = tab + 256;     // [32] column powers of the weights within a chunk
-  const uint32_t bars = smem_addr(tab + 288);
+  // weights within a chunk, with the output's scale: [32] column powers, and [64] those of
+  // row r and column c of a diagonal block, at 32 + r - c
+  float* const ctab = tab + 256;
+  float* const dtab = tab + 288;
+  const uint32_t bars = smem_addr(tab + 352);
   const uint32_t bFull12 = bars, bFull3 = bars + 32, bFree12 = bars + 64, bFree3 = bars + 96, bS1 = bars + 128,
                  bP = bars + 136, bSb = bars + 144, bSt = bars + 152, bX = bars + 160, bXf = bars + 192,
                  bOi = bars + 224, bOs = bars + 232, bOf = bars + 240, bOx = bars + 248, bClean = bars + 256,
                  bInit = bars + 264;
   constexpr int kBufs = STATE_ONLY ? 4 : 2;  // of 32 steps of the update's operand
-  uint32_t* const tmem_ptr = reinterpret_cast<uint32_t*>(tab + 288) + 72;
+  uint32_t* const tmem_ptr = reinterpret_cast<uint32_t*>(tab + 352) + 72;
   uint32_t* const stop_flag = tmem_ptr + 1;
 
-  // which (sequence, head, segment)
-  const int parts = STATE_ONLY ? (a.nseg - 1) * a.pieces : a.nseg;
-  const int part = item % parts;
-  const int64_t row = item / parts;
-  const int seg = STATE_ONLY ? part / a.pieces : part;
-  const int h = (int)(row % a.H);
-  const int64_t sq = row / a.H;
+  // which (sequence, head, segment): dense rows have nseg segments each; packed
+  // sequences are cut into segments that are numbered through
   Span s{0, a.T, 0, 0};
+  int h, seg = 0;
+  int64_t sq, slot;  // slot: of the state after this part, among the workspace's
+  bool last = true;  // the sequence's last segment
   if (a.cu) {
-    int64_t e;
-    seq_bounds(a.cu, (int)sq, a.T, &s.beg, &e);
+    h = (int)(item % a.H);
+    const int64_t tile = item / a.H;
+    int64_t e, local;
+    int q;
+    if (blockIdx.x == 0 && warp == 0 && !STATE_ONLY) check_seqlens(a.cu, a.n_seqs, a.T, a.hdr);
+    if (!locate_tile(a.cu, a.n_seqs, a.T, tile, a.cps * kChunk, &s.beg, &e, &local, &q)) return;
     s.len = e - s.beg;
-    if (blockIdx.x == 0 && warp == 0) check_seqlens(a.cu, a.n_seqs, a.T, a.hdr);
+    sq = q;
+    seg = (int)local;
+    slot = tile * a.H + h;
+    last = (local + 1) * a.cps * kChunk >= s.len;
+    if (STATE_ONLY && last) return;
+  } else {
+    const int parts = STATE_ONLY ? (a.nseg - 1) * a.pieces : a.nseg;
+    const int part = item % parts;
+    const int64_t row = item / parts;
+    h = (int)(row % a.H);
+    sq = row / a.H;
+    seg = STATE_ONLY ? part / a.pieces : part;
+    slot = STATE_ONLY ? row * parts + part : (row * (a.nseg - 1) + seg + 1) * a.pieces - 1;
+    last = seg == a.nseg - 1;
   }
+  const int64_t row = sq * a.H + h;
   const int b = a.cu ? 0 : (int)sq;
   const int64_t all = (s.len + kChunk - 1) / kChunk;
-  if (STATE_ONLY) {
-    const int i = part % a.pieces, c0 = a.cps * i / a.pieces;
+  if (STATE_ONLY && !a.cu) {
+    const int i = item % a.pieces, c0 = a.cps * i / a.pieces;
     s.first = (int64_t)seg * a.cps + c0;
     s.nch = a.cps * (i + 1) / a.pieces - c0;
-  } else if (a.nseg == 1) {
-    s.nch = (int)all;
   } else {
     s.first = (int64_t)seg * a.cps;
     s.nch = (int)(all - s.first < a.cps ? all - s.first : a.cps);
@@ -163,7 +181,7 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_co
       s0m = p.s_in_mul;
     }
   } else if (!STATE_ONLY) {
-    s0 = p.seg + (row * (a.nseg - 1) + seg) * a.pieces * p.K * p.V - p.K * p.V;
+    s0 = p.seg + (a.cu ? slot - a.H : slot - a.pieces) * p.K * p.V;
     s0k = p.V;
     s0v = 1;
   }
@@ -171,8 +189,8 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_co
   float* s1 = nullptr;
   float s1m = 1.f;
   if (STATE_ONLY) {
-    s1 = p.seg + (row * (a.nseg - 1) * a.pieces + part) * p.K * p.V;
-  } else if (seg == a.nseg - 1 && p.s_out) {
+    s1 = p.seg + slot * p.K * p.V;
+  } else if (last && p.s_out) {
     s1 = p.s_out + row * p.K * p.V;
     s1m = p.s_out_mul;
   }
@@ -184,7 +202,11 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_co
     wtab[tid] = exp2f(l2 * (float)(rev ? tid + 1 : 127 - tid));
     wlast[tid] = tid < n ? exp2f(l2 * (float)(rev ? tid + 1 : n - 1 - tid)) : 0.f;
   }
-  if (tid < 32) ctab[tid] = exp2f(l2 * (float)(rev ? tid : 31 - tid));
+  if (tid < 64) {
+    const int d = rev ? 32 - tid : tid - 32;
+    dtab[tid] = d >= 0 ? a.scale * exp2f(l2 * (float)d) : 0.f;
+  }
+  if (tid < 32) ctab[tid] = a.scale * exp2f(l2 * (float)(rev ? tid : 31 - tid));
   if (tid == 0) {
     *stop_flag = 0;
     for (int i = 0; i < P::kStages; ++i) {
@@ -365,7 +387,6 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_co
     // of lambda that are both at most 1; the diagonal block takes the power of
     // the difference.
     const int w = warp % 4;
-    const float lanef = (float)lane;
     bool ok = true;
 #pragma unroll 1
     for (int c = 0; c < s.nch; ++c) {
@@ -384,22 +405,19 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_co
           if (jb == w) {
 #pragma unroll
             for (int x = 0; x < 32; x += 2) {
-              float f[2];
-#pragma unroll
-              for (int y = 0; y < 2; ++y) {
-                const float d = rev ? (float)(x + y) - lanef : lanef - (float)(x + y);
-                f[y] = d >= 0.f ? __uint_as_float(r[x + y]) * fast_exp2(l2 * d) : 0.f;
-              }
-              o[x / 2] = pack_bf16(f[0], f[1]);
+              const float2 f = mul2(pair_of(r + x), make_float2(dtab[32 + lane - x], dtab[31 + lane - x]));
+              o[x / 2] = pack_bf16(f.x, f.y);
             }
           } else {
-            const float rf = exp2f(l2 * (float)(rev ? 32 * (jb - w) - lane : 32 * (w - jb) + lane - 31));
+            const float f = exp2f(l2 * (float)(rev ? 32 * (jb - w) - lane : 32 * (w - jb) + lane - 31));
+            const float2 rf = make_float2(f, f);
 #pragma unroll
             for (int x = 0; x < 32; x += 4) {
               const float4 k = *reinterpret_cast<const float4*>(ctab + x);
-              o[x / 2] = pack_bf16(__uint_as_float(r[x]) * (rf * k.x), __uint_as_float(r[x + 1]) * (rf * k.y));
-              o[x / 2 + 1] =
-                  pack_bf16(__uint_as_float(r[x + 2]) * (rf * k.z), __uint_as_float(r[x + 3]) * (rf * k.w));
+              const float2 f0 = mul2(pair_of(r + x), mul2(rf, make_float2(k.x, k.y)));
+              const float2 f1 = mul2(pair_of(r + x + 2), mul2(rf, make_float2(k.z, k.w)));
+              o[x / 2] = pack_bf16(f0.x, f0.y);
+              o[x / 2 + 1] = pack_bf16(f1.x, f1.y);
             }
           }
         }
@@ -527,7 +545,7 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_co
         if (!warp_wait(bOi, (c - late) & 1, stop)) break;
         fence_after();
         const int r = rev ? n - 1 - i : i;
-        const float f = r >= 0 ? exp2f(l2 * (float)(r + e)) : 0.f;
+        const float f = r >= 0 ? a.scale * exp2f(l2 * (float)(r + e)) : 0.f;
 #pragma unroll 1
         for (int vb = 0; vb < VP / 32; ++vb) {
           uint32_t x[32];
@@ -544,43 +562,31 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_co
       }
       if (!warp_wait(bOf, c & 1, stop)) break;
       fence_after();
+      __nv_bfloat16* const orow = p.o + b * p.o_sb + (s.beg + t0 + i) * p.o_st + h * p.o_sh;
 #pragma unroll 1
       for (int vb = 0; vb < VP / 32; ++vb) {
-        uint32_t x[32];
+        uint32_t x[32], o[16];
         tmem_ld32(tO + lanes + 32 * vb, x);
         ld_wait();
-        if (vb == VP / 32 - 1) {
+        if (vb == VP / 32 - 1) {  // O may be written again
           fence_before();
           __syncwarp();
           if (lane == 0) bar_arrive(bOx);
           __syncwarp();
         }
-        uint32_t o[4][4];  // 16-byte pieces of the row
 #pragma unroll
-        for (int y = 0; y < 16; ++y)
-          o[y / 4][y % 4] = pack_bf16(a.scale * __uint_as_float(x[2 * y]), a.scale * __uint_as_float(x[2 * y + 1]));
-        // four lanes swap pieces, so that together they write 64 bytes of a row
+        for (int y = 0; y < 16; ++y) o[y] = pack_bf16(__uint_as_float(x[2 * y]), __uint_as_float(x[2 * y + 1]));
+        // whole 32-byte sectors a lane where the rows allow
 #pragma unroll
-        for (int d = 1; d < 4; d <<= 1) {
-          const bool up = lane & d;
-#pragma unroll
-          for (int y = 0; y < 4; ++y) {
-            if (y & d) continue;
-#pragma unroll
-            for (int z = 0; z < 4; ++z) {
-              const uint32_t got = __shfl_xor_sync(0xffffffffu, up ? o[y][z] : o[y | d][z], d);
-              if (up) o[y][z] = got;
-              else o[y | d][z] = got;
-            }
+        for (int y = 0; y < 16; y += 8) {
+          const int col = 32 * vb + 2 * y;
+          if (i < n && p.o_wide) {
+            if (col < p.V) st_global32(orow + col, o + y);
+          } else if (i < n) {
+            if (col < p.V) *reinterpret_cast<uint4*>(orow + col) = make_uint4(o[y], o[y + 1], o[y + 2], o[y + 3]);
+            if (col + 8 < p.V)
+              *reinterpret_cast<uint4*>(orow + col + 8) = make_uint4(o[y + 4], o[y + 5], o[y + 6], o[y + 7]);
           }
-        }
-        const int col = 32 * vb + 8 * (lane & 3);
-#pragma unroll
-        for (int y = 0; y < 4; ++y) {
-          const int row_i = (i & ~3) + y;
-          if (row_i < n && col < p.V)
-            *reinterpret_cast<uint4*>(p.o + b * p.o_sb + (s.beg + t0 + row_i) * p.o_st + h * p.o_sh + col) =
-                make_uint4(o[y][0], o[y][1], o[y][2], o[y][3]);
         }
         __syncwarp();
       }
@@ -628,29 +634,67 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_co
   }
 }
 
-// The states after pieces, from each piece's own: S_i = lambda^steps S_(i-1) + own_i.
+// The states after parts, from each part's own: S_i = lambda^steps S_(i-1) + own_i;
+// the parts are a dense row's pieces, or a packed sequence's segments but its last
+// (of whole chunks all but the row's first, which adds to nothing). An empty packed
+// sequence has no part of the row; its final state is written here.
 __global__ void __launch_bounds__(256) linattn_chain_kernel(const __grid_constant__ TcArgs a) {
   const TcPass& p = a.pass[blockIdx.z];
-  const int64_t n = (int64_t)p.K * p.V, row = blockIdx.y;
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  __shared__ float keep[64];  // lambda^steps of a segment's pieces (whole chunks but the row's first,
-                              // which adds to nothing)
-  if (threadIdx.x < a.pieces) {
-    const float l2 = fmaxf(a.log_decay[row % a.H] * 1.44269504088896341f, -1e30f);
+  const int n = p.K * p.V;  // a multiple of 64
+  const int64_t row = blockIdx.y;
+  const int i = (blockIdx.x * 256 + threadIdx.x) * 4;
+  const int h = (int)(row % a.H), seq = (int)(row / a.H);
+  const float l2 = fmaxf(a.log_decay[h] * 1.44269504088896341f, -1e30f);
+  __shared__ float keep[64];  // lambda^steps of a dense segment's pieces
+  if (!a.cu && threadIdx.x < a.pieces) {
     const int y = threadIdx.x, chunks = a.cps * (y + 1) / a.pieces - a.cps * y / a.pieces;
     keep[y] = exp2f(l2 * (float)(chunks * kChunk));
   }
   __syncthreads();
-  if (i >= n) return;
-  const int count = (a.nseg - 1) * a.pieces;
-  float* s = p.seg + row * count * n + i;
-  float h = s[0];
+  int count = (a.nseg - 1) * a.pieces;
+  int64_t first = row * count, step = 1;
+  float whole = 1.f;
+  if (a.cu) {
+    int64_t beg, end, before = 0;  // segments of the sequences before this one
+    for (int q = threadIdx.x % 32; q < seq; q += 32) {
+      seq_bounds(a.cu, q, a.T, &beg, &end);
+      before += (end - beg + a.cps * kChunk - 1) / (a.cps * kChunk);
+    }
+#pragma unroll
+    for (int d = 16; d; d >>= 1) before += __shfl_xor_sync(0xffffffffu, before, d);
+    seq_bounds(a.cu, seq, a.T, &beg, &end);
+    count = (int)((end - beg + a.cps * kChunk - 1) / (a.cps * kChunk)) - 1;
+    first = before * a.H + h;
+    step = a.H;
+    whole = exp2f(l2 * (float)(a.cps * kChunk));
+    if (count < 0 && p.s_out) {
+      for (int j = i; j < i + 4 && j < n; ++j) {
+        const int k = j / p.V, v = j % p.V;
+        p.s_out[row * n + j] = !p.s_in ? 0.f : p.s_out_mul * p.s_in_mul * p.s_in[row * n + (p.s_in_t ? v * p.K + k : j)];
+      }
+    }
+  }
+  if (i >= n || count < 2) return;
+  float4* s = reinterpret_cast<float4*>(p.seg + first * n + i);
+  const int64_t by = step * n / 4;
+  float4 acc = s[0];
   int y = 0;
-#pragma unroll 4
-  for (int g = 1; g < count; ++g) {
-    y = y + 1 == a.pieces ? 0 : y + 1;
-    h = fmaf(keep[y], h, s[g * n]);
-    s[g * n] = h;
+  for (int g = 1; g < count; g += 4) {  // four loads at a time
+    float4 own[4];
+#pragma unroll
+    for (int x = 0; x < 4; ++x)
+      if (g + x < count) own[x] = s[(g + x) * by];
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      if (g + x >= count) break;
+      y = y + 1 == a.pieces ? 0 : y + 1;
+      const float f = a.cu ? whole : keep[y];
+      acc.x = fmaf(f, acc.x, own[x].x);
+      acc.y = fmaf(f, acc.y, own[x].y);
+      acc.z = fmaf(f, acc.z, own[x].z);
+      acc.w = fmaf(f, acc.w, own[x].w);
+      s[(g + x) * by] = acc;
+    }
   }
 }
 
@@ -662,9 +706,9 @@ struct Split {
 // each), whole chunks. A row's segments cost a second read of x2 and x3, so rows
 // that fill more than half of the SMs by themselves are left whole. The segments'
 // own states are found in pieces, as many as fill the SMs.
-Split split_rows(int64_t rows, int64_t T, bool packed) {
+Split split_rows(int64_t rows, int64_t T) {
   const int64_t nch = (T + kChunk - 1) / kChunk;
-  if (packed || rows <= 0 || rows * 2 > 152 || nch < 4) return Split{1, (int)nch, 1};
+  if (rows <= 0 || rows * 2 > 152 || nch < 4) return Split{1, (int)nch, 1};
   int64_t n = 152 / rows;
   if (n > nch / 2) n = nch / 2;
   const int64_t cps = (nch + n - 1) / n;
@@ -673,6 +717,17 @@ Split split_rows(int64_t rows, int64_t T, bool packed) {
   m = m < 1 ? 1 : m > 64 ? 64 : m;
   m = m > cps / 2 ? (cps / 2 > 0 ? cps / 2 : 1) : m;
   return Split{(int)n, (int)cps, (int)m};
+}
+// Packed sequences, whose lengths the host does not know: segments of one size,
+// such that the row's own number of them, and half a segment more a sequence, fill
+// the SMs once; at least four chunks each. nseg: segments of a head at most.
+Split split_packed(int64_t n_seqs, int64_t H, int64_t T) {
+  const int64_t nch = (T + kChunk - 1) / kChunk;
+  int64_t want = H > 0 ? 152 / H - n_seqs / 2 : 1;
+  want = want < 1 ? 1 : want;
+  int64_t cps = (nch + want - 1) / want;
+  cps = cps < 4 ? 4 : cps;
+  return Split{(int)((nch + cps - 1) / cps + n_seqs), (int)cps, 1};
 }
 
 int padded(int d) { return d <= 64 ? 64 : 128; }
@@ -685,14 +740,19 @@ cudaError_t launch_kv(const TcArgs& t, int npass, int64_t rows, cudaStream_t s) 
   cudaError_t e = cudaFuncSetAttribute(linattn_tc_kernel<KP, VP, false>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, P::kSmem);
   if (e != cudaSuccess) return e;
-  if (t.nseg > 1) {
+  // a packed row of one segment's length has none to chain, but may have empty sequences
+  const bool split = t.cu ? (int64_t)t.cps * kChunk < t.T : t.nseg > 1;
+  const int64_t own = t.cu ? (int64_t)t.nseg * t.H : rows * (t.nseg - 1) * t.pieces;
+  const int64_t parts = t.cu ? (int64_t)t.nseg * t.H : rows * t.nseg;
+  if (split) {
     e = cudaFuncSetAttribute(linattn_tc_kernel<KP, VP, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              Q::kSmem);
     if (e != cudaSuccess) return e;
-    linattn_tc_kernel<KP, VP, true><<<(unsigned)(rows * (t.nseg - 1) * t.pieces * npass), kThreads, Q::kSmem, s>>>(t);
-    linattn_chain_kernel<<<dim3(KP * VP / 256, (unsigned)rows, npass), 256, 0, s>>>(t);
+    linattn_tc_kernel<KP, VP, true><<<(unsigned)(own * npass), kThreads, Q::kSmem, s>>>(t);
   }
-  linattn_tc_kernel<KP, VP, false><<<(unsigned)(rows * t.nseg * npass), kThreads, P::kSmem, s>>>(t);
+  if (split || t.cu)
+    linattn_chain_kernel<<<dim3(KP * VP / 1024, (unsigned)rows, npass), 256, 0, s>>>(t);
+  linattn_tc_kernel<KP, VP, false><<<(unsigned)(parts * npass), kThreads, P::kSmem, s>>>(t);
   return cudaGetLastError();
 }
 
@@ -723,14 +783,15 @@ bool linattn_tc_fits(const LinArgs& a, scan_dtype dt) {
 
 size_t linattn_tc_workspace_bytes(int64_t B, int64_t T, int64_t H, int64_t Dk, int64_t Dv,
                                   int64_t n_seqs) {
-  if (n_seqs > 0) return 0;
-  const Split sp = split_rows(B * H, T, false);
-  return (size_t)(3 * B * H * (sp.nseg - 1) * sp.pieces * Dk * Dv) * 4;
+  const Split sp = n_seqs > 0 ? split_packed(n_seqs, H, T) : split_rows(B * H, T);
+  const int64_t slots = n_seqs > 0 ? (int64_t)sp.nseg * H : B * H * (sp.nseg - 1) * sp.pieces;
+  return (size_t)(3 * slots * Dk * Dv) * 4;
 }
 
 cudaError_t launch_linattn_tc(const LinArgs& a, cudaStream_t s) {
   const int64_t n = a.cu ? a.n_seqs : a.B, rows = n * a.H;
-  const Split sp = split_rows(rows, a.T, a.cu != nullptr);
+  const Split sp = a.cu ? split_packed(a.n_seqs, a.H, a.T) : split_rows(rows, a.T);
+  const int64_t slots = a.cu ? (int64_t)sp.nseg * a.H : rows * (sp.nseg - 1) * sp.pieces;
   TcArgs t[2];
   int count[2] = {0, 0};
   for (int i = 0; i < a.npass; ++i) {
@@ -746,6 +807,8 @@ cudaError_t launch_linattn_tc(const LinArgs& a, cudaStream_t s) {
     d.o_sb = p.out.stride_b;
     d.o_st = p.out.stride_t;
     d.o_sh = p.out.stride_h;
+    d.o_wide = (uintptr_t)p.out.ptr % 32 == 0 && p.V % 16 == 0 && (a.B == 1 || d.o_sb % 16 == 0) &&
+               (a.T == 1 || d.o_st % 16 == 0) && (a.H == 1 || d.o_sh % 16 == 0);
     d.s_in = p.s_in;
     d.s_out = p.s_out;
     d.s_in_mul = p.s_in_mul;
@@ -754,7 +817,7 @@ cudaError_t launch_linattn_tc(const LinArgs& a, cudaStream_t s) {
     d.K = p.K;
     d.V = p.V;
     d.reverse = p.reverse;
-    d.seg = a.ws + (int64_t)i * rows * (sp.nseg - 1) * sp.pieces * p.K * p.V;
+    d.seg = a.ws + (int64_t)i * slots * p.K * p.V;
   }
   for (int g = 0; g < 2; ++g) {
     if (!count[g]) continue;

@@ -72,7 +72,8 @@ __device__ __forceinline__ void check_seqlens(const int32_t* cu, int n, int64_t 
 // The sequence and the place in it of row tile `tile` when every sequence is
 // cut into tiles of `rows` rows. One warp; false past the last tile.
 __device__ __forceinline__ bool locate_tile(const int32_t* cu, int n, int64_t T, int64_t tile,
-                                            int rows, int64_t* beg, int64_t* end, int64_t* local) {
+                                            int rows, int64_t* beg, int64_t* end, int64_t* local,
+                                            int* seq = nullptr) {
   const int lane = threadIdx.x & 31;
   int64_t before = 0;
   for (int base = 0; base < n; base += 32) {
@@ -91,6 +92,7 @@ __device__ __forceinline__ bool locate_tile(const int32_t* cu, int n, int64_t T,
       *beg = __shfl_sync(0xffffffffu, a, src);
       *end = __shfl_sync(0xffffffffu, e, src);
       *local = tile - before - __shfl_sync(0xffffffffu, upto - mine, src);
+      if (seq) *seq = base + src;
       return true;
     }
     before += __shfl_sync(0xffffffffu, upto, 31);
