@@ -341,19 +341,21 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_co
         else if (s0) ok = warp_wait(bInit, 0, stop);
         if (!ok) break;
         fence_after();
-        if (c + 1 < s.nch || s1) {
-#pragma unroll
-          for (int jb = 0; jb < 4; ++jb) {
-            const int buf = jb % kBufs;
-            if (!(ok = warp_wait(bX + 8 * buf, (STATE_ONLY ? c : jb >> 1) & 1, stop))) break;
-            fence_after();
-            mma_tn<32>(lead, tSt, tX + 32 * buf, x2 + jb * (32 * kPitch >> 4), dSt, have || jb > 0);
-            mma_tn<32>(lead, tSt, tX + 32 * buf + 16, x2 + jb * (32 * kPitch >> 4), dSt, true);
-            mma_commit(lead, bXf + 8 * buf);
-          }
-          if (!ok) break;
-        }
+        // the update's four pieces; two of them wait for the first two to be used, so the
+        // state is read in between
+        const bool more = c + 1 < s.nch || s1;
+        const auto piece = [&](int jb) {
+          const int buf = jb % kBufs;
+          if (!warp_wait(bX + 8 * buf, (STATE_ONLY ? c : jb >> 1) & 1, stop)) return false;
+          fence_after();
+          mma_tn<32>(lead, tSt, tX + 32 * buf, x2 + jb * (32 * kPitch >> 4), dSt, have || jb > 0);
+          mma_tn<32>(lead, tSt, tX + 32 * buf + 16, x2 + jb * (32 * kPitch >> 4), dSt, true);
+          mma_commit(lead, bXf + 8 * buf);
+          return true;
+        };
+        if (more && !(ok = piece(0) && piece(1))) break;
         if (STATE_ONLY) {
+          if (!(ok = piece(2) && piece(3))) break;
           mma_commit(lead, bFree12 + 8 * st);
           mma_commit(lead, bFree3 + 8 * st);
           if (c + 1 == s.nch) mma_commit(lead, bSt);
@@ -365,6 +367,7 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_co
           mma_kk<KP, kHalf, VP * kPitch>(lead, tO, x1, kmajor(sState), dOi, false);
           mma_commit(lead, bOi);
         }
+        if (more && !(ok = piece(2) && piece(3))) break;
         mma_commit(lead, bSt);
         mma_commit(lead, bFree12 + 8 * st);
         if (!(ok = warp_wait(bP, c & 1, stop))) break;
