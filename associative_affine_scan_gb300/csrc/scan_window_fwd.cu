@@ -93,10 +93,18 @@ __global__ void __launch_bounds__(kThreads, 1) window_fwd_kernel(const __grid_co
     if (all.last < 0) all = kt[1];
     all.last = kt[1].last;
   }
+  // The u-th of these tiles is tile() of the sequence. Query tile x sees it where u is
+  // at most hi and below sk (first tokens) or at least lo. (32-bit numbers: the product
+  // warp's own instructions are time that the tensor cores wait.)
   const int n = (int)all.count();
-  const int64_t sinks = (a.S + kRows - 1) / kRows;  // tiles that hold first tokens
-  const auto visits = [&](int x, int64_t t) {
-    return t <= kt[x].last && (t < sinks || t >= kt[x].near);
+  const int n_sink = (int)all.sink, near = (int)all.near;
+  const int sk = (int)((a.S < (int64_t)n * kRows ? a.S : (int64_t)n * kRows) + kRows - 1) / kRows;
+  const int lo0 = n_sink + (int)(kt[0].near - all.near), lo1 = n_sink + (int)(kt[1].near - all.near);
+  const int hi0 = kt[0].last < 0 ? -1 : n_sink + (int)(kt[0].last - all.near);
+  const int hi1 = kt[1].last < 0 ? -1 : n_sink + (int)(kt[1].last - all.near);
+  const auto tile = [&](int u) { return u < n_sink ? u : near + (u - n_sink); };
+  const auto visits = [&](int x, int u) {
+    return u <= (x ? hi1 : hi0) && (u < sk || u >= (x ? lo1 : lo0));
   };
 
   if (tid == 0) {
@@ -104,7 +112,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_fwd_kernel(const __grid_co
     bar_init(bQ, 1);
     for (int i = 0; i < NS; ++i) {
       bar_init(bFull + 8 * i, 1);
-      bar_init(bEmpty + 8 * i, 1);
+      bar_init(bEmpty + 8 * i, 2);  // from both query tiles
     }
     for (int x = 0; x < 2; ++x) {
       bar_init(bS + 8 * x, 1);
@@ -135,7 +143,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_fwd_kernel(const __grid_co
         const int sl = u % NS;
         if (u >= NS && !bar_wait(bEmpty + 8 * sl, (u / NS - 1) & 1, stop)) break;
         const CUtensorMap* m = u & 1 ? &a.v : &a.k;
-        const int t = (int)(g.kbeg + all.at(u / 2) * kRows);
+        const int t = (int)(g.kbeg + (int64_t)tile(u / 2) * kRows);
         bar_expect(bFull + 8 * sl, P::kTileBytes);
 #pragma unroll
         for (int i = 0; i < DP / 64; ++i)
@@ -158,31 +166,34 @@ __global__ void __launch_bounds__(kThreads, 1) window_fwd_kernel(const __grid_co
       ok = ok && warp_wait(bFull, 0, stop);
       if (ok) {
         for (int x = 0; x < 2; ++x)
-          if (visits(x, all.at(0))) scores(x, 0);
-        mma_commit(lead, bEmpty);
+          if (visits(x, 0)) scores(x, 0);
       }
+      // What a softmax role hands over also says that the value tile, and the key tile
+      // of the next scores, are there; and it is that role that gives slots back (its
+      // scores arriving say that the products issued before them are done). Each wait
+      // and each commit here would cost the tensor cores 100 to 200 cycles.
+#pragma unroll 1
       for (int u = 0; ok && u < n; ++u) {
-        const int kn = (2 * u + 2) % NS, vs = (2 * u + 1) % NS;
-        ok = warp_wait(bFull + 8 * vs, ((2 * u + 1) / NS) & 1, stop);
-        if (ok && u + 1 < n) ok = warp_wait(bFull + 8 * kn, ((2 * u + 2) / NS) & 1, stop);
-        for (int x = 0; ok && x < 2; ++x) {
-          if (visits(x, all.at(u))) {
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const bool now = visits(x, u);
+          if (now) {
             const uint32_t o = tm + 256 + 128 * x, p = tm + 128 * x;
-            const uint32_t v = mnmajor(sKV, kHalf) + vs * (P::kTileBytes >> 4);
+            const uint32_t v = mnmajor(sKV, kHalf) + ((2 * u + 1) % NS) * (P::kTileBytes >> 4);
             if (!(ok = warp_wait(bP + 16 * x, seen[x] & 1, stop))) break;
             fence_after();
             mma_tn<64>(lead, o, p, v, dO, seen[x] > 0);
             if (!(ok = warp_wait(bP + 16 * x + 8, seen[x] & 1, stop))) break;
             fence_after();
             mma_tn<64>(lead, o, p + 32, v + (64 * kPitch >> 4), dO, true);
-            mma_commit(lead, bO + 8 * x);
+            if (u == (x ? hi1 : hi0)) mma_commit(lead, bO + 8 * x);
             ++seen[x];
           }
-          if (u + 1 < n && visits(x, all.at(u + 1))) scores(x, u + 1);
+          if (u + 1 < n && visits(x, u + 1)) {
+            if (!now && !(ok = warp_wait(bFull + 8 * ((2 * u + 2) % NS), ((2 * u + 2) / NS) & 1, stop))) break;
+            scores(x, u + 1);
+          }
         }
-        if (!ok) break;
-        mma_commit(lead, bEmpty + 8 * vs);
-        if (u + 1 < n) mma_commit(lead, bEmpty + 8 * kn);
       }
     }
   } else {
@@ -194,12 +205,30 @@ __global__ void __launch_bounds__(kThreads, 1) window_fwd_kernel(const __grid_co
     const int64_t wlo = g.off + first(x) + (warp % 4) * 32;  // the warp's first and last
     const int64_t whi = wlo + 31;
     float m = -INFINITY, l = 0.f;
-    int k = 0;  // tiles seen
+    int k = 0;     // tiles seen
+    int prev = 0;  // slot of the last one's values
     bool ok = true;
     for (int u = 0; u < n; ++u) {
-      const int64_t t = all.at(u), j0 = t * kRows;
-      if (!visits(x, t)) continue;
+      const int64_t j0 = (int64_t)tile(u) * kRows;
+      const int ks = 2 * u % NS, vs = (2 * u + 1) % NS;
+      if (!visits(x, u)) {  // nothing here for this tile; its slots' earlier uses are over
+        if (warp % 4 == 0) {
+          if (!(ok = warp_wait(bFull + 8 * ks, (2 * u / NS) & 1, stop))) break;
+          if (!(ok = warp_wait(bFull + 8 * vs, ((2 * u + 1) / NS) & 1, stop))) break;
+          if (lane == 0) {
+            bar_arrive(bEmpty + 8 * ks);
+            bar_arrive(bEmpty + 8 * vs);
+          }
+          __syncwarp();
+        }
+        continue;
+      }
       const bool tail = a.cu && j0 + kRows > g.nk;  // the tile holds rows of the next sequence
+      // before the scores come: this tile's values and the next one's keys are there
+      if (warp % 4 == 0) {
+        if (!(ok = warp_wait(bFull + 8 * vs, ((2 * u + 1) / NS) & 1, stop))) break;
+        if (u + 1 < n && !(ok = warp_wait(bFull + 8 * ((2 * u + 2) % NS), ((2 * u + 2) / NS) & 1, stop))) break;
+      }
       if (!(ok = warp_wait(bS + 8 * x, k & 1, stop))) break;
       fence_after();
       const bool whole = j0 + kRows - 1 <= wlo && (whi - j0 < a.W || j0 + kRows <= a.S);
@@ -245,8 +274,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_fwd_kernel(const __grid_co
         const float mn = grow ? top : m;
         const float f = m == mn ? 1.f : fast_exp2(m - mn);
         if (k > 0) {
-          if (!(ok = warp_wait(bO + 8 * x, (k - 1) & 1, stop))) break;
-          fence_after();
+          // (the products into it are done: this tile's scores were issued after them)
 #pragma unroll 1
           for (int i = 0; i < DP / 32; ++i) {
             uint32_t o[32];
@@ -297,7 +325,6 @@ __global__ void __launch_bounds__(kThreads, 1) window_fwd_kernel(const __grid_co
       if (tail) {
         // value rows past the sequence belong to the next one: both roles clear
         // them before their product may start
-        const int vs = (2 * u + 1) % NS;
         if (!(ok = warp_wait(bFull + 8 * vs, ((2 * u + 1) / NS) & 1, stop))) break;
         const int from_row = (int)(g.nk - j0), left = kRows - from_row;
         const uint32_t v = sKV + vs * P::kTileBytes;
@@ -312,11 +339,17 @@ __global__ void __launch_bounds__(kThreads, 1) window_fwd_kernel(const __grid_co
       if (lane == 0) {
         if (tail) bar_arrive(bP + 16 * x);
         bar_arrive(bP + 16 * x + 8);
+        if (warp % 4 == 0) {
+          bar_arrive(bEmpty + 8 * ks);
+          if (k > 0) bar_arrive(bEmpty + 8 * prev);
+        }
       }
+      __syncwarp();
+      prev = vs;
       ++k;
     }
     // ---- o / l to shared memory (the queries' place: their products are done), then out
-    if (ok && k > 0) ok = warp_wait(bO + 8 * x, (k - 1) & 1, stop);
+    if (ok && k > 0) ok = warp_wait(bO + 8 * x, 0, stop);
     if (__all_sync(0xffffffffu, ok)) {
       fence_after();
       const bool some = l > 0.f;
