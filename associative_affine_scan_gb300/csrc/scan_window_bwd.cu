@@ -153,10 +153,12 @@ __global__ void __launch_bounds__(kThreads, 1) window_dkv_kernel(const __grid_co
   uint32_t* const misc = reinterpret_cast<uint32_t*>(gen + (2 + NS) * P::kTileBytes);
   const uint32_t bars = smem_addr(misc);
   const uint32_t bKV = bars, bFull = bars + 8, bEmpty = bFull + 8 * NS, bS = bEmpty + 8 * NS, bDp = bS + 8,
-                 bP = bDp + 8, bDs = bP + 8, bEnd = bDs + 8, bOut = bEnd + 8, bStat = bOut + 16;
+                 bP = bDp + 8, bDs = bP + 8, bEnd = bDs + 8, bOut = bEnd + 8, bLse = bOut + 16,
+                 bDelta = bLse + 8;
   uint32_t* const tmem_ptr = misc + 64;
   uint32_t* const stop_flag = misc + 65;
-  float* const stat = reinterpret_cast<float*>(misc + 72);  // 128 of (lse log2(e), delta)
+  float* const s_lse = reinterpret_cast<float*>(misc + 72);  // lse log2(e) of a tile's queries
+  float* const s_delta = s_lse + kRows;
 
   // which keys: the cut tiles' pieces first, then the others
   const int hk = blockIdx.y % a.Hk, b = blockIdx.y / a.Hk;
@@ -204,7 +206,8 @@ __global__ void __launch_bounds__(kThreads, 1) window_dkv_kernel(const __grid_co
     bar_init(bEnd, 1);
     bar_init(bOut, 4);
     bar_init(bOut + 8, 4);
-    bar_init(bStat, 8);
+    bar_init(bLse, 4);
+    bar_init(bDelta, 4);
     bar_init_fence();
   }
   if (warp == 9) tmem_alloc(smem_addr(tmem_ptr), 512);
@@ -285,28 +288,30 @@ __global__ void __launch_bounds__(kThreads, 1) window_dkv_kernel(const __grid_co
     const int64_t jlo = g.t0 + (warp % 4) * 32, jhi = jlo + 31;  // the warp's keys
     const bool first = j < a.S;
     bool ok = true;
-    // this thread's share of the row statistics: thread t < 128 has query t
-    const auto fetch = [&](int u, float* x, float* y) {
-      const int64_t row = qrow(u) + tid;
-      *x = INFINITY;  // rows past the sequence: p = 0
-      *y = 0.f;
-      if (u < n && tid < kRows && row < g.nq) {
-        const int64_t at = ((int64_t)b * a.Hq + head(u)) * a.Tq + g.qbeg + row;
-        *x = a.lse[at] * 1.44269504088896341f;
-        *y = a.delta[at];
-      }
+    // The queries' statistics, one of each a tile: warpgroup 0 brings the next tile's
+    // lse as soon as every warp has P, warpgroup 1 this tile's delta once dS of the
+    // last is done, both from loads that were issued a tile earlier.
+    int hh = n > 0 ? u0 / per : 0, tt = n > 0 ? u0 % per : 0;  // head and query tile of the next load
+    const auto fetch = [&](bool some) {
+      const int64_t row = (lo + tt) * kRows + r;
+      const bool on = some && row < g.nq;
+      const int64_t at = ((int64_t)b * a.Hq + hk * a.G + hh) * a.Tq + g.qbeg + row;
+      if (++tt == per) tt = 0, ++hh;
+      if (w == 0) return on ? a.lse[at] * 1.44269504088896341f : INFINITY;  // past the sequence: p = 0
+      return on ? a.delta[at] : 0.f;
     };
-    float nx = 0.f, ny = 0.f;
-    if (n > 0) fetch(0, &nx, &ny);
-    for (int u = 0; u < n; ++u) {
-      // the statistics of the last tile have been read by all (they arrived on bDs after)
-      if (u > 0 && !(ok = warp_wait(bDs, (u - 1) & 1, stop))) break;
-      if (tid < kRows) *reinterpret_cast<float2*>(stat + 2 * tid) = make_float2(nx, ny);
+    float stat = fetch(n > 0);
+    if (w == 0 && n > 0) {
+      s_lse[r] = stat;
       __syncwarp();
-      if (lane == 0) bar_arrive(bStat);
-      if (u + 1 < n) fetch(u + 1, &nx, &ny);
-      const int64_t t0 = qrow(u), p0 = g.off + t0 + 64 * w;  // first position of the columns
-      if (!(ok = warp_wait(bStat, u & 1, stop))) break;
+      if (lane == 0) bar_arrive(bLse);
+      __syncwarp();
+      stat = fetch(n > 1);
+    }
+    int64_t t0 = (lo + (n > 0 ? u0 % per : 0)) * kRows;  // first query row of the tile
+    for (int u = 0; u < n; ++u, t0 = t0 + kRows == (lo + per) * kRows ? lo * kRows : t0 + kRows) {
+      const int64_t p0 = g.off + t0 + 64 * w;  // first position of the columns
+      if (!(ok = warp_wait(bLse, u & 1, stop))) break;
       if (!(ok = warp_wait(bS, u & 1, stop))) break;
       fence_after();
       uint32_t s[2][32];
@@ -321,7 +326,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_dkv_kernel(const __grid_co
 #pragma unroll
           for (int c = 0; c < 32; ++c)
             s[i][c] = __float_as_uint(
-                fast_exp2(fmaf(__uint_as_float(s[i][c]), a.sl2, -stat[2 * (64 * w + 32 * i + c)])));
+                fast_exp2(fmaf(__uint_as_float(s[i][c]), a.sl2, -s_lse[64 * w + 32 * i + c])));
       } else {
         const int64_t left = g.nq - t0 - 64 * w - 1;
         int64_t z = first ? 63 : j + a.W - 1 - p0;
@@ -332,7 +337,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_dkv_kernel(const __grid_co
 #pragma unroll
           for (int c = 0; c < 32; ++c) {
             const int x = 32 * i + c;
-            const float e = fast_exp2(fmaf(__uint_as_float(s[i][c]), a.sl2, -stat[2 * (64 * w + x)]));
+            const float e = fast_exp2(fmaf(__uint_as_float(s[i][c]), a.sl2, -s_lse[64 * w + x]));
             s[i][c] = x >= lo_c && x <= hi_c ? __float_as_uint(e) : 0u;
           }
       }
@@ -355,6 +360,21 @@ __global__ void __launch_bounds__(kThreads, 1) window_dkv_kernel(const __grid_co
       fence_before();
       __syncwarp();
       if (lane == 0) bar_arrive(bP);
+      if (w == 0 && u + 1 < n) {
+        if (!(ok = warp_wait(bP, u & 1, stop))) break;
+        s_lse[r] = stat;
+        __syncwarp();
+        if (lane == 0) bar_arrive(bLse);
+        stat = fetch(u + 2 < n);
+      }
+      if (w == 1) {
+        if (u > 0 && !(ok = warp_wait(bDs, (u - 1) & 1, stop))) break;
+        s_delta[r] = stat;
+        __syncwarp();
+        if (lane == 0) bar_arrive(bDelta);
+        stat = fetch(u + 1 < n);
+      }
+      if (!(ok = warp_wait(bDelta, u & 1, stop))) break;
       if (!(ok = warp_wait(bDp, u & 1, stop))) break;
       fence_after();
       uint32_t o[32];
@@ -369,7 +389,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_dkv_kernel(const __grid_co
 #pragma unroll
           for (int y = 0; y < 2; ++y) {
             const float p = __uint_as_float(s[i][c + y]);
-            const float v = p * (__uint_as_float(d[c + y]) - stat[2 * (64 * w + 32 * i + c + y) + 1]);
+            const float v = p * (__uint_as_float(d[c + y]) - s_delta[64 * w + 32 * i + c + y]);
             e[y] = whole || p != 0.f ? v : 0.f;  // what lies outside may be anything
           }
           o[16 * i + c / 2] = pack_bf16(e[0], e[1]);
