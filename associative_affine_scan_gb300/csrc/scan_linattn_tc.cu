@@ -705,21 +705,31 @@ struct Split {
   int nseg, cps, pieces;
 };
 
-// Segments of a row: enough that the blocks fill the SMs once (152, one block
-// each), whole chunks. A row's segments cost a second read of x2 and x3, so rows
-// that fill more than half of the SMs by themselves are left whole. The segments'
-// own states are found in pieces, as many as fill the SMs.
+// Segments of a row, by the time that they would take in chunks of one block (152
+// blocks at a time, two chunks for a block's start and end): more segments fill the
+// SMs and shorten what one block does, but their own states have to be found first
+// from a second read of x2 and x3 (half a chunk's time each, in pieces that fill the
+// SMs as well; three chunks for the two launches). `rows` are the (sequence, head)
+// rows of all passes.
 Split split_rows(int64_t rows, int64_t T) {
   const int64_t nch = (T + kChunk - 1) / kChunk;
-  if (rows <= 0 || rows * 2 > 152 || nch < 4) return Split{1, (int)nch, 1};
-  int64_t n = 152 / rows;
-  if (n > nch / 2) n = nch / 2;
-  const int64_t cps = (nch + n - 1) / n;
-  n = (nch + cps - 1) / cps;
-  int64_t m = n > 1 ? 152 / (rows * (n - 1)) : 1;
-  m = m < 1 ? 1 : m > 64 ? 64 : m;
-  m = m > cps / 2 ? (cps / 2 > 0 ? cps / 2 : 1) : m;
-  return Split{(int)n, (int)cps, (int)m};
+  Split best{1, (int)nch, 1};
+  if (rows <= 0) return best;
+  const auto rounds = [](int64_t blocks) { return (double)((blocks + 151) / 152); };
+  double least = rounds(rows) * (double)(nch + 2);
+  for (int64_t n = 2; n <= 32 && n <= nch / 2; ++n) {
+    const int64_t cps = (nch + n - 1) / n, used = (nch + cps - 1) / cps;
+    if (used != n) continue;
+    for (int64_t m = 1; m <= 8 && m <= cps; ++m) {
+      const double own = rounds(rows * (n - 1) * m) * (double)((cps + m - 1) / m + 2) * 0.5;
+      const double time = rounds(rows * n) * (double)(cps + 2) + own + 3.0;
+      if (time < least) {
+        least = time;
+        best = Split{(int)n, (int)cps, (int)m};
+      }
+    }
+  }
+  return best;
 }
 // Packed sequences, whose lengths the host does not know: segments of one size,
 // such that the row's own number of them, and half a segment more a sequence, fill
@@ -786,14 +796,22 @@ bool linattn_tc_fits(const LinArgs& a, scan_dtype dt) {
 
 size_t linattn_tc_workspace_bytes(int64_t B, int64_t T, int64_t H, int64_t Dk, int64_t Dv,
                                   int64_t n_seqs) {
-  const Split sp = n_seqs > 0 ? split_packed(n_seqs, H, T) : split_rows(B * H, T);
-  const int64_t slots = n_seqs > 0 ? (int64_t)sp.nseg * H : B * H * (sp.nseg - 1) * sp.pieces;
-  return (size_t)(3 * slots * Dk * Dv) * 4;
+  int64_t slots = 0;  // of all passes: three backward, one forward
+  if (n_seqs > 0) {
+    slots = 3 * (int64_t)split_packed(n_seqs, H, T).nseg * H;
+  } else {
+    for (int passes = 1; passes <= 3; passes += 2) {
+      const Split sp = split_rows(B * H * passes, T);
+      const int64_t need = passes * B * H * (sp.nseg - 1) * sp.pieces;
+      slots = need > slots ? need : slots;
+    }
+  }
+  return (size_t)(slots * Dk * Dv) * 4;
 }
 
 cudaError_t launch_linattn_tc(const LinArgs& a, cudaStream_t s) {
   const int64_t n = a.cu ? a.n_seqs : a.B, rows = n * a.H;
-  const Split sp = a.cu ? split_packed(a.n_seqs, a.H, a.T) : split_rows(rows, a.T);
+  const Split sp = a.cu ? split_packed(a.n_seqs, a.H, a.T) : split_rows(rows * a.npass, a.T);
   const int64_t slots = a.cu ? (int64_t)sp.nseg * a.H : rows * (sp.nseg - 1) * sp.pieces;
   TcArgs t[2];
   int count[2] = {0, 0};

@@ -54,7 +54,7 @@ __device__ __forceinline__ uint32_t word(const uint4& v, int i) {
 
 // ROWS: 8 or 16 query heads a block (the fragments' second eight rows are empty at 8).
 template <int DP, int ROWS>
-__global__ void __launch_bounds__(32 * kWarps) window_step_kernel(const WinStepArgs a) {
+__global__ void __launch_bounds__(32 * kWarps, ROWS == 8 ? 3 : 2) window_step_kernel(const WinStepArgs a) {
   using bf16 = __nv_bfloat16;
   constexpr int KK = DP / 32, HALF = DP / 64;
   __shared__ float s_m[kWarps][ROWS], s_l[kWarps][ROWS];
@@ -263,12 +263,17 @@ bool window_step_fits(const WinStepArgs& a, scan_dtype dt) {
   return dt == SCAN_BF16 && aligned16(a.q) && aligned16(a.k) && aligned16(a.v);
 }
 
-// Splits: two blocks an SM or more, as long as a warp still has 16 keys.
+// Splits of a request's keys, by the rounds of blocks that they take (two to three an
+// SM) and the keys of one, with 64 more for a block's start and end.
 cudaError_t launch_window_step(const WinStepArgs& a, int64_t B, cudaStream_t s) {
   const int G = a.Hq / a.Hk, rows = G <= 8 ? 8 : 16;
-  const int64_t blocks = B * a.Hk * ((G + rows - 1) / rows);
+  const int64_t blocks = B * a.Hk * ((G + rows - 1) / rows), slots = (rows == 8 ? 3 : 2) * 152;
   int splits = 1;
-  while (splits < 16 && blocks * splits < 2 * 152 && a.cap >= (int64_t)splits * 2 * 16 * kWarps) splits *= 2;
+  int64_t least = INT64_MAX;
+  for (int n = 1; n <= 16; n *= 2) {
+    const int64_t time = (blocks * n + slots - 1) / slots * ((a.cap + n - 1) / n + 64);
+    if (time < least) least = time, splits = n;
+  }
   if (a.D <= 64) return rows == 8 ? launch_step<64, 8>(a, B, splits, s) : launch_step<64, 16>(a, B, splits, s);
   return rows == 8 ? launch_step<128, 8>(a, B, splits, s) : launch_step<128, 16>(a, B, splits, s);
 }
