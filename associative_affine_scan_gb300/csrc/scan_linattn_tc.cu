@@ -197,17 +197,32 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_co
   const bool packed = a.cu != nullptr;
   const int late = s0 ? 0 : 1;  // the first chunk whose queries read a state
 
-  if (tid < 128) {
-    const int n = s.len % kChunk ? (int)(s.len % kChunk) : kChunk;
-    wtab[tid] = exp2f(l2 * (float)(rev ? tid + 1 : 127 - tid));
-    wlast[tid] = tid < n ? exp2f(l2 * (float)(rev ? tid + 1 : n - 1 - tid)) : 0.f;
-  }
-  if (tid < 64) {
-    const int d = rev ? 32 - tid : tid - 32;
-    dtab[tid] = d >= 0 ? a.scale * exp2f(l2 * (float)d) : 0.f;
-  }
-  if (tid < 32) ctab[tid] = a.scale * exp2f(l2 * (float)(rev ? tid : 31 - tid));
-  if (tid == 0) {
+  // one chunk of x1, x2 and x3 into its stage
+  const auto load12 = [&](int c) {
+    int64_t t0;
+    int n;
+    chunk_at(s, rev, c, &t0, &n);
+    const int st = c % P::kStages, t = (int)(s.beg + t0);
+    const uint32_t d = base + st * P::kStage;
+    bar_expect(bFull12 + 8 * st, P::kX1 + P::kX2);
+#pragma unroll
+    for (int i = 0; i < KP / 64; ++i) {
+      if (!STATE_ONLY) copy_in_4d(d + i * kHalf, &p.x1, bFull12 + 8 * st, 64 * i, h, t, b);
+      copy_in_4d(d + P::kX1 + i * kHalf, &p.x2, bFull12 + 8 * st, 64 * i, h, t, b);
+    }
+  };
+  const auto load3 = [&](int c) {
+    int64_t t0;
+    int n;
+    chunk_at(s, rev, c, &t0, &n);
+    const int st = c % P::kStages, t = (int)(s.beg + t0);
+    bar_expect(bFull3 + 8 * st, P::kX3);
+#pragma unroll
+    for (int i = 0; i < VP / 64; ++i)
+      copy_in_4d(base + st * P::kStage + P::kX1 + P::kX2 + i * kHalf, &p.x3, bFull3 + 8 * st, 64 * i, h, t, b);
+  };
+  // the copy warp sets the barriers up and fills the stages while the others prepare
+  if (warp == 16 && lane == 0) {
     *stop_flag = 0;
     for (int i = 0; i < P::kStages; ++i) {
       bar_init(bFull12 + 8 * i, 1);
@@ -230,7 +245,22 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_co
     bar_init(bClean, 4);
     bar_init(bInit, 4 * (KP / 32));
     bar_init_fence();
+    for (int c = 0; c < P::kStages && c < s.nch; ++c) {
+      load12(c);
+      load3(c);
+    }
   }
+  __syncwarp();
+  if (tid < 128) {
+    const int n = s.len % kChunk ? (int)(s.len % kChunk) : kChunk;
+    wtab[tid] = exp2f(l2 * (float)(rev ? tid + 1 : 127 - tid));
+    wlast[tid] = tid < n ? exp2f(l2 * (float)(rev ? tid + 1 : n - 1 - tid)) : 0.f;
+  }
+  if (tid < 64) {
+    const int d = rev ? 32 - tid : tid - 32;
+    dtab[tid] = d >= 0 ? a.scale * exp2f(l2 * (float)d) : 0.f;
+  }
+  if (tid < 32) ctab[tid] = a.scale * exp2f(l2 * (float)(rev ? tid : 31 - tid));
   if (warp == 17) tmem_alloc(smem_addr(tmem_ptr), 512);
   fence_before();
   __syncthreads();
@@ -286,26 +316,13 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_co
   if (warp == 16) {
     // ---- copies
     if (lane == 0) {
-      for (int c = 0; c < s.nch; ++c) {
+      for (int c = P::kStages; c < s.nch; ++c) {
         const int st = c % P::kStages;
         const uint32_t again = (c / P::kStages - 1) & 1;
-        if (c >= P::kStages && !bar_wait(bFree12 + 8 * st, again, stop)) break;
-        int64_t t0;
-        int n;
-        chunk_at(s, rev, c, &t0, &n);
-        const int t = (int)(s.beg + t0);
-        const uint32_t d = base + st * P::kStage;
-        bar_expect(bFull12 + 8 * st, P::kX1 + P::kX2);
-#pragma unroll
-        for (int i = 0; i < KP / 64; ++i) {
-          if (!STATE_ONLY) copy_in_4d(d + i * kHalf, &p.x1, bFull12 + 8 * st, 64 * i, h, t, b);
-          copy_in_4d(d + P::kX1 + i * kHalf, &p.x2, bFull12 + 8 * st, 64 * i, h, t, b);
-        }
-        if (c >= P::kStages && !bar_wait(bFree3 + 8 * st, again, stop)) break;
-        bar_expect(bFull3 + 8 * st, P::kX3);
-#pragma unroll
-        for (int i = 0; i < VP / 64; ++i)
-          copy_in_4d(d + P::kX1 + P::kX2 + i * kHalf, &p.x3, bFull3 + 8 * st, 64 * i, h, t, b);
+        if (!bar_wait(bFree12 + 8 * st, again, stop)) break;
+        load12(c);
+        if (!bar_wait(bFree3 + 8 * st, again, stop)) break;
+        load3(c);
       }
     }
   } else if (warp == 17) {
@@ -608,25 +625,36 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_co
       // a segment on its own starts from nothing: what came in is added here
       const float in = STATE_ONLY ? s0m * exp2f(l2 * (float)steps) : s0m;
       const bool add = s0 && (STATE_ONLY || s.nch == 0);
+      const bool on = v < p.V;
+      const float* const si = add ? s0 + (on ? v : 0) * s0v : nullptr;
+      float* const so = s1 + v;
 #pragma unroll 1
       for (int kb = 0; kb < KP / 32; ++kb) {
         uint32_t r[32];
         if (s.nch > 0) {
           tmem_ld32(tSt + lanes + 32 * kb, r);
           ld_wait();
+        } else {
+#pragma unroll
+          for (int x = 0; x < 32; ++x) r[x] = 0;
+        }
+        if (add) {
+          float f[32];
+#pragma unroll
+          for (int x = 0; x < 32; ++x) f[x] = si[(32 * kb + x < p.K ? 32 * kb + x : 0) * s0k];
+#pragma unroll
+          for (int x = 0; x < 32; ++x) r[x] = __float_as_uint(fmaf(in, f[x], __uint_as_float(r[x])));
         }
 #pragma unroll
-        for (int x = 0; x < 32; ++x) {
-          const int k = 32 * kb + x;
-          if (v < p.V && k < p.K) {
-            float f = s.nch > 0 ? __uint_as_float(r[x]) : 0.f;
-            if (add) f = fmaf(in, s0[k * s0k + v * s0v], f);
-            s1[(int64_t)k * p.V + v] = s1m * f;
+        for (int x = 0; x < 32; x += 8) {  // K is a multiple of 8
+          if (on && 32 * kb + x < p.K) {
+#pragma unroll
+            for (int y = 0; y < 8; ++y) so[(32 * kb + x + y) * p.V] = s1m * __uint_as_float(r[x + y]);
           }
         }
       }
     }
-    }
+  }
   __syncwarp();
   linger(stop);
   fence_before();

@@ -192,7 +192,16 @@ __global__ void __launch_bounds__(kThreads, 1) window_dkv_kernel(const __grid_co
   const auto head = [&](int u) { return hk * a.G + (u0 + u) / per; };
   const auto qrow = [&](int u) { return (lo + (u0 + u) % per) * kRows; };
 
-  if (tid == 0) {
+  // queries (u even) or output gradients of tile u / 2 into their slot
+  const auto load = [&](int u) {
+    const int sl = u % NS, t = (int)(g.qbeg + qrow(u / 2)), hq = head(u / 2);
+    bar_expect(bFull + 8 * sl, P::kTileBytes);
+#pragma unroll
+    for (int i = 0; i < DP / 64; ++i)
+      copy_in_4d(sR + sl * P::kTileBytes + i * kHalf, u & 1 ? &a.dout : &a.q, bFull + 8 * sl, 64 * i, hq, t, b);
+  };
+  // the copy warp sets the barriers up and starts the first copies while the others prepare
+  if (warp == 8 && lane == 0) {
     *stop_flag = 0;
     bar_init(bKV, 1);
     for (int i = 0; i < NS; ++i) {
@@ -209,7 +218,17 @@ __global__ void __launch_bounds__(kThreads, 1) window_dkv_kernel(const __grid_co
     bar_init(bLse, 4);
     bar_init(bDelta, 4);
     bar_init_fence();
+    if (n > 0) {
+      bar_expect(bKV, 2 * P::kTileBytes);
+#pragma unroll
+      for (int i = 0; i < DP / 64; ++i) {
+        copy_in_4d(sK + i * kHalf, &a.k, bKV, 64 * i, hk, (int)(g.kbeg + g.t0), b);
+        copy_in_4d(sV + i * kHalf, &a.v, bKV, 64 * i, hk, (int)(g.kbeg + g.t0), b);
+      }
+      for (int u = 0; u < NS && u < 2 * n; ++u) load(u);
+    }
   }
+  __syncwarp();
   if (warp == 9) tmem_alloc(smem_addr(tmem_ptr), 512);
   fence_before();
   __syncthreads();
@@ -219,22 +238,10 @@ __global__ void __launch_bounds__(kThreads, 1) window_dkv_kernel(const __grid_co
 
   if (warp == 8) {
     // ---- copies: keys and values once, then queries and output gradients
-    if (lane == 0 && n > 0) {
-      bar_expect(bKV, 2 * P::kTileBytes);
-#pragma unroll
-      for (int i = 0; i < DP / 64; ++i) {
-        copy_in_4d(sK + i * kHalf, &a.k, bKV, 64 * i, hk, (int)(g.kbeg + g.t0), b);
-        copy_in_4d(sV + i * kHalf, &a.v, bKV, 64 * i, hk, (int)(g.kbeg + g.t0), b);
-      }
-      for (int u = 0; u < 2 * n; ++u) {
-        const int sl = u % NS;
-        if (u >= NS && !bar_wait(bEmpty + 8 * sl, (u / NS - 1) & 1, stop)) break;
-        const CUtensorMap* m = u & 1 ? &a.dout : &a.q;
-        bar_expect(bFull + 8 * sl, P::kTileBytes);
-#pragma unroll
-        for (int i = 0; i < DP / 64; ++i)
-          copy_in_4d(sR + sl * P::kTileBytes + i * kHalf, m, bFull + 8 * sl, 64 * i, head(u / 2),
-                     (int)(g.qbeg + qrow(u / 2)), b);
+    if (lane == 0) {
+      for (int u = NS; u < 2 * n; ++u) {
+        if (!bar_wait(bEmpty + 8 * (u % NS), (u / NS - 1) & 1, stop)) break;
+        load(u);
       }
     }
   } else if (warp == 9) {
@@ -508,7 +515,16 @@ __global__ void __launch_bounds__(kThreadsDq, 1) window_dq_kernel(const __grid_c
   const KeyTiles kt = key_tiles(g.off + g.t0, g.off + g.t0 + rows - 1, g.nk, a.W, a.S, kRows);
   const int n = (int)kt.count();
 
-  if (tid == 0) {
+  // keys (u even) or values of tile u / 2 into their slot
+  const auto load = [&](int u) {
+    const int sl = u % NS, t = (int)(g.kbeg + kt.at(u / 2) * kRows);
+    bar_expect(bFull + 8 * sl, P::kTileBytes);
+#pragma unroll
+    for (int i = 0; i < DP / 64; ++i)
+      copy_in_4d(sR + sl * P::kTileBytes + i * kHalf, u & 1 ? &a.v : &a.k, bFull + 8 * sl, 64 * i, hk, t, b);
+  };
+  // the copy warp sets the barriers up and starts the first copies while the others prepare
+  if (warp == 8 && lane == 0) {
     *stop_flag = 0;
     bar_init(bQ, 1);
     for (int i = 0; i < NS; ++i) {
@@ -522,7 +538,17 @@ __global__ void __launch_bounds__(kThreadsDq, 1) window_dq_kernel(const __grid_c
     bar_init(bEnd, 1);
     bar_init(bOut, 4);
     bar_init_fence();
+    if (n > 0) {
+      bar_expect(bQ, 2 * P::kTileBytes);
+#pragma unroll
+      for (int i = 0; i < DP / 64; ++i) {
+        copy_in_4d(sQ + i * kHalf, &a.q, bQ, 64 * i, h, (int)(g.qbeg + g.t0), b);
+        copy_in_4d(sD + i * kHalf, &a.dout, bQ, 64 * i, h, (int)(g.qbeg + g.t0), b);
+      }
+      for (int u = 0; u < NS && u < 2 * n; ++u) load(u);
+    }
   }
+  __syncwarp();
   if (warp == 9) tmem_alloc(smem_addr(tmem_ptr), 512);
   fence_before();
   __syncthreads();
@@ -531,21 +557,10 @@ __global__ void __launch_bounds__(kThreadsDq, 1) window_dq_kernel(const __grid_c
   const Stop stop{stop_flag, a.hdr};
 
   if (warp == 8) {
-    if (lane == 0 && n > 0) {
-      bar_expect(bQ, 2 * P::kTileBytes);
-#pragma unroll
-      for (int i = 0; i < DP / 64; ++i) {
-        copy_in_4d(sQ + i * kHalf, &a.q, bQ, 64 * i, h, (int)(g.qbeg + g.t0), b);
-        copy_in_4d(sD + i * kHalf, &a.dout, bQ, 64 * i, h, (int)(g.qbeg + g.t0), b);
-      }
-      for (int u = 0; u < 2 * n; ++u) {
-        const int sl = u % NS;
-        if (u >= NS && !bar_wait(bEmpty + 8 * sl, (u / NS - 1) & 1, stop)) break;
-        bar_expect(bFull + 8 * sl, P::kTileBytes);
-#pragma unroll
-        for (int i = 0; i < DP / 64; ++i)
-          copy_in_4d(sR + sl * P::kTileBytes + i * kHalf, u & 1 ? &a.v : &a.k, bFull + 8 * sl, 64 * i, hk,
-                     (int)(g.kbeg + kt.at(u / 2) * kRows), b);
+    if (lane == 0) {
+      for (int u = NS; u < 2 * n; ++u) {
+        if (!bar_wait(bEmpty + 8 * (u % NS), (u / NS - 1) & 1, stop)) break;
+        load(u);
       }
     }
   } else if (warp == 9) {

@@ -107,7 +107,16 @@ __global__ void __launch_bounds__(kThreads, 1) window_fwd_kernel(const __grid_co
     return u <= (x ? hi1 : hi0) && (u < sk || u >= (x ? lo1 : lo0));
   };
 
-  if (tid == 0) {
+  // tile u / 2 of the keys (u even) or values into its slot
+  const auto load = [&](int u) {
+    const int sl = u % NS, t = (int)(g.kbeg + (int64_t)tile(u / 2) * kRows);
+    bar_expect(bFull + 8 * sl, P::kTileBytes);
+#pragma unroll
+    for (int i = 0; i < DP / 64; ++i)
+      copy_in_4d(sKV + sl * P::kTileBytes + i * kHalf, u & 1 ? &a.v : &a.k, bFull + 8 * sl, 64 * i, hk, t, b);
+  };
+  // the copy warp sets the barriers up and starts the first copies while the others prepare
+  if (warp == 8 && lane == 0) {
     *stop_flag = 0;
     bar_init(bQ, 1);
     for (int i = 0; i < NS; ++i) {
@@ -122,7 +131,17 @@ __global__ void __launch_bounds__(kThreads, 1) window_fwd_kernel(const __grid_co
       bar_init(bOut + 8 * x, 4);
     }
     bar_init_fence();
+    if (n > 0) {
+      bar_expect(bQ, 2 * P::kTileBytes);
+#pragma unroll
+      for (int x = 0; x < 2; ++x)
+#pragma unroll
+        for (int i = 0; i < DP / 64; ++i)
+          copy_in_4d(sQ + x * P::kTileBytes + i * kHalf, &a.q, bQ, 64 * i, head(x), (int)(g.qbeg + first(x)), b);
+      for (int u = 0; u < NS && u < 2 * n; ++u) load(u);
+    }
   }
+  __syncwarp();
   if (warp == 9) tmem_alloc(smem_addr(tmem_ptr), 512);
   fence_before();
   __syncthreads();
@@ -132,22 +151,10 @@ __global__ void __launch_bounds__(kThreads, 1) window_fwd_kernel(const __grid_co
 
   if (warp == 8) {
     // ---- copies
-    if (lane == 0 && n > 0) {
-      bar_expect(bQ, 2 * P::kTileBytes);
-#pragma unroll
-      for (int x = 0; x < 2; ++x)
-#pragma unroll
-        for (int i = 0; i < DP / 64; ++i)
-          copy_in_4d(sQ + x * P::kTileBytes + i * kHalf, &a.q, bQ, 64 * i, head(x), (int)(g.qbeg + first(x)), b);
-      for (int u = 0; u < 2 * n; ++u) {
-        const int sl = u % NS;
-        if (u >= NS && !bar_wait(bEmpty + 8 * sl, (u / NS - 1) & 1, stop)) break;
-        const CUtensorMap* m = u & 1 ? &a.v : &a.k;
-        const int t = (int)(g.kbeg + (int64_t)tile(u / 2) * kRows);
-        bar_expect(bFull + 8 * sl, P::kTileBytes);
-#pragma unroll
-        for (int i = 0; i < DP / 64; ++i)
-          copy_in_4d(sKV + sl * P::kTileBytes + i * kHalf, m, bFull + 8 * sl, 64 * i, hk, t, b);
+    if (lane == 0) {
+      for (int u = NS; u < 2 * n; ++u) {
+        if (!bar_wait(bEmpty + 8 * (u % NS), (u / NS - 1) & 1, stop)) break;
+        load(u);
       }
     }
   } else if (warp == 9) {
