@@ -2,13 +2,15 @@
 // ring of cached keys and values (bf16 caches).
 //
 // Bound by DRAM: each cached row is read once for the query heads that share it
-// (4 G multiply-adds a byte pair at most). A warp takes 16 keys at a time: all of
-// its 16-byte loads of their K and V rows go out together, 8 KB a warp, then two
-// sets of m16n8k16 products: scores of up to 16 query heads (the rows) by 16 keys,
-// and weights by V. The sums' index order is free, so each fragment is what a
-// thread loaded 16 bytes of: the scores' index runs over the D elements in the
-// order that a row's quarter-warp chunks have, and the columns of the output are
-// the elements in the order 8 n + j. Fragments of V pair two keys' elements.
+// (4 G multiply-adds a byte pair at most). A warp takes 16 keys at a time, by 16-byte
+// loads; the next keys' are issued when these have been used and the next values' when
+// these have, so 4 to 8 KB a warp are always on their way. Two sets of m16n8k16
+// products: scores of up to 16 query heads (the rows) by 16 keys, and weights by V.
+// The sums' index order is free, so each fragment is what a thread loaded 16 bytes
+// of: the scores' index runs over the D elements in the order of the four lanes'
+// pieces, and the columns of the output are the elements in the order 8 n + j.
+// Fragments of V pair two keys' elements. The warps of a block take different key
+// heads of the same keys where there are several (neighbours in the cache).
 //
 // A request's keys are split over the blocks of a cluster (up to 16) when the
 // requests alone do not fill the SMs; the partial maxima, sums and outputs meet
@@ -52,28 +54,33 @@ __device__ __forceinline__ uint32_t word(const uint4& v, int i) {
   return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
 }
 
-// ROWS: 8 or 16 query heads a block (the fragments' second eight rows are empty at 8).
-template <int DP, int ROWS>
+// ROWS: 8 or 16 query heads a warp (the fragments' second eight rows are empty at 8).
+// WH: key heads a block; the other warps share a head's keys.
+template <int DP, int ROWS, int WH>
 __global__ void __launch_bounds__(32 * kWarps, ROWS == 8 ? 3 : 2) window_step_kernel(const WinStepArgs a) {
   using bf16 = __nv_bfloat16;
-  constexpr int KK = DP / 32, HALF = DP / 64;
+  constexpr int KK = DP / 32, HALF = DP / 64, WK = kWarps / WH;
   __shared__ float s_m[kWarps][ROWS], s_l[kWarps][ROWS];
   __shared__ float s_o[kWarps][ROWS][DP];
-  __shared__ float b_m[ROWS], b_l[ROWS];
+  __shared__ float b_m[WH][ROWS], b_l[WH][ROWS];
   cg::cluster_group cluster = cg::this_cluster();
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
   const int g = lane / 4, c = lane % 4;
   const int split = blockIdx.x, splits = gridDim.x;
   const int G = a.Hq / a.Hk, tiles = (G + ROWS - 1) / ROWS;
-  const int hk = blockIdx.y / tiles, r0 = (blockIdx.y % tiles) * ROWS;  // heads r0.. of the group
+  const int wh = warp % WH, wk = warp / WH;  // this warp's key head, and its share of the keys
+  const int hk0 = blockIdx.y / tiles * WH, hk = hk0 + wh, r0 = (blockIdx.y % tiles) * ROWS;  // heads r0.. of the group
   const int rows = G - r0 < ROWS ? G - r0 : ROWS;
   const int64_t b = blockIdx.z;
   const int64_t slot = a.slots ? (int64_t)a.slots[b] : b, pos = a.pos[b];
-  bf16* const o = static_cast<bf16*>(a.o.ptr) + b * a.o.stride_b + ((int64_t)hk * G + r0) * a.o.stride_h;
+  // output row r of key head x of the block
+  const auto out = [&](int x, int r) {
+    return static_cast<bf16*>(a.o.ptr) + b * a.o.stride_b + ((int64_t)(hk0 + x) * G + r0 + r) * a.o.stride_h;
+  };
   if (slot < 0 || slot >= a.n_slots || pos < 0) {  // an idle request (the whole cluster)
     if (split == 0)
-      for (int i = threadIdx.x; i < rows * a.D; i += 32 * kWarps)
-        o[(i / a.D) * a.o.stride_h + i % a.D] = __float2bfloat16_rn(0.f);
+      for (int i = threadIdx.x; i < WH * rows * a.D; i += 32 * kWarps)
+        out(i / a.D / rows, i / a.D % rows)[i % a.D] = __float2bfloat16_rn(0.f);
     return;
   }
   const int64_t at = pos < a.S ? pos : a.S + (pos - a.S) % a.W;
@@ -84,8 +91,8 @@ __global__ void __launch_bounds__(32 * kWarps, ROWS == 8 ? 3 : 2) window_step_ke
   const bf16* const kn = static_cast<const bf16*>(a.k.ptr) + b * a.k.stride_b + hk * a.k.stride_h;
   const bf16* const vn = static_cast<const bf16*>(a.v.ptr) + b * a.v.stride_b + hk * a.v.stride_h;
   // the new token joins the cache; its row is read from k and v, never from there
-  if (split == 0 && r0 == 0)
-    for (int i = threadIdx.x; i < a.D; i += 32 * kWarps) kc[at * row + i] = kn[i], vc[at * row + i] = vn[i];
+  if (split == 0 && r0 == 0 && wk == 0)
+    for (int i = lane; i < a.D; i += 32) kc[at * row + i] = kn[i], vc[at * row + i] = vn[i];
 
   // queries as the left operand: rows g and g + 8
   uint4 q[KK], q8[KK];
@@ -110,23 +117,30 @@ __global__ void __launch_bounds__(32 * kWarps, ROWS == 8 ? 3 : 2) window_step_ke
 
   const int64_t groups = (n + 15) / 16, per = (groups + splits - 1) / splits;
   const int64_t first = split * per, last = first + per < groups ? first + per : groups;
-  for (int64_t t = first + warp; t < last; t += kWarps) {
-    const int64_t j0 = t * 16;
-    uint4 kv[2][KK], vv[4][HALF];
+  uint4 kv[2][KK], vv[4][HALF];
+  const auto load_k = [&](int64_t t) {
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
-      const int64_t j = j0 + 8 * x + g;
+      const int64_t j = t * 16 + 8 * x + g;
       const bf16* p = j == at ? kn : kc + j * row;
 #pragma unroll
-      for (int k = 0; k < KK; ++k) kv[x][k] = ld16(p + 32 * k + 8 * c, j < n && 32 * k + 8 * c < a.D);
+      for (int k = 0; k < KK; ++k) kv[x][k] = ld16(p + 32 * k + 8 * c, t < last && j < n && 32 * k + 8 * c < a.D);
     }
+  };
+  const auto load_v = [&](int64_t t) {
 #pragma unroll
     for (int x = 0; x < 4; ++x) {
-      const int64_t j = j0 + 2 * c + (x & 1) + 8 * (x >> 1);
+      const int64_t j = t * 16 + 2 * c + (x & 1) + 8 * (x >> 1);
       const bf16* p = j == at ? vn : vc + j * row;
 #pragma unroll
-      for (int h = 0; h < HALF; ++h) vv[x][h] = ld16(p + 64 * h + 8 * g, j < n && 64 * h + 8 * g < a.D);
+      for (int h = 0; h < HALF; ++h) vv[x][h] = ld16(p + 64 * h + 8 * g, t < last && j < n && 64 * h + 8 * g < a.D);
     }
+  };
+  load_k(first + wk);
+  load_v(first + wk);
+#pragma unroll 1
+  for (int64_t t = first + wk; t < last; t += WK) {
+    const int64_t j0 = t * 16;
     float s[2][4];
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
@@ -138,6 +152,7 @@ __global__ void __launch_bounds__(32 * kWarps, ROWS == 8 ? 3 : 2) window_step_ke
         mma16816(s[x], q[k].z, q8[k].z, q[k].w, q8[k].w, kv[x][k].z, kv[x][k].w);
       }
     }
+    load_k(t + WK);  // on its way while the weights are taken and used
     // s[x][y], s[x][2 + y]: heads g and g + 8, key j0 + 8 x + 2 c + y
 #pragma unroll
     for (int x = 0; x < 2; ++x)
@@ -177,6 +192,7 @@ __global__ void __launch_bounds__(32 * kWarps, ROWS == 8 ? 3 : 2) window_step_ke
         mma16816(acc[i][j], a0, a1, a2, a3, __byte_perm(word(vv[0][i], j / 2), word(vv[1][i], j / 2), sel),
                  __byte_perm(word(vv[2][i], j / 2), word(vv[3][i], j / 2), sel));
       }
+    load_v(t + WK);
   }
   // the warps' parts, then the block's
 #pragma unroll
@@ -193,49 +209,49 @@ __global__ void __launch_bounds__(32 * kWarps, ROWS == 8 ? 3 : 2) window_step_ke
       }
   }
   __syncthreads();
-  for (int i = threadIdx.x; i < ROWS * DP; i += 32 * kWarps) {
-    const int r = i / DP, d = i % DP;
-    float top = s_m[0][r];
+  for (int i = threadIdx.x; i < WH * ROWS * DP; i += 32 * kWarps) {
+    const int x = i / DP / ROWS, r = i / DP % ROWS, d = i % DP;
+    float top = s_m[x][r];
 #pragma unroll
-    for (int w = 1; w < kWarps; ++w) top = fmaxf(top, s_m[w][r]);
+    for (int w = 1; w < WK; ++w) top = fmaxf(top, s_m[x + w * WH][r]);
     const float from = top == -INFINITY ? 0.f : top;
     float sum = 0.f, e = 0.f;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      const float f = ex2(s_m[w][r] - from);
-      sum = fmaf(s_l[w][r], f, sum);
-      e = fmaf(s_o[w][r][d], f, e);
+    for (int w = 0; w < WK; ++w) {
+      const float f = ex2(s_m[x + w * WH][r] - from);
+      sum = fmaf(s_l[x + w * WH][r], f, sum);
+      e = fmaf(s_o[x + w * WH][r][d], f, e);
     }
     if (splits == 1) {
-      if (r < rows && d < a.D) o[r * a.o.stride_h + d] = __float2bfloat16_rn(e / sum);
+      if (r < rows && d < a.D) out(x, r)[d] = __float2bfloat16_rn(e / sum);
     } else {
-      s_o[0][r][d] = e;  // read by no other thread
-      if (d == 0) b_m[r] = top, b_l[r] = sum;
+      s_o[x][r][d] = e;  // read by no other thread
+      if (d == 0) b_m[x][r] = top, b_l[x][r] = sum;
     }
   }
   if (splits == 1) return;
   // the cluster's parts: rank by rank, each block a share of the outputs
   cluster.sync();
-  for (int i = split * 32 * kWarps + threadIdx.x; i < rows * DP; i += splits * 32 * kWarps) {
-    const int r = i / DP, d = i % DP;
+  for (int i = split * 32 * kWarps + threadIdx.x; i < WH * rows * DP; i += splits * 32 * kWarps) {
+    const int x = i / DP / rows, r = i / DP % rows, d = i % DP;
     float top = -INFINITY;
-    for (int k = 0; k < splits; ++k) top = fmaxf(top, *cluster.map_shared_rank(&b_m[r], k));
+    for (int k = 0; k < splits; ++k) top = fmaxf(top, *cluster.map_shared_rank(&b_m[x][r], k));
     float sum = 0.f, e = 0.f;
     for (int k = 0; k < splits; ++k) {
-      const float f = ex2(*cluster.map_shared_rank(&b_m[r], k) - top);
-      sum = fmaf(*cluster.map_shared_rank(&b_l[r], k), f, sum);
-      e = fmaf(*cluster.map_shared_rank(&s_o[0][r][d], k), f, e);
+      const float f = ex2(*cluster.map_shared_rank(&b_m[x][r], k) - top);
+      sum = fmaf(*cluster.map_shared_rank(&b_l[x][r], k), f, sum);
+      e = fmaf(*cluster.map_shared_rank(&s_o[x][r][d], k), f, e);
     }
-    if (d < a.D) o[r * a.o.stride_h + d] = __float2bfloat16_rn(e / sum);
+    if (d < a.D) out(x, r)[d] = __float2bfloat16_rn(e / sum);
   }
   cluster.sync();  // no block leaves while its part may be read
 }
 
-template <int DP, int ROWS>
+template <int DP, int ROWS, int WH>
 cudaError_t launch_step(const WinStepArgs& a, int64_t B, int splits, cudaStream_t s) {
   const int G = a.Hq / a.Hk, tiles = (G + ROWS - 1) / ROWS;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(splits, (unsigned)(a.Hk * tiles), (unsigned)B);
+  cfg.gridDim = dim3(splits, (unsigned)(a.Hk / WH * tiles), (unsigned)B);
   cfg.blockDim = dim3(32 * kWarps);
   cfg.stream = s;
   cudaLaunchAttribute at[1];
@@ -245,11 +261,11 @@ cudaError_t launch_step(const WinStepArgs& a, int64_t B, int splits, cudaStream_
   cfg.attrs = at;
   cfg.numAttrs = 1;
   if (splits > 8) {
-    const cudaError_t e = cudaFuncSetAttribute(window_step_kernel<DP, ROWS>,
+    const cudaError_t e = cudaFuncSetAttribute(window_step_kernel<DP, ROWS, WH>,
                                                cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return e;
   }
-  return cudaLaunchKernelEx(&cfg, window_step_kernel<DP, ROWS>, a);
+  return cudaLaunchKernelEx(&cfg, window_step_kernel<DP, ROWS, WH>, a);
 }
 
 // Rows of 16-byte pieces that this kernel's loads can address.
@@ -263,19 +279,31 @@ bool window_step_fits(const WinStepArgs& a, scan_dtype dt) {
   return dt == SCAN_BF16 && aligned16(a.q) && aligned16(a.k) && aligned16(a.v);
 }
 
-// Splits of a request's keys, by the rounds of blocks that they take (two to three an
-// SM) and the keys of one, with 64 more for a block's start and end.
+namespace {
+
+template <int DP, int ROWS>
+cudaError_t launch_heads(const WinStepArgs& a, int64_t B, int wh, int splits, cudaStream_t s) {
+  if (wh == 4) return launch_step<DP, ROWS, 4>(a, B, splits, s);
+  if (wh == 2) return launch_step<DP, ROWS, 2>(a, B, splits, s);
+  return launch_step<DP, ROWS, 1>(a, B, splits, s);
+}
+
+}  // namespace
+
+// Splits of a request's keys: as many as stay resident at once (two to three blocks
+// an SM, on 128 of the SMs: clusters do not fill every group of SMs), as long as a
+// warp has two steps of 16 keys. 64 requests of 4100 keys and 4 key heads, in us by
+// splits: 332 (1), 184, 141, 114, 120, 111 (6), 138 (7: a second round of clusters).
 cudaError_t launch_window_step(const WinStepArgs& a, int64_t B, cudaStream_t s) {
-  const int G = a.Hq / a.Hk, rows = G <= 8 ? 8 : 16;
-  const int64_t blocks = B * a.Hk * ((G + rows - 1) / rows), slots = (rows == 8 ? 3 : 2) * 152;
-  int splits = 1;
-  int64_t least = INT64_MAX;
-  for (int n = 1; n <= 16; n *= 2) {
-    const int64_t time = (blocks * n + slots - 1) / slots * ((a.cap + n - 1) / n + 64);
-    if (time < least) least = time, splits = n;
-  }
-  if (a.D <= 64) return rows == 8 ? launch_step<64, 8>(a, B, splits, s) : launch_step<64, 16>(a, B, splits, s);
-  return rows == 8 ? launch_step<128, 8>(a, B, splits, s) : launch_step<128, 16>(a, B, splits, s);
+  const int G = a.Hq / a.Hk, rows = G <= 8 ? 8 : 16, wh = a.Hk % 4 == 0 ? 4 : a.Hk % 2 == 0 ? 2 : 1;
+  const int64_t blocks = B * (a.Hk / wh) * ((G + rows - 1) / rows), slots = (rows == 8 ? 3 : 2) * 128;
+  int64_t n = slots / blocks;
+  const int64_t most = a.cap / (2 * 16 * (kWarps / wh));
+  n = n > most ? most : n;
+  const int splits = (int)(n < 1 ? 1 : n > 16 ? 16 : n);
+  if (a.D <= 64)
+    return rows == 8 ? launch_heads<64, 8>(a, B, wh, splits, s) : launch_heads<64, 16>(a, B, wh, splits, s);
+  return rows == 8 ? launch_heads<128, 8>(a, B, wh, splits, s) : launch_heads<128, 16>(a, B, wh, splits, s);
 }
 
 }  // namespace scan
