@@ -213,7 +213,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_fwd_kernel(const __grid_co
     const int64_t whi = wlo + 31;
     float m = -INFINITY, l = 0.f;
     int k = 0;     // tiles seen
-    int prev = 0;  // slot of the last one's values
+    int prev = 0, prev_u = 0;  // slot of the last one's values, and its number
     bool ok = true;
     for (int u = 0; u < n; ++u) {
       const int64_t j0 = (int64_t)tile(u) * kRows;
@@ -231,13 +231,24 @@ __global__ void __launch_bounds__(kThreads, 1) window_fwd_kernel(const __grid_co
         continue;
       }
       const bool tail = a.cu && j0 + kRows > g.nk;  // the tile holds rows of the next sequence
-      // before the scores come: this tile's values and the next one's keys are there
+      // Before the scores come: this tile's values and the next one's keys are there.
+      // After a tile that was passed over, the slot of the values before it may be what
+      // the next keys wait for: it is given back first, once the scores say that it can be.
+      const bool passed = k > 0 && prev_u != u - 1;
+      const auto next_keys = [&]() {
+        return u + 1 >= n || warp_wait(bFull + 8 * ((2 * u + 2) % NS), ((2 * u + 2) / NS) & 1, stop);
+      };
       if (warp % 4 == 0) {
         if (!(ok = warp_wait(bFull + 8 * vs, ((2 * u + 1) / NS) & 1, stop))) break;
-        if (u + 1 < n && !(ok = warp_wait(bFull + 8 * ((2 * u + 2) % NS), ((2 * u + 2) / NS) & 1, stop))) break;
+        if (!passed && !(ok = next_keys())) break;
       }
       if (!(ok = warp_wait(bS + 8 * x, k & 1, stop))) break;
       fence_after();
+      if (passed && warp % 4 == 0) {
+        if (lane == 0) bar_arrive(bEmpty + 8 * prev);
+        __syncwarp();
+        if (!(ok = next_keys())) break;
+      }
       const bool whole = j0 + kRows - 1 <= wlo && (whi - j0 < a.W || j0 + kRows <= a.S);
       if (!whole) {  // what this row does not see becomes -inf where it lies
         const int lo = clamp_col(pos - a.W + 1 - j0), hi = clamp_col(pos - j0), sk = clamp_col(a.S - j0);
@@ -348,11 +359,12 @@ __global__ void __launch_bounds__(kThreads, 1) window_fwd_kernel(const __grid_co
         bar_arrive(bP + 16 * x + 8);
         if (warp % 4 == 0) {
           bar_arrive(bEmpty + 8 * ks);
-          if (k > 0) bar_arrive(bEmpty + 8 * prev);
+          if (k > 0 && !passed) bar_arrive(bEmpty + 8 * prev);
         }
       }
       __syncwarp();
       prev = vs;
+      prev_u = u;
       ++k;
     }
     // ---- o / l to shared memory (the queries' place: their products are done), then out

@@ -344,6 +344,15 @@ def test_window_heads(lib, dtype, Hq, Hk, D):
     win_check(lib, win_inputs(2, 200, 200, Hq, Hk, D, dtype, Hq + D), 70, 4, scale=0.2)
 
 
+@pytest.mark.parametrize("Hq,Hk", [(1, 1), (3, 1), (4, 2)])
+@pytest.mark.parametrize("W,S", [(16, 1), (100, 4), (129, 16), (300, 4), (150, 300)])
+def test_window_first_tokens_and_gaps(lib, Hq, Hk, W, S):
+    """Rows long enough that first tokens and window lie tiles apart, heads of 128
+    in blocks of one and of two heads: tiles that one query tile passes over."""
+    for Tq, Tk in ((900, 900), (513, 1100)):
+        win_check(lib, win_inputs(1, Tq, Tk, Hq, Hk, 128, BF, W + S + Hq), W, S)
+
+
 @pytest.mark.parametrize("dtype", [BF, F32])
 @pytest.mark.parametrize("Tq,Tk", [(1, 300), (100, 300), (130, 257), (300, 100), (5, 0), (0, 5), (200, 1)])
 def test_window_fewer_or_more_queries_than_keys(lib, dtype, Tq, Tk):
