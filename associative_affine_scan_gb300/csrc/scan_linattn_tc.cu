@@ -117,7 +117,8 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_co
                  bP = bars + 136, bSb = bars + 144, bSt = bars + 152, bX = bars + 160, bXf = bars + 192,
                  bOi = bars + 224, bOs = bars + 232, bOf = bars + 240, bOx = bars + 248, bClean = bars + 256,
                  bInit = bars + 264;
-  constexpr int kBufs = STATE_ONLY ? 4 : 2;  // of 32 steps of the update's operand
+  // places for 32 steps of the update's operand: half a chunk, or two whole ones
+  constexpr int kBufs = STATE_ONLY ? 8 : 2;
   uint32_t* const tmem_ptr = reinterpret_cast<uint32_t*>(tab + 352) + 72;
   uint32_t* const stop_flag = tmem_ptr + 1;
 
@@ -230,8 +231,8 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_co
       bar_init(bFree12 + 8 * i, 1);
       bar_init(bFree3 + 8 * i, 1);
     }
-    for (int i = 0; i < kBufs; ++i) {
-      bar_init(bX + 8 * i, 4);
+    for (int i = 0; i < 2; ++i) {
+      bar_init(bX + 8 * i, STATE_ONLY ? 16 : 4);
       bar_init(bXf + 8 * i, 1);
     }
     bar_init(bS1, 1);
@@ -358,25 +359,33 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_co
         else if (s0) ok = warp_wait(bInit, 0, stop);
         if (!ok) break;
         fence_after();
-        // the update's four pieces; two of them wait for the first two to be used, so the
-        // state is read in between
+        // Each wait or commit of this warp costs the tensor cores 100 to 200 cycles, so
+        // what a role hands over also says that the copies it has waited for are there,
+        // and roles give operands back. The update's operand comes in halves of a chunk;
+        // the second waits for the first to be used, so the state is read in between.
         const bool more = c + 1 < s.nch || s1;
-        const auto piece = [&](int jb) {
-          const int buf = jb % kBufs;
-          if (!warp_wait(bX + 8 * buf, (STATE_ONLY ? c : jb >> 1) & 1, stop)) return false;
-          fence_after();
-          mma_tn<32>(lead, tSt, tX + 32 * buf, x2 + jb * (32 * kPitch >> 4), dSt, have || jb > 0);
-          mma_tn<32>(lead, tSt, tX + 32 * buf + 16, x2 + jb * (32 * kPitch >> 4), dSt, true);
-          mma_commit(lead, bXf + 8 * buf);
-          return true;
+        const auto piece = [&](int jb, uint32_t at) {
+          mma_tn<32>(lead, tSt, at, x2 + jb * (32 * kPitch >> 4), dSt, have || jb > 0);
+          mma_tn<32>(lead, tSt, at + 16, x2 + jb * (32 * kPitch >> 4), dSt, true);
         };
-        if (more && !(ok = piece(0) && piece(1))) break;
         if (STATE_ONLY) {
-          if (!(ok = piece(2) && piece(3))) break;
+          const int set = c & 1;
+          if (!(ok = warp_wait(bX + 8 * set, (c >> 1) & 1, stop))) break;
+          fence_after();
+#pragma unroll
+          for (int jb = 0; jb < 4; ++jb) piece(jb, tX + 128 * set + 32 * jb);
+          mma_commit(lead, bXf + 8 * set);
           mma_commit(lead, bFree12 + 8 * st);
           mma_commit(lead, bFree3 + 8 * st);
           if (c + 1 == s.nch) mma_commit(lead, bSt);
           continue;
+        }
+        if (more) {
+          if (!(ok = warp_wait(bX, c & 1, stop))) break;
+          fence_after();
+          piece(0, tX);
+          piece(1, tX + 32);
+          mma_commit(lead, bXf);
         }
         if (c > 0 && !(ok = warp_wait(bOx, (c - 1) & 1, stop))) break;
         fence_after();
@@ -384,21 +393,24 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_co
           mma_kk<KP, kHalf, VP * kPitch>(lead, tO, x1, kmajor(sState), dOi, false);
           mma_commit(lead, bOi);
         }
-        if (more && !(ok = piece(2) && piece(3))) break;
+        if (more) {
+          if (!(ok = warp_wait(bX + 8, c & 1, stop))) break;
+          fence_after();
+          piece(2, tX);
+          piece(3, tX + 32);
+        } else if (!(ok = warp_wait(bFull3 + 8 * st, (c / P::kStages) & 1, stop))) {
+          break;
+        }
         mma_commit(lead, bSt);
-        mma_commit(lead, bFree12 + 8 * st);
         if (!(ok = warp_wait(bP, c & 1, stop))) break;
         if (c + 1 < s.nch) {
-          if (!(ok = ready(c + 1))) break;
           fence_after();
           scores(c + 1);
         }
         if (have && !(ok = warp_wait(bOs, (c - late) & 1, stop))) break;
-        if (!(ok = warp_wait(bFull3 + 8 * st, (c / P::kStages) & 1, stop))) break;
         fence_after();
         mma_tn<kChunk>(lead, tO, tP, x3, dO, have);
         mma_commit(lead, bOf);
-        mma_commit(lead, bFree3 + 8 * st);
       }
     }
   } else if (role == 0 && !STATE_ONLY) {
@@ -448,6 +460,13 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_co
       if (!ok) break;
       st_wait();
       fence_before();
+      if (w == 0 && c + 1 < s.nch) {  // the next chunk's x1 and x2 are there
+        int64_t t0;
+        int n;
+        chunk_at(s, rev, c + 1, &t0, &n);
+        if (!warp_wait(bFull12 + 8 * ((c + 1) % P::kStages), ((c + 1) / P::kStages) & 1, stop)) break;
+        if (packed && n < kChunk && !warp_wait(bClean, 0, stop)) break;
+      }
       __syncwarp();
       if (lane == 0) bar_arrive(bP);
     }
@@ -461,6 +480,8 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_co
       const float keep = exp2f(l2 * (float)n);
       if (!warp_wait(bSt, (c - 1) & 1, stop)) break;
       fence_after();
+      if (warp == 4 && lane == 0) bar_arrive(bFree12 + 8 * ((c - 1) % P::kStages));  // all their products are done
+      __syncwarp();
 #pragma unroll 1
       for (int kb = 0; kb < KP / 32; ++kb) {
         uint32_t r[32];
@@ -540,17 +561,24 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_co
             }
           }
         }
-        const int buf = jb % kBufs, use = STATE_ONLY ? c : 2 * c + (jb >> 1);  // the buffer's use-th time
-        if (use > 0 && !(ok = warp_wait(bXf + 8 * buf, (use - 1) & 1, stop))) break;
+        // the place's last use is over
+        if (STATE_ONLY) ok = c < 2 || warp_wait(bXf + 8 * (c & 1), ((c >> 1) - 1) & 1, stop);
+        else if (jb == 0) ok = c == 0 || warp_wait(bSt, (c - 1) & 1, stop);
+        else if (jb == 2) ok = warp_wait(bXf, c & 1, stop);
+        if (!ok) break;
         fence_after();
+        const uint32_t at = tX + (STATE_ONLY ? 128 * (c & 1) + 32 * jb : 32 * (jb & 1)) + lanes;
         if (v < VP) {
-          tmem_st16(tX + 32 * buf + lanes, hi);
-          tmem_st16(tX + 32 * buf + 16 + lanes, lo);
+          tmem_st16(at, hi);
+          tmem_st16(at + 16, lo);
           st_wait();
         }
-        fence_before();
-        __syncwarp();
-        if (lane == 0) bar_arrive(bX + 8 * buf);
+        if (STATE_ONLY || (jb & 1)) {
+          fence_before();
+          __syncwarp();
+          if (lane == 0) bar_arrive(bX + 8 * (STATE_ONLY ? c & 1 : jb >> 1));
+          __syncwarp();
+        }
       }
     }
   } else if (role == 3 && !STATE_ONLY) {
@@ -582,6 +610,8 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_co
       }
       if (!warp_wait(bOf, c & 1, stop)) break;
       fence_after();
+      if (i == 0) bar_arrive(bFree3 + 8 * (c % P::kStages));
+      __syncwarp();
       __nv_bfloat16* const orow = p.o + b * p.o_sb + (s.beg + t0 + i) * p.o_st + h * p.o_sh;
 #pragma unroll 1
       for (int vb = 0; vb < VP / 32; ++vb) {
