@@ -13,12 +13,12 @@
 // SM), each working on its own part of the chain at any time:
 //   copy warp     two to four chunks of x1, x2, x3 in flight
 //   product warp  S1 = x1 x2^T, O = x1 S, S^T += x3'^T x2, O += P x3
-//   weights       P = S1 * lambda^(r - r'), masked, to bf16
+//   weights       P = S1 * lambda^(r - r'), masked, to bf16 over S1
 //   state         S^T to bf16 for the next chunk's x1 S, and S^T *= lambda^n
-//   update        x3'^T = lambda^(n - e - r') x3^T as hi + lo bf16 parts, 32 steps
-//                 at a time: the state's update is then exact to 2^-17, so that the
-//                 state (fp32 in tensor memory) keeps fp32 accuracy over any number
-//                 of chunks
+//   update        x3'^T = lambda^(n - e - r') x3^T as the sum of two bf16 parts (three
+//                 where the state is an output), 32 steps at a time: the state's
+//                 update is then exact to 2^-17 (2^-24), so that the state, fp32 in
+//                 tensor memory, keeps that accuracy over any number of chunks
 //   output        O *= lambda^(r + e) between the two products into it; O to bf16
 // The state lies transposed (lanes are v): its bf16 copy is then written by rows
 // into the operand layout, and the weighted operand of the update is one that the
@@ -267,8 +267,13 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_co
   __syncthreads();
   fence_after();
   const uint32_t tm = *tmem_ptr;
-  // tensor memory: S1, P, two 32-step pieces of the update's operand (hi, lo), O, S^T
-  const uint32_t tS1 = tm, tP = tm + 128, tX = STATE_ONLY ? tm : tm + 192, tO = tm + 256, tSt = tm + 384;
+  // tensor memory: S1 (P over its first half), the update's pieces of 32 steps (two or
+  // three bf16 parts of 16 columns each), O, S^T
+  const uint32_t tS1 = tm, tX = STATE_ONLY ? tm : tm + 128, tO = tm + 256, tSt = tm + 384;
+  constexpr int kPiece = 48;
+  // two parts carry the state to 2^-17 a step, which the bf16 outputs never show; a
+  // state that is an output itself gets three
+  const bool three = p.s_out != nullptr;
   const uint32_t lanes = (uint32_t)(warp % 4) << 21;  // this warp's first tensor-memory lane
   const Stop stop{stop_flag, a.hdr};
   const int role = warp / 4;
@@ -367,13 +372,14 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_co
         const auto piece = [&](int jb, uint32_t at) {
           mma_tn<32>(lead, tSt, at, x2 + jb * (32 * kPitch >> 4), dSt, have || jb > 0);
           mma_tn<32>(lead, tSt, at + 16, x2 + jb * (32 * kPitch >> 4), dSt, true);
+          if (three) mma_tn<32>(lead, tSt, at + 32, x2 + jb * (32 * kPitch >> 4), dSt, true);
         };
         if (STATE_ONLY) {
           const int set = c & 1;
           if (!(ok = warp_wait(bX + 8 * set, (c >> 1) & 1, stop))) break;
           fence_after();
 #pragma unroll
-          for (int jb = 0; jb < 4; ++jb) piece(jb, tX + 128 * set + 32 * jb);
+          for (int jb = 0; jb < 4; ++jb) piece(jb, tX + kPiece * (4 * set + jb));
           mma_commit(lead, bXf + 8 * set);
           mma_commit(lead, bFree12 + 8 * st);
           mma_commit(lead, bFree3 + 8 * st);
@@ -384,7 +390,7 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_co
           if (!(ok = warp_wait(bX, c & 1, stop))) break;
           fence_after();
           piece(0, tX);
-          piece(1, tX + 32);
+          piece(1, tX + kPiece);
           mma_commit(lead, bXf);
         }
         if (c > 0 && !(ok = warp_wait(bOx, (c - 1) & 1, stop))) break;
@@ -397,20 +403,17 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_co
           if (!(ok = warp_wait(bX + 8, c & 1, stop))) break;
           fence_after();
           piece(2, tX);
-          piece(3, tX + 32);
+          piece(3, tX + kPiece);
         } else if (!(ok = warp_wait(bFull3 + 8 * st, (c / P::kStages) & 1, stop))) {
           break;
         }
         mma_commit(lead, bSt);
         if (!(ok = warp_wait(bP, c & 1, stop))) break;
-        if (c + 1 < s.nch) {
-          fence_after();
-          scores(c + 1);
-        }
         if (have && !(ok = warp_wait(bOs, (c - late) & 1, stop))) break;
         fence_after();
-        mma_tn<kChunk>(lead, tO, tP, x3, dO, have);
+        mma_tn<kChunk>(lead, tO, tS1, x3, dO, have);
         mma_commit(lead, bOf);
+        if (c + 1 < s.nch) scores(c + 1);  // over P, which the product before has read
       }
     }
   } else if (role == 0 && !STATE_ONLY) {
@@ -419,7 +422,6 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_co
     // of lambda that are both at most 1; the diagonal block takes the power of
     // the difference.
     const int w = warp % 4;
-    bool ok = true;
 #pragma unroll 1
     for (int c = 0; c < s.nch; ++c) {
       if (!warp_wait(bS1, c & 1, stop)) break;
@@ -453,11 +455,8 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_co
             }
           }
         }
-        // P of the chunk before has been used
-        if (jb == 0 && c > 0 && !(ok = warp_wait(bOf, (c - 1) & 1, stop))) break;
-        tmem_st16(tP + lanes + 16 * jb, o);
+        tmem_st16(tS1 + lanes + 16 * jb, o);  // over columns that have been read
       }
-      if (!ok) break;
       st_wait();
       fence_before();
       if (w == 0 && c + 1 < s.nch) {  // the next chunk's x1 and x2 are there
@@ -504,7 +503,7 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_co
 #pragma unroll
       for (int x = 0; x < 32; ++x) z[x] = 0;
 #pragma unroll
-      for (int x = 0; x < kBufs; ++x) tmem_st32(tX + lanes + 32 * x, z);
+      for (int x = 0; x < kBufs * kPiece / 32; ++x) tmem_st32(tX + lanes + 32 * x, z);
       st_wait();
     }
     bool ok = true;
@@ -538,7 +537,7 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_co
       const float far = STATE_ONLY ? exp2f(l2 * (float)((s.nch - 1 - c) * kChunk)) : 1.f;
 #pragma unroll 1
       for (int jb = STATE_ONLY ? role : 0; jb < 4; jb += STATE_ONLY ? 4 : 1) {
-        uint32_t hi[16], lo[16];
+        uint32_t hi[16], mid[16], lo[16];
         if (v < VP) {
 #pragma unroll
           for (int x = 0; x < 16; x += 2) {
@@ -555,9 +554,12 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_co
 #pragma unroll
             for (int y = 0; y < 2; ++y) {
               const uint32_t h = pack_bf16(f[2 * y], f[2 * y + 1]);
+              const float g0 = f[2 * y] - __uint_as_float(h << 16);
+              const float g1 = f[2 * y + 1] - __uint_as_float(h & 0xffff0000u);
+              const uint32_t m = pack_bf16(g0, g1);
               hi[x + y] = h;
-              lo[x + y] = pack_bf16(f[2 * y] - __uint_as_float(h << 16),
-                                    f[2 * y + 1] - __uint_as_float(h & 0xffff0000u));
+              mid[x + y] = m;
+              if (three) lo[x + y] = pack_bf16(g0 - __uint_as_float(m << 16), g1 - __uint_as_float(m & 0xffff0000u));
             }
           }
         }
@@ -567,10 +569,11 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_co
         else if (jb == 2) ok = warp_wait(bXf, c & 1, stop);
         if (!ok) break;
         fence_after();
-        const uint32_t at = tX + (STATE_ONLY ? 128 * (c & 1) + 32 * jb : 32 * (jb & 1)) + lanes;
+        const uint32_t at = tX + kPiece * (STATE_ONLY ? 4 * (c & 1) + jb : jb & 1) + lanes;
         if (v < VP) {
           tmem_st16(at, hi);
-          tmem_st16(at + 16, lo);
+          tmem_st16(at + 16, mid);
+          if (three) tmem_st16(at + 32, lo);
           st_wait();
         }
         if (STATE_ONLY || (jb & 1)) {
