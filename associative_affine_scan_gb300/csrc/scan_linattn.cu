@@ -201,7 +201,7 @@ __global__ void __launch_bounds__(256) linattn_step_kernel(const StepArgs a) {
 scan_status lin_common(const LinArgs& a, scan_dtype dt, int64_t H, int64_t Dk, int64_t Dv) {
   if (dt != SCAN_F32 && dt != SCAN_BF16) return SCAN_ERR_INVALID_ARG;
   if (a.B < 0 || a.T < 0 || H < 0 || Dk < 1 || Dv < 1 || a.n_seqs < 0) return SCAN_ERR_INVALID_ARG;
-  if (a.cu && a.B != 1) return SCAN_ERR_INVALID_ARG;
+  if (a.cu && (a.B != 1 || (a.n_seqs == 0 && a.T > 0))) return SCAN_ERR_INVALID_ARG;
   if (!(a.scale > 0.f) || !(a.scale < INFINITY)) return SCAN_ERR_INVALID_ARG;
   if (Dk > kMixMaxDim || Dv > kMixMaxDim || Dk % 8 || Dv % 8) return SCAN_ERR_UNSUPPORTED;
   const int64_t n = a.cu ? a.n_seqs : a.B;

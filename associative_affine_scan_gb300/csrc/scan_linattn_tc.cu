@@ -705,8 +705,8 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_co
 __global__ void __launch_bounds__(256) linattn_chain_kernel(const __grid_constant__ TcArgs a) {
   const TcPass& p = a.pass[blockIdx.z];
   const int n = p.K * p.V;  // a multiple of 64
-  const int64_t row = blockIdx.y;
-  const int i = (blockIdx.x * 256 + threadIdx.x) * 4;
+  const int64_t row = blockIdx.x;  // (there may be more rows than a grid's other axes hold)
+  const int i = (blockIdx.y * 256 + threadIdx.x) * 4;
   const int h = (int)(row % a.H), seq = (int)(row / a.H);
   const float l2 = fmaxf(a.log_decay[h] * 1.44269504088896341f, -1e30f);
   __shared__ float keep[64];  // lambda^steps of a dense segment's pieces
@@ -825,7 +825,7 @@ cudaError_t launch_kv(const TcArgs& t, int npass, int64_t rows, cudaStream_t s) 
     linattn_tc_kernel<KP, VP, true><<<(unsigned)(own * npass), kThreads, Q::kSmem, s>>>(t);
   }
   if (split || t.cu)
-    linattn_chain_kernel<<<dim3(KP * VP / 1024, (unsigned)rows, npass), 256, 0, s>>>(t);
+    linattn_chain_kernel<<<dim3((unsigned)rows, KP * VP / 1024, npass), 256, 0, s>>>(t);
   linattn_tc_kernel<KP, VP, false><<<(unsigned)(parts * npass), kThreads, P::kSmem, s>>>(t);
   return cudaGetLastError();
 }

@@ -299,7 +299,7 @@ scan_status win_common(WinArgs* a, scan_dtype dt, int64_t Hq, int64_t Hk, int64_
     return SCAN_ERR_INVALID_ARG;
   if (a->W < 1 || a->S < 0 || !(a->scale > 0.f) || !(a->scale < INFINITY)) return SCAN_ERR_INVALID_ARG;
   if (Hk == 0 ? Hq != 0 : Hq % Hk != 0) return SCAN_ERR_INVALID_ARG;
-  if (a->cu && (a->B != 1 || a->Tq != a->Tk)) return SCAN_ERR_INVALID_ARG;
+  if (a->cu && (a->B != 1 || a->Tq != a->Tk || (n_seqs == 0 && a->Tq > 0))) return SCAN_ERR_INVALID_ARG;
   if (D > kMixMaxDim || D % 8) return SCAN_ERR_UNSUPPORTED;
   if (Hq > 65535 || a->B > 65535 || a->B * Hq > 65535 || a->Tq > 0x7fffffffLL || a->Tk > 0x7fffffffLL)
     return SCAN_ERR_UNSUPPORTED;

@@ -199,6 +199,28 @@ def test_linattn_packed(lib, dtype, lengths):
                   cu=offsets(lengths))
 
 
+def test_linattn_many_packed_sequences(lib):
+    """More (sequence, head) rows than the second axis of a grid holds, empty ones
+    among them: every final state against its closed form for constant operands."""
+    H, D, n = 34, 8, 2000
+    lengths = torch.full((n,), 48)
+    lengths[::7] = 0
+    cu = torch.cat([torch.zeros(1), lengths.cumsum(0)]).to(torch.int32).to(DEV)
+    T = int(lengths.sum())
+    assert n * H > 65535 and T >= 32 * n  # the chunked form takes it
+    g = -torch.linspace(0.01, 2.0, H, device=DEV)
+    q = torch.ones(1, T, H, D, dtype=BF, device=DEV)
+    o, hT = lib.linattn_fwd(q, q, q, g, None, cu, scale=1.0)
+    lam = f64(g).exp()
+    full = (1 - lam ** 48) / (1 - lam)
+    want = torch.where(lengths[:, None] > 0, full[None], 0.0)[:, :, None, None].expand(n, H, D, D)
+    gate(hT, want, want, dtype=F32, terms=48 + D + 2 ** 7, name="hT")
+    ends = (cu[1:][lengths.to(DEV) > 0] - 1).long()
+    got, last = f64(o[0, ends]), D * full[None, :, None].expand(len(ends), H, D)
+    assert float(((got - last).abs() / last).max()) <= 3 * U16
+    assert lib.scan_get_device_status() == lib.SCAN_OK
+
+
 @pytest.mark.parametrize("dtype", [BF, F32])
 def test_linattn_sequences_do_not_leak(lib, dtype):
     """A sequence of NaN between two others leaves their results as they are."""

@@ -70,6 +70,7 @@ def test_linattn_checks(lib):
     assert lin(lib, q=NULL) == INVALID
     assert lin(lib, o=None) == INVALID
     assert lin(lib, cu=P, n=3, B=2) == INVALID
+    assert lin(lib, cu=P, n=0) == INVALID
     assert lin(lib, Dk=20) == UNSUPPORTED
     assert lin(lib, Dv=136) == UNSUPPORTED
     assert lin(lib, ws=None) == WORKSPACE
@@ -102,6 +103,7 @@ def test_window_checks(lib):
     assert win(lib, lse=None) == INVALID
     assert win(lib, cu=P, n=2, Tk=65) == INVALID
     assert win(lib, cu=P, n=2, B=2) == INVALID
+    assert win(lib, cu=P, n=0) == INVALID
     assert win(lib, D=68) == UNSUPPORTED
     assert win(lib, D=136) == UNSUPPORTED
     assert win(lib, B=40000, Hq=4) == UNSUPPORTED
