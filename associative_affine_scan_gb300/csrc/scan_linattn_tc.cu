@@ -845,7 +845,12 @@ cudaError_t launch_passes(const TcArgs& t, int npass, int64_t rows, cudaStream_t
 bool linattn_tc_fits(const LinArgs& a, scan_dtype dt) {
   if (dt != SCAN_BF16 || a.T < 1 || a.T > 0x7fffffffLL) return false;
   const int64_t n = a.cu ? a.n_seqs : a.B;
-  if (a.T < 32 * (a.cu ? n : 1)) return false;
+  // Rows of fewer steps go one step at a time. A row's chunk costs the same whatever it
+  // holds: at 16 / 24 steps 16 heads take 8 us by chunks against 12 / 17 us by
+  // steps (128 x 128; 7 against 8 / 12 us at 64 x 64), 1024 rows 51 against 99 / 140 us
+  // (45 against 28 / 39 us at 64 x 64, where steps are ahead up to 32); at 8 steps
+  // 16 heads take 8 against 8 us (7 against 6 us).
+  if (a.T < 16 * (a.cu ? n : 1)) return false;
   for (int i = 0; i < a.npass; ++i) {
     const LinPass& p = a.pass[i];
     if (!heads_map_fits(p.x1, a.B, a.T, a.H) || !heads_map_fits(p.x2, a.B, a.T, a.H) ||

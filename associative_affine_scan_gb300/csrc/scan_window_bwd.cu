@@ -111,15 +111,21 @@ struct DeltaArgs {
 __global__ void __launch_bounds__(256) window_delta16_kernel(const DeltaArgs a) {
   const int lane = threadIdx.x % 16;
   const int64_t r0 = ((int64_t)blockIdx.x * 16 + threadIdx.x / 16) * 4;
+  int64_t tok = r0 / a.H, b = tok / a.T, t = tok - b * a.T;
+  int h = (int)(r0 - tok * a.H);
+  int64_t at[4];
   uint4 x[4], y[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     x[i] = y[i] = make_uint4(0, 0, 0, 0);
-    const int64_t r = r0 + i;
-    if (r < a.rows && 8 * lane < a.D) {
-      const int64_t h = r % a.H, t = r / a.H % a.T, b = r / a.H / a.T;
+    at[i] = (b * a.H + h) * a.T + t;
+    if (r0 + i < a.rows && 8 * lane < a.D) {
       x[i] = *reinterpret_cast<const uint4*>(a.o + b * a.o_sb + t * a.o_st + h * a.o_sh + 8 * lane);
       y[i] = *reinterpret_cast<const uint4*>(a.d + b * a.d_sb + t * a.d_st + h * a.d_sh + 8 * lane);
+    }
+    if (++h == a.H) {
+      h = 0;
+      if (++t == a.T) t = 0, ++b;
     }
   }
 #pragma unroll
@@ -133,11 +139,7 @@ __global__ void __launch_bounds__(256) window_delta16_kernel(const DeltaArgs a) 
     }
 #pragma unroll
     for (int k = 8; k; k >>= 1) s += __shfl_xor_sync(0xffffffffu, s, k);
-    const int64_t r = r0 + i;
-    if (lane == 0 && r < a.rows) {
-      const int64_t h = r % a.H, t = r / a.H % a.T, b = r / a.H / a.T;
-      a.delta[(b * a.H + h) * a.T + t] = s;
-    }
+    if (lane == 0 && r0 + i < a.rows) a.delta[at[i]] = s;
   }
 }
 
