@@ -8,29 +8,40 @@
 //   backward: dz = rotate by the opposite angle (dy), g = w dz,
 //             dx = r (g - n mean(g n)),  dw = sum over rows of dz n
 //
-// Bound by DRAM: one read and one write of every element forward, two reads
-// and one write backward, about ten operations on each. A row of D elements is
-// held by the 8, 16 or 32 lanes that cover it, eight elements a lane, so the
-// norm's sum is three to five shuffles and no row is read twice. A lane's eight
-// elements are four pairs (elements 4u.. and R/2 + 4u.., or 8u.. where
-// neighbours are paired), so the rotation needs no exchange. A group of lanes
-// takes up to four heads of one token (two in the backward): the token's cosines
-// and sines are read once for them. A block has either queries or keys; the
-// backward's walk over the tokens, with their weight's gradient in registers. What
-// hides the latency of DRAM is the number of warps: rows stay in their own type
-// until they are used, to keep registers for four (backward three) blocks an SM.
+// One read and one write of every element forward, two reads and one write
+// backward, about ten operations on each. A row of D elements is held by the 8, 16
+// or 32 lanes that cover it, eight elements a lane, so the norm's sum is three to
+// five shuffles and no row is read twice. A lane's eight elements are four pairs
+// (elements 4u.. and R/2 + 4u.., or 8u.. where neighbours are paired), so the rotation
+// needs no exchange, and go through the arithmetic two at a time. A group of lanes
+// takes four heads of one token (two in fp32): the token's cosines and sines are read
+// once for them. A block has either queries or keys; the backward's walk over the
+// tokens, with their weight's gradient in registers. What hides the latency of DRAM is
+// the number of rows in flight: they stay in their own type until they are used.
+//
+// Forward of 8 x 4096 tokens, 16 + 4 heads of 128, bf16: 57 us, 5.9 TB/s, bound by
+// DRAM. Backward: 96 us, 5.3 TB/s, bound half by DRAM and half by the issue of
+// instructions (scalar arithmetic and two heads a group: 116 us). A ring of
+// asynchronous copies to shared memory, two items ahead, took 175 us, and the next
+// item's rows in registers 145 us: a lane's copies of 8 bytes and what they spill cost
+// more than the latency that they hide.
 #include "scan_mixer.h"
+#include "scan_tc.cuh"
 
 namespace scan {
 namespace {
 
+using tc::add2;
+using tc::fma2;
+using tc::mul2;
+
 constexpr int kThreads = 256;
-// Heads of one token that a group of lanes takes: 64 bytes of each operand a lane
-// forward, 32 backward.
+// Heads of one token that a group of lanes takes: 64 bytes of each operand a lane.
+// What an item costs besides (its place, pointers, table entries) is shared by them:
+// the backward of 8 x 4096 x 20 heads of 128 in bf16 took 137 / 117 / 100 / 112 us with
+// 1 / 2 / 4 / 8, each at its best block size and number of blocks.
 template <typename T>
-constexpr int kFwdHeads = sizeof(T) == 2 ? 4 : 2;
-template <typename T>
-constexpr int kBwdHeads = sizeof(T) == 2 ? 2 : 1;
+constexpr int kHeads = sizeof(T) == 2 ? 4 : 2;
 
 // Division of numbers below 2^31 by a fixed divisor: one high product, one add and
 // one shift (Granlund and Montgomery, "Division by invariant integers using
@@ -79,9 +90,11 @@ struct Raw<float> {
     b = *reinterpret_cast<const float4*>(row + hi);
   }
   __device__ __forceinline__ void clear() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
-  __device__ __forceinline__ void get(float (&v)[8]) const {
-    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+  __device__ __forceinline__ void get(float2 (&v)[4]) const {
+    v[0] = make_float2(a.x, a.y);
+    v[1] = make_float2(a.z, a.w);
+    v[2] = make_float2(b.x, b.y);
+    v[3] = make_float2(b.z, b.w);
   }
 };
 template <>
@@ -92,29 +105,27 @@ struct Raw<__nv_bfloat16> {
     b = *reinterpret_cast<const uint2*>(row + hi);
   }
   __device__ __forceinline__ void clear() { a = b = make_uint2(0u, 0u); }
-  __device__ __forceinline__ void get(float (&v)[8]) const {
+  __device__ __forceinline__ void get(float2 (&v)[4]) const {
     const uint32_t u[4] = {a.x, a.y, b.x, b.y};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      v[2 * i] = __uint_as_float(u[i] << 16);
-      v[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
-    }
+    for (int i = 0; i < 4; ++i)
+      v[i] = make_float2(__uint_as_float(u[i] << 16), __uint_as_float(u[i] & 0xffff0000u));
   }
 };
 template <typename T>
-__device__ __forceinline__ void store8(T* row, int lo, int hi, const float (&v)[8]);
+__device__ __forceinline__ void store8(T* row, int lo, int hi, const float2 (&v)[4]);
 template <>
-__device__ __forceinline__ void store8<float>(float* row, int lo, int hi, const float (&v)[8]) {
-  *reinterpret_cast<float4*>(row + lo) = make_float4(v[0], v[1], v[2], v[3]);
-  *reinterpret_cast<float4*>(row + hi) = make_float4(v[4], v[5], v[6], v[7]);
+__device__ __forceinline__ void store8<float>(float* row, int lo, int hi, const float2 (&v)[4]) {
+  *reinterpret_cast<float4*>(row + lo) = make_float4(v[0].x, v[0].y, v[1].x, v[1].y);
+  *reinterpret_cast<float4*>(row + hi) = make_float4(v[2].x, v[2].y, v[3].x, v[3].y);
 }
 template <>
 __device__ __forceinline__ void store8<__nv_bfloat16>(__nv_bfloat16* row, int lo, int hi,
-                                                      const float (&v)[8]) {
+                                                      const float2 (&v)[4]) {
   uint32_t u[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+    const __nv_bfloat162 h = __floats2bfloat162_rn(v[i].x, v[i].y);
     u[i] = *reinterpret_cast<const uint32_t*>(&h);
   }
   *reinterpret_cast<uint2*>(row + lo) = make_uint2(u[0], u[1]);
@@ -145,21 +156,28 @@ __device__ __forceinline__ Unit unit_of(int u, const QkArgs& a) {
 }
 
 // (a, b) -> (a c - b s, a s + b c) on a lane's four pairs.
-__device__ __forceinline__ void rotate(float (&v)[8], const float (&c)[4], const float (&s)[4],
+__device__ __forceinline__ void rotate(float2 (&v)[4], const float (&c)[4], const float (&s)[4],
                                        bool pairs) {
+  if (pairs) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int ia = pairs ? 2 * i : i, ib = pairs ? 2 * i + 1 : 4 + i;
-    const float x = v[ia], y = v[ib];
-    v[ia] = x * c[i] - y * s[i];
-    v[ib] = x * s[i] + y * c[i];
+    for (int i = 0; i < 4; ++i)
+      v[i] = fma2(v[i], make_float2(c[i], c[i]), mul2(make_float2(v[i].y, v[i].x), make_float2(-s[i], s[i])));
+  } else {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const float2 x = v[i], y = v[2 + i], ci = make_float2(c[2 * i], c[2 * i + 1]);
+      v[i] = fma2(x, ci, mul2(y, make_float2(-s[2 * i], -s[2 * i + 1])));
+      v[2 + i] = fma2(y, ci, mul2(x, make_float2(s[2 * i], s[2 * i + 1])));
+    }
   }
 }
 
+// Sums of both numbers over a group of lanes.
 template <int G>
-__device__ __forceinline__ float group_sum(float v) {
+__device__ __forceinline__ float2 group_sum(float2 v) {
 #pragma unroll
-  for (int d = G / 2; d; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
+  for (int d = G / 2; d; d >>= 1)
+    v = add2(v, make_float2(__shfl_xor_sync(0xffffffffu, v.x, d), __shfl_xor_sync(0xffffffffu, v.y, d)));
   return v;
 }
 
@@ -180,14 +198,14 @@ __device__ __forceinline__ void load_turn(const QkArgs& a, int64_t p, const Unit
   }
 }
 
-__device__ __forceinline__ void load_weight(const float* w, const Unit& u, float (&v)[8]) {
+__device__ __forceinline__ void load_weight(const float* w, const Unit& u, float2 (&v)[4]) {
   Raw<float> r;
   if (w && u.on) {
     r.load(w, u.lo, u.hi);
     r.get(v);
   } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = 1.f;
+    for (int i = 0; i < 4; ++i) v[i] = make_float2(1.f, 1.f);
   }
 }
 
@@ -233,7 +251,7 @@ __device__ __forceinline__ View<T> qk_view(const scan_view4& v) {
 
 template <typename T, int G, bool PAIRS>
 __global__ void __launch_bounds__(kThreads, 4) qknorm_fwd_kernel(const QkArgs a) {
-  constexpr int N = kFwdHeads<T>;
+  constexpr int N = kHeads<T>;
   const int m = blockIdx.x >= a.blocks[0];
   const int64_t block = m ? blockIdx.x - a.blocks[0] : blockIdx.x;
   const int64_t i0 = block * (kThreads / G) + threadIdx.x / G;
@@ -244,28 +262,31 @@ __global__ void __launch_bounds__(kThreads, 4) qknorm_fwd_kernel(const QkArgs a)
   const int64_t p = a.pos ? (int64_t)a.pos[w.tok] : w.t;
   Raw<T> r[N];
   load_heads<T, N>(m ? qk_view<const T>(a.x[1]) : qk_view<const T>(a.x[0]), w, u, H, live, r);
-  float wt[8], cs[4] = {1.f, 1.f, 1.f, 1.f}, sn[4] = {0.f, 0.f, 0.f, 0.f};
+  float2 wt[4];
+  float cs[4] = {1.f, 1.f, 1.f, 1.f}, sn[4] = {0.f, 0.f, 0.f, 0.f};
   load_weight(a.w[m], u, wt);
   load_turn(a, p, u, cs, sn);
   const View<T> y = m ? qk_view<T>(a.y[1]) : qk_view<T>(a.y[0]);
   T* out = y.row(w.b, w.t, w.h);
-  float rs[N];
+  float2 rs[N / 2];  // of two heads each
 #pragma unroll
   for (int i = 0; i < N; ++i) {
-    float v[8];
+    float2 v[4], sq = make_float2(0.f, 0.f);
     r[i].get(v);
-    rs[i] = 0.f;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) rs[i] = fmaf(v[j], v[j], rs[i]);
+    for (int j = 0; j < 4; ++j) sq = fma2(v[j], v[j], sq);
+    (i % 2 ? rs[i / 2].y : rs[i / 2].x) = sq.x + sq.y;
   }
 #pragma unroll
-  for (int i = 0; i < N; ++i) rs[i] = rsqrtf(fmaf(group_sum<G>(rs[i]), a.inv_D, a.eps));
+  for (int i = 0; i < N / 2; ++i) rs[i] = group_sum<G>(rs[i]);
 #pragma unroll
   for (int i = 0; i < N; ++i) {
-    float v[8];
+    const float f = rsqrtf(fmaf(i % 2 ? rs[i / 2].y : rs[i / 2].x, a.inv_D, a.eps));
+    const float2 f2 = make_float2(f, f);
+    float2 v[4];
     r[i].get(v);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] *= rs[i] * wt[j];
+    for (int j = 0; j < 4; ++j) v[j] = mul2(v[j], mul2(wt[j], f2));
     if (u.rot) rotate(v, cs, sn, PAIRS);
     if (live && u.on && w.h + i < H) store8<T>(out + i * y.sh, u.lo, u.hi, v);
   }
@@ -275,8 +296,8 @@ __global__ void __launch_bounds__(kThreads, 4) qknorm_fwd_kernel(const QkArgs a)
 // partial sum; the partial sums are added in block order by the kernel below, so
 // the result does not depend on the order in which blocks finish.
 template <typename T, int G, bool PAIRS>
-__global__ void __launch_bounds__(kThreads, 3) qknorm_bwd_kernel(const QkArgs a) {
-  constexpr int N = kBwdHeads<T>, NG = kThreads / G;
+__global__ void __launch_bounds__(kThreads, 2) qknorm_bwd_kernel(const QkArgs a) {
+  constexpr int N = kHeads<T>, NG = kThreads / G;
   const int m = blockIdx.x >= a.blocks[0];
   const int64_t block = m ? blockIdx.x - a.blocks[0] : blockIdx.x;
   const int64_t items = a.BT * a.chunks[m], step = (int64_t)a.blocks[m] * NG;
@@ -285,9 +306,9 @@ __global__ void __launch_bounds__(kThreads, 3) qknorm_bwd_kernel(const QkArgs a)
   const View<const T> dy = m ? qk_view<const T>(a.dy[1]) : qk_view<const T>(a.dy[0]);
   const View<T> dx = m ? qk_view<T>(a.dx[1]) : qk_view<T>(a.dx[0]);
   const int H = a.H[m];
-  float wt[8], dw[8];
+  float2 wt[4], dw[4];
 #pragma unroll
-  for (int j = 0; j < 8; ++j) dw[j] = 0.f;
+  for (int j = 0; j < 4; ++j) dw[j] = make_float2(0.f, 0.f);
   load_weight(a.w[m], u, wt);
   // whole warps leave together: the bound is on the warp's first group
   int64_t lead = block * NG + (threadIdx.x / 32) * (32 / G), i0 = lead + (threadIdx.x % 32) / G;
@@ -310,24 +331,25 @@ __global__ void __launch_bounds__(kThreads, 3) qknorm_bwd_kernel(const QkArgs a)
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       const bool here = live && u.on && h + i < H;
-      float v[8], d[8], sq = 0.f, gn = 0.f;
+      float2 v[4], d[4], e[4], sq = make_float2(0.f, 0.f), gn = sq;
       r[i].get(v);
       g[i].get(d);
       if (u.rot) rotate(d, cs, sn, PAIRS);
       // (rows that are not there are zeros, and add nothing)
-      float e[8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        e[j] = d[j] * wt[j];
-        sq = fmaf(v[j], v[j], sq);
-        gn = fmaf(e[j], v[j], gn);
+      for (int j = 0; j < 4; ++j) {
+        e[j] = mul2(d[j], wt[j]);
+        sq = fma2(v[j], v[j], sq);
+        gn = fma2(e[j], v[j], gn);
       }
-      const float rs = rsqrtf(fmaf(group_sum<G>(sq), a.inv_D, a.eps));
-      const float back = -(group_sum<G>(gn) * a.inv_D) * rs * rs * rs;  // -r^2 mean(g n) of each x
+      const float2 sum = group_sum<G>(make_float2(sq.x + sq.y, gn.x + gn.y));
+      const float rs = rsqrtf(fmaf(sum.x, a.inv_D, a.eps));
+      const float back = -(sum.y * a.inv_D) * rs * rs * rs;  // -r^2 mean(g n) of each x
+      const float2 rs2 = make_float2(rs, rs), back2 = make_float2(back, back);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        dw[j] = fmaf(d[j] * rs, v[j], dw[j]);
-        v[j] = fmaf(v[j], back, e[j] * rs);
+      for (int j = 0; j < 4; ++j) {
+        dw[j] = fma2(mul2(d[j], rs2), v[j], dw[j]);
+        v[j] = fma2(v[j], back2, mul2(e[j], rs2));
       }
       if (here) store8<T>(out + i * dx.sh, u.lo, u.hi, v);
     }
@@ -335,7 +357,7 @@ __global__ void __launch_bounds__(kThreads, 3) qknorm_bwd_kernel(const QkArgs a)
   // groups of the block, in order
   __shared__ float red[kThreads * 8];
 #pragma unroll
-  for (int j = 0; j < 8; ++j) red[j * kThreads + threadIdx.x] = dw[j];
+  for (int j = 0; j < 8; ++j) red[j * kThreads + threadIdx.x] = j % 2 ? dw[j / 2].y : dw[j / 2].x;
   __syncthreads();
   for (int i = threadIdx.x; i < 8 * G; i += kThreads) {
     const int lane = i % G, j = i / G;
@@ -348,7 +370,8 @@ __global__ void __launch_bounds__(kThreads, 3) qknorm_bwd_kernel(const QkArgs a)
 }
 
 // Columns of the partial sums, one block per (queries or keys, 32 columns): 32
-// lanes of columns by 32 slices of blocks, the slices then added in order.
+// lanes of columns by 32 slices of blocks, the slices then added in order. 6 us, the
+// latency of ten dependent rounds of loads and sums.
 __global__ void __launch_bounds__(1024) qknorm_dw_kernel(const QkArgs a) {
   const int m = blockIdx.y, lane = threadIdx.x % 32, col = blockIdx.x * 32 + lane, sl = threadIdx.x / 32;
   if (!a.dw[m]) return;
@@ -369,7 +392,7 @@ __global__ void __launch_bounds__(1024) qknorm_dw_kernel(const QkArgs a) {
 
 // Blocks of the backward's walk: what stays resident, shared between queries and
 // keys by their numbers of items.
-constexpr int kBwdBlocks = 152 * 3;
+constexpr int kBwdBlocks = 152 * 2;
 
 void share_blocks(QkArgs* a, int groups, bool fwd) {
   const int64_t items[2] = {a->BT * a->chunks[0], a->BT * a->chunks[1]};
@@ -389,7 +412,7 @@ int group_lanes(int D) { return D <= 64 ? 8 : D <= 128 ? 16 : 32; }
 
 template <typename T, int G>
 cudaError_t qk_launch_g(QkArgs a, bool fwd, cudaStream_t s) {
-  const int heads = fwd ? kFwdHeads<T> : kBwdHeads<T>;
+  constexpr int heads = kHeads<T>;
   for (int m = 0; m < 2; ++m) a.chunks[m] = (a.H[m] + heads - 1) / heads;
   share_blocks(&a, kThreads / G, fwd);
   const int blocks = a.blocks[0] + a.blocks[1];
