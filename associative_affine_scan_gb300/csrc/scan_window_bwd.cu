@@ -7,7 +7,9 @@
 //
 // Two kernels, each with its sums in tensor memory and no sum across blocks: the
 // five products become seven, but no result depends on the order in which blocks
-// run and nothing is added in global memory.
+// run and nothing is added in global memory. 2 x 4096 tokens, 16 query heads of 128
+// over 4 key heads, window 1024: keys 155 us (0.78 PFLOP/s of seen pairs' four products),
+// queries 131 us (0.69, three products), row sums 14 us, pieces 5 us.
 //   keys:    a block owns 128 keys and walks the tiles of 128 queries that see
 //            them: S = k q^T, dP = v do^T, dv += P do, dk += dS q. Keys are the
 //            rows of S, so P and dS (bf16, over S and dP in tensor memory) are
@@ -16,8 +18,10 @@
 //            S = q k^T, dP = do v^T, dq += dS k.
 // The order of issue keeps the tensor cores busy while two warpgroups turn S and
 // dP into P and dS, half of the columns each: the first product of the next tile
-// is issued between the two that wait for them. Both are bound by the tensor
-// cores (512 cycles a product at D = 128). The queries' kernel issues dP from a
+// is issued between the two that wait for them. Both are bound by that chain: the tensor
+// cores (512 cycles a product at D = 128) are busy for 51 % (keys) and 39 % (queries) of
+// a block's cycles; 280 blocks of keys on 152 SMs leave a quarter of the time idle besides,
+// which smaller pieces would fill at the price of sums in memory. The queries' kernel issues dP from a
 // warp of its own (141 -> 132 us on 2 x 4096 x 16 heads, window 1024); the same
 // in the keys' kernel, whose two chains then alternate, took 170 us for 160.
 //
@@ -107,7 +111,7 @@ struct DeltaArgs {
 };
 
 // delta = sum of dout o of every row: 16 lanes of 16 bytes a row, four rows in
-// flight a lane. Bound by DRAM.
+// flight a lane. Bound by DRAM: 67 MB in 14.5 us, 4.6 TB/s.
 __global__ void __launch_bounds__(256) window_delta16_kernel(const DeltaArgs a) {
   const int lane = threadIdx.x % 16;
   const int64_t r0 = ((int64_t)blockIdx.x * 16 + threadIdx.x / 16) * 4;

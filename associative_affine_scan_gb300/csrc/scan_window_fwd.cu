@@ -19,6 +19,12 @@
 // The maximum that p is taken from follows the true one only when that has grown
 // by more than 2^8: until then p stays below 2^8, which changes no rounding (bf16
 // and fp32 have the same exponents), and the outputs need no rescaling.
+//
+// 16384 tokens, 16 query heads of 128 over 4 key heads, window 2048: 266 us, 0.97 PFLOP/s
+// of seen pairs; 2 x 4096 tokens, window 1024: 89 us, 0.68 PFLOP/s. The tensor cores are
+// busy for half of a block's cycles: scores, weights and outputs pass from role to role
+// twice a tile, and tiles at the window's edges and of the first tokens are worked in
+// whole. A second product warp, one a query tile, took 306 us for 266.
 #include "scan_tc.cuh"
 #include "scan_window_tc.h"
 

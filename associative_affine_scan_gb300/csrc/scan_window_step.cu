@@ -9,8 +9,10 @@
 // The sums' index order is free, so each fragment is what a thread loaded 16 bytes
 // of: the scores' index runs over the D elements in the order of the four lanes'
 // pieces, and the columns of the output are the elements in the order 8 n + j.
-// Fragments of V pair two keys' elements. The warps of a block take different key
-// heads of the same keys where there are several (neighbours in the cache).
+// Fragments of V pair two keys' elements. The warps of a block take different keys of
+// one key head, or with many requests different key heads of the same keys (neighbours
+// in the cache). 64 requests of 4100 keys, 4 key heads of 128: 106 us, 5.1 TB/s, set by
+// the bytes in flight; 32-byte loads a lane were slower (174 us for 136 at the time).
 //
 // A request's keys are split over the blocks of a cluster (up to 16) when the
 // requests alone do not fill the SMs; the partial maxima, sums and outputs meet
@@ -290,13 +292,19 @@ cudaError_t launch_heads(const WinStepArgs& a, int64_t B, int wh, int splits, cu
 
 }  // namespace
 
+// A block takes one key head, its four warps a quarter of the keys each, where these
+// blocks are resident at once, and else up to four key heads, a warp each. In us by key
+// heads a block (4 / 1), 4 key heads of 128: 1 request of 2052 keys 21 / 11, 8 of them
+// 25 / 17, 32 of 4100 keys 63 / 55, 64 of them 110 / 106, 100 of them 182 / 139; past
+// what is resident, 128 of them 199 / 237.
 // Splits of a request's keys: as many as stay resident at once (two to three blocks
 // an SM, on 128 of the SMs: clusters do not fill every group of SMs), as long as a
-// warp has two steps of 16 keys. 64 requests of 4100 keys and 4 key heads, in us by
-// splits: 332 (1), 184, 141, 114, 120, 111 (6), 138 (7: a second round of clusters).
+// warp has two steps of 16 keys. 64 requests of 4100 keys and 4 key heads a block, in us
+// by splits: 332 (1), 184, 141, 114, 120, 111 (6), 138 (7: a second round of clusters).
 cudaError_t launch_window_step(const WinStepArgs& a, int64_t B, cudaStream_t s) {
-  const int G = a.Hq / a.Hk, rows = G <= 8 ? 8 : 16, wh = a.Hk % 4 == 0 ? 4 : a.Hk % 2 == 0 ? 2 : 1;
-  const int64_t blocks = B * (a.Hk / wh) * ((G + rows - 1) / rows), slots = (rows == 8 ? 3 : 2) * 128;
+  const int G = a.Hq / a.Hk, rows = G <= 8 ? 8 : 16, tiles = (G + rows - 1) / rows, per_sm = rows == 8 ? 3 : 2;
+  const int wh = B * a.Hk * tiles <= per_sm * 152 ? 1 : a.Hk % 4 == 0 ? 4 : a.Hk % 2 == 0 ? 2 : 1;
+  const int64_t blocks = B * (a.Hk / wh) * tiles, slots = per_sm * 128;
   int64_t n = slots / blocks;
   const int64_t most = a.cap / (2 * 16 * (kWarps / wh));
   n = n > most ? most : n;

@@ -480,6 +480,32 @@ def test_window_step(lib, dtype, Hq, Hk, D, W, S):
         assert torch.equal(torch.nan_to_num(f64(got), nan=9e9), torch.nan_to_num(want, nan=9e9))
 
 
+@pytest.mark.parametrize("B,Hq,Hk,D", [(130, 16, 4, 128), (240, 4, 2, 64), (90, 40, 4, 64), (500, 3, 1, 72)])
+def test_window_step_many_requests(lib, B, Hq, Hk, D):
+    """More (request, key head) pairs than run at once: key heads share a block."""
+    g = gen(B)
+    W, S, G = 90, 3, Hq // Hk
+    C = W + S
+    q, k, v = (normal(g, B, h, D, dtype=BF) for h in (Hq, Hk, Hk))
+    kc, vc = (normal(g, B, C, Hk, D, dtype=BF) for _ in range(2))
+    pos = torch.randint(-1, 3 * C, (B,), generator=g)
+    rk, rv = f64(kc), f64(vc)
+    o = lib.window_attn_step(q, k, v, kc, vc, pos.to(torch.int32).to(DEV), W, S)
+    p = pos.to(DEV)
+    live = p >= 0
+    at = torch.where(p < S, p, S + (p - S) % W)[live]
+    rk[live, at], rv[live, at] = f64(k)[live], f64(v)[live]
+    kk, vv = (x.repeat_interleave(G, 2) for x in (rk, rv))
+    sc = torch.einsum("bhd,bnhd->bhn", f64(q), kk) * D ** -0.5
+    sc = sc.masked_fill(torch.arange(C, device=DEV) > p[:, None, None], float("-inf"))
+    w = torch.softmax(sc[live], -1)
+    smag = max(1.0, float(f64(q).norm(dim=-1).max() * kk.norm(dim=-1).max()) * D ** -0.5)
+    gate(o[live], torch.einsum("bhn,bnhd->bhd", w, vv[live]), torch.einsum("bhn,bnhd->bhd", w, vv[live].abs()),
+         dtype=BF, roundings=1, terms=C + D + 2 * D * smag, name="o")
+    assert float(o[~live].abs().sum()) == 0.0
+    assert torch.equal(f64(kc), rk) and torch.equal(f64(vc), rv)
+
+
 @pytest.mark.parametrize("dtype", [BF, F32])
 def test_window_steps_equal_the_prompt(lib, dtype):
     """Tokens one at a time through the ring give what the whole row gives."""
