@@ -490,14 +490,13 @@ def test_window_step_many_requests(lib, B, Hq, Hk, D):
     kc, vc = (normal(g, B, C, Hk, D, dtype=BF) for _ in range(2))
     pos = torch.randint(-1, 3 * C, (B,), generator=g)
     rk, rv = f64(kc), f64(vc)
-    o = lib.window_attn_step(q, k, v, kc, vc, pos.to(torch.int32).to(DEV), W, S)
-    p = pos.to(DEV)
-    live = p >= 0
-    at = torch.where(p < S, p, S + (p - S) % W)[live]
+    o = lib.window_attn_step(q, k, v, kc, vc, pos.to(torch.int32).to(DEV), W, S).cpu()
+    live = pos >= 0
+    at = torch.where(pos < S, pos, S + (pos - S) % W)[live]
     rk[live, at], rv[live, at] = f64(k)[live], f64(v)[live]
     kk, vv = (x.repeat_interleave(G, 2) for x in (rk, rv))
     sc = torch.einsum("bhd,bnhd->bhn", f64(q), kk) * D ** -0.5
-    sc = sc.masked_fill(torch.arange(C, device=DEV) > p[:, None, None], float("-inf"))
+    sc = sc.masked_fill(torch.arange(C) > pos[:, None, None], float("-inf"))
     w = torch.softmax(sc[live], -1)
     smag = max(1.0, float(f64(q).norm(dim=-1).max() * kk.norm(dim=-1).max()) * D ** -0.5)
     gate(o[live], torch.einsum("bhn,bnhd->bhd", w, vv[live]), torch.einsum("bhn,bnhd->bhd", w, vv[live].abs()),
