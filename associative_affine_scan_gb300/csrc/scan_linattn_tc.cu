@@ -252,7 +252,7 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_co
     bar_init(bOs, 4);
     bar_init(bOf, 1);
     bar_init(bOx, 4);
-    bar_init(bClean, 4);
+    bar_init(bClean, STATE_ONLY ? 16 : 4);  // every warp that clears rows of the next sequence
     bar_init(bInit, 4 * (KP / 32));
     bar_init_fence();
     for (int c = 0; c < P::kStages && c < s.nch; ++c) {
