@@ -199,6 +199,15 @@ def test_linattn_packed(lib, dtype, lengths):
                   cu=offsets(lengths))
 
 
+@pytest.mark.parametrize("lengths", [[606, 644, 22, 33, 439, 88, 337, 152, 480], [1100, 1, 700]])
+def test_linattn_packed_segments(lib, lengths):
+    """Sequences of several segments, the first in reversed order with a ragged chunk."""
+    n, T = len(lengths), sum(lengths)
+    for Dk, Dv in ((64, 64), (128, 64), (64, 128)):
+        lin_check(lib, lin_inputs(1, T, 2, Dk, Dv, BF, T + n, n=n, state=n % 2 == 0), decays(2), offsets(lengths))
+    assert lib.scan_get_device_status() == lib.SCAN_OK
+
+
 def test_linattn_many_packed_sequences(lib):
     """More (sequence, head) rows than the second axis of a grid holds, empty ones
     among them: every final state against its closed form for constant operands."""
