@@ -737,6 +737,8 @@ __global__ void __launch_bounds__(256) linattn_chain_kernel(const __grid_constan
     for (int d = 16; d; d >>= 1) before += __shfl_xor_sync(0xffffffffu, before, d);
     seq_bounds(a.cu, seq, a.T, &beg, &end);
     count = (int)((end - beg + a.cps * kChunk - 1) / (a.cps * kChunk)) - 1;
+    // offsets that overlap (malformed) add up to more segments than the workspace holds
+    if (before + count > a.nseg) count = 0;
     first = before * a.H + h;
     step = a.H;
     whole = exp2f(l2 * (float)(a.cps * kChunk));
