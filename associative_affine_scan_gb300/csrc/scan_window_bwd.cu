@@ -29,6 +29,7 @@
 // walk is cut into pieces of about the length of any other tile's, whose partial
 // sums (fp32, workspace) are added in order by a last kernel.
 #include "scan_tc.cuh"
+#include "scan_window_phases.h"
 #include "scan_window_tc.h"
 
 namespace scan {
@@ -510,7 +511,7 @@ __global__ void __launch_bounds__(kThreadsDq, 1) window_dq_kernel(const __grid_c
   uint32_t* const misc = reinterpret_cast<uint32_t*>(gen + (2 + NS) * P::kTileBytes);
   const uint32_t bars = smem_addr(misc);
   const uint32_t bQ = bars, bFull = bars + 8, bEmpty = bFull + 8 * NS, bS = bEmpty + 8 * NS, bDp = bS + 16,
-                 bDs = bDp + 8, bEnd = bDs + 8, bOut = bEnd + 8;
+                 bDs = bDp + 8, bEnd = bDs + 8 * kDsBarriers, bOut = bEnd + 8;
   uint32_t* const tmem_ptr = misc + 64;
   uint32_t* const stop_flag = misc + 65;
 
@@ -540,7 +541,7 @@ __global__ void __launch_bounds__(kThreadsDq, 1) window_dq_kernel(const __grid_c
     bar_init(bS, 1);
     bar_init(bS + 8, 1);
     bar_init(bDp, 1);
-    bar_init(bDs, 8);
+    for (int i = 0; i < kDsBarriers; ++i) bar_init(bDs + 8 * i, 8);
     bar_init(bEnd, 1);
     bar_init(bOut, 4);
     bar_init_fence();
@@ -586,7 +587,7 @@ __global__ void __launch_bounds__(kThreadsDq, 1) window_dq_kernel(const __grid_c
       if (ok && n > 1 && (ok = full(2))) scores(1);
 #pragma unroll 1
       for (int u = 0; ok && u < n; ++u) {
-        if (!(ok = warp_wait(bDs, u & 1, stop))) break;
+        if (!(ok = warp_wait(bDs + 8 * ds_barrier(u), ds_parity(u), stop))) break;
         fence_after();
         const uint32_t w = tS + 128 * (u & 1), t = mnmajor(sR, kHalf) + slot(2 * u);
         mma_tn<64>(lead, tDq, w, t, dO, u > 0);
@@ -609,7 +610,7 @@ __global__ void __launch_bounds__(kThreadsDq, 1) window_dq_kernel(const __grid_c
       for (int u = 0; ok && u < n; ++u) {
         const int v = (2 * u + 1) % NS;
         if (!(ok = warp_wait(bFull + 8 * v, ((2 * u + 1) / NS) & 1, stop))) break;
-        if (u > 0 && !(ok = warp_wait(bDs, (u - 1) & 1, stop))) break;  // the last dP has been read
+        if (u > 0 && !(ok = warp_wait(bDs + 8 * ds_barrier(u - 1), ds_parity(u - 1), stop))) break;  // the last dP has been read
         fence_after();
         mma_kk<DP, kHalf, kHalf>(lead, tDp, kmajor(sD), kmajor(sR) + v * (P::kTileBytes >> 4), dS, false);
         mma_commit(lead, bDp);
@@ -676,7 +677,7 @@ __global__ void __launch_bounds__(kThreadsDq, 1) window_dq_kernel(const __grid_c
       st_wait();
       fence_before();
       __syncwarp();
-      if (lane == 0) bar_arrive(bDs);
+      if (lane == 0) bar_arrive(bDs + 8 * ds_barrier(u));
     }
     if (ok && n > 0) ok = warp_wait(bEnd, 0, stop);
     if (w == 0 && __all_sync(0xffffffffu, ok)) {
