@@ -330,12 +330,11 @@ __global__ void __launch_bounds__(kThreads, 2) qknorm_bwd_kernel(const QkArgs a)
     p = a.pos ? (int64_t)a.pos[w.tok] : w.t;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      const bool here = live && u.on && h + i < H;
+      const bool some = live && h + i < H, here = some && u.on;
       float2 v[4], d[4], e[4], sq = make_float2(0.f, 0.f), gn = sq;
       r[i].get(v);
       g[i].get(d);
       if (u.rot) rotate(d, cs, sn, PAIRS);
-      // (rows that are not there are zeros, and add nothing)
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         e[j] = mul2(d[j], wt[j]);
@@ -343,7 +342,8 @@ __global__ void __launch_bounds__(kThreads, 2) qknorm_bwd_kernel(const QkArgs a)
         gn = fma2(e[j], v[j], gn);
       }
       const float2 sum = group_sum<G>(make_float2(sq.x + sq.y, gn.x + gn.y));
-      const float rs = rsqrtf(fmaf(sum.x, a.inv_D, a.eps));
+      // a row that is not there is zeros and adds nothing, also where eps is 0
+      const float rs = some ? rsqrtf(fmaf(sum.x, a.inv_D, a.eps)) : 0.f;
       const float back = -(sum.y * a.inv_D) * rs * rs * rs;  // -r^2 mean(g n) of each x
       const float2 rs2 = make_float2(rs, rs), back2 = make_float2(back, back);
 #pragma unroll

@@ -7,7 +7,9 @@ import struct
 import pytest
 import torch
 
-from test_gpu_mixers import BF, DEV, lin_inputs
+import _mixer_ref as ref
+from _mixer_ref import f64, gate
+from test_gpu_mixers import BF, DEV, F32, gen, lin_inputs, normal, tables
 
 pytestmark = pytest.mark.gpu
 
@@ -43,3 +45,32 @@ def test_linattn_overlapping_offsets_stay_in_the_workspace(lib, T, H, D, times):
         assert st == lib.SCAN_OK
         assert raw.scan_get_device_status(buf.data_ptr(), s) == lib.SCAN_ERR_SEQLENS
         assert bool((buf[size:] == 0x5a).all()), run
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("B,T,Hq,Hk,D", [(1, 3, 1, 1, 64), (2, 7, 5, 1, 96), (1, 33, 2, 6, 128), (3, 5, 4, 3, 256)])
+def test_qk_norm_rope_without_epsilon(lib, dtype, B, T, Hq, Hk, D):
+    """eps = 0: heads and tokens that only fill up a group of lanes have no norm,
+    and add nothing to the weights' gradients of the ones that are there."""
+    g = gen(D + T)
+    x = [normal(g, B, T, h, D, dtype=dtype) for h in (Hq, Hk)]
+    dy = [normal(g, B, T, h, D, dtype=dtype) for h in (Hq, Hk)]
+    w = [normal(g, D) + 1.0 for _ in range(2)]
+    cos, sin = tables(T, D)
+    y = lib.qk_norm_rope_fwd(*x, *w, cos, sin, eps=0.0)
+    d = lib.qk_norm_rope_bwd(*x, *w, cos, sin, *dy, eps=0.0)
+    pos = torch.arange(T).expand(B, T)
+    for m in range(2):
+        xr, wr = f64(x[m]).requires_grad_(), f64(w[m]).requires_grad_()
+        yr = ref.qk_norm_rope(xr, wr, f64(cos), f64(sin), pos, 0.0, False)
+        dxr, dwr = torch.autograd.grad((yr * f64(dy[m])).sum(), (xr, wr))
+        r = 1 / torch.sqrt((f64(x[m]) ** 2).mean(-1, keepdim=True))
+        n = f64(x[m]) * r
+        # terms: the two products of a pair; D of the norm's sum
+        zmag = (n * wr.detach()).abs().amax(-1, keepdim=True)
+        gate(y[m], yr.detach(), zmag.expand_as(yr), dtype=dtype, terms=D, name="y")
+        gmag = 2 * f64(dy[m]).abs().amax(-1, keepdim=True) * wr.detach().abs().amax()
+        mag = (r * gmag * (1 + n.abs() * n.abs().mean(-1, keepdim=True))).expand_as(dxr)
+        gate(d[m], dxr, mag, dtype=dtype, terms=D, name="dx")
+        dwmag = (2 * f64(dy[m]).abs().amax(-1, keepdim=True) * n.abs()).sum((0, 1, 2))
+        gate(d[2 + m], dwr, dwmag, dtype=F32, terms=D, name="dw")
