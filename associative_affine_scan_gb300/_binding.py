@@ -296,6 +296,10 @@ class _Workspaces:
                 # is zeroed on `stream`. Buffers only grow, so this is rare.
                 torch.cuda.synchronize(device)
                 buf = torch.empty(size, dtype=torch.uint8, device=device)
+                # a call that was handed this buffer may still launch after another
+                # thread has put a larger one in its place: once freed it is reused
+                # only when the work queued on `stream` by then is done
+                buf.record_stream(torch.cuda.ExternalStream(stream.value or 0, device=device))
                 _check(_call(device, "scan_workspace_init", _ptr(buf), size, stream),
                        "scan_workspace_init")
                 self._buf[key] = buf
@@ -934,8 +938,9 @@ def _rank(t, name, n):
 
 
 def _mixer_workspace(nbytes, dev, s):
-    ws = _mixer_ws.get(max(int(nbytes), 256), dev, ctypes.c_void_p(s))
-    return ws.data_ptr(), ws.numel()
+    """The workspace as a tensor: the caller holds it until its launch has been made,
+    as another thread may put a larger one in its place in the meantime."""
+    return _mixer_ws.get(max(int(nbytes), 256), dev, ctypes.c_void_p(s))
 
 
 def qk_norm_rope_workspace_bytes(D) -> int:
@@ -1002,11 +1007,11 @@ def qk_norm_rope_bwd(q, k, q_weight, k_weight, cos, sin, dq_out, dk_out, positio
         dwq, dwk = (None if w is None else torch.empty(D, dtype=torch.float32, device=dev)
                     for w in (q_weight, k_weight))
     s = _raw_stream(stream, dev)
-    ws, nws = _mixer_workspace(256 + qk_norm_rope_workspace_bytes(D), dev, s)
+    ws = _mixer_workspace(256 + qk_norm_rope_workspace_bytes(D), dev, s)
     _enter(dev, "qk_norm_rope_bwd", _view4(q), _view4(k), _at(q_weight), _at(k_weight),
                _at(cos), _at(sin), _at(positions), _view4(dq_out), _view4(dk_out), _view4(dq),
                _view4(dk), _at(dwq), _at(dwk), B, T, Hq, Hk, D, R, P, int(bool(interleaved)), eps,
-               _dtype_code(q), ws + 256, nws - 256, s)  # past the status word
+               _dtype_code(q), ws.data_ptr() + 256, ws.numel() - 256, s)  # past the status word
     return dq, dk, dwq, dwk
 
 
@@ -1054,10 +1059,11 @@ def linattn_fwd(q, k, v, log_decay, h0=None, cu_seqlens=None, *, scale=None, nee
         o = torch.empty(v.shape, dtype=dt, device=dev)
         hT = torch.empty(states, dtype=torch.float32, device=dev) if need_state else None
     s = _raw_stream(stream, dev)
-    ws, nws = _mixer_workspace(linattn_workspace_bytes(B, T, H, Dk, Dv, n), dev, s)
+    ws = _mixer_workspace(linattn_workspace_bytes(B, T, H, Dk, Dv, n), dev, s)
     _enter(dev, "linattn_fwd", _view4(q), _view4(k), _view4(v), _at(log_decay), _at(h0),
                _at(cu_seqlens), n, _view4(o), _at(hT), B, T, H, Dk, Dv,
-               Dk ** -0.5 if scale is None else scale, _dtype_code(q), ws, nws, s)
+               Dk ** -0.5 if scale is None else scale, _dtype_code(q),
+               ws.data_ptr(), ws.numel(), s)
     return o, hT
 
 
@@ -1080,11 +1086,11 @@ def linattn_bwd(q, k, v, log_decay, dout, h0=None, cu_seqlens=None, dhT=None, *,
         dq, dk, dv = (torch.empty(t.shape, dtype=dt, device=dev) for t in (q, k, v))
         dh0 = torch.empty(states, dtype=torch.float32, device=dev) if need_dh0 else None
     s = _raw_stream(stream, dev)
-    ws, nws = _mixer_workspace(linattn_workspace_bytes(B, T, H, Dk, Dv, n), dev, s)
+    ws = _mixer_workspace(linattn_workspace_bytes(B, T, H, Dk, Dv, n), dev, s)
     _enter(dev, "linattn_bwd", _view4(q), _view4(k), _view4(v), _at(log_decay), _at(h0),
                _at(cu_seqlens), n, _view4(dout), _at(dhT), _view4(dq), _view4(dk), _view4(dv),
                _at(dh0), B, T, H, Dk, Dv, Dk ** -0.5 if scale is None else scale, _dtype_code(q),
-               ws, nws, s)
+               ws.data_ptr(), ws.numel(), s)
     return dq, dk, dv, dh0
 
 
@@ -1147,11 +1153,12 @@ def window_attn_fwd(q, k, v, window, sinks=0, cu_seqlens=None, *, scale=None, ou
         o = torch.empty(q.shape, dtype=dt, device=dev)
         lse = torch.empty((B, Hq, Tq), dtype=torch.float32, device=dev)
     s = _raw_stream(stream, dev)
-    ws, nws = _mixer_workspace(
+    ws = _mixer_workspace(
         window_attn_workspace_bytes(B, Tq, Tk, Hq, Hk, D, window, sinks, n), dev, s)
     _enter(dev, "window_attn_fwd", _view4(q), _view4(k), _view4(v), _at(cu_seqlens), n,
                _view4(o), _at(lse), B, Tq, Tk, Hq, Hk, D, window, sinks,
-               D ** -0.5 if scale is None else scale, _dtype_code(q), ws, nws, s)
+               D ** -0.5 if scale is None else scale, _dtype_code(q),
+               ws.data_ptr(), ws.numel(), s)
     return o, lse
 
 
@@ -1170,11 +1177,12 @@ def window_attn_bwd(q, k, v, o, lse, dout, window, sinks=0, cu_seqlens=None, *, 
     else:
         dq, dk, dv = (torch.empty(t.shape, dtype=dt, device=dev) for t in (q, k, v))
     s = _raw_stream(stream, dev)
-    ws, nws = _mixer_workspace(
+    ws = _mixer_workspace(
         window_attn_workspace_bytes(B, Tq, Tk, Hq, Hk, D, window, sinks, n, True), dev, s)
     _enter(dev, "window_attn_bwd", _view4(q), _view4(k), _view4(v), _view4(o), _at(lse),
                _view4(dout), _at(cu_seqlens), n, _view4(dq), _view4(dk), _view4(dv), B, Tq, Tk, Hq,
-               Hk, D, window, sinks, D ** -0.5 if scale is None else scale, _dtype_code(q), ws, nws, s)
+               Hk, D, window, sinks, D ** -0.5 if scale is None else scale, _dtype_code(q),
+               ws.data_ptr(), ws.numel(), s)
     return dq, dk, dv
 
 

@@ -74,3 +74,37 @@ def test_qk_norm_rope_without_epsilon(lib, dtype, B, T, Hq, Hk, D):
         gate(d[m], dxr, mag, dtype=dtype, terms=D, name="dx")
         dwmag = (2 * f64(dy[m]).abs().amax(-1, keepdim=True) * n.abs()).sum((0, 1, 2))
         gate(d[2 + m], dwr, dwmag, dtype=F32, terms=D, name="dw")
+
+
+def test_two_threads_on_one_stream(lib):
+    """Calls of growing size from two threads on one stream, whose workspace grows
+    under them: each gives what it gives alone."""
+    import threading
+    sizes = [(1, 1000 + 700 * i, 4 + i) for i in range(8)]
+    work = []
+    for B, T, H in sizes:
+        q, k, v, do, _, _ = lin_inputs(B, T, H, 64, 64, BF, T, state=False)
+        work.append((q, k, v, torch.full((H,), -0.02, device=DEV), do))
+    want = [lib.linattn_bwd(*w) for w in work]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    got, errors = [None] * len(work), []
+
+    def run(which):
+        try:
+            for i in which:
+                with torch.cuda.stream(side):
+                    got[i] = lib.linattn_bwd(*work[i])
+        except Exception as e:  # noqa: BLE001 - shown below
+            errors.append(e)
+
+    threads = [threading.Thread(target=run, args=(range(r, len(work), 2),)) for r in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    side.synchronize()
+    assert not errors
+    for a, b in zip(got, want):
+        assert all(torch.equal(x, y) for x, y in zip(a, b))
+    assert lib.scan_get_device_status(stream=side) == lib.SCAN_OK

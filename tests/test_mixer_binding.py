@@ -1,0 +1,48 @@
+"""The binding's workspaces and device findings, without a GPU: the library's
+calls are replaced by a note of what they were given."""
+
+import weakref
+
+import pytest
+import torch
+
+import associative_affine_scan_gb300 as scan
+from associative_affine_scan_gb300 import _binding
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    from associative_affine_scan_gb300 import build_lib
+    build_lib.build()
+
+
+@pytest.mark.parametrize("name", ["qk_norm_rope_bwd", "linattn_fwd", "linattn_bwd", "window_attn_fwd",
+                                  "window_attn_bwd"])
+def test_workspace_lives_until_the_call_has_returned(monkeypatch, name):
+    """Another thread may grow the pool's buffer between a call's look-up and its
+    launch: the call itself has to hold what it was given."""
+    given = []
+
+    def get(nbytes, device, stream):
+        buf = torch.empty(nbytes, dtype=torch.uint8)
+        given.append((weakref.ref(buf), buf.data_ptr(), buf.numel()))
+        return buf
+
+    def enter(device, where, *args):
+        buf, at, size = given.pop()
+        assert where == name and buf() is not None
+        offset = 256 if name.startswith("qk") else 0
+        assert (at + offset, size - offset) in list(zip(args, args[1:]))
+
+    monkeypatch.setattr(_binding, "_heads", lambda t, *a, **k: t)
+    monkeypatch.setattr(_binding, "_need", lambda t, *a, **k: t)
+    monkeypatch.setattr(_binding, "_raw_stream", lambda stream, device: 0)
+    monkeypatch.setattr(_binding._mixer_ws, "get", get)
+    monkeypatch.setattr(_binding, "_enter", enter)
+    x, g = torch.zeros(1, 8, 2, 64), torch.zeros(2)
+    {"qk_norm_rope_bwd": lambda: scan.qk_norm_rope_bwd(x, x, None, None, None, None, x, x),
+     "linattn_fwd": lambda: scan.linattn_fwd(x, x, x, g),
+     "linattn_bwd": lambda: scan.linattn_bwd(x, x, x, g, x),
+     "window_attn_fwd": lambda: scan.window_attn_fwd(x, x, x, 4),
+     "window_attn_bwd": lambda: scan.window_attn_bwd(x, x, x, x, torch.zeros(1, 2, 8), x, 4)}[name]()
+    assert not given
