@@ -276,10 +276,14 @@ def _scalar_dims(a: torch.Tensor, cu_seqlens):
 
 
 class _Workspaces:
-    """One zeroed workspace per (device, stream), grown on demand."""
+    """One zeroed workspace per (device, stream), grown on demand. It cannot grow
+    during a capture: the calls that a CUDA graph records are made once before on
+    the stream that it is captured on."""
 
     def __init__(self):
         self._buf = {}
+        self._captured = set()  # keys whose buffer a CUDA graph uses
+        self._held = []         # buffers that graphs use and larger ones have replaced
         self._lk = threading.Lock()
 
     def get(self, nbytes: int, device: torch.device, stream: ctypes.c_void_p) -> torch.Tensor:
@@ -302,7 +306,12 @@ class _Workspaces:
                 buf.record_stream(torch.cuda.ExternalStream(stream.value or 0, device=device))
                 _check(_call(device, "scan_workspace_init", _ptr(buf), size, stream),
                        "scan_workspace_init")
+                if key in self._captured:  # its graph may be replayed at any time
+                    self._captured.discard(key)
+                    self._held.append(self._buf[key])
                 self._buf[key] = buf
+            if torch.cuda.is_current_stream_capturing():
+                self._captured.add(key)
             return buf
 
     def current(self, device, stream):

@@ -9,7 +9,7 @@ import torch
 
 import _mixer_ref as ref
 from _mixer_ref import f64, gate
-from test_gpu_mixers import BF, DEV, F32, gen, lin_inputs, normal, tables
+from test_gpu_mixers import BF, DEV, F32, calls, gen, lin_inputs, normal, tables
 
 pytestmark = pytest.mark.gpu
 
@@ -107,4 +107,34 @@ def test_two_threads_on_one_stream(lib):
     assert not errors
     for a, b in zip(got, want):
         assert all(torch.equal(x, y) for x, y in zip(a, b))
+    assert lib.scan_get_device_status(stream=side) == lib.SCAN_OK
+
+
+@pytest.mark.parametrize("name", ["rope", "rope_bwd", "lin", "lin_bwd", "lin_step", "win", "win_bwd", "win_step"])
+def test_captured_calls(lib, name):
+    """Each call in a CUDA graph: replays give what the call gives, also after a
+    larger call on the same stream has replaced the workspace that they use, and
+    leave the memory that is handed out since alone."""
+    call = calls(lib, BF)[name]
+    want = call()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        call()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        got = call()
+    for t in got:
+        t.zero_()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        q, k, v, do, _, _ = lin_inputs(1, 9000, 8, 128, 128, BF, 1, state=False)
+        lib.linattn_bwd(q, k, v, torch.full((8,), -0.1, device=DEV), do)
+        # as many small blocks as the freed workspace could have become
+        since = [torch.full((1024,), 0x5a, dtype=torch.uint8, device=DEV) for _ in range(2000)]
+        graph.replay()
+    side.synchronize()
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+    assert all(bool((t == 0x5a).all()) for t in since)
     assert lib.scan_get_device_status(stream=side) == lib.SCAN_OK

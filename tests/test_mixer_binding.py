@@ -46,3 +46,27 @@ def test_workspace_lives_until_the_call_has_returned(monkeypatch, name):
      "window_attn_fwd": lambda: scan.window_attn_fwd(x, x, x, 4),
      "window_attn_bwd": lambda: scan.window_attn_bwd(x, x, x, x, torch.zeros(1, 2, 8), x, 4)}[name]()
     assert not given
+
+
+@pytest.mark.parametrize("captured", [False, True])
+def test_a_larger_workspace_leaves_the_captured_one(monkeypatch, captured):
+    """A graph writes into the workspace of its capture whenever it is replayed:
+    the buffer stays when a later call needs a larger one, and only then."""
+    import ctypes
+    monkeypatch.setattr(_binding, "_call", lambda *a: scan.SCAN_OK)
+    monkeypatch.setattr(_binding.torch.cuda, "synchronize", lambda device: None)
+    monkeypatch.setattr(_binding.torch.cuda, "ExternalStream", lambda *a, **k: None)
+    monkeypatch.setattr(torch.Tensor, "record_stream", lambda self, stream: None)
+    monkeypatch.setattr(_binding.torch.cuda, "is_current_stream_capturing", lambda: capturing)
+    pool, dev, s = _binding._Workspaces(), torch.device("cpu"), ctypes.c_void_p(3)
+    capturing = False
+    first = weakref.ref(pool.get(5000, dev, s))
+    capturing = captured
+    assert pool.get(4000, dev, s) is first()
+    capturing = False
+    other = weakref.ref(pool.get(5000, dev, ctypes.c_void_p(4)))
+    second = weakref.ref(pool.get(9000, dev, s))
+    assert pool.get(9000, dev, s) is second() and (first() is not None) == captured
+    pool.get(20000, dev, s)
+    pool.get(20000, dev, ctypes.c_void_p(4))
+    assert second() is None and other() is None and (first() is not None) == captured
