@@ -283,7 +283,7 @@ class _Workspaces:
     def __init__(self):
         self._buf = {}
         self._captured = set()  # keys whose buffer a CUDA graph uses
-        self._held = []         # buffers that graphs use and larger ones have replaced
+        self._held = {}         # buffers of a key that graphs use and larger ones have replaced
         self._lk = threading.Lock()
 
     def get(self, nbytes: int, device: torch.device, stream: ctypes.c_void_p) -> torch.Tensor:
@@ -308,7 +308,7 @@ class _Workspaces:
                        "scan_workspace_init")
                 if key in self._captured:  # its graph may be replayed at any time
                     self._captured.discard(key)
-                    self._held.append(self._buf[key])
+                    self._held.setdefault(key, []).append(self._buf[key])
                 self._buf[key] = buf
             if torch.cuda.is_current_stream_capturing():
                 self._captured.add(key)
@@ -316,6 +316,12 @@ class _Workspaces:
 
     def current(self, device, stream):
         return self._buf.get((device.index, stream.value))
+
+    def all(self, device, stream):
+        """Every buffer that work on (device, stream) may write its findings to."""
+        with self._lk:
+            held = self._held.get((device.index, stream.value), ())
+            return [b for b in (self.current(device, stream), *held) if b is not None]
 
 
 _ws = _Workspaces()
@@ -358,15 +364,17 @@ def scan_workspace_init(workspace: torch.Tensor, stream=None) -> None:
 
 
 def scan_get_device_status(device=None, stream=None) -> int:
-    """Sticky device status of the workspaces used on (device, stream); resets it."""
+    """Sticky device status of the workspaces used on (device, stream): the first
+    finding, which is reset. One that another workspace holds as well (the scans and
+    the token mixers have their own) is what the next call returns."""
     device = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
     s = _stream(stream, device)
-    found = SCAN_OK
     for pool in (_ws, _mixer_ws):
-        buf = pool.current(device, s)
-        if buf is not None:
-            found = int(_call(device, "scan_get_device_status", _ptr(buf), s)) or found
-    return found
+        for buf in pool.all(device, s):
+            found = int(_call(device, "scan_get_device_status", _ptr(buf), s))
+            if found != SCAN_OK:
+                return found
+    return SCAN_OK
 
 
 def scan_fwd(a, x, h0=None, cu_seqlens=None, reverse=False, *, out=None, opts=None, stream=None):

@@ -138,3 +138,14 @@ def test_captured_calls(lib, name):
         assert torch.equal(a, b)
     assert all(bool((t == 0x5a).all()) for t in since)
     assert lib.scan_get_device_status(stream=side) == lib.SCAN_OK
+
+
+def test_findings_of_scans_and_mixers(lib):
+    """A scan and a token mixer with malformed offsets: both findings are reported."""
+    bad = torch.tensor([0, 40, 30], dtype=torch.int32, device=DEV)
+    assert lib.scan_get_device_status() == lib.SCAN_OK
+    q = lin_inputs(1, 30, 2, 64, 64, BF, 3, state=False)[0]
+    lib.window_attn_fwd(q, q, q, 8, 0, bad)
+    a = torch.rand(4, 30, device=DEV)
+    lib.scan_fwd(a, a, None, bad)
+    assert [lib.scan_get_device_status() for _ in range(3)] == [lib.SCAN_ERR_SEQLENS] * 2 + [lib.SCAN_OK]

@@ -70,3 +70,25 @@ def test_a_larger_workspace_leaves_the_captured_one(monkeypatch, captured):
     pool.get(20000, dev, s)
     pool.get(20000, dev, ctypes.c_void_p(4))
     assert second() is None and other() is None and (first() is not None) == captured
+
+
+def test_no_finding_is_lost(monkeypatch):
+    """The scans' workspace, the mixers' and one that a graph still uses have a
+    status word each: as many calls as there are findings return them all."""
+    import ctypes
+    dev, s = torch.device("cpu"), ctypes.c_void_p(3)
+    bufs = [torch.empty(16, dtype=torch.uint8) for _ in range(3)]
+    found = {b.data_ptr(): f for b, f in zip(bufs, (scan.SCAN_ERR_SEQLENS, scan.SCAN_ERR_TIMEOUT,
+                                                    scan.SCAN_ERR_SEQLENS))}
+
+    def call(device, name, ptr, stream):
+        assert name == "scan_get_device_status"
+        return found.pop(ptr.value, scan.SCAN_OK)
+
+    monkeypatch.setattr(_binding, "_call", call)
+    monkeypatch.setattr(_binding, "_stream", lambda stream, device: s)
+    for pool, buf in ((_binding._ws, bufs[0]), (_binding._mixer_ws, bufs[1])):
+        monkeypatch.setitem(pool._buf, (None, 3), buf)
+    monkeypatch.setattr(_binding._mixer_ws, "_held", {(None, 3): [bufs[2]]}, raising=False)
+    assert [scan.scan_get_device_status(dev) for _ in range(4)] == [
+        scan.SCAN_ERR_SEQLENS, scan.SCAN_ERR_TIMEOUT, scan.SCAN_ERR_SEQLENS, scan.SCAN_OK]
