@@ -191,6 +191,8 @@ __global__ void __launch_bounds__(4 * kTile) window_dkv_general(const WinArgs a)
   extern __shared__ float sm[];
   float *sk = sm, *sv = sk + kTile * kLd, *sq = sv + kTile * kLd, *sd = sq + kTile * kLd,
         *sp = sd + kTile * kLd, *ss = sp + kTile * (kTile + 1), *st = ss + kTile * (kTile + 1);
+  if (a.cu && blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x < 32)
+    check_seqlens(a.cu, a.n_seqs, a.Tk, a.hdr);
   TileRows g;
   if (!tile_rows(a.cu, a.n_seqs, a.Tq, a.Tk, blockIdx.x, kTile, &g)) return;
   const int hk = blockIdx.y % a.Hk, G = a.Hq / a.Hk;

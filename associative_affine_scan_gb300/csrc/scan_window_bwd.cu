@@ -167,6 +167,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_dkv_kernel(const __grid_co
   float* const s_lse = reinterpret_cast<float*>(misc + 72);  // lse log2(e) of a tile's queries
   float* const s_delta = s_lse + kRows;
 
+  if (a.cu && blockIdx.x == 0 && blockIdx.y == 0 && warp == 0) check_seqlens(a.cu, a.n_seqs, a.Tk, a.hdr);
   // which keys: the cut tiles' pieces first, then the others
   const int hk = blockIdx.y % a.Hk, b = blockIdx.y / a.Hk;
   int piece = -1;

@@ -149,3 +149,13 @@ def test_findings_of_scans_and_mixers(lib):
     a = torch.rand(4, 30, device=DEV)
     lib.scan_fwd(a, a, None, bad)
     assert [lib.scan_get_device_status() for _ in range(3)] == [lib.SCAN_ERR_SEQLENS] * 2 + [lib.SCAN_OK]
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("bad", [[0, 90, 20, 300], [-7, 90, 300], [0, 90, 299], [0, 301]])
+def test_window_backward_reports_malformed_offsets(lib, dtype, bad):
+    q, k, v, do = (normal(gen(i), 1, 300, 2, 64, dtype=dtype) for i in range(4))
+    o, lse = lib.window_attn_fwd(q, k, v, 50, 2)
+    assert lib.scan_get_device_status() == lib.SCAN_OK
+    lib.window_attn_bwd(q, k, v, o, lse, do, 50, 2, torch.tensor(bad, dtype=torch.int32, device=DEV))
+    assert [lib.scan_get_device_status() for _ in range(2)] == [lib.SCAN_ERR_SEQLENS, lib.SCAN_OK]
