@@ -85,6 +85,13 @@ struct Plan {
   static constexpr int kSmem = kStages * kStage + kState + kTables + 1024;
 };
 
+// log2(lambda); no memory at all (-inf) as a number, so that its 0th power is 1. NaN
+// stays NaN (which fmaxf would hide).
+__device__ __forceinline__ float log2_decay(float log_decay) {
+  const float l2 = log_decay * 1.44269504088896341f;
+  return l2 < -1e30f ? -1e30f : l2;
+}
+
 // The part of the sequence that a block works on, in processing order.
 struct Span {
   int64_t beg, len;  // the sequence
@@ -176,8 +183,7 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_co
   const int64_t steps = s.nch * (int64_t)kChunk -
                         ((rev ? s.first == 0 : s.first + s.nch == all) ? all * kChunk - s.len : 0);
   const int e = rev ? 0 : 1;
-  // log2(lambda); no memory at all (-inf) as a number, so that its 0th power is 1
-  const float l2 = fmaxf(a.log_decay[h] * 1.44269504088896341f, -1e30f);
+  const float l2 = log2_decay(a.log_decay[h]);
 
   // initial state: the caller's for the first segment, else the one before
   const float* s0 = nullptr;
@@ -717,7 +723,7 @@ __global__ void __launch_bounds__(256) linattn_chain_kernel(const __grid_constan
   const int64_t row = blockIdx.x;  // (there may be more rows than a grid's other axes hold)
   const int i = (blockIdx.y * 256 + threadIdx.x) * 4;
   const int h = (int)(row % a.H), seq = (int)(row / a.H);
-  const float l2 = fmaxf(a.log_decay[h] * 1.44269504088896341f, -1e30f);
+  const float l2 = log2_decay(a.log_decay[h]);
   __shared__ float keep[64];  // lambda^steps of a dense segment's pieces
   if (!a.cu && threadIdx.x < a.pieces) {
     const int y = threadIdx.x, chunks = a.cps * (y + 1) / a.pieces - a.cps * y / a.pieces;

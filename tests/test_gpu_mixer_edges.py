@@ -159,3 +159,22 @@ def test_window_backward_reports_malformed_offsets(lib, dtype, bad):
     assert lib.scan_get_device_status() == lib.SCAN_OK
     lib.window_attn_bwd(q, k, v, o, lse, do, 50, 2, torch.tensor(bad, dtype=torch.int32, device=DEV))
     assert [lib.scan_get_device_status() for _ in range(2)] == [lib.SCAN_ERR_SEQLENS, lib.SCAN_OK]
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("T", [7, 300, 1500])
+def test_linattn_decay_of_nan_shows(lib, dtype, T):
+    """A decay that is no number makes its head's outputs, states and gradients no
+    numbers, whichever path the length takes, and leaves the other heads alone."""
+    q, k, v, do, h0, dh = lin_inputs(1, T, 3, 64, 64, dtype, T)
+    good, bad = torch.full((3,), -0.1, device=DEV), torch.tensor([-0.1, float("nan"), -0.1], device=DEV)
+    want = lib.linattn_fwd(q, k, v, good, h0) + lib.linattn_bwd(q, k, v, good, do, h0, None, dh)
+    got = lib.linattn_fwd(q, k, v, bad, h0) + lib.linattn_bwd(q, k, v, bad, do, h0, None, dh)
+    for i, (a, b) in enumerate(zip(got, want)):
+        axis = 1 if i in (1, 5) else 2  # states are [B, H, K, V]
+        one, other = (t.movedim(axis, 0) for t in (a, b))
+        assert torch.equal(one[[0, 2]], other[[0, 2]]), i
+        if i in (3, 4):  # dk, dv: only the last step's have nothing of a later one
+            assert one[1].isnan()[:, :-1].all(), i
+        else:
+            assert one[1].isnan().all(), i
