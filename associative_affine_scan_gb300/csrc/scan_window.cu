@@ -106,12 +106,12 @@ __global__ void __launch_bounds__(4 * kTile) window_fwd_general(const WinArgs a)
     }
   }
   if (g.t0 + r >= g.nq) return;
-  const float inv = l > 0.f ? 1.f / l : 0.f;
+  const float inv = l == 0.f ? 0.f : 1.f / l;  // l is 0 where no key is seen; NaN stays
   T* out = vw<T>(a.o).row(b, g.qbeg + g.t0 + r, h);
 #pragma unroll
   for (int x = 0; x < kColsT; ++x)
     if (4 * x < a.D) out[c + 4 * x] = from_f32<T>(o[x] * inv);
-  if (c == 0) a.lse[(b * a.Hq + h) * a.Tq + g.qbeg + g.t0 + r] = l > 0.f ? m + logf(l) : -INFINITY;
+  if (c == 0) a.lse[(b * a.Hq + h) * a.Tq + g.qbeg + g.t0 + r] = l == 0.f ? -INFINITY : m + logf(l);
 }
 
 // delta_i = sum_d dout o of every query row: one warp a row.

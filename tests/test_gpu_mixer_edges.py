@@ -178,3 +178,16 @@ def test_linattn_decay_of_nan_shows(lib, dtype, T):
             assert one[1].isnan()[:, :-1].all(), i
         else:
             assert one[1].isnan().all(), i
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_window_scores_that_overflow_show(lib, dtype):
+    """A score of +inf (finite queries and keys whose product is too large) gives NaN
+    in its row's output and statistic, not the -inf of a row that sees nothing."""
+    q, k, v = (normal(gen(i), 1, 100, 2, 64, dtype=dtype) for i in range(3))
+    want = lib.window_attn_fwd(q, k, v, 20, 0)
+    q[0, 60, 1], k[0, 60, 1] = 1e25, 1e25
+    o, lse = lib.window_attn_fwd(q, k, v, 20, 0)
+    assert o[0, 60, 1].isnan().all() and bool(lse[0, 1, 60].isnan())
+    assert torch.equal(o[0, :60], want[0][0, :60]) and torch.equal(lse[0, :, :60], want[1][0, :, :60])
+    assert torch.equal(o[0, 80:], want[0][0, 80:]) and torch.equal(lse[0, 0], want[1][0, 0])
