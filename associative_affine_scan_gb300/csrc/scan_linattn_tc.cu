@@ -820,6 +820,8 @@ Split split_packed(int64_t n_seqs, int64_t H, int64_t T) {
   cps = cps < 4 ? 4 : cps;
   return Split{(int)((nch + cps - 1) / cps + n_seqs), (int)cps, 1};
 }
+// A row of one segment's length has none to chain, however its sequences lie.
+bool packed_chains(const Split& sp, int64_t T) { return (int64_t)sp.cps * kChunk < T; }
 
 int padded(int d) { return d <= 64 ? 64 : 128; }
 
@@ -831,8 +833,8 @@ cudaError_t launch_kv(const TcArgs& t, int npass, int64_t rows, cudaStream_t s) 
   cudaError_t e = cudaFuncSetAttribute(linattn_tc_kernel<KP, VP, false>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, P::kSmem);
   if (e != cudaSuccess) return e;
-  // a packed row of one segment's length has none to chain, but may have empty sequences
-  const bool split = t.cu ? (int64_t)t.cps * kChunk < t.T : t.nseg > 1;
+  // (a packed row without segments to chain may have empty sequences)
+  const bool split = t.cu ? packed_chains(Split{t.nseg, t.cps, t.pieces}, t.T) : t.nseg > 1;
   const int64_t own = t.cu ? (int64_t)t.nseg * t.H : rows * (t.nseg - 1) * t.pieces;
   const int64_t parts = t.cu ? (int64_t)t.nseg * t.H : rows * t.nseg;
   if (split) {
@@ -881,7 +883,8 @@ size_t linattn_tc_workspace_bytes(int64_t B, int64_t T, int64_t H, int64_t Dk, i
                                   int64_t n_seqs) {
   int64_t slots = 0;  // of all passes: three backward, one forward
   if (n_seqs > 0) {
-    slots = 3 * (int64_t)split_packed(n_seqs, H, T).nseg * H;
+    const Split sp = split_packed(n_seqs, H, T);
+    slots = packed_chains(sp, T) ? 3 * (int64_t)sp.nseg * H : 0;
   } else {
     for (int passes = 1; passes <= 3; passes += 2) {
       const Split sp = split_rows(B * H * passes, T);

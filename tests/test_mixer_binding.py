@@ -92,3 +92,12 @@ def test_no_finding_is_lost(monkeypatch):
     monkeypatch.setattr(_binding._mixer_ws, "_held", {(None, 3): [bufs[2]]}, raising=False)
     assert [scan.scan_get_device_status(dev) for _ in range(4)] == [
         scan.SCAN_ERR_SEQLENS, scan.SCAN_ERR_TIMEOUT, scan.SCAN_ERR_SEQLENS, scan.SCAN_OK]
+
+
+def test_packed_rows_that_are_not_cut_need_no_states():
+    """Many sequences fill the GPU uncut: room for the status word, not for a state
+    of every sequence and head (4000 x 16 x 128 x 128 fp32, three passes: 12.6 GB).
+    Few are cut: room for their segments' states, and no more."""
+    assert scan.linattn_workspace_bytes(1, 4000 * 200, 16, 128, 128, 4000) == 256
+    assert scan.linattn_workspace_bytes(1, 500, 1, 128, 128, 1) == 256
+    assert 256 < scan.linattn_workspace_bytes(1, 60000, 16, 128, 128, 3) < 1 << 28
