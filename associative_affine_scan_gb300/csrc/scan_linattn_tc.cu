@@ -817,7 +817,7 @@ Split split_packed(int64_t n_seqs, int64_t H, int64_t T) {
   int64_t want = H > 0 ? 152 / H - n_seqs / 2 : 1;
   want = want < 1 ? 1 : want;
   int64_t cps = (nch + want - 1) / want;
-  cps = cps < 4 ? 4 : cps;
+  cps = cps < 4 ? 4 : cps > 1 << 20 ? 1 << 20 : cps;  // a segment's steps are 32-bit numbers
   return Split{(int)((nch + cps - 1) / cps + n_seqs), (int)cps, 1};
 }
 // A row of one segment's length has none to chain, however its sequences lie.

@@ -101,3 +101,11 @@ def test_packed_rows_that_are_not_cut_need_no_states():
     assert scan.linattn_workspace_bytes(1, 4000 * 200, 16, 128, 128, 4000) == 256
     assert scan.linattn_workspace_bytes(1, 500, 1, 128, 128, 1) == 256
     assert 256 < scan.linattn_workspace_bytes(1, 60000, 16, 128, 128, 3) < 1 << 28
+
+
+def test_packed_segments_have_32_bit_lengths():
+    """Rows of close to 2^31 steps are cut where many sequences would leave them
+    whole: the kernels count a segment's steps in 32 bits."""
+    for T in (2 ** 31 - 1, 2 ** 31 - 128, 2 ** 30):
+        assert scan.linattn_workspace_bytes(1, T, 1, 8, 8, 400) >= 256 + 3 * (T >> 27) * 8 * 8 * 4
+    assert scan.linattn_workspace_bytes(1, 2 ** 27, 1, 8, 8, 400) == 256
