@@ -865,11 +865,15 @@ bool linattn_tc_fits(const LinArgs& a, scan_dtype dt) {
   if (dt != SCAN_BF16 || a.T < 1 || a.T > 0x7fffffffLL) return false;
   const int64_t n = a.cu ? a.n_seqs : a.B;
   // Rows of fewer steps go one step at a time. A row's chunk costs the same whatever it
-  // holds: at 16 / 24 steps 16 heads take 8 us by chunks against 12 / 17 us by
-  // steps (128 x 128; 7 against 8 / 12 us at 64 x 64), 1024 rows 51 against 99 / 140 us
-  // (45 against 28 / 39 us at 64 x 64, where steps are ahead up to 32); at 8 steps
-  // 16 heads take 8 against 8 us (7 against 6 us).
-  if (a.T < 16 * (a.cu ? n : 1)) return false;
+  // holds and whatever its heads are padded to; a step's cost follows the head. Forward,
+  // us by chunks / by steps, for 16 and 1024 (sequence, head) rows:
+  //   128 x 128:  8 steps 5.5 / 7.1 and 33 / 50,   16 steps 5.7 / 11 and 32 / 87
+  //    64 x 64:   8 steps 5.1 / 5.2 and 28 / 16,   16 steps 4.9 / 7.9 and 28 / 26
+  //    32 x 32:  16 steps 5.1 / 7.8 and 28 / 14,   32 steps 5.1 / 14 and 28 / 25
+  // so that small heads in more rows than three rounds of blocks have a bound of their own
+  // (their backward, 1024 rows: 24 steps 79 / 53, 32 steps 78 / 67, 40 steps 79 / 83).
+  const bool small = a.pass[0].K <= 32 && a.pass[0].V <= 32 && n * a.H * a.npass > 3 * 152;
+  if (a.T < (small ? 32 : 16) * (a.cu ? n : 1)) return false;
   for (int i = 0; i < a.npass; ++i) {
     const LinPass& p = a.pass[i];
     if (!heads_map_fits(p.x1, a.B, a.T, a.H) || !heads_map_fits(p.x2, a.B, a.T, a.H) ||

@@ -9,7 +9,7 @@ import torch
 
 import _mixer_ref as ref
 from _mixer_ref import f64, gate
-from test_gpu_mixers import BF, DEV, F32, calls, gen, lin_inputs, normal, tables
+from test_gpu_mixers import BF, DEV, F32, calls, decays, gen, lin_inputs, normal, tables
 
 pytestmark = pytest.mark.gpu
 
@@ -191,3 +191,31 @@ def test_window_scores_that_overflow_show(lib, dtype):
     assert o[0, 60, 1].isnan().all() and bool(lse[0, 1, 60].isnan())
     assert torch.equal(o[0, :60], want[0][0, :60]) and torch.equal(lse[0, :, :60], want[1][0, :, :60])
     assert torch.equal(o[0, 80:], want[0][0, 80:]) and torch.equal(lse[0, 0], want[1][0, 0])
+
+
+@pytest.mark.parametrize("T", [15, 16, 31, 32])
+@pytest.mark.parametrize("D,B", [(32, 30), (32, 80), (64, 80)])
+def test_linattn_short_rows(lib, T, D, B):
+    """Both sides of the length at which rows go by chunks, for few and many rows of
+    small heads: 16 steps, or 32."""
+    q, k, v, do, h0, dh = lin_inputs(B, T, 6, D, D, BF, T + B)
+    keep = [0, B // 2, B - 1]
+    few = lambda t: t[keep]  # noqa: E731
+    g = decays(6)
+    o, hT = lib.linattn_fwd(q, k, v, g, h0)
+    grads = lib.linattn_bwd(q, k, v, g, do, h0, None, dh)
+    args = [f64(few(t)) for t in (q, k, v)]
+    mags = [t.abs() for t in args]
+    ro, rh = ref.linattn(*args, f64(g), f64(few(h0)), None, D ** -0.5)
+    mo, mh = ref.linattn(*mags, f64(g), f64(few(h0)).abs(), None, D ** -0.5)
+    rg = ref.linattn_grads(*args, f64(g), f64(few(do)), f64(few(h0)), f64(few(dh)), None, D ** -0.5)
+    mg = ref.linattn_grads(*mags, f64(g), *(f64(few(t)).abs() for t in (do, h0, dh)), None, D ** -0.5)
+    # one rounding of a weight or of the state as it is read; the states by chunks: their
+    # update's operand in two bf16 parts at least, 2^-17 off
+    gate(few(o), ro, mo, dtype=BF, roundings=1, terms=T + D, name="o")
+    gate(few(hT), rh, mh, dtype=F32, terms=T + D + 2 ** 7, name="hT")
+    for got, want, mag, name in zip(grads, rg, mg, ("dq", "dk", "dv", "dh0")):
+        if name == "dh0":
+            gate(few(got), want, mag, dtype=F32, terms=T + D + 2 ** 7, name=name)
+        else:
+            gate(few(got), want, mag, dtype=BF, roundings=1, terms=T + D, name=name)
