@@ -26,6 +26,11 @@ if ROOT not in sys.path:
 import associative_affine_scan_gb300 as scan  # noqa: E402
 
 
+def _rows(grad):
+    """A gradient with a unit stride along D: a sum's, for one, is a broadcast number."""
+    return grad if grad.stride(-1) == 1 else grad.contiguous()
+
+
 class QkNormRope(torch.autograd.Function):
     @staticmethod
     def forward(ctx, q, k, q_weight, k_weight, cos, sin):
@@ -34,7 +39,7 @@ class QkNormRope(torch.autograd.Function):
 
     @staticmethod
     def backward(ctx, dq, dk):
-        return scan.qk_norm_rope_bwd(*ctx.saved_tensors, dq, dk) + (None, None)
+        return scan.qk_norm_rope_bwd(*ctx.saved_tensors, _rows(dq), _rows(dk)) + (None, None)
 
 
 class LinearAttention(torch.autograd.Function):
@@ -45,7 +50,7 @@ class LinearAttention(torch.autograd.Function):
 
     @staticmethod
     def backward(ctx, dout):
-        return scan.linattn_bwd(*ctx.saved_tensors, dout, need_dh0=False)[:3] + (None,)
+        return scan.linattn_bwd(*ctx.saved_tensors, _rows(dout), need_dh0=False)[:3] + (None,)
 
 
 class WindowAttention(torch.autograd.Function):
@@ -58,7 +63,7 @@ class WindowAttention(torch.autograd.Function):
 
     @staticmethod
     def backward(ctx, dout):
-        return scan.window_attn_bwd(*ctx.saved_tensors, dout, *ctx.sizes) + (None, None)
+        return scan.window_attn_bwd(*ctx.saved_tensors, _rows(dout), *ctx.sizes) + (None, None)
 
 
 @dataclass

@@ -65,3 +65,23 @@ def test_training_step_against_plain(lib, dtype, tol):
             got, ex = layer[n].grad.double().cpu(), p[n].grad
             rel = float((got - ex).norm() / ex.norm())
             assert rel <= tol, (n, rel)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_broadcast_gradients(lib, dtype):
+    """A sum of an operator's outputs: the gradient that comes back is one number,
+    broadcast, and counts as the same gradient written out."""
+    import hybrid_mixer as hm
+    g = torch.Generator().manual_seed(5)
+    q, k, v = (torch.randn(1, 70, 2, 64, generator=g).to(dtype).to("cuda").requires_grad_() for _ in range(3))
+    w = torch.ones(64, device="cuda")
+    angle = torch.arange(70.0, device="cuda")[:, None] * 10000.0 ** (-torch.arange(0, 64, 2, device="cuda") / 64)
+    cos, sin, decay = angle.cos(), angle.sin(), torch.full((2,), -0.1, device="cuda")
+    for call in (lambda: hm.QkNormRope.apply(q, k, w, w, cos, sin),
+                 lambda: (hm.LinearAttention.apply(q, k, v, decay),),
+                 lambda: (hm.WindowAttention.apply(q, k, v, 20, 2),)):
+        got = torch.autograd.grad(sum(y.sum() for y in call()), (q, k, v), allow_unused=True)
+        out = call()
+        want = torch.autograd.grad(out, (q, k, v), [torch.ones_like(y) for y in out], allow_unused=True)
+        for a, b in zip(got, want):
+            assert (a is None and b is None) or torch.equal(a, b)
