@@ -219,3 +219,28 @@ def test_linattn_short_rows(lib, T, D, B):
             gate(few(got), want, mag, dtype=F32, terms=T + D + 2 ** 7, name=name)
         else:
             gate(few(got), want, mag, dtype=BF, roundings=1, terms=T + D, name=name)
+
+
+@pytest.mark.parametrize("K,V", [(64, 64), (128, 64), (64, 128), (128, 128), (96, 40)])
+@pytest.mark.parametrize("T,at", [(16, 0), (16, 15), (100, 31), (128, 64), (300, 7), (300, 299), (5000, 1203)])
+def test_linattn_states_are_exact_to_fp32(lib, K, V, T, at):
+    """A row with one value row that is not zero: its last state is that step's product
+    times a power of the decay, a sum of one term, and so is the gradient of the
+    initial state for one output gradient. In units of 2^-24 of the element: two for
+    each unit of the power's exponent (the rounded log of the decay and its product
+    with the steps), 16 for the exponential, the weights and the three adds of the
+    term's three bf16 parts, 8 a chunk for the powers that the state is multiplied
+    with. A term of two parts would be up to 128 off."""
+    H = 5
+    g = -torch.tensor([0.0, 1e-4, 3e-3, 0.02, 0.1], device=DEV) * min(1.0, 300 / T)
+    k, q = normal(gen(T), 1, T, H, K, dtype=BF), normal(gen(T + 1), 1, T, H, K, dtype=BF)
+    v, do = torch.zeros(1, T, H, V, dtype=BF, device=DEV), torch.zeros(1, T, H, V, dtype=BF, device=DEV)
+    v[:, at], do[:, at] = normal(gen(T + 2), 1, H, V, dtype=BF), normal(gen(T + 3), 1, H, V, dtype=BF)
+    _, hT = lib.linattn_fwd(q, k, v, g, scale=0.5)
+    dh0 = lib.linattn_bwd(q, k, v, g, do, scale=0.5)[3]
+    for got, x, y, n, mul in ((hT, k, v, T - 1 - at, 1.0), (dh0, q, do, at + 1, 0.5)):
+        power = (f64(g) * n)[:, None, None]
+        want = mul * power.exp() * f64(x[0, at])[:, :, None] * f64(y[0, at])[:, None, :]
+        units = 2 * power.abs() + 16 + 8 * (T // 128 + 1)
+        bad = (f64(got[0]) - want).abs() > units * 2.0 ** -24 * want.abs() + 1e-37
+        assert not bad.any(), (int(bad.sum()), float(((f64(got[0]) - want).abs() / want.abs().clamp(min=1e-37)).max()) * 2 ** 24)
