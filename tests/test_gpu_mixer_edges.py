@@ -9,7 +9,8 @@ import torch
 
 import _mixer_ref as ref
 from _mixer_ref import f64, gate
-from test_gpu_mixers import BF, DEV, F32, calls, decays, gen, lin_inputs, normal, tables
+from test_gpu_mixers import (BF, DEV, F32, calls, decays, gen, lin_inputs, normal, offsets, tables, win_check,
+                             win_inputs)
 
 pytestmark = pytest.mark.gpu
 
@@ -244,3 +245,10 @@ def test_linattn_states_are_exact_to_fp32(lib, K, V, T, at):
         units = 2 * power.abs() + 16 + 8 * (T // 128 + 1)
         bad = (f64(got[0]) - want).abs() > units * 2.0 ** -24 * want.abs() + 1e-37
         assert not bad.any(), (int(bad.sum()), float(((f64(got[0]) - want).abs() / want.abs().clamp(min=1e-37)).max()) * 2 ** 24)
+
+
+@pytest.mark.parametrize("lengths", [[1], [130, 1, 127, 0, 256, 70], [300, 1, 1, 400], [513, 900]])
+@pytest.mark.parametrize("Hq,Hk,W,S", [(1, 1, 64, 0), (4, 2, 100, 4), (3, 1, 129, 130)])
+def test_window_packed_heads_of_128(lib, lengths, Hq, Hk, W, S):
+    T = sum(lengths)
+    win_check(lib, win_inputs(1, T, T, Hq, Hk, 128, BF, T + W), W, S, cu=offsets(lengths))
