@@ -96,7 +96,7 @@ __device__ __forceinline__ float log2_decay(float log_decay) {
 struct Span {
   int64_t beg, len;  // the sequence
   int64_t first;     // first chunk of the segment, in processing order
-  int nch;           // chunks of the segment
+  int nch;           // chunks of the segment, one at least
 };
 
 // Where the c-th chunk of the segment lies, and how many steps it holds.
@@ -310,7 +310,7 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_co
     for (int x = 0; x < 32; ++x) r[x] = __float_as_uint(__uint_as_float(r[x]) * keep);
     tmem_st32(tSt + lanes + 32 * kb, r);
   };
-  if (!STATE_ONLY && s0 && s.nch > 0 && role < KP / 32) {
+  if (!STATE_ONLY && s0 && role < KP / 32) {
     // the state that comes in: 32 of its rows a role, all loads in flight at once
     const int v = tid % 128;
     int64_t t0;
@@ -366,8 +366,8 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_co
         mma_kk<KP, kHalf, kHalf>(lead, tS1, x1, x1 + (P::kX1 >> 4), dS1, false);
         mma_commit(lead, bS1);
       };
-      bool ok = s.nch > 0;
-      if (!STATE_ONLY && ok && (ok = ready(0))) scores(0);
+      bool ok = true;
+      if (!STATE_ONLY && (ok = ready(0))) scores(0);
 #pragma unroll 1
       for (int c = 0; ok && c < s.nch; ++c) {
         const int st = c % P::kStages;
@@ -664,28 +664,19 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_co
   if (role == 1 && s1) {
     // ---- the final state, by the state's role: column v in lane v
     const int v = tid % 128;
-    bool ok = true;
-    if (s.nch > 0) {
-      ok = warp_wait(bSt, STATE_ONLY ? 0 : (s.nch - 1) & 1, stop);
+    if (warp_wait(bSt, STATE_ONLY ? 0 : (s.nch - 1) & 1, stop)) {
       fence_after();
-    }
-    if (ok) {
       // a segment on its own starts from nothing: what came in is added here
-      const float in = STATE_ONLY ? s0m * exp2f(l2 * (float)steps) : s0m;
-      const bool add = s0 && (STATE_ONLY || s.nch == 0);
+      const float in = s0m * exp2f(l2 * (float)steps);
+      const bool add = STATE_ONLY && s0;
       const bool on = v < p.V;
       const float* const si = add ? s0 + (on ? v : 0) * s0v : nullptr;
       float* const so = s1 + v;
 #pragma unroll 1
       for (int kb = 0; kb < KP / 32; ++kb) {
         uint32_t r[32];
-        if (s.nch > 0) {
-          tmem_ld32(tSt + lanes + 32 * kb, r);
-          ld_wait();
-        } else {
-#pragma unroll
-          for (int x = 0; x < 32; ++x) r[x] = 0;
-        }
+        tmem_ld32(tSt + lanes + 32 * kb, r);
+        ld_wait();
         if (add) {
           float f[32];
 #pragma unroll

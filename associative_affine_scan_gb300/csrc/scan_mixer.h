@@ -25,11 +25,6 @@ struct View {
   }
 };
 
-template <typename T>
-inline View<T> view_of(const scan_view4* v) {
-  return View<T>{static_cast<T*>(v->ptr), v->stride_b, v->stride_t, v->stride_h};
-}
-
 __device__ __forceinline__ float to_f32(float x) { return x; }
 __device__ __forceinline__ float to_f32(__nv_bfloat16 x) { return __bfloat162float(x); }
 template <typename T>
@@ -39,11 +34,6 @@ __device__ __forceinline__ float from_f32<float>(float x) { return x; }
 template <>
 __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float x) {
   return __float2bfloat16_rn(x);
-}
-
-// lambda^n from log2(lambda); 1 at n = 0 also where lambda is 0.
-__device__ __forceinline__ float decay_pow(float log2_lambda, int n) {
-  return n == 0 ? 1.f : exp2f(log2_lambda * (float)n);
 }
 
 // Bounds of sequence i, forced into [0, T] whatever the device array holds, so
@@ -154,7 +144,6 @@ struct WinArgs {
   float scale;
   WsHeader* hdr;
   float* ws;
-  size_t ws_floats;
 };
 
 // Tiles of `rows` keys that the queries at positions [p0, p1] see: those that hold

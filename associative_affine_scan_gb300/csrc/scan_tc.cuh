@@ -116,10 +116,6 @@ __device__ __forceinline__ void copy_out_4d(const CUtensorMap* map, uint32_t src
 __device__ __forceinline__ void copy_out_commit() {
   asm volatile("cp.async.bulk.commit_group;" ::: "memory");
 }
-// Until the copies committed by this thread have read their shared memory.
-__device__ __forceinline__ void copy_out_read() {
-  asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-}
 __device__ __forceinline__ void copy_out_done() {
   asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
 }
@@ -295,11 +291,6 @@ __device__ __forceinline__ uint32_t swizzled(uint32_t panel, int row, int piece)
 __device__ __forceinline__ void st_shared16(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d)
                : "memory");
-}
-__device__ __forceinline__ uint32_t ld_shared_u16(uint32_t addr) {
-  uint16_t v;
-  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(addr));
-  return v;
 }
 }  // namespace tc
 

@@ -320,7 +320,6 @@ scan_status win_workspace(WinArgs* a, void* ws, size_t bytes, size_t need) {
   if (!ws || (uintptr_t)ws % 16 || bytes < need) return SCAN_ERR_WORKSPACE;
   a->hdr = static_cast<WsHeader*>(ws);
   a->ws = reinterpret_cast<float*>(static_cast<char*>(ws) + kWsHeaderBytes);
-  a->ws_floats = (need - kWsHeaderBytes) / 4;
   return SCAN_OK;
 }
 
