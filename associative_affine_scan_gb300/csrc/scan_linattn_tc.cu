@@ -20,6 +20,10 @@
 //                 update is then exact to 2^-17 (2^-24), so that the state, fp32 in
 //                 tensor memory, keeps that accuracy over any number of chunks
 //   output        O *= lambda^(r + e) between the two products into it; O to bf16
+// P, and the state as x1 reads it, are rounded once to bf16, the type that the tensor
+// cores take next to bf16 operands: each term of an output is off by 2^-9 of itself at
+// most, which is the size of the output's own rounding. Neither is carried on: the state
+// itself and all sums stay in 32 bits.
 // The state lies transposed (lanes are v): its bf16 copy is then written by rows
 // into the operand layout, and the weighted operand of the update is one that the
 // tensor cores read from tensor memory, which shared memory has no room for.
@@ -29,8 +33,8 @@
 // the state before it. This reads x2 and x3 twice.
 //
 // Heads of 128 x 128, bf16. 16384 steps of 16 heads (one row): own states 31 us, chain
-// 6 us, chunks 62 us (269 MB, 4.3 TB/s). 4 x 4096 steps of 16 heads: own states 20 us,
-// chunks 63 us; backward, three passes at once, 215 us (805 MB, 3.7 TB/s). A chunk
+// 6 us, chunks 62 us (269 MB, 4.3 TB/s). 4 x 4096 steps of 16 heads: own states 19 us,
+// chunks 61 us; backward, three passes at once, 213 us (805 MB, 3.8 TB/s). A chunk
 // takes two to three times the tensor cores' cycles (busy for 39 % of a block's): each
 // product waits for operands that another role makes from the one before it, and every
 // wait or commit of the product warp costs 100 to 200 cycles, so that fewer of them, not

@@ -20,7 +20,7 @@
 // the number of rows in flight: they stay in their own type until they are used.
 //
 // Forward of 8 x 4096 tokens, 16 + 4 heads of 128, bf16: 57 us, 5.9 TB/s, bound by
-// DRAM. Backward: 96 us, 5.3 TB/s, bound half by DRAM and half by the issue of
+// DRAM. Backward: 95 us, 5.3 TB/s, bound half by DRAM and half by the issue of
 // instructions (scalar arithmetic and two heads a group: 116 us). A ring of
 // asynchronous copies to shared memory, two items ahead, took 175 us, and the next
 // item's rows in registers 145 us: a lane's copies of 8 bytes and what they spill cost

@@ -8,8 +8,8 @@
 // Two kernels, each with its sums in tensor memory and no sum across blocks: the
 // five products become seven, but no result depends on the order in which blocks
 // run and nothing is added in global memory. 2 x 4096 tokens, 16 query heads of 128
-// over 4 key heads, window 1024: keys 155 us (0.78 PFLOP/s of seen pairs' four products),
-// queries 131 us (0.69, three products), row sums 14 us, pieces 5 us.
+// over 4 key heads, window 1024: keys 157 us (0.77 PFLOP/s of seen pairs' four products),
+// queries 132 us (0.69, three products), row sums 14 us, pieces 5 us.
 //   keys:    a block owns 128 keys and walks the tiles of 128 queries that see
 //            them: S = k q^T, dP = v do^T, dv += P do, dk += dS q. Keys are the
 //            rows of S, so P and dS (bf16, over S and dP in tensor memory) are
@@ -357,6 +357,9 @@ __global__ void __launch_bounds__(kThreads, 1) window_dkv_kernel(const __grid_co
           }
       }
       {
+        // P and, below, dS go to the products as bf16, the type that the tensor cores take
+        // next to bf16 operands: off by 2^-9 of themselves at most. dS is formed from the P
+        // of 32 bits, and all sums are of 32 bits.
         uint32_t o[32];
 #pragma unroll
         for (int i = 0; i < 2; ++i)
@@ -669,6 +672,7 @@ __global__ void __launch_bounds__(kThreadsDq, 1) window_dq_kernel(const __grid_c
             const float v = p * (__uint_as_float(d[c + y]) - delta);
             e[y] = whole || p != 0.f ? v : 0.f;
           }
+          // (bf16 as in the keys' kernel)
           o[16 * i + c / 2] = pack_bf16(e[0], e[1]);
         }
       }

@@ -5,7 +5,8 @@
 // share a key head where their number is even, else 256 rows of one head. It
 // walks the tiles of 128 keys that the queries see -- those of the first tokens,
 // then those of the window -- in one pass with the running maximum m and sum l of
-// each row's softmax:
+// each row's softmax (Milakov and Gimelshein, "Online normalizer calculation for
+// softmax"):
 //   s = scale q k, p = 2^(s log2(e) - m), l = sum p, o = sum p v; at the end o / l.
 // Two products of 128 x 128 x D a tile (1024 tensor cycles at D = 128) against
 // 128 exponentials a row, so the two tiles take turns: while one's softmax runs,
@@ -20,11 +21,11 @@
 // by more than 2^8: until then p stays below 2^8, which changes no rounding (bf16
 // and fp32 have the same exponents), and the outputs need no rescaling.
 //
-// 16384 tokens, 16 query heads of 128 over 4 key heads, window 2048: 266 us, 0.97 PFLOP/s
-// of seen pairs; 2 x 4096 tokens, window 1024: 89 us, 0.68 PFLOP/s. The tensor cores are
+// 16384 tokens, 16 query heads of 128 over 4 key heads, window 2048: 269 us, 0.96 PFLOP/s
+// of seen pairs; 2 x 4096 tokens, window 1024: 91 us, 0.67 PFLOP/s. The tensor cores are
 // busy for half of a block's cycles: scores, weights and outputs pass from role to role
 // twice a tile, and tiles at the window's edges and of the first tokens are worked in
-// whole. A second product warp, one a query tile, took 306 us for 266.
+// whole. A second product warp, one a query tile, took 306 us for 266 at the time.
 #include "scan_tc.cuh"
 #include "scan_window_tc.h"
 
@@ -313,6 +314,9 @@ __global__ void __launch_bounds__(kThreads, 1) window_fwd_kernel(const __grid_co
         m = mn;
       }
       const float from = m == -INFINITY ? 0.f : m;
+      // p goes to the product as bf16, the type that the tensor cores take next to bf16
+      // values: each weight is off by 2^-9 of itself at most, the output by about one
+      // rounding of its own type. The sum l is of p before that, in fp32.
       float2 sum[4] = {};
       const float2 f2 = make_float2(-from, -from), sl2 = make_float2(a.sl2, a.sl2);
       {

@@ -11,8 +11,9 @@
 // pieces, and the columns of the output are the elements in the order 8 n + j.
 // Fragments of V pair two keys' elements. The warps of a block take different keys of
 // one key head, or with many requests different key heads of the same keys (neighbours
-// in the cache). 64 requests of 4100 keys, 4 key heads of 128: 106 us, 5.1 TB/s, set by
+// in the cache). 64 requests of 4100 keys, 4 key heads of 128: 107 us, 5.0 TB/s, set by
 // the bytes in flight; 32-byte loads a lane were slower (174 us for 136 at the time).
+// One request of 2052 keys: 14 us with its rows from DRAM, 9 us from L2.
 //
 // A request's keys are split over the blocks of a cluster (up to 16) when the
 // requests alone do not fill the SMs; the partial maxima, sums and outputs meet
@@ -184,6 +185,8 @@ __global__ void __launch_bounds__(32 * kWarps, ROWS == 8 ? 3 : 2) window_step_ke
           acc[i][j][2 * h + 1] *= keep;
         }
     }
+    // (weights as bf16, as the values they multiply: off by 2^-9 of themselves at most; l is
+    // the sum of the unrounded ones)
     const uint32_t a0 = pack2(p[0][0], p[0][1]), a2 = pack2(p[1][0], p[1][1]);
     const uint32_t a1 = ROWS == 16 ? pack2(p[0][2], p[0][3]) : 0u, a3 = ROWS == 16 ? pack2(p[1][2], p[1][3]) : 0u;
 #pragma unroll
