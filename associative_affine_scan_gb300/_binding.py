@@ -13,6 +13,7 @@ from __future__ import annotations
 import ctypes
 import os
 import struct
+import sys
 import threading
 from typing import Optional
 
@@ -284,6 +285,7 @@ class _Workspaces:
         self._buf = {}
         self._captured = set()  # keys whose buffer a CUDA graph uses
         self._held = {}         # buffers of a key that graphs use and larger ones have replaced
+        self._replaced = []     # (device, buffer): other replaced ones, until nothing uses them
         self._lk = threading.Lock()
 
     def get(self, nbytes: int, device: torch.device, stream: ctypes.c_void_p) -> torch.Tensor:
@@ -298,18 +300,22 @@ class _Workspaces:
                 # kernel on `stream` may still read it) and before a new block,
                 # which may still be in use by work queued on another stream,
                 # is zeroed on `stream`. Buffers only grow, so this is rare.
+                # A call of another thread may hold the smaller buffer and launch after
+                # this wait, so it is kept at first. A replaced one that no call holds
+                # (this list, the loop and the count are its three references) has all
+                # its launches behind it, and after the wait their work too.
+                idle = {id(b) for d, b in self._replaced if d == device and sys.getrefcount(b) <= 3}
                 torch.cuda.synchronize(device)
-                buf = torch.empty(size, dtype=torch.uint8, device=device)
-                # a call that was handed this buffer may still launch after another
-                # thread has put a larger one in its place: once freed it is reused
-                # only when the work queued on `stream` by then is done
-                buf.record_stream(torch.cuda.ExternalStream(stream.value or 0, device=device))
-                _check(_call(device, "scan_workspace_init", _ptr(buf), size, stream),
+                self._replaced = [e for e in self._replaced if id(e[1]) not in idle]
+                new = torch.empty(size, dtype=torch.uint8, device=device)
+                _check(_call(device, "scan_workspace_init", _ptr(new), size, stream),
                        "scan_workspace_init")
                 if key in self._captured:  # its graph may be replayed at any time
                     self._captured.discard(key)
-                    self._held.setdefault(key, []).append(self._buf[key])
-                self._buf[key] = buf
+                    self._held.setdefault(key, []).append(buf)
+                elif buf is not None:
+                    self._replaced.append((device, buf))
+                self._buf[key] = buf = new
             if torch.cuda.is_current_stream_capturing():
                 self._captured.add(key)
             return buf

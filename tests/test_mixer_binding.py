@@ -51,12 +51,11 @@ def test_workspace_lives_until_the_call_has_returned(monkeypatch, name):
 @pytest.mark.parametrize("captured", [False, True])
 def test_a_larger_workspace_leaves_the_captured_one(monkeypatch, captured):
     """A graph writes into the workspace of its capture whenever it is replayed:
-    the buffer stays when a later call needs a larger one, and only then."""
+    the buffer stays when later calls need larger ones. Any other goes when the
+    next one is replaced."""
     import ctypes
     monkeypatch.setattr(_binding, "_call", lambda *a: scan.SCAN_OK)
     monkeypatch.setattr(_binding.torch.cuda, "synchronize", lambda device: None)
-    monkeypatch.setattr(_binding.torch.cuda, "ExternalStream", lambda *a, **k: None)
-    monkeypatch.setattr(torch.Tensor, "record_stream", lambda self, stream: None)
     monkeypatch.setattr(_binding.torch.cuda, "is_current_stream_capturing", lambda: capturing)
     pool, dev, s = _binding._Workspaces(), torch.device("cpu"), ctypes.c_void_p(3)
     capturing = False
@@ -66,10 +65,33 @@ def test_a_larger_workspace_leaves_the_captured_one(monkeypatch, captured):
     capturing = False
     other = weakref.ref(pool.get(5000, dev, ctypes.c_void_p(4)))
     second = weakref.ref(pool.get(9000, dev, s))
-    assert pool.get(9000, dev, s) is second() and (first() is not None) == captured
+    assert pool.get(9000, dev, s) is second() and first() is not None
     pool.get(20000, dev, s)
+    assert second() is not None and (first() is not None) == captured
+    pool.get(30000, dev, s)
     pool.get(20000, dev, ctypes.c_void_p(4))
+    pool.get(30000, dev, ctypes.c_void_p(4))
     assert second() is None and other() is None and (first() is not None) == captured
+
+
+def test_a_replaced_workspace_stays_while_a_call_holds_it(monkeypatch):
+    """A thread between its look-up and its launch, while others need ever larger
+    buffers: its own goes only with a wait for the device that comes after."""
+    import ctypes
+    monkeypatch.setattr(_binding, "_call", lambda *a: scan.SCAN_OK)
+    monkeypatch.setattr(_binding.torch.cuda, "is_current_stream_capturing", lambda: False)
+    pool, dev, s = _binding._Workspaces(), torch.device("cpu"), ctypes.c_void_p(3)
+    waits = []
+    monkeypatch.setattr(_binding.torch.cuda, "synchronize", lambda device: waits.append(mine() is not None))
+    mine = lambda: None  # noqa: E731
+    handed = pool.get(5000, dev, s)
+    mine = weakref.ref(handed)
+    for n in range(2, 6):
+        pool.get(5000 * n, dev, s)
+    del handed  # the launch has been made
+    assert mine() is not None
+    pool.get(40000, dev, s)
+    assert waits == [False] + [True] * 5 and mine() is None
 
 
 def test_no_finding_is_lost(monkeypatch):
