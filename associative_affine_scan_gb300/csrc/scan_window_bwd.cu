@@ -75,6 +75,11 @@ __device__ __forceinline__ void clear_rows(uint32_t tile, int from, int t) {
   __syncwarp();
 }
 
+// What a pair of bf16 numbers leaves of the numbers they were rounded from, as bf16.
+__device__ __forceinline__ uint32_t rest_bf16(uint32_t h, float a, float b) {
+  return pack_bf16(a - __uint_as_float(h << 16), b - __uint_as_float(h & 0xffff0000u));
+}
+
 // A row of D fp32 sums in tensor memory times f, as bf16: to a tile in shared
 // memory, or straight to `out`.
 template <int DP>
@@ -148,7 +153,7 @@ __global__ void __launch_bounds__(256) window_delta16_kernel(const DeltaArgs a) 
   }
 }
 
-template <int DP>
+template <int DP, bool TWO>
 __global__ void __launch_bounds__(kThreads, 1) window_dkv_kernel(const __grid_constant__ BwdArgs a) {
   using P = Plan<DP>;
   constexpr int NS = P::kSlots;
@@ -285,6 +290,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_dkv_kernel(const __grid_co
         if (!(ok = warp_wait(bDs, u & 1, stop))) break;
         fence_after();
         second(tDk, tDp, slot_mn(2 * u), u > 0);
+        if (TWO) second(tDk, tDp + 32, slot_mn(2 * u), true);
         mma_commit(lead, bEmpty + 8 * (2 * u % NS));
         mma_commit(lead, bEmpty + 8 * ((2 * u + 1) % NS));
         if (u + 1 < n) {
@@ -358,8 +364,8 @@ __global__ void __launch_bounds__(kThreads, 1) window_dkv_kernel(const __grid_co
       }
       {
         // P and, below, dS go to the products as bf16, the type that the tensor cores take
-        // next to bf16 operands: off by 2^-9 of themselves at most. dS is formed from the P
-        // of 32 bits, and all sums are of 32 bits.
+        // next to bf16 operands: off by 2^-9 of themselves at most (TWO: dS as two parts, off
+        // by 2^-18). dS is formed from the P of 32 bits, and all sums are of 32 bits.
         uint32_t o[32];
 #pragma unroll
         for (int i = 0; i < 2; ++i)
@@ -395,7 +401,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_dkv_kernel(const __grid_co
       if (!(ok = warp_wait(bDelta, u & 1, stop))) break;
       if (!(ok = warp_wait(bDp, u & 1, stop))) break;
       fence_after();
-      uint32_t o[32];
+      uint32_t o[32], rest[TWO ? 32 : 1];
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         uint32_t d[32];
@@ -411,9 +417,11 @@ __global__ void __launch_bounds__(kThreads, 1) window_dkv_kernel(const __grid_co
             e[y] = whole || p != 0.f ? v : 0.f;  // what lies outside may be anything
           }
           o[16 * i + c / 2] = pack_bf16(e[0], e[1]);
+          if (TWO) rest[16 * i + c / 2] = rest_bf16(o[16 * i + c / 2], e[0], e[1]);
         }
       }
       tmem_st32(tDp + lanes + 64 * w, o);
+      if constexpr (TWO) tmem_st32(tDp + lanes + 64 * w + 32, rest);
       if (past < kRows) clear_rows<DP>(sR + (2 * u % NS) * P::kTileBytes, past, tid);
       st_wait();
       fence_before();
@@ -503,7 +511,7 @@ __global__ void __launch_bounds__(256) window_pieces_kernel(const __grid_constan
 
 // ---------------------------------------------------------------------------
 
-template <int DP>
+template <int DP, bool TWO>
 __global__ void __launch_bounds__(kThreadsDq, 1) window_dq_kernel(const __grid_constant__ BwdArgs a) {
   using P = Plan<DP>;
   constexpr int NS = P::kSlots;
@@ -596,6 +604,10 @@ __global__ void __launch_bounds__(kThreadsDq, 1) window_dq_kernel(const __grid_c
         const uint32_t w = tS + 128 * (u & 1), t = mnmajor(sR, kHalf) + slot(2 * u);
         mma_tn<64>(lead, tDq, w, t, dO, u > 0);
         mma_tn<64>(lead, tDq, w + 64, t + (64 * kPitch >> 4), dO, true);
+        if (TWO) {
+          mma_tn<64>(lead, tDq, w + 32, t, dO, true);
+          mma_tn<64>(lead, tDq, w + 96, t + (64 * kPitch >> 4), dO, true);
+        }
         mma_commit(lead, bEmpty + 8 * (2 * u % NS));
         if (u + 2 < n) {
           if (!(ok = full(2 * u + 4))) break;
@@ -657,7 +669,7 @@ __global__ void __launch_bounds__(kThreadsDq, 1) window_dq_kernel(const __grid_c
       }
       if (!(ok = warp_wait(bDp, u & 1, stop))) break;
       fence_after();
-      uint32_t o[32];
+      uint32_t o[32], rest[TWO ? 32 : 1];
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         uint32_t d[32];
@@ -672,11 +684,13 @@ __global__ void __launch_bounds__(kThreadsDq, 1) window_dq_kernel(const __grid_c
             const float v = p * (__uint_as_float(d[c + y]) - delta);
             e[y] = whole || p != 0.f ? v : 0.f;
           }
-          // (bf16 as in the keys' kernel)
+          // (one bf16 part or two, as in the keys' kernel)
           o[16 * i + c / 2] = pack_bf16(e[0], e[1]);
+          if (TWO) rest[16 * i + c / 2] = rest_bf16(o[16 * i + c / 2], e[0], e[1]);
         }
       }
       tmem_st32(tS + 128 * (u & 1) + lanes + 64 * w, o);
+      if constexpr (TWO) tmem_st32(tS + 128 * (u & 1) + lanes + 64 * w + 32, rest);
       if (a.cu && j0 + kRows > g.nk)  // key rows of the next sequence (its scores are done)
         clear_rows<DP>(sR + (2 * u % NS) * P::kTileBytes, (int)(g.nk - j0), tid);
       st_wait();
@@ -719,19 +733,19 @@ __global__ void __launch_bounds__(kThreadsDq, 1) window_dq_kernel(const __grid_c
   }
 }
 
-template <int DP>
+template <int DP, bool TWO>
 cudaError_t launch_bwd(const BwdArgs& t, int64_t B, cudaStream_t s) {
   using P = Plan<DP>;
   static_assert(P::kSmem <= 232448, "fits a block's shared memory");
-  cudaError_t e = cudaFuncSetAttribute(window_dkv_kernel<DP>, cudaFuncAttributeMaxDynamicSharedMemorySize, P::kSmem);
+  cudaError_t e = cudaFuncSetAttribute(window_dkv_kernel<DP, TWO>, cudaFuncAttributeMaxDynamicSharedMemorySize, P::kSmem);
   if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(window_dq_kernel<DP>, cudaFuncAttributeMaxDynamicSharedMemorySize, P::kSmem);
+    e = cudaFuncSetAttribute(window_dq_kernel<DP, TWO>, cudaFuncAttributeMaxDynamicSharedMemorySize, P::kSmem);
   if (e != cudaSuccess) return e;
   const int64_t extra = t.cu ? t.n_seqs : 0;
   const int64_t tk = (t.Tk + kRows - 1) / kRows + extra, tq = (t.Tq + kRows - 1) / kRows + extra;
   const int64_t cut = t.pieces > 1 ? (int64_t)t.sink_tiles * (t.pieces - 1) : 0;
-  window_dkv_kernel<DP><<<dim3((unsigned)(tk + cut), (unsigned)(B * t.Hk)), kThreads, P::kSmem, s>>>(t);
-  window_dq_kernel<DP><<<dim3((unsigned)tq, (unsigned)(B * t.Hq)), kThreadsDq, P::kSmem, s>>>(t);
+  window_dkv_kernel<DP, TWO><<<dim3((unsigned)(tk + cut), (unsigned)(B * t.Hk)), kThreads, P::kSmem, s>>>(t);
+  window_dq_kernel<DP, TWO><<<dim3((unsigned)tq, (unsigned)(B * t.Hq)), kThreadsDq, P::kSmem, s>>>(t);
   if (t.pieces > 1)
     window_pieces_kernel<<<dim3((unsigned)(t.sink_tiles * kRows), (unsigned)(B * t.Hk)), 256, 0, s>>>(t);
   return cudaGetLastError();
@@ -750,6 +764,19 @@ Cut cut_sinks(int64_t Tq, int64_t Tk, int64_t W, int64_t S, bool packed) {
   if (p > 64) p = 64;
   if (p < 2 || tiles > 16) return Cut{0, 1};
   return Cut{(int)tiles, (int)p};
+}
+
+// Whether dS goes to its products as the sum of two bf16 parts. delta comes from the
+// output as it was rounded, which is felt where a row sees few keys (an error of
+// (keys / e - 1)^(-1/2) roundings for scores of unit variance): together with the rounding
+// of dS it would be more than the gradients' own. Short rows, and narrow windows, so take
+// the two parts; elsewhere one rounding is what is left. Error of dq and dk in the 2-norm
+// and us of the backward, one part / two, 16 heads of 128 over 4: 4 x 64 tokens 2.6e-3 /
+// 2.0e-3, 24 / 26 us; 2 x 512 2.5e-3 / 1.9e-3, 48 / 55 us; 2 x 4096, window 1024 2.4e-3 /
+// 1.8e-3, 302 / 346 us (rounding the exact gradients alone: 1.7e-3).
+bool two_parts(const WinArgs& a) {
+  const int64_t len = a.cu ? a.Tk / a.n_seqs : a.Tk;  // of a sequence, in the mean
+  return len <= 512 || a.W + a.S <= 32;
 }
 
 }  // namespace
@@ -806,7 +833,9 @@ cudaError_t launch_window_tc_bwd(const WinArgs& a, float* part, cudaStream_t s) 
   t.pieces = c.pieces;
   t.sl2 = a.scale * 1.44269504088896341f;
   t.scale = a.scale;
-  return a.D <= 64 ? launch_bwd<64>(t, a.B, s) : launch_bwd<128>(t, a.B, s);
+  const bool two = two_parts(a);
+  if (a.D <= 64) return two ? launch_bwd<64, true>(t, a.B, s) : launch_bwd<64, false>(t, a.B, s);
+  return two ? launch_bwd<128, true>(t, a.B, s) : launch_bwd<128, false>(t, a.B, s);
 }
 
 }  // namespace scan

@@ -252,3 +252,35 @@ def test_linattn_states_are_exact_to_fp32(lib, K, V, T, at):
 def test_window_packed_heads_of_128(lib, lengths, Hq, Hk, W, S):
     T = sum(lengths)
     win_check(lib, win_inputs(1, T, T, Hq, Hk, 128, BF, T + W), W, S, cu=offsets(lengths))
+
+
+@pytest.mark.parametrize("T,W,S,lengths", [(64, 1000, 0, None), (200, 1000, 4, None), (512, 1000, 4, None), (900, 20, 4, None),
+                                           (378, 138, 4, [20, 100, 60, 150, 48]), (1500, 300, 0, [500, 31, 469, 500])])
+@pytest.mark.parametrize("D", [64, 96, 128])
+def test_window_gradients_where_rows_see_few_keys(lib, T, W, S, lengths, D):
+    """dq and dk in the 2-norm against 64 bits: the rounding of the result to bf16, and
+    what a delta from the rounded output leaves, both taken from the exact values;
+    a tenth more for all else, which 32 bits hold. One more rounding, of dS, would add
+    as much as the first."""
+    cu = None if lengths is None else offsets(lengths)
+    q, k, v, do = win_inputs(1, T, T, 6, 2, D, BF, T + D)
+    o, lse = lib.window_attn_fwd(q, k, v, W, S, cu)
+    got = lib.window_attn_bwd(q, k, v, o, lse, do, W, S, cu)
+    args, c, scale = [f64(t) for t in (q, k, v, do)], None if cu is None else cu.cpu(), D ** -0.5
+    want, _ = ref.window_grads(*args, W, S, c, scale)
+    ro, _ = ref.window(*args[:3], W, S, c, scale)
+    # a change of delta_i by e_i changes dq_i by -e_i sum_j p_ij k_j scale, and dk alike:
+    # the gradients of sum (e_i log-sum-exp_i)
+    e = ((ro.to(BF).double() - ro) * args[3]).sum(-1).transpose(1, 2)  # [B, Hq, T]
+    leaves = [args[0].clone().requires_grad_(), args[1].clone().requires_grad_()]
+    loss = 0.0
+    for _, lo, hi in ref.sequences(1, T, c):
+        s = torch.einsum("ihd,jhd->hij", leaves[0][0, lo:hi], leaves[1][0, lo:hi].repeat_interleave(3, 1)) * scale
+        s = s.masked_fill(~ref.visible(hi - lo, hi - lo, W, S), -torch.inf)
+        loss = loss + (torch.logsumexp(s, -1) * e[0, :, lo:hi]).sum()
+    moved = torch.autograd.grad(loss, leaves)
+    for g, w, m, name in zip(got, want, moved, ("dq", "dk")):
+        rounded = float((w.to(BF).double() - w).norm() / w.norm())
+        limit = 1.1 * (rounded ** 2 + float(m.norm() / w.norm()) ** 2) ** 0.5
+        err = float((f64(g) - w).norm() / w.norm())
+        assert err <= limit, (name, err, limit, rounded)
