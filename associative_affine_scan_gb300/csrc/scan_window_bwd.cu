@@ -15,7 +15,8 @@
 //            rows of S, so P and dS (bf16, over S and dP in tensor memory) are
 //            read as they lie by the two second products.
 //   queries: a block owns 128 queries of a head and walks the key tiles they see:
-//            S = q k^T, dP = do v^T, dq += dS k.
+//            S = q k^T, dP = do v^T, dq += dS k. It runs first: where the queries see one
+//            tile, it forms their delta anew from p and dP, for the keys' kernel as well.
 // The order of issue keeps the tensor cores busy while two warpgroups turn S and
 // dP into P and dS, half of the columns each: the first product of the next tile
 // is issued between the two that wait for them. Both are bound by that chain: the tensor
@@ -47,7 +48,7 @@ struct BwdArgs {
   __nv_bfloat16 *dqp, *dkp, *dvp;
   int64_t dq_sb, dq_st, dq_sh, dk_sb, dk_st, dk_sh, dv_sb, dv_st, dv_sh;
   const float* lse;
-  const float* delta;
+  float* delta;
   float* part;  // [B, Hk, pieces, sink tiles, 2, 128, D]
   const int32_t* cu;
   WsHeader* hdr;
@@ -523,9 +524,10 @@ __global__ void __launch_bounds__(kThreadsDq, 1) window_dq_kernel(const __grid_c
   uint32_t* const misc = reinterpret_cast<uint32_t*>(gen + (2 + NS) * P::kTileBytes);
   const uint32_t bars = smem_addr(misc);
   const uint32_t bQ = bars, bFull = bars + 8, bEmpty = bFull + 8 * NS, bS = bEmpty + 8 * NS, bDp = bS + 16,
-                 bDs = bDp + 8, bEnd = bDs + 8 * kDsBarriers, bOut = bEnd + 8;
+                 bDs = bDp + 8, bEnd = bDs + 8 * kDsBarriers, bOut = bEnd + 8, bRow = bOut + 8;
   uint32_t* const tmem_ptr = misc + 64;
   uint32_t* const stop_flag = misc + 65;
+  float* const s_row = reinterpret_cast<float*>(misc + 72);  // a row's sum of p dP, of each half of the columns
 
   TileRows g;
   if (!tile_rows(a.cu, a.n_seqs, a.Tq, a.Tk, blockIdx.x, kRows, &g)) return;
@@ -556,6 +558,7 @@ __global__ void __launch_bounds__(kThreadsDq, 1) window_dq_kernel(const __grid_c
     for (int i = 0; i < kDsBarriers; ++i) bar_init(bDs + 8 * i, 8);
     bar_init(bEnd, 1);
     bar_init(bOut, 4);
+    bar_init(bRow, 8);
     bar_init_fence();
     if (n > 0) {
       bar_expect(bQ, 2 * P::kTileBytes);
@@ -640,7 +643,8 @@ __global__ void __launch_bounds__(kThreadsDq, 1) window_dq_kernel(const __grid_c
     const int64_t wlo = g.off + g.t0 + (warp % 4) * 32, whi = wlo + 31;
     const bool live = row < g.nq;
     const int64_t at = ((int64_t)b * a.Hq + h) * a.Tq + g.qbeg + row;
-    const float lse = live ? a.lse[at] * 1.44269504088896341f : INFINITY, delta = live ? a.delta[at] : 0.f;
+    const float lse = live ? a.lse[at] * 1.44269504088896341f : INFINITY;
+    float delta = live && n > 1 ? a.delta[at] : 0.f;
     bool ok = true;
     for (int u = 0; u < n; ++u) {
       const int64_t j0 = kt.at(u) * kRows, c0 = j0 + 64 * w;  // first key of the columns
@@ -669,6 +673,29 @@ __global__ void __launch_bounds__(kThreadsDq, 1) window_dq_kernel(const __grid_c
       }
       if (!(ok = warp_wait(bDp, u & 1, stop))) break;
       fence_after();
+      if (n == 1) {
+        // The row's weights are all here, so delta = do o = sum p dP is formed from them, in
+        // 32 bits: where keys are few, one from the output as it was rounded is a large part
+        // of the error. The keys' kernel, which comes after, reads it.
+        float sum = 0.f;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          uint32_t d[32];
+          tmem_ld32(tDp + lanes + 64 * w + 32 * i, d);
+          ld_wait();
+#pragma unroll
+          for (int c = 0; c < 32; ++c) {
+            const float p = __uint_as_float(s[i][c]);
+            if (whole || p != 0.f) sum = fmaf(p, __uint_as_float(d[c]), sum);
+          }
+        }
+        s_row[128 * w + r] = sum;
+        __syncwarp();
+        if (lane == 0) bar_arrive(bRow);
+        if (!(ok = warp_wait(bRow, 0, stop))) break;
+        delta = s_row[r] + s_row[128 + r];
+        if (w == 0 && live) a.delta[at] = delta;
+      }
       uint32_t o[32], rest[TWO ? 32 : 1];
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
@@ -744,8 +771,8 @@ cudaError_t launch_bwd(const BwdArgs& t, int64_t B, cudaStream_t s) {
   const int64_t extra = t.cu ? t.n_seqs : 0;
   const int64_t tk = (t.Tk + kRows - 1) / kRows + extra, tq = (t.Tq + kRows - 1) / kRows + extra;
   const int64_t cut = t.pieces > 1 ? (int64_t)t.sink_tiles * (t.pieces - 1) : 0;
-  window_dkv_kernel<DP, TWO><<<dim3((unsigned)(tk + cut), (unsigned)(B * t.Hk)), kThreads, P::kSmem, s>>>(t);
   window_dq_kernel<DP, TWO><<<dim3((unsigned)tq, (unsigned)(B * t.Hq)), kThreadsDq, P::kSmem, s>>>(t);
+  window_dkv_kernel<DP, TWO><<<dim3((unsigned)(tk + cut), (unsigned)(B * t.Hk)), kThreads, P::kSmem, s>>>(t);
   if (t.pieces > 1)
     window_pieces_kernel<<<dim3((unsigned)(t.sink_tiles * kRows), (unsigned)(B * t.Hk)), 256, 0, s>>>(t);
   return cudaGetLastError();
@@ -766,14 +793,15 @@ Cut cut_sinks(int64_t Tq, int64_t Tk, int64_t W, int64_t S, bool packed) {
   return Cut{(int)tiles, (int)p};
 }
 
-// Whether dS goes to its products as the sum of two bf16 parts. delta comes from the
-// output as it was rounded, which is felt where a row sees few keys (an error of
-// (keys / e - 1)^(-1/2) roundings for scores of unit variance): together with the rounding
-// of dS it would be more than the gradients' own. Short rows, and narrow windows, so take
-// the two parts; elsewhere one rounding is what is left. Error of dq and dk in the 2-norm
-// and us of the backward, one part / two, 16 heads of 128 over 4: 4 x 64 tokens 2.6e-3 /
-// 2.0e-3, 24 / 26 us; 2 x 512 2.5e-3 / 1.9e-3, 48 / 55 us; 2 x 4096, window 1024 2.4e-3 /
-// 1.8e-3, 302 / 346 us (rounding the exact gradients alone: 1.7e-3).
+// Whether dS goes to its products as the sum of two bf16 parts. Past its first tile of
+// keys a row's delta comes from the output as it was rounded, which is felt where it sees
+// few keys (an error of (keys / e - 1)^(-1/2) roundings for scores of unit variance):
+// together with the rounding of dS it would be more than the gradients' own. Short rows,
+// and narrow windows, so take the two parts; elsewhere one rounding is what is left. Error
+// of dq and dk in the 2-norm (with delta from the rounded output everywhere) and us of the
+// backward, one part / two, 16 heads of 128 over 4: 4 x 64 tokens 2.6e-3 / 2.0e-3, 24 / 26
+// us; 2 x 512 2.5e-3 / 1.9e-3, 48 / 55 us; 2 x 4096, window 1024 2.4e-3 / 1.8e-3, 302 / 346
+// us (rounding the exact gradients alone: 1.7e-3).
 bool two_parts(const WinArgs& a) {
   const int64_t len = a.cu ? a.Tk / a.n_seqs : a.Tk;  // of a sequence, in the mean
   return len <= 512 || a.W + a.S <= 32;

@@ -645,8 +645,10 @@ scan_status window_attn_fwd(const scan_view4* q, const scan_view4* k, const scan
 /* Its backward from the forward's o and lse:
  *   p_ij = exp(scale q_i k_j - lse_i), ds_ij = scale p_ij (dout_i v_j - dout_i o_i),
  *   dq_i = sum_j ds_ij k_j, dk_j = sum_i ds_ij q_i, dv_j = sum_i p_ij dout_i,
- * the last two over the query heads that share the key head as well. dq, dk,
- * dv: dtype dt, written. No sum depends on the order in which blocks run.
+ * the last two over the query heads that share the key head as well. (bf16 on
+ * the tensor cores: rows that see one tile of 128 keys form dout_i o_i anew, as
+ * the sum of p_ij dout_i v_j in fp32, since o is rounded.) dq, dk, dv: dtype dt,
+ * written. No sum depends on the order in which blocks run.
  * Errors and workspace as the forward's. */
 scan_status window_attn_bwd(const scan_view4* q, const scan_view4* k, const scan_view4* v,
                             const scan_view4* o, const float* lse, const scan_view4* dout,

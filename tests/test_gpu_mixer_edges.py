@@ -284,3 +284,20 @@ def test_window_gradients_where_rows_see_few_keys(lib, T, W, S, lengths, D):
         limit = 1.1 * (rounded ** 2 + float(m.norm() / w.norm()) ** 2) ** 0.5
         err = float((f64(g) - w).norm() / w.norm())
         assert err <= limit, (name, err, limit, rounded)
+
+
+@pytest.mark.parametrize("lengths", [[19], [2, 2, 3], [6, 1, 12], [128], [9, 127, 64, 1, 33]])
+@pytest.mark.parametrize("Hq,Hk,D", [(2, 1, 64), (3, 3, 128)])
+@pytest.mark.parametrize("W,S", [(1000, 0), (35, 16), (5, 0)])
+def test_window_gradients_of_a_few_tokens(lib, lengths, Hq, Hk, D, W, S):
+    """dq and dk in the 2-norm against 64 bits: rows that see one tile of keys have
+    nothing but the rounding of the result to bf16 (and a tenth of it for all else)."""
+    T, cu = sum(lengths), offsets(lengths)
+    q, k, v, do = win_inputs(1, T, T, Hq, Hk, D, BF, T + D)
+    o, lse = lib.window_attn_fwd(q, k, v, W, S, cu)
+    got = lib.window_attn_bwd(q, k, v, o, lse, do, W, S, cu)
+    want, _ = ref.window_grads(*[f64(t) for t in (q, k, v, do)], W, S, cu.cpu(), D ** -0.5)
+    for g, w, name in zip(got, want, ("dq", "dk")):
+        rounded = float((w.to(BF).double() - w).norm() / w.norm())
+        err = float((f64(g) - w).norm() / w.norm())
+        assert err <= 1.1 * rounded, (name, err, rounded)
