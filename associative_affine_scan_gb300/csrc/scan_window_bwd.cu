@@ -804,7 +804,7 @@ Cut cut_sinks(int64_t Tq, int64_t Tk, int64_t W, int64_t S, bool packed) {
 // us (rounding the exact gradients alone: 1.7e-3).
 bool two_parts(const WinArgs& a) {
   const int64_t len = a.cu ? a.Tk / a.n_seqs : a.Tk;  // of a sequence, in the mean
-  return len <= 512 || a.W + a.S <= 32;
+  return len <= 512 || a.W + a.S <= 64;
 }
 
 }  // namespace
