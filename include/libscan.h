@@ -572,7 +572,7 @@ scan_status qk_norm_rope_bwd(const scan_view4* q, const scan_view4* k, const flo
  * 32 x 32); packed rows go by the mean length of their sequences, so that a long
  * one among many of a few steps is walked step by step as well. Operands off 16
  * bytes, or broadcast over an axis by a stride of 0, take the recurrence too: it
- * costs 0.35 to 0.6 us a step.
+ * costs 0.35 to 0.9 us a step.
  * Values within a sequence must be finite: in chunks, a value that is not makes
  * earlier results of its chunk NaN too. Values outside the sequences are never
  * used. An output must not overlap an input or another output.

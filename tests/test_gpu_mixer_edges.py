@@ -301,3 +301,59 @@ def test_window_gradients_of_a_few_tokens(lib, lengths, Hq, Hk, D, W, S):
         rounded = float((w.to(BF).double() - w).norm() / w.norm())
         err = float((f64(g) - w).norm() / w.norm())
         assert err <= 1.1 * rounded, (name, err, rounded)
+
+
+def chunked(q, k, v, g, h0, scale):
+    """The recurrence in 64 bits, 256 steps at a time: o, hT."""
+    o, S = [], h0
+    i = torch.arange(256, dtype=torch.float64, device=q.device)
+    for t in range(0, q.shape[1], 256):
+        a, b, c = (x[0, t:t + 256].double().transpose(0, 1) for x in (q, k, v))  # [H, n, D]
+        n = a.shape[1]
+        w = torch.exp(g[:, None, None] * (i[:n, None] - i[:n]).clamp(min=0)).tril()
+        o.append((a @ S) * torch.exp(g[:, None] * (i[:n] + 1))[..., None] + (a @ b.transpose(1, 2) * w) @ c)
+        S = S * torch.exp(g * n)[:, None, None] + (b * torch.exp(g[:, None] * (n - 1 - i[:n]))[..., None]).transpose(1, 2) @ c
+    return scale * torch.cat(o, 1).transpose(0, 1)[None], S
+
+
+@pytest.mark.parametrize("T", [100, 3000])
+def test_linattn_recurrence_keeps_slow_decays(lib, T):
+    """fp32, memories of 20 to 260 steps: outputs, gradients and states in the 2-norm of
+    each head against 64 bits. An entry is rounded twice a step over a memory of 1 / (1 -
+    lambda) steps: 2^-25 each (root mean square at most) that add up as their squares,
+    times 4; and 2^-22 for the sums of D products. The rounding of lambda would add
+    up to 2^-25 a step of the memory."""
+    H, D = 12, 64
+    q, k, v, do, h0, dh = lin_inputs(1, T, H, D, D, F32, T)
+    g = -torch.logspace(-8, -4.3, H, base=2.0, device=DEV)
+    o, hT = lib.linattn_fwd(q, k, v, g, h0, scale=0.5)
+    dq, dk, dv, dh0 = lib.linattn_bwd(q, k, v, g, do, h0, None, dh, scale=0.5)
+    G = g.double()
+    flip = lambda t: t.flip(1)  # noqa: E731
+    lam = torch.exp(G)[:, None, None]
+    ro, rh = chunked(q, k, v, G, h0[0].double(), 0.5)
+    rq, _ = chunked(do, v, k, G, h0[0].double().transpose(1, 2), 0.5)
+    init = dh[0].double() / 0.5 / lam  # (comes in not yet decayed)
+    rk, _ = chunked(flip(v), flip(do), flip(q), G, init.transpose(1, 2), 0.5)
+    rv, end = chunked(flip(k), flip(q), flip(do), G, init, 0.5)
+    for got, want, name in ((o, ro, "o"), (dq, rq, "dq"), (dk, flip(rk), "dk"), (dv, flip(rv), "dv"),
+                            (hT[0], rh, "hT"), (dh0[0], 0.5 * lam * end, "dh0")):
+        got = got.double()
+        axes = (0, 1, 3) if got.dim() == 4 else (1, 2)
+        err = (got - want).square().sum(axes).sqrt() / want.square().sum(axes).sqrt()
+        limit = 4 * 2.0 ** -25 * (2 / (1 - torch.exp(G))).clamp(max=2 * T).sqrt() + 2.0 ** -22
+        assert bool((err <= limit).all()), (name, (err / limit).tolist())
+
+
+def test_linattn_recurrence_over_a_million_steps(lib):
+    """What the rounding of lambda leaves out is settled on the way: the end of a row of
+    more than 2^20 steps is that of its last steps alone, whose memory is 260 steps."""
+    T, last = (1 << 20) + 700, 20000
+    q, k, v, _, _, _ = lin_inputs(1, T, 2, 8, 8, F32, 2, state=False)
+    g = -torch.logspace(-8, -6, 2, base=2.0, device=DEV)
+    o, hT = lib.linattn_fwd(q, k, v, g)
+    po, pT = lib.linattn_fwd(q[:, -last:], k[:, -last:], v[:, -last:], g)
+    # both are within the limit of the test above of the exact value
+    limit = 2 * (4 * 2.0 ** -25 * (2 * 260) ** 0.5 + 2.0 ** -22)
+    assert float((hT - pT).norm() / pT.norm()) <= limit
+    assert float((o[:, -600:] - po[:, -600:]).norm() / po[:, -600:].norm()) <= limit
