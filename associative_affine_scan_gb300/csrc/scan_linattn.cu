@@ -21,12 +21,19 @@
 // (the last writes are still in L2 when it ends). A block takes one (request, head);
 // thread x owns four columns, thread y every 8th or 16th row, so all loads and
 // stores are whole 512-byte rows, and the read-out's sum over rows ends in shared
-// memory.
+// memory. lambda is held in two parts, so that the states of many tokens do not gather
+// its rounding (1e-5 over a memory of 260 tokens).
 #include "scan_linattn_tc.h"
 #include "scan_mixer.h"
 
 namespace scan {
 namespace {
+
+// log(lambda / lam) of a lambda that was rounded to lam: lam - 1 is exact where it is used.
+// A state that loses most of itself every step gathers no such error.
+__device__ __forceinline__ float rounding_of(float lam, float log_decay) {
+  return lam > 0.25f && lam < 4.f ? log_decay - log1pf(lam - 1.f) : 0.f;
+}
 
 constexpr int kCols = 32;   // columns of S a block of the general path owns
 constexpr int kSteps = 16;  // steps staged in shared memory
@@ -52,9 +59,7 @@ __global__ void __launch_bounds__(4 * kCols, KP == 64 ? 8 : 6) linattn_general_k
   const View<const T> x3{static_cast<const T*>(p.x3.ptr), p.x3.stride_b, p.x3.stride_t, p.x3.stride_h};
   const View<T> out{static_cast<T*>(p.out.ptr), p.out.stride_b, p.out.stride_t, p.out.stride_h};
   const float lam = expf(a.log_decay[h]);
-  // log(lambda / fl(lambda)), held in shared memory for the few who use it: fl(lambda) - 1
-  // is exact here. A state that loses most of itself every step gathers no such error.
-  if (threadIdx.x == 0) drift = lam > 0.25f && lam < 4.f ? a.log_decay[h] - log1pf(lam - 1.f) : 0.f;
+  if (threadIdx.x == 0) drift = rounding_of(lam, a.log_decay[h]);  // in shared memory for the few who use it
   const int skip = p.reverse ? 0 : 1;  // multiplications that step 0's entry is ahead of the initial state
   const int col = threadIdx.x >> 2, part = threadIdx.x & 3, c = v0 + col;
   // rows 16 i + 4 part + r of S, r < 4
@@ -193,7 +198,7 @@ __global__ void __launch_bounds__(256) linattn_step_kernel(const StepArgs a) {
     sq[i] = to_f32(q[i]);
     sk[i] = to_f32(k[i]);
   }
-  const float lam = expf(a.log_decay[h]);
+  const float lam = expf(a.log_decay[h]), low = lam * rounding_of(lam, a.log_decay[h]);  // lambda in two parts
   float4 vv = make_float4(0.f, 0.f, 0.f, 0.f);
   if (on) vv = make_float4(to_f32(v[c]), to_f32(v[c + 1]), to_f32(v[c + 2]), to_f32(v[c + 3]));
   __syncthreads();
@@ -204,10 +209,10 @@ __global__ void __launch_bounds__(256) linattn_step_kernel(const StepArgs a) {
     if (on && r < a.Dk) {
       const float kk = sk[r], qq = sq[r];
       float4 x = e[i];
-      x.x = fmaf(kk, vv.x, x.x * lam);
-      x.y = fmaf(kk, vv.y, x.y * lam);
-      x.z = fmaf(kk, vv.z, x.z * lam);
-      x.w = fmaf(kk, vv.w, x.w * lam);
+      x.x = fmaf(kk, vv.x, fmaf(x.x, lam, x.x * low));
+      x.y = fmaf(kk, vv.y, fmaf(x.y, lam, x.y * low));
+      x.z = fmaf(kk, vv.z, fmaf(x.z, lam, x.z * low));
+      x.w = fmaf(kk, vv.w, fmaf(x.w, lam, x.w * low));
       __stcs(reinterpret_cast<float4*>(S + (int64_t)r * a.Dv + c), x);
       acc.x = fmaf(qq, x.x, acc.x);
       acc.y = fmaf(qq, x.y, acc.y);

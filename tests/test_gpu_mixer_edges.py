@@ -357,3 +357,22 @@ def test_linattn_recurrence_over_a_million_steps(lib):
     limit = 2 * (4 * 2.0 ** -25 * (2 * 260) ** 0.5 + 2.0 ** -22)
     assert float((hT - pT).norm() / pT.norm()) <= limit
     assert float((o[:, -600:] - po[:, -600:]).norm() / po[:, -600:].norm()) <= limit
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_linattn_steps_keep_slow_decays(lib, dtype):
+    """1500 single tokens over memories of 20 to 260: the state that is left against 64
+    bits, in the 2-norm of each head, within the limit of the recurrence over a row."""
+    H, D, T = 12, 64, 1500
+    q, k, v, _, h0, _ = lin_inputs(1, T, H, D, D, dtype, 4)
+    g = -torch.logspace(-8, -4.3, H, base=2.0, device=DEV)
+    state = h0.clone()
+    for t in range(T):
+        o = lib.linattn_step(q[:, t], k[:, t], v[:, t], g, state, scale=0.5)
+    ro, rh = chunked(q, k, v, g.double(), h0[0].double(), 0.5)
+    limit = 4 * 2.0 ** -25 * (2 / (1 - torch.exp(g.double()))).sqrt() + 2.0 ** -22
+    err = (state[0].double() - rh).square().sum((1, 2)).sqrt() / rh.square().sum((1, 2)).sqrt()
+    assert bool((err <= limit).all()), (err / limit).tolist()
+    if dtype == F32:
+        err = (o[0].double() - ro[0, -1]).norm() / ro[0, -1].norm()
+        assert float(err) <= float(limit.max())
