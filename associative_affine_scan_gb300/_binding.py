@@ -60,6 +60,9 @@ EXPORTED = (
     "rglru_fwd", "rglru_bwd", "qk_norm_rope_workspace_bytes", "qk_norm_rope_fwd",
     "qk_norm_rope_bwd", "linattn_workspace_bytes", "linattn_fwd", "linattn_bwd", "linattn_step",
     "window_attn_workspace_bytes", "window_attn_fwd", "window_attn_bwd", "window_attn_step",
+    "cross_attn_workspace_bytes", "cross_attn_fwd", "cross_attn_bwd", "cross_attn_step",
+    "dropout_fwd", "dropout_bwd", "residual_norm_workspace_bytes", "residual_norm_fwd",
+    "residual_norm_bwd",
 )
 
 
@@ -97,6 +100,8 @@ _i64 = ctypes.c_int64
 _i32 = ctypes.c_int32
 _sz = ctypes.c_size_t
 _f32 = ctypes.c_float
+_f64 = ctypes.c_double
+_u64 = ctypes.c_uint64
 _opt = ctypes.POINTER(ScanOpts)
 _v4 = ctypes.c_void_p  # scan_view4*: the bytes of one (see _view4)
 
@@ -161,6 +166,22 @@ _SIGS = {
                         + [_f32, ctypes.c_int, _vp, _sz, _vp], ctypes.c_int),
     "window_attn_step": ([_v4] * 3 + [_vp] * 4 + [_i64, _v4] + [_i64] * 6
                          + [_f32, ctypes.c_int, _vp], ctypes.c_int),
+    "cross_attn_workspace_bytes": ([_i64] * 7 + [_i32], _sz),
+    "cross_attn_fwd": ([_v4] * 3 + [_vp] * 3 + [_i32, _v4, _vp] + [_i64] * 6
+                       + [_f32, ctypes.c_int, _vp, _sz, _vp], ctypes.c_int),
+    "cross_attn_bwd": ([_v4] * 4 + [_vp, _v4] + [_vp] * 3 + [_i32] + [_v4] * 3 + [_i64] * 6
+                       + [_f32, ctypes.c_int, _vp, _sz, _vp], ctypes.c_int),
+    "cross_attn_step": ([_v4] * 3 + [_vp] * 2 + [_i64, _v4] + [_i64] * 5
+                        + [_f32, ctypes.c_int, _vp], ctypes.c_int),
+    "dropout_fwd": ([_v4] * 2 + [_i64] * 3 + [_f64, _u64, _u64, _vp, ctypes.c_int, _vp], ctypes.c_int),
+    "dropout_bwd": ([_v4] * 2 + [_i64] * 3 + [_f64, _u64, _u64, _vp, ctypes.c_int, _vp], ctypes.c_int),
+    "residual_norm_workspace_bytes": ([_i64] * 3 + [_i32], _sz),
+    "residual_norm_fwd": ([_v4] * 2 + [_vp] * 3 + [_v4] * 2 + [_i64] * 3
+                          + [_i32, _f32, _f32, _f64, _u64, _u64, _vp, ctypes.c_int, ctypes.c_int, _vp],
+                          ctypes.c_int),
+    "residual_norm_bwd": ([_v4] * 4 + [_vp] * 3 + [_v4] * 2 + [_vp] * 3 + [_i64] * 3
+                          + [_i32, _f32, _f32, _f64, _u64, _u64, _vp, ctypes.c_int, ctypes.c_int, _vp,
+                             _sz, _vp], ctypes.c_int),
 }
 
 _lock = threading.Lock()
@@ -239,12 +260,16 @@ def _optref(o: Optional[ScanOpts]):
     return None if o is None else ctypes.byref(o)
 
 
-def _dtype_code(t: torch.Tensor) -> int:
-    if t.dtype == torch.float32:
+def _type_code(dtype: torch.dtype) -> int:
+    if dtype == torch.float32:
         return SCAN_F32
-    if t.dtype == torch.bfloat16:
+    if dtype == torch.bfloat16:
         return SCAN_BF16
-    raise TypeError(f"unsupported dtype {t.dtype}: fp32 or bf16 expected")
+    raise TypeError(f"unsupported dtype {dtype}: fp32 or bf16 expected")
+
+
+def _dtype_code(t: torch.Tensor) -> int:
+    return _type_code(t.dtype)
 
 
 def _need(t: Optional[torch.Tensor], name: str, *, dtype=None, shape=None, device=None):
@@ -1237,3 +1262,257 @@ def window_attn_step(q, k, v, k_cache, v_cache, positions, window, sinks=0, slot
                _at(positions), _at(slots), k_cache.shape[0], _view4(o), B, Hq, Hk, D, window, sinks,
                D ** -0.5 if scale is None else scale, _dtype_code(q), _raw_stream(stream, dev))
     return o
+
+
+def cross_attn_workspace_bytes(B, Tq, Tk, Hq, Hk, D, n_seqs=0, backward=False) -> int:
+    return int(lib().cross_attn_workspace_bytes(B, Tq, Tk, Hq, Hk, D, n_seqs, int(bool(backward))))
+
+
+def _cross_args(q, k, v, k_lens, cu_q, cu_k):
+    _heads(_rank(q, "q", 4), "q")
+    dev, dt = q.device, q.dtype
+    B, Tq, Hq, D = q.shape
+    _rank(k, "k", 4)
+    Tk, Hk = k.shape[1:3]
+    _heads(k, "k", dtype=dt, shape=(B, Tk, Hk, D), device=dev)
+    _heads(v, "v", dtype=dt, shape=k.shape, device=dev)
+    if (cu_q is None) != (cu_k is None):
+        raise ValueError("cu_seqlens_q and cu_seqlens_k are given together or not at all")
+    if cu_q is not None and k_lens is not None:
+        raise ValueError("k_lens is for whole rows, cu_seqlens_q and cu_seqlens_k for packed ones")
+    _need(k_lens, "k_lens", dtype=torch.int32, shape=(B,), device=dev)
+    n = _packed(cu_q, B, dev)
+    if cu_k is not None:
+        _need(cu_k, "cu_seqlens_k", dtype=torch.int32, shape=cu_q.shape, device=dev)
+    return dev, dt, B, Tq, Tk, Hq, Hk, D, n
+
+
+def cross_attn_fwd(q, k, v, k_lens=None, cu_seqlens_q=None, cu_seqlens_k=None, *, scale=None, out=None,
+                   stream=None):
+    """Attention of each query to every key of another sequence (an encoder's
+    states). q [B, Tq, Hq, D], k, v [B, Tk, Hk, D] fp32 or bf16, unit stride
+    along D; Hq a multiple of Hk; k_lens int32 [B]: row b sees its first
+    k_lens[b] keys (None: all); cu_seqlens_q, cu_seqlens_k int32 [n + 1]: packed
+    pairs of sequences (B = 1); scale: D^-0.5 when None. Returns (o, lse): o in
+    q's dtype, lse fp32 [B, Hq, Tq]; a query without keys has o = 0, lse =
+    -inf."""
+    dev, dt, B, Tq, Tk, Hq, Hk, D, n = _cross_args(q, k, v, k_lens, cu_seqlens_q, cu_seqlens_k)
+    if out is not None:
+        o, lse = out
+        _written(o, "o", dtype=dt, shape=q.shape, device=dev)
+        _need(lse, "lse", dtype=torch.float32, shape=(B, Hq, Tq), device=dev)
+    else:
+        o = torch.empty(q.shape, dtype=dt, device=dev)
+        lse = torch.empty((B, Hq, Tq), dtype=torch.float32, device=dev)
+    s = _raw_stream(stream, dev)
+    ws = _mixer_workspace(cross_attn_workspace_bytes(B, Tq, Tk, Hq, Hk, D, n), dev, s)
+    _enter(dev, "cross_attn_fwd", _view4(q), _view4(k), _view4(v), _at(k_lens), _at(cu_seqlens_q),
+           _at(cu_seqlens_k), n, _view4(o), _at(lse), B, Tq, Tk, Hq, Hk, D,
+           D ** -0.5 if scale is None else scale, _dtype_code(q), ws.data_ptr(), ws.numel(), s)
+    return o, lse
+
+
+def cross_attn_bwd(q, k, v, o, lse, dout, k_lens=None, cu_seqlens_q=None, cu_seqlens_k=None, *, scale=None,
+                   out=None, stream=None):
+    """Gradients of L = sum dout o for cross_attn_fwd's inputs, from its
+    outputs: (dq, dk, dv) in q's dtype; rows of dk and dv past k_lens are 0."""
+    dev, dt, B, Tq, Tk, Hq, Hk, D, n = _cross_args(q, k, v, k_lens, cu_seqlens_q, cu_seqlens_k)
+    _heads(o, "o", dtype=dt, shape=q.shape, device=dev)
+    _heads(dout, "dout", dtype=dt, shape=q.shape, device=dev)
+    _need(lse, "lse", dtype=torch.float32, shape=(B, Hq, Tq), device=dev)
+    if out is not None:
+        dq, dk, dv = out
+        for t, name, like in ((dq, "dq", q), (dk, "dk", k), (dv, "dv", v)):
+            _written(t, name, dtype=dt, shape=like.shape, device=dev)
+    else:
+        dq, dk, dv = (torch.empty(t.shape, dtype=dt, device=dev) for t in (q, k, v))
+    s = _raw_stream(stream, dev)
+    ws = _mixer_workspace(cross_attn_workspace_bytes(B, Tq, Tk, Hq, Hk, D, n, True), dev, s)
+    _enter(dev, "cross_attn_bwd", _view4(q), _view4(k), _view4(v), _view4(o), _at(lse), _view4(dout),
+           _at(k_lens), _at(cu_seqlens_q), _at(cu_seqlens_k), n, _view4(dq), _view4(dk), _view4(dv), B, Tq,
+           Tk, Hq, Hk, D, D ** -0.5 if scale is None else scale, _dtype_code(q), ws.data_ptr(),
+           ws.numel(), s)
+    return dq, dk, dv
+
+
+def cross_attn_step(q, k_cache, v_cache, lens=None, slots=None, *, scale=None, out=None, stream=None):
+    """One query token of each request over a pool of encoders' keys and values,
+    which are only read. q [B, Hq, D]; k_cache, v_cache [n_slots, Tk, Hk, D],
+    unit stride along D; lens int32 [n_slots], the keys that each cache holds
+    (None: Tk); slots int32 [B] or None (request b has cache b): requests may
+    share one, a slot outside the pool marks an idle request (o = 0). Returns o
+    [B, Hq, D]."""
+    _heads(_rank(q, "q", 3), "q")
+    dev, dt = q.device, q.dtype
+    B, Hq, D = q.shape
+    n_slots, Tk, Hk = _rank(k_cache, "k_cache", 4).shape[:3]
+    _heads(k_cache, "k_cache", dtype=dt, shape=(n_slots, Tk, Hk, D), device=dev)
+    _heads(v_cache, "v_cache", dtype=dt, shape=k_cache.shape, device=dev)
+    _need(lens, "lens", dtype=torch.int32, shape=(n_slots,), device=dev)
+    _need(slots, "slots", dtype=torch.int32, shape=(B,), device=dev)
+    o = out if out is not None else torch.empty(q.shape, dtype=dt, device=dev)
+    if out is not None:
+        _written(o, "out", dtype=dt, shape=q.shape, device=dev)
+    _enter(dev, "cross_attn_step", _view4(q), _view4(k_cache), _view4(v_cache), _at(lens), _at(slots),
+           n_slots, _view4(o), B, Tk, Hq, Hk, D, D ** -0.5 if scale is None else scale, _dtype_code(q),
+           _raw_stream(stream, dev))
+    return o
+
+
+# ---------------------------------------------------------------------------
+# around a block: [B, T, C] operands
+# ---------------------------------------------------------------------------
+
+def _view3(t):
+    s = t.stride()
+    return _pack_view(t.data_ptr(), s[0], s[1] if len(s) == 3 else 0, 0)
+
+
+def _random(rng, p, dev):
+    """(p, seed, call, device pointer) of a dropout's arguments."""
+    if not 0.0 <= p <= 1.0:
+        raise ValueError(f"p must be within [0, 1], got {p}")
+    if rng is None:
+        if p > 0:
+            raise ValueError("dropout needs rng: (seed, call), or both as an int64 CUDA tensor")
+        return p, 0, 0, None
+    if isinstance(rng, torch.Tensor):
+        _need(rng, "rng", dtype=torch.int64, shape=(2,), device=dev)
+        return p, 0, 0, rng.data_ptr()
+    seed, call = rng
+    if not (0 <= seed < 1 << 64 and 0 <= call < 1 << 64):
+        raise ValueError("rng: seed and call must be within [0, 2^64)")
+    return p, seed, call, None
+
+
+def _dropout(name, x, p, rng, out, stream):
+    if not isinstance(x, torch.Tensor):
+        raise TypeError("x must be a torch.Tensor")
+    if not x.is_cuda:
+        raise ValueError("x must be a CUDA tensor")
+    dev, dt = x.device, x.dtype
+    y = torch.empty(x.shape, dtype=dt, device=dev) if out is None else out
+    if out is not None:
+        _written(y, "out", dtype=dt, shape=x.shape, device=dev)
+    if x.is_contiguous() and y.is_contiguous():
+        B, T, C = 1, 1, x.numel()
+        views = _pack_view(x.data_ptr(), 0, 0, 0), _pack_view(y.data_ptr(), 0, 0, 0)
+    else:
+        if x.dim() not in (2, 3):
+            raise ValueError("x: expected [B, T, C], [B, C] or a contiguous tensor")
+        _heads(x, "x")
+        B, C = x.shape[0], x.shape[-1]
+        T = x.shape[1] if x.dim() == 3 else 1
+        views = _view3(x), _view3(y)
+    _enter(dev, name, *views, B, T, C, *_random(rng, p, dev), _dtype_code(x), _raw_stream(stream, dev))
+    return y
+
+
+def dropout_fwd(x, p, rng, *, out=None, stream=None):
+    """Dropout whose mask is never stored: x / (1 - p) where an element is kept,
+    else 0. x fp32 or bf16, contiguous or [B, T, C] with a unit stride along C;
+    rng: (seed, call), two whole numbers, or an int64 CUDA tensor of both, read
+    when the kernel runs. The mask is a function of rng, p (in steps of 2^-16)
+    and the element's place in the shape. out may be x."""
+    return _dropout("dropout_fwd", x, p, rng, out, stream)
+
+
+def dropout_bwd(dy, p, rng, *, out=None, stream=None):
+    """The gradient of dropout_fwd's input: the same mask over dy."""
+    return _dropout("dropout_bwd", dy, p, rng, out, stream)
+
+
+def residual_norm_workspace_bytes(B, T, C, row_gate=False) -> int:
+    return int(lib().residual_norm_workspace_bytes(B, T, C, int(bool(row_gate))))
+
+
+def _norm_args(x, name, y, post_weight, gate, next_weight):
+    _heads(x, name)
+    if x.dim() not in (2, 3):
+        raise ValueError(f"{name}: expected [B, T, C] or [B, C]")
+    dev = x.device
+    B, C = x.shape[0], x.shape[-1]
+    T = x.shape[1] if x.dim() == 3 else 1
+    if y is not None:
+        _heads(y, "y", shape=x.shape, device=dev)
+    _need(post_weight, "post_weight", dtype=torch.float32, shape=(C,), device=dev)
+    _need(next_weight, "next_weight", dtype=torch.float32, shape=(C,), device=dev)
+    row_gate = isinstance(gate, torch.Tensor) and gate.dim() == 2
+    _need(gate, "gate", dtype=torch.float32, shape=(B, C) if row_gate else (C,), device=dev)
+    return dev, B, T, C, int(row_gate)
+
+
+def residual_norm_fwd(x, y, post_weight=None, gate=None, next_weight=None, *, alpha=1.0, eps=1e-6, p=0.0,
+                      rng=None, dtype=None, out=None, stream=None):
+    """The norms around a block, with its gate, dropout and residual scale:
+        x_out = alpha x + drop(gate rmsnorm(y, post_weight)),
+        n = rmsnorm(x_out, next_weight).
+    x, the residual stream before the block, and y, what the block gave:
+    [B, T, C] or [B, C], fp32 or bf16 (x fp32 or both bf16), unit stride along
+    C. post_weight, next_weight fp32 [C], gate fp32 [C] or [B, C]: None leaves
+    that part out. y None: only n, the norm of x (x itself is returned as
+    x_out). p, rng: as for dropout_fwd. n has y's dtype (without y: dtype, or
+    x's). out: (x_out, n), which may be (x, y). Returns (x_out, n); n is None
+    without next_weight."""
+    dev, B, T, C, row_gate = _norm_args(x, "x", y, post_weight, gate, next_weight)
+    dt = y.dtype if y is not None else dtype or x.dtype
+    if out is not None:
+        x_out, n = out
+    else:
+        x_out = x if y is None else torch.empty(x.shape, dtype=x.dtype, device=dev)
+        n = None if next_weight is None else torch.empty(x.shape, dtype=dt, device=dev)
+    if y is None:
+        x_out = x
+    elif out is not None:
+        _written(x_out, "x_out", dtype=x.dtype, shape=x.shape, device=dev)
+    if next_weight is None:
+        n = None
+    elif out is not None:
+        _written(n, "n", dtype=dt, shape=x.shape, device=dev)
+    _enter(dev, "residual_norm_fwd", _view3(x), None if y is None else _view3(y), _at(post_weight), _at(gate),
+           _at(next_weight), None if y is None else _view3(x_out), None if n is None else _view3(n), B, T, C,
+           row_gate, alpha, eps, *_random(rng, p, dev), _dtype_code(x), _type_code(dt),
+           _raw_stream(stream, dev))
+    return x_out, n
+
+
+def residual_norm_bwd(x_out, y, dx_out, dn, post_weight=None, gate=None, next_weight=None, *, alpha=1.0,
+                      eps=1e-6, p=0.0, rng=None, out=None, stream=None):
+    """Gradients of L = sum dx_out x_out + dn n for residual_norm_fwd's inputs,
+    from its x_out and y (without y: from x): (dx, dy, dpost_weight, dgate,
+    dnext_weight), dx in x's dtype, dy in y's, the others fp32; None for what
+    was not given. dx_out None: 0 (with next_weight); dn is None without
+    next_weight. out: the same five."""
+    dev, B, T, C, row_gate = _norm_args(x_out, "x_out", y, post_weight, gate, next_weight)
+    sdt = x_out.dtype
+    dt = y.dtype if y is not None else dn.dtype if dn is not None else sdt
+    if (dn is None) != (next_weight is None):
+        raise ValueError("dn and next_weight are given together or not at all")
+    if dx_out is None and dn is None:
+        raise ValueError("one of dx_out and dn is needed")
+    if dx_out is not None:
+        _heads(dx_out, "dx_out", dtype=sdt, shape=x_out.shape, device=dev)
+    if dn is not None:
+        _heads(dn, "dn", dtype=dt, shape=x_out.shape, device=dev)
+    if out is not None:
+        dx, dy, dwp, dg, dwn = out
+        _written(dx, "dx", dtype=sdt, shape=x_out.shape, device=dev)
+        if y is not None:
+            _written(dy, "dy", dtype=dt, shape=x_out.shape, device=dev)
+        for t, name, like in ((dwp, "dpost_weight", post_weight), (dg, "dgate", gate),
+                              (dwn, "dnext_weight", next_weight)):
+            if like is not None:
+                _need(t, name, dtype=torch.float32, shape=like.shape, device=dev)
+    else:
+        dx = torch.empty(x_out.shape, dtype=sdt, device=dev)
+        dy = None if y is None else torch.empty(x_out.shape, dtype=dt, device=dev)
+        dwp, dg, dwn = (None if t is None else torch.empty(t.shape, dtype=torch.float32, device=dev)
+                        for t in (post_weight, gate, next_weight))
+    s = _raw_stream(stream, dev)
+    ws = _mixer_workspace(256 + residual_norm_workspace_bytes(B, T, C, row_gate), dev, s)
+    _enter(dev, "residual_norm_bwd", _view3(x_out), None if y is None else _view3(y),
+           None if dx_out is None else _view3(dx_out), None if dn is None else _view3(dn), _at(post_weight),
+           _at(gate), _at(next_weight), _view3(dx), None if y is None else _view3(dy), _at(dwp), _at(dg),
+           _at(dwn), B, T, C, row_gate, alpha, eps, *_random(rng, p, dev), _dtype_code(x_out),
+           _type_code(dt), ws.data_ptr() + 256, ws.numel() - 256, s)  # past the status word
+    return dx, dy, dwp, dg, dwn

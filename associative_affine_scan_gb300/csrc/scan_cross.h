@@ -1,0 +1,81 @@
+// scan_cross.h -- attention to the states of another sequence (an encoder's): its
+// arguments, and which of its kernels takes a call.
+#pragma once
+
+#include "scan_mixer.h"
+
+namespace scan {
+
+// Whole rows: batch row b's queries see the first lens[b] keys of row b (all Tk
+// without lens). Packed (cu_q): sequence i's queries see sequence i's keys.
+struct CrossArgs {
+  scan_view4 q, k, v, o, dout, dq, dk, dv;
+  float* lse;           // [B, Hq, Tq]
+  float* delta;         // [B, Hq, Tq] (workspace): sum of dout o
+  const int32_t* lens;  // [B], nullable
+  const int32_t* cu_q;  // [n_seqs + 1], nullable
+  const int32_t* cu_k;
+  int n_seqs;
+  int64_t B, Tq, Tk;
+  int Hq, Hk, D;
+  float scale;
+  WsHeader* hdr;
+  float* ws;  // after delta
+};
+
+// Keys that batch row b has, forced into [0, Tk] whatever the array holds.
+__device__ __forceinline__ int64_t keys_of(const int32_t* lens, int64_t b, int64_t Tk) {
+  if (!lens) return Tk;
+  const int64_t n = lens[b];
+  return n < 0 ? 0 : n > Tk ? Tk : n;
+}
+
+// Where a tile of rows lies: first query and key row of its sequence, rows of each,
+// and the tile's first row within the sequence.
+struct CrossRows {
+  int64_t qbeg, kbeg, nq, nk, t0;
+};
+// Tile `tile` of `rows` query rows (by_keys: key rows) of batch row b; a whole warp
+// (packed sequences are searched). False past the last tile.
+__device__ __forceinline__ bool cross_rows(const int32_t* lens, const int32_t* cu_q, const int32_t* cu_k, int n_seqs,
+                                           int64_t Tq, int64_t Tk, int64_t b, int64_t tile, int rows, bool by_keys,
+                                           CrossRows* r) {
+  if (!cu_q) {
+    *r = CrossRows{0, 0, Tq, keys_of(lens, b, Tk), tile * rows};
+    return true;
+  }
+  int64_t beg, end, local, obeg, oend;
+  int seq;
+  if (!locate_tile(by_keys ? cu_k : cu_q, n_seqs, by_keys ? Tk : Tq, tile, rows, &beg, &end, &local, &seq)) return false;
+  seq_bounds(by_keys ? cu_q : cu_k, seq, by_keys ? Tq : Tk, &obeg, &oend);
+  *r = by_keys ? CrossRows{obeg, beg, oend - obeg, end - beg, local * rows}
+               : CrossRows{beg, obeg, end - beg, oend - obeg, local * rows};
+  return true;
+}
+// Records malformed offsets or lengths. One warp.
+__device__ __forceinline__ void check_cross(const int32_t* lens, const int32_t* cu_q, const int32_t* cu_k, int n_seqs,
+                                            int64_t B, int64_t Tq, int64_t Tk, WsHeader* hdr) {
+  if (cu_q) {
+    check_seqlens(cu_q, n_seqs, Tq, hdr);
+    check_seqlens(cu_k, n_seqs, Tk, hdr);
+  } else if (lens) {
+    bool bad = false;
+    for (int64_t i = threadIdx.x & 31; i < B; i += 32) bad |= lens[i] < 0 || lens[i] > Tk;
+    if (bad) hdr->status = SCAN_ERR_SEQLENS;
+  }
+}
+
+cudaError_t launch_cross_general_fwd(const CrossArgs& a, scan_dtype dt, cudaStream_t s);
+cudaError_t launch_cross_general_bwd(const CrossArgs& a, scan_dtype dt, cudaStream_t s);
+
+// One query token a request over a pool of cached keys and values [n_slots, Tk, Hk, D].
+struct CrossStepArgs {
+  scan_view4 q, k, v, o;
+  const int32_t* lens;   // [n_slots], nullable
+  const int32_t* slots;  // [B], nullable
+  int64_t n_slots, Tk;
+  int Hq, Hk, D;
+  float scale;
+};
+
+}  // namespace scan

@@ -675,6 +675,125 @@ scan_status window_attn_step(const scan_view4* q, const scan_view4* k, const sca
                              int64_t Hq, int64_t Hk, int64_t D, int64_t window, int64_t sinks,
                              float scale, scan_dtype dt, cudaStream_t stream);
 
+/* Attention to the states of another sequence, of another length (an encoder's):
+ *   o_i = sum_j softmax_j(scale q_i k_j) v_j over the keys of the query's sequence.
+ *   q, o: [B, Tq, Hq, D]; k, v: [B, Tk, Hk, D] of dtype dt, Hq a multiple of Hk
+ *   (query heads h Hq/Hk .. share key head h).
+ *   k_lens (nullable): int32 [B] on the device; batch row b's queries see its first
+ *   k_lens[b] keys (a padded batch), else all Tk.
+ *   Packed (cu_seqlens_q and cu_seqlens_k, no k_lens): B = 1, int32 [n_seqs + 1]
+ *   offsets each, from 0 to Tq and to Tk; the queries of sequence i see the keys of
+ *   sequence i. Malformed offsets and lengths outside [0, Tk] set the workspace's
+ *   device status to SCAN_ERR_SEQLENS (and are clamped).
+ *   A query that has no key has o = 0, lse = -inf. lse: fp32 [B, Hq, Tq], the log of
+ *   each row's sum of exponentials, written.
+ * Statistics and sums are fp32. Keys and values past a row's length are never used,
+ * whatever they hold; values within have to be finite. An output must not overlap an
+ * input or another output.
+ * workspace: cross_attn_workspace_bytes() (n_seqs = 0 unless packed, backward != 0 for
+ * the backward's), zeroed once with scan_workspace_init. SCAN_ERR_UNSUPPORTED unless D
+ * is a multiple of 8 up to 128 and B Hq <= 65535; SCAN_ERR_INVALID_ARG unless Hq % Hk
+ * == 0 and scale > 0 and finite. */
+size_t cross_attn_workspace_bytes(int64_t B, int64_t Tq, int64_t Tk, int64_t Hq, int64_t Hk,
+                                  int64_t D, int64_t n_seqs, int32_t backward);
+scan_status cross_attn_fwd(const scan_view4* q, const scan_view4* k, const scan_view4* v,
+                           const int32_t* k_lens, const int32_t* cu_seqlens_q,
+                           const int32_t* cu_seqlens_k, int32_t n_seqs, const scan_view4* o,
+                           float* lse, int64_t B, int64_t Tq, int64_t Tk, int64_t Hq, int64_t Hk,
+                           int64_t D, float scale, scan_dtype dt, void* workspace,
+                           size_t workspace_bytes, cudaStream_t stream);
+
+/* Its backward from the forward's o and lse, by the formulas of window_attn_bwd over
+ * the same pairs. dq, dk, dv: dtype dt, written; the rows of dk and dv past a length
+ * are zeros. No sum depends on the order in which blocks run. Errors and workspace as
+ * the forward's. */
+scan_status cross_attn_bwd(const scan_view4* q, const scan_view4* k, const scan_view4* v,
+                           const scan_view4* o, const float* lse, const scan_view4* dout,
+                           const int32_t* k_lens, const int32_t* cu_seqlens_q,
+                           const int32_t* cu_seqlens_k, int32_t n_seqs, const scan_view4* dq,
+                           const scan_view4* dk, const scan_view4* dv, int64_t B, int64_t Tq,
+                           int64_t Tk, int64_t Hq, int64_t Hk, int64_t D, float scale,
+                           scan_dtype dt, void* workspace, size_t workspace_bytes,
+                           cudaStream_t stream);
+
+/* One query token of each of B requests over a pool of encoders' keys and values,
+ * which are only read.
+ *   q, o: [B, Hq, D] of dtype dt (views with stride_t unused); k_cache, v_cache:
+ *   [n_slots, Tk, Hk, D] of dtype dt, any strides but along D; lens (nullable): int32
+ *   [n_slots], the keys that each cache holds (forced into [0, Tk]), else Tk; slots:
+ *   int32 [B], the cache of each request, or NULL (request b has cache b). Requests may
+ *   share a cache. A slot outside [0, n_slots) marks an idle request, which gets o = 0,
+ *   as one without keys does. Rows past a length are never used. */
+scan_status cross_attn_step(const scan_view4* q, const scan_view4* k_cache,
+                            const scan_view4* v_cache, const int32_t* lens, const int32_t* slots,
+                            int64_t n_slots, const scan_view4* o, int64_t B, int64_t Tk, int64_t Hq,
+                            int64_t Hk, int64_t D, float scale, scan_dtype dt, cudaStream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * What a network runs around its blocks. Operands are [B, T, C] with a unit stride
+ * along C (scan_view4 with stride_h unused). */
+
+/* Dropout whose mask is never stored: y = x / (1 - p) where an element is kept, else 0
+ * (whatever x holds there).
+ * Element i (counted over [B, T, C] in order) has 16 bits of block i / 8 of Philox 4x32
+ * with ten rounds (Salmon, Moraes, Dror and Shaw, SC 2011): key = seed, counter =
+ * (block, call), number i % 8 counted from the low half of the first word. It is dropped
+ * where they are below 65536 p, rounded to a whole number (p is taken in steps of 2^-16,
+ * also in the factor 1 / (1 - p)). The mask depends on nothing else: not on types, strides
+ * or the GPU. Other values of `call` are independent masks of the same seed.
+ *   x, y: dtype dt, any strides; y may be x. rng (nullable): int64 {seed, call} on the
+ *   device, read instead of seed and call when the kernel runs, so that a captured graph
+ *   draws anew as its owner changes them.
+ * SCAN_ERR_INVALID_ARG unless 0 <= p <= 1; SCAN_ERR_UNSUPPORTED past 2^41 elements;
+ * SCAN_ERR_ALIGNMENT unless rng is 8-byte aligned. */
+scan_status dropout_fwd(const scan_view4* x, const scan_view4* y, int64_t B, int64_t T, int64_t C,
+                        double p, uint64_t seed, uint64_t call, const int64_t* rng, scan_dtype dt,
+                        cudaStream_t stream);
+/* Its backward, the same pass over the gradient: dx = dy / (1 - p) where kept, else 0. */
+scan_status dropout_bwd(const scan_view4* dy, const scan_view4* dx, int64_t B, int64_t T, int64_t C,
+                        double p, uint64_t seed, uint64_t call, const int64_t* rng, scan_dtype dt,
+                        cudaStream_t stream);
+
+/* The norms after and before a block, with its gate, dropout and residual scale:
+ *   z = post_weight y (mean(y^2) + eps)^(-1/2)          (y itself without post_weight)
+ *   x_out = alpha x + drop(gate z)
+ *   n = next_weight x_out (mean(x_out^2) + eps)^(-1/2)  (not formed without next_weight)
+ * y is what the block gave, x the residual stream before it, n what the next block reads;
+ * n is the norm of x_out as it is stored.
+ *   x, x_out: [B, T, C] of dtype stream_dt; y, n: of dtype dt (stream_dt fp32 with either
+ *   dt, or bf16 with bf16). post_weight, next_weight: fp32 [C] or NULL; gate: fp32 [C], or
+ *   [B, C] with row_gate != 0, or NULL (ones). p, seed, call, rng: as for dropout_fwd, over
+ *   the elements of [B, T, C]. y NULL: only the norm of x (no post_weight and gate, alpha =
+ *   1, p = 0; x_out is not written). x_out may be x, n may be y.
+ * Norms and sums are fp32, each result is rounded once. With eps = 0 a row of zeros has no
+ * norm and gives NaN.
+ * SCAN_ERR_UNSUPPORTED unless C % 8 == 0, C <= 8192 and B T < 2^31; SCAN_ERR_ALIGNMENT
+ * unless every pointer is 16-byte aligned and every stride a multiple of 16 bytes;
+ * SCAN_ERR_INVALID_ARG for negative sizes, a NaN or negative eps, an alpha that is not
+ * finite, p outside [0, 1] or a missing pointer. */
+size_t residual_norm_workspace_bytes(int64_t B, int64_t T, int64_t C, int32_t row_gate);
+scan_status residual_norm_fwd(const scan_view4* x, const scan_view4* y, const float* post_weight,
+                              const float* gate, const float* next_weight, const scan_view4* x_out,
+                              const scan_view4* n, int64_t B, int64_t T, int64_t C, int32_t row_gate,
+                              float alpha, float eps, double p, uint64_t seed, uint64_t call,
+                              const int64_t* rng, scan_dtype stream_dt, scan_dtype dt,
+                              cudaStream_t stream);
+
+/* Its backward for L = sum <dx_out, x_out> + <dn, n>, from x_out and y; the same mask is
+ * drawn again. dx_out may be NULL (0) where next_weight is given; x_out and dn are not used
+ * without it. dx: stream_dt, dy: dt, written (dx may be dx_out, dy may be dn); dpost_weight,
+ * dgate, dnext_weight: fp32 in their inputs' shapes, written, or NULL. The sums over rows are
+ * fp32 in a fixed order. workspace: residual_norm_workspace_bytes() bytes, 16-byte aligned,
+ * nothing kept between calls. Other errors as the forward's. */
+scan_status residual_norm_bwd(const scan_view4* x_out, const scan_view4* y, const scan_view4* dx_out,
+                              const scan_view4* dn, const float* post_weight, const float* gate,
+                              const float* next_weight, const scan_view4* dx, const scan_view4* dy,
+                              float* dpost_weight, float* dgate, float* dnext_weight, int64_t B,
+                              int64_t T, int64_t C, int32_t row_gate, float alpha, float eps,
+                              double p, uint64_t seed, uint64_t call, const int64_t* rng,
+                              scan_dtype stream_dt, scan_dtype dt, void* workspace,
+                              size_t workspace_bytes, cudaStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
