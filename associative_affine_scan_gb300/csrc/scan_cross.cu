@@ -15,6 +15,7 @@
 // both factors are read 16 bytes at a time: three shared-memory cycles a warp for 16
 // multiply-adds a thread.
 #include "scan_cross.h"
+#include "scan_cross_tc.h"
 
 namespace scan {
 namespace {
@@ -474,7 +475,8 @@ scan_status cross_attn_fwd(const scan_view4* q, const scan_view4* k, const scan_
   if (Tk > 0) a.k = *k, a.v = *v;
   a.o = *o;
   a.lse = lse;
-  const cudaError_t e = launch_cross_general_fwd(a, dt, stream);
+  const cudaError_t e = cross_tc_fits(a, dt, false) ? launch_cross_tc_fwd(a, stream)
+                                                    : launch_cross_general_fwd(a, dt, stream);
   return e == cudaSuccess ? SCAN_OK : SCAN_ERR_CUDA;
 }
 
