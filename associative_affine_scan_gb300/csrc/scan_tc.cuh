@@ -88,6 +88,23 @@ __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, const St
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, const Stop& s) {
   return __all_sync(0xffffffffu, bar_wait(bar, parity, s));
 }
+// The same without a call: a kernel that moves registers between its warpgroups makes none.
+__device__ __forceinline__ bool bar_wait_here(uint32_t bar, uint32_t parity, const Stop& s) {
+  if (bar_try(bar, parity)) return true;
+  const uint64_t t0 = now_ns();
+  while (!bar_try(bar, parity)) {
+    if (*s.flag) return false;
+    if (now_ns() - t0 > kWaitNs) {
+      *s.flag = 1;
+      s.hdr->status = SCAN_ERR_TIMEOUT;
+      return false;
+    }
+  }
+  return true;
+}
+__device__ __forceinline__ bool warp_wait_here(uint32_t bar, uint32_t parity, const Stop& s) {
+  return __all_sync(0xffffffffu, bar_wait_here(bar, parity, s));
+}
 // After an expired wait copies may still be in flight towards the block's
 // shared memory: stay until they must have landed.
 __device__ __forceinline__ void linger(const Stop& s) {
@@ -115,6 +132,10 @@ __device__ __forceinline__ void copy_out_4d(const CUtensorMap* map, uint32_t src
 }
 __device__ __forceinline__ void copy_out_commit() {
   asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+// The copies' sources may be written again.
+__device__ __forceinline__ void copy_out_read() {
+  asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
 }
 __device__ __forceinline__ void copy_out_done() {
   asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
@@ -241,6 +262,36 @@ __device__ __forceinline__ void mma_tn(bool lead, uint32_t d, uint32_t a, uint32
   for (int k = 0; k < K / 16; ++k) mma_ts(lead, d, a + k * 8, b + k * (2048 >> 4), desc, add || k > 0);
 }
 
+// The same products issued by one lane of a converged warp, `if (elect()) { ... }`: its
+// instructions are then as few as the tensor cores take (48 cycles a 128 x 64 x 16
+// product, the operands' own time, where the predicated form above takes 59), so that
+// one or two products wait in the queue while the warp commits or waits.
+__device__ __forceinline__ bool elect() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n}" : "=r"(p));
+  return p != 0;
+}
+__device__ __forceinline__ uint64_t desc64(uint32_t low) { return ((uint64_t)kDescHigh << 32) | low; }
+__device__ __forceinline__ void mma_ss1(uint32_t d, uint32_t a, uint32_t b, uint32_t desc, bool add) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d),
+      "l"(desc64(a)), "l"(desc64(b)), "r"(desc), "r"((uint32_t)add)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts1(uint32_t d, uint32_t a, uint32_t b, uint32_t desc, bool add) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d),
+      "r"(a), "l"(desc64(b)), "r"(desc), "r"((uint32_t)add)
+      : "memory");
+}
+__device__ __forceinline__ void commit1(uint32_t bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+// A value that is the same in all lanes, for the compiler to know.
+__device__ __forceinline__ uint32_t uniform(uint32_t v) { return __shfl_sync(0xffffffffu, v, 0); }
+
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&h);
@@ -255,6 +306,11 @@ __device__ __forceinline__ float fast_exp2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
 }
 // Pairs of fp32 in one operation.
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {

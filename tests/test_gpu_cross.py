@@ -231,3 +231,28 @@ def test_caches_past_32_bits(lib):
     q = normal(g, N, 4, D, dtype=BF)
     step_check(lib, q, kc, kc, ints(20, 3, 17), ints(2, 0, 1))
     check(lib, (q[:, None].contiguous(), kc, kc, normal(g, N, 1, 4, D, dtype=BF)))
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("place", [1, 40, 127, 128, 300])
+def test_scores_that_grow(lib, D, place):
+    """Keys from `place` on score some 200 above those before: the weights of what came
+    before are as nothing, and the reference that they were taken from has to move, within
+    a tile and between tiles, for some rows only."""
+    q, k, v, do = inputs(1, 130, 400, 2, 1, D, BF, place)
+    q[..., 0], k[..., 0] = 16.0, 0.0
+    q[:, ::3, :, 0] = 0.0
+    k[:, place:, :, 0] = 12.5
+    check(lib, (q, k, v, do), scale=1.0)
+
+
+def test_values_that_are_no_numbers_show(lib):
+    """A score that overflows makes its own row NaN and leaves the others alone."""
+    q, k, v, do = inputs(1, 200, 300, 2, 2, 64, BF, 5)
+    want, _ = lib.cross_attn_fwd(q, k, v)
+    q[0, 7, 1] = NAN
+    got, lse = lib.cross_attn_fwd(q, k, v)
+    assert bool(got[0, 7, 1].isnan().all()) and bool(lse[0, 1, 7].isnan())
+    rest = torch.ones_like(got, dtype=torch.bool)
+    rest[0, 7, 1] = False
+    assert torch.equal(got[rest], want[rest])
