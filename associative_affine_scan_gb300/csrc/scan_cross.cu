@@ -456,7 +456,7 @@ size_t cross_attn_workspace_bytes(int64_t B, int64_t Tq, int64_t Tk, int64_t Hq,
                                   int32_t backward) {
   if (B < 0 || Tq < 0 || Tk < 0 || Hq < 0 || Hk < 0 || D < 1 || D > kMixMaxDim || n_seqs < 0) return 0;
   if (!backward) return kWsHeaderBytes;
-  return kWsHeaderBytes + round_up((size_t)(B * Hq * Tq) * 4, 256);
+  return kWsHeaderBytes + round_up((size_t)(B * Hq * Tq) * 4, 256) + cross_tc_bwd_floats(B, Tq, Tk, Hq, D, n_seqs) * 4;
 }
 
 scan_status cross_attn_fwd(const scan_view4* q, const scan_view4* k, const scan_view4* v, const int32_t* k_lens,
@@ -497,7 +497,8 @@ scan_status cross_attn_bwd(const scan_view4* q, const scan_view4* k, const scan_
   if (Tq > 0) a.q = *q, a.o = *o, a.dout = *dout, a.dq = *dq;
   if (Tk > 0) a.k = *k, a.v = *v, a.dk = *dk, a.dv = *dv;
   a.lse = const_cast<float*>(lse);
-  const cudaError_t e = launch_cross_general_bwd(a, dt, stream);
+  const cudaError_t e = cross_tc_fits(a, dt, true) ? launch_cross_tc_bwd(a, stream)
+                                                   : launch_cross_general_bwd(a, dt, stream);
   return e == cudaSuccess ? SCAN_OK : SCAN_ERR_CUDA;
 }
 

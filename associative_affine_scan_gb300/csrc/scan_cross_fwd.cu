@@ -451,8 +451,7 @@ cudaError_t launch_cross_tc_fwd(const CrossArgs& a, cudaStream_t s) {
   t.G = a.Hq / a.Hk;
   t.two_heads = t.G % 2 == 0;
   t.D = a.D;
-  t.wide = a.D % 16 == 0 && (uintptr_t)a.o.ptr % 32 == 0 && (a.B == 1 || a.o.stride_b % 16 == 0) &&
-           (a.Tq == 1 || a.o.stride_t % 16 == 0) && (a.Hq == 1 || a.o.stride_h % 16 == 0);
+  t.wide = rows_on_32(a.o, a.B, a.Tq, a.Hq, a.D);
   t.sl2 = a.scale * 1.44269504088896341f;
   const int rows = t.two_heads ? kRows : 2 * kRows;
   t.tiles = (a.Tq + rows - 1) / rows + (a.cu_q ? a.n_seqs : 0);
