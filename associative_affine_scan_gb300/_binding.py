@@ -60,7 +60,8 @@ EXPORTED = (
     "rglru_fwd", "rglru_bwd", "qk_norm_rope_workspace_bytes", "qk_norm_rope_fwd",
     "qk_norm_rope_bwd", "linattn_workspace_bytes", "linattn_fwd", "linattn_bwd", "linattn_step",
     "window_attn_workspace_bytes", "window_attn_fwd", "window_attn_bwd", "window_attn_step",
-    "cross_attn_workspace_bytes", "cross_attn_fwd", "cross_attn_bwd", "cross_attn_step",
+    "cross_attn_workspace_bytes", "cross_attn_fwd", "cross_attn_bwd",
+    "cross_attn_step_workspace_bytes", "cross_attn_step",
     "dropout_fwd", "dropout_bwd", "residual_norm_workspace_bytes", "residual_norm_fwd",
     "residual_norm_bwd",
 )
@@ -171,8 +172,9 @@ _SIGS = {
                        + [_f32, ctypes.c_int, _vp, _sz, _vp], ctypes.c_int),
     "cross_attn_bwd": ([_v4] * 4 + [_vp, _v4] + [_vp] * 3 + [_i32] + [_v4] * 3 + [_i64] * 6
                        + [_f32, ctypes.c_int, _vp, _sz, _vp], ctypes.c_int),
+    "cross_attn_step_workspace_bytes": ([_i64] * 5, _sz),
     "cross_attn_step": ([_v4] * 3 + [_vp] * 2 + [_i64, _v4] + [_i64] * 5
-                        + [_f32, ctypes.c_int, _vp], ctypes.c_int),
+                        + [_f32, ctypes.c_int, _vp, _sz, _vp], ctypes.c_int),
     "dropout_fwd": ([_v4] * 2 + [_i64] * 3 + [_f64, _u64, _u64, _vp, ctypes.c_int, _vp], ctypes.c_int),
     "dropout_bwd": ([_v4] * 2 + [_i64] * 3 + [_f64, _u64, _u64, _vp, ctypes.c_int, _vp], ctypes.c_int),
     "residual_norm_workspace_bytes": ([_i64] * 3 + [_i32], _sz),
@@ -1335,6 +1337,10 @@ def cross_attn_bwd(q, k, v, o, lse, dout, k_lens=None, cu_seqlens_q=None, cu_seq
     return dq, dk, dv
 
 
+def cross_attn_step_workspace_bytes(B, Tk, Hq, Hk, D) -> int:
+    return int(lib().cross_attn_step_workspace_bytes(B, Tk, Hq, Hk, D))
+
+
 def cross_attn_step(q, k_cache, v_cache, lens=None, slots=None, *, scale=None, out=None, stream=None):
     """One query token of each request over a pool of encoders' keys and values,
     which are only read. q [B, Hq, D]; k_cache, v_cache [n_slots, Tk, Hk, D],
@@ -1353,9 +1359,11 @@ def cross_attn_step(q, k_cache, v_cache, lens=None, slots=None, *, scale=None, o
     o = out if out is not None else torch.empty(q.shape, dtype=dt, device=dev)
     if out is not None:
         _written(o, "out", dtype=dt, shape=q.shape, device=dev)
+    s = _raw_stream(stream, dev)
+    ws = _mixer_workspace(cross_attn_step_workspace_bytes(B, Tk, Hq, Hk, D), dev, s)
     _enter(dev, "cross_attn_step", _view4(q), _view4(k_cache), _view4(v_cache), _at(lens), _at(slots),
            n_slots, _view4(o), B, Tk, Hq, Hk, D, D ** -0.5 if scale is None else scale, _dtype_code(q),
-           _raw_stream(stream, dev))
+           ws.data_ptr(), ws.numel(), s)
     return o
 
 

@@ -502,17 +502,26 @@ scan_status cross_attn_bwd(const scan_view4* q, const scan_view4* k, const scan_
   return e == cudaSuccess ? SCAN_OK : SCAN_ERR_CUDA;
 }
 
+size_t cross_attn_step_workspace_bytes(int64_t B, int64_t Tk, int64_t Hq, int64_t Hk, int64_t D) {
+  if (B < 0 || Tk < 0 || Hq < 0 || Hk < 0 || D < 1 || D > kMixMaxDim) return 0;
+  return kWsHeaderBytes + cross_step_bytes(B, Tk, Hq, Hk, D);
+}
+
 scan_status cross_attn_step(const scan_view4* q, const scan_view4* k_cache, const scan_view4* v_cache,
                             const int32_t* lens, const int32_t* slots, int64_t n_slots, const scan_view4* o, int64_t B,
-                            int64_t Tk, int64_t Hq, int64_t Hk, int64_t D, float scale, scan_dtype dt,
-                            cudaStream_t stream) {
+                            int64_t Tk, int64_t Hq, int64_t Hk, int64_t D, float scale, scan_dtype dt, void* workspace,
+                            size_t workspace_bytes, cudaStream_t stream) {
   const scan_status st = cross_sizes(B, 1, Tk, Hq, Hk, D, scale, dt);
   if (st != SCAN_OK) return st;
   if (n_slots < 0 || (!slots && n_slots < B)) return SCAN_ERR_INVALID_ARG;
   if (B * Hq == 0) return SCAN_OK;
   if (!given(q) || !given(o) || (n_slots * Tk > 0 && (!given(k_cache) || !given(v_cache)))) return SCAN_ERR_INVALID_ARG;
-  CrossStepArgs a{*q, {}, {}, *o, lens, slots, n_slots, Tk, (int)Hq, (int)Hk, (int)D, scale};
+  if (!workspace || (uintptr_t)workspace % 16 || workspace_bytes < cross_attn_step_workspace_bytes(B, Tk, Hq, Hk, D))
+    return SCAN_ERR_WORKSPACE;
+  CrossStepArgs a{*q, {}, {}, *o, lens, slots, n_slots, Tk, (int)Hq, (int)Hk, (int)D, scale,
+                  static_cast<WsHeader*>(workspace), static_cast<char*>(workspace) + kWsHeaderBytes};
   if (n_slots * Tk > 0) a.k = *k_cache, a.v = *v_cache;
+  if (cross_step_fits(a, dt, B)) return launch_cross_step(a, B, stream) == cudaSuccess ? SCAN_OK : SCAN_ERR_CUDA;
   if (dt == SCAN_BF16) cross_step_general<__nv_bfloat16><<<(unsigned)(B * Hq), 256, 0, stream>>>(a);
   else cross_step_general<float><<<(unsigned)(B * Hq), 256, 0, stream>>>(a);
   return cudaGetLastError() == cudaSuccess ? SCAN_OK : SCAN_ERR_CUDA;

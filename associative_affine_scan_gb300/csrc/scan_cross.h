@@ -76,6 +76,8 @@ struct CrossStepArgs {
   int64_t n_slots, Tk;
   int Hq, Hk, D;
   float scale;
+  WsHeader* hdr;
+  void* ws;  // after the header
 };
 
 }  // namespace scan

@@ -1,5 +1,6 @@
 // scan_cross_tc.h -- the tensor-core form of attention to another sequence
-// (scan_cross_fwd.cu, scan_cross_bwd.cu): which calls it takes and its launches.
+// (scan_cross_fwd.cu, scan_cross_bwd.cu) and its form for single tokens
+// (scan_cross_step.cu): which calls they take and their launches.
 #pragma once
 
 #include "scan_cross.h"
@@ -12,6 +13,11 @@ cudaError_t launch_cross_tc_fwd(const CrossArgs& a, cudaStream_t s);
 // Floats of workspace for the parts of the keys' tiles that blocks share.
 size_t cross_tc_bwd_floats(int64_t B, int64_t Tq, int64_t Tk, int64_t Hq, int64_t D, int64_t n_seqs);
 cudaError_t launch_cross_tc_bwd(const CrossArgs& a, cudaStream_t s);
+
+// Bytes of workspace for the parts of the units that blocks share.
+size_t cross_step_bytes(int64_t B, int64_t Tk, int64_t Hq, int64_t Hk, int64_t D);
+bool cross_step_fits(const CrossStepArgs& a, scan_dtype dt, int64_t B);
+cudaError_t launch_cross_step(const CrossStepArgs& a, int64_t B, cudaStream_t s);
 
 // Whether the rows of a [B, T, H, D] bf16 output start on 32 bytes and are whole pieces of them.
 inline bool rows_on_32(const scan_view4& v, int64_t B, int64_t T, int64_t H, int64_t D) {

@@ -723,11 +723,15 @@ scan_status cross_attn_bwd(const scan_view4* q, const scan_view4* k, const scan_
  *   [n_slots], the keys that each cache holds (forced into [0, Tk]), else Tk; slots:
  *   int32 [B], the cache of each request, or NULL (request b has cache b). Requests may
  *   share a cache. A slot outside [0, n_slots) marks an idle request, which gets o = 0,
- *   as one without keys does. Rows past a length are never used. */
+ *   as one without keys does. Rows past a length are never used.
+ * workspace: cross_attn_step_workspace_bytes(), zeroed once with scan_workspace_init;
+ * nothing is kept in it between calls but its status word. */
+size_t cross_attn_step_workspace_bytes(int64_t B, int64_t Tk, int64_t Hq, int64_t Hk, int64_t D);
 scan_status cross_attn_step(const scan_view4* q, const scan_view4* k_cache,
                             const scan_view4* v_cache, const int32_t* lens, const int32_t* slots,
                             int64_t n_slots, const scan_view4* o, int64_t B, int64_t Tk, int64_t Hq,
-                            int64_t Hk, int64_t D, float scale, scan_dtype dt, cudaStream_t stream);
+                            int64_t Hk, int64_t D, float scale, scan_dtype dt, void* workspace,
+                            size_t workspace_bytes, cudaStream_t stream);
 
 /* ---------------------------------------------------------------------------
  * What a network runs around its blocks. Operands are [B, T, C] with a unit stride

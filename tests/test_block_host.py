@@ -62,8 +62,9 @@ def test_cross_checks(lib):
     assert bwd(dk=NULL) == INVALID
     assert bwd(dout=None) == INVALID
     assert bwd(nws=256) == WORKSPACE
-    step = lambda kc=V, slots=P, n=4, B=2, D=64, scale=1.0: lib.cross_attn_step(  # noqa: E731
-        V, kc, V, P, slots, n, V, B, 50, 4, 2, D, scale, 1, None)
+    step = lambda kc=V, slots=P, n=4, B=2, D=64, scale=1.0, nws=1 << 30: lib.cross_attn_step(  # noqa: E731
+        V, kc, V, P, slots, n, V, B, 50, 4, 2, D, scale, 1, P, nws, None)
+    assert step(nws=256) == WORKSPACE
     assert step(kc=NULL) == INVALID
     assert step(n=-1) == INVALID
     assert step(slots=None, n=1) == INVALID
