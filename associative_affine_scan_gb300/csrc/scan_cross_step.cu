@@ -55,7 +55,8 @@ struct Plan {
   // that is to come for one that was.
   static constexpr int kStages = DP == 128 ? 6 : 12;
   static_assert(kStages % 2 == 0, "a stage belongs to one group");
-  static constexpr int kFold = 2 * kHeads * DP * 4;  // sums of two warps
+  static constexpr int kRow = DP + 8;                // floats: rows eight apart lie in different banks
+  static constexpr int kFold = 4 * 8 * kRow * 4;     // sums of four warps, eight heads
   static constexpr int kSmem = kStages * 2 * kTileBytes + kFold + 1024 + 2048;
 };
 
@@ -123,12 +124,16 @@ __global__ void __launch_bounds__(kThreads, 1) cross_step_kernel(const __grid_co
   const uint32_t bFull = smem_addr(misc), bEmpty = bFull + 8 * NS;
   float* const s_m = reinterpret_cast<float*>(misc + 256);  // [8 warps][16]
   float* const s_l = s_m + kWarps * kHeads;
+  float* const s_sum = s_l + kWarps * kHeads;  // [16]
   __shared__ int64_t s_scan[kThreads / 32], s_place[3];
   __shared__ uint32_t stop_flag, s_quit;
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
   const int units = a.Hk * a.rounds;
 
+  asm volatile("griddepcontrol.launch_dependents;");  // the second kernel's blocks come beside this one's
   if (tid == 0) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(&a.k) : "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(&a.v) : "memory");
     stop_flag = s_quit = 0;
     for (int i = 0; i < NS; ++i) {
       bar_init(bFull + 8 * i, 1);
@@ -340,64 +345,53 @@ __global__ void __launch_bounds__(kThreads, 1) cross_step_kernel(const __grid_co
         for (int i = 0; i < kWarps; ++i)
           sum[h] = fmaf(s_l[i * kHeads + 8 * h + g], fast_exp2(s_m[i * kHeads + 8 * h + g] - from), sum[h]);
       }
+      // eight heads at a time: the sums of warps 4 to 7 are added to those of warps 0 to 3,
+      // then these four in order, by all threads
+      const bool whole = count == w.tiles;
+      const int place = w.tile > 0 ? 0 : 1;  // of a part: begun in an earlier share, or in this
 #pragma unroll
-      for (int i = 0; i < NN; ++i) {
-        acc[i][0] *= f[0];
-        acc[i][1] *= f[0];
-        acc[i][2] *= f[1];
-        acc[i][3] *= f[1];
-      }
-      // two at a time: 4, 5 to 0, 1; 6, 7 to 2, 3; 2, 3 to 0, 1; 1 to 0
+      for (int h = 0; h < 2; ++h) {
+        if (8 * h >= heads) break;
+        float* const at = fold + ((warp % 4) * 8 + g) * P::kRow + 2 * c;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int from = i == 0 ? 4 : i == 1 ? 6 : i == 2 ? 2 : 1, to = i == 1 ? 2 : 0, many = i == 3 ? 1 : 2;
-        if (warp >= from && warp < from + many) {
-          float* const at = fold + (warp - from) * kHeads * DP;
+        for (int i = 0; i < NN; ++i) acc[i][2 * h] *= f[h], acc[i][2 * h + 1] *= f[h];
+        if (warp >= 4)
 #pragma unroll
-          for (int j = 0; j < NN; ++j) {
-            *reinterpret_cast<float2*>(at + g * DP + 8 * j + 2 * c) = make_float2(acc[j][0], acc[j][1]);
-            *reinterpret_cast<float2*>(at + (g + 8) * DP + 8 * j + 2 * c) = make_float2(acc[j][2], acc[j][3]);
+          for (int i = 0; i < NN; ++i) *reinterpret_cast<float2*>(at + 8 * i) = make_float2(acc[i][2 * h], acc[i][2 * h + 1]);
+        sync_compute();
+        if (warp < 4)
+#pragma unroll
+          for (int i = 0; i < NN; ++i) {
+            const float2 e = *reinterpret_cast<const float2*>(at + 8 * i);
+            *reinterpret_cast<float2*>(at + 8 * i) = make_float2(acc[i][2 * h] + e.x, acc[i][2 * h + 1] + e.y);
           }
+        if (warp == 0 && c == 0) {  // what the outputs are divided by, of each head
+          s_sum[8 * h + g] = sum[h];
+          if (!whole) part[place].m[8 * h + g] = top[h], part[place].l[8 * h + g] = sum[h];
         }
         sync_compute();
-        if (warp >= to && warp < to + many) {
-          const float* const at = fold + (warp - to) * kHeads * DP;
+        if (!quit)
+          for (int i = tid; i < 8 * (DP / 2); i += 32 * kWarps) {
+            const int r = i / (DP / 2), d = 2 * (i % (DP / 2));
+            if (8 * h + r >= heads || d >= a.D) continue;
+            float2 e = *reinterpret_cast<const float2*>(fold + r * P::kRow + d);
 #pragma unroll
-          for (int j = 0; j < NN; ++j) {
-            const float2 x = *reinterpret_cast<const float2*>(at + g * DP + 8 * j + 2 * c);
-            const float2 y = *reinterpret_cast<const float2*>(at + (g + 8) * DP + 8 * j + 2 * c);
-            acc[j][0] += x.x, acc[j][1] += x.y, acc[j][2] += y.x, acc[j][3] += y.y;
+            for (int k = 1; k < 4; ++k) {
+              const float2 y = *reinterpret_cast<const float2*>(fold + (8 * k + r) * P::kRow + d);
+              e.x += y.x, e.y += y.y;
+            }
+            if (whole) {
+              const float inv = s_sum[8 * h + r] == 0.f ? 0.f : 1.f / s_sum[8 * h + r];
+              *reinterpret_cast<uint32_t*>(o + (8 * h + r) * a.o_sh + d) = pack_bf16(e.x * inv, e.y * inv);
+            } else {
+              *reinterpret_cast<float2*>(a.out + ((2 * (int64_t)blockIdx.x + place) * kHeads + 8 * h + r) * a.D + d) = e;
+            }
           }
-        }
-        sync_compute();
+        if (h == 0 && heads > 8) sync_compute();  // the place is free again
       }
-      if (warp == 0 && !quit) {
-        if (count == w.tiles) {
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const float inv = sum[h] == 0.f ? 0.f : 1.f / sum[h];
-#pragma unroll
-            for (int i = 0; i < NN; ++i)
-              if (g + 8 * h < heads && 8 * i < a.D)
-                *reinterpret_cast<uint32_t*>(o + (g + 8 * h) * a.o_sh + 8 * i + 2 * c) =
-                    pack_bf16(acc[i][2 * h] * inv, acc[i][2 * h + 1] * inv);
-          }
-        } else {
-          const int place = w.tile > 0 ? 0 : 1;  // begun in an earlier share, or in this
-          float* const to = a.out + (2 * (int64_t)blockIdx.x + place) * kHeads * a.D;
-          if (lane == 0) {
-            part[place].unit = w.b * units + w.unit;
-            part[place].goes_on = w.tile + count < w.tiles;
-          }
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            if (c == 0) part[place].m[g + 8 * h] = top[h], part[place].l[g + 8 * h] = sum[h];
-#pragma unroll
-            for (int i = 0; i < NN; ++i)
-              if (8 * i < a.D)
-                *reinterpret_cast<float2*>(to + (g + 8 * h) * a.D + 8 * i + 2 * c) = make_float2(acc[i][2 * h], acc[i][2 * h + 1]);
-          }
-        }
+      if (tid == 0 && !quit && !whole) {
+        part[place].unit = w.b * units + w.unit;
+        part[place].goes_on = w.tile + count < w.tiles;
       }
       ok = !quit;
     }
@@ -410,6 +404,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_step_kernel(const __grid_co
 
 // Adds the parts of the unit whose first part is block blockIdx.x's last, in order.
 __global__ void __launch_bounds__(256) cross_step_parts_kernel(const __grid_constant__ StepArgs a, int grid) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // for the first kernel's end
   const Part* const p = a.part + 2 * blockIdx.x + 1;
   const int64_t id = p->unit;
   if (id < 0) return;
@@ -448,8 +443,18 @@ cudaError_t launch_step(const StepArgs& t, unsigned grid, cudaStream_t s) {
       cudaFuncSetAttribute(cross_step_kernel<DP>, cudaFuncAttributeMaxDynamicSharedMemorySize, Plan<DP>::kSmem);
   if (e != cudaSuccess) return e;
   cross_step_kernel<DP><<<grid, kThreads, Plan<DP>::kSmem, s>>>(t);
-  if (grid > 1) cross_step_parts_kernel<<<grid, 256, 0, s>>>(t, (int)grid);
-  return cudaGetLastError();
+  if (grid == 1) return cudaGetLastError();
+  // launched while the first kernel runs, whose end it waits for itself
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(256);
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, cross_step_parts_kernel, t, (int)grid);
 }
 
 // Blocks: no more than there can be tiles.

@@ -31,46 +31,34 @@ struct Eight<float> {
     a = __ldcs(reinterpret_cast<const float4*>(p));
     b = __ldcs(reinterpret_cast<const float4*>(p) + 1);
   }
-  __device__ __forceinline__ void get(float (&v)[8]) const {
-    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+  __device__ __forceinline__ void get(float2 (&v)[4]) const {
+    v[0] = make_float2(a.x, a.y), v[1] = make_float2(a.z, a.w), v[2] = make_float2(b.x, b.y), v[3] = make_float2(b.z, b.w);
   }
-  __device__ __forceinline__ static void store(float* p, const float (&v)[8]) {
-    __stcs(reinterpret_cast<float4*>(p), make_float4(v[0], v[1], v[2], v[3]));
-    __stcs(reinterpret_cast<float4*>(p) + 1, make_float4(v[4], v[5], v[6], v[7]));
+  __device__ __forceinline__ static void store(float* p, const float2 (&v)[4]) {
+    __stcs(reinterpret_cast<float4*>(p), make_float4(v[0].x, v[0].y, v[1].x, v[1].y));
+    __stcs(reinterpret_cast<float4*>(p) + 1, make_float4(v[2].x, v[2].y, v[3].x, v[3].y));
   }
 };
 template <>
 struct Eight<__nv_bfloat16> {
   uint4 a;
   __device__ __forceinline__ void load(const __nv_bfloat16* p) { a = __ldcs(reinterpret_cast<const uint4*>(p)); }
-  __device__ __forceinline__ void get(float (&v)[8]) const {
+  __device__ __forceinline__ void get(float2 (&v)[4]) const {
     const uint32_t u[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      v[2 * i] = __uint_as_float(u[i] << 16);
-      v[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
-    }
+    for (int i = 0; i < 4; ++i)
+      v[i] = make_float2(__uint_as_float(u[i] << 16), __uint_as_float(u[i] & 0xffff0000u));
   }
-  __device__ __forceinline__ static void store(__nv_bfloat16* p, const float (&v)[8]) {
+  __device__ __forceinline__ static void store(__nv_bfloat16* p, const float2 (&v)[4]) {
     uint32_t u[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+      const __nv_bfloat162 h = __floats2bfloat162_rn(v[i].x, v[i].y);
       u[i] = *reinterpret_cast<const uint32_t*>(&h);
     }
     __stcs(reinterpret_cast<uint4*>(p), make_uint4(u[0], u[1], u[2], u[3]));
   }
 };
-
-// An element that is dropped is 0 whatever it holds.
-__device__ __forceinline__ void apply(float (&v)[8], const uint4& r, const Drop& d) {
-  const uint32_t w[4] = {r.x, r.y, r.z, r.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    v[2 * i] = kept_low(w[i], d.limit) ? v[2 * i] * d.scale : 0.f;
-    v[2 * i + 1] = kept_high(w[i], d.limit) ? v[2 * i + 1] * d.scale : 0.f;
-  }
-}
 
 // ROWS: rows of C elements (a multiple of 8) at any 16-byte strides; else n elements
 // one after the other. The last, shorter block of those goes element by element.
@@ -98,19 +86,19 @@ __global__ void __launch_bounds__(kThreads) dropout_kernel(const DropArgs a) {
   for (int i = 0; i < kUnroll; ++i) {
     const int64_t blk = first + i * kThreads;
     if (blk < whole) {
-      float v[8];
+      float2 v[4];
       e[i].get(v);
-      apply(v, philox((uint64_t)blk, call, seed), a.drop);
+      if (a.drop.limit) drop8(v, a.drop, (uint64_t)blk, call, seed);
       Eight<T>::store(y + to[i], v);
     } else if (!ROWS && blk == whole && a.n % 8) {
       const int left = (int)(a.n % 8);
-      float v[8];
+      float2 v[4];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = j < left ? to_f32(x[blk * 8 + j]) : 0.f;
-      apply(v, philox((uint64_t)blk, call, seed), a.drop);
+      for (int j = 0; j < 8; ++j) (j % 2 ? v[j / 2].y : v[j / 2].x) = j < left ? to_f32(x[blk * 8 + j]) : 0.f;
+      if (a.drop.limit) drop8(v, a.drop, (uint64_t)blk, call, seed);
 #pragma unroll
       for (int j = 0; j < 8; ++j)
-        if (j < left) y[blk * 8 + j] = from_f32<T>(v[j]);
+        if (j < left) y[blk * 8 + j] = from_f32<T>(j % 2 ? v[j / 2].y : v[j / 2].x);
     }
   }
 }
@@ -124,22 +112,23 @@ __global__ void __launch_bounds__(kThreads) dropout_general(const DropArgs a) {
   if (blk * 8 >= a.n) return;
   int64_t row = blk * 8 / a.C, c = blk * 8 - row * a.C, b = row / a.T, t = row - b * a.T;
   const int left = a.n - blk * 8 < 8 ? (int)(a.n - blk * 8) : 8;
-  float v[8];
+  float2 v[4];
   int64_t to[8];
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
-    v[j] = 0.f;
+    float& e = j % 2 ? v[j / 2].y : v[j / 2].x;
+    e = 0.f;
     to[j] = b * a.y_sb + t * a.y_st + c;
-    if (j < left) v[j] = to_f32(static_cast<const T*>(a.x)[b * a.x_sb + t * a.x_st + c]);
+    if (j < left) e = to_f32(static_cast<const T*>(a.x)[b * a.x_sb + t * a.x_st + c]);
     if (++c == a.C) {
       c = 0;
       if (++t == a.T) t = 0, ++b;
     }
   }
-  apply(v, philox((uint64_t)blk, call, seed), a.drop);
+  if (a.drop.limit) drop8(v, a.drop, (uint64_t)blk, call, seed);
 #pragma unroll
   for (int j = 0; j < 8; ++j)
-    if (j < left) static_cast<T*>(a.y)[to[j]] = from_f32<T>(v[j]);
+    if (j < left) static_cast<T*>(a.y)[to[j]] = from_f32<T>(j % 2 ? v[j / 2].y : v[j / 2].x);
 }
 
 bool on16(const void* p) { return (uintptr_t)p % 16 == 0; }

@@ -36,6 +36,7 @@ __device__ __forceinline__ uint4 philox(uint64_t block, uint64_t call, uint64_t 
 // bits an element halve the generator's work against 32; p is off by 2^-17 at most.
 struct Drop {
   uint32_t limit;       // 0: nothing is dropped
+  uint32_t above;       // 65536 limit - 1: what a number's 16 bits, as a word's upper ones, have to pass
   float scale;
   uint64_t seed, call;  // used where rng is null
   const int64_t* rng;   // nullable: {seed, call} on the device
@@ -48,6 +49,7 @@ struct Drop {
 inline Drop make_drop(double p, uint64_t seed, uint64_t call, const int64_t* rng) {
   Drop d{};
   d.limit = (uint32_t)nearbyint(p * 65536.0);  // 0 <= p <= 1; ties to even
+  d.above = (uint32_t)(((uint64_t)d.limit << 16) - 1);
   d.scale = d.limit < 65536u ? (float)(65536.0 / (65536.0 - d.limit)) : 0.f;
   d.seed = seed;
   d.call = call;
@@ -55,8 +57,26 @@ inline Drop make_drop(double p, uint64_t seed, uint64_t call, const int64_t* rng
   return d;
 }
 
-// Numbers 2 i and 2 i + 1 of a block are in word i.
-__device__ __forceinline__ bool kept_low(uint32_t w, uint32_t limit) { return (w & 0xffffu) >= limit; }
-__device__ __forceinline__ bool kept_high(uint32_t w, uint32_t limit) { return (w >> 16) >= limit; }
+// The eight elements of a block times what they are kept with. An element that is dropped
+// is 0 whatever it holds. (limit > 0)
+__device__ __forceinline__ void drop8(float2 (&v)[4], const Drop& d, uint64_t block, uint64_t call, uint64_t seed) {
+  const uint4 r = philox(block, call, seed);
+  const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[i].x = w[i] << 16 > d.above ? v[i].x * d.scale : 0.f;
+    v[i].y = w[i] > d.above ? v[i].y * d.scale : 0.f;
+  }
+}
+
+// Which of the eight elements of a block are kept, a bit each.
+__device__ __forceinline__ uint32_t kept8(const Drop& d, uint64_t block, uint64_t call, uint64_t seed) {
+  const uint4 r = philox(block, call, seed);
+  const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) m |= (w[i] << 16 > d.above ? 1u << 2 * i : 0u) | (w[i] > d.above ? 2u << 2 * i : 0u);
+  return m;
+}
 
 }  // namespace scan

@@ -18,9 +18,14 @@
 // twice; sums are shuffles and one exchange through shared memory.
 #include "scan_mixer.h"
 #include "scan_philox.cuh"
+#include "scan_tc.cuh"
 
 namespace scan {
 namespace {
+
+using tc::add2;
+using tc::fma2;
+using tc::mul2;
 
 struct NormArgs {
   const void *x, *y, *dxo, *dn;  // forward: x, y; backward: x', y, dx', dn
@@ -31,6 +36,7 @@ struct NormArgs {
   int64_t gate_sb;                      // C where each batch row has a gate, else 0
   int64_t B, T, rows;
   int C, W;          // W: warps a row
+  int wide;          // rows of the stream and of gradients are on 32 bytes
   float alpha, eps, inv_C;
   Drop drop;
   // backward
@@ -40,102 +46,121 @@ struct NormArgs {
   int row_gate;
 };
 
+__device__ __forceinline__ float4 shared16(uint32_t at) {
+  float4 v;
+  asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(at) : "memory");
+  return v;
+}
+
 // Eight elements of a row, in memory and as numbers.
 template <typename T>
 struct Eight;
 template <>
 struct Eight<float> {
   float4 a, b;
-  __device__ __forceinline__ void load(const float* p) {
-    a = *reinterpret_cast<const float4*>(p);
-    b = *(reinterpret_cast<const float4*>(p) + 1);
+  __device__ __forceinline__ void load(const float* p, bool wide) {  // wide: p is on 32 bytes
+    if (wide) {
+      asm volatile("ld.global.v8.f32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                   : "=f"(a.x), "=f"(a.y), "=f"(a.z), "=f"(a.w), "=f"(b.x), "=f"(b.y), "=f"(b.z), "=f"(b.w)
+                   : "l"(p));
+    } else {
+      a = *reinterpret_cast<const float4*>(p);
+      b = *(reinterpret_cast<const float4*>(p) + 1);
+    }
   }
   __device__ __forceinline__ void clear() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
-  __device__ __forceinline__ void get(float (&v)[8]) const {
-    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+  __device__ __forceinline__ void take(uint32_t at, uint32_t apart) {  // pieces in shared memory
+    a = shared16(at);
+    b = shared16(at + apart);
   }
-  __device__ __forceinline__ void set(const float (&v)[8]) {
-    a = make_float4(v[0], v[1], v[2], v[3]);
-    b = make_float4(v[4], v[5], v[6], v[7]);
+  __device__ __forceinline__ void get(float2 (&v)[4]) const {
+    v[0] = make_float2(a.x, a.y);
+    v[1] = make_float2(a.z, a.w);
+    v[2] = make_float2(b.x, b.y);
+    v[3] = make_float2(b.z, b.w);
   }
-  __device__ __forceinline__ void store(float* p) const {
-    *reinterpret_cast<float4*>(p) = a;
-    *(reinterpret_cast<float4*>(p) + 1) = b;
+  __device__ __forceinline__ void set(const float2 (&v)[4]) {
+    a = make_float4(v[0].x, v[0].y, v[1].x, v[1].y);
+    b = make_float4(v[2].x, v[2].y, v[3].x, v[3].y);
+  }
+  __device__ __forceinline__ void store(float* p, bool wide) const {
+    if (wide) {
+      asm volatile("st.global.v8.f32 [%8], {%0, %1, %2, %3, %4, %5, %6, %7};" ::"f"(a.x), "f"(a.y), "f"(a.z), "f"(a.w),
+                   "f"(b.x), "f"(b.y), "f"(b.z), "f"(b.w), "l"(p)
+                   : "memory");
+    } else {
+      *reinterpret_cast<float4*>(p) = a;
+      *(reinterpret_cast<float4*>(p) + 1) = b;
+    }
   }
 };
 template <>
 struct Eight<__nv_bfloat16> {
   uint4 a;
-  __device__ __forceinline__ void load(const __nv_bfloat16* p) { a = *reinterpret_cast<const uint4*>(p); }
+  __device__ __forceinline__ void load(const __nv_bfloat16* p, bool) { a = *reinterpret_cast<const uint4*>(p); }
   __device__ __forceinline__ void clear() { a = make_uint4(0u, 0u, 0u, 0u); }
-  __device__ __forceinline__ void get(float (&v)[8]) const {
+  __device__ __forceinline__ void take(uint32_t at, uint32_t) {
+    const float4 v = shared16(at);
+    a = make_uint4(__float_as_uint(v.x), __float_as_uint(v.y), __float_as_uint(v.z), __float_as_uint(v.w));
+  }
+  __device__ __forceinline__ void get(float2 (&v)[4]) const {
     const uint32_t u[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      v[2 * i] = __uint_as_float(u[i] << 16);
-      v[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
-    }
+    for (int i = 0; i < 4; ++i)
+      v[i] = make_float2(__uint_as_float(u[i] << 16), __uint_as_float(u[i] & 0xffff0000u));
   }
-  __device__ __forceinline__ void set(const float (&v)[8]) {
+  __device__ __forceinline__ void set(const float2 (&v)[4]) {
     uint32_t u[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+      const __nv_bfloat162 h = __floats2bfloat162_rn(v[i].x, v[i].y);
       u[i] = *reinterpret_cast<const uint32_t*>(&h);
     }
     a = make_uint4(u[0], u[1], u[2], u[3]);
   }
-  __device__ __forceinline__ void store(__nv_bfloat16* p) const { *reinterpret_cast<uint4*>(p) = a; }
+  __device__ __forceinline__ void store(__nv_bfloat16* p, bool) const { *reinterpret_cast<uint4*>(p) = a; }
 };
 
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+
 // Weights of eight columns, ones where there are none.
-__device__ __forceinline__ void weights(const float* w, int c, bool on, float (&v)[8]) {
+__device__ __forceinline__ void weights(const float* w, int c, bool on, float2 (&v)[4]) {
   Eight<float> e;
   if (w && on) {
-    e.load(w + c);
+    e.load(w + c, false);
     e.get(v);
   } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = 1.f;
+    for (int i = 0; i < 4; ++i) v[i] = both(1.f);
   }
 }
 
-// Sums of N numbers over the W warps of a row, in warp order, for all its threads.
-// `red`: one slot a warp of the block; every thread of the block comes here.
+// Sums of up to four numbers over the W warps of a row, in warp order, for all its
+// threads. `red`: one slot a warp of the block; every thread of the block comes here.
 template <int N>
-__device__ __forceinline__ void row_sums(float (&s)[N], float (*red)[4], int W) {
+__device__ __forceinline__ void row_sums(float (&s)[N], float4* red, int W) {
 #pragma unroll
   for (int d = 16; d; d >>= 1)
 #pragma unroll
     for (int i = 0; i < N; ++i) s[i] += __shfl_xor_sync(0xffffffffu, s[i], d);
   if (W == 1) return;
   const int warp = threadIdx.x / 32, first = warp / W * W;
-  if (threadIdx.x % 32 == 0)
-#pragma unroll
-    for (int i = 0; i < N; ++i) red[warp][i] = s[i];
+  if (threadIdx.x % 32 == 0) red[warp] = make_float4(s[0], N > 1 ? s[N > 1 ? 1 : 0] : 0.f, N > 2 ? s[N > 2 ? 2 : 0] : 0.f, 0.f);
   __syncthreads();
-#pragma unroll
-  for (int i = 0; i < N; ++i) s[i] = 0.f;
-  for (int w = 0; w < W; ++w)
-#pragma unroll
-    for (int i = 0; i < N; ++i) s[i] += red[first + w][i];
-}
-
-// u = drop(u) of the eight elements of block `block` of the tensor.
-__device__ __forceinline__ void dropped(float (&v)[8], const Drop& d, uint64_t block, uint64_t call, uint64_t seed) {
-  const uint4 r = philox(block, call, seed);
-  const uint32_t w[4] = {r.x, r.y, r.z, r.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    v[2 * i] = kept_low(w[i], d.limit) ? v[2 * i] * d.scale : 0.f;
-    v[2 * i + 1] = kept_high(w[i], d.limit) ? v[2 * i + 1] * d.scale : 0.f;
+  float4 t = red[first];
+  for (int w = 1; w < W; ++w) {
+    const float4 o = red[first + w];
+    t.x += o.x, t.y += o.y, t.z += o.z;
   }
+  s[0] = t.x;
+  if (N > 1) s[N > 1 ? 1 : 0] = t.y;
+  if (N > 2) s[N > 2 ? 2 : 0] = t.z;
 }
 
 // V: vectors of eight elements a thread.
 template <typename X, typename Y, int V>
 __global__ void __launch_bounds__(512) residual_fwd_kernel(const NormArgs a) {
-  __shared__ float red[2][32][4];
+  __shared__ float4 red[2][16];
   const int per = blockDim.x / 32 / a.W, lane = threadIdx.x % (32 * a.W);  // rows a block, place in the row
   const int64_t row = (int64_t)blockIdx.x * per + threadIdx.x / (32 * a.W);
   const bool live = row < a.rows;
@@ -150,8 +175,8 @@ __global__ void __launch_bounds__(512) residual_fwd_kernel(const NormArgs a) {
     ex[v].clear();
     ey[v].clear();
     if (live && c < a.C) {
-      ex[v].load(x + c);
-      if (a.y) ey[v].load(y + c);
+      ex[v].load(x + c, a.wide);
+      if (a.y) ey[v].load(y + c, a.wide);
     }
   }
   if (a.y) {
@@ -159,188 +184,355 @@ __global__ void __launch_bounds__(512) residual_fwd_kernel(const NormArgs a) {
     a.drop.read(&seed, &call);
     float r = 1.f;
     if (a.w_post) {
-      float s[1] = {0.f};
+      float2 sq = both(0.f);
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        float f[8];
+        float2 f[4];
         ey[v].get(f);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) s[0] = fmaf(f[i], f[i], s[0]);
+        for (int i = 0; i < 4; ++i) sq = fma2(f[i], f[i], sq);
       }
+      float s[1] = {sq.x + sq.y};
       row_sums(s, red[0], a.W);
       r = rsqrtf(fmaf(s[0], a.inv_C, a.eps));
     }
+    X* const xo = static_cast<X*>(a.xo) + b * a.xo_sb + t * a.xo_st;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       const int c = 8 * (lane + v * 32 * a.W);
       const bool on = live && c < a.C;
-      float f[8], g[8], w[8];
+      float2 f[4], g[4], w[4];
       ey[v].get(f);
       weights(a.w_post, c, on, w);
       weights(a.gate ? a.gate + b * a.gate_sb : nullptr, c, on, g);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) f[i] = f[i] * r * w[i] * g[i];
-      if (a.drop.limit) dropped(f, a.drop, (uint64_t)(row * (a.C / 8) + c / 8), call, seed);
+      for (int i = 0; i < 4; ++i) f[i] = mul2(mul2(f[i], both(r)), mul2(w[i], g[i]));
+      if (a.drop.limit) drop8(f, a.drop, (uint64_t)(row * (a.C / 8) + c / 8), call, seed);
       ex[v].get(g);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) f[i] = fmaf(a.alpha, g[i], f[i]);
+      for (int i = 0; i < 4; ++i) f[i] = fma2(both(a.alpha), g[i], f[i]);
       ex[v].set(f);
-      if (on) ex[v].store(static_cast<X*>(a.xo) + b * a.xo_sb + t * a.xo_st + c);
+      if (on) ex[v].store(xo + c, a.wide);
     }
   }
   if (!a.w_next) return;
-  float s[1] = {0.f};
+  float2 sq = both(0.f);
 #pragma unroll
   for (int v = 0; v < V; ++v) {
-    float f[8];
+    float2 f[4];
     ex[v].get(f);
     if (8 * (lane + v * 32 * a.W) < a.C)
 #pragma unroll
-      for (int i = 0; i < 8; ++i) s[0] = fmaf(f[i], f[i], s[0]);
+      for (int i = 0; i < 4; ++i) sq = fma2(f[i], f[i], sq);
   }
+  float s[1] = {sq.x + sq.y};
   row_sums(s, red[1], a.W);
   const float q = rsqrtf(fmaf(s[0], a.inv_C, a.eps));
+  Y* const n = static_cast<Y*>(a.n) + b * a.n_sb + t * a.n_st;
 #pragma unroll
   for (int v = 0; v < V; ++v) {
     const int c = 8 * (lane + v * 32 * a.W);
     const bool on = live && c < a.C;
-    float f[8], w[8];
+    float2 f[4], w[4];
     ex[v].get(f);
     weights(a.w_next, c, on, w);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = f[i] * q * w[i];
+    for (int i = 0; i < 4; ++i) f[i] = mul2(mul2(f[i], both(q)), w[i]);
     Eight<Y> e;
     e.set(f);
-    if (on) e.store(static_cast<Y*>(a.n) + b * a.n_sb + t * a.n_st + c);
+    if (on) e.store(n + c, a.wide);
   }
 }
 
+// 16 bytes of a row to this thread's own place in shared memory.
+__device__ __forceinline__ void copy16(uint32_t to, const void* from) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+// Eight elements in pieces of 16 bytes.
+template <typename T>
+constexpr int kPieces = sizeof(T) * 8 / 16;
+__device__ __forceinline__ void keep16(uint32_t at, float2 a, float2 b) {
+  asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(at), "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y) : "memory");
+}
+
+// Sums of six numbers over the W warps of a row, for all its threads: a lane keeps half
+// of the numbers at each of three exchanges (16, 8 and 4 lanes away), so that seven
+// exchanges serve all; then the warps' in order. `red`: a slot a warp of the block.
+__device__ __forceinline__ void six_sums(float (&s)[6], float4 (*red)[2], int W) {
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, first = warp / W * W;
+  float v[4] = {s[0], s[1], s[2], s[3]};
+  {
+    const bool up = lane & 16;
+    const float u[4] = {s[4], s[5], 0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = (up ? u[i] : v[i]) + __shfl_xor_sync(0xffffffffu, up ? v[i] : u[i], 16);
+  }
+  {
+    const bool up = lane & 8;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) v[i] = (up ? v[i + 2] : v[i]) + __shfl_xor_sync(0xffffffffu, up ? v[i] : v[i + 2], 8);
+  }
+  {
+    const bool up = lane & 4;
+    v[0] = (up ? v[1] : v[0]) + __shfl_xor_sync(0xffffffffu, up ? v[0] : v[1], 4);
+  }
+  v[0] += __shfl_xor_sync(0xffffffffu, v[0], 2);
+  v[0] += __shfl_xor_sync(0xffffffffu, v[0], 1);
+  if (lane % 4 == 0) reinterpret_cast<float*>(red[warp])[lane / 4] = v[0];
+  if (W == 1) __syncwarp();
+  else __syncthreads();
+  float4 a = red[first][0], b = red[first][1];
+  for (int w = 1; w < W; ++w) {
+    const float4 c = red[first + w][0], d = red[first + w][1];
+    a.x += c.x, a.y += c.y, a.z += c.z, a.w += c.w, b.x += d.x, b.y += d.y;
+  }
+  s[0] = a.x, s[1] = a.y, s[2] = a.z, s[3] = a.w, s[4] = b.x, s[5] = b.y;
+}
+
+// A row of an operand, walked row by row without products of strides.
+template <typename T>
+struct Walk {
+  T* p;
+  int64_t step, wrap;  // to the next row of this thread's, and what a batch's end adds
+  __device__ __forceinline__ void start(T* base, int64_t sb, int64_t st, int64_t b, int64_t t, int64_t T_, int per, int c) {
+    p = base ? base + b * sb + t * st + c : nullptr;
+    step = per * st;
+    wrap = sb - T_ * st;
+  }
+  __device__ __forceinline__ void on(int wraps) {
+    p += step;
+    if (wraps) p += wraps * wrap;
+  }
+};
+
 // A block walks units: a part of the rows that share a gate, its column sums in
-// registers, left in the workspace and added in order by the kernel below.
-template <typename X, typename Y, int V>
-__global__ void __launch_bounds__(512) residual_bwd_kernel(const NormArgs a) {
-  __shared__ float red[2][32][4];
-  extern __shared__ float fold[];  // [rows a block - 1][2][C]
+// registers, left in the workspace and added in order by the kernel below. A thread
+// copies its pieces of the next rows to its own places in shared memory, AHEAD rows
+// ahead, so no barrier is needed for them; its weights lie there as well.
+template <typename X, typename Y, int V, int AHEAD>
+__global__ void __launch_bounds__(V == 4 ? 256 : 128, V == 4 ? 1 : 3) residual_bwd_kernel(const NormArgs a) {
+  constexpr int PX = kPieces<X>, PY = kPieces<Y>, PR = 2 * PX + 2 * PY, NS = AHEAD + 1;
+  __shared__ float4 red[2][8][2];
+  extern __shared__ float4 ring[];  // [NS V PR + 4 V][threads]; then the fold: [rows a block - 1][2][C]
   const int per = blockDim.x / 32 / a.W, lane = threadIdx.x % (32 * a.W), mine = threadIdx.x / (32 * a.W);
+  const uint32_t apart = blockDim.x * 16;  // bytes between a thread's pieces
+  const uint32_t own = (uint32_t)__cvta_generic_to_shared(ring) + threadIdx.x * 16, own_w = own + NS * V * PR * apart;
+  float* const fold = reinterpret_cast<float*>(ring);
   const int64_t units = a.groups * a.chunks;
+  asm volatile("griddepcontrol.launch_dependents;");  // the sums' blocks come beside this one's
   uint64_t seed, call;
   a.drop.read(&seed, &call);
+  const int c0 = 8 * lane, apart_c = 8 * 32 * a.W;  // a thread's first column, and from vector to vector
   for (int64_t unit = blockIdx.x; unit < units; unit += gridDim.x) {
     const int64_t grp = unit / a.chunks, ch = unit - grp * a.chunks;
     const int64_t beg = grp * a.span + a.span * ch / a.chunks, end = grp * a.span + a.span * (ch + 1) / a.chunks;
     const float* const gate = a.gate ? a.gate + (a.row_gate ? grp * a.gate_sb : 0) : nullptr;
-    float h[V][8], dw[V][8];
+    float2 h[V][4], dw[V][4];
 #pragma unroll
-    for (int v = 0; v < V; ++v)
+    for (int v = 0; v < V; ++v) {
+      const int c = c0 + v * apart_c;
+      float2 wn[4], wu[4];  // next_weight; post_weight times gate
+      weights(a.w_next, c, c < a.C, wn);
+      weights(a.w_post, c, c < a.C, wu);
+      weights(gate, c, c < a.C, h[v]);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) h[v][i] = dw[v][i] = 0.f;
+      for (int i = 0; i < 4; ++i) {
+        wu[i] = mul2(wu[i], h[v][i]);
+        h[v][i] = dw[v][i] = both(0.f);
+      }
+      keep16(own_w + (4 * v) * apart, wn[0], wn[1]);
+      keep16(own_w + (4 * v + 1) * apart, wn[2], wn[3]);
+      keep16(own_w + (4 * v + 2) * apart, wu[0], wu[1]);
+      keep16(own_w + (4 * v + 3) * apart, wu[2], wu[3]);
+    }
+    // the rows that are copied, and behind them those that are worked
+    const int64_t b0 = (beg + mine) / a.T;
+    int64_t lt = beg + mine - b0 * a.T, t = lt;
+    Walk<const X> wx, wg;
+    Walk<const Y> wy, we;
+    Walk<X> ox;
+    Walk<Y> oy;
+    wx.start(static_cast<const X*>(a.x), a.x_sb, a.x_st, b0, t, a.T, per, c0);
+    wg.start(static_cast<const X*>(a.dxo), a.xo_sb, a.xo_st, b0, t, a.T, per, c0);
+    wy.start(static_cast<const Y*>(a.y), a.y_sb, a.y_st, b0, t, a.T, per, c0);
+    we.start(static_cast<const Y*>(a.dn), a.n_sb, a.n_st, b0, t, a.T, per, c0);
+    ox.start(static_cast<X*>(a.dx), a.dx_sb, a.dx_st, b0, t, a.T, per, c0);
+    oy.start(static_cast<Y*>(a.dy), a.dy_sb, a.dy_st, b0, t, a.T, per, c0);
+    const auto wraps = [&](int64_t* t) {
+      int n = 0;
+      *t += per;
+      while (*t >= a.T) *t -= a.T, ++n;
+      return n;
+    };
+    const auto copy = [&](int64_t row, int slot) {
+      if (row < end) {
+        uint32_t to = own + (uint32_t)(slot * V * PR) * apart;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          if (c0 + v * apart_c < a.C) {
+            const int at = v * apart_c;
+            if (a.x) {
+#pragma unroll
+              for (int j = 0; j < PX; ++j) copy16(to + j * apart, reinterpret_cast<const char*>(wx.p + at) + 16 * j);
+#pragma unroll
+              for (int j = 0; j < PY; ++j)
+                copy16(to + (2 * PX + PY + j) * apart, reinterpret_cast<const char*>(we.p + at) + 16 * j);
+            }
+            if (a.dxo)
+#pragma unroll
+              for (int j = 0; j < PX; ++j) copy16(to + (PX + j) * apart, reinterpret_cast<const char*>(wg.p + at) + 16 * j);
+            if (a.y)
+#pragma unroll
+              for (int j = 0; j < PY; ++j) copy16(to + (2 * PX + j) * apart, reinterpret_cast<const char*>(wy.p + at) + 16 * j);
+          }
+          to += PR * apart;
+        }
+        const int n = wraps(&lt);
+        wx.on(n), wg.on(n), wy.on(n), we.on(n);
+      }
+      copies_commit();
+    };
+    int head = 0, odd = 0;
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i) copy(beg + mine + (int64_t)i * per, i);
     for (int64_t r0 = beg; r0 < end; r0 += per) {
       const int64_t row = r0 + mine;
       const bool live = row < end;
-      const int64_t b = live ? row / a.T : 0, t = live ? row - b * a.T : 0;
+      copy(row + (int64_t)AHEAD * per, head >= 1 ? head - 1 : NS - 1);
+      copies_wait<AHEAD>();
+      const uint32_t at0 = own + (uint32_t)(head * V * PR) * apart;
+      head = head + 1 == NS ? 0 : head + 1;
+      // x', dx', y, dn; zeros where there is nothing
       Eight<X> ex[V], eg[V];
       Eight<Y> ey[V], en[V];
+      uint32_t keep[V];  // a bit an element
+      float2 sum[6];     // y y; x' x'; e x'; and of d = post_weight gate y / (1 - p) where kept: d dx', d e, d x'
+#pragma unroll
+      for (int i = 0; i < 6; ++i) sum[i] = both(0.f);
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        const int c = 8 * (lane + v * 32 * a.W);
-        ex[v].clear();
-        eg[v].clear();
-        ey[v].clear();
-        en[v].clear();
-        if (live && c < a.C) {
-          if (a.w_next) {
-            ex[v].load(static_cast<const X*>(a.x) + b * a.x_sb + t * a.x_st + c);
-            en[v].load(static_cast<const Y*>(a.dn) + b * a.n_sb + t * a.n_st + c);
-          }
-          if (a.dxo) eg[v].load(static_cast<const X*>(a.dxo) + b * a.xo_sb + t * a.xo_st + c);
-          if (a.y) ey[v].load(static_cast<const Y*>(a.y) + b * a.y_sb + t * a.y_st + c);
-        }
-      }
-      float s[3] = {0.f, 0.f, 0.f};
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        const int c = 8 * (lane + v * 32 * a.W);
-        float y[8], x[8], e[8], w[8];
-        ey[v].get(y);
+        const int c = c0 + v * apart_c;
+        const uint32_t at = at0 + (uint32_t)(v * PR) * apart;
+        const bool here = live && c < a.C;
+        ex[v].clear(), eg[v].clear(), ey[v].clear(), en[v].clear();
+        if (here && a.x) ex[v].take(at, apart), en[v].take(at + (2 * PX + PY) * apart, apart);
+        if (here && a.dxo) eg[v].take(at + PX * apart, apart);
+        if (here && a.y) ey[v].take(at + 2 * PX * apart, apart);
+        float2 x[4], g[4], y[4], e[4], w[4];
         ex[v].get(x);
         en[v].get(e);
-        weights(a.w_next, c, c < a.C, w);
+        Eight<float> held;
+        held.take(own_w + 4 * v * apart, apart);
+        held.get(w);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          s[0] = fmaf(y[i], y[i], s[0]);
-          s[1] = fmaf(x[i], x[i], s[1]);
-          s[2] = fmaf(e[i] * w[i], x[i], s[2]);
+        for (int i = 0; i < 4; ++i) {
+          e[i] = mul2(e[i], w[i]);
+          sum[1] = fma2(x[i], x[i], sum[1]);
+          sum[2] = fma2(e[i], x[i], sum[2]);
+        }
+        keep[v] = 0xffu;
+        if (a.y) {
+          ey[v].get(y);
+          eg[v].get(g);
+          held.take(own_w + (4 * v + 2) * apart, apart);
+          held.get(w);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            sum[0] = fma2(y[i], y[i], sum[0]);
+            w[i] = mul2(w[i], y[i]);
+          }
+          if (a.drop.limit) {
+            keep[v] = kept8(a.drop, (uint64_t)(row * (a.C / 8) + c / 8), call, seed);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              w[i].x = keep[v] & 1u << 2 * i ? w[i].x * a.drop.scale : 0.f;
+              w[i].y = keep[v] & 2u << 2 * i ? w[i].y * a.drop.scale : 0.f;
+              g[i].x = keep[v] & 1u << 2 * i ? g[i].x : 0.f;
+              g[i].y = keep[v] & 2u << 2 * i ? g[i].y : 0.f;
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            sum[3] = fma2(w[i], g[i], sum[3]);
+            sum[4] = fma2(w[i], e[i], sum[4]);
+            sum[5] = fma2(w[i], x[i], sum[5]);
+          }
         }
       }
-      row_sums(s, red[0], a.W);
+      float s[6];
+#pragma unroll
+      for (int i = 0; i < 6; ++i) s[i] = sum[i].x + sum[i].y;
+      six_sums(s, red[odd], a.W);
+      odd ^= 1;
       // a row that is not there is zeros and adds nothing, also where eps is 0
       const float r = !a.w_post ? 1.f : live ? rsqrtf(fmaf(s[0], a.inv_C, a.eps)) : 0.f;
       const float q = live && a.w_next ? rsqrtf(fmaf(s[1], a.inv_C, a.eps)) : 0.f;
-      const float mean = s[2] * a.inv_C * q;  // of e x' q
-      float f[V][8], s2[1] = {0.f};
+      const float mean = s[2] * a.inv_C * q;                                        // of e x' q
+      // of f y r, f = post_weight gate u: G is linear in what is known by now
+      const float mean2 = a.w_post ? fmaf(q, fmaf(-q * mean, s[5], s[4]), s[3]) * a.inv_C * r : 0.f;
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        const int c = 8 * (lane + v * 32 * a.W);
-        const bool on = live && c < a.C;
-        float x[8], e[8], w[8], g[8];
+        const int c = c0 + v * apart_c;
+        const bool here = live && c < a.C;
+        float2 x[4], e[4], g[4], w[4];
         ex[v].get(x);
         en[v].get(e);
         eg[v].get(g);
-        weights(a.w_next, c, on, w);
+        Eight<float> held;
+        held.take(own_w + 4 * v * apart, apart);
+        held.get(w);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          x[i] *= q;
-          dw[v][i] = fmaf(e[i], x[i], dw[v][i]);
-          g[i] = fmaf(q, fmaf(x[i], -mean, e[i] * w[i]), g[i]);
+        for (int i = 0; i < 4; ++i) {
+          x[i] = mul2(x[i], both(q));
+          dw[v][i] = fma2(e[i], x[i], dw[v][i]);
+          g[i] = fma2(both(q), fma2(x[i], both(-mean), mul2(e[i], w[i])), g[i]);
+          e[i] = mul2(g[i], both(a.alpha));
         }
         Eight<X> out;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) e[i] = a.alpha * g[i];
         out.set(e);
-        if (on) out.store(static_cast<X*>(a.dx) + b * a.dx_sb + t * a.dx_st + c);
+        if (here) out.store(ox.p + v * apart_c, a.wide);
         if (a.y) {
-          if (a.drop.limit) dropped(g, a.drop, (uint64_t)(row * (a.C / 8) + c / 8), call, seed);
-          float y[8];
-          ey[v].get(y);
-          weights(a.w_post, c, on, w);
-          weights(gate, c, on, e);
+          if (a.drop.limit)
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            h[v][i] = fmaf(g[i], y[i] * r, h[v][i]);
-            f[v][i] = g[i] * w[i] * e[i];
-            s2[0] = fmaf(f[v][i], y[i], s2[0]);
+            for (int i = 0; i < 4; ++i) {
+              g[i].x = keep[v] & 1u << 2 * i ? g[i].x * a.drop.scale : 0.f;
+              g[i].y = keep[v] & 2u << 2 * i ? g[i].y * a.drop.scale : 0.f;
+            }
+          ey[v].get(x);
+          held.take(own_w + (4 * v + 2) * apart, apart);
+          held.get(w);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            x[i] = mul2(x[i], both(r));
+            h[v][i] = fma2(g[i], x[i], h[v][i]);
+            g[i] = mul2(both(r), fma2(x[i], both(-mean2), mul2(g[i], w[i])));
           }
+          Eight<Y> back;
+          back.set(g);
+          if (here) back.store(oy.p + v * apart_c, a.wide);
         }
       }
-      if (a.y) {
-        if (a.w_post) row_sums(s2, red[1], a.W);
-        const float mean2 = a.w_post ? s2[0] * a.inv_C * r : 0.f;
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-          const int c = 8 * (lane + v * 32 * a.W);
-          float y[8];
-          ey[v].get(y);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) f[v][i] = r * fmaf(y[i] * r, -mean2, f[v][i]);
-          Eight<Y> out;
-          out.set(f[v]);
-          if (live && c < a.C) out.store(static_cast<Y*>(a.dy) + b * a.dy_sb + t * a.dy_st + c);
-        }
-      }
-      if (!a.y || !a.w_post) __syncthreads();  // `red` is free again
+      const int n = wraps(&t);
+      ox.on(n), oy.on(n);
     }
+    copies_wait<0>();
     // the block's rows, in order
     if (per > 1) {
       __syncthreads();
       if (mine > 0)
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-          const int c = 8 * (lane + v * 32 * a.W);
+          const int c = c0 + v * apart_c;
           if (c < a.C)
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              fold[((mine - 1) * 2) * a.C + c + i] = h[v][i];
-              fold[((mine - 1) * 2 + 1) * a.C + c + i] = dw[v][i];
+            for (int i = 0; i < 4; ++i) {
+              *reinterpret_cast<float2*>(fold + ((mine - 1) * 2) * a.C + c + 2 * i) = h[v][i];
+              *reinterpret_cast<float2*>(fold + ((mine - 1) * 2 + 1) * a.C + c + 2 * i) = dw[v][i];
             }
         }
       __syncthreads();
@@ -348,19 +540,19 @@ __global__ void __launch_bounds__(512) residual_bwd_kernel(const NormArgs a) {
     if (mine == 0)
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        const int c = 8 * (lane + v * 32 * a.W);
+        const int c = c0 + v * apart_c;
         if (c >= a.C) continue;
         for (int k = 0; k < per - 1; ++k)
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            h[v][i] += fold[(k * 2) * a.C + c + i];
-            dw[v][i] += fold[(k * 2 + 1) * a.C + c + i];
+          for (int i = 0; i < 4; ++i) {
+            h[v][i] = add2(h[v][i], *reinterpret_cast<const float2*>(fold + (k * 2) * a.C + c + 2 * i));
+            dw[v][i] = add2(dw[v][i], *reinterpret_cast<const float2*>(fold + (k * 2 + 1) * a.C + c + 2 * i));
           }
         Eight<float> e;
         e.set(h[v]);
-        e.store(a.part_h + unit * a.C + c);
+        e.store(a.part_h + unit * a.C + c, false);
         e.set(dw[v]);
-        e.store(a.part_n + unit * a.C + c);
+        e.store(a.part_n + unit * a.C + c, false);
       }
     if (per > 1) __syncthreads();
   }
@@ -374,107 +566,166 @@ struct SumArgs {
 };
 
 // Columns of the partial sums: 32 lanes of columns by 32 slices of units, the slices
-// then added in order. blockIdx.y 0: dw_next; 1: dw_post and a shared gate's gradient.
+// then added in order. blockIdx.y 0: dw_next; 1: dw_post and a shared gate's gradient;
+// 2 ..: the gradients of gates that each batch row has for itself.
 __global__ void __launch_bounds__(1024) residual_sums_kernel(const SumArgs a) {
-  const int lane = threadIdx.x % 32, c = blockIdx.x * 32 + lane, sl = threadIdx.x / 32;
-  if (blockIdx.y == 0 ? !a.dw_next : !a.dw_post && (!a.dgate || a.row_gate)) return;
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // for the walk's end
+  const int lane = threadIdx.x % 32, c = blockIdx.x * 32 + lane, sl = threadIdx.x / 32, y = blockIdx.y;
+  if (y == 0 ? !a.dw_next : y == 1 ? !a.dw_post && (!a.dgate || a.row_gate) : !a.dgate) return;
   __shared__ float red[32][33];
-  const float* p = (blockIdx.y ? a.part_h : a.part_n) + c;
-  const bool scaled = blockIdx.y && a.row_gate;
+  const float* const p = (y ? a.part_h : a.part_n) + c;
+  const bool scaled = y == 1 && a.row_gate;
+  const int64_t first = y > 1 ? (int64_t)(y - 2) * a.chunks : 0, last = y > 1 ? first + a.chunks : a.units;
   float s = 0.f;
   if (c < a.C) {
-#pragma unroll 4
-    for (int64_t k = sl; k < a.units; k += 32)
+#pragma unroll 8
+    for (int64_t k = first + sl; k < last; k += 32)
       s += scaled ? a.gate[k / a.chunks * a.C + c] * p[k * a.C] : p[k * a.C];
   }
   red[sl][lane] = s;
   __syncthreads();
   if (sl || c >= a.C) return;
   for (int k = 1; k < 32; ++k) s += red[k][lane];
-  if (blockIdx.y == 0) {
+  if (y == 0) {
     a.dw_next[c] = s;
-    return;
+  } else if (y > 1) {
+    a.dgate[(int64_t)(y - 2) * a.C + c] = a.w_post ? a.w_post[c] * s : s;
+  } else {
+    if (a.dw_post) a.dw_post[c] = scaled || !a.gate ? s : a.gate[c] * s;
+    if (a.dgate && !a.row_gate) a.dgate[c] = a.w_post ? a.w_post[c] * s : s;
   }
-  if (a.dw_post) a.dw_post[c] = scaled || !a.gate ? s : a.gate[c] * s;
-  if (a.dgate && !a.row_gate) a.dgate[c] = a.w_post ? a.w_post[c] * s : s;
 }
 
-// The gradients of gates that each batch row has for itself.
+// The gradients of gates of more batch rows than there are blocks, whose sums are whole.
 __global__ void __launch_bounds__(256) residual_gates_kernel(const SumArgs a, int64_t n) {
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (i >= n) return;
-  const int64_t b = i / a.C;
-  const int c = (int)(i - b * a.C);
-  float s = 0.f;
-  for (int k = 0; k < a.chunks; ++k) s += a.part_h[(b * a.chunks + k) * a.C + c];
-  a.dgate[i] = a.w_post ? a.w_post[c] * s : s;
+  if (i < n) a.dgate[i] = a.w_post ? a.w_post[i % a.C] * a.part_h[i] : a.part_h[i];
 }
 
 constexpr int kMaxC = 8192;
-constexpr int kBwdBlocks = 152 * 4;
+constexpr int kSms = 152;
+constexpr int kMostBlocks = 3 * kSms;  // of the backward's walk
 
-// Threads of a row, rows of a block.
+// Vectors of eight elements a thread, warps a row, threads a block.
 struct Shape {
   int V, W, threads;
 };
-Shape shape_of(int64_t C) {
-  const int64_t vecs = C / 8;
-  Shape s;
-  s.V = vecs > 512 ? 2 : 1;
-  const int64_t lanes = (vecs + s.V - 1) / s.V;
-  s.W = 1;
-  while (s.W * 32 < lanes) s.W *= 2;
-  s.threads = s.W < 8 ? 256 : s.W * 32;
+Shape shape_with(int C, int V, int threads) {
+  Shape s{V, 1, threads};
+  while (s.W * 32 * V * 8 < C) s.W *= 2;
+  if (s.W * 32 > threads) s.threads = s.W * 32;
   return s;
 }
+// Forward: four vectors a thread and small blocks, so that much is on its way with little
+// to wait for: 8 x 4096 rows of 2048 in us, by vectors a thread, blocks of 64 / 256
+// threads: 202 / 202 (1), 147 / 157 (2), 143 / 171 (4), 146 / 144 (8). Few rows are
+// spread over more threads instead.
+Shape fwd_shape(int C, int64_t rows) {
+  if (C <= 256 || (rows < 8 * kSms && C <= 4096)) return shape_with(C, 1, 64);
+  return shape_with(C, C <= 512 ? 2 : 4, 64);
+}
+// Backward: two vectors a thread where 128 threads hold a row of them: 8 x 4096 rows of
+// 2048 in us, by vectors a thread and blocks an SM: 311 (1, two), 291 (2, two), 265 (2,
+// three; registers held to 168), 569 (2, four; they spill), 439 (4, one).
+Shape bwd_shape(int C) { return shape_with(C, C <= 256 ? 1 : C <= 2048 ? 2 : 4, 128); }
 
 struct Units {
   int64_t groups, span;
   int chunks;
 };
-Units units_of(int64_t B, int64_t T, bool row_gate) {
+Units units_of(int64_t B, int64_t T, bool row_gate, int blocks) {
   Units u;
   u.groups = row_gate ? B : 1;
   u.span = row_gate ? T : B * T;
-  int64_t n = kBwdBlocks / u.groups;
+  int64_t n = blocks / u.groups;
   n = n < 1 ? 1 : n;
   u.chunks = (int)(n < u.span ? n : u.span);
   return u;
 }
 
-template <typename X, typename Y>
-cudaError_t launch_fwd(NormArgs a, cudaStream_t s) {
-  const Shape h = shape_of(a.C);
-  a.W = h.W;
-  const int64_t per = h.threads / 32 / h.W, blocks = (a.rows + per - 1) / per;
-  if (h.V == 1) residual_fwd_kernel<X, Y, 1><<<(unsigned)blocks, h.threads, 0, s>>>(a);
-  else residual_fwd_kernel<X, Y, 2><<<(unsigned)blocks, h.threads, 0, s>>>(a);
-  return cudaGetLastError();
+// The backward's copies run three rows ahead or one, or not at all, as shared memory
+// holds them; and how many blocks an SM then holds.
+struct Ring {
+  int ahead, per_sm;
+  size_t bytes;
+};
+Ring ring_of(const Shape& h, int pieces) {
+  const size_t row = (size_t)h.V * pieces * h.threads * 16, held = (size_t)h.V * 4 * h.threads * 16;
+  const size_t sm = (size_t)226 << 10, third = (size_t)74 << 10;
+  Ring r;
+  r.ahead = 4 * row + held <= third ? 3 : 2 * row + held <= sm ? 1 : 0;
+  r.bytes = (r.ahead + 1) * row + held;
+  const int fit = (int)(sm / (r.bytes + 1024)), regs = h.V < 4 ? 3 : h.threads <= 128 ? 2 : 1;
+  r.per_sm = fit < 1 ? 1 : fit < regs ? fit : regs;
+  return r;
+}
+int pieces_of(scan_dtype stream_dt, scan_dtype dt) {
+  return 2 * (stream_dt == SCAN_BF16 ? 1 : 2) + 2 * (dt == SCAN_BF16 ? 1 : 2);
 }
 
 template <typename X, typename Y>
-cudaError_t launch_bwd(NormArgs a, SumArgs m, cudaStream_t s) {
-  const Shape h = shape_of(a.C);
+cudaError_t launch_fwd(NormArgs a, cudaStream_t s) {
+  const Shape h = fwd_shape(a.C, a.rows);
   a.W = h.W;
-  const int per = h.threads / 32 / h.W;
-  const size_t smem = (size_t)(per - 1) * 2 * a.C * 4;
-  const int64_t units = a.groups * a.chunks, blocks = units < kBwdBlocks ? units : kBwdBlocks;
-  if (h.V == 1) residual_bwd_kernel<X, Y, 1><<<(unsigned)blocks, h.threads, smem, s>>>(a);
-  else residual_bwd_kernel<X, Y, 2><<<(unsigned)blocks, h.threads, smem, s>>>(a);
-  cudaError_t e = cudaGetLastError();
+  const int64_t per = h.threads / 32 / h.W, blocks = (a.rows + per - 1) / per;
+  if (h.V == 1) residual_fwd_kernel<X, Y, 1><<<(unsigned)blocks, h.threads, 0, s>>>(a);
+  else if (h.V == 2) residual_fwd_kernel<X, Y, 2><<<(unsigned)blocks, h.threads, 0, s>>>(a);
+  else residual_fwd_kernel<X, Y, 4><<<(unsigned)blocks, h.threads, 0, s>>>(a);
+  return cudaGetLastError();
+}
+
+template <typename X, typename Y, int V, int AHEAD>
+cudaError_t launch_walk(const NormArgs& a, const Shape& h, const Ring& r, cudaStream_t s) {
+  const size_t fold = (size_t)(h.threads / 32 / h.W - 1) * 2 * a.C * 4, smem = r.bytes > fold ? r.bytes : fold;
+  const cudaError_t e =
+      cudaFuncSetAttribute(residual_bwd_kernel<X, Y, V, AHEAD>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  if (m.dw_next || m.dw_post || (m.dgate && !m.row_gate))
-    residual_sums_kernel<<<dim3((a.C + 31) / 32, 2), 1024, 0, s>>>(m);
-  if (m.dgate && m.row_gate) {
-    const int64_t n = a.B * a.C;
-    residual_gates_kernel<<<(unsigned)((n + 255) / 256), 256, 0, s>>>(m, n);
+  const int64_t units = a.groups * a.chunks, blocks = units < r.per_sm * kSms ? units : r.per_sm * kSms;
+  residual_bwd_kernel<X, Y, V, AHEAD><<<(unsigned)blocks, h.threads, smem, s>>>(a);
+  return cudaGetLastError();
+}
+template <typename X, typename Y, int V>
+cudaError_t launch_walk(const NormArgs& a, const Shape& h, const Ring& r, cudaStream_t s) {
+  if (r.ahead == 3) return launch_walk<X, Y, V, 3>(a, h, r, s);
+  if (r.ahead == 1) return launch_walk<X, Y, V, 1>(a, h, r, s);
+  return launch_walk<X, Y, V, 0>(a, h, r, s);
+}
+
+template <typename X, typename Y>
+cudaError_t launch_bwd(NormArgs a, SumArgs m, const Shape& h, const Ring& r, cudaStream_t s) {
+  a.W = h.W;
+  cudaError_t e = h.V == 1   ? launch_walk<X, Y, 1>(a, h, r, s)
+                  : h.V == 2 ? launch_walk<X, Y, 2>(a, h, r, s)
+                             : launch_walk<X, Y, 4>(a, h, r, s);
+  if (e != cudaSuccess) return e;
+  const bool gates = m.dgate && m.row_gate, single = gates && m.chunks == 1;
+  if (m.dw_next || m.dw_post || (m.dgate && !single)) {
+    // launched while the walk runs, whose end it waits for itself
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((a.C + 31) / 32, gates && !single ? (unsigned)(2 + a.B) : 2u);
+    cfg.blockDim = dim3(1024);
+    cfg.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, residual_sums_kernel, m);
+    if (e != cudaSuccess) return e;
   }
+  if (single) residual_gates_kernel<<<(unsigned)((a.B * a.C + 255) / 256), 256, 0, s>>>(m, a.B * a.C);
   return cudaGetLastError();
 }
 
 bool rows_aligned(const scan_view4* v, const NormArgs& a, scan_dtype dt) {
   const int64_t n = dt == SCAN_BF16 ? 8 : 4;  // an axis of one element has no stride of its own
   return (uintptr_t)v->ptr % 16 == 0 && (a.B == 1 || v->stride_b % n == 0) && (a.T == 1 || v->stride_t % n == 0);
+}
+
+// fp32 rows on 32 bytes (bf16 ones take 16-byte pieces anyway).
+bool rows_wide(const scan_view4* v, const NormArgs& a, scan_dtype dt) {
+  return !v || !v->ptr || dt == SCAN_BF16 ||
+         ((uintptr_t)v->ptr % 32 == 0 && (a.B == 1 || v->stride_b % 8 == 0) && (a.T == 1 || v->stride_t % 8 == 0));
 }
 
 bool given(const scan_view4* v) { return v && v->ptr; }
@@ -518,7 +769,7 @@ size_t residual_norm_workspace_bytes(int64_t B, int64_t T, int64_t C, int32_t ro
   if (B < 0 || T < 0 || C < 1 || C % 8 || C > kMaxC) return 0;
   if (B == 0 || T == 0) return 16;
   if ((double)B * (double)T > 2147483647.) return 0;
-  const Units u = units_of(B, T, row_gate != 0);
+  const Units u = units_of(B, T, row_gate != 0, kMostBlocks);
   return (size_t)(u.groups * u.chunks) * 2 * (size_t)C * 4;
 }
 
@@ -537,6 +788,8 @@ scan_status residual_norm_fwd(const scan_view4* x, const scan_view4* y, const fl
   if (!rows_aligned(x, a, stream_dt) || (y && (!rows_aligned(y, a, dt) || !rows_aligned(x_out, a, stream_dt))) ||
       (next_weight && !rows_aligned(n, a, dt)))
     return SCAN_ERR_ALIGNMENT;
+  a.wide = rows_wide(x, a, stream_dt) && rows_wide(y, a, dt) && (!y || rows_wide(x_out, a, stream_dt)) &&
+           (!next_weight || rows_wide(n, a, dt));
   a.x = x->ptr, a.x_sb = x->stride_b, a.x_st = x->stride_t;
   if (y) {
     a.y = y->ptr, a.y_sb = y->stride_b, a.y_st = y->stride_t;
@@ -580,6 +833,8 @@ scan_status residual_norm_bwd(const scan_view4* x_out, const scan_view4* y, cons
   if (!workspace || (uintptr_t)workspace % 16 ||
       workspace_bytes < residual_norm_workspace_bytes(B, T, C, a.row_gate))
     return SCAN_ERR_WORKSPACE;
+  a.wide = rows_wide(dx, a, stream_dt) && rows_wide(dx_out, a, stream_dt) && rows_wide(y, a, dt) &&
+           (!y || rows_wide(dy, a, dt)) && (!next_weight || (rows_wide(x_out, a, stream_dt) && rows_wide(dn, a, dt)));
   if (next_weight) {
     a.x = x_out->ptr, a.x_sb = x_out->stride_b, a.x_st = x_out->stride_t;
     a.dn = dn->ptr, a.n_sb = dn->stride_b, a.n_st = dn->stride_t;
@@ -590,7 +845,9 @@ scan_status residual_norm_bwd(const scan_view4* x_out, const scan_view4* y, cons
     a.y = y->ptr, a.y_sb = y->stride_b, a.y_st = y->stride_t;
     a.dy = dy->ptr, a.dy_sb = dy->stride_b, a.dy_st = dy->stride_t;
   }
-  const Units u = units_of(B, T, a.row_gate);
+  const Shape h = bwd_shape(a.C);
+  const Ring r = ring_of(h, pieces_of(stream_dt, dt));
+  const Units u = units_of(B, T, a.row_gate, r.per_sm * kSms);
   a.groups = u.groups;
   a.span = u.span;
   a.chunks = u.chunks;
@@ -598,9 +855,9 @@ scan_status residual_norm_bwd(const scan_view4* x_out, const scan_view4* y, cons
   a.part_n = a.part_h + u.groups * u.chunks * C;
   const SumArgs m{a.part_h, a.part_n, post_weight, gate, dpost_weight, dgate, dnext_weight, u.groups * u.chunks,
                   a.C, u.chunks, a.row_gate};
-  const cudaError_t e = stream_dt == SCAN_BF16 ? launch_bwd<__nv_bfloat16, __nv_bfloat16>(a, m, stream)
-                        : dt == SCAN_BF16      ? launch_bwd<float, __nv_bfloat16>(a, m, stream)
-                                               : launch_bwd<float, float>(a, m, stream);
+  const cudaError_t e = stream_dt == SCAN_BF16 ? launch_bwd<__nv_bfloat16, __nv_bfloat16>(a, m, h, r, stream)
+                        : dt == SCAN_BF16      ? launch_bwd<float, __nv_bfloat16>(a, m, h, r, stream)
+                                               : launch_bwd<float, float>(a, m, h, r, stream);
   return e == cudaSuccess ? SCAN_OK : SCAN_ERR_CUDA;
 }
 
