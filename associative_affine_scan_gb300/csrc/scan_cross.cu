@@ -10,172 +10,282 @@
 // sequence of no keys gives o = 0, lse = -inf and zero gradients.
 //
 // The kernels here serve fp32 operands and operands that tensor copies cannot
-// address: tiles of 64 by 64 in shared memory, four by four products a thread in fp32
-// multiply-adds. An operand that is summed over its columns lies transposed, so that
-// both factors are read 16 bytes at a time: three shared-memory cycles a warp for 16
-// multiply-adds a thread.
+// address. Products are of fp32 accuracy on the tensor cores: each factor is the sum of
+// two tf32 numbers, hi of its upper 11 bits and lo of what is left, and a b = hi hi + hi lo
+// + lo hi (what is left out is 2^-22 of a b, as the rounding of lo is), summed in fp32.
+// Three m16n8k8 products are 169 multiply-adds a cycle and SM, where fp32 arithmetic
+// has 128 and reads more of its factors from shared memory. A warp has 16 rows; tiles lie
+// in shared memory row by row, with a pitch that puts the elements of a fragment into
+// different banks both as rows (q k) and as columns (p v): the summed index of the
+// second product runs over the keys in the order in which the first one's results lie
+// with the threads.
 #include "scan_cross.h"
 #include "scan_cross_tc.h"
 
 namespace scan {
 namespace {
 
-constexpr int kTile = 64;
-constexpr int kPitch = kTile + 4;
-constexpr int kThreads = 256;
+constexpr int kWarps = 4;
+constexpr int kThreads = 32 * kWarps;
+constexpr int kOwn = 16 * kWarps;  // rows that a block owns
+constexpr int kOther = 32;         // rows of the other sequence that it takes at a time
+
+template <int DP>
+constexpr int kPitch = DP + 4;
 
 template <typename T>
 __device__ __forceinline__ View<T> vw(const scan_view4& v) {
   return View<T>{static_cast<T*>(v.ptr), v.stride_b, v.stride_t, v.stride_h};
 }
 
-// Rows [t0, t0 + 64) of one head as fp32, zeros from row `end` and column D on:
-// transposed (d, row), or as they lie (row, d).
-template <typename T, int DP>
-__device__ __forceinline__ void load_t(float* dst, const View<const T>& v, int64_t b, int64_t t0, int64_t end, int64_t h,
-                                       int D) {
-  const int r = threadIdx.x % kTile;
-  const bool on = t0 + r < end;
-  const T* const p = v.row(b, on ? t0 + r : t0, h);
-#pragma unroll 8
-  for (int c = threadIdx.x / kTile; c < DP; c += kThreads / kTile)
-    dst[c * kPitch + r] = on && c < D ? to_f32(p[c]) : 0.f;
-}
-template <typename T, int DP>
-__device__ __forceinline__ void load_r(float* dst, const View<const T>& v, int64_t b, int64_t t0, int64_t end, int64_t h,
-                                       int D) {
-#pragma unroll 8
-  for (int i = threadIdx.x; i < kTile * DP; i += kThreads) {
-    const int r = i / DP, c = i % DP;
-    dst[i] = t0 + r < end && c < D ? to_f32(v.row(b, t0 + r, h)[c]) : 0.f;
-  }
-}
-
-__device__ __forceinline__ float4 ld4(const float* p) { return *reinterpret_cast<const float4*>(p); }
-
-// acc[i][j] += sum over d of a[d][4 ty + i] b[d][4 tx + j].
-template <int DP>
-__device__ __forceinline__ void product_tt(float (&acc)[4][4], const float* a, const float* b, int ty, int tx) {
-#pragma unroll 8
-  for (int d = 0; d < DP; ++d) {
-    const float4 x = ld4(a + d * kPitch + 4 * ty), y = ld4(b + d * kPitch + 4 * tx);
-    const float u[4] = {x.x, x.y, x.z, x.w}, v[4] = {y.x, y.y, y.z, y.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(u[i], v[j], acc[i][j]);
-  }
-}
-// acc[i][h][j] += sum over k of p[k][4 ty + i] m[k][64 h + 4 tx + j], 64 rows k.
-template <int DP>
-__device__ __forceinline__ void product_pm(float (&acc)[4][DP / 64][4], const float* p, const float* m, int ty, int tx) {
-#pragma unroll 4
-  for (int k = 0; k < kTile; ++k) {
-    const float4 x = ld4(p + k * kPitch + 4 * ty);
-    const float u[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-    for (int h = 0; h < DP / 64; ++h) {
-      const float4 y = ld4(m + k * DP + 64 * h + 4 * tx);
-      const float v[4] = {y.x, y.y, y.z, y.w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][h][j] = fmaf(u[i], v[j], acc[i][h][j]);
+// Rows [t0, t0 + ROWS) of one head as fp32, zeros from row `end` and column D on. fp32
+// rows come by asynchronous copies, of 16 bytes where they lie on 16 bytes.
+template <typename T, int DP, int ROWS>
+__device__ __forceinline__ void load_rows(float* dst, const View<const T>& v, int64_t b, int64_t t0, int64_t end,
+                                          int64_t h, int D, bool on16) {
+  if constexpr (sizeof(T) == 4) {
+    const int step = on16 ? 4 : 1, per = DP / step;
+    for (int i = threadIdx.x; i < ROWS * per; i += kThreads) {
+      const int r = i / per, c = i % per * step;
+      const bool on = t0 + r < end && c < D;
+      const T* const p = v.row(b, on ? t0 + r : 0, h) + (on ? c : 0);
+      const uint32_t to = (uint32_t)__cvta_generic_to_shared(dst + r * kPitch<DP> + c);
+      if (!on) {  // (nothing is read: the operand may be empty)
+        if (step == 4) *reinterpret_cast<float4*>(dst + r * kPitch<DP> + c) = make_float4(0.f, 0.f, 0.f, 0.f);
+        else dst[r * kPitch<DP> + c] = 0.f;
+      } else if (step == 4) {
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(p) : "memory");
+      } else {
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to), "l"(p) : "memory");
+      }
+    }
+  } else {
+    for (int i = threadIdx.x; i < ROWS * DP; i += kThreads) {
+      const int r = i / DP, c = i % DP;
+      dst[r * kPitch<DP> + c] = t0 + r < end && c < D ? to_f32(v.row(b, t0 + r, h)[c]) : 0.f;
     }
   }
 }
-// A thread's 4 x 4 of a tile, transposed into shared memory.
-__device__ __forceinline__ void store_t(float* dst, const float (&s)[4][4], int ty, int tx) {
-#pragma unroll
-  for (int j = 0; j < 4; ++j)
-    *reinterpret_cast<float4*>(dst + (4 * tx + j) * kPitch + 4 * ty) = make_float4(s[0][j], s[1][j], s[2][j], s[3][j]);
+__device__ __forceinline__ void loads_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void loads_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
-template <typename T, int DP>
-__device__ __forceinline__ void write_rows(const View<T>& out, const float (&acc)[4][DP / 64][4], int64_t b, int64_t t0,
-                                           int64_t end, int64_t h, int D, const float (&f)[4], int ty, int tx) {
+bool rows_on_16(const scan_view4& v, int64_t B, int64_t T, int64_t H) {
+  return (uintptr_t)v.ptr % 16 == 0 && (B <= 1 || v.stride_b % 4 == 0) && (T <= 1 || v.stride_t % 4 == 0) &&
+         (H <= 1 || v.stride_h % 4 == 0);
+}
+
+// x = hi + lo, hi rounded to the 11 bits of a tf32 number (the products ignore what lo has
+// beyond its own).
+__device__ __forceinline__ void split(float x, uint32_t* hi, uint32_t* lo) {
+  *hi = (__float_as_uint(x) + 0x1000u) & 0xffffe000u;
+  *lo = __float_as_uint(x - __uint_as_float(*hi));
+}
+__device__ __forceinline__ void mma1688(float (&c)[4], const uint32_t (&a)[4], const uint32_t (&b)[2]) {
+  asm("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
+}
+// A thread of a warp has rows g and g + 8 and columns 2 c, 2 c + 1 of each 16 x 8 result.
+struct Lane {
+  int g, c;
+  __device__ Lane() : g(threadIdx.x % 32 / 4), c(threadIdx.x % 4) {}
+};
+
+// The products add to their sums by cutting off, not by rounding, which a long sum would
+// show (7.6e-6 of an output over 1031 keys). So sums run over one tile only, the small
+// terms by themselves, and are added to the others by rounding additions.
+
+// acc[j] += rows of `a` (16, from the warp's first) times rows 8 j .. of `b`, over D columns.
+template <int DP>
+__device__ __forceinline__ void rows_by_rows(float (&acc)[kOther / 8][4], const float* a, const float* b, int D) {
+  constexpr int N = kOther / 8;
+  const Lane w;
+  float small[N][4] = {};
+#pragma unroll 2
+  for (int k = 0; k < D; k += 8) {
+    uint32_t hi[4], lo[4], bh[N][2], bl[N][2];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int64_t t = t0 + 4 * ty + i;
-    if (t >= end) continue;
-    T* const row = out.row(b, t, h);
+    for (int i = 0; i < 4; ++i) split(a[(w.g + 8 * (i & 1)) * kPitch<DP> + k + w.c + 4 * (i >> 1)], &hi[i], &lo[i]);
 #pragma unroll
-    for (int x = 0; x < DP / 64; ++x)
+    for (int j = 0; j < N; ++j)
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        if (64 * x + 4 * tx + j < D) row[64 * x + 4 * tx + j] = from_f32<T>(acc[i][x][j] * f[i]);
+      for (int i = 0; i < 2; ++i) split(b[(8 * j + w.g) * kPitch<DP> + k + w.c + 4 * i], &bh[j][i], &bl[j][i]);
+#pragma unroll
+    for (int j = 0; j < N; ++j) mma1688(small[j], lo, bh[j]);
+#pragma unroll
+    for (int j = 0; j < N; ++j) mma1688(acc[j], hi, bh[j]);
+#pragma unroll
+    for (int j = 0; j < N; ++j) mma1688(small[j], hi, bl[j]);
+  }
+#pragma unroll
+  for (int j = 0; j < N; ++j)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) acc[j][i] += small[j][i];
+}
+// acc[i] += p times columns 8 i .. of `b`, over its rows; p as rows_by_rows left it.
+template <int DP>
+__device__ __forceinline__ void weights_by_columns(float (&acc)[DP / 8][4], const float (&p)[kOther / 8][4], const float* b,
+                                                   int D) {
+  constexpr int N = kOther / 8;
+  const Lane w;
+  uint32_t hi[N][4], lo[N][4];
+#pragma unroll
+  for (int j = 0; j < N; ++j) {
+    split(p[j][0], &hi[j][0], &lo[j][0]);
+    split(p[j][2], &hi[j][1], &lo[j][1]);
+    split(p[j][1], &hi[j][2], &lo[j][2]);
+    split(p[j][3], &hi[j][3], &lo[j][3]);
+  }
+#pragma unroll
+  for (int i0 = 0; i0 < DP / 8; i0 += 4) {  // 32 columns at a time
+    if (8 * i0 >= D) break;
+    float sum[4][4] = {}, small[4][4] = {};
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      const float* const at = b + (8 * j + 2 * w.c) * kPitch<DP> + 8 * i0 + w.g;
+      uint32_t bh[4][2], bl[4][2];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int y = 0; y < 2; ++y) split(at[8 * i + y * kPitch<DP>], &bh[i][y], &bl[i][y]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) mma1688(small[i], lo[j], bh[i]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) mma1688(sum[i], hi[j], bh[i]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) mma1688(small[i], hi[j], bl[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int y = 0; y < 4; ++y) acc[i0 + i][y] += sum[i][y] + small[i][y];
   }
 }
-// The 16 threads of a row are half a warp.
-__device__ __forceinline__ float row_max(float v) {
+// The warp's 16 rows from row t0 on, rows g times f[0] and g + 8 times f[1].
+template <typename T, int DP>
+__device__ __forceinline__ void write_rows(const View<T>& out, const float (&acc)[DP / 8][4], int64_t b, int64_t t0,
+                                           int64_t end, int64_t h, int D, const float (&f)[2]) {
+  const Lane w;
 #pragma unroll
-  for (int d = 8; d; d >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, d));
-  return v;
+  for (int y = 0; y < 2; ++y) {
+    const int64_t t = t0 + w.g + 8 * y;
+    if (t >= end) continue;
+    T* const row = out.row(b, t, h) + 2 * w.c;
+#pragma unroll
+    for (int i = 0; i < DP / 8; ++i)
+      if (8 * i < D) {
+        row[8 * i] = from_f32<T>(acc[i][2 * y] * f[y]);
+        row[8 * i + 1] = from_f32<T>(acc[i][2 * y + 1] * f[y]);
+      }
+  }
+}
+// Over the four threads of a row.
+__device__ __forceinline__ float row_max(float v) {
+  v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 1));
+  return fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
 }
 __device__ __forceinline__ float row_sum(float v) {
-#pragma unroll
-  for (int d = 8; d; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
-  return v;
+  v += __shfl_xor_sync(0xffffffffu, v, 1);
+  return v + __shfl_xor_sync(0xffffffffu, v, 2);
+}
+
+// Pairs of tiles (of two operands) that a walk holds at a time: the next one is on its way
+// while this one is used, where shared memory has room for both and two blocks an SM.
+template <int DP, int OWN>
+constexpr int kStages = (OWN * kOwn + 4 * kOther) * kPitch<DP> * 4 <= (112 << 10) ? 2 : 1;
+template <int DP, int OWN>
+constexpr int kSmem = (OWN * kOwn + 2 * kStages<DP, OWN> * kOther) * kPitch<DP> * 4;
+
+// Brings pair after pair of tiles to shared memory: use(x, y, n) with tile n of both.
+template <int DP, int OWN, typename L, typename U>
+__device__ __forceinline__ void walk(float* tiles, int64_t n, const L& load, const U& use) {
+  constexpr int NS = kStages<DP, OWN>, size = kOther * kPitch<DP>;
+  if (NS == 2 && n > 0) load(tiles, tiles + size, 0);
+  loads_commit();
+  for (int64_t i = 0; i < n; ++i) {
+    float* const x = tiles + (NS == 2 ? (i & 1) * 2 * size : 0);
+    if (NS == 1) {
+      __syncthreads();  // the last tiles have been used
+      load(x, x + size, i);
+      loads_commit();
+      loads_wait<0>();
+    } else {
+      float* const y = tiles + ((i + 1) & 1) * 2 * size;
+      if (i > 0) __syncthreads();
+      if (i + 1 < n) load(y, y + size, i + 1);
+      loads_commit();
+      loads_wait<1>();
+    }
+    __syncthreads();
+    use(x, x + size, i);
+  }
+  loads_wait<0>();
 }
 
 template <typename T, int DP>
-__global__ void __launch_bounds__(kThreads) cross_fwd_general(const CrossArgs a) {
+__global__ void __launch_bounds__(kThreads) cross_fwd_general(const CrossArgs a, int on16) {
   extern __shared__ float4 raw[];
-  float *const sq = reinterpret_cast<float*>(raw), *const sk = sq + DP * kPitch, *const sv = sk + DP * kPitch;
-  float* const sp = sk;  // the weights, once the scores are formed
+  float *const sq = reinterpret_cast<float*>(raw), *const tiles = sq + kOwn * kPitch<DP>;
   if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x < 32)
     check_cross(a.lens, a.cu_q, a.cu_k, a.n_seqs, a.B, a.Tq, a.Tk, a.hdr);
   CrossRows g;
   const int h = blockIdx.y % a.Hq, hk = h / (a.Hq / a.Hk);
   const int64_t b = blockIdx.y / a.Hq;
-  if (!cross_rows(a.lens, a.cu_q, a.cu_k, a.n_seqs, a.Tq, a.Tk, b, blockIdx.x, kTile, false, &g)) return;
-  const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
-  const View<const T> q = vw<const T>(a.q), k = vw<const T>(a.k), v = vw<const T>(a.v);
-  load_t<T, DP>(sq, q, b, g.qbeg + g.t0, g.qbeg + g.nq, h, a.D);
-  float m[4], l[4], o[4][DP / 64][4] = {};
+  if (!cross_rows(a.lens, a.cu_q, a.cu_k, a.n_seqs, a.Tq, a.Tk, b, blockIdx.x, kOwn, false, &g)) return;
+  const Lane w;
+  const int warp = threadIdx.x / 32;
+  const View<const T> k = vw<const T>(a.k), v = vw<const T>(a.v);
+  load_rows<T, DP, kOwn>(sq, vw<const T>(a.q), b, g.qbeg + g.t0, g.qbeg + g.nq, h, a.D, on16);
+  const float* const own = sq + 16 * warp * kPitch<DP>;
+  float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f}, o[DP / 8][4] = {};
+  walk<DP, 1>(
+      tiles, (g.nk + kOther - 1) / kOther,
+      [&](float* x, float* y, int64_t i) {
+        load_rows<T, DP, kOther>(x, k, b, g.kbeg + i * kOther, g.kbeg + g.nk, hk, a.D, on16);
+        load_rows<T, DP, kOther>(y, v, b, g.kbeg + i * kOther, g.kbeg + g.nk, hk, a.D, on16);
+      },
+      [&](const float* sk, const float* sv, int64_t i) {
+        float s[kOther / 8][4] = {};
+        rows_by_rows<DP>(s, own, sk, a.D);
+        const int64_t left = g.nk - i * kOther;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) m[i] = -INFINITY, l[i] = 0.f;
-  for (int64_t j0 = 0; j0 < g.nk; j0 += kTile) {
-    __syncthreads();
-    load_t<T, DP>(sk, k, b, g.kbeg + j0, g.kbeg + g.nk, hk, a.D);
-    load_r<T, DP>(sv, v, b, g.kbeg + j0, g.kbeg + g.nk, hk, a.D);
-    __syncthreads();
-    float s[4][4] = {};
-    product_tt<DP>(s, sq, sk, ty, tx);
-    __syncthreads();
-    float keep[4];
+        for (int y = 0; y < 2; ++y) {
+          float top = -INFINITY;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      float top = -INFINITY;
+          for (int j = 0; j < kOther / 8; ++j)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        s[i][j] = j0 + 4 * tx + j < g.nk ? s[i][j] * a.scale : -INFINITY;
-        top = fmaxf(top, s[i][j]);
-      }
-      const float mn = fmaxf(m[i], row_max(top)), base = mn == -INFINITY ? 0.f : mn;
-      keep[i] = expf(m[i] - base);
-      float sum = 0.f;
+            for (int z = 0; z < 2; ++z) {
+              float& e = s[j][2 * y + z];
+              e = 8 * j + 2 * w.c + z < left ? e * a.scale : -INFINITY;
+              top = fmaxf(top, e);
+            }
+          const float mn = fmaxf(m[y], row_max(top)), base = mn == -INFINITY ? 0.f : mn;
+          const float keep = expf(m[y] - base);
+          float sum = 0.f;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) sum += s[i][j] = expf(s[i][j] - base);
-      l[i] = l[i] * keep[i] + row_sum(sum);
-      m[i] = mn;
+          for (int j = 0; j < kOther / 8; ++j)
 #pragma unroll
-      for (int x = 0; x < DP / 64; ++x)
+            for (int z = 0; z < 2; ++z) sum += s[j][2 * y + z] = expf(s[j][2 * y + z] - base);
+          l[y] = l[y] * keep + sum;
+          m[y] = mn;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) o[i][x][j] *= keep[i];
-    }
-    store_t(sp, s, ty, tx);
-    __syncthreads();
-    product_pm<DP>(o, sp, sv, ty, tx);
+          for (int x = 0; x < DP / 8; ++x) o[x][2 * y] *= keep, o[x][2 * y + 1] *= keep;
+        }
+        weights_by_columns<DP>(o, s, sv, a.D);
+      });
+  float f[2];
+#pragma unroll
+  for (int y = 0; y < 2; ++y) {
+    l[y] = row_sum(l[y]);
+    f[y] = l[y] == 0.f ? 0.f : 1.f / l[y];  // l is 0 where there is no key; NaN stays
+    const int64_t t = g.t0 + 16 * warp + w.g + 8 * y;
+    if (w.c == 0 && t < g.nq)
+      a.lse[(b * a.Hq + h) * a.Tq + g.qbeg + t] = l[y] == 0.f ? -INFINITY : m[y] + logf(l[y]);
   }
-  float f[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    f[i] = l[i] == 0.f ? 0.f : 1.f / l[i];  // l is 0 where there is no key; NaN stays
-    const int64_t t = g.t0 + 4 * ty + i;
-    if (tx == 0 && t < g.nq)
-      a.lse[(b * a.Hq + h) * a.Tq + g.qbeg + t] = l[i] == 0.f ? -INFINITY : m[i] + logf(l[i]);
-  }
-  write_rows<T, DP>(vw<T>(a.o), o, b, g.qbeg + g.t0, g.qbeg + g.nq, h, a.D, f, ty, tx);
+  write_rows<T, DP>(vw<T>(a.o), o, b, g.qbeg + g.t0 + 16 * warp, g.qbeg + g.nq, h, a.D, f);
 }
 
 // delta_i = sum_d dout o of every query row: one warp a row.
@@ -196,107 +306,137 @@ __global__ void __launch_bounds__(256) cross_delta_general(const CrossArgs a, in
 
 // A tile of queries against every key.
 template <typename T, int DP>
-__global__ void __launch_bounds__(kThreads) cross_dq_general(const CrossArgs a) {
+__global__ void __launch_bounds__(kThreads) cross_dq_general(const CrossArgs a, int on16) {
   extern __shared__ float4 raw[];
-  float *const sq = reinterpret_cast<float*>(raw), *const sd = sq + DP * kPitch, *const sb = sd + DP * kPitch,
-                *const sp = sb + DP * kPitch;
+  float *const sq = reinterpret_cast<float*>(raw), *const sd = sq + kOwn * kPitch<DP>, *const tiles = sd + kOwn * kPitch<DP>;
   CrossRows g;
   const int h = blockIdx.y % a.Hq, hk = h / (a.Hq / a.Hk);
   const int64_t b = blockIdx.y / a.Hq;
-  if (!cross_rows(a.lens, a.cu_q, a.cu_k, a.n_seqs, a.Tq, a.Tk, b, blockIdx.x, kTile, false, &g)) return;
-  const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
+  if (!cross_rows(a.lens, a.cu_q, a.cu_k, a.n_seqs, a.Tq, a.Tk, b, blockIdx.x, kOwn, false, &g)) return;
+  const Lane w;
+  const int warp = threadIdx.x / 32;
   const View<const T> k = vw<const T>(a.k), v = vw<const T>(a.v);
-  load_t<T, DP>(sq, vw<const T>(a.q), b, g.qbeg + g.t0, g.qbeg + g.nq, h, a.D);
-  load_t<T, DP>(sd, vw<const T>(a.dout), b, g.qbeg + g.t0, g.qbeg + g.nq, h, a.D);
-  float lse[4], delta[4], dq[4][DP / 64][4] = {};
+  load_rows<T, DP, kOwn>(sq, vw<const T>(a.q), b, g.qbeg + g.t0, g.qbeg + g.nq, h, a.D, on16);
+  load_rows<T, DP, kOwn>(sd, vw<const T>(a.dout), b, g.qbeg + g.t0, g.qbeg + g.nq, h, a.D, on16);
+  float lse[2], delta[2], dq[DP / 8][4] = {};
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int64_t t = g.t0 + 4 * ty + i, at = (b * a.Hq + h) * a.Tq + g.qbeg + t;
-    lse[i] = t < g.nq ? a.lse[at] : INFINITY;
-    delta[i] = t < g.nq ? a.delta[at] : 0.f;
+  for (int y = 0; y < 2; ++y) {
+    const int64_t t = g.t0 + 16 * warp + w.g + 8 * y, at = (b * a.Hq + h) * a.Tq + g.qbeg + t;
+    lse[y] = t < g.nq ? a.lse[at] : INFINITY;
+    delta[y] = t < g.nq ? a.delta[at] : 0.f;
   }
-  for (int64_t j0 = 0; j0 < g.nk; j0 += kTile) {
-    __syncthreads();
-    load_t<T, DP>(sb, v, b, g.kbeg + j0, g.kbeg + g.nk, hk, a.D);
-    __syncthreads();
-    float dp[4][4] = {}, s[4][4] = {};
-    product_tt<DP>(dp, sd, sb, ty, tx);
-    __syncthreads();
-    load_t<T, DP>(sb, k, b, g.kbeg + j0, g.kbeg + g.nk, hk, a.D);
-    __syncthreads();
-    product_tt<DP>(s, sq, sb, ty, tx);
+  walk<DP, 2>(
+      tiles, (g.nk + kOther - 1) / kOther,
+      [&](float* x, float* y, int64_t i) {
+        load_rows<T, DP, kOther>(x, k, b, g.kbeg + i * kOther, g.kbeg + g.nk, hk, a.D, on16);
+        load_rows<T, DP, kOther>(y, v, b, g.kbeg + i * kOther, g.kbeg + g.nk, hk, a.D, on16);
+      },
+      [&](const float* sk, const float* sv, int64_t i) {
+        float s[kOther / 8][4] = {}, dp[kOther / 8][4] = {};
+        rows_by_rows<DP>(s, sq + 16 * warp * kPitch<DP>, sk, a.D);
+        rows_by_rows<DP>(dp, sd + 16 * warp * kPitch<DP>, sv, a.D);
+        const int64_t left = g.nk - i * kOther;
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+        for (int j = 0; j < kOther / 8; ++j)
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        s[i][j] = j0 + 4 * tx + j < g.nk ? expf(s[i][j] * a.scale - lse[i]) * (dp[i][j] - delta[i]) : 0.f;
-    __syncthreads();
-    store_t(sp, s, ty, tx);
-    load_r<T, DP>(sb, k, b, g.kbeg + j0, g.kbeg + g.nk, hk, a.D);
-    __syncthreads();
-    product_pm<DP>(dq, sp, sb, ty, tx);
-  }
-  const float f[4] = {a.scale, a.scale, a.scale, a.scale};
-  write_rows<T, DP>(vw<T>(a.dq), dq, b, g.qbeg + g.t0, g.qbeg + g.nq, h, a.D, f, ty, tx);
+          for (int z = 0; z < 4; ++z)
+            s[j][z] = 8 * j + 2 * w.c + z % 2 < left
+                          ? expf(s[j][z] * a.scale - lse[z / 2]) * (dp[j][z] - delta[z / 2])
+                          : 0.f;
+        weights_by_columns<DP>(dq, s, sk, a.D);
+      });
+  const float f[2] = {a.scale, a.scale};
+  write_rows<T, DP>(vw<T>(a.dq), dq, b, g.qbeg + g.t0 + 16 * warp, g.qbeg + g.nq, h, a.D, f);
 }
 
-// A tile of keys against every query, over the heads that share it. Rows past a
-// sequence's keys (padding) get zeros.
+// A tile of keys against every query, over the heads that share it, or one of `pieces`
+// parts of that walk, whose sums go to the workspace. Rows past a sequence's keys
+// (padding) get zeros.
 template <typename T, int DP>
-__global__ void __launch_bounds__(kThreads) cross_dkv_general(const CrossArgs a) {
+__global__ void __launch_bounds__(kThreads) cross_dkv_general(const CrossArgs a, int on16, int pieces) {
   extern __shared__ float4 raw[];
-  float *const sk = reinterpret_cast<float*>(raw), *const sv = sk + DP * kPitch, *const sb = sv + DP * kPitch,
-                *const sp = sb + DP * kPitch, *const ss = sp + kTile * kPitch;
+  float *const sk = reinterpret_cast<float*>(raw), *const sv = sk + kOwn * kPitch<DP>, *const tiles = sv + kOwn * kPitch<DP>;
   if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x < 32)
     check_cross(a.lens, a.cu_q, a.cu_k, a.n_seqs, a.B, a.Tq, a.Tk, a.hdr);
   CrossRows g;
-  const int hk = blockIdx.y % a.Hk, G = a.Hq / a.Hk;
+  const int hk = blockIdx.y % a.Hk, G = a.Hq / a.Hk, piece = blockIdx.x % pieces;
   const int64_t b = blockIdx.y / a.Hk;
-  if (!cross_rows(a.lens, a.cu_q, a.cu_k, a.n_seqs, a.Tq, a.Tk, b, blockIdx.x, kTile, true, &g)) return;
-  const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
+  if (!cross_rows(a.lens, a.cu_q, a.cu_k, a.n_seqs, a.Tq, a.Tk, b, blockIdx.x / pieces, kOwn, true, &g)) return;
+  const Lane w;
+  const int warp = threadIdx.x / 32;
   const View<const T> q = vw<const T>(a.q), dout = vw<const T>(a.dout);
-  load_t<T, DP>(sk, vw<const T>(a.k), b, g.kbeg + g.t0, g.kbeg + g.nk, hk, a.D);
-  load_t<T, DP>(sv, vw<const T>(a.v), b, g.kbeg + g.t0, g.kbeg + g.nk, hk, a.D);
-  float dk[4][DP / 64][4] = {}, dv[4][DP / 64][4] = {};
-  const int64_t nq = g.t0 < g.nk ? g.nq : 0;
-  for (int hh = 0; hh < G; ++hh) {
-    const int h = hk * G + hh;
-    for (int64_t t0 = 0; t0 < nq; t0 += kTile) {
-      __syncthreads();
-      load_t<T, DP>(sb, dout, b, g.qbeg + t0, g.qbeg + nq, h, a.D);
-      __syncthreads();
-      float dp[4][4] = {}, s[4][4] = {};
-      product_tt<DP>(dp, sv, sb, ty, tx);
-      __syncthreads();
-      load_t<T, DP>(sb, q, b, g.qbeg + t0, g.qbeg + nq, h, a.D);
-      __syncthreads();
-      product_tt<DP>(s, sk, sb, ty, tx);
+  load_rows<T, DP, kOwn>(sk, vw<const T>(a.k), b, g.kbeg + g.t0, g.kbeg + g.nk, hk, a.D, on16);
+  load_rows<T, DP, kOwn>(sv, vw<const T>(a.v), b, g.kbeg + g.t0, g.kbeg + g.nk, hk, a.D, on16);
+  float dk[DP / 8][4] = {}, dv[DP / 8][4] = {};
+  const int64_t per = g.t0 < g.nk ? (g.nq + kOther - 1) / kOther : 0;
+  const int64_t first = per * G * piece / pieces, last = per * G * (piece + 1) / pieces;
+  walk<DP, 2>(
+      tiles, last - first,
+      [&](float* x, float* y, int64_t i) {
+        const int64_t h = hk * G + (first + i) / per, t0 = (first + i) % per * kOther;
+        load_rows<T, DP, kOther>(x, q, b, g.qbeg + t0, g.qbeg + g.nq, h, a.D, on16);
+        load_rows<T, DP, kOther>(y, dout, b, g.qbeg + t0, g.qbeg + g.nq, h, a.D, on16);
+      },
+      [&](const float* sq, const float* sd, int64_t i) {
+        const int64_t h = hk * G + (first + i) / per, t0 = (first + i) % per * kOther;
+        float s[kOther / 8][4] = {}, dp[kOther / 8][4] = {};
+        rows_by_rows<DP>(s, sk + 16 * warp * kPitch<DP>, sq, a.D);
+        rows_by_rows<DP>(dp, sv + 16 * warp * kPitch<DP>, sd, a.D);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int64_t t = t0 + 4 * tx + j, at = (b * a.Hq + h) * a.Tq + g.qbeg + t;
-        const float lse = t < nq ? a.lse[at] : INFINITY, delta = t < nq ? a.delta[at] : 0.f;
+        for (int j = 0; j < kOther / 8; ++j)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          s[i][j] = t < nq && g.t0 + 4 * ty + i < g.nk ? expf(s[i][j] * a.scale - lse) : 0.f;
-          dp[i][j] = s[i][j] * (dp[i][j] - delta);
-        }
-      }
-      store_t(sp, s, ty, tx);
-      store_t(ss, dp, ty, tx);
-      __syncthreads();
-      load_r<T, DP>(sb, dout, b, g.qbeg + t0, g.qbeg + nq, h, a.D);
-      __syncthreads();
-      product_pm<DP>(dv, sp, sb, ty, tx);
-      __syncthreads();
-      load_r<T, DP>(sb, q, b, g.qbeg + t0, g.qbeg + nq, h, a.D);
-      __syncthreads();
-      product_pm<DP>(dk, ss, sb, ty, tx);
-    }
+          for (int z = 0; z < 2; ++z) {
+            const int64_t t = t0 + 8 * j + 2 * w.c + z, at = (b * a.Hq + h) * a.Tq + g.qbeg + t;
+            const bool on = t < g.nq;
+            const float lse = on ? a.lse[at] : INFINITY, delta = on ? a.delta[at] : 0.f;
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+              float &e = s[j][2 * y + z], &f = dp[j][2 * y + z];
+              e = on && g.t0 + 16 * warp + w.g + 8 * y < g.nk ? expf(e * a.scale - lse) : 0.f;
+              f = e * (f - delta);
+            }
+          }
+        weights_by_columns<DP>(dv, s, sd, a.D);
+        weights_by_columns<DP>(dk, dp, sq, a.D);
+      });
+  const int64_t rows = a.cu_q ? g.nk : a.Tk, t0 = g.kbeg + g.t0 + 16 * warp;
+  const float one[2] = {1.f, 1.f}, f[2] = {a.scale, a.scale};
+  if (pieces > 1) {
+    const int64_t row = (int64_t)a.Hk * a.D, all = a.B * a.Tk * row;
+    const View<float> pk{a.ws + 2 * piece * all, a.Tk * row, row, a.D}, pv{pk.p + all, a.Tk * row, row, a.D};
+    write_rows<float, DP>(pk, dk, b, t0, g.kbeg + rows, hk, a.D, f);
+    write_rows<float, DP>(pv, dv, b, t0, g.kbeg + rows, hk, a.D, one);
+  } else {
+    write_rows<T, DP>(vw<T>(a.dk), dk, b, t0, g.kbeg + rows, hk, a.D, f);
+    write_rows<T, DP>(vw<T>(a.dv), dv, b, t0, g.kbeg + rows, hk, a.D, one);
   }
-  const int64_t rows = a.cu_q ? g.nk : a.Tk;
-  const float one[4] = {1.f, 1.f, 1.f, 1.f}, f[4] = {a.scale, a.scale, a.scale, a.scale};
-  write_rows<T, DP>(vw<T>(a.dk), dk, b, g.kbeg + g.t0, g.kbeg + rows, hk, a.D, f, ty, tx);
-  write_rows<T, DP>(vw<T>(a.dv), dv, b, g.kbeg + g.t0, g.kbeg + rows, hk, a.D, one, ty, tx);
+}
+
+// The pieces' sums, added in order: an element of dk and of dv a thread.
+template <typename T>
+__global__ void __launch_bounds__(256) cross_pieces_general(const CrossArgs a, int pieces) {
+  const int64_t all = a.B * a.Tk * a.Hk * a.D, i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i >= all) return;
+  float k = 0.f, v = 0.f;
+#pragma unroll 4
+  for (int p = 0; p < pieces; ++p) {
+    k += a.ws[2 * p * all + i];
+    v += a.ws[(2 * p + 1) * all + i];
+  }
+  const int64_t d = i % a.D, h = i / a.D % a.Hk, t = i / a.D / a.Hk % a.Tk, b = i / a.D / a.Hk / a.Tk;
+  vw<T>(a.dk).row(b, t, h)[d] = from_f32<T>(k);
+  vw<T>(a.dv).row(b, t, h)[d] = from_f32<T>(v);
+}
+
+// Pieces of a key tile's walk: as many as fill the SMs four times over, of four tiles of
+// queries at least.
+int general_pieces(int64_t B, int64_t Tq, int64_t Tk, int64_t Hq, int64_t Hk, int64_t n_seqs) {
+  if (Hk < 1 || B < 1 || Tk < 1) return 1;
+  const int64_t blocks = ((Tk + kOwn - 1) / kOwn + n_seqs) * B * Hk;
+  const int64_t walk = Hq / Hk * ((Tq + kOther - 1) / kOther) / (n_seqs > 1 ? n_seqs : 1);
+  int64_t p = 4 * 152 / blocks;
+  p = p < walk / 4 ? p : walk / 4;
+  return (int)(p < 1 ? 1 : p);
 }
 
 template <typename K>
@@ -306,28 +446,34 @@ cudaError_t allow_smem(K kernel, size_t bytes) {
 
 template <typename T, int DP>
 cudaError_t general_fwd(const CrossArgs& a, cudaStream_t s) {
-  const size_t smem = (2 * DP * kPitch + kTile * DP) * 4;
-  static_assert(DP >= kTile, "the weights fit the keys' place");
+  constexpr int smem = kSmem<DP, 1>;
   const cudaError_t e = allow_smem(cross_fwd_general<T, DP>, smem);
   if (e != cudaSuccess) return e;
-  const int64_t tiles = (a.Tq + kTile - 1) / kTile + (a.cu_q ? a.n_seqs : 0);
-  cross_fwd_general<T, DP><<<dim3((unsigned)tiles, (unsigned)(a.B * a.Hq)), kThreads, smem, s>>>(a);
+  const int on16 = rows_on_16(a.q, a.B, a.Tq, a.Hq) && rows_on_16(a.k, a.B, a.Tk, a.Hk) && rows_on_16(a.v, a.B, a.Tk, a.Hk);
+  const int64_t tiles = (a.Tq + kOwn - 1) / kOwn + (a.cu_q ? a.n_seqs : 0);
+  cross_fwd_general<T, DP><<<dim3((unsigned)tiles, (unsigned)(a.B * a.Hq)), kThreads, smem, s>>>(a, on16);
   return cudaGetLastError();
 }
 
 template <typename T, int DP>
 cudaError_t general_bwd(const CrossArgs& a, cudaStream_t s) {
-  const size_t sq = (3 * DP * kPitch + kTile * kPitch) * 4, skv = sq + kTile * kPitch * 4;
-  cudaError_t e = allow_smem(cross_dq_general<T, DP>, sq);
-  if (e == cudaSuccess) e = allow_smem(cross_dkv_general<T, DP>, skv);
+  constexpr int smem = kSmem<DP, 2>;
+  cudaError_t e = allow_smem(cross_dq_general<T, DP>, smem);
+  if (e == cudaSuccess) e = allow_smem(cross_dkv_general<T, DP>, smem);
   if (e != cudaSuccess) return e;
+  const int on16 = rows_on_16(a.q, a.B, a.Tq, a.Hq) && rows_on_16(a.dout, a.B, a.Tq, a.Hq) &&
+                   rows_on_16(a.k, a.B, a.Tk, a.Hk) && rows_on_16(a.v, a.B, a.Tk, a.Hk);
   const int64_t rows = a.B * a.Tq * a.Hq, extra = a.cu_q ? a.n_seqs : 0;
-  const int64_t tq = (a.Tq + kTile - 1) / kTile + extra, tk = (a.Tk + kTile - 1) / kTile + extra;
+  const int64_t tq = (a.Tq + kOwn - 1) / kOwn + extra, tk = (a.Tk + kOwn - 1) / kOwn + extra;
   if (rows > 0) {
     cross_delta_general<T><<<(unsigned)((rows + 7) / 8), 256, 0, s>>>(a, rows);
-    cross_dq_general<T, DP><<<dim3((unsigned)tq, (unsigned)(a.B * a.Hq)), kThreads, sq, s>>>(a);
+    cross_dq_general<T, DP><<<dim3((unsigned)tq, (unsigned)(a.B * a.Hq)), kThreads, smem, s>>>(a, on16);
   }
-  if (a.Tk > 0) cross_dkv_general<T, DP><<<dim3((unsigned)tk, (unsigned)(a.B * a.Hk)), kThreads, skv, s>>>(a);
+  if (a.Tk < 1) return cudaGetLastError();
+  const int pieces = general_pieces(a.B, a.Tq, a.Tk, a.Hq, a.Hk, a.n_seqs);
+  cross_dkv_general<T, DP><<<dim3((unsigned)(tk * pieces), (unsigned)(a.B * a.Hk)), kThreads, smem, s>>>(a, on16, pieces);
+  if (pieces > 1)
+    cross_pieces_general<T><<<(unsigned)((a.B * a.Tk * a.Hk * a.D + 255) / 256), 256, 0, s>>>(a, pieces);
   return cudaGetLastError();
 }
 
@@ -456,7 +602,10 @@ size_t cross_attn_workspace_bytes(int64_t B, int64_t Tq, int64_t Tk, int64_t Hq,
                                   int32_t backward) {
   if (B < 0 || Tq < 0 || Tk < 0 || Hq < 0 || Hk < 0 || D < 1 || D > kMixMaxDim || n_seqs < 0) return 0;
   if (!backward) return kWsHeaderBytes;
-  return kWsHeaderBytes + round_up((size_t)(B * Hq * Tq) * 4, 256) + cross_tc_bwd_floats(B, Tq, Tk, Hq, D, n_seqs) * 4;
+  const size_t tc = cross_tc_bwd_floats(B, Tq, Tk, Hq, D, n_seqs);
+  const int pieces = general_pieces(B, Tq, Tk, Hq, Hk, n_seqs);
+  const size_t general = pieces > 1 ? (size_t)pieces * 2 * (size_t)(B * Tk * Hk * D) : 0;
+  return kWsHeaderBytes + round_up((size_t)(B * Hq * Tq) * 4, 256) + (tc > general ? tc : general) * 4;
 }
 
 scan_status cross_attn_fwd(const scan_view4* q, const scan_view4* k, const scan_view4* v, const int32_t* k_lens,

@@ -33,19 +33,28 @@ constexpr int kThreads = 12 * 32;  // two warpgroups of softmax; copies, two of 
 constexpr uint32_t kHalf = kRows * kPitch;
 constexpr int kBlocks = 152;  // one an SM
 
+// A key tile that is cut: what the block whose share it begins in leaves for the last kernel.
+struct Cut {
+  int32_t parts;  // blocks that have parts of it; 0: none
+  int32_t b, hk, live;
+  int64_t key;    // its first key row, and how many of its rows have gradients
+  int64_t rows;   // and how many are written
+};
+
 struct BwdArgs {
   CUtensorMap q, k, v, dout;
   __nv_bfloat16 *dqp, *dkp, *dvp;
   int64_t dq_sb, dq_st, dq_sh, dk_sb, dk_st, dk_sh, dv_sb, dv_st, dv_sh;
   const float* lse;
   float* delta;
-  float* part;  // [blocks][2][2][128][D]: a block's cut tiles, the first and the last; dv and dk
+  float* part;  // [blocks][2][2][D / 4][128][4]: a block's cut tiles, the first and the last; dv and dk
+  Cut* cut;     // [blocks]
   const int32_t *lens, *cu_q, *cu_k;
   WsHeader* hdr;
   int64_t B, Tq, Tk;
   int64_t tiles, items;  // query tiles of a (batch row, head), and of all
   int n_seqs, Hq, Hk, G, D;
-  int wide;  // rows of dq are on 32 bytes
+  int wide, wide_kv;  // rows of dq, and of dk and dv, are on 32 bytes
   float sl2, scale;
 };
 
@@ -126,6 +135,7 @@ struct DeltaArgs {
 // delta = sum of dout o of every row: 16 lanes of 16 bytes a row, four rows in flight a
 // lane. Bound by DRAM.
 __global__ void __launch_bounds__(256) cross_delta_kernel(const DeltaArgs a) {
+  asm volatile("griddepcontrol.launch_dependents;");
   const int lane = threadIdx.x % 16;
   const int64_t r0 = ((int64_t)blockIdx.x * 16 + threadIdx.x / 16) * 4;
   int64_t tok = r0 / a.H, b = tok / a.T, t = tok - b * a.T;
@@ -226,6 +236,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_dq_kernel(const __grid_cons
   const uint32_t tm = uniform(*tmem_ptr), tS = tm, tDp = tm + 256, tDq = tm + 384;  // two S tiles
   const Stop stop{stop_flag, a.hdr};
   bool ok = true;
+  asm volatile("griddepcontrol.launch_dependents;");
   Item w;
   const auto full = [&](uint32_t c) { return warp_wait(bFull + 8 * (c % NS), (c / NS) & 1, stop); };
   // the next item with keys
@@ -345,6 +356,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_dq_kernel(const __grid_cons
     }
   } else if (warp < 8) {
     // ---- dS: row r in lane r, 64 key columns a warpgroup
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // for delta
     const int x = warp / 4, r = tid - 128 * x;
     const uint32_t lanes = (uint32_t)(warp % 4) << 21;
     uint32_t t = 0, items = 0, single = 0;
@@ -610,6 +622,8 @@ __global__ void __launch_bounds__(kThreads, 1) cross_dkv_kernel(const __grid_con
   const uint32_t tm = uniform(*tmem_ptr), tS = tm, tDp = tm + 128, tDv = tm + 256, tDk = tm + 384;
   const Stop stop{stop_flag, a.hdr};
   bool ok = true;
+  asm volatile("griddepcontrol.launch_dependents;");  // the last kernel's blocks come beside this one's
+  if (tid == 0) a.cut[blockIdx.x].parts = 0;
 
   // this block's pairs [p0, p1), and its walk over them: key tile by key tile, pairs [u0, u1) of each
   KeyTile w;
@@ -643,7 +657,19 @@ __global__ void __launch_bounds__(kThreads, 1) cross_dkv_kernel(const __grid_con
     while (ok && more(false)) {
       if (lane == 0) {
         const int b = a.cu_q ? 0 : w.seq;
-        if (seen > 0) ok = bar_wait(bKVfree, (seen - 1) & 1, stop);
+        const auto load = [&](int u) {
+          const uint32_t sl = qd % NS;
+          if (qd >= NS && !bar_wait(bEmpty + 8 * sl, (qd / NS - 1) & 1, stop)) return false;
+          bar_expect(bFull + 8 * sl, P::kTileBytes);
+#pragma unroll
+          for (int c = 0; c < DP / 64; ++c)
+            copy_in_4d(sR + sl * P::kTileBytes + c * kHalf, u & 1 ? &a.dout : &a.q, bFull + 8 * sl, 64 * c,
+                       w.hk * a.G + u / 2 / w.per, (int)(w.g.qbeg + (int64_t)(u / 2 % w.per) * kRows), b);
+          ++qd;
+          return true;
+        };
+        // the first queries go ahead: their slots are free before the last keys are
+        ok = load(2 * u0) && load(2 * u0 + 1) && (seen == 0 || bar_wait(bKVfree, (seen - 1) & 1, stop));
         if (ok) {
           bar_expect(bKV, 2 * P::kTileBytes);
 #pragma unroll
@@ -652,15 +678,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_dkv_kernel(const __grid_con
             copy_in_4d(sV + c * kHalf, &a.v, bKV, 64 * c, w.hk, (int)(w.g.kbeg + w.g.t0), b);
           }
         }
-        for (int u = 2 * u0; ok && u < 2 * u1; ++u, ++qd) {
-          const uint32_t sl = qd % NS;
-          if (qd >= NS && !(ok = bar_wait(bEmpty + 8 * sl, (qd / NS - 1) & 1, stop))) break;
-          bar_expect(bFull + 8 * sl, P::kTileBytes);
-#pragma unroll
-          for (int c = 0; c < DP / 64; ++c)
-            copy_in_4d(sR + sl * P::kTileBytes + c * kHalf, u & 1 ? &a.dout : &a.q, bFull + 8 * sl, 64 * c,
-                       w.hk * a.G + u / 2 / w.per, (int)(w.g.qbeg + (int64_t)(u / 2 % w.per) * kRows), b);
-        }
+        for (int u = 2 * u0 + 2; ok && u < 2 * u1; ++u) ok = load(u);
       }
       ++seen;
       ok = __all_sync(0xffffffffu, ok);
@@ -711,6 +729,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_dkv_kernel(const __grid_con
   } else if (warp == 11) {
     // ---- row statistics: lse of the next tile of queries as soon as every warp has P, delta
     // once every warp has dS; loaded a tile ahead
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // for the queries' kernel, which may change delta
     uint32_t t = 0;
     float l[4], d[4];
     const auto load = [&](int u) {
@@ -867,9 +886,18 @@ __global__ void __launch_bounds__(kThreads, 1) cross_dkv_kernel(const __grid_con
       __nv_bfloat16* const out = x == 0 ? a.dvp + b * a.dv_sb + (w.g.kbeg + key) * a.dv_st + w.hk * a.dv_sh
                                         : a.dkp + b * a.dk_sb + (w.g.kbeg + key) * a.dk_st + w.hk * a.dk_sh;
       const bool cut = n > 0 && n < w.n, live = key < w.g.nk;
+      if (cut && u0 == 0 && tid == 0) {
+        int e = blockIdx.x;  // the block with its last pair
+        while (share(all, blocks, e + 1) < w.last()) ++e;
+        const int64_t left = w.g.nk - w.g.t0, rows = (a.cu_q ? w.g.nk : a.Tk) - w.g.t0;
+        a.cut[blockIdx.x] = Cut{e - (int)blockIdx.x + 1, b, w.hk, (int)(left < kRows ? left : kRows), w.g.kbeg + w.g.t0,
+                                rows < kRows ? rows : kRows};
+      }
       if (cut) {
-        // the parts of a tile that began in an earlier block's share go to the first place
-        float* const to = a.part + ((((int64_t)blockIdx.x * 2 + (u0 > 0 ? 0 : 1)) * 2 + x) * kRows + r) * a.D;
+        // the parts of a tile that began in an earlier block's share go to the first place; four
+        // columns of neighbouring rows lie side by side, as the threads of a warp have them (a row
+        // in one piece: 6 us a tile)
+        float* const to = a.part + (((int64_t)blockIdx.x * 2 + (u0 > 0 ? 0 : 1)) * 2 + x) * kRows * a.D + 4 * r;
 #pragma unroll
         for (int c = 0; c < DP / 32; ++c) {
           uint32_t o[32];
@@ -877,10 +905,11 @@ __global__ void __launch_bounds__(kThreads, 1) cross_dkv_kernel(const __grid_con
           ld_wait();
 #pragma unroll
           for (int j = 0; j < 32; j += 4)
-            if (32 * c + j < a.D) *reinterpret_cast<uint4*>(to + 32 * c + j) = make_uint4(o[j], o[j + 1], o[j + 2], o[j + 3]);
+            if (32 * c + j < a.D)
+              *reinterpret_cast<uint4*>(to + (32 * c + j) * kRows) = make_uint4(o[j], o[j + 1], o[j + 2], o[j + 3]);
         }
       } else {
-        if (n > 0) write_row<DP>(sum, x == 0 ? 1.f : a.scale, live, false, out, a.D);
+        if (n > 0) write_row<DP>(sum, x == 0 ? 1.f : a.scale, live, a.wide_kv, out, a.D);
         // no query sees these keys, or they are padding
         zero_row(n > 0 ? !live && !a.cu_q && key < a.Tk : live || (!a.cu_q && key < a.Tk), out, a.D);
       }
@@ -897,32 +926,49 @@ __global__ void __launch_bounds__(kThreads, 1) cross_dkv_kernel(const __grid_con
   }
 }
 
-// Adds the parts of the tile whose first part is block blockIdx.x's last, in order: 16 of
-// its keys a block.
-__global__ void __launch_bounds__(256) cross_parts_kernel(const __grid_constant__ BwdArgs a, int grid) {
-  KeyTile w;
-  const int64_t all = find_pair(a, -1, &w), blocks = sharers(all, grid);
-  if (blockIdx.x >= blocks) return;
-  const int64_t p0 = share(all, blocks, blockIdx.x), p1 = share(all, blocks, blockIdx.x + 1);
-  if (p0 >= p1) return;
-  find_pair(a, p1 - 1, &w);
-  if (w.first < p0 || w.last() <= p1) return;  // it began earlier, or ends here
-  int64_t e = blockIdx.x;  // the block with its last pair
-  while (share(all, blocks, e + 1) < w.last()) ++e;
-  const int b = a.cu_q ? 0 : w.seq;
-  const int64_t rows = a.cu_q ? w.g.nk : a.Tk;
-  for (int i = threadIdx.x; i < 2 * 16 * a.D; i += 256) {
-    const int x = i / (16 * a.D), r = blockIdx.y * 16 + i / a.D % 16, c = i % a.D;
-    const int64_t key = w.g.t0 + r;
-    if (key >= rows) continue;
-    float s = 0.f;
-    if (key < w.g.nk)
-      for (int64_t k = blockIdx.x; k <= e; ++k)
-        s += a.part[(((k * 2 + (k == blockIdx.x ? 1 : 0)) * 2 + x) * kRows + r) * a.D + c];
-    __nv_bfloat16* const out = x == 0 ? a.dvp + b * a.dv_sb + (w.g.kbeg + key) * a.dv_st + w.hk * a.dv_sh
-                                      : a.dkp + b * a.dk_sb + (w.g.kbeg + key) * a.dk_st + w.hk * a.dk_sh;
-    out[c] = __float2bfloat16_rn(x == 0 ? s : s * a.scale);
+// Adds the parts of the tile that block blockIdx.x's share begins and does not end, in
+// order: eight columns of a row a thread, neighbouring rows in neighbouring threads.
+__global__ void __launch_bounds__(256) cross_parts_kernel(const __grid_constant__ BwdArgs a) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // for the keys' kernel to end
+  const Cut w = a.cut[blockIdx.x];
+  const int i = blockIdx.y * 256 + threadIdx.x, r = i % kRows, x = i / kRows % 2, c = i / kRows / 2 * 8;
+  if (w.parts == 0 || c >= a.D || r >= w.rows) return;
+  float4 s[2];
+  s[0] = s[1] = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (r < w.live) {
+    // the first part is its block's last place, the others their blocks' first
+    const int64_t size = (int64_t)2 * kRows * a.D, at = (int64_t)x * kRows * a.D + c * kRows + 4 * r;
+#pragma unroll 4
+    for (int k = 0; k < w.parts; ++k) {
+      const float* const p = a.part + (2 * ((int64_t)blockIdx.x + k) + (k == 0 ? 1 : 0)) * size + at;
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const float4 e = *reinterpret_cast<const float4*>(p + 4 * j * kRows);
+        s[j].x += e.x, s[j].y += e.y, s[j].z += e.z, s[j].w += e.w;
+      }
+    }
   }
+  const float f = x == 0 ? 1.f : a.scale;
+  __nv_bfloat16* const out = x == 0 ? a.dvp + w.b * a.dv_sb + (w.key + r) * a.dv_st + w.hk * a.dv_sh
+                                    : a.dkp + w.b * a.dk_sb + (w.key + r) * a.dk_st + w.hk * a.dk_sh;
+  *reinterpret_cast<uint4*>(out + c) = make_uint4(pack_bf16(s[0].x * f, s[0].y * f), pack_bf16(s[0].z * f, s[0].w * f),
+                                                  pack_bf16(s[1].x * f, s[1].y * f), pack_bf16(s[1].z * f, s[1].w * f));
+}
+
+// A kernel that is launched while the one before it runs, whose end it waits for itself.
+template <typename... P, typename... A>
+cudaError_t launch_early(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t s, A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
 template <int DP, bool TWO>
@@ -933,10 +979,11 @@ cudaError_t launch_bwd(const BwdArgs& t, unsigned blocks, cudaStream_t s) {
   if (e == cudaSuccess)
     e = cudaFuncSetAttribute(cross_dq_kernel<DP, TWO>, cudaFuncAttributeMaxDynamicSharedMemorySize, P::kSmem);
   if (e != cudaSuccess) return e;
-  cross_dq_kernel<DP, TWO><<<(unsigned)(t.items < kBlocks ? t.items : kBlocks), kThreads, P::kSmem, s>>>(t);
-  cross_dkv_kernel<DP, TWO><<<blocks, kThreads, P::kSmem, s>>>(t);
-  cross_parts_kernel<<<dim3(blocks, kRows / 16), 256, 0, s>>>(t, (int)blocks);
-  return cudaGetLastError();
+  e = launch_early(cross_dq_kernel<DP, TWO>, dim3((unsigned)(t.items < kBlocks ? t.items : kBlocks)), kThreads, P::kSmem, s, t);
+  if (e == cudaSuccess) e = launch_early(cross_dkv_kernel<DP, TWO>, dim3(blocks), kThreads, P::kSmem, s, t);
+  if (e == cudaSuccess && blocks > 1)
+    e = launch_early(cross_parts_kernel, dim3(blocks, (2 * kRows * t.D / 8 + 255) / 256), 256, 0, s, t);
+  return e;
 }
 
 // Blocks of the keys' kernel: no more than can have two pairs each.
@@ -958,7 +1005,7 @@ bool two_parts(const CrossArgs& a) {
 
 size_t cross_tc_bwd_floats(int64_t B, int64_t Tq, int64_t Tk, int64_t Hq, int64_t D, int64_t n_seqs) {
   if (Tq < 1 || Tk < 1) return 0;
-  return (size_t)key_blocks(B, Tq, Tk, Hq, n_seqs) * 4 * kRows * (size_t)D;
+  return (size_t)key_blocks(B, Tq, Tk, Hq, n_seqs) * (4 * kRows * (size_t)D + sizeof(Cut) / 4);
 }
 
 cudaError_t launch_cross_tc_bwd(const CrossArgs& a, cudaStream_t s) {
@@ -976,7 +1023,9 @@ cudaError_t launch_cross_tc_bwd(const CrossArgs& a, cudaStream_t s) {
   t.dv_sb = a.dv.stride_b, t.dv_st = a.dv.stride_t, t.dv_sh = a.dv.stride_h;
   t.lse = a.lse;
   t.delta = a.delta;
+  const unsigned blocks = (unsigned)key_blocks(a.B, a.Tq, a.Tk, a.Hq, a.n_seqs);
   t.part = a.ws;
+  t.cut = reinterpret_cast<Cut*>(a.ws + (size_t)blocks * 4 * kRows * a.D);
   t.lens = a.lens, t.cu_q = a.cu_q, t.cu_k = a.cu_k;
   t.hdr = a.hdr;
   t.B = a.B, t.Tq = a.Tq, t.Tk = a.Tk;
@@ -985,6 +1034,7 @@ cudaError_t launch_cross_tc_bwd(const CrossArgs& a, cudaStream_t s) {
   t.tiles = (a.Tq + kRows - 1) / kRows + (a.cu_q ? a.n_seqs : 0);
   t.items = t.tiles * a.B * a.Hq;
   t.wide = rows_on_32(a.dq, a.B, a.Tq, a.Hq, a.D);
+  t.wide_kv = rows_on_32(a.dk, a.B, a.Tk, a.Hk, a.D) && rows_on_32(a.dv, a.B, a.Tk, a.Hk, a.D);
   t.sl2 = a.scale * 1.44269504088896341f;
   t.scale = a.scale;
   DeltaArgs d;
@@ -998,7 +1048,6 @@ cudaError_t launch_cross_tc_bwd(const CrossArgs& a, cudaStream_t s) {
   d.D = a.D;
   d.rows = a.B * a.Tq * a.Hq;
   cross_delta_kernel<<<(unsigned)((d.rows + 63) / 64), 256, 0, s>>>(d);
-  const unsigned blocks = (unsigned)key_blocks(a.B, a.Tq, a.Tk, a.Hq, a.n_seqs);
   const bool two = two_parts(a);
   if (a.D <= 64) return two ? launch_bwd<64, true>(t, blocks, s) : launch_bwd<64, false>(t, blocks, s);
   return two ? launch_bwd<128, true>(t, blocks, s) : launch_bwd<128, false>(t, blocks, s);
