@@ -20,6 +20,7 @@
 //            workspace (at most two a block), which a last kernel adds in order.
 // Either kernel issues the products of its two chains from two warps, so that one's waits
 // and commits are under the other's products.
+#include "scan_cross_phases.h"
 #include "scan_cross_tc.h"
 #include "scan_tc.cuh"
 
@@ -61,7 +62,7 @@ struct BwdArgs {
 template <int DP>
 struct Plan {
   static constexpr int kTileBytes = kRows * DP * 2;
-  static constexpr int kSlots = DP == 128 ? 5 : 8;
+  static constexpr int kSlots = bwd_slots(DP);
   static constexpr int kMisc = 2048;  // barriers, row statistics
   static constexpr int kSmem = (2 + kSlots) * kTileBytes + 1024 + kMisc;
 };

@@ -30,6 +30,7 @@
 // 1.58 PFLOP/s. Bound by the chain of a tile: 1000 cycles of products, 1340 of softmax
 // (512 of them the special-function unit's) and 600 to 700 of handing over, against
 // 2 x 1000 of tensor time for the pair; a pair's beginning and end cost another 5500.
+#include "scan_cross_phases.h"
 #include "scan_cross_tc.h"
 #include "scan_tc.cuh"
 
@@ -76,7 +77,7 @@ struct FwdArgs {
 template <int DP>
 struct Plan {
   static constexpr int kTileBytes = kRows * DP * 2;
-  static constexpr int kSlots = DP == 128 ? 5 : 8;
+  static constexpr int kSlots = fwd_slots(DP);
   static constexpr int kSmem = (2 + kSlots) * kTileBytes  + 1024 + 512;
 };
 

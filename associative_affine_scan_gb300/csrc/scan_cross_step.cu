@@ -10,6 +10,7 @@
 // each row, and the weights by the values. A warp keeps its own sums until the request's
 // last tile; then the warps' are added in order. A request that a share's end cuts leaves
 // its parts in the workspace (at most two a block), which a second kernel adds in order.
+#include "scan_cross_phases.h"
 #include "scan_cross_tc.h"
 #include "scan_tc.cuh"
 
@@ -50,10 +51,7 @@ struct StepArgs {
 template <int DP>
 struct Plan {
   static constexpr int kTileBytes = kKeys * DP * 2;  // of keys or values
-  // An even number, so that a stage is always the same group's: a wait tells a barrier's
-  // phases apart only by parity, and a group that saw every second one would take a phase
-  // that is to come for one that was.
-  static constexpr int kStages = DP == 128 ? 6 : 12;
+  static constexpr int kStages = step_stages(DP);
   static_assert(kStages % 2 == 0, "a stage belongs to one group");
   static constexpr int kRow = DP + 8;                // floats: rows eight apart lie in different banks
   static constexpr int kFold = 4 * 8 * kRow * 4;     // sums of four warps, eight heads

@@ -133,10 +133,6 @@ __device__ __forceinline__ void copy_out_4d(const CUtensorMap* map, uint32_t src
 __device__ __forceinline__ void copy_out_commit() {
   asm volatile("cp.async.bulk.commit_group;" ::: "memory");
 }
-// The copies' sources may be written again.
-__device__ __forceinline__ void copy_out_read() {
-  asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-}
 __device__ __forceinline__ void copy_out_done() {
   asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
 }
