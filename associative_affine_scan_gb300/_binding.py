@@ -1517,10 +1517,10 @@ def residual_norm_bwd(x_out, y, dx_out, dn, post_weight=None, gate=None, next_we
         dwp, dg, dwn = (None if t is None else torch.empty(t.shape, dtype=torch.float32, device=dev)
                         for t in (post_weight, gate, next_weight))
     s = _raw_stream(stream, dev)
-    ws = _mixer_workspace(256 + residual_norm_workspace_bytes(B, T, C, row_gate), dev, s)
+    ws = _mixer_workspace(residual_norm_workspace_bytes(B, T, C, row_gate), dev, s)
     _enter(dev, "residual_norm_bwd", _view3(x_out), None if y is None else _view3(y),
            None if dx_out is None else _view3(dx_out), None if dn is None else _view3(dn), _at(post_weight),
            _at(gate), _at(next_weight), _view3(dx), None if y is None else _view3(dy), _at(dwp), _at(dg),
            _at(dwn), B, T, C, row_gate, alpha, eps, *_random(rng, p, dev), _dtype_code(x_out),
-           _type_code(dt), ws.data_ptr() + 256, ws.numel() - 256, s)  # past the status word
+           _type_code(dt), ws.data_ptr(), ws.numel(), s)
     return dx, dy, dwp, dg, dwn

@@ -40,6 +40,7 @@ struct NormArgs {
   float alpha, eps, inv_C;
   Drop drop;
   // backward
+  WsHeader* hdr;
   float *part_h, *part_n;  // [units][C]
   int64_t groups, span;    // rows that share a gate: `groups` runs of `span` rows
   int chunks;              // units a group
@@ -244,18 +245,12 @@ __global__ void __launch_bounds__(512) residual_fwd_kernel(const NormArgs a) {
   }
 }
 
-// 16 bytes of a row to this thread's own place in shared memory.
-__device__ __forceinline__ void copy16(uint32_t to, const void* from) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+// A run of a row to shared memory; `bar` counts its bytes.
+__device__ __forceinline__ void copy_run(uint32_t to, const void* from, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(to),
+               "l"(from), "r"(bytes), "r"(bar)
+               : "memory");
 }
-__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void copies_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-// Eight elements in pieces of 16 bytes.
-template <typename T>
-constexpr int kPieces = sizeof(T) * 8 / 16;
 __device__ __forceinline__ void keep16(uint32_t at, float2 a, float2 b) {
   asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(at), "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y) : "memory");
 }
@@ -294,45 +289,49 @@ __device__ __forceinline__ void six_sums(float (&s)[6], float4 (*red)[2], int W)
   s[0] = a.x, s[1] = a.y, s[2] = a.z, s[3] = a.w, s[4] = b.x, s[5] = b.y;
 }
 
-// A row of an operand, walked row by row without products of strides.
-template <typename T>
-struct Walk {
-  T* p;
-  int64_t step, wrap;  // to the next row of this thread's, and what a batch's end adds
-  __device__ __forceinline__ void start(T* base, int64_t sb, int64_t st, int64_t b, int64_t t, int64_t T_, int per, int c) {
-    p = base ? base + b * sb + t * st + c : nullptr;
-    step = per * st;
-    wrap = sb - T_ * st;
-  }
-  __device__ __forceinline__ void on(int wraps) {
-    p += step;
-    if (wraps) p += wraps * wrap;
-  }
-};
-
-// A block walks units: a part of the rows that share a gate, its column sums in
-// registers, left in the workspace and added in order by the kernel below. A thread
-// copies its pieces of the next rows to its own places in shared memory, AHEAD rows
-// ahead, so no barrier is needed for them; its weights lie there as well.
+// A block walks units: every chunks-th row of those that share a gate (so that blocks at
+// work are at neighbouring rows), its column sums in registers, left in the workspace and
+// added in order by the kernel below. A row's operands are copied to shared memory as
+// whole runs, AHEAD rows ahead, by one thread of its own; the unit's weights lie there as
+// well. Where the rows to come begin is worked out by six threads, one an operand, which
+// leave it in shared memory: six walks in every thread took 30 registers. Copies by the
+// threads themselves, 16 bytes each, moved every sector of the fp32 operands twice.
 template <typename X, typename Y, int V, int AHEAD>
 __global__ void __launch_bounds__(V == 4 ? 256 : 128, V == 4 ? 1 : 3) residual_bwd_kernel(const NormArgs a) {
-  constexpr int PX = kPieces<X>, PY = kPieces<Y>, PR = 2 * PX + 2 * PY, NS = AHEAD + 1;
+  constexpr int NS = AHEAD + 1;  // 1, 2 or 4
   __shared__ float4 red[2][8][2];
-  extern __shared__ float4 ring[];  // [NS V PR + 4 V][threads]; then the fold: [rows a block - 1][2][C]
+  __shared__ char* begins[8][8][6];  // a slot a row of the block
+  __shared__ uint64_t bars[8][NS];
+  __shared__ uint32_t expired;
+  // [NS][rows a block] of x', dx', y, dn; the weights' pieces [4 V][threads a row]; then the
+  // fold: [rows a block - 1][2][C]
+  extern __shared__ float4 ring[];
   const int per = blockDim.x / 32 / a.W, lane = threadIdx.x % (32 * a.W), mine = threadIdx.x / (32 * a.W);
-  const uint32_t apart = blockDim.x * 16;  // bytes between a thread's pieces
-  const uint32_t own = (uint32_t)__cvta_generic_to_shared(ring) + threadIdx.x * 16, own_w = own + NS * V * PR * apart;
+  const uint32_t run_x = a.C * sizeof(X), run_y = a.C * sizeof(Y), run = 2 * (run_x + run_y);
+  const uint32_t apart = 32 * a.W * 16;  // bytes between a thread's pieces of the weights
+  const uint32_t rows_at = tc::smem_addr(ring), own_w = rows_at + NS * per * run + lane * 16;
+  const uint32_t bar0 = tc::smem_addr(&bars[mine][0]);
+  const tc::Stop stop{&expired, a.hdr};
   float* const fold = reinterpret_cast<float*>(ring);
   const int64_t units = a.groups * a.chunks;
   asm volatile("griddepcontrol.launch_dependents;");  // the sums' blocks come beside this one's
   uint64_t seed, call;
   a.drop.read(&seed, &call);
   const int c0 = 8 * lane, apart_c = 8 * 32 * a.W;  // a thread's first column, and from vector to vector
+  if (threadIdx.x == 0) expired = 0;
+  if (lane == 0) {
+    for (int i = 0; i < NS; ++i) tc::bar_init(bar0 + 8 * i, 1);
+    tc::bar_init_fence();
+  }
+  uint32_t turn = 0;  // rows walked before this unit
   for (int64_t unit = blockIdx.x; unit < units; unit += gridDim.x) {
     const int64_t grp = unit / a.chunks, ch = unit - grp * a.chunks;
-    const int64_t beg = grp * a.span + a.span * ch / a.chunks, end = grp * a.span + a.span * (ch + 1) / a.chunks;
+    const int64_t beg = grp * a.span + ch * per, end = (grp + 1) * a.span, step = (int64_t)a.chunks * per;
+    const int64_t on_b = step / a.T, on_t = step - on_b * a.T;
     const float* const gate = a.gate ? a.gate + (a.row_gate ? grp * a.gate_sb : 0) : nullptr;
     float2 h[V][4], dw[V][4];
+    tc::fence_async();  // (the fold's writes, before copies to the same place)
+    __syncthreads();    // the last unit's rows are done
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       const int c = c0 + v * apart_c;
@@ -345,68 +344,66 @@ __global__ void __launch_bounds__(V == 4 ? 256 : 128, V == 4 ? 1 : 3) residual_b
         wu[i] = mul2(wu[i], h[v][i]);
         h[v][i] = dw[v][i] = both(0.f);
       }
-      keep16(own_w + (4 * v) * apart, wn[0], wn[1]);
-      keep16(own_w + (4 * v + 1) * apart, wn[2], wn[3]);
-      keep16(own_w + (4 * v + 2) * apart, wu[0], wu[1]);
-      keep16(own_w + (4 * v + 3) * apart, wu[2], wu[3]);
-    }
-    // the rows that are copied, and behind them those that are worked
-    const int64_t b0 = (beg + mine) / a.T;
-    int64_t lt = beg + mine - b0 * a.T, t = lt;
-    Walk<const X> wx, wg;
-    Walk<const Y> wy, we;
-    Walk<X> ox;
-    Walk<Y> oy;
-    wx.start(static_cast<const X*>(a.x), a.x_sb, a.x_st, b0, t, a.T, per, c0);
-    wg.start(static_cast<const X*>(a.dxo), a.xo_sb, a.xo_st, b0, t, a.T, per, c0);
-    wy.start(static_cast<const Y*>(a.y), a.y_sb, a.y_st, b0, t, a.T, per, c0);
-    we.start(static_cast<const Y*>(a.dn), a.n_sb, a.n_st, b0, t, a.T, per, c0);
-    ox.start(static_cast<X*>(a.dx), a.dx_sb, a.dx_st, b0, t, a.T, per, c0);
-    oy.start(static_cast<Y*>(a.dy), a.dy_sb, a.dy_st, b0, t, a.T, per, c0);
-    const auto wraps = [&](int64_t* t) {
-      int n = 0;
-      *t += per;
-      while (*t >= a.T) *t -= a.T, ++n;
-      return n;
-    };
-    const auto copy = [&](int64_t row, int slot) {
-      if (row < end) {
-        uint32_t to = own + (uint32_t)(slot * V * PR) * apart;
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-          if (c0 + v * apart_c < a.C) {
-            const int at = v * apart_c;
-            if (a.x) {
-#pragma unroll
-              for (int j = 0; j < PX; ++j) copy16(to + j * apart, reinterpret_cast<const char*>(wx.p + at) + 16 * j);
-#pragma unroll
-              for (int j = 0; j < PY; ++j)
-                copy16(to + (2 * PX + PY + j) * apart, reinterpret_cast<const char*>(we.p + at) + 16 * j);
-            }
-            if (a.dxo)
-#pragma unroll
-              for (int j = 0; j < PX; ++j) copy16(to + (PX + j) * apart, reinterpret_cast<const char*>(wg.p + at) + 16 * j);
-            if (a.y)
-#pragma unroll
-              for (int j = 0; j < PY; ++j) copy16(to + (2 * PX + j) * apart, reinterpret_cast<const char*>(wy.p + at) + 16 * j);
-          }
-          to += PR * apart;
-        }
-        const int n = wraps(&lt);
-        wx.on(n), wg.on(n), wy.on(n), we.on(n);
+      if (mine == 0) {
+        keep16(own_w + (4 * v) * apart, wn[0], wn[1]);
+        keep16(own_w + (4 * v + 1) * apart, wn[2], wn[3]);
+        keep16(own_w + (4 * v + 2) * apart, wu[0], wu[1]);
+        keep16(own_w + (4 * v + 3) * apart, wu[2], wu[3]);
       }
-      copies_commit();
+    }
+    // x', dx', y, dn, dx, dy of the rows to come, until one row after their own
+    char* next = nullptr;
+    int64_t on = 0, wrap = 0, at_t = 0;
+    if (lane < 6) {
+      const int64_t b = (beg + mine) / a.T;
+      at_t = beg + mine - b * a.T;
+      const bool x = lane == 0 || lane == 1 || lane == 4;
+      const int64_t sb = lane == 0 ? a.x_sb : lane == 1 ? a.xo_sb : lane == 2 ? a.y_sb : lane == 3 ? a.n_sb : lane == 4 ? a.dx_sb : a.dy_sb;
+      const int64_t st = lane == 0 ? a.x_st : lane == 1 ? a.xo_st : lane == 2 ? a.y_st : lane == 3 ? a.n_st : lane == 4 ? a.dx_st : a.dy_st;
+      const void* const base = lane == 0 ? a.x : lane == 1 ? a.dxo : lane == 2 ? a.y : lane == 3 ? a.dn : lane == 4 ? a.dx : a.dy;
+      const int64_t size = x ? sizeof(X) : sizeof(Y);
+      next = static_cast<char*>(const_cast<void*>(base)) + (b * sb + at_t * st) * size;
+      on = (on_b * sb + on_t * st) * size;
+      wrap = (sb - a.T * st) * size;
+    }
+    char* const* const mine_at = &begins[mine][0][0];
+    const auto begin_of = [&](int i) {
+      if (lane < 6) {
+        begins[mine][i & 7][lane] = next;
+        next += on;
+        at_t += on_t;
+        if (at_t >= a.T) at_t -= a.T, next += wrap;
+      }
     };
-    int head = 0, odd = 0;
+    for (int i = 0; i <= AHEAD; ++i) begin_of(i);
+    __syncthreads();
+    // row r0 of the block's next ones, this thread's among them: the i-th of the unit
+    const auto copy = [&](int64_t r0, int i) {
+      if (lane == 0 && r0 < end) {
+        const uint32_t slot = (turn + i) % NS, bar = bar0 + 8 * slot;
+        if (r0 + mine < end) {
+          const uint32_t to = rows_at + (slot * per + mine) * run;
+          char* const* const from = mine_at + (i & 7) * 6;
+          tc::bar_expect(bar, (a.x ? run_x + run_y : 0) + (a.dxo ? run_x : 0) + (a.y ? run_y : 0));
+          if (a.x) copy_run(to, from[0], run_x, bar);
+          if (a.dxo) copy_run(to + run_x, from[1], run_x, bar);
+          if (a.y) copy_run(to + 2 * run_x, from[2], run_y, bar);
+          if (a.x) copy_run(to + 2 * run_x + run_y, from[3], run_y, bar);
+        } else {
+          tc::bar_arrive(bar);
+        }
+      }
+    };
+    int odd = 0, count = 0;
 #pragma unroll
-    for (int i = 0; i < AHEAD; ++i) copy(beg + mine + (int64_t)i * per, i);
-    for (int64_t r0 = beg; r0 < end; r0 += per) {
+    for (int i = 0; i < AHEAD; ++i) copy(beg + i * step, i);
+    for (int64_t r0 = beg; r0 < end; r0 += step, ++count) {
       const int64_t row = r0 + mine;
       const bool live = row < end;
-      copy(row + (int64_t)AHEAD * per, head >= 1 ? head - 1 : NS - 1);
-      copies_wait<AHEAD>();
-      const uint32_t at0 = own + (uint32_t)(head * V * PR) * apart;
-      head = head + 1 == NS ? 0 : head + 1;
+      begin_of(count + AHEAD + 1);
+      copy(r0 + AHEAD * step, count + AHEAD);
+      const uint32_t slot = (turn + count) % NS, at0 = rows_at + (slot * per + mine) * run;
+      tc::bar_wait(bar0 + 8 * slot, (turn + count) / NS & 1, stop);
       // x', dx', y, dn; zeros where there is nothing
       Eight<X> ex[V], eg[V];
       Eight<Y> ey[V], en[V];
@@ -417,12 +414,12 @@ __global__ void __launch_bounds__(V == 4 ? 256 : 128, V == 4 ? 1 : 3) residual_b
 #pragma unroll
       for (int v = 0; v < V; ++v) {
         const int c = c0 + v * apart_c;
-        const uint32_t at = at0 + (uint32_t)(v * PR) * apart;
+        const uint32_t at_x = at0 + c * sizeof(X), at_y = at0 + 2 * run_x + c * sizeof(Y);
         const bool here = live && c < a.C;
         ex[v].clear(), eg[v].clear(), ey[v].clear(), en[v].clear();
-        if (here && a.x) ex[v].take(at, apart), en[v].take(at + (2 * PX + PY) * apart, apart);
-        if (here && a.dxo) eg[v].take(at + PX * apart, apart);
-        if (here && a.y) ey[v].take(at + 2 * PX * apart, apart);
+        if (here && a.x) ex[v].take(at_x, 16), en[v].take(at_y + run_y, 16);
+        if (here && a.dxo) eg[v].take(at_x + run_x, 16);
+        if (here && a.y) ey[v].take(at_y, 16);
         float2 x[4], g[4], y[4], e[4], w[4];
         ex[v].get(x);
         en[v].get(e);
@@ -495,7 +492,7 @@ __global__ void __launch_bounds__(V == 4 ? 256 : 128, V == 4 ? 1 : 3) residual_b
         }
         Eight<X> out;
         out.set(e);
-        if (here) out.store(ox.p + v * apart_c, a.wide);
+        if (here) out.store(reinterpret_cast<X*>(mine_at[(count & 7) * 6 + 4]) + c, a.wide);
         if (a.y) {
           if (a.drop.limit)
 #pragma unroll
@@ -514,13 +511,11 @@ __global__ void __launch_bounds__(V == 4 ? 256 : 128, V == 4 ? 1 : 3) residual_b
           }
           Eight<Y> back;
           back.set(g);
-          if (here) back.store(oy.p + v * apart_c, a.wide);
+          if (here) back.store(reinterpret_cast<Y*>(mine_at[(count & 7) * 6 + 5]) + c, a.wide);
         }
       }
-      const int n = wraps(&t);
-      ox.on(n), oy.on(n);
     }
-    copies_wait<0>();
+    turn += count;
     // the block's rows, in order
     if (per > 1) {
       __syncthreads();
@@ -556,6 +551,7 @@ __global__ void __launch_bounds__(V == 4 ? 256 : 128, V == 4 ? 1 : 3) residual_b
       }
     if (per > 1) __syncthreads();
   }
+  tc::linger(stop);
 }
 
 struct SumArgs {
@@ -649,18 +645,18 @@ struct Ring {
   int ahead, per_sm;
   size_t bytes;
 };
-Ring ring_of(const Shape& h, int pieces) {
-  const size_t row = (size_t)h.V * pieces * h.threads * 16, held = (size_t)h.V * 4 * h.threads * 16;
-  const size_t sm = (size_t)226 << 10, third = (size_t)74 << 10;
+Ring ring_of(const Shape& h, int C, int bytes) {
+  const size_t row = (size_t)(h.threads / 32 / h.W) * C * bytes, held = (size_t)h.V * 4 * h.W * 32 * 16;
+  const size_t sm = (size_t)221 << 10, third = (size_t)70 << 10, fixed = 5 << 10;  // fixed: what a block has besides
   Ring r;
   r.ahead = 4 * row + held <= third ? 3 : 2 * row + held <= sm ? 1 : 0;
   r.bytes = (r.ahead + 1) * row + held;
-  const int fit = (int)(sm / (r.bytes + 1024)), regs = h.V < 4 ? 3 : h.threads <= 128 ? 2 : 1;
+  const int fit = (int)(((size_t)228 << 10) / (r.bytes + fixed)), regs = h.V < 4 ? 3 : h.threads <= 128 ? 2 : 1;
   r.per_sm = fit < 1 ? 1 : fit < regs ? fit : regs;
   return r;
 }
-int pieces_of(scan_dtype stream_dt, scan_dtype dt) {
-  return 2 * (stream_dt == SCAN_BF16 ? 1 : 2) + 2 * (dt == SCAN_BF16 ? 1 : 2);
+int bytes_of(scan_dtype stream_dt, scan_dtype dt) {  // of x', dx', y and dn, an element of each
+  return 2 * (stream_dt == SCAN_BF16 ? 2 : 4) + 2 * (dt == SCAN_BF16 ? 2 : 4);
 }
 
 template <typename X, typename Y>
@@ -767,10 +763,10 @@ extern "C" {
 
 size_t residual_norm_workspace_bytes(int64_t B, int64_t T, int64_t C, int32_t row_gate) {
   if (B < 0 || T < 0 || C < 1 || C % 8 || C > kMaxC) return 0;
-  if (B == 0 || T == 0) return 16;
+  if (B == 0 || T == 0) return kWsHeaderBytes;
   if ((double)B * (double)T > 2147483647.) return 0;
   const Units u = units_of(B, T, row_gate != 0, kMostBlocks);
-  return (size_t)(u.groups * u.chunks) * 2 * (size_t)C * 4;
+  return kWsHeaderBytes + (size_t)(u.groups * u.chunks) * 2 * (size_t)C * 4;
 }
 
 scan_status residual_norm_fwd(const scan_view4* x, const scan_view4* y, const float* post_weight, const float* gate,
@@ -846,12 +842,13 @@ scan_status residual_norm_bwd(const scan_view4* x_out, const scan_view4* y, cons
     a.dy = dy->ptr, a.dy_sb = dy->stride_b, a.dy_st = dy->stride_t;
   }
   const Shape h = bwd_shape(a.C);
-  const Ring r = ring_of(h, pieces_of(stream_dt, dt));
+  const Ring r = ring_of(h, a.C, bytes_of(stream_dt, dt));
   const Units u = units_of(B, T, a.row_gate, r.per_sm * kSms);
   a.groups = u.groups;
   a.span = u.span;
   a.chunks = u.chunks;
-  a.part_h = static_cast<float*>(workspace);
+  a.hdr = static_cast<WsHeader*>(workspace);
+  a.part_h = reinterpret_cast<float*>(static_cast<char*>(workspace) + kWsHeaderBytes);
   a.part_n = a.part_h + u.groups * u.chunks * C;
   const SumArgs m{a.part_h, a.part_n, post_weight, gate, dpost_weight, dgate, dnext_weight, u.groups * u.chunks,
                   a.C, u.chunks, a.row_gate};

@@ -788,7 +788,7 @@ scan_status residual_norm_fwd(const scan_view4* x, const scan_view4* y, const fl
  * without it. dx: stream_dt, dy: dt, written (dx may be dx_out, dy may be dn); dpost_weight,
  * dgate, dnext_weight: fp32 in their inputs' shapes, written, or NULL. The sums over rows are
  * fp32 in a fixed order. workspace: residual_norm_workspace_bytes() bytes, 16-byte aligned,
- * nothing kept between calls. Other errors as the forward's. */
+ * zeroed once with scan_workspace_init. Other errors as the forward's. */
 scan_status residual_norm_bwd(const scan_view4* x_out, const scan_view4* y, const scan_view4* dx_out,
                               const scan_view4* dn, const float* post_weight, const float* gate,
                               const float* next_weight, const scan_view4* dx, const scan_view4* dy,
