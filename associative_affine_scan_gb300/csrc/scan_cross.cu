@@ -225,9 +225,25 @@ __device__ __forceinline__ void walk(float* tiles, int64_t n, const L& load, con
   loads_wait<0>();
 }
 
+// What a piece of a query tile's walk over the keys leaves of a row: the maximum and the sum
+// of its weights, and the sum of its values, in the workspace.
+struct Pieces {
+  float *m, *l;     // [pieces][B][Hq][Tq]
+  View<float> o;    // the first piece's [B, Tq, Hq, D]
+  int64_t rows, size;  // rows and floats of o from piece to piece
+};
+__host__ __device__ inline Pieces pieces_at(const CrossArgs& a, int pieces) {
+  const int64_t rows = a.B * a.Hq * a.Tq, stats = (rows * pieces + 3) / 4 * 4;
+  return Pieces{a.ws, a.ws + stats, View<float>{a.ws + 2 * stats, a.Hq * a.Tq * a.D, a.D, a.Tq * a.D}, rows, rows * a.D};
+}
+size_t pieces_floats(int64_t B, int64_t Tq, int64_t Hq, int64_t D, int pieces) {
+  return pieces > 1 ? (size_t)pieces * (size_t)(B * Hq * Tq) * (size_t)(D + 2) + 8 : 0;
+}
+
 template <typename T, int DP>
-__global__ void __launch_bounds__(kThreads) cross_fwd_general(const CrossArgs a, int on16) {
+__global__ void __launch_bounds__(kThreads) cross_fwd_general(const CrossArgs a, int on16, int pieces) {
   extern __shared__ float4 raw[];
+  asm volatile("griddepcontrol.launch_dependents;");
   float *const sq = reinterpret_cast<float*>(raw), *const tiles = sq + kOwn * kPitch<DP>;
   if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x < 32)
     check_cross(a.lens, a.cu_q, a.cu_k, a.n_seqs, a.B, a.Tq, a.Tk, a.hdr);
@@ -241,16 +257,18 @@ __global__ void __launch_bounds__(kThreads) cross_fwd_general(const CrossArgs a,
   load_rows<T, DP, kOwn>(sq, vw<const T>(a.q), b, g.qbeg + g.t0, g.qbeg + g.nq, h, a.D, on16);
   const float* const own = sq + 16 * warp * kPitch<DP>;
   float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f}, o[DP / 8][4] = {};
+  const int64_t all = (g.nk + kOther - 1) / kOther, first = all * blockIdx.z / pieces, last = all * (blockIdx.z + 1) / pieces;
   walk<DP, 1>(
-      tiles, (g.nk + kOther - 1) / kOther,
+      tiles, last - first,
       [&](float* x, float* y, int64_t i) {
-        load_rows<T, DP, kOther>(x, k, b, g.kbeg + i * kOther, g.kbeg + g.nk, hk, a.D, on16);
-        load_rows<T, DP, kOther>(y, v, b, g.kbeg + i * kOther, g.kbeg + g.nk, hk, a.D, on16);
+        const int64_t t = g.kbeg + (first + i) * kOther;
+        load_rows<T, DP, kOther>(x, k, b, t, g.kbeg + g.nk, hk, a.D, on16);
+        load_rows<T, DP, kOther>(y, v, b, t, g.kbeg + g.nk, hk, a.D, on16);
       },
       [&](const float* sk, const float* sv, int64_t i) {
         float s[kOther / 8][4] = {};
         rows_by_rows<DP>(s, own, sk, a.D);
-        const int64_t left = g.nk - i * kOther;
+        const int64_t left = g.nk - (first + i) * kOther;
 #pragma unroll
         for (int y = 0; y < 2; ++y) {
           float top = -INFINITY;
@@ -276,7 +294,19 @@ __global__ void __launch_bounds__(kThreads) cross_fwd_general(const CrossArgs a,
         }
         weights_by_columns<DP>(o, s, sv, a.D);
       });
-  float f[2];
+  float f[2] = {1.f, 1.f};
+  if (pieces > 1) {
+    Pieces p = pieces_at(a, pieces);
+    p.o.p += blockIdx.z * p.size;
+#pragma unroll
+    for (int y = 0; y < 2; ++y) {
+      l[y] = row_sum(l[y]);
+      const int64_t t = g.t0 + 16 * warp + w.g + 8 * y, at = blockIdx.z * p.rows + (b * a.Hq + h) * a.Tq + g.qbeg + t;
+      if (w.c == 0 && t < g.nq) p.m[at] = m[y], p.l[at] = l[y];
+    }
+    write_rows<float, DP>(p.o, o, b, g.qbeg + g.t0 + 16 * warp, g.qbeg + g.nq, h, a.D, f);
+    return;
+  }
 #pragma unroll
   for (int y = 0; y < 2; ++y) {
     l[y] = row_sum(l[y]);
@@ -286,6 +316,40 @@ __global__ void __launch_bounds__(kThreads) cross_fwd_general(const CrossArgs a,
       a.lse[(b * a.Hq + h) * a.Tq + g.qbeg + t] = l[y] == 0.f ? -INFINITY : m[y] + logf(l[y]);
   }
   write_rows<T, DP>(vw<T>(a.o), o, b, g.qbeg + g.t0 + 16 * warp, g.qbeg + g.nq, h, a.D, f);
+}
+
+// The pieces of a row, added in order: a warp a row, four columns a lane; eight blocks a
+// tile of 64 rows (with one, 24 us of a call of 142).
+template <typename T>
+__global__ void __launch_bounds__(256) cross_join_general(const CrossArgs a, int pieces) {
+  CrossRows g;
+  const int h = blockIdx.y % a.Hq, lane = threadIdx.x % 32;
+  const int64_t b = blockIdx.y / a.Hq;
+  const bool any = cross_rows(a.lens, a.cu_q, a.cu_k, a.n_seqs, a.Tq, a.Tk, b, blockIdx.x, kOwn, false, &g);
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (!any) return;
+  const Pieces p = pieces_at(a, pieces);
+  const int64_t t = g.t0 + 8 * blockIdx.z + threadIdx.x / 32, at = (b * a.Hq + h) * a.Tq + g.qbeg + t;
+  if (t >= g.nq) return;
+  float top = -INFINITY, sum = 0.f;
+#pragma unroll 4
+  for (int z = 0; z < pieces; ++z) top = fmaxf(top, p.m[z * p.rows + at]);
+  const float base = top == -INFINITY ? 0.f : top;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int z = 0; z < pieces; ++z) {
+    float4 e = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (4 * lane < a.D) e = *reinterpret_cast<const float4*>(p.o.row(b, g.qbeg + t, h) + z * p.size + 4 * lane);
+    const float f = expf(p.m[z * p.rows + at] - base);
+    sum = fmaf(p.l[z * p.rows + at], f, sum);
+    o.x = fmaf(e.x, f, o.x), o.y = fmaf(e.y, f, o.y), o.z = fmaf(e.z, f, o.z), o.w = fmaf(e.w, f, o.w);
+  }
+  const float r = sum == 0.f ? 0.f : 1.f / sum;  // no key; NaN stays
+  if (lane == 0) a.lse[at] = sum == 0.f ? -INFINITY : top + logf(sum);
+  if (4 * lane < a.D) {
+    T* const row = vw<T>(a.o).row(b, g.qbeg + t, h) + 4 * lane;
+    row[0] = from_f32<T>(o.x * r), row[1] = from_f32<T>(o.y * r), row[2] = from_f32<T>(o.z * r), row[3] = from_f32<T>(o.w * r);
+  }
 }
 
 // delta_i = sum_d dout o of every query row: one warp a row.
@@ -439,6 +503,19 @@ int general_pieces(int64_t B, int64_t Tq, int64_t Tk, int64_t Hq, int64_t Hk, in
   return (int)(p < 1 ? 1 : p);
 }
 
+// Pieces of a query tile's walk: as many as give every SM eight blocks, of 128 keys at least
+// (2 x 777 rows of 12 heads over 1031 keys, 312 tiles, in us: 162 whole or up to four blocks
+// an SM, of which some SMs get one more than most; 151 with six, 134 with eight, 132 with
+// twelve).
+int fwd_pieces(int64_t B, int64_t Tq, int64_t Tk, int64_t Hq, int64_t n_seqs) {
+  if (Hq < 1 || B < 1 || Tq < 1) return 1;
+  const int64_t blocks = ((Tq + kOwn - 1) / kOwn + n_seqs) * B * Hq;
+  const int64_t walk = Tk / (n_seqs > 1 ? n_seqs : 1);
+  int64_t p = 8 * 152 / blocks;
+  p = p < walk / 128 ? p : walk / 128;
+  return (int)(p < 1 ? 1 : p);
+}
+
 template <typename K>
 cudaError_t allow_smem(K kernel, size_t bytes) {
   return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
@@ -451,8 +528,11 @@ cudaError_t general_fwd(const CrossArgs& a, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   const int on16 = rows_on_16(a.q, a.B, a.Tq, a.Hq) && rows_on_16(a.k, a.B, a.Tk, a.Hk) && rows_on_16(a.v, a.B, a.Tk, a.Hk);
   const int64_t tiles = (a.Tq + kOwn - 1) / kOwn + (a.cu_q ? a.n_seqs : 0);
-  cross_fwd_general<T, DP><<<dim3((unsigned)tiles, (unsigned)(a.B * a.Hq)), kThreads, smem, s>>>(a, on16);
-  return cudaGetLastError();
+  const int pieces = fwd_pieces(a.B, a.Tq, a.Tk, a.Hq, a.n_seqs);
+  const dim3 grid((unsigned)tiles, (unsigned)(a.B * a.Hq), (unsigned)pieces);
+  cross_fwd_general<T, DP><<<grid, kThreads, smem, s>>>(a, on16, pieces);
+  if (pieces == 1) return cudaGetLastError();
+  return launch_early(cross_join_general<T>, dim3(grid.x, grid.y, kOwn / 8), 256, 0, s, a, pieces);
 }
 
 template <typename T, int DP>
@@ -601,7 +681,7 @@ extern "C" {
 size_t cross_attn_workspace_bytes(int64_t B, int64_t Tq, int64_t Tk, int64_t Hq, int64_t Hk, int64_t D, int64_t n_seqs,
                                   int32_t backward) {
   if (B < 0 || Tq < 0 || Tk < 0 || Hq < 0 || Hk < 0 || D < 1 || D > kMixMaxDim || n_seqs < 0) return 0;
-  if (!backward) return kWsHeaderBytes;
+  if (!backward) return kWsHeaderBytes + pieces_floats(B, Tq, Hq, D, fwd_pieces(B, Tq, Tk, Hq, n_seqs)) * 4;
   const size_t tc = cross_tc_bwd_floats(B, Tq, Tk, Hq, D, n_seqs);
   const int pieces = general_pieces(B, Tq, Tk, Hq, Hk, n_seqs);
   const size_t general = pieces > 1 ? (size_t)pieces * 2 * (size_t)(B * Tk * Hk * D) : 0;
@@ -624,6 +704,7 @@ scan_status cross_attn_fwd(const scan_view4* q, const scan_view4* k, const scan_
   if (Tk > 0) a.k = *k, a.v = *v;
   a.o = *o;
   a.lse = lse;
+  a.ws = a.delta;
   const cudaError_t e = cross_tc_fits(a, dt, false) ? launch_cross_tc_fwd(a, stream)
                                                     : launch_cross_general_fwd(a, dt, stream);
   return e == cudaSuccess ? SCAN_OK : SCAN_ERR_CUDA;

@@ -65,6 +65,22 @@ __device__ __forceinline__ void check_cross(const int32_t* lens, const int32_t* 
   }
 }
 
+// A kernel that is launched while the one before it runs, whose end it waits for itself.
+template <typename... P, typename... A>
+cudaError_t launch_early(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t s, A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 cudaError_t launch_cross_general_fwd(const CrossArgs& a, scan_dtype dt, cudaStream_t s);
 cudaError_t launch_cross_general_bwd(const CrossArgs& a, scan_dtype dt, cudaStream_t s);
 

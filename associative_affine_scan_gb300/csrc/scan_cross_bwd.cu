@@ -956,22 +956,6 @@ __global__ void __launch_bounds__(256) cross_parts_kernel(const __grid_constant_
                                                   pack_bf16(s[1].x * f, s[1].y * f), pack_bf16(s[1].z * f, s[1].w * f));
 }
 
-// A kernel that is launched while the one before it runs, whose end it waits for itself.
-template <typename... P, typename... A>
-cudaError_t launch_early(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t s, A... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, args...);
-}
-
 template <int DP, bool TWO>
 cudaError_t launch_bwd(const BwdArgs& t, unsigned blocks, cudaStream_t s) {
   using P = Plan<DP>;

@@ -442,17 +442,7 @@ cudaError_t launch_step(const StepArgs& t, unsigned grid, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   cross_step_kernel<DP><<<grid, kThreads, Plan<DP>::kSmem, s>>>(t);
   if (grid == 1) return cudaGetLastError();
-  // launched while the first kernel runs, whose end it waits for itself
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(256);
-  cfg.stream = s;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, cross_step_parts_kernel, t, (int)grid);
+  return launch_early(cross_step_parts_kernel, dim3(grid), 256, 0, s, t, (int)grid);
 }
 
 // Blocks: no more than there can be tiles.
