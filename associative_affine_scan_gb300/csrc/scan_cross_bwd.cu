@@ -82,12 +82,13 @@ __device__ __forceinline__ uint32_t rest_bf16(uint32_t h, float a, float b) {
   return pack_bf16(a - __uint_as_float(h << 16), b - __uint_as_float(h & 0xffff0000u));
 }
 
-// d (+)= A B over DP columns of K-major tiles, or over 64 rows of an MN-major tile with A
-// in tensor memory; by the elected lane.
+// d (+)= A B over 16 `steps` columns of K-major tiles, or over 64 rows of an MN-major tile
+// with A in tensor memory; by the elected lane.
 template <int DP>
-__device__ __forceinline__ void issue_kk(uint32_t d, uint32_t a, uint32_t b, uint32_t desc) {
+__device__ __forceinline__ void issue_kk(uint32_t d, uint32_t a, uint32_t b, uint32_t desc, int steps) {
 #pragma unroll
   for (int c = 0; c < DP / 16; ++c) {
+    if (c >= steps) break;
     const uint32_t step = (c / 4) * (kHalf >> 4) + (c % 4) * 2;
     mma_ss1(d, a + step, b + step, desc, c > 0);
   }
@@ -198,6 +199,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_dq_kernel(const __grid_cons
   const uint32_t base = (smem_addr(raw) + 1023) & ~1023u;
   uint8_t* const gen = raw + (base - smem_addr(raw));
   const int tid = threadIdx.x, warp = (int)uniform(tid / 32), lane = tid % 32;
+  const int steps = (a.D + 15) / 16;  // what D leaves of the DP columns is neither multiplied nor summed
   const uint32_t sQ = base, sD = base + P::kTileBytes, sR = base + 2 * P::kTileBytes;
   uint32_t* const misc = reinterpret_cast<uint32_t*>(gen + (2 + NS) * P::kTileBytes);
   const uint32_t bars = smem_addr(misc);
@@ -283,7 +285,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_dq_kernel(const __grid_cons
   } else if (warp == 9) {
     // ---- products: S, two tiles ahead, and dq += dS k
     constexpr uint32_t dS = product_desc(128, 128, false, false);
-    constexpr uint32_t dO = product_desc(128, DP, false, true);
+    const uint32_t dO = product_desc(128, 16 * steps, false, true);
     uint32_t s = 0, items = 0;  // scores issued, items begun
     int left = 0;               // tiles of the current item whose scores are to come
     bool more = true;
@@ -298,7 +300,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_dq_kernel(const __grid_cons
       if (!(ok = full(2 * s))) return;
       const uint32_t k = uniform(kmajor(sR) + (2 * s % NS) * (P::kTileBytes >> 4)), d = tS + 128 * (s & 1);
       if (elect()) {
-        issue_kk<DP>(d, kmajor(sQ), k, dS);
+        issue_kk<DP>(d, kmajor(sQ), k, dS, steps);
         commit1(bS + 8 * (s & 1));
       }
       __syncwarp();
@@ -349,7 +351,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_dq_kernel(const __grid_cons
         if (t > 0 && !(ok = warp_wait(bRead, (t - 1) & 1, stop))) break;  // the last dP has been read
         fence_after();
         if (elect()) {
-          issue_kk<DP>(tDp, kmajor(sD), v, dS);
+          issue_kk<DP>(tDp, kmajor(sD), v, dS, steps);
           commit1(bDp);
         }
         __syncwarp();
@@ -587,6 +589,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_dkv_kernel(const __grid_con
   const uint32_t base = (smem_addr(raw) + 1023) & ~1023u;
   uint8_t* const gen = raw + (base - smem_addr(raw));
   const int tid = threadIdx.x, warp = (int)uniform(tid / 32), lane = tid % 32;
+  const int steps = (a.D + 15) / 16;  // what D leaves of the DP columns is neither multiplied nor summed
   const uint32_t sK = base, sV = base + P::kTileBytes, sR = base + 2 * P::kTileBytes;
   uint32_t* const misc = reinterpret_cast<uint32_t*>(gen + (2 + NS) * P::kTileBytes);
   const uint32_t bars = smem_addr(misc);
@@ -689,7 +692,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_dkv_kernel(const __grid_con
     // of the next (warp 10)
     const int x = warp - 9;
     constexpr uint32_t dS = product_desc(128, 128, false, false);
-    constexpr uint32_t dO = product_desc(128, DP, false, true);
+    const uint32_t dO = product_desc(128, 16 * steps, false, true);
     const uint32_t first = x ? tDp : tS, second = x ? tDk : tDv, own = kmajor(x ? sV : sK);
     const uint32_t bFirst = x ? bDp : bS, bSecond = x ? bDs : bP;
     uint32_t t = 0, seen = 0;
@@ -700,7 +703,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_dkv_kernel(const __grid_con
         if (!full(2 * c + x)) return false;
         const uint32_t rows = uniform(kmajor(sR) + ((2 * c + x) % NS) * (P::kTileBytes >> 4));
         if (elect()) {
-          issue_kk<DP>(first, own, rows, dS);
+          issue_kk<DP>(first, own, rows, dS, steps);
           commit1(bFirst);
         }
         __syncwarp();

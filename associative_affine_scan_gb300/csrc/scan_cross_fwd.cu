@@ -181,7 +181,9 @@ __global__ void __launch_bounds__(kThreads, 1) cross_fwd_kernel(const __grid_con
       // next, which may be the next pair's first
       const int x = warp - 9;
       constexpr uint32_t dS = product_desc(128, 128, false, false);
-      constexpr uint32_t dO = product_desc(128, DP, false, true);
+      // what D leaves of the DP columns is neither multiplied nor summed
+      const int steps = (a.D + 15) / 16;
+      const uint32_t dO = product_desc(128, 16 * steps, false, true);
       const uint32_t p = tm + 128 * x, o = tm + 256 + 128 * x, q = kmajor(sQ) + x * (P::kTileBytes >> 4);
       uint32_t kv = 0, t = 0, seen = 1;  // copies used, tiles of keys so far, pairs so far
       int64_t i = blockIdx.x;
@@ -198,7 +200,8 @@ __global__ void __launch_bounds__(kThreads, 1) cross_fwd_kernel(const __grid_con
         if (elect()) {
 #pragma unroll
           for (int c = 0; c < DP / 16; ++c) {
-            if (turn && c == DP / 16 - 2) bar_arrive(bTurn + 8 * (x ^ 1));
+            if (c >= steps) break;
+            if (turn && c == (steps > 2 ? steps - 2 : 0)) bar_arrive(bTurn + 8 * (x ^ 1));
             const uint32_t step = (c / 4) * (kHalf >> 4) + (c % 4) * 2;
             mma_ss1(p, q + step, k + step, dS, c > 0);
           }
