@@ -55,6 +55,7 @@ struct BwdArgs {
   int64_t B, Tq, Tk;
   int64_t tiles, items;  // query tiles of a (batch row, head), and of all
   int n_seqs, Hq, Hk, G, D;
+  int order;          // query tiles: the longest sequences first
   int wide, wide_kv;  // rows of dq, and of dk and dv, are on 32 bytes
   float sl2, scale;
 };
@@ -181,7 +182,18 @@ struct Item {
   int b, h, hk;
   int n;  // tiles of keys
 };
-__device__ __forceinline__ bool item_at(const BwdArgs& a, int64_t i, Item* w) {
+__device__ __forceinline__ bool item_at(const BwdArgs& a, const Order& order, int64_t i, Item* w) {
+  if (a.order) {
+    int64_t unit, tile;
+    int s;
+    if (!order.find(i, a.Hq, &s, &unit, &tile)) return false;
+    w->g = rows_of(a.lens, a.cu_q, a.cu_k, a.Tq, a.Tk, s, tile * kRows);
+    w->b = a.cu_q ? 0 : s;
+    w->h = (int)unit;
+    w->hk = w->h / a.G;
+    w->n = (int)((w->g.nk + kRows - 1) / kRows);
+    return true;
+  }
   const int64_t unit = i / a.tiles, tile = i - unit * a.tiles;
   w->b = (int)(unit / a.Hq);
   w->h = (int)(unit % a.Hq);
@@ -209,6 +221,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_dq_kernel(const __grid_cons
   uint32_t* const tmem_ptr = misc + 64;
   uint32_t* const stop_flag = misc + 65;
   float* const s_row = reinterpret_cast<float*>(misc + 72);  // a row's sum of p dP, of each half of the columns
+  Order& order = *reinterpret_cast<Order*>(misc + 332);
 
   if (warp == 8 && lane == 0) {
     *stop_flag = 0;
@@ -233,6 +246,8 @@ __global__ void __launch_bounds__(kThreads, 1) cross_dq_kernel(const __grid_cons
     bar_init_fence();
   }
   if (warp == 9) tmem_alloc(smem_addr(tmem_ptr), 512);
+  if (a.order && warp == 10)
+    order.make(a.lens, a.cu_q, a.cu_k, a.n_seqs, a.B, a.Tq, a.Tk, kRows, a.Hq);
   fence_before();
   __syncthreads();
   fence_after();
@@ -243,12 +258,12 @@ __global__ void __launch_bounds__(kThreads, 1) cross_dq_kernel(const __grid_cons
   Item w;
   const auto full = [&](uint32_t c) { return warp_wait(bFull + 8 * (c % NS), (c / NS) & 1, stop); };
   // the next item with keys
-  int64_t at = blockIdx.x;
+  int64_t round = 0;
   const auto next_item = [&]() {
-    for (; at < a.items; at += gridDim.x)
-      if (item_at(a, at, &w) && w.n > 0) break;
-    const bool some = __any_sync(0xffffffffu, at < a.items);
-    at += gridDim.x;
+    for (; item_of(round, a.order) < a.items; ++round)
+      if (item_at(a, order, item_of(round, a.order), &w) && w.n > 0) break;
+    const bool some = __any_sync(0xffffffffu, item_of(round, a.order) < a.items);
+    ++round;
     return some;
   };
 
@@ -308,7 +323,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_dq_kernel(const __grid_cons
       ++s;
     };
     // which tiles begin and end an item: a second walk, two tiles behind
-    int64_t back_at = blockIdx.x;
+    int64_t back_round = 0;
     Item bw;
     int back_left = 0;
     scores();
@@ -316,9 +331,9 @@ __global__ void __launch_bounds__(kThreads, 1) cross_dq_kernel(const __grid_cons
     for (uint32_t t = 0; ok && t < s; ++t) {
       const bool begin = back_left == 0;
       if (begin) {
-        for (; back_at < a.items; back_at += gridDim.x)
-          if (item_at(a, back_at, &bw) && bw.n > 0) break;
-        back_at += gridDim.x;
+        for (; item_of(back_round, a.order) < a.items; ++back_round)
+          if (item_at(a, order, item_of(back_round, a.order), &bw) && bw.n > 0) break;
+        ++back_round;
         back_left = (int)uniform(bw.n);
       }
       const bool end = --back_left == 0;
@@ -363,8 +378,8 @@ __global__ void __launch_bounds__(kThreads, 1) cross_dq_kernel(const __grid_cons
     const int x = warp / 4, r = tid - 128 * x;
     const uint32_t lanes = (uint32_t)(warp % 4) << 21;
     uint32_t t = 0, items = 0, single = 0;
-    for (int64_t i = blockIdx.x; ok && i < a.items; i += gridDim.x) {
-      if (!item_at(a, i, &w)) continue;
+    for (int64_t round = 0; ok && item_of(round, a.order) < a.items; ++round) {
+      if (!item_at(a, order, item_of(round, a.order), &w)) continue;
       const int64_t row = w.g.t0 + r;
       const bool live = row < w.g.nq;
       __nv_bfloat16* const out = a.dqp + w.b * a.dq_sb + (w.g.qbeg + row) * a.dq_st + w.h * a.dq_sh;
@@ -1018,6 +1033,7 @@ cudaError_t launch_cross_tc_bwd(const CrossArgs& a, cudaStream_t s) {
   t.hdr = a.hdr;
   t.B = a.B, t.Tq = a.Tq, t.Tk = a.Tk;
   t.n_seqs = a.n_seqs;
+  t.order = orders(a.lens, a.cu_q, a.n_seqs, a.B);
   t.Hq = a.Hq, t.Hk = a.Hk, t.G = a.Hq / a.Hk, t.D = a.D;
   t.tiles = (a.Tq + kRows - 1) / kRows + (a.cu_q ? a.n_seqs : 0);
   t.items = t.tiles * a.B * a.Hq;

@@ -68,6 +68,7 @@ struct FwdArgs {
   int64_t B, Tq, Tk;
   int64_t tiles, items;  // pairs of query tiles of a (batch row, head or two), and of all
   int n_seqs, Hq, G;
+  int order;      // the longest sequences first
   int two_heads;  // the two tiles are two heads' (else 256 rows of one)
   int D;
   int wide;  // rows of outputs are on 32 bytes
@@ -78,7 +79,7 @@ template <int DP>
 struct Plan {
   static constexpr int kTileBytes = kRows * DP * 2;
   static constexpr int kSlots = fwd_slots(DP);
-  static constexpr int kSmem = (2 + kSlots) * kTileBytes  + 1024 + 512;
+  static constexpr int kSmem = (2 + kSlots) * kTileBytes + 1024 + 1024;
 };
 
 // A pair of query tiles.
@@ -88,14 +89,24 @@ struct Item {
   int n;  // tiles of keys
 };
 // False: there is no such pair. A whole warp.
-__device__ __forceinline__ bool item_at(const FwdArgs& a, int64_t i, Item* w) {
+__device__ __forceinline__ bool item_at(const FwdArgs& a, const Order& order, int64_t i, Item* w) {
+  const int units = a.two_heads ? a.Hq / 2 : a.Hq, rows = a.two_heads ? kRows : 2 * kRows;
+  if (a.order) {
+    int64_t unit, tile;
+    int s;
+    if (!order.find(i, units, &s, &unit, &tile)) return false;
+    w->g = rows_of(a.lens, a.cu_q, a.cu_k, a.Tq, a.Tk, s, tile * rows);
+    w->b = a.cu_q ? 0 : s;
+    w->h0 = (int)unit * (a.two_heads ? 2 : 1);
+    w->hk = w->h0 / a.G;
+    w->n = (int)((w->g.nk + kRows - 1) / kRows);
+    return true;
+  }
   const int64_t unit = i / a.tiles, tile = i - unit * a.tiles;
-  const int units = a.two_heads ? a.Hq / 2 : a.Hq;
   w->b = (int)(unit / units);
   w->h0 = (int)(unit % units) * (a.two_heads ? 2 : 1);
   w->hk = w->h0 / a.G;
-  if (!cross_rows(a.lens, a.cu_q, a.cu_k, a.n_seqs, a.Tq, a.Tk, w->b, tile, a.two_heads ? kRows : 2 * kRows, false, &w->g))
-    return false;
+  if (!cross_rows(a.lens, a.cu_q, a.cu_k, a.n_seqs, a.Tq, a.Tk, w->b, tile, rows, false, &w->g)) return false;
   w->n = (int)((w->g.nk + kRows - 1) / kRows);
   return true;
 }
@@ -115,6 +126,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_fwd_kernel(const __grid_con
                  bP = bS + 16, bO = bP + 16, bTurn = bO + 16;
   uint32_t* const tmem_ptr = misc + 96;
   uint32_t* const stop_flag = tmem_ptr + 1;
+  Order& order = *reinterpret_cast<Order*>(misc + 100);
 
   if (warp == 8 && lane == 0) {
     *stop_flag = 0;
@@ -134,6 +146,9 @@ __global__ void __launch_bounds__(kThreads, 1) cross_fwd_kernel(const __grid_con
   }
   if (warp == 9) tmem_alloc(smem_addr(tmem_ptr), 512);
   if (blockIdx.x == 0 && warp == 0) check_cross(a.lens, a.cu_q, a.cu_k, a.n_seqs, a.B, a.Tq, a.Tk, a.hdr);
+  if (a.order && warp == 10)
+    order.make(a.lens, a.cu_q, a.cu_k, a.n_seqs, a.B, a.Tq, a.Tk, a.two_heads ? kRows : 2 * kRows,
+               a.two_heads ? a.Hq / 2 : a.Hq);
   fence_before();
   __syncthreads();
   fence_after();
@@ -147,8 +162,8 @@ __global__ void __launch_bounds__(kThreads, 1) cross_fwd_kernel(const __grid_con
     if (warp == 8) {
       // ---- copies: keys (kv even) and values of tile after tile through the ring
       uint32_t kv = 0, seen = 0;  // copies so far, pairs of query tiles so far
-      for (int64_t i = blockIdx.x; ok && i < a.items; i += gridDim.x) {
-        if (!item_at(a, i, &w) || w.n == 0) continue;
+      for (int64_t r = 0; ok && item_of(r, a.order) < a.items; ++r) {
+        if (!item_at(a, order, item_of(r, a.order), &w) || w.n == 0) continue;
         if (lane == 0) {
           const auto load = [&](int u) {
             const uint32_t sl = kv % NS;
@@ -186,12 +201,12 @@ __global__ void __launch_bounds__(kThreads, 1) cross_fwd_kernel(const __grid_con
       const uint32_t dO = product_desc(128, 16 * steps, false, true);
       const uint32_t p = tm + 128 * x, o = tm + 256 + 128 * x, q = kmajor(sQ) + x * (P::kTileBytes >> 4);
       uint32_t kv = 0, t = 0, seen = 1;  // copies used, tiles of keys so far, pairs so far
-      int64_t i = blockIdx.x;
+      int64_t round = 0;
       const auto next_item = [&]() {
-        for (; i < a.items; i += gridDim.x)
-          if (item_at(a, i, &w) && w.n > 0) break;
-        const bool some = __any_sync(0xffffffffu, i < a.items);
-        i += gridDim.x;
+        for (; item_of(round, a.order) < a.items; ++round)
+          if (item_at(a, order, item_of(round, a.order), &w) && w.n > 0) break;
+        const bool some = __any_sync(0xffffffffu, item_of(round, a.order) < a.items);
+        ++round;
         return some;
       };
       const auto full = [&](uint32_t c) { return warp_wait_here(bFull + 8 * (c % NS), (c / NS) & 1, stop); };
@@ -256,8 +271,8 @@ __global__ void __launch_bounds__(kThreads, 1) cross_fwd_kernel(const __grid_con
     uint32_t t = 0, kv = 0, seen = 0;
     
 
-    for (int64_t i = blockIdx.x; ok && i < a.items; i += gridDim.x) {
-      if (!item_at(a, i, &w)) continue;
+    for (int64_t round = 0; ok && item_of(round, a.order) < a.items; ++round) {
+      if (!item_at(a, order, item_of(round, a.order), &w)) continue;
       float m = 0.f, l = 0.f;
       for (int u = 0; u < w.n; ++u, ++t, kv += 2) {
         const int here = w.g.nk - (int64_t)u * kRows < kRows ? (int)(w.g.nk - (int64_t)u * kRows) : kRows;  // keys
@@ -454,6 +469,7 @@ cudaError_t launch_cross_tc_fwd(const CrossArgs& a, cudaStream_t s) {
   t.Hq = a.Hq;
   t.G = a.Hq / a.Hk;
   t.two_heads = t.G % 2 == 0;
+  t.order = orders(a.lens, a.cu_q, a.n_seqs, a.B);
   t.D = a.D;
   t.wide = rows_on_32(a.o, a.B, a.Tq, a.Hq, a.D);
   t.sl2 = a.scale * 1.44269504088896341f;
