@@ -19,6 +19,10 @@
 // different banks both as rows (q k) and as columns (p v): the summed index of the
 // second product runs over the keys in the order in which the first one's results lie
 // with the threads.
+// fp32, 2 x 777 queries, 1031 keys, 12 heads of 64 over 4: 134 us, 37 TFLOP/s of fp32
+// products (fp32 arithmetic would take 66 us at its peak). Bound by instruction issue and its
+// waits: each warp splits the tile's factors for itself, and products are a ninth of its
+// instructions (44 % of what the tensor cores do in this form).
 #include "scan_cross.h"
 #include "scan_cross_tc.h"
 

@@ -16,10 +16,18 @@
 //            so P and dS (bf16, over S and dP in tensor memory) are read as they lie by the
 //            second products. Encoders have few tiles of keys, each with many queries: the
 //            (key tile, query tile) pairs are dealt out in order to one block an SM, equal
-//            shares each. A key tile that a share's end cuts leaves its parts in the
+//            shares of the work each. A key tile that a share's end cuts leaves its parts in the
 //            workspace (at most two a block), which a last kernel adds in order.
 // Either kernel issues the products of its two chains from two warps, so that one's waits
 // and commits are under the other's products.
+//
+// 4 x 4096 queries over 1280 to 2048 keys, 16 heads of 128 over 4: row sums 25 us (DRAM, 5.4
+// TB/s), queries 246 us (three products, 1.36 PFLOP/s), keys 347 us (four, 1.29 PFLOP/s),
+// parts 12 us.
+// Bound by a pair of tiles' chain: the softmax of S, dS from dP, and their handing over and
+// back leave the tensor cores idle for a quarter to a third of the time. Shorter rows are
+// bound by the tiles' beginnings and ends (seven packed sequences of 46 to 1314 keys, 12
+// heads of 96: row sums 8 us, queries 40 us, keys 52 us, parts 8 us).
 #include "scan_cross_phases.h"
 #include "scan_cross_tc.h"
 #include "scan_tc.cuh"
@@ -500,19 +508,23 @@ __global__ void __launch_bounds__(kThreads, 1) cross_dq_kernel(const __grid_cons
 
 // The (key tile, query tile) pairs in the order that they are dealt out: sequence by
 // sequence, key head by key head, tile by tile of its keys, then of its queries over
-// the heads that share them. A tile without a pair counts as one.
+// the heads that share them. What is dealt out in equal shares are turns: a pair is one, a
+// tile's beginning and end are three more, ahead of its pairs (12 heads of 96: 1.4 us a pair,
+// 4 us a beginning and end; seven packed sequences of 46 to 1314 keys, dealt out by pairs
+// alone 75 us, so 52 us), and a tile without a pair is one.
+constexpr int kEnds = 3;
 struct KeyTile {
   CrossRows g;     // t0: its first key row
-  int64_t first;   // number of its first pair
+  int64_t first;   // its first turn
   int64_t tile;    // within the sequence and head
   int64_t tiles;   // of the sequence and head (dense: of the whole row)
   int64_t live;    // those with pairs
   int seq, hk;
   int n;           // its pairs, 0 for a tile without
   int per;         // query tiles of a head
-  __device__ int64_t last() const { return first + (n > 0 ? n : 1); }
+  __device__ int64_t last() const { return first + (n > 0 ? n + kEnds : 1); }
 };
-// Rows, tiles and pairs of sequence i.
+// Rows, tiles and turns of sequence i.
 __device__ __forceinline__ void sequence(const BwdArgs& a, int i, KeyTile* w) {
   CrossRows& g = w->g;
   if (a.cu_q) {
@@ -532,22 +544,23 @@ __device__ __forceinline__ void sequence(const BwdArgs& a, int i, KeyTile* w) {
   w->per = (int)((g.nq + kRows - 1) / kRows);
   w->live = g.nq > 0 ? (g.nk + kRows - 1) / kRows : 0;
 }
-__device__ __forceinline__ int64_t pairs_of(const BwdArgs& a, const KeyTile& w) {  // of one key head
-  return w.live * (int64_t)w.per * a.G + (w.tiles - w.live);
+__device__ __forceinline__ int64_t deep(const BwdArgs& a, const KeyTile& w) { return (int64_t)w.per * a.G + kEnds; }
+__device__ __forceinline__ int64_t turns_of(const BwdArgs& a, const KeyTile& w) {  // of one key head
+  return w.live * deep(a, w) + (w.tiles - w.live);
 }
 __device__ __forceinline__ void place(const BwdArgs& a, KeyTile* w) {
   w->g.t0 = w->tile * kRows;
   w->n = w->tile < w->live ? w->per * a.G : 0;
 }
-// The tile that holds pair `p`, or (p < 0) the number of all pairs. A whole warp.
-__device__ __forceinline__ int64_t find_pair(const BwdArgs& a, int64_t p, KeyTile* w) {
+// The tile that holds turn `p`, or (p < 0) the number of all turns. A whole warp.
+__device__ __forceinline__ int64_t find_turn(const BwdArgs& a, int64_t p, KeyTile* w) {
   const int lane = threadIdx.x & 31, n = a.cu_q ? a.n_seqs : (int)a.B;
   int64_t before = 0;
   for (int i0 = 0; i0 < n; i0 += 32) {
     int64_t mine = 0;
     if (i0 + lane < n) {
       sequence(a, i0 + lane, w);
-      mine = pairs_of(a, *w) * a.Hk;
+      mine = turns_of(a, *w) * a.Hk;
     }
     int64_t upto = mine;
     for (int d = 1; d < 32; d <<= 1) {
@@ -559,15 +572,15 @@ __device__ __forceinline__ int64_t find_pair(const BwdArgs& a, int64_t p, KeyTil
       const int src = __ffs(who) - 1;
       before += __shfl_sync(0xffffffffu, upto - mine, src);
       sequence(a, i0 + src, w);
-      const int64_t head = pairs_of(a, *w), deep = (int64_t)w->per * a.G;
+      const int64_t head = turns_of(a, *w), d = deep(a, *w);
       w->hk = (int)((p - before) / head);
       before += w->hk * head;
       const int64_t in = p - before;
-      if (in < w->live * deep) {
-        w->tile = in / deep;
-        w->first = before + w->tile * deep;
+      if (in < w->live * d) {
+        w->tile = in / d;
+        w->first = before + w->tile * d;
       } else {
-        w->tile = w->live + (in - w->live * deep);
+        w->tile = w->live + (in - w->live * d);
         w->first = p;
       }
       place(a, w);
@@ -589,9 +602,9 @@ __device__ __forceinline__ void next_tile(const BwdArgs& a, KeyTile* w) {
   }
   place(a, w);
 }
-// How many blocks share `all` pairs, and block c's first.
+// How many blocks share `all` turns, and block c's first.
 __device__ __forceinline__ int64_t sharers(int64_t all, int64_t blocks) {
-  const int64_t n = (all + 1) / 2;  // two pairs each at least: a tile's beginning and end cost as much
+  const int64_t n = (all + kEnds + 1) / (kEnds + 2);  // two pairs each at least
   return n < blocks ? n : blocks;
 }
 __device__ __forceinline__ int64_t share(int64_t all, int64_t n, int64_t c) { return all / n * c + (all % n) * c / n; }
@@ -644,12 +657,12 @@ __global__ void __launch_bounds__(kThreads, 1) cross_dkv_kernel(const __grid_con
   asm volatile("griddepcontrol.launch_dependents;");  // the last kernel's blocks come beside this one's
   if (tid == 0) a.cut[blockIdx.x].parts = 0;
 
-  // this block's pairs [p0, p1), and its walk over them: key tile by key tile, pairs [u0, u1) of each
+  // this block's turns [p0, p1), and its walk over them: key tile by key tile, pairs [u0, u1) of each
   KeyTile w;
-  const int64_t all = find_pair(a, -1, &w), blocks = sharers(all, gridDim.x);
+  const int64_t all = find_turn(a, -1, &w), blocks = sharers(all, gridDim.x);
   const int64_t p0 = blockIdx.x < blocks ? share(all, blocks, blockIdx.x) : 0;
   const int64_t p1 = blockIdx.x < blocks ? share(all, blocks, blockIdx.x + 1) : 0;
-  if (p0 < p1) find_pair(a, p0, &w);
+  if (p0 < p1) find_turn(a, p0, &w);
   int u0 = 0, u1 = 0;
   bool begun = false;
   // the next tile with pairs (any: of those without, too)
@@ -662,9 +675,10 @@ __global__ void __launch_bounds__(kThreads, 1) cross_dkv_kernel(const __grid_con
         return false;
       }
       begun = true;
-      u0 = (int)uniform(w.first < p0 ? (uint32_t)(p0 - w.first) : 0u);
-      u1 = (int)uniform(w.last() > p1 ? (uint32_t)(p1 - w.first) : (uint32_t)w.n);
-      if (any || w.n > 0) return true;
+      const int64_t pairs = w.first + kEnds;  // from here on
+      u0 = (int)uniform(pairs < p0 ? (uint32_t)(p0 - pairs) : 0u);
+      u1 = (int)uniform(w.last() <= p1 ? (uint32_t)w.n : pairs < p1 ? (uint32_t)(p1 - pairs) : 0u);
+      if (w.n > 0 ? u0 < u1 : any) return true;
     }
   };
   const auto more = [&](bool any) { return __any_sync(0xffffffffu, step(any)); };

@@ -26,8 +26,8 @@
 // the others between them. The next pair's keys and queries are copied and its first
 // scores formed while this one's outputs are written.
 //
-// 4 x 4096 queries, 1500 keys, 16 heads of 128: 154 us, 1.31 PFLOP/s; 4096 keys: 348 us,
-// 1.58 PFLOP/s. Bound by the chain of a tile: 1000 cycles of products, 1340 of softmax
+// 4 x 4096 queries, 1500 keys, 16 heads of 128: 156 us, 1.29 PFLOP/s; 4096 keys: 354 us,
+// 1.55 PFLOP/s. Bound by the chain of a tile: 1000 cycles of products, 1340 of softmax
 // (512 of them the special-function unit's) and 600 to 700 of handing over, against
 // 2 x 1000 of tensor time for the pair; a pair's beginning and end cost another 5500.
 #include "scan_cross_phases.h"

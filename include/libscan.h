@@ -687,9 +687,14 @@ scan_status window_attn_step(const scan_view4* q, const scan_view4* k, const sca
  *   device status to SCAN_ERR_SEQLENS (and are clamped).
  *   A query that has no key has o = 0, lse = -inf. lse: fp32 [B, Hq, Tq], the log of
  *   each row's sum of exponentials, written.
- * Statistics and sums are fp32. Keys and values past a row's length are never used,
- * whatever they hold; values within have to be finite. An output must not overlap an
- * input or another output.
+ * Statistics and sums are fp32. bf16 operands on 16-byte boundaries with strides of
+ * whole 16 bytes (and none of 0) take the tensor cores: the weights, and in the backward
+ * their gradients, are rounded to bf16 before the second product, each by half a step at
+ * most (the gradients in two parts where rows have 512 keys or fewer on average, since
+ * few terms do not average a rounding out). All other operands take the general kernels,
+ * whose products are of fp32 accuracy (each factor as the sum of two tf32 numbers).
+ * Keys and values past a row's length are never used, whatever they hold; values within
+ * have to be finite. An output must not overlap an input or another output.
  * workspace: cross_attn_workspace_bytes() (n_seqs = 0 unless packed, backward != 0 for
  * the backward's), zeroed once with scan_workspace_init. SCAN_ERR_UNSUPPORTED unless D
  * is a multiple of 8 up to 128 and B Hq <= 65535; SCAN_ERR_INVALID_ARG unless Hq % Hk
@@ -723,7 +728,8 @@ scan_status cross_attn_bwd(const scan_view4* q, const scan_view4* k, const scan_
  *   [n_slots], the keys that each cache holds (forced into [0, Tk]), else Tk; slots:
  *   int32 [B], the cache of each request, or NULL (request b has cache b). Requests may
  *   share a cache. A slot outside [0, n_slots) marks an idle request, which gets o = 0,
- *   as one without keys does. Rows past a length are never used.
+ *   as one without keys does. Rows past a length are never used. bf16 caches on 16-byte
+ *   boundaries are read by tensor copies, the weights rounded to bf16 as in the forward.
  * workspace: cross_attn_step_workspace_bytes(), zeroed once with scan_workspace_init;
  * nothing is kept in it between calls but its status word. */
 size_t cross_attn_step_workspace_bytes(int64_t B, int64_t Tk, int64_t Hq, int64_t Hk, int64_t D);
