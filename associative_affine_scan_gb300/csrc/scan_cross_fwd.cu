@@ -228,7 +228,6 @@ __global__ void __launch_bounds__(kThreads, 1) cross_fwd_kernel(const __grid_con
       int left = (int)uniform(w.n);
       bool add = false;
       if (more && (ok = warp_wait_here(bQ, 0, stop) && full(0))) scores(kmajor(sKV), false);
-      
 
       while (ok && more) {
         const uint32_t v = uniform(mnmajor(sKV, kHalf) + ((kv + 1) % NS) * (P::kTileBytes >> 4));
@@ -258,7 +257,6 @@ __global__ void __launch_bounds__(kThreads, 1) cross_fwd_kernel(const __grid_con
         if (more) scores(k, true);
         ++t;
       }
-      
 
     }
   } else {
@@ -267,10 +265,8 @@ __global__ void __launch_bounds__(kThreads, 1) cross_fwd_kernel(const __grid_con
     const int x = warp / 4, r = tid - 128 * x;
     const uint32_t lanes = (uint32_t)(warp % 4) << 21;
     const uint32_t tS = tm + 128 * x + lanes, tO = tm + 256 + 128 * x + lanes;
-    
-    uint32_t t = 0, kv = 0, seen = 0;
-    
 
+    uint32_t t = 0, kv = 0, seen = 0;
     for (int64_t round = 0; ok && item_of(round, a.order) < a.items; ++round) {
       if (!item_at(a, order, item_of(round, a.order), &w)) continue;
       float m = 0.f, l = 0.f;
@@ -416,7 +412,6 @@ __global__ void __launch_bounds__(kThreads, 1) cross_fwd_kernel(const __grid_con
         a.lse[((int64_t)w.b * a.Hq + h) * a.Tq + w.g.qbeg + row] =
             l == 0.f ? -INFINITY : (m + log2f(l)) * 0.693147180559945309f;
     }
-    
 
   }
   __syncwarp();

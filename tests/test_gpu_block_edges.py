@@ -181,6 +181,33 @@ def test_many_sequences_and_heads(lib):
     cross_check(lib, inputs(70, 3, 9, 2, 1, 64, BF, 2), lens=torch.randint(0, 10, (70,), generator=g).to(torch.int32).to(DEV))
 
 
+@pytest.mark.parametrize("mode", ["plain", "odd"])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_walks_that_are_cut(lib, dtype, mode):
+    """Few queries and many keys, whose walks are cut into pieces (or shares): padded rows of
+    lengths at the pieces' ends, none and one, packed pairs with empty sequences."""
+    cross_check(lib, inputs(4, 40, 900, 4, 2, 64, dtype, 1), lens=ints(900, 0, 1, 130), mode=mode)
+    cross_check(lib, inputs(1, 200, 1500, 3, 1, 96, dtype, 2), cu_q=ints(0, 50, 50, 90, 200),
+                cu_k=ints(0, 900, 901, 901, 1500), mode=mode)
+    q, k, v, _ = inputs(1, 65, 1000, 2, 1, 128, dtype, 3)
+    a, b = (lib.cross_attn_fwd(q, k, v, scale=0.1) for _ in range(2))
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+def test_few_queries_of_many_key_tiles(lib):
+    """Key tiles of one or two pairs each, so that shares end within a tile's beginning."""
+    for B, Tq, Tk, Hq, Hk in ((1, 5, 20000, 2, 1), (1, 200, 9000, 1, 1), (3, 1, 5000, 4, 4)):
+        q, k, v, do = inputs(B, Tq, Tk, Hq, Hk, 64, BF, Tk)
+        o, lse = lib.cross_attn_fwd(q, k, v)
+        got = lib.cross_attn_bwd(q, k, v, o, lse, do)
+        want, _ = ref.cross_grads(f64(q), f64(k), f64(v), f64(do), 64 ** -0.5, ref.spans(B, Tq, Tk))
+        # in the 2-norm: an output's rounding 2^-9.2, p's or ds's the same, delta's of o's
+        for a, b in zip(got, want):
+            assert float((f64(a) - b).norm() / b.norm()) <= 2 ** -8
+        again = lib.cross_attn_bwd(q, k, v, o, lse, do)
+        assert all(torch.equal(a, b) for a, b in zip(got, again))
+
+
 def test_long_rows(lib):
     """One head, tens of thousands of keys or queries, against 64 bits on the GPU."""
     for Tq, Tk in ((130, 40000), (40000, 130)):

@@ -71,6 +71,19 @@ def test_prompt_and_tokens_equal_whole_rows(lib, dtype, tol):
     assert rel <= tol and norm > 0, (rel, norm)
 
 
+def test_norms_without_an_encoder(lib):
+    import hybrid_mixer
+    mixer = hybrid_mixer.HybridMixer(layers=2, channels=256, heads=4, key_heads=2, window=32, norms=True)
+    x = torch.randn(2, 110, 256, generator=torch.Generator().manual_seed(3)).to("cuda")
+    with torch.no_grad():
+        whole = mixer(x)
+    y, cache = mixer.prompt(x[:, :100], torch.tensor([1, 0], dtype=torch.int32, device="cuda"))
+    got = torch.cat([y] + [mixer.token(x[:, 100 + i], cache)[:, None] for i in range(10)], 1)
+    assert float((got - whole).double().norm() / whole.double().norm()) <= 2e-2
+    with pytest.raises(ValueError):
+        hybrid_mixer.HybridMixer(layers=1, channels=256, heads=4, key_heads=2, context=True)
+
+
 # The gradients pass the roundings on the way back as well: three times the forward's.
 @pytest.mark.parametrize("dtype,tol", [(torch.bfloat16, 6e-2), (torch.float32, 3e-4)])
 def test_training_step_against_plain(lib, dtype, tol):
