@@ -372,10 +372,11 @@ __global__ void __launch_bounds__(256) cross_delta_general(const CrossArgs a, in
   if (threadIdx.x % 32 == 0) a.delta[(b * a.Hq + h) * a.Tq + t] = s;
 }
 
-// A tile of queries against every key.
+// A tile of queries against the keys, or a piece of them (blockIdx.z).
 template <typename T, int DP>
-__global__ void __launch_bounds__(kThreads) cross_dq_general(const CrossArgs a, int on16) {
+__global__ void __launch_bounds__(kThreads) cross_dq_general(const CrossArgs a, int on16, int pieces) {
   extern __shared__ float4 raw[];
+  asm volatile("griddepcontrol.launch_dependents;");
   float *const sq = reinterpret_cast<float*>(raw), *const sd = sq + kOwn * kPitch<DP>, *const tiles = sd + kOwn * kPitch<DP>;
   CrossRows g;
   const int h = blockIdx.y % a.Hq, hk = h / (a.Hq / a.Hk);
@@ -393,17 +394,19 @@ __global__ void __launch_bounds__(kThreads) cross_dq_general(const CrossArgs a, 
     lse[y] = t < g.nq ? a.lse[at] : INFINITY;
     delta[y] = t < g.nq ? a.delta[at] : 0.f;
   }
+  const int64_t all = (g.nk + kOther - 1) / kOther, first = all * blockIdx.z / pieces, last = all * (blockIdx.z + 1) / pieces;
   walk<DP, 2>(
-      tiles, (g.nk + kOther - 1) / kOther,
+      tiles, last - first,
       [&](float* x, float* y, int64_t i) {
-        load_rows<T, DP, kOther>(x, k, b, g.kbeg + i * kOther, g.kbeg + g.nk, hk, a.D, on16);
-        load_rows<T, DP, kOther>(y, v, b, g.kbeg + i * kOther, g.kbeg + g.nk, hk, a.D, on16);
+        const int64_t t = g.kbeg + (first + i) * kOther;
+        load_rows<T, DP, kOther>(x, k, b, t, g.kbeg + g.nk, hk, a.D, on16);
+        load_rows<T, DP, kOther>(y, v, b, t, g.kbeg + g.nk, hk, a.D, on16);
       },
       [&](const float* sk, const float* sv, int64_t i) {
         float s[kOther / 8][4] = {}, dp[kOther / 8][4] = {};
         rows_by_rows<DP>(s, sq + 16 * warp * kPitch<DP>, sk, a.D);
         rows_by_rows<DP>(dp, sd + 16 * warp * kPitch<DP>, sv, a.D);
-        const int64_t left = g.nk - i * kOther;
+        const int64_t left = g.nk - (first + i) * kOther;
 #pragma unroll
         for (int j = 0; j < kOther / 8; ++j)
 #pragma unroll
@@ -414,7 +417,34 @@ __global__ void __launch_bounds__(kThreads) cross_dq_general(const CrossArgs a, 
         weights_by_columns<DP>(dq, s, sk, a.D);
       });
   const float f[2] = {a.scale, a.scale};
-  write_rows<T, DP>(vw<T>(a.dq), dq, b, g.qbeg + g.t0 + 16 * warp, g.qbeg + g.nq, h, a.D, f);
+  const int64_t t0 = g.qbeg + g.t0 + 16 * warp;
+  if (pieces > 1) {
+    const View<float> part{a.ws + blockIdx.z * (a.B * a.Hq * a.Tq * a.D), a.Hq * a.Tq * a.D, a.D, a.Tq * a.D};
+    write_rows<float, DP>(part, dq, b, t0, g.qbeg + g.nq, h, a.D, f);
+  } else {
+    write_rows<T, DP>(vw<T>(a.dq), dq, b, t0, g.qbeg + g.nq, h, a.D, f);
+  }
+}
+
+// The pieces of dq, added in order: a warp a row, four columns a lane; eight blocks a tile.
+template <typename T>
+__global__ void __launch_bounds__(256) cross_dq_join_general(const CrossArgs a, int pieces) {
+  CrossRows g;
+  const int h = blockIdx.y % a.Hq, c = threadIdx.x % 32 * 4;
+  const int64_t b = blockIdx.y / a.Hq;
+  const bool any = cross_rows(a.lens, a.cu_q, a.cu_k, a.n_seqs, a.Tq, a.Tk, b, blockIdx.x, kOwn, false, &g);
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int64_t t = g.t0 + 8 * blockIdx.z + threadIdx.x / 32;
+  if (!any || t >= g.nq || c >= a.D) return;
+  const float* const from = a.ws + ((b * a.Hq + h) * a.Tq + g.qbeg + t) * a.D + c;
+  float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int z = 0; z < pieces; ++z) {
+    const float4 e = *reinterpret_cast<const float4*>(from + z * (a.B * a.Hq * a.Tq * a.D));
+    s.x += e.x, s.y += e.y, s.z += e.z, s.w += e.w;
+  }
+  T* const row = vw<T>(a.dq).row(b, g.qbeg + t, h) + c;
+  row[0] = from_f32<T>(s.x), row[1] = from_f32<T>(s.y), row[2] = from_f32<T>(s.z), row[3] = from_f32<T>(s.w);
 }
 
 // A tile of keys against every query, over the heads that share it, or one of `pieces`
@@ -510,7 +540,8 @@ int general_pieces(int64_t B, int64_t Tq, int64_t Tk, int64_t Hq, int64_t Hk, in
 // Pieces of a query tile's walk: as many as give every SM eight blocks, of 128 keys at least
 // (2 x 777 rows of 12 heads over 1031 keys, 312 tiles, in us: 162 whole or up to four blocks
 // an SM, of which some SMs get one more than most; 151 with six, 134 with eight, 132 with
-// twelve).
+// twelve). Of dq as well (900 queries of five packed sequences over 3000 keys, 8 heads of
+// 96, forward and backward: 584 us with dq whole, 387 so).
 int fwd_pieces(int64_t B, int64_t Tq, int64_t Tk, int64_t Hq, int64_t n_seqs) {
   if (Hq < 1 || B < 1 || Tq < 1) return 1;
   const int64_t blocks = ((Tq + kOwn - 1) / kOwn + n_seqs) * B * Hq;
@@ -551,7 +582,13 @@ cudaError_t general_bwd(const CrossArgs& a, cudaStream_t s) {
   const int64_t tq = (a.Tq + kOwn - 1) / kOwn + extra, tk = (a.Tk + kOwn - 1) / kOwn + extra;
   if (rows > 0) {
     cross_delta_general<T><<<(unsigned)((rows + 7) / 8), 256, 0, s>>>(a, rows);
-    cross_dq_general<T, DP><<<dim3((unsigned)tq, (unsigned)(a.B * a.Hq)), kThreads, smem, s>>>(a, on16);
+    const int parts = fwd_pieces(a.B, a.Tq, a.Tk, a.Hq, a.n_seqs);
+    const dim3 grid((unsigned)tq, (unsigned)(a.B * a.Hq), (unsigned)parts);
+    cross_dq_general<T, DP><<<grid, kThreads, smem, s>>>(a, on16, parts);
+    if (parts > 1) {
+      e = launch_early(cross_dq_join_general<T>, dim3(grid.x, grid.y, kOwn / 8), 256, 0, s, a, parts);
+      if (e != cudaSuccess) return e;
+    }
   }
   if (a.Tk < 1) return cudaGetLastError();
   const int pieces = general_pieces(a.B, a.Tq, a.Tk, a.Hq, a.Hk, a.n_seqs);
@@ -688,7 +725,10 @@ size_t cross_attn_workspace_bytes(int64_t B, int64_t Tq, int64_t Tk, int64_t Hq,
   if (!backward) return kWsHeaderBytes + pieces_floats(B, Tq, Hq, D, fwd_pieces(B, Tq, Tk, Hq, n_seqs)) * 4;
   const size_t tc = cross_tc_bwd_floats(B, Tq, Tk, Hq, D, n_seqs);
   const int pieces = general_pieces(B, Tq, Tk, Hq, Hk, n_seqs);
-  const size_t general = pieces > 1 ? (size_t)pieces * 2 * (size_t)(B * Tk * Hk * D) : 0;
+  const int parts = fwd_pieces(B, Tq, Tk, Hq, n_seqs);  // of dq, in the same place before
+  const size_t of_dq = parts > 1 ? (size_t)parts * (size_t)(B * Hq * Tq * D) : 0;
+  size_t general = pieces > 1 ? (size_t)pieces * 2 * (size_t)(B * Tk * Hk * D) : 0;
+  if (of_dq > general) general = of_dq;
   return kWsHeaderBytes + round_up((size_t)(B * Hq * Tq) * 4, 256) + (tc > general ? tc : general) * 4;
 }
 
