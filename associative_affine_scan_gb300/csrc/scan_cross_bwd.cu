@@ -86,11 +86,6 @@ __device__ __forceinline__ void clear_rows(uint32_t tile, int from, int t) {
   __syncwarp();
 }
 
-// What a pair of bf16 numbers leaves of the numbers they were rounded from, as bf16.
-__device__ __forceinline__ uint32_t rest_bf16(uint32_t h, float a, float b) {
-  return pack_bf16(a - __uint_as_float(h << 16), b - __uint_as_float(h & 0xffff0000u));
-}
-
 // d (+)= A B over 16 `steps` columns of K-major tiles, or over 64 rows of an MN-major tile
 // with A in tensor memory; by the elected lane.
 template <int DP>

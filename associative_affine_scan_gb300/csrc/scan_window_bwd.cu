@@ -76,11 +76,6 @@ __device__ __forceinline__ void clear_rows(uint32_t tile, int from, int t) {
   __syncwarp();
 }
 
-// What a pair of bf16 numbers leaves of the numbers they were rounded from, as bf16.
-__device__ __forceinline__ uint32_t rest_bf16(uint32_t h, float a, float b) {
-  return pack_bf16(a - __uint_as_float(h << 16), b - __uint_as_float(h & 0xffff0000u));
-}
-
 // A row of D fp32 sums in tensor memory times f, as bf16: to a tile in shared
 // memory, or straight to `out`.
 template <int DP>

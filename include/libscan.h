@@ -729,7 +729,8 @@ scan_status cross_attn_bwd(const scan_view4* q, const scan_view4* k, const scan_
  *   int32 [B], the cache of each request, or NULL (request b has cache b). Requests may
  *   share a cache. A slot outside [0, n_slots) marks an idle request, which gets o = 0,
  *   as one without keys does. Rows past a length are never used. bf16 caches on 16-byte
- *   boundaries are read by tensor copies, the weights rounded to bf16 as in the forward.
+ *   boundaries are read by tensor copies, the weights of their values the sum of two bf16
+ *   numbers each (2^-16 of themselves).
  * workspace: cross_attn_step_workspace_bytes(), zeroed once with scan_workspace_init;
  * nothing is kept in it between calls but its status word. */
 size_t cross_attn_step_workspace_bytes(int64_t B, int64_t Tk, int64_t Hq, int64_t Hk, int64_t D);
