@@ -666,9 +666,8 @@ scan_status cross_sizes(int64_t B, int64_t Tq, int64_t Tk, int64_t Hq, int64_t H
   if (!(scale > 0.f) || !(scale < INFINITY)) return SCAN_ERR_INVALID_ARG;
   if (Hk == 0 ? Hq != 0 : Hq % Hk != 0) return SCAN_ERR_INVALID_ARG;
   if (D > kMixMaxDim || D % 8) return SCAN_ERR_UNSUPPORTED;
-  if (Hq > 65535 || B > 65535 || B * Hq > 65535 || Tq > 0x7fffffffLL || Tk > 0x7fffffffLL)
-    return SCAN_ERR_UNSUPPORTED;
-  if (B * Hq * Tq > (1LL << 33)) return SCAN_ERR_UNSUPPORTED;  // blocks of the row sums
+  if (Tq > 0x7fffffffLL || Tk > 0x7fffffffLL) return SCAN_ERR_UNSUPPORTED;
+  if (B > 0x7fffffffLL || Hq > 0x7fffffffLL || B * Hq > 0x7fffffffLL) return SCAN_ERR_UNSUPPORTED;  // a grid's blocks
   return SCAN_OK;
 }
 
@@ -677,6 +676,8 @@ scan_status cross_common(CrossArgs* a, const int32_t* lens, const int32_t* cu_q,
                          scan_dtype dt) {
   const scan_status st = cross_sizes(B, Tq, Tk, Hq, Hk, D, scale, dt);
   if (st != SCAN_OK) return st;
+  if (B * Hq > 65535) return SCAN_ERR_UNSUPPORTED;             // a grid's second axis
+  if (B * Hq * Tq > (1LL << 33)) return SCAN_ERR_UNSUPPORTED;  // blocks of the row sums
   if (n_seqs < 0 || !cu_q != !cu_k || (cu_q && lens)) return SCAN_ERR_INVALID_ARG;
   if (cu_q && (B != 1 || (n_seqs == 0 && Tq + Tk > 0))) return SCAN_ERR_INVALID_ARG;
   *a = CrossArgs{};

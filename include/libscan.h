@@ -732,7 +732,8 @@ scan_status cross_attn_bwd(const scan_view4* q, const scan_view4* k, const scan_
  *   boundaries are read by tensor copies, the weights of their values the sum of two bf16
  *   numbers each (2^-16 of themselves).
  * workspace: cross_attn_step_workspace_bytes(), zeroed once with scan_workspace_init;
- * nothing is kept in it between calls but its status word. */
+ * nothing is kept in it between calls but its status word. Errors as the forward's, but
+ * B Hq may be up to 2^31 - 1. */
 size_t cross_attn_step_workspace_bytes(int64_t B, int64_t Tk, int64_t Hq, int64_t Hk, int64_t D);
 scan_status cross_attn_step(const scan_view4* q, const scan_view4* k_cache,
                             const scan_view4* v_cache, const int32_t* lens, const int32_t* slots,

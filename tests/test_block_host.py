@@ -196,3 +196,17 @@ def test_formulas_against_autograd():
     got, _ = ref.cross_grads(*(t.detach() for t in (q, k, v)), do, 0.6, ref.spans(2, 7, 9, lens))
     for a, b in zip(got, want):
         assert torch.allclose(a, b)
+
+
+def test_steps_of_many_heads(lib):
+    """Single tokens are no blocks of a grid's second axis: 1024 requests of 64 heads pass the
+    checks of sizes (and are refused for their workspace)."""
+    step = lambda B, Hq, Hk, dt: lib.cross_attn_step(  # noqa: E731
+        V, V, V, P, P, 4, V, B, 50, Hq, Hk, 64, 1.0, dt, P, 16, None)
+    for dt in (0, 1):
+        assert step(1024, 64, 8, dt) == WORKSPACE
+        assert step(1, 1 << 20, 1, dt) == WORKSPACE
+        assert step(1 << 26, 32, 8, dt) == UNSUPPORTED
+        assert step(1 << 40, 1, 1, dt) == UNSUPPORTED
+        assert step(1, 1 << 40, 1, dt) == UNSUPPORTED
+    assert cross(lib, B=1, Hq=1 << 17, nws=16) == UNSUPPORTED

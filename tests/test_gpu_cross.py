@@ -256,3 +256,26 @@ def test_values_that_are_no_numbers_show(lib):
     rest = torch.ones_like(got, dtype=torch.bool)
     rest[0, 7, 1] = False
     assert torch.equal(got[rest], want[rest])
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_step_of_more_heads_than_a_grid_has_rows(lib, dtype):
+    """Requests times heads just above 65535, over a few shared caches."""
+    g = gen(21)
+    B, Hq, Hk, D, N, Tk = 16387, 4, 2, 64, 5, 40
+    q = normal(g, B, Hq, D, dtype=dtype)
+    kc, vc = (normal(g, N, Tk, Hk, D, dtype=dtype) for _ in range(2))
+    lens = [40, 1, 0, 33, 17]
+    slots = torch.randint(-1, N + 1, (B,), generator=g).to(torch.int32)
+    o = lib.cross_attn_step(q, kc, vc, ints(*lens), slots.to(DEV))
+    o, q64 = f64(o), f64(q)
+    for s in range(-1, N + 1):
+        at = slots == s
+        if not 0 <= s < N or lens[s] == 0:
+            assert float(o[at].abs().max()) == 0.0
+            continue
+        kk, vv = (f64(x[s, :lens[s]]).repeat_interleave(Hq // Hk, 1) for x in (kc, vc))
+        w = torch.softmax(torch.einsum("bhd,nhd->bhn", q64[at], kk) * D ** -0.5, -1)
+        smag = max(1.0, float(q64[at].norm(dim=-1).max() * kk.norm(dim=-1).max()) * D ** -0.5)
+        gate(o[at], torch.einsum("bhn,nhd->bhd", w, vv), torch.einsum("bhn,nhd->bhd", w, vv.abs()), dtype=dtype,
+             roundings=1 if dtype == BF else 0, terms=lens[s] + D + 2 * D * smag, name=f"cache {s}")
