@@ -86,6 +86,14 @@ __device__ __forceinline__ void clear_rows(uint32_t tile, int from, int t) {
   __syncwarp();
 }
 
+// Whether dS goes to its products as the sum of two bf16 parts: its rounding to one adds as
+// much to dq and dk as their own does (0.0024 of them in the 2-norm, 0.0017 with two), at any
+// number of keys. The second part's products make four of the queries' kernel's three, and
+// five of the keys' four. So sequences of few keys, whose pairs of tiles are a small part of
+// the time, take two. By the sequence's own keys: its gradients do not depend on what else is
+// in the batch, or on what that is padded to.
+__device__ __forceinline__ bool two_parts(const CrossRows& g) { return g.nk <= 512; }
+
 // d (+)= A B over 16 `steps` columns of K-major tiles, or over 64 rows of an MN-major tile
 // with A in tensor memory; by the elected lane.
 template <int DP>
@@ -206,7 +214,7 @@ __device__ __forceinline__ bool item_at(const BwdArgs& a, const Order& order, in
   return true;
 }
 
-template <int DP, bool TWO>
+template <int DP>
 __global__ void __launch_bounds__(kThreads, 1) cross_dq_kernel(const __grid_constant__ BwdArgs a) {
   using P = Plan<DP>;
   constexpr int NS = P::kSlots;
@@ -329,6 +337,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_dq_kernel(const __grid_cons
     int64_t back_round = 0;
     Item bw;
     int back_left = 0;
+    bool two = false;
     scores();
     if (ok && more) scores();
     for (uint32_t t = 0; ok && t < s; ++t) {
@@ -338,6 +347,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_dq_kernel(const __grid_cons
           if (item_at(a, order, item_of(back_round, a.order), &bw) && bw.n > 0) break;
         ++back_round;
         back_left = (int)uniform(bw.n);
+        two = uniform(two_parts(bw.g)) != 0;
       }
       const bool end = --back_left == 0;
       const uint32_t k = uniform(mnmajor(sR, kHalf) + (2 * t % NS) * (P::kTileBytes >> 4)), d = tS + 128 * (t & 1);
@@ -346,7 +356,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_dq_kernel(const __grid_cons
       if (elect()) {
         issue_tn64(tDq, d, k, dO, !begin);
         issue_tn64(tDq, d + 64, k + (64 * kPitch >> 4), dO, true);
-        if (TWO) {
+        if (two) {
           issue_tn64(tDq, d + 32, k, dO, true);
           issue_tn64(tDq, d + 96, k + (64 * kPitch >> 4), dO, true);
         }
@@ -393,6 +403,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_dq_kernel(const __grid_cons
       const int64_t st = ((int64_t)w.b * a.Hq + w.h) * a.Tq + w.g.qbeg + row;
       const float lse = live ? a.lse[st] * 1.44269504088896341f : INFINITY;
       float delta = live && w.n > 1 ? a.delta[st] : 0.f;
+      const bool two = two_parts(w.g);
       for (int u = 0; u < w.n; ++u, ++t) {
         const int here = w.g.nk - (int64_t)u * kRows < kRows ? (int)(w.g.nk - (int64_t)u * kRows) : kRows;  // keys
         if (!(ok = warp_wait(bS + 8 * (t & 1), (t >> 1) & 1, stop))) break;
@@ -458,8 +469,8 @@ __global__ void __launch_bounds__(kThreads, 1) cross_dq_kernel(const __grid_cons
           if (x == 0 && live) a.delta[st] = delta;
         }
         // dS goes to its product as bf16, the type that the tensor cores take next to bf16
-        // operands: off by 2^-9 of itself at most (TWO: as two parts, off by 2^-18)
-        uint32_t o[32], rest[TWO ? 32 : 1];
+        // operands: off by 2^-8 of itself at most (as two parts, by 2^-16)
+        uint32_t o[32];
         const float2 less = make_float2(-delta, -delta);
 #pragma unroll
         for (int c = 0; c < 2; ++c)
@@ -467,10 +478,15 @@ __global__ void __launch_bounds__(kThreads, 1) cross_dq_kernel(const __grid_cons
           for (int j = 0; j < 32; j += 2) {
             const float2 e = mul2(pair_of(s[c] + j), add2(pair_of(d[c] + j), less));
             o[16 * c + j / 2] = pack_bf16(e.x, e.y);
-            if (TWO) rest[16 * c + j / 2] = rest_bf16(o[16 * c + j / 2], e.x, e.y);
+            s[c][j] = __float_as_uint(e.x), s[c][j + 1] = __float_as_uint(e.y);
           }
         tmem_st32(tS + 128 * (t & 1) + lanes + 64 * x, o);
-        if constexpr (TWO) tmem_st32(tS + 128 * (t & 1) + lanes + 64 * x + 32, rest);
+        if (two) {
+#pragma unroll
+          for (int j = 0; j < 32; ++j)
+            o[j] = rest_bf16(o[j], __uint_as_float(s[j / 16][2 * j % 32]), __uint_as_float(s[j / 16][2 * j % 32 + 1]));
+          tmem_st32(tS + 128 * (t & 1) + lanes + 64 * x + 32, o);
+        }
         if (!whole && (a.cu_q || a.lens))  // key rows past the sequence (their scores are done)
           clear_rows<DP>(sR + (2 * t % NS) * P::kTileBytes, here, tid);
         st_wait();
@@ -604,7 +620,7 @@ __device__ __forceinline__ int64_t sharers(int64_t all, int64_t blocks) {
 }
 __device__ __forceinline__ int64_t share(int64_t all, int64_t n, int64_t c) { return all / n * c + (all % n) * c / n; }
 
-template <int DP, bool TWO>
+template <int DP>
 __global__ void __launch_bounds__(kThreads, 1) cross_dkv_kernel(const __grid_constant__ BwdArgs a) {
   using P = Plan<DP>;
   constexpr int NS = P::kSlots;
@@ -722,6 +738,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_dkv_kernel(const __grid_con
     uint32_t t = 0, seen = 0;
     while (ok && more(false)) {
       const int n = u1 - u0;
+      const bool two = x == 1 && uniform(two_parts(w.g)) != 0;
       if (!(ok = warp_wait(bKV, seen & 1, stop))) break;
       const auto scores = [&](uint32_t c) {
         if (!full(2 * c + x)) return false;
@@ -743,7 +760,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_dkv_kernel(const __grid_con
         if (elect()) {
           issue_tn64(second, first, rows, dO, u > 0);
           issue_tn64(second, first + 64, rows + (64 * kPitch >> 4), dO, true);
-          if (TWO && x) {
+          if (two) {
             issue_tn64(second, first + 32, rows, dO, true);
             issue_tn64(second, first + 96, rows + (64 * kPitch >> 4), dO, true);
           }
@@ -795,6 +812,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_dkv_kernel(const __grid_con
     uint32_t t = 0, seen = 0;
     while (ok && more(true)) {
       const int n = w.n > 0 ? u1 - u0 : 0;
+      const bool two = two_parts(w.g);
       for (int u = 0; u < n; ++u, ++t) {
         const int64_t left = w.g.nq - (int64_t)((u0 + u) % w.per) * kRows;
         const int here = left < kRows ? (int)left : kRows;  // queries
@@ -831,8 +849,8 @@ __global__ void __launch_bounds__(kThreads, 1) cross_dkv_kernel(const __grid_con
         }
         {
           // P and, below, dS go to the products as bf16, the type that the tensor cores take
-          // next to bf16 operands: off by 2^-9 of themselves at most (TWO: dS as two parts, off
-          // by 2^-18). dS is formed from the P of 32 bits, and all sums are of 32 bits.
+          // next to bf16 operands: off by 2^-8 of themselves at most (dS as two parts, by
+          // 2^-16). dS is formed from the P of 32 bits, and all sums are of 32 bits.
           uint32_t o[32];
 #pragma unroll
           for (int c = 0; c < 2; ++c)
@@ -863,7 +881,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_dkv_kernel(const __grid_con
         }
         __syncwarp();
         ld_wait();
-        uint32_t o[32], rest[TWO ? 32 : 1];
+        uint32_t o[32];
 #pragma unroll
         for (int c = 0; c < 2; ++c)
 #pragma unroll
@@ -873,22 +891,26 @@ __global__ void __launch_bounds__(kThreads, 1) cross_dkv_kernel(const __grid_con
             const float2 z = mul2(pair_of(s[c] + j + 2), add2(pair_of(d[c] + j + 2), make_float2(-less.z, -less.w)));
             o[16 * c + j / 2] = pack_bf16(y.x, y.y);
             o[16 * c + j / 2 + 1] = pack_bf16(z.x, z.y);
-            if (TWO) {
-              rest[16 * c + j / 2] = rest_bf16(o[16 * c + j / 2], y.x, y.y);
-              rest[16 * c + j / 2 + 1] = rest_bf16(o[16 * c + j / 2 + 1], z.x, z.y);
-            }
+            s[c][j] = __float_as_uint(y.x), s[c][j + 1] = __float_as_uint(y.y);
+            s[c][j + 2] = __float_as_uint(z.x), s[c][j + 3] = __float_as_uint(z.y);
           }
-        if (!whole) {
+        const auto cut_off = [&]() {  // what lies past the queries may be anything
+          if (whole) return;
 #pragma unroll
           for (int j = 0; j < 32; ++j) {
             const int c = 64 * x + 2 * j;
-            const uint32_t keep = c + 1 < here ? 0xffffffffu : c < here ? 0xffffu : 0u;
-            o[j] &= keep;
-            if (TWO) rest[j] &= keep;
+            o[j] &= c + 1 < here ? 0xffffffffu : c < here ? 0xffffu : 0u;
           }
-        }
+        };
+        cut_off();
         tmem_st32(tDp + lanes + 64 * x, o);
-        if constexpr (TWO) tmem_st32(tDp + lanes + 64 * x + 32, rest);
+        if (two) {
+#pragma unroll
+          for (int j = 0; j < 32; ++j)
+            o[j] = rest_bf16(o[j], __uint_as_float(s[j / 16][2 * j % 32]), __uint_as_float(s[j / 16][2 * j % 32 + 1]));
+          cut_off();
+          tmem_st32(tDp + lanes + 64 * x + 32, o);
+        }
         if (!whole && a.cu_q) clear_rows<DP>(sR + (2 * t % NS) * P::kTileBytes, here, tid);
         st_wait();
         fence_before();
@@ -983,16 +1005,16 @@ __global__ void __launch_bounds__(256) cross_parts_kernel(const __grid_constant_
                                                   pack_bf16(s[1].x * f, s[1].y * f), pack_bf16(s[1].z * f, s[1].w * f));
 }
 
-template <int DP, bool TWO>
+template <int DP>
 cudaError_t launch_bwd(const BwdArgs& t, unsigned blocks, cudaStream_t s) {
   using P = Plan<DP>;
   static_assert(P::kSmem <= 232448, "fits a block's shared memory");
-  cudaError_t e = cudaFuncSetAttribute(cross_dkv_kernel<DP, TWO>, cudaFuncAttributeMaxDynamicSharedMemorySize, P::kSmem);
+  cudaError_t e = cudaFuncSetAttribute(cross_dkv_kernel<DP>, cudaFuncAttributeMaxDynamicSharedMemorySize, P::kSmem);
   if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(cross_dq_kernel<DP, TWO>, cudaFuncAttributeMaxDynamicSharedMemorySize, P::kSmem);
+    e = cudaFuncSetAttribute(cross_dq_kernel<DP>, cudaFuncAttributeMaxDynamicSharedMemorySize, P::kSmem);
   if (e != cudaSuccess) return e;
-  e = launch_early(cross_dq_kernel<DP, TWO>, dim3((unsigned)(t.items < kBlocks ? t.items : kBlocks)), kThreads, P::kSmem, s, t);
-  if (e == cudaSuccess) e = launch_early(cross_dkv_kernel<DP, TWO>, dim3(blocks), kThreads, P::kSmem, s, t);
+  e = launch_early(cross_dq_kernel<DP>, dim3((unsigned)(t.items < kBlocks ? t.items : kBlocks)), kThreads, P::kSmem, s, t);
+  if (e == cudaSuccess) e = launch_early(cross_dkv_kernel<DP>, dim3(blocks), kThreads, P::kSmem, s, t);
   if (e == cudaSuccess && blocks > 1)
     e = launch_early(cross_parts_kernel, dim3(blocks, (2 * kRows * t.D / 8 + 255) / 256), 256, 0, s, t);
   return e;
@@ -1003,14 +1025,6 @@ int64_t key_blocks(int64_t B, int64_t Tq, int64_t Tk, int64_t Hq, int64_t n_seqs
   const double q = (double)((Tq + kRows - 1) / kRows + n_seqs), k = (double)((Tk + kRows - 1) / kRows + n_seqs);
   const double most = (double)B * (double)Hq * q * k / 2. + 1.;
   return most < kBlocks ? (int64_t)most : kBlocks;
-}
-
-// Whether dS goes to its products as the sum of two bf16 parts. Past its first tile of
-// keys a row's delta comes from the output as it was rounded, which is felt where it sees
-// few keys; together with the rounding of dS it would be more than the gradients' own.
-// Short encoders so take the two parts; elsewhere one rounding is what is left.
-bool two_parts(const CrossArgs& a) {
-  return (a.cu_q ? a.Tk / a.n_seqs : a.Tk) <= 512;  // of a sequence, in the mean
 }
 
 }  // namespace
@@ -1061,9 +1075,7 @@ cudaError_t launch_cross_tc_bwd(const CrossArgs& a, cudaStream_t s) {
   d.D = a.D;
   d.rows = a.B * a.Tq * a.Hq;
   cross_delta_kernel<<<(unsigned)((d.rows + 63) / 64), 256, 0, s>>>(d);
-  const bool two = two_parts(a);
-  if (a.D <= 64) return two ? launch_bwd<64, true>(t, blocks, s) : launch_bwd<64, false>(t, blocks, s);
-  return two ? launch_bwd<128, true>(t, blocks, s) : launch_bwd<128, false>(t, blocks, s);
+  return a.D <= 64 ? launch_bwd<64>(t, blocks, s) : launch_bwd<128>(t, blocks, s);
 }
 
 }  // namespace scan

@@ -690,8 +690,8 @@ scan_status window_attn_step(const scan_view4* q, const scan_view4* k, const sca
  * Statistics and sums are fp32. bf16 operands on 16-byte boundaries with strides of
  * whole 16 bytes (and none of 0) take the tensor cores: the weights, and in the backward
  * their gradients, are rounded to bf16 before the second product, each by half a step at
- * most (the gradients in two parts where rows have 512 keys or fewer on average, since
- * few terms do not average a rounding out). All other operands take the general kernels,
+ * most (2^-8 of itself; the gradients in two parts, 2^-16, for a sequence or batch row of
+ * 512 keys or fewer, by its own length, where that takes little time). All other operands take the general kernels,
  * whose products are of fp32 accuracy (each factor as the sum of two tf32 numbers).
  * Keys and values past a row's length are never used, whatever they hold; values within
  * have to be finite. An output must not overlap an input or another output.
