@@ -503,6 +503,12 @@ __global__ void __launch_bounds__(V == 4 ? 256 : 128, V == 4 ? 1 : 3) residual_b
               g[i].y = keep[v] & 2u << 2 * i ? g[i].y * a.drop.scale : 0.f;
             }
           ey[v].get(x);
+          if (a.drop.limit && !a.w_post)  // what was dropped may have been anything (a norm would have taken it in)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              x[i].x = keep[v] & 1u << 2 * i ? x[i].x : 0.f;
+              x[i].y = keep[v] & 2u << 2 * i ? x[i].y : 0.f;
+            }
           held.take(own_w + (4 * v + 2) * apart, apart);
           held.get(w);
 #pragma unroll

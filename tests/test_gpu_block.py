@@ -218,6 +218,30 @@ def test_dropped_elements_are_zero_whatever_they_hold(lib):
         assert float(y.abs().max()) == 0.0
 
 
+@pytest.mark.parametrize("types", TYPES)
+@pytest.mark.parametrize("C", [64, 1000, 4104])
+@pytest.mark.parametrize("gated", ["none", "channel", "row"])
+def test_what_is_dropped_leaves_no_trace_in_the_gradients(lib, types, C, gated):
+    """Infinities and NaN of the block where its dropout falls (and no norm has taken them in
+    before): results and gradients are the same bits as with zeros there."""
+    st, dt = types
+    g = gen(C)
+    x, dxo = (normal(g, 2, 9, C, dtype=st) for _ in range(2))
+    y, dn = (normal(g, 2, 9, C, dtype=dt) for _ in range(2))
+    wn, gt = normal(g, C), {"none": None, "channel": normal(g, C), "row": normal(g, 2, C)}[gated]
+    kw = dict(p=0.3, rng=(8, 2), alpha=0.9)
+    gone = (ref.kept((2, 9, C), 0.3, (8, 2)) == 0).to(DEV)
+    odd = torch.tensor([NAN, float("inf"), -float("inf")], device=DEV)[torch.arange(2 * 9 * C, device=DEV) % 3].view(2, 9, C)
+    results = []
+    for fill in (torch.zeros_like(y), odd.to(dt)):
+        z = torch.where(gone, fill, y)
+        xo, n = lib.residual_norm_fwd(x, z, None, gt, wn, **kw)
+        results.append((xo, n, *lib.residual_norm_bwd(xo, z, dxo, dn, None, gt, wn, **kw)))
+    for a, b in zip(*results):
+        assert (a is None) == (b is None)
+        assert a is None or (torch.equal(a, b) and bool(a.isfinite().all()))
+
+
 def test_dropout_statistics(lib):
     """Of 2^22 elements the kept ones are a binomial number, those of other calls and seeds
     independent: five standard deviations."""
