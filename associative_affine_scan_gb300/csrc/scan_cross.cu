@@ -590,7 +590,7 @@ cudaError_t general_bwd(const CrossArgs& a, cudaStream_t s) {
       if (e != cudaSuccess) return e;
     }
   }
-  if (a.Tk < 1) return cudaGetLastError();
+  if (a.Tk < 1 || a.Hk < 1) return cudaGetLastError();
   const int pieces = general_pieces(a.B, a.Tq, a.Tk, a.Hq, a.Hk, a.n_seqs);
   cross_dkv_general<T, DP><<<dim3((unsigned)(tk * pieces), (unsigned)(a.B * a.Hk)), kThreads, smem, s>>>(a, on16, pieces);
   if (pieces > 1)
@@ -667,7 +667,8 @@ scan_status cross_sizes(int64_t B, int64_t Tq, int64_t Tk, int64_t Hq, int64_t H
   if (Hk == 0 ? Hq != 0 : Hq % Hk != 0) return SCAN_ERR_INVALID_ARG;
   if (D > kMixMaxDim || D % 8) return SCAN_ERR_UNSUPPORTED;
   if (Tq > 0x7fffffffLL || Tk > 0x7fffffffLL) return SCAN_ERR_UNSUPPORTED;
-  if (B > 0x7fffffffLL || Hq > 0x7fffffffLL || B * Hq > 0x7fffffffLL) return SCAN_ERR_UNSUPPORTED;  // a grid's blocks
+  const int64_t H = Hq > Hk ? Hq : Hk;  // (no query heads may read some key heads)
+  if (B > 0x7fffffffLL || H > 0x7fffffffLL || B * H > 0x7fffffffLL) return SCAN_ERR_UNSUPPORTED;  // a grid's blocks
   return SCAN_OK;
 }
 
@@ -676,7 +677,7 @@ scan_status cross_common(CrossArgs* a, const int32_t* lens, const int32_t* cu_q,
                          scan_dtype dt) {
   const scan_status st = cross_sizes(B, Tq, Tk, Hq, Hk, D, scale, dt);
   if (st != SCAN_OK) return st;
-  if (B * Hq > 65535) return SCAN_ERR_UNSUPPORTED;             // a grid's second axis
+  if (B * Hq > 65535 || B * Hk > 65535) return SCAN_ERR_UNSUPPORTED;  // a grid's second axis
   if (B * Hq * Tq > (1LL << 33)) return SCAN_ERR_UNSUPPORTED;  // blocks of the row sums
   if (n_seqs < 0 || !cu_q != !cu_k || (cu_q && lens)) return SCAN_ERR_INVALID_ARG;
   if (cu_q && (B != 1 || (n_seqs == 0 && Tq + Tk > 0))) return SCAN_ERR_INVALID_ARG;
@@ -764,13 +765,13 @@ scan_status cross_attn_bwd(const scan_view4* q, const scan_view4* k, const scan_
   CrossArgs a;
   scan_status st = cross_common(&a, k_lens, cu_seqlens_q, cu_seqlens_k, n_seqs, B, Tq, Tk, Hq, Hk, D, scale, dt);
   if (st != SCAN_OK) return st;
-  if (B * Hq * (Tq + Tk) == 0) return SCAN_OK;
-  if (Tq > 0 && (!given(q) || !given(o) || !given(dout) || !given(dq) || !lse)) return SCAN_ERR_INVALID_ARG;
-  if (Tk > 0 && (!given(k) || !given(v) || !given(dk) || !given(dv))) return SCAN_ERR_INVALID_ARG;
+  if (B * (Hq * Tq + Hk * Tk) == 0) return SCAN_OK;
+  if (Hq * Tq > 0 && (!given(q) || !given(o) || !given(dout) || !given(dq) || !lse)) return SCAN_ERR_INVALID_ARG;
+  if (Hk * Tk > 0 && (!given(k) || !given(v) || !given(dk) || !given(dv))) return SCAN_ERR_INVALID_ARG;
   st = cross_workspace(&a, workspace, workspace_bytes, cross_attn_workspace_bytes(B, Tq, Tk, Hq, Hk, D, a.n_seqs, 1));
   if (st != SCAN_OK) return st;
-  if (Tq > 0) a.q = *q, a.o = *o, a.dout = *dout, a.dq = *dq;
-  if (Tk > 0) a.k = *k, a.v = *v, a.dk = *dk, a.dv = *dv;
+  if (Hq * Tq > 0) a.q = *q, a.o = *o, a.dout = *dout, a.dq = *dq;
+  if (Hk * Tk > 0) a.k = *k, a.v = *v, a.dk = *dk, a.dv = *dv;
   a.lse = const_cast<float*>(lse);
   const cudaError_t e = cross_tc_fits(a, dt, true) ? launch_cross_tc_bwd(a, stream)
                                                    : launch_cross_general_bwd(a, dt, stream);

@@ -441,7 +441,7 @@ cudaError_t launch_fwd(const FwdArgs& t, unsigned grid, cudaStream_t s) {
 
 // bf16 operands that tensor copies can address.
 bool cross_tc_fits(const CrossArgs& a, scan_dtype dt, bool backward) {
-  if (dt != SCAN_BF16 || a.Tq < 1 || a.Tk < 1) return false;
+  if (dt != SCAN_BF16 || a.Tq < 1 || a.Tk < 1 || a.Hq < 1) return false;
   const auto q = [&](const scan_view4& v) { return heads_map_fits(v, a.B, a.Tq, a.Hq); };
   const auto k = [&](const scan_view4& v) { return heads_map_fits(v, a.B, a.Tk, a.Hk); };
   if (!q(a.q) || !k(a.k) || !k(a.v) || !q(a.o)) return false;

@@ -210,3 +210,14 @@ def test_steps_of_many_heads(lib):
         assert step(1 << 40, 1, 1, dt) == UNSUPPORTED
         assert step(1, 1 << 40, 1, dt) == UNSUPPORTED
     assert cross(lib, B=1, Hq=1 << 17, nws=16) == UNSUPPORTED
+
+
+def test_gradients_of_keys_without_query_heads(lib):
+    """They are written, so they and the workspace are asked for."""
+    bwd = lambda dk, nws, Tk=50, Hk=2, B=1: lib.cross_attn_bwd(  # noqa: E731
+        None, V, V, None, None, None, None, None, None, 0, None, dk, V, B, 64, Tk, 0, Hk, 64, 1.0, 1, P, nws, None)
+    assert bwd(NULL, 1 << 30) == INVALID
+    assert bwd(V, 16) == WORKSPACE
+    assert bwd(V, 1 << 30, B=40000) == UNSUPPORTED
+    assert bwd(V, 1 << 30, Hk=1 << 40) == UNSUPPORTED
+    assert bwd(NULL, 16, Tk=0) == OK and bwd(NULL, 16, Hk=0) == OK

@@ -279,3 +279,16 @@ def test_step_of_more_heads_than_a_grid_has_rows(lib, dtype):
         smag = max(1.0, float(q64[at].norm(dim=-1).max() * kk.norm(dim=-1).max()) * D ** -0.5)
         gate(o[at], torch.einsum("bhn,nhd->bhd", w, vv), torch.einsum("bhn,nhd->bhd", w, vv.abs()), dtype=dtype,
              roundings=1 if dtype == BF else 0, terms=lens[s] + D + 2 * D * smag, name=f"cache {s}")
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_no_query_heads(lib, dtype):
+    """Key heads that no query head reads, and key rows that no query does: their gradients are
+    sums of nothing, written."""
+    for Tq, Hq in ((5, 0), (0, 0), (0, 2)):
+        q, k, v, do = inputs(2, Tq, 70, Hq, 2, 64, dtype, 1)
+        o, lse = lib.cross_attn_fwd(q, k, v)
+        out = torch.empty_like(q), *(torch.full_like(t, NAN) for t in (k, v))
+        lib.cross_attn_bwd(q, k, v, o, lse, do, out=out)
+        assert all(float(t.abs().max()) == 0.0 for t in out[1:])
+    assert lib.scan_get_device_status() == lib.SCAN_OK
