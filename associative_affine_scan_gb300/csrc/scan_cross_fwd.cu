@@ -30,6 +30,8 @@
 // 1.55 PFLOP/s. Bound by the chain of a tile: 1000 cycles of products, 1340 of softmax
 // (512 of them the special-function unit's) and 600 to 700 of handing over, against
 // 2 x 1000 of tensor time for the pair; a pair's beginning and end cost another 5500.
+#include <atomic>
+
 #include "scan_cross_phases.h"
 #include "scan_cross_tc.h"
 #include "scan_tc.cuh"
@@ -424,14 +426,27 @@ __global__ void __launch_bounds__(kThreads, 1) cross_fwd_kernel(const __grid_con
   }
 }
 
+// Whether the kernel is launched with the registers that its warpgroups' shares are of: the
+// compiler's choice, of which the launch bounds are the upper limit. Asked once.
+template <int DP>
+cudaError_t shares_fit(bool* fit) {
+  static std::atomic<int> regs{0};
+  int n = regs.load(std::memory_order_relaxed);
+  if (n == 0) {
+    cudaFuncAttributes f;
+    const cudaError_t e = cudaFuncGetAttributes(&f, cross_fwd_kernel<DP>);
+    if (e != cudaSuccess) return e;
+    regs.store(n = f.numRegs, std::memory_order_relaxed);
+  }
+  *fit = n == kRegs;
+  return cudaSuccess;
+}
+
 template <int DP>
 cudaError_t launch_fwd(const FwdArgs& t, unsigned grid, cudaStream_t s) {
   static_assert(Plan<DP>::kSmem <= 232448, "fits a block's shared memory");
-  cudaFuncAttributes f;
-  cudaError_t e = cudaFuncGetAttributes(&f, cross_fwd_kernel<DP>);
-  if (e == cudaSuccess && f.numRegs != kRegs) e = cudaErrorInvalidConfiguration;
-  if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(cross_fwd_kernel<DP>, cudaFuncAttributeMaxDynamicSharedMemorySize, Plan<DP>::kSmem);
+  const cudaError_t e =
+      cudaFuncSetAttribute(cross_fwd_kernel<DP>, cudaFuncAttributeMaxDynamicSharedMemorySize, Plan<DP>::kSmem);
   if (e != cudaSuccess) return e;
   cross_fwd_kernel<DP><<<grid, kThreads, Plan<DP>::kSmem, s>>>(t);
   return cudaGetLastError();
@@ -449,6 +464,10 @@ bool cross_tc_fits(const CrossArgs& a, scan_dtype dt, bool backward) {
 }
 
 cudaError_t launch_cross_tc_fwd(const CrossArgs& a, cudaStream_t s) {
+  bool fit;
+  const cudaError_t e = a.D <= 64 ? shares_fit<64>(&fit) : shares_fit<128>(&fit);
+  if (e != cudaSuccess) return e;
+  if (!fit) return launch_cross_general_fwd(a, SCAN_BF16, s);  // built by a compiler that took other registers
   FwdArgs t;
   if (!encode_heads_map(&t.q, a.q, a.B, a.Tq, a.Hq, a.D, kRows) ||
       !encode_heads_map(&t.k, a.k, a.B, a.Tk, a.Hk, a.D, kRows) ||
