@@ -57,17 +57,23 @@ def cross_grads(q, k, v, dout, scale, seqs):
     return (dq, dk, dv), (mq, mk, mv)
 
 
-def numbers(n, seed, call):
-    """The generator's 16-bit numbers of elements 0 .. n - 1, in Python's whole numbers."""
+def philox(c, k):
+    """The four words of a counter of four and a key of two, after ten rounds, in Python's
+    whole numbers."""
+    c, k = list(c), list(k)
+    for _ in range(10):
+        a, b = c[0] * 0xD2511F53, c[2] * 0xCD9E8D57
+        c = [(b >> 32) ^ c[1] ^ k[0], b & 0xffffffff, (a >> 32) ^ c[3] ^ k[1], a & 0xffffffff]
+        k = [(k[0] + 0x9E3779B9) & 0xffffffff, (k[1] + 0xBB67AE85) & 0xffffffff]
+    return c
+
+
+def numbers(n, seed, call, first=0):
+    """The generator's 16-bit numbers of n elements from block `first` on."""
     out = []
-    for block in range((n + 7) // 8):
-        c = [block & 0xffffffff, block >> 32, call & 0xffffffff, call >> 32]
-        k = [seed & 0xffffffff, seed >> 32]
-        for _ in range(10):
-            a, b = c[0] * 0xD2511F53, c[2] * 0xCD9E8D57
-            c = [(b >> 32) ^ c[1] ^ k[0], b & 0xffffffff, (a >> 32) ^ c[3] ^ k[1], a & 0xffffffff]
-            k = [(k[0] + 0x9E3779B9) & 0xffffffff, (k[1] + 0xBB67AE85) & 0xffffffff]
-        for w in c:
+    for block in range(first, first + (n + 7) // 8):
+        for w in philox((block & 0xffffffff, block >> 32, call & 0xffffffff, call >> 32),
+                        (seed & 0xffffffff, seed >> 32)):
             out += [w & 0xffff, w >> 16]
     return torch.tensor(out[:n], dtype=torch.int64)
 

@@ -221,3 +221,19 @@ def test_gradients_of_keys_without_query_heads(lib):
     assert bwd(V, 1 << 30, B=40000) == UNSUPPORTED
     assert bwd(V, 1 << 30, Hk=1 << 40) == UNSUPPORTED
     assert bwd(NULL, 16, Tk=0) == OK and bwd(NULL, 16, Hk=0) == OK
+
+
+def test_generator_published_values():
+    """The three published test vectors of Philox 4x32 with ten rounds: zeros, ones, and the
+    digits of pi, whose words all differ, so that they hold the order of the counter's words (block,
+    then call, low word first) and of the key's (the seed, low word first)."""
+    for counter, key, want in (
+        ((0, 0, 0, 0), (0, 0), (0x6627e8d5, 0xe169c58d, 0xbc57ac4c, 0x9b00dbd8)),
+        ((0xffffffff,) * 4, (0xffffffff,) * 2, (0x408f276d, 0x41c83b0e, 0xa20bc7c6, 0x6d5451fd)),
+        ((0x243f6a88, 0x85a308d3, 0x13198a2e, 0x03707344), (0xa4093822, 0x299f31d0),
+         (0xd16cfe09, 0x94fdcceb, 0x5001e420, 0x24126ea1)),
+    ):
+        pair = lambda w: w[0] | w[1] << 32  # noqa: E731
+        block, call, seed = pair(counter[:2]), pair(counter[2:]), pair(key)
+        got = ref.numbers(8, seed, call, first=block).tolist()
+        assert got == [h for w in want for h in (w & 0xffff, w >> 16)]
