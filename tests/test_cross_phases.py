@@ -234,3 +234,13 @@ def test_the_check_finds_what_it_is_for():
     broken = queries([4], 5)
     broken.roles[3] = [op for op in broken.roles[3] if op[0] != "arrive" or broken.names[op[1]] != "read"]
     assert ("stuck",) in broken.faults()
+
+
+def test_an_odd_ring_is_taken_too_early():
+    """What goes wrong with an odd ring for the two groups is that one takes a place before it
+    has been filled, not that a role is stuck; rings of one copy more are sound."""
+    for n, places in ((9, 5), (9, 3)):
+        faults = step(n, places).faults()
+        assert any(f[0] == "early" and f[1][0] == "full" for f in faults), faults
+        assert ("stuck",) not in faults
+        assert not step(n, places + 1).faults()
