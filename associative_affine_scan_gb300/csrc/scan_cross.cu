@@ -559,14 +559,15 @@ cudaError_t allow_smem(K kernel, size_t bytes) {
 template <typename T, int DP>
 cudaError_t general_fwd(const CrossArgs& a, cudaStream_t s) {
   constexpr int smem = kSmem<DP, 1>;
-  const cudaError_t e = allow_smem(cross_fwd_general<T, DP>, smem);
+  cudaError_t e = allow_smem(cross_fwd_general<T, DP>, smem);
   if (e != cudaSuccess) return e;
   const int on16 = rows_on_16(a.q, a.B, a.Tq, a.Hq) && rows_on_16(a.k, a.B, a.Tk, a.Hk) && rows_on_16(a.v, a.B, a.Tk, a.Hk);
   const int64_t tiles = (a.Tq + kOwn - 1) / kOwn + (a.cu_q ? a.n_seqs : 0);
   const int pieces = fwd_pieces(a.B, a.Tq, a.Tk, a.Hq, a.n_seqs);
   const dim3 grid((unsigned)tiles, (unsigned)(a.B * a.Hq), (unsigned)pieces);
   cross_fwd_general<T, DP><<<grid, kThreads, smem, s>>>(a, on16, pieces);
-  if (pieces == 1) return cudaGetLastError();
+  e = cudaGetLastError();
+  if (e != cudaSuccess || pieces == 1) return e;
   return launch_early(cross_join_general<T>, dim3(grid.x, grid.y, kOwn / 8), 256, 0, s, a, pieces);
 }
 
@@ -585,6 +586,8 @@ cudaError_t general_bwd(const CrossArgs& a, cudaStream_t s) {
     const int parts = fwd_pieces(a.B, a.Tq, a.Tk, a.Hq, a.n_seqs);
     const dim3 grid((unsigned)tq, (unsigned)(a.B * a.Hq), (unsigned)parts);
     cross_dq_general<T, DP><<<grid, kThreads, smem, s>>>(a, on16, parts);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
     if (parts > 1) {
       e = launch_early(cross_dq_join_general<T>, dim3(grid.x, grid.y, kOwn / 8), 256, 0, s, a, parts);
       if (e != cudaSuccess) return e;

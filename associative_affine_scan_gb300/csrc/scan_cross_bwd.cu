@@ -1075,6 +1075,8 @@ cudaError_t launch_cross_tc_bwd(const CrossArgs& a, cudaStream_t s) {
   d.D = a.D;
   d.rows = a.B * a.Tq * a.Hq;
   cross_delta_kernel<<<(unsigned)((d.rows + 63) / 64), 256, 0, s>>>(d);
+  const cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
   return a.D <= 64 ? launch_bwd<64>(t, blocks, s) : launch_bwd<128>(t, blocks, s);
 }
 

@@ -459,11 +459,12 @@ cudaError_t launch_step(const StepArgs& t, unsigned grid, cudaStream_t s) {
       cudaFuncSetAttribute(cross_step_kernel<DP>, cudaFuncAttributeMaxDynamicSharedMemorySize, Plan<DP>::kSmem);
   if (e != cudaSuccess) return e;
   cross_step_kernel<DP><<<grid, kThreads, Plan<DP>::kSmem, s>>>(t);
-  if (grid == 1) return cudaGetLastError();
+  const cudaError_t made = cudaGetLastError();
+  if (made != cudaSuccess) return made;
   return launch_early(cross_step_parts_kernel, dim3(grid), 256, 0, s, t, (int)grid);
 }
 
-// Blocks: no more than there can be tiles.
+// Blocks: no more than there can be tiles, two at least.
 int64_t step_blocks(int64_t B, int64_t Tk, int64_t Hk, int64_t Hq) {
   const double rounds = Hk > 0 ? (double)((Hq / Hk + kHeads - 1) / kHeads) : 0.;
   const double most = (double)B * (double)Hk * rounds * (double)((Tk + kKeys - 1) / kKeys + 1);
