@@ -691,10 +691,15 @@ scan_status window_attn_step(const scan_view4* q, const scan_view4* k, const sca
  * whole 16 bytes (and none of 0) take the tensor cores: the weights, and in the backward
  * their gradients, are rounded to bf16 before the second product, each by half a step at
  * most (2^-8 of itself; the gradients in two parts, 2^-16, for a sequence or batch row of
- * 512 keys or fewer, by its own length, where that takes little time). All other operands take the general kernels,
- * whose products are of fp32 accuracy (each factor as the sum of two tf32 numbers).
+ * 512 keys or fewer, by its own length, where that takes little time). All other operands
+ * take the general kernels, whose products are of fp32 accuracy (each factor as the sum of
+ * two tf32 numbers).
  * Keys and values past a row's length are never used, whatever they hold; values within
- * have to be finite. An output must not overlap an input or another output.
+ * have to be finite: v 2^80 in magnitude at most, since its sums are divided by the sum of
+ * weights at the end (up to 2^16 for 128 keys, before the reference of a row's softmax
+ * moves), and other fp32 operands 2^127, since they are rounded to 11 bits on the way. With
+ * larger ones a result that is finite by its formula may come out infinite or NaN. An
+ * output must not overlap an input or another output.
  * workspace: cross_attn_workspace_bytes() (n_seqs = 0 unless packed, backward != 0 for
  * the backward's), zeroed once with scan_workspace_init. SCAN_ERR_UNSUPPORTED unless D
  * is a multiple of 8 up to 128 and B Hq <= 65535; SCAN_ERR_INVALID_ARG unless Hq % Hk
@@ -728,9 +733,9 @@ scan_status cross_attn_bwd(const scan_view4* q, const scan_view4* k, const scan_
  *   [n_slots], the keys that each cache holds (forced into [0, Tk]), else Tk; slots:
  *   int32 [B], the cache of each request, or NULL (request b has cache b). Requests may
  *   share a cache. A slot outside [0, n_slots) marks an idle request, which gets o = 0,
- *   as one without keys does. Rows past a length are never used. bf16 caches on 16-byte
- *   boundaries are read by tensor copies, the weights of their values the sum of two bf16
- *   numbers each (2^-16 of themselves).
+ *   as one without keys does. Rows past a length are never used; values are as large as the
+ *   forward's may be. bf16 caches on 16-byte boundaries are read by tensor copies, the
+ *   weights of their values the sum of two bf16 numbers each (2^-16 of themselves).
  * workspace: cross_attn_step_workspace_bytes(), zeroed once with scan_workspace_init;
  * nothing is kept in it between calls but its status word. Errors as the forward's, but
  * B Hq may be up to 2^31 - 1. */
@@ -775,7 +780,8 @@ scan_status dropout_bwd(const scan_view4* dy, const scan_view4* dx, int64_t B, i
  *   x, x_out: [B, T, C] of dtype stream_dt; y, n: of dtype dt (stream_dt fp32 with either
  *   dt, or bf16 with bf16). post_weight, next_weight: fp32 [C] or NULL; gate: fp32 [C], or
  *   [B, C] with row_gate != 0, or NULL (ones). p, seed, call, rng: as for dropout_fwd, over
- *   the elements of [B, T, C]. y NULL: only the norm of x (no post_weight and gate, alpha =
+ *   the elements of [B, T, C] (without post_weight, what y holds at a dropped element leaves no
+ *   trace, forward or backward; with it, y's norm has it in). y NULL: only the norm of x (no post_weight and gate, alpha =
  *   1, p = 0; x_out is not written). x_out may be x, n may be y.
  * Norms and sums are fp32, each result is rounded once. With eps = 0 a row of zeros has no
  * norm and gives NaN.

@@ -292,3 +292,21 @@ def test_no_query_heads(lib, dtype):
         lib.cross_attn_bwd(q, k, v, o, lse, do, out=out)
         assert all(float(t.abs().max()) == 0.0 for t in out[1:])
     assert lib.scan_get_device_status() == lib.SCAN_OK
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("D", [64, 128])
+def test_large_values(lib, dtype, D):
+    """Values of up to 2^80, also where weights grow before the reference moves (scores that rise
+    by four from tile to tile, so that 128 weights add up to 2^13 and more): the same bits as
+    without that factor, which is exact."""
+    q, k, v, _ = inputs(1, 130, 900, 2, 1, D, dtype, 12)
+    v = v.clamp(-1, 1)
+    q[..., 0] = 1.0
+    k[0, :, :, 0] = (4.0 * (torch.arange(900, device=DEV) // 128) / D ** -0.5)[:, None].to(dtype)
+    huge = (v.float() * 2.0 ** 80).to(dtype)
+    o, lse = lib.cross_attn_fwd(q, k, v)
+    big, same = lib.cross_attn_fwd(q, k, huge)
+    assert torch.equal(big.float(), o.float() * 2.0 ** 80) and torch.equal(lse, same)
+    o, big = (lib.cross_attn_step(q[:, 5], k, x) for x in (v, huge))
+    assert torch.equal(big.float(), o.float() * 2.0 ** 80)
