@@ -17,11 +17,11 @@
 //   state         S^T to bf16 for the next chunk's x1 S, and S^T *= lambda^n
 //   update        x3'^T = lambda^(n - e - r') x3^T as the sum of two bf16 parts (three
 //                 where the state is an output), 32 steps at a time: the state's
-//                 update is then exact to 2^-17 (2^-24), so that the state, fp32 in
+//                 update is then exact to 2^-16 (2^-24), so that the state, fp32 in
 //                 tensor memory, keeps that accuracy over any number of chunks
 //   output        O *= lambda^(r + e) between the two products into it; O to bf16
 // P, and the state as x1 reads it, are rounded once to bf16, the type that the tensor
-// cores take next to bf16 operands: each term of an output is off by 2^-9 of itself at
+// cores take next to bf16 operands: each term of an output is off by 2^-8 of itself at
 // most, which is the size of the output's own rounding. Neither is carried on: the state
 // itself and all sums stay in 32 bits.
 // The state lies transposed (lanes are v): its bf16 copy is then written by rows
@@ -290,7 +290,7 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_co
   // three bf16 parts of 16 columns each), O, S^T
   const uint32_t tS1 = tm, tX = STATE_ONLY ? tm : tm + 128, tO = tm + 256, tSt = tm + 384;
   constexpr int kPiece = 48;
-  // two parts carry the state to 2^-17 a step, which the bf16 outputs never show; a
+  // two parts carry the state to 2^-16 a step, which the bf16 outputs never show; a
   // state that is an output itself gets three
   const bool three = p.s_out != nullptr;
   const uint32_t lanes = (uint32_t)(warp % 4) << 21;  // this warp's first tensor-memory lane

@@ -360,8 +360,8 @@ __global__ void __launch_bounds__(kThreads, 1) window_dkv_kernel(const __grid_co
       }
       {
         // P and, below, dS go to the products as bf16, the type that the tensor cores take
-        // next to bf16 operands: off by 2^-9 of themselves at most (TWO: dS as two parts, off
-        // by 2^-18). dS is formed from the P of 32 bits, and all sums are of 32 bits.
+        // next to bf16 operands: off by 2^-8 of themselves at most (TWO: dS as two parts, off
+        // by 2^-16). dS is formed from the P of 32 bits, and all sums are of 32 bits.
         uint32_t o[32];
 #pragma unroll
         for (int i = 0; i < 2; ++i)

@@ -315,7 +315,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_fwd_kernel(const __grid_co
       }
       const float from = m == -INFINITY ? 0.f : m;
       // p goes to the product as bf16, the type that the tensor cores take next to bf16
-      // values: each weight is off by 2^-9 of itself at most, the output by about one
+      // values: each weight is off by 2^-8 of itself at most, the output by about one
       // rounding of its own type. The sum l is of p before that, in fp32.
       float2 sum[4] = {};
       const float2 f2 = make_float2(-from, -from), sl2 = make_float2(a.sl2, a.sl2);

@@ -185,7 +185,7 @@ __global__ void __launch_bounds__(32 * kWarps, ROWS == 8 ? 3 : 2) window_step_ke
           acc[i][j][2 * h + 1] *= keep;
         }
     }
-    // (weights as bf16, as the values they multiply: off by 2^-9 of themselves at most; l is
+    // (weights as bf16, as the values they multiply: off by 2^-8 of themselves at most; l is
     // the sum of the unrounded ones)
     const uint32_t a0 = pack2(p[0][0], p[0][1]), a2 = pack2(p[1][0], p[1][1]);
     const uint32_t a1 = ROWS == 16 ? pack2(p[0][2], p[0][3]) : 0u, a3 = ROWS == 16 ? pack2(p[1][2], p[1][3]) : 0u;
