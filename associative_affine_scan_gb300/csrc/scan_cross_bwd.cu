@@ -22,12 +22,13 @@
 // and commits are under the other's products.
 //
 // 4 x 4096 queries over 1280 to 2048 keys, 16 heads of 128 over 4: row sums 25 us (DRAM, 5.4
-// TB/s), queries 246 us (three products, 1.36 PFLOP/s), keys 347 us (four, 1.29 PFLOP/s),
+// TB/s), queries 249 us (three products, 1.34 PFLOP/s), keys 348 us (four, 1.29 PFLOP/s),
 // parts 12 us.
 // Bound by a pair of tiles' chain: the softmax of S, dS from dP, and their handing over and
 // back leave the tensor cores idle for a quarter to a third of the time. Shorter rows are
 // bound by the tiles' beginnings and ends (seven packed sequences of 46 to 1314 keys, 12
-// heads of 96: row sums 8 us, queries 40 us, keys 52 us, parts 8 us).
+// heads of 96: row sums 8 us, queries 42 us, keys 57 us, parts 8 us; with dS of the short ones
+// in one part queries 40 us, keys 52 us).
 #include "scan_cross_phases.h"
 #include "scan_cross_tc.h"
 #include "scan_tc.cuh"
@@ -522,7 +523,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_dq_kernel(const __grid_cons
 // the heads that share them. What is dealt out in equal shares are turns: a pair is one, a
 // tile's beginning and end are three more, ahead of its pairs (12 heads of 96: 1.4 us a pair,
 // 4 us a beginning and end; seven packed sequences of 46 to 1314 keys, dealt out by pairs
-// alone 75 us, so 52 us), and a tile without a pair is one.
+// alone 75 us, so 52 us, dS in one part), and a tile without a pair is one.
 constexpr int kEnds = 3;
 struct KeyTile {
   CrossRows g;     // t0: its first key row

@@ -14,10 +14,11 @@
 //
 // Two reads and two writes of each element forward, four and two backward, some ten
 // and thirty operations: bound by DRAM. A row is held by the 32 to 512 threads that
-// cover it, eight elements a thread (or two times eight), so that no row is read
-// twice; sums are shuffles and one exchange through shared memory.
-// 8 x 4096 rows of 2048, the stream in fp32, y in bf16, dropout: forward 138 us (5.8 TB/s),
-// backward 194 us and the sums 10 us (6.2 TB/s during the walk).
+// cover it, one, two or four times eight elements a thread (fwd_shape, bwd_shape), so that no
+// row is read twice. Sums are shuffles and an exchange through shared memory: one a norm
+// forward, one of six sums backward.
+// 8 x 4096 rows of 2048, the stream in fp32, y in bf16, dropout: forward 134 us (6.0 TB/s),
+// backward 195 us and the sums 11 us (6.2 TB/s during the walk).
 #include "scan_mixer.h"
 #include "scan_philox.cuh"
 #include "scan_tc.cuh"

@@ -693,7 +693,8 @@ scan_status window_attn_step(const scan_view4* q, const scan_view4* k, const sca
  * most (2^-8 of itself; the gradients in two parts, 2^-16, for a sequence or batch row of
  * 512 keys or fewer, by its own length, where that takes little time). All other operands
  * take the general kernels, whose products are of fp32 accuracy (each factor as the sum of
- * two tf32 numbers).
+ * two tf32 numbers); bf16 operands, those broadcast over an axis by a stride of 0 among
+ * them, are some thirty-five times slower there.
  * Keys and values past a row's length are never used, whatever they hold; values within
  * have to be finite: v 2^80 in magnitude at most, since its sums are divided by the sum of
  * weights at the end (up to 2^16 for 128 keys, before the reference of a row's softmax
