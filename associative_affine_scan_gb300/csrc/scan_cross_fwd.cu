@@ -317,7 +317,8 @@ __global__ void __launch_bounds__(kThreads, 1) cross_fwd_kernel(const __grid_con
         }
         // p goes to the product as bf16, the type that the tensor cores take next to bf16
         // values: each weight is off by 2^-8 of itself at most, the output by about one
-        // rounding of its own type (0.0022 of it in the 2-norm with its own, 0.0017 alone). The sum l is of p before that, in fp32.
+        // rounding of its own type (0.0023 of it in the 2-norm, 0.0017 for its own rounding
+        // alone). The sum l is of p before that, in fp32.
         float tot;
 #pragma unroll 1
         for (int round = 0;; ++round) {

@@ -7,9 +7,10 @@
 // such tiles (32 KB each at D = 128) on its way ahead of the arithmetic, across the
 // borders of requests. Two groups of four warps take the tiles by turns, 16 keys a warp:
 // scores of up to 16 query heads by m16n8k16 products, the running maximum and sum of
-// each row, and the weights, in two bf16 parts, by the values. A warp keeps its own sums until the request's
-// last tile; then the warps' are added in order. A request that a share's end cuts leaves
-// its parts in the workspace (at most two a block), which a second kernel adds in order.
+// each row, and the weights, in two bf16 parts, by the values. A warp keeps its own sums
+// until the request's last tile; then the warps' are added in order. A request that a share's
+// end cuts leaves its parts in the workspace (at most two a block), which a second kernel adds
+// in order.
 //
 // 64 requests over 800 to 4096 keys, 16 heads of 128 over 4: 60 us (5.4 TB/s) and 7 us; one
 // request over 1500 keys, 16 heads: 10 us and 8 us, all latency. The ring holds 192 KB an SM

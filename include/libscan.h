@@ -782,7 +782,8 @@ scan_status dropout_bwd(const scan_view4* dy, const scan_view4* dx, int64_t B, i
  *   dt, or bf16 with bf16). post_weight, next_weight: fp32 [C] or NULL; gate: fp32 [C], or
  *   [B, C] with row_gate != 0, or NULL (ones). p, seed, call, rng: as for dropout_fwd, over
  *   the elements of [B, T, C] (without post_weight, what y holds at a dropped element leaves no
- *   trace, forward or backward; with it, y's norm has it in). y NULL: only the norm of x (no post_weight and gate, alpha =
+ *   trace, forward or backward; with it, y's norm has it in).
+ *   y NULL: only the norm of x (no post_weight and gate, alpha =
  *   1, p = 0; x_out is not written). x_out may be x, n may be y.
  * Norms and sums are fp32, each result is rounded once. With eps = 0 a row of zeros has no
  * norm and gives NaN.
